@@ -25,6 +25,11 @@ BITLINEAR_ERR_HIP = -5
 BITLINEAR_ERR_SCRATCH = -6
 BITLINEAR_MAX_K = 16909320
 
+# bitlinear_activation
+BITLINEAR_ACT_GELU = 1
+BITLINEAR_ACT_SILU = 2
+BITLINEAR_ACT_RELU2 = 3
+
 # Every symbol the header declares, with (restype, argtypes).
 _P, _I64, _SZ, _INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
 SIGNATURES = {
@@ -53,6 +58,14 @@ SIGNATURES = {
     "bitlinear_hadamard_rows": (_INT, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "bitlinear_quantize_act_hadamard": (_INT, [_P, _I64, _I64, _I64, _P, _P, _P, _P]),
     "bitlinear_forward_fused_hadamard": (_INT, [_P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P, _P, _P, _P]),
+    "bitlinear_gated_forward": (_INT, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _INT, _P, _P, _P, _P, _P, _P]),
+    "bitlinear_backward_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "bitlinear_backward": (_INT, [_P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bitlinear_gated_backward_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "bitlinear_gated_backward": (_INT, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _INT, _P, _P, _P, _P, _P,
+                                        _P, _SZ, _P]),
+    "bitlinear_quantize_weights_i8": (_INT, [_P, _I64, _I64, _P, _P, _P]),
+    "bitlinear_forward_i8": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P]),
 }
 
 
@@ -410,6 +423,158 @@ def bitlinear_forward_fused_rows(x, W_packed, alpha_rows, bias=None, y=None, x_q
     """bitlinear_forward_fused with alpha_rows [N] fp32 (one alpha per output row); also the
     call for grouped projections (stacked packed rows, each projection's alpha repeated)."""
     return _forward_fused("bitlinear_forward_fused_rows", x, W_packed, alpha_rows, bias, y, x_q, beta, acc, stream)
+
+
+def _shaped(t, dtype, name, shape, device):
+    """Device pointer of t (None for None) after checking that it is a contiguous tensor of exactly
+    this dtype and shape on this device.  Of integer codes and packed bytes as of floats."""
+    if t is None:
+        return None
+    ptr = _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return ptr
+
+
+def _rows(t, name):
+    """Shape [rows, columns] and device of a matrix argument, which has to lie on the current device
+    (the library launches there)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device")
+    return t.shape[0], t.shape[1], t.device
+
+
+def bitlinear_gated_forward(x, Wg_packed, alpha_g, Wu_packed, alpha_u, act, bias_g=None, bias_u=None, h=None, g=None,
+                            u=None, x_q=None, beta=None, stream=None):
+    """h [M, F] = a(g) * u with g, u the BitLinears of fp32 x [M, K] under Wg, Wu [F, K/4]; act is one
+    of BITLINEAR_ACT_GELU / _SILU / _RELU2.  g and u (fp32 [M, F], both or neither), x_q and beta
+    (tensors) receive what bitlinear_gated_backward needs; x_q and beta are allocated if not given.
+    Returns h."""
+    torch = _torch()
+    M, K, dev = _rows(x, "x")
+    F = Wg_packed.shape[0]
+    if h is None:
+        h = torch.empty((M, F), dtype=torch.float32, device=dev)
+    if x_q is None:
+        x_q = torch.empty((M, K), dtype=torch.int8, device=dev)
+    if beta is None:
+        beta = torch.empty(M, dtype=torch.float32, device=dev)
+    f32, u8 = torch.float32, torch.uint8
+    _check("bitlinear_gated_forward", lib.bitlinear_gated_forward(
+        _shaped(x, f32, "x", (M, K), dev), M, K, _shaped(Wg_packed, u8, "Wg_packed", (F, K // 4), dev),
+        _shaped(alpha_g, f32, "alpha_g", (1,), dev), _shaped(bias_g, f32, "bias_g", (F,), dev),
+        _shaped(Wu_packed, u8, "Wu_packed", (F, K // 4), dev), _shaped(alpha_u, f32, "alpha_u", (1,), dev),
+        _shaped(bias_u, f32, "bias_u", (F,), dev), F, int(act), _shaped(h, f32, "h", (M, F), dev),
+        _shaped(g, f32, "g", (M, F), dev), _shaped(u, f32, "u", (M, F), dev),
+        _shaped(x_q, torch.int8, "x_q", (M, K), dev), _shaped(beta, f32, "beta", (M,), dev), _stream(stream)))
+    return h
+
+
+def bitlinear_backward_workspace_size(M, K, N) -> int:
+    """Bytes of workspace of bitlinear_backward (0 for invalid sizes)."""
+    return lib.bitlinear_backward_workspace_size(M, K, N)
+
+
+def bitlinear_gated_backward_workspace_size(M, K, F) -> int:
+    """Bytes of workspace of bitlinear_gated_backward (0 for invalid sizes)."""
+    return lib.bitlinear_gated_backward_workspace_size(M, K, F)
+
+
+def _workspace(workspace, need, dev):
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    if workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
+    return _dev(workspace, torch.uint8, "workspace"), workspace.numel()
+
+
+def bitlinear_backward(dy, x_q, beta, W_packed, alpha, dx=None, dW=None, dbias=None, workspace=None, stream=None):
+    """Gradients of y = bitlinear_forward(x_q, beta, W_packed, alpha, bias): dx [M, K], dW [N, K] and
+    dbias [N], each written if its tensor is given; with none given, dx and dW are allocated.
+    Returns (dx, dW, dbias), None for what was not asked for."""
+    torch = _torch()
+    M, N, dev = _rows(dy, "dy")
+    _, K, _ = _rows(x_q, "x_q")
+    f32 = torch.float32
+    if dx is None and dW is None and dbias is None:
+        dx = torch.empty((M, K), dtype=f32, device=dev)
+        dW = torch.empty((N, K), dtype=f32, device=dev)
+    ws, ws_bytes = _workspace(workspace, lib.bitlinear_backward_workspace_size(M, K, N), dev)
+    _check("bitlinear_backward", lib.bitlinear_backward(
+        _shaped(dy, f32, "dy", (M, N), dev), M, N, _shaped(x_q, torch.int8, "x_q", (M, K), dev),
+        _shaped(beta, f32, "beta", (M,), dev), K, _shaped(W_packed, torch.uint8, "W_packed", (N, K // 4), dev),
+        _shaped(alpha, f32, "alpha", (1,), dev), _shaped(dx, f32, "dx", (M, K), dev),
+        _shaped(dW, f32, "dW", (N, K), dev), _shaped(dbias, f32, "dbias", (N,), dev), ws, ws_bytes, _stream(stream)))
+    return dx, dW, dbias
+
+
+def bitlinear_gated_backward(dh, g, u, x_q, beta, Wg_packed, alpha_g, Wu_packed, alpha_u, act, dx=None, dWg=None,
+                             dWu=None, dbias_g=None, dbias_u=None, workspace=None, stream=None):
+    """Gradients of bitlinear_gated_forward from dh [M, F] and the g, u, x_q, beta it left: dx [M, K],
+    dWg and dWu [F, K] (both or neither), dbias_g and dbias_u [F], each written if its tensor is
+    given; with none given, dx, dWg and dWu are allocated.  Returns (dx, dWg, dWu, dbias_g, dbias_u),
+    None for what was not asked for."""
+    torch = _torch()
+    M, F, dev = _rows(dh, "dh")
+    _, K, _ = _rows(x_q, "x_q")
+    f32, u8 = torch.float32, torch.uint8
+    if dx is None and dWg is None and dWu is None and dbias_g is None and dbias_u is None:
+        dx = torch.empty((M, K), dtype=f32, device=dev)
+        dWg = torch.empty((F, K), dtype=f32, device=dev)
+        dWu = torch.empty((F, K), dtype=f32, device=dev)
+    ws, ws_bytes = _workspace(workspace, lib.bitlinear_gated_backward_workspace_size(M, K, F), dev)
+    _check("bitlinear_gated_backward", lib.bitlinear_gated_backward(
+        _shaped(dh, f32, "dh", (M, F), dev), _shaped(g, f32, "g", (M, F), dev), _shaped(u, f32, "u", (M, F), dev), M, F,
+        _shaped(x_q, torch.int8, "x_q", (M, K), dev), _shaped(beta, f32, "beta", (M,), dev), K,
+        _shaped(Wg_packed, u8, "Wg_packed", (F, K // 4), dev), _shaped(alpha_g, f32, "alpha_g", (1,), dev),
+        _shaped(Wu_packed, u8, "Wu_packed", (F, K // 4), dev), _shaped(alpha_u, f32, "alpha_u", (1,), dev), int(act),
+        _shaped(dx, f32, "dx", (M, K), dev), _shaped(dWg, f32, "dWg", (F, K), dev), _shaped(dWu, f32, "dWu", (F, K), dev),
+        _shaped(dbias_g, f32, "dbias_g", (F,), dev), _shaped(dbias_u, f32, "dbias_u", (F,), dev), ws, ws_bytes,
+        _stream(stream)))
+    return dx, dWg, dWu, dbias_g, dbias_u
+
+
+def bitlinear_quantize_weights_i8(W, W_q=None, gamma=None, stream=None):
+    """W [N, K] fp32 -> (W_q int8 [N, K], gamma fp32 [N]): absmax int8 codes, one scale per row."""
+    torch = _torch()
+    N, K, dev = _rows(W, "W")
+    if W_q is None:
+        W_q = torch.empty((N, K), dtype=torch.int8, device=dev)
+    if gamma is None:
+        gamma = torch.empty(N, dtype=torch.float32, device=dev)
+    _check("bitlinear_quantize_weights_i8", lib.bitlinear_quantize_weights_i8(
+        _shaped(W, torch.float32, "W", (N, K), dev), N, K, _shaped(W_q, torch.int8, "W_q", (N, K), dev),
+        _shaped(gamma, torch.float32, "gamma", (N,), dev), _stream(stream)))
+    return W_q, gamma
+
+
+def bitlinear_forward_i8(x_q, beta, W_q, gamma, bias=None, y=None, acc=None, stream=None):
+    """y [M, N] = (x_q . W_q^T) * (beta / 127) * (gamma / 127) (+ bias).  acc=True (or an int32
+    [M, N] tensor) also returns the exact integer sums: (y, acc)."""
+    torch = _torch()
+    M, K, dev = _rows(x_q, "x_q")
+    N = W_q.shape[0]
+    f32 = torch.float32
+    if y is None:
+        y = torch.empty((M, N), dtype=f32, device=dev)
+    if acc is True:
+        acc = torch.empty((M, N), dtype=torch.int32, device=dev)
+    elif acc is False:
+        acc = None
+    _check("bitlinear_forward_i8", lib.bitlinear_forward_i8(
+        _shaped(x_q, torch.int8, "x_q", (M, K), dev), _shaped(beta, f32, "beta", (M,), dev), M, K,
+        _shaped(W_q, torch.int8, "W_q", (N, K), dev), _shaped(gamma, f32, "gamma", (N,), dev), N,
+        _shaped(bias, f32, "bias", (N,), dev), _shaped(y, f32, "y", (M, N), dev),
+        _shaped(acc, torch.int32, "acc", (M, N), dev), _stream(stream)))
+    return y if acc is None else (y, acc)
 
 
 def bitlinear_forward_fused_kernel(M, K, N, x=None, W_packed=None, x_q=None) -> str:

@@ -6,6 +6,7 @@
 #include <limits.h>
 
 #include "common.hpp"
+#include "ffn.hpp"
 
 using namespace bitlinear;
 
@@ -338,6 +339,89 @@ int bitlinear_forward_fused_hadamard(const float* x, int64_t M, int64_t K, int64
     st = hip_status(launch_quantize_act_hadamard(x, M, K, (int)block, signs, x_q, beta, stream));
     if (st) return st;
     return bitlinear_forward(x_q, beta, M, K, W_packed, alpha, N, bias, y, nullptr, stream);
+}
+
+// Sizes of the gated block and of the gradients: K % 4 == 0, every product of two sizes in range
+// (times 8: the byte counts of fp32 pairs), M and N within a grid dimension.
+static int check_sizes(int64_t M, int64_t K, int64_t N) {
+    if (M <= 0 || K <= 0 || N <= 0) return BITLINEAR_ERR_INVALID_ARG;
+    if (K % 4 != 0 || K > BITLINEAR_MAX_K || M > INT_MAX || N > INT_MAX) return BITLINEAR_ERR_SHAPE;
+    constexpr int64_t most = (int64_t)1 << 40;
+    if (M > most / K || N > most / K || M > most / N) return BITLINEAR_ERR_SHAPE;
+    return BITLINEAR_OK;
+}
+
+static bool known_activation(int act) {
+    return act == BITLINEAR_ACT_GELU || act == BITLINEAR_ACT_SILU || act == BITLINEAR_ACT_RELU2;
+}
+
+int bitlinear_gated_forward(const float* x, int64_t M, int64_t K, const uint8_t* Wg_packed, const float* alpha_g,
+                            const float* bias_g, const uint8_t* Wu_packed, const float* alpha_u, const float* bias_u,
+                            int64_t F, int act, float* h, float* g, float* u, int8_t* x_q, float* beta,
+                            hipStream_t stream) {
+    if (!x || !Wg_packed || !alpha_g || !Wu_packed || !alpha_u || !h || !x_q || !beta) return BITLINEAR_ERR_INVALID_ARG;
+    if (!g != !u || !known_activation(act)) return BITLINEAR_ERR_INVALID_ARG;
+    int st = check_sizes(M, K, F);
+    if (st) return st;
+    st = hip_status(launch_quantize_act(x, M, K, x_q, beta, stream));
+    if (st) return st;
+    const GatedArgs a{x_q, beta, M, K, F, Wg_packed, Wu_packed, alpha_g, alpha_u, bias_g, bias_u, act, h, g, u};
+    return hip_status(launch_gated(a, stream));
+}
+
+// Workspace of a backward call for valid sizes, else 0.
+static size_t backward_bytes(int64_t M, int64_t K, int64_t N, bool gated) {
+    return check_sizes(M, K, N) == BITLINEAR_OK ? backward_workspace(M, K, N, gated) : 0;
+}
+
+size_t bitlinear_backward_workspace_size(int64_t M, int64_t K, int64_t N) { return backward_bytes(M, K, N, false); }
+
+size_t bitlinear_gated_backward_workspace_size(int64_t M, int64_t K, int64_t F) {
+    return backward_bytes(M, K, F, true);
+}
+
+static int run_backward(const BackwardArgs& a, size_t workspace_bytes, bool gated, hipStream_t stream) {
+    const int st = check_sizes(a.M, a.K, a.N);
+    if (st) return st;
+    if (!a.ws || workspace_bytes < backward_workspace(a.M, a.K, a.N, gated)) return BITLINEAR_ERR_WORKSPACE;
+    if (!aligned(a.ws, 256)) return BITLINEAR_ERR_ALIGNMENT;
+    return hip_status(launch_backward(a, stream));
+}
+
+int bitlinear_backward(const float* dy, int64_t M, int64_t N, const int8_t* x_q, const float* beta, int64_t K,
+                       const uint8_t* W_packed, const float* alpha, float* dx, float* dW, float* dbias,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!dy || !x_q || !beta || !W_packed || !alpha || (!dx && !dW && !dbias)) return BITLINEAR_ERR_INVALID_ARG;
+    const BackwardArgs a{dy, nullptr, nullptr, 0, M, K, N, x_q, beta, W_packed, nullptr, alpha, nullptr,
+                         dx, dW, nullptr, dbias, nullptr, workspace};
+    return run_backward(a, workspace_bytes, false, stream);
+}
+
+int bitlinear_gated_backward(const float* dh, const float* g, const float* u, int64_t M, int64_t F, const int8_t* x_q,
+                             const float* beta, int64_t K, const uint8_t* Wg_packed, const float* alpha_g,
+                             const uint8_t* Wu_packed, const float* alpha_u, int act, float* dx, float* dWg, float* dWu,
+                             float* dbias_g, float* dbias_u, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+    if (!dh || !g || !u || !x_q || !beta || !Wg_packed || !alpha_g || !Wu_packed || !alpha_u)
+        return BITLINEAR_ERR_INVALID_ARG;
+    if (!dWg != !dWu || (!dx && !dWg && !dbias_g && !dbias_u) || !known_activation(act)) return BITLINEAR_ERR_INVALID_ARG;
+    const BackwardArgs a{dh, g, u, act, M, K, F, x_q, beta, Wg_packed, Wu_packed, alpha_g, alpha_u,
+                         dx, dWg, dWu, dbias_g, dbias_u, workspace};
+    return run_backward(a, workspace_bytes, true, stream);
+}
+
+int bitlinear_quantize_weights_i8(const float* W, int64_t N, int64_t K, int8_t* W_q, float* gamma, hipStream_t stream) {
+    return bitlinear_quantize_act(W, N, K, W_q, gamma, stream);
+}
+
+int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_t K, const int8_t* W_q,
+                         const float* gamma, int64_t N, const float* bias, float* y, int32_t* acc, hipStream_t stream) {
+    if (!x_q || !beta || !W_q || !gamma || !y) return BITLINEAR_ERR_INVALID_ARG;
+    if (M <= 0 || K <= 0 || N <= 0) return BITLINEAR_ERR_INVALID_ARG;
+    constexpr int64_t most = (int64_t)1 << 40;
+    if (K > I8_MAX_K || M > INT_MAX || N > INT_MAX || M > most / N) return BITLINEAR_ERR_SHAPE;
+    const I8Args a{x_q, beta, M, K, N, W_q, gamma, bias, y, acc};
+    return hip_status(launch_forward_i8(a, stream));
 }
 
 const char* bitlinear_forward_fused_kernel(int64_t M, int64_t K, int64_t N, const float* x, const uint8_t* W_packed,

@@ -1,0 +1,103 @@
+// ffn.hpp -- the gated feed-forward block, the BitLinear gradients and the W8A8 product:
+// activation helpers and launch declarations.
+#pragma once
+
+#include "bitlinear.h"
+#include "common.hpp"
+
+namespace bitlinear {
+
+// a(g) of the gated block, in fp32.  SiLU: g / (1 + exp(-g)), the exponential within two units
+// in the last place and the sum and quotient rounded once each (exp(-g) = inf gives -0, the
+// limit).  GELU: the BitMLP's.  Squared ReLU: one rounding.
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+    if constexpr (ACT == BITLINEAR_ACT_SILU) return g / (1.0f + expf(-g));
+    else if constexpr (ACT == BITLINEAR_ACT_GELU) return gelu_f32(g);
+    else {
+        const float r = fmaxf(g, 0.0f);
+        return r * r;
+    }
+}
+
+// a(g) and a'(g) for the gradients, to a few fp32 roundings.
+//   SiLU: with e = exp(-|g|), s(|g|) = 1 / (1 + e) and s(-|g|) = e / (1 + e), so neither
+//     logistic value is formed as a difference; a = g s(g), a' = s(g) + a s(-g).
+//   GELU: a = g Phi(g), a' = Phi(g) + g phi(g) in fp64 (Phi from the erfc polynomial of the
+//     forward pass, whose tail below g = -8 is off relative to itself but below 1e-14).
+//   Squared ReLU: a = r^2, a' = 2 r.
+template <int ACT>
+__device__ __forceinline__ void act_grad(float g, float& a, float& slope) {
+    if constexpr (ACT == BITLINEAR_ACT_SILU) {
+        const float e = expf(-fabsf(g)), t = 1.0f / (1.0f + e), p = e * t;
+        const float s = g >= 0.0f ? t : p, sc = g >= 0.0f ? p : t;
+        a = g * s;
+        slope = s + a * sc;
+    } else if constexpr (ACT == BITLINEAR_ACT_GELU) {
+        const double v = (double)g, y = fabs(v) * 0.70710678118654752440, d = 2.0 + y;
+        double r = __builtin_amdgcn_rcp(d);
+        r = fma(r, fma(-d, r, 1.0), r);
+        r = fma(r, fma(-d, r, 1.0), r);
+        const double t = fmax(fma(r, gelu_poly::kS2, gelu_poly::kO), -1.0);
+        double c = gelu_poly::kC[16];
+#pragma unroll
+        for (int i = 15; i >= 0; --i) c = fma(c, t, gelu_poly::kC[i]);
+        const double ex = exp(-0.5 * v * v), q = 0.5 * ex * c;
+        const double cdf = v < 0.0 ? q : 1.0 - q;
+        a = (float)(v * cdf);
+        slope = (float)(cdf + v * ex * 0.39894228040143267794);
+    } else {
+        const float r = fmaxf(g, 0.0f);
+        a = r * r;
+        slope = 2.0f * r;
+    }
+}
+
+struct GatedArgs {
+    const int8_t* xq;
+    const float* beta;
+    int64_t M, K, F;
+    const uint8_t *wg, *wu;        // packed [F, K/4]
+    const float *ag, *au;          // alpha [1]
+    const float *bg, *bu;          // bias [F] or null
+    int act;                       // bitlinear_activation
+    float* h;                      // [M, F]
+    float *g, *u;                  // [M, F] or both null
+};
+
+hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
+
+struct I8Args {
+    const int8_t* xq;
+    const float* beta;
+    int64_t M, K, N;
+    const int8_t* wq;              // [N, K]
+    const float* gamma;            // [N]
+    const float* bias;             // [N] or null
+    float* y;
+    int32_t* acc;                  // [M, N] or null
+};
+
+// Largest K for which |acc| <= 127 * 127 * K fits int32.
+constexpr int64_t I8_MAX_K = 133144;
+hipError_t launch_forward_i8(const I8Args& a, hipStream_t s);
+
+// Gradients of one or two (gate and up) ternary projections of the same x_q.
+struct BackwardArgs {
+    const float* dy;               // one projection: dy [M, N]; gated: dh [M, N]
+    const float *g, *u;            // gated: saved [M, N]; one projection: null
+    int act;
+    int64_t M, K, N;               // N: rows of each weight matrix
+    const int8_t* xq;
+    const float* beta;
+    const uint8_t *w0, *w1;        // packed [N, K/4]; w1 null for one projection
+    const float *al0, *al1;        // alpha [1]
+    float* dx;                     // [M, K] or null
+    float *dw0, *dw1;              // [N, K] or null
+    float *db0, *db1;              // [N] or null
+    void* ws;
+};
+size_t backward_workspace(int64_t M, int64_t K, int64_t N, bool gated);
+hipError_t launch_backward(const BackwardArgs& a, hipStream_t s);
+
+}  // namespace bitlinear

@@ -337,6 +337,107 @@ int bitlinear_forward_fused_hadamard(const float* x, int64_t M, int64_t K, int64
                                      const uint8_t* W_packed, const float* alpha, int64_t N, const float* bias,
                                      float* y, int8_t* x_q, float* beta, hipStream_t stream);
 
+/* Activation a(g) of the gated feed-forward block. */
+typedef enum bitlinear_activation {
+    BITLINEAR_ACT_GELU = 1, /* g Phi(g), the erf form of bitlinear_mlp_forward */
+    BITLINEAR_ACT_SILU = 2, /* g / (1 + exp(-g)) */
+    BITLINEAR_ACT_RELU2 = 3 /* max(g, 0)^2 */
+} bitlinear_activation;
+
+/*
+ * Gated feed-forward block, both projections, the activation and the product in one call:
+ *     g = BitLinear(x; Wg, alpha_g, bias_g),  u = BitLinear(x; Wu, alpha_u, bias_u),
+ *     h[m, n] = a(g[m, n]) * u[m, n].
+ * x is quantized as by bitlinear_quantize_act; g and u equal bitlinear_forward's y for the two
+ * matrices bit for bit; a(g) is evaluated in fp32 (SiLU within 7 * 2^-24 relative; GELU as
+ * bitlinear_mlp_forward; squared ReLU one rounding) and the product is one fp32 rounding.  The
+ * block's down projection is a bitlinear_quantize_act of h and any forward call.
+ *
+ *   x          [M, K] fp32.                                                  (in)
+ *   Wg_packed, Wu_packed  [F, K/4] uint8; alpha_g, alpha_u [1]; bias_g, bias_u [F] or NULL. (in)
+ *   act        a bitlinear_activation.
+ *   h          [M, F] fp32.                                                  (out)
+ *   g, u       [M, F] fp32, both or neither: kept for bitlinear_gated_backward. (out)
+ *   x_q, beta  [M, K] int8, [M] fp32: receive the quantized activations.     (out, required)
+ * K % 4 == 0; any alignment.  Outputs must not overlap inputs or each other.
+ * Errors: INVALID_ARG (null pointer, size <= 0, unknown act, one of g and u), SHAPE, HIP.
+ */
+int bitlinear_gated_forward(const float* x, int64_t M, int64_t K, const uint8_t* Wg_packed, const float* alpha_g,
+                            const float* bias_g, const uint8_t* Wu_packed, const float* alpha_u,
+                            const float* bias_u, int64_t F, int act, float* h, float* g, float* u, int8_t* x_q,
+                            float* beta, hipStream_t stream);
+
+/*
+ * Gradients of one BitLinear y = bitlinear_forward(x_q, beta, W_packed, alpha, bias), straight
+ * through both quantizers [P3 §3.3]: x and the latent W get the gradients of the products with
+ * the values that were used,
+ *     dx[m, k]  = alpha sum_n dy[m, n] W_hat[n, k]
+ *     dW[n, k]  = sum_m dy[m, n] (beta[m] / 127) x_q[m, k]
+ *     dbias[n]  = sum_m dy[m, n].
+ * Each gradient element enters its products with at least 22 significant bits, relative to
+ * itself down to 2^-17 of the largest of its row (dx) or column (dW) and as a fixed-point value
+ * below that; products are exact, and sums are taken in fp32 (dbias in fp64) in an order fixed
+ * by the sizes, so results are reproducible bit for bit.
+ *
+ *   dy        [M, N] fp32.                                                   (in)
+ *   x_q       [M, K] int8, beta [M] fp32: as bitlinear_forward used them.    (in)
+ *   W_packed  [N, K/4] uint8, alpha [1] fp32.                                (in)
+ *   dx        [M, K] fp32 or NULL.     dW  [N, K] fp32 or NULL.              (out)
+ *   dbias     [N] fp32 or NULL.                                              (out)
+ *   workspace >= bitlinear_backward_workspace_size(M, K, N) bytes, 256-byte aligned; scratch,
+ *             one for each call that may overlap another.
+ * K % 4 == 0; any alignment of the tensors.  At least one output is given; outputs must not
+ * overlap inputs or each other.  Errors: INVALID_ARG, SHAPE, ALIGNMENT and WORKSPACE (the
+ * workspace), HIP.
+ */
+size_t bitlinear_backward_workspace_size(int64_t M, int64_t K, int64_t N);
+int bitlinear_backward(const float* dy, int64_t M, int64_t N, const int8_t* x_q, const float* beta, int64_t K,
+                       const uint8_t* W_packed, const float* alpha, float* dx, float* dW, float* dbias,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of bitlinear_gated_forward from dh, the gradient of h, and the g, u, x_q and beta it
+ * left.  With dg = dh u a'(g) and du = dh a(g) (fp32), dx is the sum of both projections' dx of
+ * bitlinear_backward, and dWg, dWu, dbias_g, dbias_u are those of the two projections; the same
+ * accuracy holds.  a' of squared ReLU is 2 max(g, 0).
+ *
+ *   dh, g, u  [M, F] fp32.                                                   (in)
+ *   dx        [M, K] or NULL.   dWg, dWu  [F, K], both or neither.           (out)
+ *   dbias_g, dbias_u  [F] or NULL, each.                                     (out)
+ *   workspace >= bitlinear_gated_backward_workspace_size(M, K, F) bytes, as bitlinear_backward.
+ * Errors: as bitlinear_backward, and INVALID_ARG for an unknown act or one of dWg and dWu.
+ */
+size_t bitlinear_gated_backward_workspace_size(int64_t M, int64_t K, int64_t F);
+int bitlinear_gated_backward(const float* dh, const float* g, const float* u, int64_t M, int64_t F,
+                             const int8_t* x_q, const float* beta, int64_t K, const uint8_t* Wg_packed,
+                             const float* alpha_g, const uint8_t* Wu_packed, const float* alpha_u, int act,
+                             float* dx, float* dWg, float* dWu, float* dbias_g, float* dbias_u, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Weights kept in 8 bits (output heads, projections too sensitive for three values), one absmax
+ * scale per output channel: W_q and gamma are what bitlinear_quantize_act gives for the rows of W,
+ *     gamma[n] = max_k |W[n, k]| + 1e-8,  W_q[n, k] = clip(round(fp32(127 W[n, k]) / gamma[n]), -127, 127).
+ *   W [N, K] fp32 (in);  W_q [N, K] int8, gamma [N] fp32 (out).  Any K >= 1.
+ * Errors: INVALID_ARG, SHAPE, HIP.
+ */
+int bitlinear_quantize_weights_i8(const float* W, int64_t N, int64_t K, int8_t* W_q, float* gamma,
+                                  hipStream_t stream);
+
+/*
+ * int8 x int8 matmul with a scale for each token and each output channel:
+ *     acc[m, n] = sum_k x_q[m, k] * W_q[n, k]                              (int32, exact)
+ *     y[m, n]   = (fp32(acc) * fp32(beta[m] / 127)) * fp32(gamma[n] / 127)  (+ bias[n])
+ * every step one fp32 rounding.  Codes lie in [-127, 127].
+ *   x_q [M, K] int8, beta [M] fp32 (from bitlinear_quantize_act); W_q [N, K] int8, gamma [N]
+ *   (from bitlinear_quantize_weights_i8); bias [N] or NULL.                  (in)
+ *   y [M, N] fp32; acc [M, N] int32 or NULL.                                 (out)
+ * K <= 133144 (so that acc fits); any alignment.  Errors: INVALID_ARG, SHAPE, HIP.
+ */
+int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_t K, const int8_t* W_q,
+                         const float* gamma, int64_t N, const float* bias, float* y, int32_t* acc,
+                         hipStream_t stream);
+
 /* Kernel(s) bitlinear_forward_fused launches for these arguments ("gemv_fused" or
  * "quantize_act+forward"; a non-NULL x_q stands for x_q and beta given); a static string. */
 const char* bitlinear_forward_fused_kernel(int64_t M, int64_t K, int64_t N, const float* x,
