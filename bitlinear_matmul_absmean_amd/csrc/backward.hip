@@ -14,12 +14,13 @@
 // f16 MFMA products into one fp32 accumulator then give the product to fp32 accuracy at half the
 // f16 matrix rate, several times the rate of fp32 products.
 //
-// Steps, each a launch over the whole problem:
-//   1. k_grad_max: the largest |d alpha| of every token and |d beta / 127| of every channel;
-//   2. k_grad_split: d once more, scaled and split, written token-major (dx) and channel-major (dW);
-//   3. k_weights_t, k_codes_t: the integer operands in fp16 with the sum's index contiguous;
-//   4. k_split_gemm (and k_split_sum where a sum is cut into parts) for dx and for dW;
-//   5. k_bias_sum.
+// Steps, each one launch over the whole problem:
+//   1. k_grad_prep: the largest |d alpha| of every token and |d beta / 127| of every channel, and the
+//      bias sums, tile by tile; the integer operands in fp16 with the sum's index contiguous;
+//   2. k_grad_reduce: the tiles' maxima and sums put together;
+//   3. k_grad_split: d once more, scaled and split, written token-major (dx) and channel-major (dW);
+//   4. k_split_gemm: both products;
+//   5. k_split_sum, where a sum was cut into parts.
 #include <limits.h>
 
 #include "ffn.hpp"
@@ -53,28 +54,35 @@ __device__ __forceinline__ void grad_at(const BackwardArgs& a, int64_t i, float 
     }
 }
 
+constexpr int SG_WI = 2, SG_BM = 64 * SG_WI, SG_BN = 256, SG_BK = 32, SG_SLOTS = 512;
+
 struct GradPlan {
     int64_t Np, Mp, Lx;            // N and M rounded up to 64, P Np
-    uint32_t *rmax, *cmax;         // bits of the largest |d alpha| [M], |d beta / 127| [P N]
-    double* bias_part;             // [ceil(M / 64)][P N]
+    int tm;                        // tokens of a maximum tile
+    int64_t mt, ct;                // maximum tiles along the tokens, along the columns
+    float *rpart, *cpart;          // largest |d alpha| [M, ct], |d beta / 127| [mt, P N] of a tile
+    double* bpart;                 // sums of d [mt, P N] of a tile
+    float *rmax, *cmax;            // [M], [P N]
     _Float16 *xh, *xl;             // dx: split gradients [M, Lx]
     _Float16 *wh, *wl;             // dW: split gradients [P N, Mp]
-    _Float16 *wt, *ct;             // W_hat^T [K, Lx], x_q^T [K, Mp]
-    float* part;                   // partial sums of a product cut into parts
+    _Float16 *wt, *cd;             // W_hat^T [K, Lx], x_q^T [K, Mp]
+    float *part_x, *part_w;        // sums cut into parts
     int parts_x, parts_w;
     size_t bytes;
 };
 
-constexpr int SG_BM = 128, SG_BN = 256, SG_BK = 32, SG_SLOTS = 512;
-
-// Parts to cut a sum of length L into: the fewest rounds of workgroups over the 512 slots per part,
-// counting each part's share of the sum; parts of at least 512 terms, at most 8.
+// Parts to cut a sum of length L into: the rounds of workgroups over the slots (a last round that
+// leaves one workgroup to a compute unit runs in 0.6 of the time), times a part's share of the sum, plus the exchange of the parts (a part is written and read once for each output, 8
+// bytes, and the output written once more; 4 bytes take the time of 220 terms).  Parts of at least
+// 256 terms, at most 32.
 static int sum_parts(int64_t I, int64_t J, int64_t L) {
     const int64_t tiles = ((I + SG_BM - 1) / SG_BM) * ((J + SG_BN - 1) / SG_BN);
     int best = 1;
     double cost = 1e30;
-    for (int s = 1; s <= 8 && (s == 1 || L / s >= 512); ++s) {
-        const double c = (double)((tiles * s + SG_SLOTS - 1) / SG_SLOTS) / s * (1.0 + 0.03 * (s > 1 ? s : 0));
+    for (int s = 1; s <= 32 && (s == 1 || L / s >= 256); ++s) {
+        const int64_t left = tiles * s % SG_SLOTS;
+        const double rounds = (double)(tiles * s / SG_SLOTS) + (left == 0 ? 0.0 : left <= SG_SLOTS / 2 ? 0.6 : 1.0);
+        const double c = (double)L * rounds * SG_SLOTS / (double)(tiles * s) + (s > 1 ? 220.0 * (2 * s + 1) : 0.0);
         if (c < cost) {
             cost = c;
             best = s;
@@ -89,48 +97,47 @@ static GradPlan grad_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws)
     p.Np = (N + 63) / 64 * 64;
     p.Mp = (M + 63) / 64 * 64;
     p.Lx = P * p.Np;
+    p.ct = (N + 255) / 256;
+    p.tm = (M + 63) / 64 * p.ct >= 512 ? 64 : 16;
+    p.mt = (M + p.tm - 1) / p.tm;
     p.parts_x = sum_parts(M, K, p.Lx);
     p.parts_w = sum_parts(P * N, K, p.Mp);
     uint8_t* base = static_cast<uint8_t*>(ws);
     size_t off = 0;
-    auto take = [&](size_t bytes) {
-        uint8_t* q = base + off;
-        off += (bytes + 255) / 256 * 256;
+    auto take = [&](int64_t count, size_t size) {
+        uint8_t* q = base ? base + off : nullptr;
+        off += ((size_t)count * size + 255) / 256 * 256;
         return q;
     };
-    p.rmax = reinterpret_cast<uint32_t*>(take((size_t)(M + P * N) * 4));
-    p.cmax = p.rmax + M;
-    p.bias_part = reinterpret_cast<double*>(take((size_t)(p.Mp / 64) * P * N * 8));
-    p.xh = reinterpret_cast<_Float16*>(take((size_t)M * p.Lx * 2));
-    p.xl = reinterpret_cast<_Float16*>(take((size_t)M * p.Lx * 2));
-    p.wh = reinterpret_cast<_Float16*>(take((size_t)P * N * p.Mp * 2));
-    p.wl = reinterpret_cast<_Float16*>(take((size_t)P * N * p.Mp * 2));
-    p.wt = reinterpret_cast<_Float16*>(take((size_t)K * p.Lx * 2));
-    p.ct = reinterpret_cast<_Float16*>(take((size_t)K * p.Mp * 2));
-    const size_t px = p.parts_x > 1 ? (size_t)p.parts_x * M * K * 4 : 0;
-    const size_t pw = p.parts_w > 1 ? (size_t)p.parts_w * P * N * K * 4 : 0;
-    p.part = reinterpret_cast<float*>(take(px > pw ? px : pw));
+    p.rpart = reinterpret_cast<float*>(take(M * p.ct, 4));
+    p.cpart = reinterpret_cast<float*>(take(p.mt * P * N, 4));
+    p.bpart = reinterpret_cast<double*>(take(p.mt * P * N, 8));
+    p.rmax = reinterpret_cast<float*>(take(M, 4));
+    p.cmax = reinterpret_cast<float*>(take(P * N, 4));
+    p.xh = reinterpret_cast<_Float16*>(take(M * p.Lx, 2));
+    p.xl = reinterpret_cast<_Float16*>(take(M * p.Lx, 2));
+    p.wh = reinterpret_cast<_Float16*>(take(P * N * p.Mp, 2));
+    p.wl = reinterpret_cast<_Float16*>(take(P * N * p.Mp, 2));
+    p.wt = reinterpret_cast<_Float16*>(take(K * p.Lx, 2));
+    p.cd = reinterpret_cast<_Float16*>(take(K * p.Mp, 2));
+    p.part_x = reinterpret_cast<float*>(take(p.parts_x > 1 ? p.parts_x * M * K : 0, 4));
+    p.part_w = reinterpret_cast<float*>(take(p.parts_w > 1 ? p.parts_w * P * N * K : 0, 4));
     p.bytes = off;
     return p;
 }
 
 size_t backward_workspace(int64_t M, int64_t K, int64_t N, bool gated) { return grad_plan(M, K, N, gated, nullptr).bytes; }
 
-__global__ __launch_bounds__(256) void k_zero(uint32_t* __restrict__ p, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) p[i] = 0u;
-}
-
-// Largest elements.  A workgroup takes 64 tokens x 256 columns, a wave 16 of the tokens, a lane four
-// columns 64 apart (whole lines whatever the alignment).  Non-negative floats compare as their
-// bits, and maxima do not depend on order, so integer atomics give the same result every time.
+// ---- step 1 -------------------------------------------------------------------------------
+// Maxima and sums.  A workgroup takes p.tm tokens x 256 columns, a wave a quarter of the tokens, a
+// lane four columns 64 apart (whole lines whatever the alignment).
 template <int ACT>
-__global__ __launch_bounds__(256) void k_grad_max(BackwardArgs a, GradPlan p, int ctiles) {
+__device__ __forceinline__ void max_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, uint8_t* lds) {
     constexpr int P = ACT == 0 ? 1 : 2;
-    __shared__ float cm[4][P][256];
-    __shared__ double cs[4][P][256];
+    double (*cs)[P][256] = reinterpret_cast<double (*)[P][256]>(lds);
+    float (*cm)[P][256] = reinterpret_cast<float (*)[P][256]>(lds + 4 * P * 256 * 8);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n0 = (int64_t)(blockIdx.x % ctiles) * 256, m0 = (int64_t)(blockIdx.x / ctiles) * 64;
+    const int64_t tn = b % p.ct, tmi = b / p.ct, n0 = tn * 256, m0 = tmi * p.tm;
     const float al[2] = {a.al0[0], ACT == 0 ? 0.0f : a.al1[0]};
     const bool bias = a.db0 || a.db1;
     float cmx[P][4];
@@ -142,8 +149,9 @@ __global__ __launch_bounds__(256) void k_grad_max(BackwardArgs a, GradPlan p, in
             cmx[q][c] = 0.0f;
             sum[q][c] = 0.0;
         }
-    for (int t = 0; t < 16; ++t) {
-        const int64_t m = m0 + 16 * wave + t;
+    const int per = p.tm / 4;
+    for (int t = 0; t < per; ++t) {
+        const int64_t m = m0 + per * wave + t;
         if (m >= a.M) break;
         const float bs = a.beta[m] / 127.0f;
         float rm = 0.0f;
@@ -162,14 +170,14 @@ __global__ __launch_bounds__(256) void k_grad_max(BackwardArgs a, GradPlan p, in
             }
         }
         rm = wave_max_f32(rm);
-        if (lane == 0) atomicMax(&p.rmax[m], __float_as_uint(rm));
+        if (lane == 0) p.rpart[m * p.ct + tn] = rm;
     }
 #pragma unroll
     for (int q = 0; q < P; ++q)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             cm[wave][q][64 * c + lane] = cmx[q][c];
-            cs[wave][q][64 * c + lane] = sum[q][c];
+            if (bias) cs[wave][q][64 * c + lane] = sum[q][c];
         }
     __syncthreads();
     const int64_t n = n0 + threadIdx.x;
@@ -181,102 +189,191 @@ __global__ __launch_bounds__(256) void k_grad_max(BackwardArgs a, GradPlan p, in
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             v = fmaxf(v, cm[w][q][threadIdx.x]);
-            s += cs[w][q][threadIdx.x];
+            if (bias) s += cs[w][q][threadIdx.x];
         }
-        atomicMax(&p.cmax[q * a.N + n], __float_as_uint(v));
-        if (bias) p.bias_part[(m0 / 64) * P * a.N + q * a.N + n] = s;
+        p.cpart[(tmi * P + q) * a.N + n] = v;
+        if (bias) p.bpart[(tmi * P + q) * a.N + n] = s;
     }
 }
 
+// Four bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.
+__device__ __forceinline__ uint32_t row_dword(const uint8_t* __restrict__ p, int64_t i, int64_t row) {
+    uint32_t v = 0;
+    if (i + 4 <= row) {
+        __builtin_memcpy(&v, p + i, 4);
+    } else {
+        for (int j = 0; j < 4; ++j)
+            if (i + j < row) v |= (uint32_t)p[i + j] << (8 * j);
+    }
+    return v;
+}
+
+// Bytes of a 64-row tile, transposed: column c of row r at lds[c * 72 + r] (72: rows of eight-byte
+// units spread over the banks).  A thread writes the four columns of a dword it has read.
+__device__ __forceinline__ void put_column_bytes(uint8_t* lds, int r, int c, uint32_t v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lds[(c + j) * 72 + r] = (uint8_t)(v >> (8 * j));
+}
+
+// W_hat^T in fp16 [K, Lx], 64 weight rows x 256 columns k per workgroup: every lane writes eight
+// rows' weights at four columns.  Codes 0, 1, 2 are -1, 0, 1: fp16 high bytes 0xBC, 0x00, 0x3C.
+__device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint8_t* lds) {
+    const int64_t k0 = b % kt * 256, l0 = b / kt * 64;
+    const int q = l0 >= p.Np;
+    const int64_t n0 = l0 - q * p.Np, rowb = a.K >> 2;
+    const uint8_t* w = q ? a.w1 : a.w0;
+    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
+        const int r = i >> 4, c = 4 * (i & 15);
+        const int64_t n = n0 + r;
+        put_column_bytes(lds, r, c, n < a.N ? row_dword(w + n * rowb, (k0 >> 2) + c, rowb) : 0x55555555u);
+    }
+    __syncthreads();
+    const int u = threadIdx.x & 7;
+    for (int c = threadIdx.x >> 3; c < 64; c += 32) {
+        const uint2 v = *reinterpret_cast<const uint2*>(lds + c * 72 + 8 * u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t k = k0 + 4 * c + i;
+            if (k >= a.K) break;
+            const uint32_t h0 = __builtin_amdgcn_perm(0u, 0x003C00BCu, (v.x >> (2 * i)) & 0x03030303u);
+            const uint32_t h1 = __builtin_amdgcn_perm(0u, 0x003C00BCu, (v.y >> (2 * i)) & 0x03030303u);
+            const u32x4 o = {__builtin_amdgcn_perm(0u, h0, 0x010C000Cu), __builtin_amdgcn_perm(0u, h0, 0x030C020Cu),
+                             __builtin_amdgcn_perm(0u, h1, 0x010C000Cu), __builtin_amdgcn_perm(0u, h1, 0x030C020Cu)};
+            *reinterpret_cast<u32x4*>(p.wt + k * p.Lx + l0 + 8 * u) = o;
+        }
+    }
+}
+
+// x_q^T in fp16 [K, Mp], 64 tokens x 64 columns per workgroup.
+__device__ __forceinline__ void codes_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint8_t* lds) {
+    const int64_t k0 = b % kt * 64, m0 = b / kt * 64;
+    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
+        const int r = i >> 4, c = 4 * (i & 15);
+        const int64_t m = m0 + r;
+        put_column_bytes(lds, r, c, m < a.M ? row_dword(reinterpret_cast<const uint8_t*>(a.xq) + m * a.K, k0 + c, a.K) : 0u);
+    }
+    __syncthreads();
+    const int u = threadIdx.x & 7;
+    for (int c = threadIdx.x >> 3; c < 64; c += 32) {
+        if (k0 + c >= a.K) break;
+        const int8_t* v = reinterpret_cast<const int8_t*>(lds + c * 72 + 8 * u);
+        f16x8 o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = (_Float16)(float)v[j];
+        *reinterpret_cast<f16x8*>(p.cd + (k0 + c) * p.Mp + m0 + 8 * u) = o;
+    }
+}
+
+template <int ACT>
+__global__ __launch_bounds__(256) void k_grad_prep(BackwardArgs a, GradPlan p, int64_t maxima, int64_t weights, int64_t ktw,
+                                                   int64_t ktc) {
+    constexpr int P = ACT == 0 ? 1 : 2;
+    __shared__ __align__(16) uint8_t lds[4 * P * 256 * 12];
+    const int64_t b = blockIdx.x;
+    if (b < maxima) max_tile<ACT>(a, p, b, lds);
+    else if (b < maxima + weights) weights_tile(a, p, b - maxima, ktw, lds);
+    else codes_tile(a, p, b - maxima - weights, ktc, lds);
+}
+
+// ---- step 2: columns (a thread each), then rows (a wave each) ------------------------------
+__global__ __launch_bounds__(256) void k_grad_reduce(BackwardArgs a, GradPlan p, int P, int64_t cblocks) {
+    const int64_t NT = P * a.N;
+    if (blockIdx.x < cblocks) {
+        const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        if (n >= NT) return;
+        float v = 0.0f;
+        for (int64_t t = 0; t < p.mt; ++t) v = fmaxf(v, p.cpart[t * NT + n]);
+        p.cmax[n] = v;
+        float* out = n < a.N ? a.db0 : a.db1;
+        if (!out) return;
+        double s = 0.0;
+        for (int64_t t = 0; t < p.mt; ++t) s += p.bpart[t * NT + n];
+        out[n < a.N ? n : n - a.N] = (float)s;
+    } else {
+        const int64_t m = ((int64_t)blockIdx.x - cblocks) * 4 + (threadIdx.x >> 6);
+        if (m >= a.M) return;
+        const int lane = threadIdx.x & 63;
+        float v = 0.0f;
+        for (int64_t t = lane; t < p.ct; t += 64) v = fmaxf(v, p.rpart[m * p.ct + t]);
+        v = wave_max_f32(v);
+        if (lane == 0) p.rmax[m] = v;
+    }
+}
+
+// ---- step 3 -------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t split_f16(float v) {
     const _Float16 hi = (_Float16)v;
     const _Float16 lo = (_Float16)(v - (float)hi);
     return (uint32_t)__builtin_bit_cast(uint16_t, hi) | (uint32_t)__builtin_bit_cast(uint16_t, lo) << 16;
 }
 
-// Scaled and split gradients, 64 tokens x 64 columns per workgroup: token-major as they are read,
-// channel-major through LDS.  Padded columns and tokens are written as zeros.
+// Scaled and split gradients, 64 tokens x 128 columns per workgroup of eight waves; a wave takes
+// eight tokens, a lane two neighbouring columns.  Token-major planes are written as they come (256
+// bytes a wave), channel-major ones through LDS (64 tokens, 128 bytes, a channel).  Padded columns
+// and tokens are written as zeros.
 template <int ACT>
-__global__ __launch_bounds__(256) void k_grad_split(BackwardArgs a, GradPlan p, int ctiles) {
+__global__ __launch_bounds__(512) void k_grad_split(BackwardArgs a, GradPlan p, int ctiles) {
     constexpr int P = ACT == 0 ? 1 : 2;
-    __shared__ uint32_t tile[P][64][65];
+    __shared__ uint32_t tile[P][128][65];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n0 = (int64_t)(blockIdx.x % ctiles) * 64, m0 = (int64_t)(blockIdx.x / ctiles) * 64;
-    const int64_t n = n0 + lane;
+    const int64_t n0 = (int64_t)(blockIdx.x % ctiles) * 128, m0 = (int64_t)(blockIdx.x / ctiles) * 64;
+    const int64_t n = n0 + 2 * lane;
     const float al[2] = {a.al0[0], ACT == 0 ? 0.0f : a.al1[0]};
-    float cscale[P];
+    float cscale[P][2];
 #pragma unroll
-    for (int q = 0; q < P; ++q) cscale[q] = n < a.N ? pow2f(scale_exponent(__uint_as_float(p.cmax[q * a.N + n]))) : 0.0f;
-    for (int t = 0; t < 16; ++t) {
-        const int64_t m = m0 + 16 * wave + t;
-        float d[2] = {0.0f, 0.0f}, bs = 0.0f, rscale = 0.0f;
+    for (int q = 0; q < P; ++q)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) cscale[q][c] = n + c < a.N ? pow2f(scale_exponent(p.cmax[q * a.N + n + c])) : 0.0f;
+#pragma unroll 4
+    for (int t = 0; t < 8; ++t) {
+        const int64_t m = m0 + 8 * wave + t;
+        float d[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, bs = 0.0f, rscale = 0.0f;   // d[column][projection]
         if (m < a.M) {
             bs = a.beta[m] / 127.0f;
-            rscale = pow2f(scale_exponent(__uint_as_float(p.rmax[m])));
-            if (n < a.N) grad_at<ACT>(a, m * a.N + n, d);
+            rscale = pow2f(scale_exponent(p.rmax[m]));
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                if (n + c < a.N) grad_at<ACT>(a, m * a.N + n + c, d[c]);
         }
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            if (a.dx && m < a.M) {
-                const uint32_t v = split_f16(d[q] * al[q] * rscale);
-                reinterpret_cast<uint16_t*>(p.xh)[m * p.Lx + q * p.Np + n] = (uint16_t)v;
-                reinterpret_cast<uint16_t*>(p.xl)[m * p.Lx + q * p.Np + n] = (uint16_t)(v >> 16);
+            if (a.dx && m < a.M && n < p.Np) {
+                const uint32_t v0 = split_f16(d[0][q] * al[q] * rscale), v1 = split_f16(d[1][q] * al[q] * rscale);
+                const int64_t o = (m * p.Lx + q * p.Np + n) / 2;
+                reinterpret_cast<uint32_t*>(p.xh)[o] = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
+                reinterpret_cast<uint32_t*>(p.xl)[o] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
             }
-            tile[q][lane][16 * wave + t] = split_f16(d[q] * bs * cscale[q]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tile[q][2 * lane + c][8 * wave + t] = split_f16(d[c][q] * bs * cscale[q][c]);
         }
     }
     if (!a.dw0) return;
     __syncthreads();
+    const int u = threadIdx.x & 7;
 #pragma unroll
     for (int q = 0; q < P; ++q)
-        for (int r = wave; r < 64; r += 4) {
+        for (int r = threadIdx.x >> 3; r < 128; r += 64) {
             if (n0 + r >= a.N) break;
-            const uint32_t v = tile[q][r][lane];
-            const int64_t o = (q * a.N + n0 + r) * p.Mp + m0 + lane;
-            reinterpret_cast<uint16_t*>(p.wh)[o] = (uint16_t)v;
-            reinterpret_cast<uint16_t*>(p.wl)[o] = (uint16_t)(v >> 16);
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = tile[q][r][8 * u + j];
+            u32x4 h, l;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], 0x05040100u);
+                l[j] = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], 0x07060302u);
+            }
+            const int64_t o = (q * a.N + n0 + r) * p.Mp + m0 + 8 * u;
+            *reinterpret_cast<u32x4*>(p.wh + o) = h;
+            *reinterpret_cast<u32x4*>(p.wl + o) = l;
         }
 }
 
-// W_hat^T in fp16, [K, Lx]: 64 weight rows x 64 columns k per workgroup.  Codes 0, 1, 2 become -1, 0, 1.
-__global__ __launch_bounds__(256) void k_weights_t(BackwardArgs a, GradPlan p, int ktiles) {
-    __shared__ uint8_t tile[64][20];
-    const int64_t k0 = (int64_t)(blockIdx.x % ktiles) * 64, l0 = (int64_t)(blockIdx.x / ktiles) * 64;
-    const int q = l0 >= p.Np;
-    const int64_t n0 = l0 - q * p.Np, rowb = a.K >> 2;
-    const uint8_t* w = q ? a.w1 : a.w0;
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-        const int r = i >> 4, b = i & 15;
-        const int64_t n = n0 + r, kb = (k0 >> 2) + b;
-        tile[r][b] = n < a.N && kb < rowb ? w[n * rowb + kb] : (uint8_t)0x55;
-    }
-    __syncthreads();
-    const int r = threadIdx.x & 63;
-    for (int j = threadIdx.x >> 6; j < 64; j += 4) {
-        if (k0 + j >= a.K) break;
-        const int c = (tile[r][j >> 2] >> (2 * (j & 3))) & 3;
-        p.wt[(k0 + j) * p.Lx + l0 + r] = (_Float16)(float)(c - 1);
-    }
-}
-
-// x_q^T in fp16, [K, Mp]: 64 tokens x 64 columns per workgroup.
-__global__ __launch_bounds__(256) void k_codes_t(BackwardArgs a, GradPlan p, int ktiles) {
-    __shared__ int8_t tile[64][68];
-    const int64_t k0 = (int64_t)(blockIdx.x % ktiles) * 64, m0 = (int64_t)(blockIdx.x / ktiles) * 64;
-    const int lane = threadIdx.x & 63;
-    for (int r = threadIdx.x >> 6; r < 64; r += 4)
-        tile[r][lane] = m0 + r < a.M && k0 + lane < a.K ? a.xq[(m0 + r) * a.K + k0 + lane] : (int8_t)0;
-    __syncthreads();
-    for (int j = threadIdx.x >> 6; j < 64; j += 4) {
-        if (k0 + j >= a.K) break;
-        p.ct[(k0 + j) * p.Mp + m0 + lane] = (_Float16)(float)tile[lane][j];
-    }
-}
-
+// ---- step 4 -------------------------------------------------------------------------------
 struct SplitArgs {
     const _Float16 *ah, *al;       // [I, L] hi and lo planes
     const _Float16* b;             // [J, L]
-    const uint32_t* amax;          // [I] bits of the rows' largest elements
+    const float* amax;             // [I] the rows' largest elements
     int64_t I, J, L;               // L a multiple of 64
     float *c0, *c1;                // rows below I0 go to c0 [I0, J], the others to c1
     int64_t I0;
@@ -290,50 +387,60 @@ struct SplitArgs {
 // loads that go past the registers; a stage is loaded while the other is multiplied.  Unit u (16
 // bytes) of row r lies at slot u ^ ((r / 2) % 4) of its row, so that eight consecutive lanes of an
 // operand read (eight rows, one unit) meet eight different bank groups.
-__global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs a) {
-    __shared__ i32x4 st0[2048];
-    __shared__ i32x4 st1[2048];
+template <int WI, int STAGES>
+__global__ __launch_bounds__(128 * WI, 2) void k_split_gemm(SplitArgs x, SplitArgs w) {
+    // the workgroups of the first product, then those of the second
+    const int TX = x.parts * x.tiles_i * x.tiles_j;
+    const bool first = blockIdx.x < TX;
+    const SplitArgs& a = first ? x : w;
+    const int blk = first ? blockIdx.x : blockIdx.x - TX;
+    constexpr int BM = 64 * WI, BN = SG_BN, WAVES = 2 * WI;
+    constexpr int AB = BM / 16 / WAVES, BB = BN / 16 / WAVES;        // load instructions of a wave: hi (or lo) rows, b rows
+    constexpr int OL = BM * 4, OB = BM * 8, UNITS = OB + BN * 4;     // units: lo, b, a stage
+    __shared__ i32x4 st0[UNITS];
+    __shared__ i32x4 st1[UNITS];
+    __shared__ i32x4 st2[STAGES == 3 ? UNITS : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // consecutive workgroups go to the eight XCDs in turn: give each XCD a contiguous run of tiles,
     // four rows of tiles at a time, so that its L2 holds the panels its workgroups share
     const int T = a.parts * a.tiles_i * a.tiles_j;
-    const int xcd = blockIdx.x & 7, per = T >> 3, rem = T & 7;
-    int t = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+    const int xcd = blk & 7, per = T >> 3, rem = T & 7;
+    int t = xcd * per + (xcd < rem ? xcd : rem) + (blk >> 3);
     const int part = t / (a.tiles_i * a.tiles_j);
     t -= part * a.tiles_i * a.tiles_j;
     const int grp = t / (4 * a.tiles_j), gi = a.tiles_i - 4 * grp < 4 ? a.tiles_i - 4 * grp : 4;
     t -= grp * 4 * a.tiles_j;
-    const int64_t i0 = (int64_t)(4 * grp + t % gi) * SG_BM, j0 = (int64_t)(t / gi) * SG_BN;
+    const int64_t i0 = (int64_t)(4 * grp + t % gi) * BM, j0 = (int64_t)(t / gi) * BN;
     const int KS = (int)(a.L / SG_BK);
     const int ks0 = (int)((int64_t)KS * part / a.parts), ks1 = (int)((int64_t)KS * (part + 1) / a.parts);
 
     // loads: instruction q of a wave fills 64 slots (16 rows); rows past the end repeat the last one
-    const int lrow = lane >> 2, unit = (lane & 3) ^ ((lane >> 3) & 3);
+    const int lrow = lane >> 2, unit = (lane & 3) ^ ((lane >> 4) & 3) ^ (((lane >> 3) & 1) << 1);
     const uint32_t ldb = (uint32_t)(a.L * 2);
-    const int64_t rows_i = a.I - i0 < SG_BM ? a.I - i0 : SG_BM, rows_j = a.J - j0 < SG_BN ? a.J - j0 : SG_BN;
+    const int64_t rows_i = a.I - i0 < BM ? a.I - i0 : BM, rows_j = a.J - j0 < BN ? a.J - j0 : BN;
     const __amdgpu_buffer_rsrc_t rh = raw_buffer(a.ah + i0 * a.L, (uint32_t)rows_i * ldb);
     const __amdgpu_buffer_rsrc_t rl = raw_buffer(a.al + i0 * a.L, (uint32_t)rows_i * ldb);
     const __amdgpu_buffer_rsrc_t rb = raw_buffer(a.b + j0 * a.L, (uint32_t)rows_j * ldb);
-    uint32_t ao[2], bo[4];
+    uint32_t ao[AB], bo[BB];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int r = 16 * (2 * wave + q) + lrow;
+    for (int q = 0; q < AB; ++q) {
+        const int r = 16 * (AB * wave + q) + lrow;
         ao[q] = (uint32_t)(r < rows_i ? r : (int)rows_i - 1) * ldb + 16u * unit;
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int r = 16 * (4 * wave + q) + lrow;
+    for (int q = 0; q < BB; ++q) {
+        const int r = 16 * (BB * wave + q) + lrow;
         bo[q] = (uint32_t)(r < rows_j ? r : (int)rows_j - 1) * ldb + 16u * unit;
     }
     auto fetch = [&](i32x4* st, int ks) {
         const uint32_t so = (uint32_t)ks * (SG_BK * 2);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) load_lds16(rh, ao[q], so, st + 64 * (2 * wave + q));
+        for (int q = 0; q < AB; ++q) load_lds16(rh, ao[q], so, st + 64 * (AB * wave + q));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) load_lds16(rl, ao[q], so, st + 512 + 64 * (2 * wave + q));
+        for (int q = 0; q < AB; ++q) load_lds16(rl, ao[q], so, st + OL + 64 * (AB * wave + q));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) load_lds16(rb, bo[q], so, st + 1024 + 64 * (4 * wave + q));
+        for (int q = 0; q < BB; ++q) load_lds16(rb, bo[q], so, st + OB + 64 * (BB * wave + q));
         __builtin_amdgcn_sched_barrier(0);         // issued here, not where their data is needed
     };
 
@@ -342,51 +449,93 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs a) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-    const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5;
-    const int sw = (lr >> 1) & 3;
+    const int wi = wave % WI, wj = wave / WI, lr = lane & 31, lg = lane >> 5;
+    const int sw = ((lr >> 2) & 3) ^ (((lr >> 1) & 1) << 1);
     auto multiply = [&](const i32x4* st) {
         f16x8 fh[2][2], fl[2][2], fb[2][4];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             const int s = (2 * kk + lg) ^ sw;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fb[kk][j] = __builtin_bit_cast(f16x8, st[1024 + (128 * wj + 32 * j + lr) * 4 + s]);
+            for (int j = 0; j < 4; ++j) fb[kk][j] = __builtin_bit_cast(f16x8, st[OB + (128 * wj + 32 * j + lr) * 4 + s]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 fh[kk][i] = __builtin_bit_cast(f16x8, st[(64 * wi + 32 * i + lr) * 4 + s]);
-                fl[kk][i] = __builtin_bit_cast(f16x8, st[512 + (64 * wi + 32 * i + lr) * 4 + s]);
+                fl[kk][i] = __builtin_bit_cast(f16x8, st[OL + (64 * wi + 32 * i + lr) * 4 + s]);
             }
         }
+#ifndef VORD
+#define VORD 0
+#endif
+#define MFH(i,j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fh[kk][i], fb[kk][j], acc[i][j], 0, 0, 0)
+#define MFL(i,j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[kk][i], fb[kk][j], acc[i][j], 0, 0, 0)
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < 2; ++kk) {
+            if (VORD == 0) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fh[kk][i], fb[kk][j], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[kk][i], fb[kk][j], acc[i][j], 0, 0, 0);
-                }
+                for (int j = 0; j < 4; ++j) { MFH(i,j); MFL(i,j); }
+            } else if (VORD == 1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) { MFH(i,j); __builtin_amdgcn_sched_barrier(0); }
+#pragma unroll
+                for (int j = 3; j >= 0; --j) { MFL(i,j); __builtin_amdgcn_sched_barrier(0); }
+            }
+            } else if (VORD == 2) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  MFH(0,j); __builtin_amdgcn_sched_barrier(0); MFH(1,j);__builtin_amdgcn_sched_barrier(0); MFL(0,j);__builtin_amdgcn_sched_barrier(0); MFL(1,j); __builtin_amdgcn_sched_barrier(0);}
+            }
+        }
     };
-    // every load into a stage has landed, for every wave, and every read of the other stage is over
-    auto turn = [&]() {
+    // the loads of the stage to be read have landed, for every wave, and every read of the stage
+    // to be filled is over
+    auto turn = [&](bool next_in_flight) {
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0x0070);        // vmcnt(0) lgkmcnt(0)
+        if (STAGES == 3 && next_in_flight) __builtin_amdgcn_s_waitcnt(0x0070 | (2 * AB + BB));   // vmcnt(a stage's loads) lgkmcnt(0)
+        else __builtin_amdgcn_s_waitcnt(0x0070);                                                // vmcnt(0) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
     int ks = ks0;
-    if (ks < ks1) fetch(st0, ks);
-    for (; ks + 2 <= ks1; ks += 2) {
-        turn();
-        fetch(st1, ks + 1);
-        multiply(st0);
-        turn();
-        if (ks + 2 < ks1) fetch(st0, ks + 2);
-        multiply(st1);
-    }
-    if (ks < ks1) {
-        turn();
-        multiply(st0);
+    if constexpr (STAGES == 2) {
+        if (ks < ks1) fetch(st0, ks);
+        for (; ks + 2 <= ks1; ks += 2) {
+            turn(false);
+            fetch(st1, ks + 1);
+            multiply(st0);
+            turn(false);
+            if (ks + 2 < ks1) fetch(st0, ks + 2);
+            multiply(st1);
+        }
+        if (ks < ks1) {
+            turn(false);
+            multiply(st0);
+        }
+    } else {
+        if (ks < ks1) fetch(st0, ks);
+        if (ks + 1 < ks1) fetch(st1, ks + 1);
+        for (; ks + 3 <= ks1; ks += 3) {
+            turn(true);
+            fetch(st2, ks + 2);
+            multiply(st0);
+            turn(true);
+            if (ks + 3 < ks1) fetch(st0, ks + 3);
+            multiply(st1);
+            turn(ks + 3 < ks1);
+            if (ks + 4 < ks1) fetch(st1, ks + 4);
+            multiply(st2);
+        }
+        if (ks < ks1) {
+            turn(ks + 1 < ks1);
+            multiply(st0);
+        }
+        if (ks + 1 < ks1) {
+            turn(false);
+            multiply(st1);
+        }
     }
 
     // accumulator r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4 of the block, column l % 32
@@ -401,7 +550,7 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs a) {
             if (a.parts > 1) {
                 out = a.part + ((int64_t)part * a.I + row) * a.J;
             } else {
-                inv = pow2f(-scale_exponent(__uint_as_float(a.amax[row])));
+                inv = pow2f(-scale_exponent(a.amax[row]));
                 out = row < a.I0 ? a.c0 + row * a.J : a.c1 + (row - a.I0) * a.J;
             }
 #pragma unroll
@@ -412,36 +561,18 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs a) {
         }
 }
 
-// The parts of a sum added in their order, scaled back.
-__global__ __launch_bounds__(256) void k_split_sum(SplitArgs a) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, n = a.I * a.J;
+// ---- step 5: the parts of a sum added in their order, scaled back ---------------------------
+__global__ __launch_bounds__(256) void k_split_sum(SplitArgs x, SplitArgs w, int64_t xblocks) {
+    const bool first = blockIdx.x < xblocks;
+    const SplitArgs& a = first ? x : w;
+    const int64_t e = ((int64_t)blockIdx.x - (first ? 0 : xblocks)) * 256 + threadIdx.x, n = a.I * a.J;
     if (e >= n) return;
     const int64_t row = e / a.J;
     float s = 0.0f;
     for (int q = 0; q < a.parts; ++q) s += a.part[q * n + e];
-    s *= pow2f(-scale_exponent(__uint_as_float(a.amax[row])));
+    s *= pow2f(-scale_exponent(a.amax[row]));
     if (row < a.I0) a.c0[e] = s;
     else a.c1[e - a.I0 * a.J] = s;
-}
-
-static hipError_t launch_split(SplitArgs a, hipStream_t s) {
-    a.tiles_i = (int)((a.I + SG_BM - 1) / SG_BM);
-    a.tiles_j = (int)((a.J + SG_BN - 1) / SG_BN);
-    const int64_t grid = (int64_t)a.parts * a.tiles_i * a.tiles_j;
-    hipLaunchKernelGGL(k_split_gemm, dim3((unsigned)grid), dim3(256), 0, s, a);
-    if (a.parts > 1) hipLaunchKernelGGL(k_split_sum, dim3((unsigned)((a.I * a.J + 255) / 256)), dim3(256), 0, s, a);
-    return hipGetLastError();
-}
-
-// Column sums from the 64-token partial sums, in token order.
-__global__ __launch_bounds__(256) void k_bias_sum(BackwardArgs a, GradPlan p, int P) {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, NT = P * a.N;
-    if (n >= NT) return;
-    float* out = n < a.N ? a.db0 : a.db1;
-    if (!out) return;
-    double s = 0.0;
-    for (int64_t t = 0; t < p.Mp / 64; ++t) s += p.bias_part[t * NT + n];
-    out[n < a.N ? n : n - a.N] = (float)s;
 }
 
 template <int ACT>
@@ -449,24 +580,26 @@ static hipError_t launch_grads(const BackwardArgs& a, hipStream_t s) {
     constexpr int P = ACT == 0 ? 1 : 2;
     const GradPlan p = grad_plan(a.M, a.K, a.N, P == 2, a.ws);
     auto blocks = [](int64_t n) { return dim3((unsigned)n); };
-    const int64_t nmax = a.M + P * a.N;
-    hipLaunchKernelGGL(k_zero, blocks((nmax + 255) / 256), dim3(256), 0, s, p.rmax, nmax);
-    const int64_t mt = p.Mp / 64, ct256 = (a.N + 255) / 256, ct64 = p.Np / 64, kt = (a.K + 63) / 64;
-    hipLaunchKernelGGL(k_grad_max<ACT>, blocks(mt * ct256), dim3(256), 0, s, a, p, (int)ct256);
-    if (a.dx || a.dw0) hipLaunchKernelGGL(k_grad_split<ACT>, blocks(mt * ct64), dim3(256), 0, s, a, p, (int)ct64);
-    if (a.dx) {
-        hipLaunchKernelGGL(k_weights_t, blocks(p.Lx / 64 * kt), dim3(256), 0, s, a, p, (int)kt);
-        const hipError_t e = launch_split(SplitArgs{p.xh, p.xl, p.wt, p.rmax, a.M, a.K, p.Lx, a.dx, nullptr, a.M, p.part,
-                                                    p.parts_x, 0, 0}, s);
-        if (e != hipSuccess) return e;
-    }
-    if (a.dw0) {
-        hipLaunchKernelGGL(k_codes_t, blocks(mt * kt), dim3(256), 0, s, a, p, (int)kt);
-        const hipError_t e = launch_split(SplitArgs{p.wh, p.wl, p.ct, p.cmax, P * a.N, a.K, p.Mp, a.dw0, a.dw1, a.N, p.part,
-                                                    p.parts_w, 0, 0}, s);
-        if (e != hipSuccess) return e;
-    }
-    if (a.db0 || a.db1) hipLaunchKernelGGL(k_bias_sum, blocks((P * a.N + 255) / 256), dim3(256), 0, s, a, p, P);
+    const int64_t ktw = (a.K + 255) / 256, ktc = (a.K + 63) / 64;
+    const int64_t maxima = p.mt * p.ct, weights = a.dx ? p.Lx / 64 * ktw : 0, codes = a.dw0 ? p.Mp / 64 * ktc : 0;
+    hipLaunchKernelGGL(k_grad_prep<ACT>, blocks(maxima + weights + codes), dim3(256), 0, s, a, p, maxima, weights, ktw, ktc);
+    const int64_t cblocks = (P * a.N + 255) / 256;
+    hipLaunchKernelGGL(k_grad_reduce, blocks(cblocks + (a.M + 3) / 4), dim3(256), 0, s, a, p, P, cblocks);
+    if (!a.dx && !a.dw0) return hipGetLastError();
+    const int64_t ct = (a.N + 127) / 128;
+    hipLaunchKernelGGL(k_grad_split<ACT>, blocks(p.Mp / 64 * ct), dim3(512), 0, s, a, p, (int)ct);
+    auto tiles = [](SplitArgs q) {
+        q.tiles_i = (int)((q.I + SG_BM - 1) / SG_BM);
+        q.tiles_j = (int)((q.J + SG_BN - 1) / SG_BN);
+        return q;
+    };
+    SplitArgs x{}, w{};
+    if (a.dx) x = tiles(SplitArgs{p.xh, p.xl, p.wt, p.rmax, a.M, a.K, p.Lx, a.dx, nullptr, a.M, p.part_x, p.parts_x, 0, 0});
+    if (a.dw0) w = tiles(SplitArgs{p.wh, p.wl, p.cd, p.cmax, P * a.N, a.K, p.Mp, a.dw0, a.dw1, a.N, p.part_w, p.parts_w, 0, 0});
+    const int64_t grid = (int64_t)x.parts * x.tiles_i * x.tiles_j + (int64_t)w.parts * w.tiles_i * w.tiles_j;
+    hipLaunchKernelGGL((k_split_gemm<SG_WI, 2>), blocks(grid), dim3(128 * SG_WI), 0, s, x, w);
+    const int64_t xb = x.parts > 1 ? (x.I * x.J + 255) / 256 : 0, wb = w.parts > 1 ? (w.I * w.J + 255) / 256 : 0;
+    if (xb + wb) hipLaunchKernelGGL(k_split_sum, blocks(xb + wb), dim3(256), 0, s, x, w, xb);
     return hipGetLastError();
 }
 

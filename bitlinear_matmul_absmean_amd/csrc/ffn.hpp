@@ -22,14 +22,14 @@ __device__ __forceinline__ float act_value(float g) {
 
 // a(g) and a'(g) for the gradients, to a few fp32 roundings.
 //   SiLU: with e = exp(-|g|), s(|g|) = 1 / (1 + e) and s(-|g|) = e / (1 + e), so neither
-//     logistic value is formed as a difference; a = g s(g), a' = s(g) + a s(-g).
+//     logistic value is formed as a difference (the reciprocal is the hardware's, within one unit); a = g s(g), a' = s(g) + a s(-g).
 //   GELU: a = g Phi(g), a' = Phi(g) + g phi(g) in fp64 (Phi from the erfc polynomial of the
 //     forward pass, whose tail below g = -8 is off relative to itself but below 1e-14).
 //   Squared ReLU: a = r^2, a' = 2 r.
 template <int ACT>
 __device__ __forceinline__ void act_grad(float g, float& a, float& slope) {
     if constexpr (ACT == BITLINEAR_ACT_SILU) {
-        const float e = expf(-fabsf(g)), t = 1.0f / (1.0f + e), p = e * t;
+        const float e = expf(-fabsf(g)), t = __builtin_amdgcn_rcpf(1.0f + e), p = e * t;
         const float s = g >= 0.0f ? t : p, sc = g >= 0.0f ? p : t;
         a = g * s;
         slope = s + a * sc;
