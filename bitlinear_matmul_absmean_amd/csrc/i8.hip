@@ -3,6 +3,13 @@
 // What is computed: acc[m, n] = sum_k x_q[m, k] W_q[n, k]  (int32, exact),
 //     y[m, n] = (fp32(acc) * fp32(beta[m] / 127)) * fp32(gamma[n] / 127)  (+ bias[n]),
 // every step one fp32 rounding.
+//
+// Three kernels by the number of tokens, each in a form for aligned rows (16-byte aligned tensors,
+// K % 16 == 0) and one for any K and alignment:
+//   * one token: k_i8_gemv, the weight stream against x_q in LDS, on v_dot4_i32_i8;
+//   * few tokens: k_i8_dec, the weight stream on the 16x16x64 int8 MFMA, the waves of a workgroup
+//     taking turns along K;
+//   * many: k_i8_gemm, LDS tiles on the 32x32x32 int8 MFMA.
 #include "ffn.hpp"
 
 namespace bitlinear {
@@ -10,31 +17,407 @@ namespace bitlinear {
 // Scale of a token or a channel: fp32(s / 127), an IEEE division.
 __device__ __forceinline__ float i8_scale(float s) { return s / 127.0f; }
 
-__device__ __forceinline__ float i8_dequant(int acc, float bs, float gs, const float* __restrict__ bias, int64_t n) {
+// Output (m, n) from its sum, with the token's and the channel's scale.
+__device__ __forceinline__ void i8_store(const I8Args& a, int64_t m, int64_t n, int acc, float bs, float gs, float bias) {
     float v = (float)acc * bs * gs;
-    if (bias) v = v + bias[n];
+    if (a.bias) v = v + bias;
+    a.y[m * a.N + n] = v;
+    if (a.acc) a.acc[m * a.N + n] = acc;
+}
+
+// 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.
+__device__ __forceinline__ i32x4 row_16(const int8_t* __restrict__ p, int64_t i, int64_t row) {
+    i32x4 v = {0, 0, 0, 0};
+    if (i + 16 <= row) {
+        __builtin_memcpy(&v, p + i, 16);
+    } else {
+        for (int j = 0; j < 16; ++j)
+            if (i + j < row) v[j >> 2] |= (int)((uint32_t)(uint8_t)p[i + j] << (8 * (j & 3)));
+    }
     return v;
 }
 
-// One wave per output column, lanes over k; any K, any alignment.
-__global__ __launch_bounds__(256) void k_i8_generic(I8Args a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (n >= a.N) return;
-    for (int64_t m = 0; m < a.M; ++m) {
-        int s = 0;
-        for (int64_t k = lane; k < a.K; k += 64) s += (int)a.xq[m * a.K + k] * (int)a.wq[n * a.K + k];
-        s = wave_sum_i32(s);
-        if (lane == 0) {
-            a.y[m * a.N + n] = i8_dequant(s, i8_scale(a.beta[m]), i8_scale(a.gamma[n]), a.bias, n);
-            if (a.acc) a.acc[m * a.N + n] = s;
+// ---- one token ------------------------------------------------------------------------------
+// A wave takes R weight rows, 1 KiB of each at a time, so that R loads of 16 bytes a lane are in
+// flight while the last ones meet x_q, which lies in LDS as it is (zeros up to the next KiB).
+template <bool ALIGNED, int R>
+__global__ __launch_bounds__(256) void k_i8_gemv(I8Args a) {
+    extern __shared__ i32x4 xs[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t K = a.K, r0 = ((int64_t)blockIdx.x * 4 + wave) * R;
+    const int chunks = (int)((K + 1023) / 1024);
+    const int8_t* w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = a.wq + (r0 + r < a.N ? r0 + r : a.N - 1) * K;
+    auto load = [&](i32x4 (&v)[R], int c) {
+        const int64_t k = (int64_t)c * 1024 + 16 * lane;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            // past the row's end x_q is zero: any bytes will do, the row's first for aligned rows
+            if constexpr (ALIGNED) v[r] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(w[r] + (k < K ? k : 0)));
+            else v[r] = row_16(w[r], k, K);
+        }
+    };
+    i32x4 v0[R], v1[R];
+    load(v0, 0);
+    for (int i = tid; i < chunks * 64; i += 256) xs[i] = row_16(a.xq, (int64_t)i * 16, K);
+    __syncthreads();
+    int s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = 0;
+    auto dot = [&](const i32x4 (&v)[R], int c) {
+        const i32x4 x = xs[c * 64 + lane];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[r] = dot4((uint32_t)v[r][j], (uint32_t)x[j], s[r]);
+    };
+    for (int c = 0; c < chunks; c += 2) {
+        if (c + 1 < chunks) load(v1, c + 1);
+        dot(v0, c);
+        if (c + 1 >= chunks) break;
+        if (c + 2 < chunks) load(v0, c + 2);
+        dot(v1, c + 1);
+    }
+    int mine = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int t = wave_sum_i32(s[r]);
+        if (lane == r) mine = t;
+    }
+    const int64_t n = r0 + lane;
+    if (lane < R && n < a.N) i8_store(a, 0, n, mine, i8_scale(a.beta[0]), i8_scale(a.gamma[n]), a.bias ? a.bias[n] : 0.0f);
+}
+
+template <bool ALIGNED>
+static hipError_t launch_i8_gemv(const I8Args& a, hipStream_t s) {
+    constexpr int R = 4;
+    const size_t lds = (size_t)((a.K + 1023) / 1024) * 1024;
+    return launch_with_lds(k_i8_gemv<ALIGNED, R>, dim3((unsigned)((a.N + 4 * R - 1) / (4 * R))), dim3(256), lds, s, a);
+}
+
+// Position of 16-byte unit u (0..3) in the four slots of row r of an LDS tile of 64-byte rows: the
+// lanes of an operand read (16 rows or more, one unit each) then meet 16 different groups of banks.
+__device__ __forceinline__ int unit_swizzle(int r) { return ((r >> 2) & 3) ^ (((r >> 1) & 1) << 1); }
+
+// ---- few tokens -----------------------------------------------------------------------------
+// A workgroup of eight waves computes 16 MT tokens x 16 RB channels; wave w takes the steps of 64 k
+// w, w + 8, ..., and the eight partial tiles are added at the end (integers: exact in any order).
+// Aligned rows: each wave has a ring of three LDS images of a step (16-row blocks of 64 bytes a
+// row), filled by loads that go past the registers, two steps ahead; no wave waits for another.
+// Any K and alignment: operands straight into registers in the MFMA's layout.
+// 16x16x64 lane layout: A/B lane l holds row/column l % 16, k = 16 (l / 16) + j; accumulator r of
+// lane l is row 4 (l / 16) + r, column l % 16.
+constexpr int I8_WAVES = 8;
+
+template <bool ALIGNED, int MT, int RB>
+__global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) {
+    constexpr int IMG = (RB + MT) * 64;
+    __shared__ i32x4 st0[I8_WAVES * IMG];
+    __shared__ i32x4 st1[ALIGNED ? I8_WAVES * IMG : 1];
+    __shared__ i32x4 st2[ALIGNED ? I8_WAVES * IMG : 1];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t K = a.K;
+    const int64_t m0 = (int64_t)(blockIdx.x % slices) * (16 * MT), n0 = (int64_t)(blockIdx.x / slices) * (16 * RB);
+    const int rows_m = (int)(a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT), rows_n = (int)(a.N - n0 < 16 * RB ? a.N - n0 : 16 * RB);
+    const int8_t* x0 = a.xq + m0 * K;
+    const int8_t* w0 = a.wq + n0 * K;
+    const int steps = (int)((K + 63) / 64);
+    const int lr = lane & 15, lg = lane >> 4;
+    i32x4 acc[RB][MT];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[r][t] = i32x4{0, 0, 0, 0};
+    auto multiply = [&](const i32x4 (&x)[MT], const i32x4 (&w)[RB]) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[t], w[r], acc[r][t], 0, 0, 0);
+    };
+    if constexpr (ALIGNED) {
+        // lane l of a load fills slot l: row l / 4; rows past the end repeat the last one, and offsets
+        // past the buffers (the end of the last step when K % 64 != 0) are not read from memory
+        const int row = lane >> 2, unit = (lane & 3) ^ unit_swizzle(row);
+        const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
+        const __amdgpu_buffer_rsrc_t rw = raw_buffer(w0, (uint32_t)rows_n * (uint32_t)K);
+        uint32_t xo[MT], wo[RB];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) xo[t] = (uint32_t)min(16 * t + row, rows_m - 1) * (uint32_t)K + 16u * unit;
+#pragma unroll
+        for (int r = 0; r < RB; ++r) wo[r] = (uint32_t)min(16 * r + row, rows_n - 1) * (uint32_t)K + 16u * unit;
+        auto fetch = [&](i32x4* st, int s) {
+            i32x4* img = st + wave * IMG;
+#pragma unroll
+            for (int r = 0; r < RB; ++r) load_lds16(rw, wo[r], (uint32_t)s * 64u, img + 64 * r);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) load_lds16(rx, xo[t], (uint32_t)s * 64u, img + 64 * (RB + t));
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        const int at = lr * 4 + (lg ^ unit_swizzle(lr));
+        // step s from its image, `behind` later steps' loads being in flight
+        auto step = [&](const i32x4* st, int s, int behind) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (behind == 2) __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * (RB + MT));       // vmcnt(two steps' loads)
+            else if (behind == 1) __builtin_amdgcn_s_waitcnt(0x0F70 | (RB + MT));
+            else __builtin_amdgcn_s_waitcnt(0x0F70);                                   // vmcnt(0)
+            __builtin_amdgcn_sched_barrier(0);
+            const i32x4* img = st + wave * IMG + at;
+            i32x4 x[MT], w[RB];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) w[r] = img[64 * r];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) x[t] = img[64 * (RB + t)];
+            if ((int64_t)s * 64 + 64 > K) {
+                const bool live = (int64_t)s * 64 + 16 * lg < K;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) x[t] = live ? x[t] : i32x4{0, 0, 0, 0};
+            }
+            multiply(x, w);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // an image is filled again only after the multiplications that read it
+        constexpr int W = I8_WAVES;
+        int s = wave;
+        if (s < steps) fetch(st0, s);
+        if (s + W < steps) fetch(st1, s + W);
+        for (; s + 2 * W < steps; s += 3 * W) {
+            fetch(st2, s + 2 * W);
+            step(st0, s, 2);
+            const bool more3 = s + 3 * W < steps, more4 = s + 4 * W < steps;
+            if (more3) fetch(st0, s + 3 * W);
+            step(st1, s + W, more3 ? 2 : 1);
+            if (more4) fetch(st1, s + 4 * W);
+            step(st2, s + 2 * W, more4 ? 2 : more3 ? 1 : 0);
+        }
+        if (s < steps) step(st0, s, s + W < steps ? 1 : 0);
+        if (s + W < steps) step(st1, s + W, 0);
+    } else {
+        const int8_t *xp[MT], *wp[RB];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) xp[t] = x0 + (int64_t)min(16 * t + lr, rows_m - 1) * K;
+#pragma unroll
+        for (int r = 0; r < RB; ++r) wp[r] = w0 + (int64_t)min(16 * r + lr, rows_n - 1) * K;
+        for (int s = wave; s < steps; s += I8_WAVES) {
+            const int64_t k = (int64_t)s * 64 + 16 * lg;
+            i32x4 x[MT], w[RB];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) w[r] = row_16(wp[r], k, K);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) x[t] = row_16(xp[t], k, K);
+            multiply(x, w);
+        }
+    }
+    // the eight partial tiles through LDS, one block of 16 channels after another
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < MT; ++t) st0[(wave * MT + t) * 64 + lane] = acc[r][t];
+        __syncthreads();
+        for (int e = tid; e < MT * 64; e += 64 * I8_WAVES) {
+            const int l = e & 63, t = e >> 6, n = 16 * r + (l & 15);
+            i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < I8_WAVES; ++w) sum += st0[(w * MT + t) * 64 + l];
+            if (n >= rows_n) continue;
+            const float gs = i8_scale(a.gamma[n0 + n]), bias = a.bias ? a.bias[n0 + n] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = 16 * t + 4 * (l >> 4) + i;
+                if (m < rows_m) i8_store(a, m0 + m, n0 + n, sum[i], i8_scale(a.beta[m0 + m]), gs, bias);
+            }
         }
     }
 }
 
-hipError_t launch_forward_i8(const I8Args& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_i8_generic, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a);
+template <bool ALIGNED, int MT, int RB>
+static hipError_t launch_i8_dec_rb(const I8Args& a, hipStream_t s) {
+    const int64_t slices = (a.M + 16 * MT - 1) / (16 * MT), blocks = (a.N + 16 * RB - 1) / (16 * RB);
+    hipLaunchKernelGGL((k_i8_dec<ALIGNED, MT, RB>), dim3((unsigned)(slices * blocks)), dim3(64 * I8_WAVES), 0, s, a, (int)slices);
     return hipGetLastError();
+}
+
+// One block of 16 channels a workgroup while that leaves at most 256 workgroups, else two.
+template <bool ALIGNED, int MT>
+static hipError_t launch_i8_dec_mt(const I8Args& a, hipStream_t s) {
+    const int64_t wgs = (a.M + 16 * MT - 1) / (16 * MT) * ((a.N + 15) / 16);
+    return wgs <= 256 ? launch_i8_dec_rb<ALIGNED, MT, 1>(a, s) : launch_i8_dec_rb<ALIGNED, MT, 2>(a, s);
+}
+
+template <bool ALIGNED>
+static hipError_t launch_i8_dec(const I8Args& a, hipStream_t s) {
+    const int64_t tiles = (a.M + 15) / 16;
+    return tiles == 1   ? launch_i8_dec_mt<ALIGNED, 1>(a, s)
+           : tiles == 2 ? launch_i8_dec_mt<ALIGNED, 2>(a, s)
+           : tiles == 3 ? launch_i8_dec_mt<ALIGNED, 3>(a, s)
+                        : launch_i8_dec_mt<ALIGNED, 4>(a, s);
+}
+
+// ---- many tokens ----------------------------------------------------------------------------
+// A workgroup of eight waves computes 128 tokens x 256 channels, a wave 64 x 64 of them in 32 x 32
+// blocks, in steps of 64 k; three LDS stages (24 KiB each), filled two steps ahead (aligned rows:
+// by loads that go past the registers; else through registers, one step ahead).
+// 32x32x32 lane layout: A/B lane l holds row/column l % 32, k = 16 (l / 32) + j; accumulator r of
+// lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
+constexpr int IG_BM = 128, IG_BN = 256, IG_BK = 64;
+
+template <bool ALIGNED>
+__global__ __launch_bounds__(512, 4) void k_i8_gemm(I8Args a, int tiles_m, int tiles_n) {
+    constexpr int OB = IG_BM * 4, UNITS = OB + IG_BN * 4;
+    __shared__ i32x4 st0[UNITS];
+    __shared__ i32x4 st1[UNITS];
+    __shared__ i32x4 st2[UNITS];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // a contiguous run of tiles for each XCD, four rows of tiles at a time
+    const int T = tiles_m * tiles_n, xcd = blockIdx.x & 7, per = T >> 3, rem = T & 7;
+    int t = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+    const int grp = t / (4 * tiles_n), gm = tiles_m - 4 * grp < 4 ? tiles_m - 4 * grp : 4;
+    t -= grp * 4 * tiles_n;
+    const int64_t m0 = (int64_t)(4 * grp + t % gm) * IG_BM, n0 = (int64_t)(t / gm) * IG_BN;
+    const int64_t K = a.K;
+    const int rows_m = (int)(a.M - m0 < IG_BM ? a.M - m0 : IG_BM), rows_n = (int)(a.N - n0 < IG_BN ? a.N - n0 : IG_BN);
+    const int8_t* x0 = a.xq + m0 * K;
+    const int8_t* w0 = a.wq + n0 * K;
+    const int steps = (int)((K + IG_BK - 1) / IG_BK);
+
+    i32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
+    const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5, sw = unit_swizzle(lr);
+    auto multiply = [&](const i32x4* st, int s) {
+        i32x4 fa[2][2], fb[2][2];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const int u = 2 * kk + lg, at = u ^ sw;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) fb[kk][j] = st[OB + (64 * wj + 32 * j + lr) * 4 + at];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fa[kk][i] = st[(64 * wi + 32 * i + lr) * 4 + at];
+            if (ALIGNED && (int64_t)s * IG_BK + IG_BK > K) {
+                // past the end of its row an aligned load has read what follows it
+                const bool live = (int64_t)s * IG_BK + 16 * u < K;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) fa[kk][i] = live ? fa[kk][i] : i32x4{0, 0, 0, 0};
+            }
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[kk][i], fb[kk][j], acc[i][j], 0, 0, 0);
+    };
+    // load block q (of 24: 8 of x_q, 16 of W_q, 16 rows each): wave w takes 3 w .. 3 w + 2
+    const int row = lane >> 2, unit = (lane & 3) ^ unit_swizzle(row);
+    if constexpr (ALIGNED) {
+        const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
+        const __amdgpu_buffer_rsrc_t rw = raw_buffer(w0, (uint32_t)rows_n * (uint32_t)K);
+        uint32_t xo, wo[2];
+        xo = (uint32_t)min(16 * wave + row, rows_m - 1) * (uint32_t)K + 16u * unit;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) wo[q] = (uint32_t)min(16 * (2 * wave + q) + row, rows_n - 1) * (uint32_t)K + 16u * unit;
+        auto fetch = [&](i32x4* st, int s) {
+            const uint32_t so = (uint32_t)s * IG_BK;
+            load_lds16(rx, xo, so, st + 64 * wave);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (2 * wave + q));
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // step s has landed for every wave, and every read of the stage to be filled is over
+        auto turn = [&](bool next) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (next) __builtin_amdgcn_s_waitcnt(0x0070 | 3);      // vmcnt(3) lgkmcnt(0)
+            else __builtin_amdgcn_s_waitcnt(0x0070);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int s = 0;
+        fetch(st0, 0);
+        if (1 < steps) fetch(st1, 1);
+        for (; s + 3 <= steps; s += 3) {
+            turn(true);
+            fetch(st2, s + 2);
+            multiply(st0, s);
+            turn(true);
+            if (s + 3 < steps) fetch(st0, s + 3);
+            multiply(st1, s + 1);
+            turn(s + 3 < steps);
+            if (s + 4 < steps) fetch(st1, s + 4);
+            multiply(st2, s + 2);
+        }
+        if (s < steps) {
+            turn(s + 1 < steps);
+            multiply(st0, s);
+        }
+        if (s + 1 < steps) {
+            turn(false);
+            multiply(st1, s + 1);
+        }
+    } else {
+        const int8_t* xp = x0 + (int64_t)min(16 * wave + row, rows_m - 1) * K;
+        const int8_t* wp[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) wp[q] = w0 + (int64_t)min(16 * (2 * wave + q) + row, rows_n - 1) * K;
+        i32x4 v[3];
+        auto load = [&](int s) {
+            const int64_t k = (int64_t)s * IG_BK + 16 * unit;
+            v[0] = row_16(xp, k, K);
+            v[1] = row_16(wp[0], k, K);
+            v[2] = row_16(wp[1], k, K);
+        };
+        auto put = [&](i32x4* st) {
+            st[64 * wave + lane] = v[0];
+            st[OB + 64 * (2 * wave) + lane] = v[1];
+            st[OB + 64 * (2 * wave + 1) + lane] = v[2];
+        };
+        load(0);
+        put(st0);
+        for (int s = 0; s < steps; ++s) {
+            __syncthreads();                       // step s is in its stage, and the other stage is free
+            if (s + 1 < steps) load(s + 1);
+            multiply(s & 1 ? st1 : st0, s);
+            if (s + 1 < steps) put(s & 1 ? st0 : st1);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int n = 64 * wj + 32 * j + lr;
+        if (n >= rows_n) continue;
+        const float gs = i8_scale(a.gamma[n0 + n]), bias = a.bias ? a.bias[n0 + n] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int m = 64 * wi + 32 * i + 8 * (r / 4) + 4 * lg + r % 4;
+                if (m < rows_m) i8_store(a, m0 + m, n0 + n, acc[i][j][r], i8_scale(a.beta[m0 + m]), gs, bias);
+            }
+    }
+}
+
+template <bool ALIGNED>
+static hipError_t launch_i8_gemm(const I8Args& a, hipStream_t s) {
+    const int64_t tm = (a.M + IG_BM - 1) / IG_BM, tn = (a.N + IG_BN - 1) / IG_BN;
+    hipLaunchKernelGGL((k_i8_gemm<ALIGNED>), dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, (int)tm, (int)tn);
+    return hipGetLastError();
+}
+
+template <bool ALIGNED>
+static hipError_t launch_i8(const I8Args& a, hipStream_t s) {
+    if (a.M == 1) return launch_i8_gemv<ALIGNED>(a, s);
+    if (a.M <= 64) return launch_i8_dec<ALIGNED>(a, s);
+    return launch_i8_gemm<ALIGNED>(a, s);
+}
+
+hipError_t launch_forward_i8(const I8Args& a, hipStream_t s) {
+    const bool aligned = a.K % 16 == 0 && (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.wq % 16 == 0;
+    return aligned ? launch_i8<true>(a, s) : launch_i8<false>(a, s);
 }
 
 }  // namespace bitlinear
