@@ -17,12 +17,12 @@ namespace bitlinear {
 // Scale of a token or a channel: fp32(s / 127), an IEEE division.
 __device__ __forceinline__ float i8_scale(float s) { return s / 127.0f; }
 
-// Output (m, n) from its sum, with the token's and the channel's scale.
-__device__ __forceinline__ void i8_store(const I8Args& a, int64_t m, int64_t n, int acc, float bs, float gs, float bias) {
+// Output `at` (m N + n) from its sum, with the token's and the channel's scale and the bias.
+__device__ __forceinline__ void i8_store(const I8Args& a, int64_t at, int acc, float bs, float gs, float bias) {
     float v = (float)acc * bs * gs;
     if (a.bias) v = v + bias;
-    a.y[m * a.N + n] = v;
-    if (a.acc) a.acc[m * a.N + n] = acc;
+    a.y[at] = v;
+    if (a.acc) a.acc[at] = acc;
 }
 
 // 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void k_i8_gemv(I8Args a) {
         if (lane == r) mine = t;
     }
     const int64_t n = r0 + lane;
-    if (lane < R && n < a.N) i8_store(a, 0, n, mine, i8_scale(a.beta[0]), i8_scale(a.gamma[n]), a.bias ? a.bias[n] : 0.0f);
+    if (lane < R && n < a.N) i8_store(a, n, mine, i8_scale(a.beta[0]), i8_scale(a.gamma[n]), a.bias ? a.bias[n] : 0.0f);
 }
 
 template <bool ALIGNED>
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int m = 16 * t + 4 * (l >> 4) + i;
-                if (m < rows_m) i8_store(a, m0 + m, n0 + n, sum[i], i8_scale(a.beta[m0 + m]), gs, bias);
+                if (m < rows_m) i8_store(a, (m0 + m) * a.N + n0 + n, sum[i], i8_scale(a.beta[m0 + m]), gs, bias);
             }
         }
     }
@@ -258,18 +258,20 @@ static hipError_t launch_i8_dec(const I8Args& a, hipStream_t s) {
 
 // ---- many tokens ----------------------------------------------------------------------------
 // A workgroup of eight waves computes 128 tokens x 256 channels, a wave 64 x 64 of them in 32 x 32
-// blocks, in steps of 64 k; three LDS stages (24 KiB each), filled two steps ahead (aligned rows:
-// by loads that go past the registers; else through registers, one step ahead).
+// blocks, in steps of 128 k (rows of whole cache lines); three LDS stages (48 KiB each), filled two
+// steps ahead by loads that go past the registers (aligned rows), or two filled through registers.
+// Unit u (16 bytes) of row r lies at slot u ^ ((r / 2) % 8) of its eight.
 // 32x32x32 lane layout: A/B lane l holds row/column l % 32, k = 16 (l / 32) + j; accumulator r of
 // lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
-constexpr int IG_BM = 128, IG_BN = 256, IG_BK = 64;
+constexpr int IG_BM = 128, IG_BN = 256, IG_BK = 128;
 
 template <bool ALIGNED>
-__global__ __launch_bounds__(512, 4) void k_i8_gemm(I8Args a, int tiles_m, int tiles_n) {
-    constexpr int OB = IG_BM * 4, UNITS = OB + IG_BN * 4;
+__global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int tiles_n) {
+    constexpr int OB = IG_BM * 8, UNITS = OB + IG_BN * 8;
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
-    __shared__ i32x4 st2[UNITS];
+    __shared__ i32x4 st2[ALIGNED ? UNITS : 1];
+    __shared__ __align__(16) float bscale[IG_BM];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // a contiguous run of tiles for each XCD, four rows of tiles at a time
@@ -282,123 +284,169 @@ __global__ __launch_bounds__(512, 4) void k_i8_gemm(I8Args a, int tiles_m, int t
     const int rows_m = (int)(a.M - m0 < IG_BM ? a.M - m0 : IG_BM), rows_n = (int)(a.N - n0 < IG_BN ? a.N - n0 : IG_BN);
     const int8_t* x0 = a.xq + m0 * K;
     const int8_t* w0 = a.wq + n0 * K;
-    const int steps = (int)((K + IG_BK - 1) / IG_BK);
 
     i32x16 acc[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
-    const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5, sw = unit_swizzle(lr);
-    auto multiply = [&](const i32x4* st, int s) {
-        i32x4 fa[2][2], fb[2][2];
+    const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
+    // scales before the loop: the tokens' in LDS, the channels' in registers
+    if (tid < IG_BM) bscale[tid] = tid < rows_m ? i8_scale(a.beta[m0 + tid]) : 0.0f;
+    float gs[2], bias[2];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const int u = 2 * kk + lg, at = u ^ sw;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) fb[kk][j] = st[OB + (64 * wj + 32 * j + lr) * 4 + at];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) fa[kk][i] = st[(64 * wi + 32 * i + lr) * 4 + at];
-            if (ALIGNED && (int64_t)s * IG_BK + IG_BK > K) {
-                // past the end of its row an aligned load has read what follows it
-                const bool live = (int64_t)s * IG_BK + 16 * u < K;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) fa[kk][i] = live ? fa[kk][i] : i32x4{0, 0, 0, 0};
-            }
-        }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[kk][i], fb[kk][j], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < 2; ++j) {
+        const int64_t n = n0 + min(64 * wj + 32 * j + lr, rows_n - 1);
+        gs[j] = i8_scale(a.gamma[n]);
+        bias[j] = a.bias ? a.bias[n] : 0.0f;
+    }
+    struct Frag {
+        i32x4 a[2], b[2];
     };
-    // load block q (of 24: 8 of x_q, 16 of W_q, 16 rows each): wave w takes 3 w .. 3 w + 2
-    const int row = lane >> 2, unit = (lane & 3) ^ unit_swizzle(row);
+    // operands of k 32 kk .. 32 kk + 31 of the step in stage st
+    auto read = [&](const i32x4* st, int kk) {
+        const int u = 2 * kk + lg, at = u ^ sw;
+        Frag f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f.b[j] = st[OB + (64 * wj + 32 * j + lr) * 8 + at];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) f.a[i] = st[(64 * wi + 32 * i + lr) * 8 + at];
+        return f;
+    };
+    auto multiply = [&](const Frag& f) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // load block q (8 rows): wave w takes 2 w, 2 w + 1 of x_q and 4 w .. 4 w + 3 of W_q
+    auto block_row = [&](int q) { return 8 * q + (lane >> 3); };
+    auto block_unit = [&](int q) { return (lane & 7) ^ ((block_row(q) >> 1) & 7); };
     if constexpr (ALIGNED) {
         const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
         const __amdgpu_buffer_rsrc_t rw = raw_buffer(w0, (uint32_t)rows_n * (uint32_t)K);
-        uint32_t xo, wo[2];
-        xo = (uint32_t)min(16 * wave + row, rows_m - 1) * (uint32_t)K + 16u * unit;
+        uint32_t xo[2], wo[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) wo[q] = (uint32_t)min(16 * (2 * wave + q) + row, rows_n - 1) * (uint32_t)K + 16u * unit;
-        auto fetch = [&](i32x4* st, int s) {
+        for (int q = 0; q < 2; ++q)
+            xo[q] = (uint32_t)min(block_row(2 * wave + q), rows_m - 1) * (uint32_t)K + 16u * block_unit(2 * wave + q);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            wo[q] = (uint32_t)min(block_row(4 * wave + q), rows_n - 1) * (uint32_t)K + 16u * block_unit(4 * wave + q);
+        // a third of a step's loads
+        auto fetch = [&](i32x4* st, int s, int third) {
             const uint32_t so = (uint32_t)s * IG_BK;
-            load_lds16(rx, xo, so, st + 64 * wave);
+            if (third == 0) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (2 * wave + q));
-            __builtin_amdgcn_sched_barrier(0);
+                for (int q = 0; q < 2; ++q) load_lds16(rx, xo[q], so, st + 64 * (2 * wave + q));
+            } else {
+#pragma unroll
+                for (int q = 2 * third - 2; q < 2 * third; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (4 * wave + q));
+            }
         };
-        // step s has landed for every wave, and every read of the stage to be filled is over
-        auto turn = [&](bool next) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (next) __builtin_amdgcn_s_waitcnt(0x0070 | 3);      // vmcnt(3) lgkmcnt(0)
-            else __builtin_amdgcn_s_waitcnt(0x0070);
+        // Step s in stage `cur`, its first operands in f0.  Operands are read one part ahead of their
+        // MFMAs, across the turn too; the stage that a turn frees is loaded with the step after next
+        // but one, a third at a time, so that the matrix cores have work while loads are issued.  Loads
+        // past the last whole step repeat it and are not read.
+        const int steps = (int)(K / IG_BK), last = steps - 1;
+        auto step = [&](i32x4* cur, i32x4* nxt, i32x4* prv, int s, Frag& f0) {
+            Frag f1 = read(cur, 1);
+            fetch(prv, min(s + 2, last), 1);
+            multiply(f0);
+            f0 = read(cur, 2);
+            fetch(prv, min(s + 2, last), 2);
+            multiply(f1);
+            f1 = read(cur, 3);
+            multiply(f0);
+            // step s + 1 has landed for every wave, and every wave holds the rest of step s in registers
+            __builtin_amdgcn_s_waitcnt(0x0070 | 6);        // vmcnt(6: the loads of step s + 2) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
+            f0 = read(nxt, 0);
+            fetch(cur, min(s + 3, last), 0);
+            multiply(f1);
         };
-        int s = 0;
-        fetch(st0, 0);
-        if (1 < steps) fetch(st1, 1);
-        for (; s + 3 <= steps; s += 3) {
-            turn(true);
-            fetch(st2, s + 2);
-            multiply(st0, s);
-            turn(true);
-            if (s + 3 < steps) fetch(st0, s + 3);
-            multiply(st1, s + 1);
-            turn(s + 3 < steps);
-            if (s + 4 < steps) fetch(st1, s + 4);
-            multiply(st2, s + 2);
+        if (steps > 0) {
+#pragma unroll
+            for (int q = 0; q < 3; ++q) fetch(st0, 0, q);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) fetch(st1, min(1, last), q);
+            fetch(st2, min(2, last), 0);
+            __builtin_amdgcn_s_waitcnt(0x0070 | 8);        // vmcnt(8: the loads after step 0's) lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            Frag f = read(st0, 0);
+            int s = 0;
+            for (; s + 3 <= steps; s += 3) {
+                step(st0, st1, st2, s, f);
+                step(st1, st2, st0, s + 1, f);
+                step(st2, st0, st1, s + 2, f);
+            }
+            if (s < steps) step(st0, st1, st2, s, f);
+            if (s + 1 < steps) step(st1, st2, st0, s + 1, f);
+            __builtin_amdgcn_s_waitcnt(0x0070);            // nothing is in flight into the stages any more
+        } else {
+            __syncthreads();                               // the tokens' scales
         }
-        if (s < steps) {
-            turn(s + 1 < steps);
-            multiply(st0, s);
-        }
-        if (s + 1 < steps) {
-            turn(false);
-            multiply(st1, s + 1);
+        // what is left of K, fewer than 128, straight into the operands
+        for (int64_t k = (int64_t)steps * IG_BK; k < K; k += 32) {
+            Frag f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) f.a[i] = row_16(x0 + (int64_t)min(64 * wi + 32 * i + lr, rows_m - 1) * K, k + 16 * lg, K);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) f.b[j] = row_16(w0 + (int64_t)min(64 * wj + 32 * j + lr, rows_n - 1) * K, k + 16 * lg, K);
+            multiply(f);
         }
     } else {
-        const int8_t* xp = x0 + (int64_t)min(16 * wave + row, rows_m - 1) * K;
-        const int8_t* wp[2];
+        const int8_t *xp[2], *wp[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) wp[q] = w0 + (int64_t)min(16 * (2 * wave + q) + row, rows_n - 1) * K;
-        i32x4 v[3];
+        for (int q = 0; q < 2; ++q) xp[q] = x0 + (int64_t)min(block_row(2 * wave + q), rows_m - 1) * K;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) wp[q] = w0 + (int64_t)min(block_row(4 * wave + q), rows_n - 1) * K;
+        i32x4 v[6];
         auto load = [&](int s) {
-            const int64_t k = (int64_t)s * IG_BK + 16 * unit;
-            v[0] = row_16(xp, k, K);
-            v[1] = row_16(wp[0], k, K);
-            v[2] = row_16(wp[1], k, K);
+            const int64_t k = (int64_t)s * IG_BK;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) v[q] = row_16(xp[q], k + 16 * block_unit(2 * wave + q), K);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[2 + q] = row_16(wp[q], k + 16 * block_unit(4 * wave + q), K);
         };
         auto put = [&](i32x4* st) {
-            st[64 * wave + lane] = v[0];
-            st[OB + 64 * (2 * wave) + lane] = v[1];
-            st[OB + 64 * (2 * wave + 1) + lane] = v[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) st[64 * (2 * wave + q) + lane] = v[q];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) st[OB + 64 * (4 * wave + q) + lane] = v[2 + q];
         };
+        const int steps = (int)((K + IG_BK - 1) / IG_BK);
         load(0);
         put(st0);
         for (int s = 0; s < steps; ++s) {
             __syncthreads();                       // step s is in its stage, and the other stage is free
             if (s + 1 < steps) load(s + 1);
-            multiply(s & 1 ? st1 : st0, s);
+            const i32x4* cur = s & 1 ? st1 : st0;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) multiply(read(cur, kk));
             if (s + 1 < steps) put(s & 1 ? st0 : st1);
         }
     }
+    // tokens 4 q .. 4 q + 3 of a block are four registers of a lane: their scales are one LDS read
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int n = 64 * wj + 32 * j + lr;
-        if (n >= rows_n) continue;
-        const float gs = i8_scale(a.gamma[n0 + n]), bias = a.bias ? a.bias[n0 + n] : 0.0f;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int q = 0; q < 4; ++q) {
+            const int m = 64 * wi + 32 * i + 8 * q + 4 * lg;
+            const float4 bs4 = *reinterpret_cast<const float4*>(&bscale[m]);
+            const float bs[4] = {bs4.x, bs4.y, bs4.z, bs4.w};
+            const int64_t at = (m0 + m) * a.N + n0 + 64 * wj + lr;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int m = 64 * wi + 32 * i + 8 * (r / 4) + 4 * lg + r % 4;
-                if (m < rows_m) i8_store(a, m0 + m, n0 + n, acc[i][j][r], i8_scale(a.beta[m0 + m]), gs, bias);
+            for (int e = 0; e < 4; ++e) {
+                if (m + e >= rows_m) break;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (64 * wj + 32 * j + lr < rows_n)
+                        i8_store(a, at + e * a.N + 32 * j, acc[i][j][4 * q + e], bs[e], gs[j], bias[j]);
             }
-    }
+        }
 }
 
 template <bool ALIGNED>
