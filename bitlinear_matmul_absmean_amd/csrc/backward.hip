@@ -14,11 +14,18 @@
 // f16 MFMA products into one fp32 accumulator then give the product to fp32 accuracy at half the
 // f16 matrix rate, several times the rate of fp32 products.
 //
+// Operands lie in panels, the blocks that a step of the product reads, each contiguous and in the
+// order of its LDS image, so that every load is 1 KiB of whole cache lines:
+//   split gradients  [rows / 128][L / 32][hi, lo][128 rows][32 l] fp16, the 16-byte unit u of row r at
+//                    position u ^ split_swizzle(r);
+//   integer operand  [columns / 256][L / 32][256 columns][32 l] as bytes v + 128, the 16-byte unit u
+//                    of column c at position u ^ (c / 8) % 2.
+//
 // Steps, each one launch over the whole problem:
 //   1. k_grad_prep: the largest |d alpha| of every token and |d beta / 127| of every channel, and the
-//      bias sums, tile by tile; the integer operands in fp16 with the sum's index contiguous;
+//      bias sums, tile by tile; the panels of the integer operands;
 //   2. k_grad_reduce: the tiles' maxima and sums put together;
-//   3. k_grad_split: d once more, scaled and split, written token-major (dx) and channel-major (dW);
+//   3. k_grad_split: d once more, scaled and split, rows being tokens (dx) and channels (dW);
 //   4. k_split_gemm: both products;
 //   5. k_split_sum, where a sum was cut into parts.
 #include <limits.h>
@@ -28,6 +35,7 @@
 namespace bitlinear {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Exponent s of the power of two that scales a row whose largest element is mx to [2^14, 2^15);
@@ -36,6 +44,19 @@ __device__ __forceinline__ int scale_exponent(float mx) {
     if (mx == 0.0f) return 0;
     const int s = 15 - __builtin_amdgcn_frexp_expf(mx);
     return s > 126 ? 126 : s < -126 ? -126 : s;
+}
+// Eight bytes v + 128 as the fp16 numbers v.
+__device__ __forceinline__ f16x8 bytes_f16(uint32_t lo, uint32_t hi) {
+    const f16x2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+    f16x2 r[4];
+    r[0] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u)) - bias;
+    r[1] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u)) - bias;
+    r[2] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u)) - bias;
+    r[3] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u)) - bias;
+    f16x8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = r[i / 2][i % 2];
+    return o;
 }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -54,7 +75,20 @@ __device__ __forceinline__ void grad_at(const BackwardArgs& a, int64_t i, float 
     }
 }
 
-constexpr int SG_WI = 2, SG_BM = 64 * SG_WI, SG_BN = 256, SG_BK = 32, SG_SLOTS = 512;
+constexpr int SG_BM = 128, SG_BN = 256, SG_BK = 32, SG_SLOTS = 512;
+
+// Where row r keeps its four 16-byte units: 16 consecutive rows then spread one unit over all 64 banks.
+__device__ __forceinline__ int split_swizzle(int r) { return ((r >> 2) & 3) ^ (((r >> 1) & 1) << 1); }
+// Index of element (row, l) of the hi plane of split panels with sums of length L; lo lies 4096 on.
+__device__ __forceinline__ int64_t split_at(int64_t row, int64_t l, int64_t L) {
+    const int r = (int)(row & 127), c = (int)(l & 31);
+    return ((row >> 7) * (L >> 5) + (l >> 5)) * 8192 + r * 32 + (((c >> 3) ^ split_swizzle(r)) << 3) + (c & 7);
+}
+// Index of the 16-byte unit that holds element (column, l) of integer panels.
+__device__ __forceinline__ int64_t code_unit(int64_t col, int64_t l, int64_t L) {
+    const int c = (int)(col & 255);
+    return ((col >> 8) * (L >> 5) + (l >> 5)) * 512 + c * 2 + (((l >> 4) & 1) ^ ((c >> 3) & 1));
+}
 
 struct GradPlan {
     int64_t Np, Mp, Lx;            // N and M rounded up to 64, P Np
@@ -63,9 +97,8 @@ struct GradPlan {
     float *rpart, *cpart;          // largest |d alpha| [M, ct], |d beta / 127| [mt, P N] of a tile
     double* bpart;                 // sums of d [mt, P N] of a tile
     float *rmax, *cmax;            // [M], [P N]
-    _Float16 *xh, *xl;             // dx: split gradients [M, Lx]
-    _Float16 *wh, *wl;             // dW: split gradients [P N, Mp]
-    _Float16 *wt, *cd;             // W_hat^T [K, Lx], x_q^T [K, Mp]
+    uint16_t *xs, *wsp;            // panels of the split gradients: M rows of Lx (dx), P N rows of Mp (dW)
+    uint8_t *wt, *cd;              // panels of W_hat^T, K columns of Lx, and of x_q^T, K columns of Mp
     float *part_x, *part_w;        // sums cut into parts
     int parts_x, parts_w;
     size_t bytes;
@@ -114,12 +147,11 @@ static GradPlan grad_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws)
     p.bpart = reinterpret_cast<double*>(take(p.mt * P * N, 8));
     p.rmax = reinterpret_cast<float*>(take(M, 4));
     p.cmax = reinterpret_cast<float*>(take(P * N, 4));
-    p.xh = reinterpret_cast<_Float16*>(take(M * p.Lx, 2));
-    p.xl = reinterpret_cast<_Float16*>(take(M * p.Lx, 2));
-    p.wh = reinterpret_cast<_Float16*>(take(P * N * p.Mp, 2));
-    p.wl = reinterpret_cast<_Float16*>(take(P * N * p.Mp, 2));
-    p.wt = reinterpret_cast<_Float16*>(take(K * p.Lx, 2));
-    p.cd = reinterpret_cast<_Float16*>(take(K * p.Mp, 2));
+    const int64_t K256 = (K + 255) / 256 * 256;
+    p.xs = reinterpret_cast<uint16_t*>(take((M + 127) / 128 * 128 * p.Lx, 4));
+    p.wsp = reinterpret_cast<uint16_t*>(take((P * N + 127) / 128 * 128 * p.Mp, 4));
+    p.wt = take(K256 * p.Lx, 1);
+    p.cd = take(K256 * p.Mp, 1);
     p.part_x = reinterpret_cast<float*>(take(p.parts_x > 1 ? p.parts_x * M * K : 0, 4));
     p.part_w = reinterpret_cast<float*>(take(p.parts_w > 1 ? p.parts_w * P * N * K : 0, 4));
     p.bytes = off;
@@ -208,15 +240,15 @@ __device__ __forceinline__ uint32_t row_dword(const uint8_t* __restrict__ p, int
     return v;
 }
 
-// Bytes of a 64-row tile, transposed: column c of row r at lds[c * 72 + r] (72: rows of eight-byte
-// units spread over the banks).  A thread writes the four columns of a dword it has read.
+// Bytes of a 64-row tile, transposed: column c of row r at lds[c * 80 + r] (80: the 16-byte reads of
+// neighbouring columns spread over the banks).  A thread writes the four columns of a dword.
 __device__ __forceinline__ void put_column_bytes(uint8_t* lds, int r, int c, uint32_t v) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) lds[(c + j) * 72 + r] = (uint8_t)(v >> (8 * j));
+    for (int j = 0; j < 4; ++j) lds[(c + j) * 80 + r] = (uint8_t)(v >> (8 * j));
 }
 
-// W_hat^T in fp16 [K, Lx], 64 weight rows x 256 columns k per workgroup: every lane writes eight
-// rows' weights at four columns.  Codes 0, 1, 2 are -1, 0, 1: fp16 high bytes 0xBC, 0x00, 0x3C.
+// Panels of W_hat^T, 64 weight rows x 256 columns k per workgroup: a lane expands the codes 0, 1, 2 of
+// sixteen rows at four columns to the bytes 127, 128, 129.
 __device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint8_t* lds) {
     const int64_t k0 = b % kt * 256, l0 = b / kt * 64;
     const int q = l0 >= p.Np;
@@ -228,23 +260,16 @@ __device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPl
         put_column_bytes(lds, r, c, n < a.N ? row_dword(w + n * rowb, (k0 >> 2) + c, rowb) : 0x55555555u);
     }
     __syncthreads();
-    const int u = threadIdx.x & 7;
-    for (int c = threadIdx.x >> 3; c < 64; c += 32) {
-        const uint2 v = *reinterpret_cast<const uint2*>(lds + c * 72 + 8 * u);
+    const int u = threadIdx.x & 3, c = threadIdx.x >> 2;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + c * 80 + 16 * u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t k = k0 + 4 * c + i;
-            if (k >= a.K) break;
-            const uint32_t h0 = __builtin_amdgcn_perm(0u, 0x003C00BCu, (v.x >> (2 * i)) & 0x03030303u);
-            const uint32_t h1 = __builtin_amdgcn_perm(0u, 0x003C00BCu, (v.y >> (2 * i)) & 0x03030303u);
-            const u32x4 o = {__builtin_amdgcn_perm(0u, h0, 0x010C000Cu), __builtin_amdgcn_perm(0u, h0, 0x030C020Cu),
-                             __builtin_amdgcn_perm(0u, h1, 0x010C000Cu), __builtin_amdgcn_perm(0u, h1, 0x030C020Cu)};
-            *reinterpret_cast<u32x4*>(p.wt + k * p.Lx + l0 + 8 * u) = o;
-        }
+    for (int i = 0; i < 4; ++i) {
+        const u32x4 o = ((v >> (uint32_t)(2 * i)) & 0x03030303u) + 0x7F7F7F7Fu;
+        reinterpret_cast<u32x4*>(p.wt)[code_unit(k0 + 4 * c + i, l0 + 16 * u, p.Lx)] = o;
     }
 }
 
-// x_q^T in fp16 [K, Mp], 64 tokens x 64 columns per workgroup.
+// Panels of x_q^T, 64 tokens x 64 columns per workgroup.
 __device__ __forceinline__ void codes_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint8_t* lds) {
     const int64_t k0 = b % kt * 64, m0 = b / kt * 64;
     for (int i = threadIdx.x; i < 64 * 16; i += 256) {
@@ -253,15 +278,9 @@ __device__ __forceinline__ void codes_tile(const BackwardArgs& a, const GradPlan
         put_column_bytes(lds, r, c, m < a.M ? row_dword(reinterpret_cast<const uint8_t*>(a.xq) + m * a.K, k0 + c, a.K) : 0u);
     }
     __syncthreads();
-    const int u = threadIdx.x & 7;
-    for (int c = threadIdx.x >> 3; c < 64; c += 32) {
-        if (k0 + c >= a.K) break;
-        const int8_t* v = reinterpret_cast<const int8_t*>(lds + c * 72 + 8 * u);
-        f16x8 o;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = (_Float16)(float)v[j];
-        *reinterpret_cast<f16x8*>(p.cd + (k0 + c) * p.Mp + m0 + 8 * u) = o;
-    }
+    const int u = threadIdx.x & 3, c = threadIdx.x >> 2;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + c * 80 + 16 * u);
+    reinterpret_cast<u32x4*>(p.cd)[code_unit(k0 + c, m0 + 16 * u, p.Mp)] = v ^ 0x80808080u;
 }
 
 template <int ACT>
@@ -308,8 +327,8 @@ __device__ __forceinline__ uint32_t split_f16(float v) {
 }
 
 // Scaled and split gradients, 64 tokens x 128 columns per workgroup of eight waves; a wave takes
-// eight tokens, a lane two neighbouring columns.  Token-major planes are written as they come (256
-// bytes a wave), channel-major ones through LDS (64 tokens, 128 bytes, a channel).  Padded columns
+// eight tokens, a lane two neighbouring columns.  Rows of tokens are written as they come, rows of
+// channels through LDS.  Padded columns
 // and tokens are written as zeros.
 template <int ACT>
 __global__ __launch_bounds__(512) void k_grad_split(BackwardArgs a, GradPlan p, int ctiles) {
@@ -339,9 +358,9 @@ __global__ __launch_bounds__(512) void k_grad_split(BackwardArgs a, GradPlan p, 
         for (int q = 0; q < P; ++q) {
             if (a.dx && m < a.M && n < p.Np) {
                 const uint32_t v0 = split_f16(d[0][q] * al[q] * rscale), v1 = split_f16(d[1][q] * al[q] * rscale);
-                const int64_t o = (m * p.Lx + q * p.Np + n) / 2;
-                reinterpret_cast<uint32_t*>(p.xh)[o] = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
-                reinterpret_cast<uint32_t*>(p.xl)[o] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
+                uint32_t* o = reinterpret_cast<uint32_t*>(p.xs + split_at(m, q * p.Np + n, p.Lx));
+                o[0] = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
+                o[2048] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) tile[q][2 * lane + c][8 * wave + t] = split_f16(d[c][q] * bs * cscale[q][c]);
@@ -363,16 +382,16 @@ __global__ __launch_bounds__(512) void k_grad_split(BackwardArgs a, GradPlan p, 
                 h[j] = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], 0x05040100u);
                 l[j] = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], 0x07060302u);
             }
-            const int64_t o = (q * a.N + n0 + r) * p.Mp + m0 + 8 * u;
-            *reinterpret_cast<u32x4*>(p.wh + o) = h;
-            *reinterpret_cast<u32x4*>(p.wl + o) = l;
+            u32x4* o = reinterpret_cast<u32x4*>(p.wsp + split_at(q * a.N + n0 + r, m0 + 8 * u, p.Mp));
+            o[0] = h;
+            o[512] = l;
         }
 }
 
 // ---- step 4 -------------------------------------------------------------------------------
 struct SplitArgs {
-    const _Float16 *ah, *al;       // [I, L] hi and lo planes
-    const _Float16* b;             // [J, L]
+    const uint16_t* a;             // panels of I rows of split gradients
+    const uint8_t* b;              // panels of J columns of the integer operand
     const float* amax;             // [I] the rows' largest elements
     int64_t I, J, L;               // L a multiple of 64
     float *c0, *c1;                // rows below I0 go to c0 [I0, J], the others to c1
@@ -383,23 +402,21 @@ struct SplitArgs {
 
 // C[i, j] = 2^-s_i sum_l (hi[i, l] + lo[i, l]) b[j, l].  A workgroup of four waves computes 128 x 256
 // outputs, a wave 64 x 128 of them in 32 x 32 blocks (128 accumulator registers), in steps of 32 l.
-// Both LDS stages (32 KiB each: 128 rows of hi, of lo, 256 rows of b, 64 bytes a row) are filled by
-// loads that go past the registers; a stage is loaded while the other is multiplied.  Unit u (16
-// bytes) of row r lies at slot u ^ ((r / 2) % 4) of its row, so that eight consecutive lanes of an
-// operand read (eight rows, one unit) meet eight different bank groups.
-template <int WI, int STAGES>
-__global__ __launch_bounds__(128 * WI, 2) void k_split_gemm(SplitArgs x, SplitArgs w) {
+// Three LDS stages (24 KiB each: a panel block of each operand) are filled two steps ahead by loads
+// that go past the registers; two workgroups share a compute unit.  Bytes v + 128 become fp16 as
+// 1024 + (v + 128), the byte under the exponent 0x64, minus 1152: two instructions for two values.
+// In the first MFMA of a step lane group g (lanes 32 g ..) holds l 16 g .. 16 g + 7, in the second
+// 16 g + 8 .. 16 g + 15, so that one read of 16 bytes brings both of the lane's integer operands.
+__global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w) {
     // the workgroups of the first product, then those of the second
     const int TX = x.parts * x.tiles_i * x.tiles_j;
     const bool first = blockIdx.x < TX;
     const SplitArgs& a = first ? x : w;
     const int blk = first ? blockIdx.x : blockIdx.x - TX;
-    constexpr int BM = 64 * WI, BN = SG_BN, WAVES = 2 * WI;
-    constexpr int AB = BM / 16 / WAVES, BB = BN / 16 / WAVES;        // load instructions of a wave: hi (or lo) rows, b rows
-    constexpr int OL = BM * 4, OB = BM * 8, UNITS = OB + BN * 4;     // units: lo, b, a stage
+    constexpr int OL = 512, OB = 1024, UNITS = 1536;           // units: lo, b, a stage
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
-    __shared__ i32x4 st2[STAGES == 3 ? UNITS : 1];
+    __shared__ i32x4 st2[UNITS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // consecutive workgroups go to the eight XCDs in turn: give each XCD a contiguous run of tiles,
@@ -411,36 +428,21 @@ __global__ __launch_bounds__(128 * WI, 2) void k_split_gemm(SplitArgs x, SplitAr
     t -= part * a.tiles_i * a.tiles_j;
     const int grp = t / (4 * a.tiles_j), gi = a.tiles_i - 4 * grp < 4 ? a.tiles_i - 4 * grp : 4;
     t -= grp * 4 * a.tiles_j;
-    const int64_t i0 = (int64_t)(4 * grp + t % gi) * BM, j0 = (int64_t)(t / gi) * BN;
+    const int ti = 4 * grp + t % gi, tj = t / gi;
+    const int64_t i0 = (int64_t)ti * SG_BM, j0 = (int64_t)tj * SG_BN;
     const int KS = (int)(a.L / SG_BK);
     const int ks0 = (int)((int64_t)KS * part / a.parts), ks1 = (int)((int64_t)KS * (part + 1) / a.parts);
 
-    // loads: instruction q of a wave fills 64 slots (16 rows); rows past the end repeat the last one
-    const int lrow = lane >> 2, unit = (lane & 3) ^ ((lane >> 4) & 3) ^ (((lane >> 3) & 1) << 1);
-    const uint32_t ldb = (uint32_t)(a.L * 2);
-    const int64_t rows_i = a.I - i0 < BM ? a.I - i0 : BM, rows_j = a.J - j0 < BN ? a.J - j0 : BN;
-    const __amdgpu_buffer_rsrc_t rh = raw_buffer(a.ah + i0 * a.L, (uint32_t)rows_i * ldb);
-    const __amdgpu_buffer_rsrc_t rl = raw_buffer(a.al + i0 * a.L, (uint32_t)rows_i * ldb);
-    const __amdgpu_buffer_rsrc_t rb = raw_buffer(a.b + j0 * a.L, (uint32_t)rows_j * ldb);
-    uint32_t ao[AB], bo[BB];
-#pragma unroll
-    for (int q = 0; q < AB; ++q) {
-        const int r = 16 * (AB * wave + q) + lrow;
-        ao[q] = (uint32_t)(r < rows_i ? r : (int)rows_i - 1) * ldb + 16u * unit;
-    }
-#pragma unroll
-    for (int q = 0; q < BB; ++q) {
-        const int r = 16 * (BB * wave + q) + lrow;
-        bo[q] = (uint32_t)(r < rows_j ? r : (int)rows_j - 1) * ldb + 16u * unit;
-    }
+    const __amdgpu_buffer_rsrc_t ra = raw_buffer(a.a + (int64_t)ti * KS * 8192, (uint32_t)KS * 16384u);
+    const __amdgpu_buffer_rsrc_t rb = raw_buffer(a.b + (int64_t)tj * KS * 8192, (uint32_t)KS * 8192u);
+    const uint32_t voff = 16u * lane;
+    const int last = ks1 - 1;
     auto fetch = [&](i32x4* st, int ks) {
-        const uint32_t so = (uint32_t)ks * (SG_BK * 2);
+        const uint32_t s = (uint32_t)(ks < last ? ks : last);
 #pragma unroll
-        for (int q = 0; q < AB; ++q) load_lds16(rh, ao[q], so, st + 64 * (AB * wave + q));
+        for (int q = 0; q < 4; ++q) load_lds16(ra, voff, s * 16384u + 1024u * (4 * wave + q), st + 64 * (4 * wave + q));
 #pragma unroll
-        for (int q = 0; q < AB; ++q) load_lds16(rl, ao[q], so, st + OL + 64 * (AB * wave + q));
-#pragma unroll
-        for (int q = 0; q < BB; ++q) load_lds16(rb, bo[q], so, st + OB + 64 * (BB * wave + q));
+        for (int q = 0; q < 2; ++q) load_lds16(rb, voff, s * 8192u + 1024u * (2 * wave + q), st + OB + 64 * (2 * wave + q));
         __builtin_amdgcn_sched_barrier(0);         // issued here, not where their data is needed
     };
 
@@ -449,94 +451,65 @@ __global__ __launch_bounds__(128 * WI, 2) void k_split_gemm(SplitArgs x, SplitAr
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-    const int wi = wave % WI, wj = wave / WI, lr = lane & 31, lg = lane >> 5;
-    const int sw = ((lr >> 2) & 3) ^ (((lr >> 1) & 1) << 1);
+    const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5;
+    const int sw = split_swizzle(lr), sb = lg ^ ((lr >> 3) & 1);
     auto multiply = [&](const i32x4* st) {
-        f16x8 fh[2][2], fl[2][2], fb[2][4];
+        i32x4 cb[4];
+        f16x8 fh[2][2], fl[2][2];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const int s = (2 * kk + lg) ^ sw;
+        for (int j = 0; j < 4; ++j) cb[j] = st[OB + (128 * wj + 32 * j + lr) * 2 + sb];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fb[kk][j] = __builtin_bit_cast(f16x8, st[OB + (128 * wj + 32 * j + lr) * 4 + s]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fh[kk][i] = __builtin_bit_cast(f16x8, st[(64 * wi + 32 * i + lr) * 4 + s]);
-                fl[kk][i] = __builtin_bit_cast(f16x8, st[OL + (64 * wi + 32 * i + lr) * 4 + s]);
-            }
-        }
-#ifndef VORD
-#define VORD 0
-#endif
-#define MFH(i,j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fh[kk][i], fb[kk][j], acc[i][j], 0, 0, 0)
-#define MFL(i,j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[kk][i], fb[kk][j], acc[i][j], 0, 0, 0)
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            if (VORD == 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) { MFH(i,j); MFL(i,j); }
-            } else if (VORD == 1) {
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) { MFH(i,j); __builtin_amdgcn_sched_barrier(0); }
-#pragma unroll
-                for (int j = 3; j >= 0; --j) { MFL(i,j); __builtin_amdgcn_sched_barrier(0); }
+                const int at = (64 * wi + 32 * i + lr) * 4 + ((2 * lg + kk) ^ sw);
+                fh[kk][i] = __builtin_bit_cast(f16x8, st[at]);
+                fl[kk][i] = __builtin_bit_cast(f16x8, st[OL + at]);
             }
-            } else if (VORD == 2) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {  MFH(0,j); __builtin_amdgcn_sched_barrier(0); MFH(1,j);__builtin_amdgcn_sched_barrier(0); MFL(0,j);__builtin_amdgcn_sched_barrier(0); MFL(1,j); __builtin_amdgcn_sched_barrier(0);}
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f16x8 fb = bytes_f16((uint32_t)cb[j][2 * kk], (uint32_t)cb[j][2 * kk + 1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fh[kk][i], fb, acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[kk][i], fb, acc[i][j], 0, 0, 0);
+                }
             }
-        }
     };
-    // the loads of the stage to be read have landed, for every wave, and every read of the stage
-    // to be filled is over
-    auto turn = [&](bool next_in_flight) {
+    // the loads of the stage to be read have landed, for every wave, and every read of the stage to
+    // be filled is over; loads past the last step repeat it and are not read
+    auto turn = [&]() {
         __builtin_amdgcn_sched_barrier(0);
-        if (STAGES == 3 && next_in_flight) __builtin_amdgcn_s_waitcnt(0x0070 | (2 * AB + BB));   // vmcnt(a stage's loads) lgkmcnt(0)
-        else __builtin_amdgcn_s_waitcnt(0x0070);                                                // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt(0x0070 | 6);    // vmcnt(6: the next stage's loads) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
     int ks = ks0;
-    if constexpr (STAGES == 2) {
-        if (ks < ks1) fetch(st0, ks);
-        for (; ks + 2 <= ks1; ks += 2) {
-            turn(false);
-            fetch(st1, ks + 1);
-            multiply(st0);
-            turn(false);
-            if (ks + 2 < ks1) fetch(st0, ks + 2);
-            multiply(st1);
-        }
-        if (ks < ks1) {
-            turn(false);
-            multiply(st0);
-        }
-    } else {
-        if (ks < ks1) fetch(st0, ks);
-        if (ks + 1 < ks1) fetch(st1, ks + 1);
-        for (; ks + 3 <= ks1; ks += 3) {
-            turn(true);
-            fetch(st2, ks + 2);
-            multiply(st0);
-            turn(true);
-            if (ks + 3 < ks1) fetch(st0, ks + 3);
-            multiply(st1);
-            turn(ks + 3 < ks1);
-            if (ks + 4 < ks1) fetch(st1, ks + 4);
-            multiply(st2);
-        }
-        if (ks < ks1) {
-            turn(ks + 1 < ks1);
-            multiply(st0);
-        }
-        if (ks + 1 < ks1) {
-            turn(false);
-            multiply(st1);
-        }
+    fetch(st0, ks);
+    fetch(st1, ks + 1);
+    for (; ks + 3 <= ks1; ks += 3) {
+        turn();
+        fetch(st2, ks + 2);
+        multiply(st0);
+        turn();
+        fetch(st0, ks + 3);
+        multiply(st1);
+        turn();
+        fetch(st1, ks + 4);
+        multiply(st2);
     }
+    if (ks < ks1) {
+        turn();
+        multiply(st0);
+    }
+    if (ks + 1 < ks1) {
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __builtin_amdgcn_s_barrier();
+        multiply(st1);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);            // nothing is in flight into the stages any more
 
     // accumulator r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4 of the block, column l % 32
 #pragma unroll
@@ -594,10 +567,10 @@ static hipError_t launch_grads(const BackwardArgs& a, hipStream_t s) {
         return q;
     };
     SplitArgs x{}, w{};
-    if (a.dx) x = tiles(SplitArgs{p.xh, p.xl, p.wt, p.rmax, a.M, a.K, p.Lx, a.dx, nullptr, a.M, p.part_x, p.parts_x, 0, 0});
-    if (a.dw0) w = tiles(SplitArgs{p.wh, p.wl, p.cd, p.cmax, P * a.N, a.K, p.Mp, a.dw0, a.dw1, a.N, p.part_w, p.parts_w, 0, 0});
+    if (a.dx) x = tiles(SplitArgs{p.xs, p.wt, p.rmax, a.M, a.K, p.Lx, a.dx, nullptr, a.M, p.part_x, p.parts_x, 0, 0});
+    if (a.dw0) w = tiles(SplitArgs{p.wsp, p.cd, p.cmax, P * a.N, a.K, p.Mp, a.dw0, a.dw1, a.N, p.part_w, p.parts_w, 0, 0});
     const int64_t grid = (int64_t)x.parts * x.tiles_i * x.tiles_j + (int64_t)w.parts * w.tiles_i * w.tiles_j;
-    hipLaunchKernelGGL((k_split_gemm<SG_WI, 2>), blocks(grid), dim3(128 * SG_WI), 0, s, x, w);
+    hipLaunchKernelGGL(k_split_gemm, blocks(grid), dim3(256), 0, s, x, w);
     const int64_t xb = x.parts > 1 ? (x.I * x.J + 255) / 256 : 0, wb = w.parts > 1 ? (w.I * w.J + 255) / 256 : 0;
     if (xb + wb) hipLaunchKernelGGL(k_split_sum, blocks(xb + wb), dim3(256), 0, s, x, w, xb);
     return hipGetLastError();
