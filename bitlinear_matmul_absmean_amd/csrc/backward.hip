@@ -417,6 +417,7 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w)
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
     __shared__ i32x4 st2[UNITS];
+    __shared__ __align__(16) float scale[SG_BM];               // 2^-s of the rows (1 for parts of a sum)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // consecutive workgroups go to the eight XCDs in turn: give each XCD a contiguous run of tiles,
@@ -489,6 +490,7 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w)
     int ks = ks0;
     fetch(st0, ks);
     fetch(st1, ks + 1);
+    if (tid < SG_BM) scale[tid] = a.parts > 1 ? 1.0f : pow2f(-scale_exponent(a.amax[i0 + tid < a.I ? i0 + tid : a.I - 1]));
     for (; ks + 3 <= ks1; ks += 3) {
         turn();
         fetch(st2, ks + 2);
@@ -512,24 +514,25 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w)
     __builtin_amdgcn_s_waitcnt(0x0070);            // nothing is in flight into the stages any more
 
     // accumulator r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4 of the block, column l % 32
+    const int64_t left = a.J - (j0 + 128 * wj + lr);           // columns from this lane's first to the end
+    const int rows = (int)(a.I - i0 < SG_BM ? a.I - i0 : SG_BM);
+    const int split = (int)(a.I0 - i0 < 0 ? 0 : a.I0 - i0 < SG_BM ? a.I0 - i0 : SG_BM);   // rows of c0 in the tile
+    float* top = (a.parts > 1 ? a.part + (int64_t)part * a.I * a.J : a.c0) + i0 * a.J + j0 + 128 * wj + lr;
+    float* bottom = a.parts > 1 || !a.c1 ? top : a.c1 + (i0 - a.I0) * a.J + j0 + 128 * wj + lr;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int64_t row = i0 + 64 * wi + 32 * i + 8 * (r / 4) + 4 * lg + r % 4;
-            if (row >= a.I) continue;
-            float* out;
-            float inv = 1.0f;
-            if (a.parts > 1) {
-                out = a.part + ((int64_t)part * a.I + row) * a.J;
-            } else {
-                inv = pow2f(-scale_exponent(a.amax[row]));
-                out = row < a.I0 ? a.c0 + row * a.J : a.c1 + (row - a.I0) * a.J;
-            }
+        for (int q = 0; q < 4; ++q) {
+            const int r = 64 * wi + 32 * i + 8 * q + 4 * lg;
+            const float4 inv4 = *reinterpret_cast<const float4*>(&scale[r]);
+            const float inv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t col = j0 + 128 * wj + 32 * j + lr;
-                if (col < a.J) out[col] = acc[i][j][r] * inv;
+            for (int e = 0; e < 4; ++e) {
+                if (r + e >= rows) break;
+                float* out = (r + e < split ? top : bottom) + (int64_t)(r + e) * a.J;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (32 * j < left) out[32 * j] = acc[i][j][4 * q + e] * inv[e];
             }
         }
 }
