@@ -363,9 +363,10 @@ int bitlinear_gated_forward(const float* x, int64_t M, int64_t K, const uint8_t*
     if (!g != !u || !known_activation(act)) return BITLINEAR_ERR_INVALID_ARG;
     int st = check_sizes(M, K, F);
     if (st) return st;
+    const GatedArgs a{x_q, beta, M, K, F, Wg_packed, Wu_packed, alpha_g, alpha_u, bias_g, bias_u, act, h, g, u};
+    if (gated_gemv_supports(a, x)) return hip_status(launch_gated_gemv(a, x, x_q, beta, stream));
     st = hip_status(launch_quantize_act(x, M, K, x_q, beta, stream));
     if (st) return st;
-    const GatedArgs a{x_q, beta, M, K, F, Wg_packed, Wu_packed, alpha_g, alpha_u, bias_g, bias_u, act, h, g, u};
     return hip_status(launch_gated(a, stream));
 }
 

@@ -66,6 +66,9 @@ struct GatedArgs {
 };
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
+// One token with x quantized in the same launch (a.xq and a.beta are written, not read).
+bool gated_gemv_supports(const GatedArgs& a, const float* x);
+hipError_t launch_gated_gemv(const GatedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s);
 
 struct I8Args {
     const int8_t* xq;

@@ -6,54 +6,492 @@
 //     p[m, n]     = fp32(acc_p) * fp32(alpha_p beta[m] / 127)  (+ bias_p[n])
 //     h[m, n]     = a(gate[m, n]) * up[m, n]                                 (one fp32 rounding)
 // so that gate and up equal two BitLinear forwards bit for bit.
+//
+// Every kernel gives the same lanes a gate row and the up row of the same column, so that the
+// product is formed where the sums end.  Three kernels by the number of tokens:
+//   * one token: k_gated_gemv, which also quantizes x, on v_dot4_i32_i8;
+//   * up to 64: k_gated_dec, the weight streams on the 16x16x64 int8 MFMA;
+//   * more: k_gated_gemm, LDS tiles on the 32x32x32 int8 MFMA;
+// the last two also in a form for any K % 4 == 0 and any alignment.
 #include "ffn.hpp"
 
 namespace bitlinear {
 
-// One wave per output column n, lanes over packed bytes; any K % 4 == 0, any alignment.
-template <int ACT>
-__global__ __launch_bounds__(256) void k_gated_generic(GatedArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (n >= a.F) return;
-    const int64_t K = a.K, rowb = K >> 2;
-    for (int64_t m = 0; m < a.M; ++m) {
-        int sg = 0, su = 0;
-        for (int64_t b = lane; b < rowb; b += 64) {
-            const uint32_t cg = a.wg[n * rowb + b], cu = a.wu[n * rowb + b];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int x = a.xq[m * K + 4 * b + i];
-                sg += ((int)((cg >> (2 * i)) & 3u) - 1) * x;
-                su += ((int)((cu >> (2 * i)) & 3u) - 1) * x;
-            }
-        }
-        sg = wave_sum_i32(sg);
-        su = wave_sum_i32(su);
-        if (lane == 0) {
-            const float g = dequant(sg, dequant_scale(a.ag[0], a.beta[m]), a.bg, n);
-            const float u = dequant(su, dequant_scale(a.au[0], a.beta[m]), a.bu, n);
-            a.h[m * a.F + n] = act_value<ACT>(g) * u;
-            if (a.g) {
-                a.g[m * a.F + n] = g;
-                a.u[m * a.F + n] = u;
-            }
-        }
+// Element (m, n): g and u from their sums and scales, the activation and the product.
+__device__ __forceinline__ void gated_store(const GatedArgs& a, int64_t at, int64_t n, int sg, int su, float scale_g,
+                                            float scale_u) {
+    const float g = dequant(sg, scale_g, a.bg, n);
+    const float u = dequant(su, scale_u, a.bu, n);
+    const float v = a.act == BITLINEAR_ACT_SILU   ? act_value<BITLINEAR_ACT_SILU>(g)
+                    : a.act == BITLINEAR_ACT_GELU ? act_value<BITLINEAR_ACT_GELU>(g)
+                                                  : act_value<BITLINEAR_ACT_RELU2>(g);
+    a.h[at] = v * u;
+    if (a.g) {
+        a.g[at] = g;
+        a.u[at] = u;
     }
 }
 
-template <int ACT>
-static hipError_t launch_gated_act(const GatedArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((k_gated_generic<ACT>), dim3((unsigned)((a.F + 3) / 4)), dim3(256), 0, s, a);
+// 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.
+__device__ __forceinline__ u32x4 row_16(const uint8_t* __restrict__ p, int64_t i, int64_t row) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (i + 16 <= row) {
+        __builtin_memcpy(&v, p + i, 16);
+    } else {
+        for (int j = 0; j < 16; ++j)
+            if (i + j < row) v[j >> 2] |= (uint32_t)p[i + j] << (8 * (j & 3));
+    }
+    return v;
+}
+
+// ---- one token ------------------------------------------------------------------------------
+// A workgroup of eight waves quantizes x for itself (absmax, codes, their sum) while its first weight
+// rows are on their way; a wave then takes `pairs` gate and up rows, R of each at a time.  A lane's
+// load is 64 codes of a row (16 bytes); the matching x_q lies in LDS transposed 4 x 4 in each group
+// of 16, so that a masked dword of codes meets its four fields' x_q in v_dot4 (chunk_sum).
+// CPL: chunks of 64 weights per lane and row.
+constexpr int GV_WAVES = 8;
+
+template <int CPL, int R>
+__global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const float* __restrict__ x, int8_t* __restrict__ xq_out,
+                                                              float* __restrict__ beta_out, int pairs) {
+    constexpr int NT = 64 * GV_WAVES, FPT = CPL * 1024 / NT;        // float4s of x per thread, at most
+    __shared__ u32x4 xs[CPL * 256];                                 // unit (chunk / 64, group of 16, lane)
+    __shared__ float red_f[GV_WAVES];
+    __shared__ int red_i[GV_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t K = a.K, rowb = K >> 2;
+    const int C = (int)(K >> 6), k4 = (int)(K >> 2);
+    const int64_t rb = ((int64_t)blockIdx.x * GV_WAVES + wave) * pairs;
+    const int64_t re = rb + pairs < a.F ? rb + pairs : a.F;         // may be <= rb: no rows
+    float4 xv[FPT];
+#pragma unroll
+    for (int i = 0; i < FPT; ++i) xv[i] = reinterpret_cast<const float4*>(x)[tid + NT * i < k4 ? tid + NT * i : 0];
+    // rows past the wave's range re-read its last row (not written); chunks past the row re-read
+    // chunk 0, whose x_q there is zero
+    u32x4 wg[R][CPL], wu[R][CPL];
+    auto load = [&](int64_t r0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = r0 + r < re ? r0 + r : re > 0 ? re - 1 : 0;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                const int c = lane + 64 * j < C ? lane + 64 * j : 0;
+                wg[r][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.wg + row * rowb + 16 * c));
+                wu[r][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.wu + row * rowb + 16 * c));
+            }
+        }
+    };
+    load(rb);
+    float mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < FPT; ++i) mx = fmaxf(mx, fmaxf(fmaxf(fabsf(xv[i].x), fabsf(xv[i].y)), fmaxf(fabsf(xv[i].z), fabsf(xv[i].w))));
+    mx = wave_max_f32(mx);
+    if (lane == 0) red_f[wave] = mx;
+    __syncthreads();
+    mx = red_f[0];
+#pragma unroll
+    for (int w = 1; w < GV_WAVES; ++w) mx = fmaxf(mx, red_f[w]);
+    const float beta = mx + 1e-8f;
+    uint8_t* xb = reinterpret_cast<uint8_t*>(xs);
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < FPT; ++i) {
+        const int f = tid + NT * i, c = f >> 4, q = (f >> 2) & 3, jj = f & 3;
+        const float v[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+        uint32_t d = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float t = fminf(fmaxf(rintf(v[e] * 127.0f / beta), -127.0f), 127.0f);
+            const int code = f < k4 ? (int)t : 0;
+            sum += code;
+            d |= (uint32_t)(uint8_t)code << (8 * e);
+            xb[((((c >> 6) * 4 + q) << 6) + (c & 63)) * 16 + 4 * e + jj] = (uint8_t)code;
+        }
+        if (blockIdx.x == 0 && f < k4) {
+            for (int e = 0; e < 4; ++e) xq_out[4 * f + e] = (int8_t)(d >> (8 * e));
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) beta_out[0] = beta;
+    sum = wave_sum_i32(sum);
+    if (lane == 0) red_i[wave] = sum;
+    __syncthreads();
+    int xsum = 0;
+#pragma unroll
+    for (int w = 0; w < GV_WAVES; ++w) xsum += red_i[w];
+    const float scale_g = dequant_scale(a.ag[0], beta), scale_u = dequant_scale(a.au[0], beta);
+    for (int64_t r0 = rb; r0 < re; r0 += R) {
+        int sg[R], su[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            sg[r] = su[r] = 0;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                sg[r] += chunk_sum(wg[r][j], xs + j * 256 + lane, 64, 0);
+                su[r] += chunk_sum(wu[r][j], xs + j * 256 + lane, 64, 0);
+            }
+        }
+        if (r0 + R < re) load(r0 + R);
+        int mg = 0, mu = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int tg = wave_sum_i32(sg[r]), tu = wave_sum_i32(su[r]);
+            if (lane == r) {
+                mg = tg;
+                mu = tu;
+            }
+        }
+        if (lane < R && r0 + lane < re) gated_store(a, r0 + lane, r0 + lane, mg - xsum, mu - xsum, scale_g, scale_u);
+    }
+}
+
+template <int CPL>
+static hipError_t launch_gated_gemv_cpl(const GatedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s) {
+    constexpr int R = CPL <= 2 ? 4 / CPL : 1;
+    // about 2048 waves: 256 workgroups, since every one of them quantizes x
+    const int64_t pairs = (a.F + 2047) / 2048, waves = (a.F + pairs - 1) / pairs;
+    hipLaunchKernelGGL((k_gated_gemv<CPL, R>), dim3((unsigned)((waves + GV_WAVES - 1) / GV_WAVES)), dim3(64 * GV_WAVES), 0, s, a, x,
+                       xq, beta, (int)pairs);
+    return hipGetLastError();
+}
+
+bool gated_gemv_supports(const GatedArgs& a, const float* x) {
+    return a.M == 1 && a.K % 64 == 0 && a.K <= 16384 && (uintptr_t)x % 16 == 0 && (uintptr_t)a.wg % 16 == 0 &&
+           (uintptr_t)a.wu % 16 == 0;
+}
+
+hipError_t launch_gated_gemv(const GatedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s) {
+    switch ((a.K / 64 + 63) / 64) {
+        case 1: return launch_gated_gemv_cpl<1>(a, x, xq, beta, s);
+        case 2: return launch_gated_gemv_cpl<2>(a, x, xq, beta, s);
+        case 3: return launch_gated_gemv_cpl<3>(a, x, xq, beta, s);
+        default: return launch_gated_gemv_cpl<4>(a, x, xq, beta, s);
+    }
+}
+
+// ---- up to 64 tokens ------------------------------------------------------------------------
+// A workgroup of eight waves computes 16 MT tokens x 16 RB columns of both projections; wave w takes
+// the steps of 256 k w, w + 8, ..., and the partial tiles are added at the end (integers: exact in
+// any order).  In MFMA q of a step lane group g (lanes 16 g ..) holds weights 64 g + 16 q ..
+// 64 g + 16 q + 15, dword q of the lane's 16 bytes of codes, expanded in weight order to signed bytes.
+// Aligned rows (K % 256 == 0): operands come through a wave's own LDS image, filled by loads that go
+// past the registers; a step's image is read into registers, the next step's loads are started into
+// it, and the MFMAs run while they are in flight.  Token T's 16-byte unit u of a step lies at position
+// u ^ (T % 16) of its sixteen.  Otherwise operands are read straight into registers.
+// 16x16x64 lane layout: A/B lane l holds row/column l % 16, k = 16 (l / 16) + j; accumulator r of
+// lane l is row 4 (l / 16) + r, column l % 16.
+constexpr int GD_WAVES = 8;
+
+template <bool ALIGNED, int MT, int RB>
+__global__ __launch_bounds__(64 * GD_WAVES) void k_gated_dec(GatedArgs a, int slices) {
+    constexpr int IMG = (4 * MT + 2 * RB) * 64;                     // 16-byte units of a wave's image
+    constexpr int TILES = 2 * RB * MT * 64;                         // of a wave's partial tiles
+    constexpr int PER = ALIGNED && IMG > TILES ? IMG : TILES;
+    __shared__ i32x4 lds[GD_WAVES * PER];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t K = a.K, rowb = K >> 2;
+    const int64_t m0 = (int64_t)(blockIdx.x % slices) * (16 * MT), n0 = (int64_t)(blockIdx.x / slices) * (16 * RB);
+    const int rows_m = (int)(a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT), rows_n = (int)(a.F - n0 < 16 * RB ? a.F - n0 : 16 * RB);
+    const int8_t* x0 = a.xq + m0 * K;
+    const uint8_t *g0 = a.wg + n0 * rowb, *u0 = a.wu + n0 * rowb;
+    const int steps = (int)((K + 255) / 256);
+    const int lr = lane & 15, lg = lane >> 4;
+    i32x4 acc[2 * RB][MT];
+#pragma unroll
+    for (int r = 0; r < 2 * RB; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[r][t] = i32x4{0, 0, 0, 0};
+    // rows 0 .. RB - 1 of w: gate blocks, RB .. 2 RB - 1: up blocks
+    auto multiply = [&](const i32x4 (&xv)[MT][4], const u32x4 (&w)[2 * RB]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int r = 0; r < 2 * RB; ++r) {
+                const i32x4 b = expand_signed_in_order(w[r][q]);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv[t][q], b, acc[r][t], 0, 0, 0);
+            }
+    };
+    if constexpr (ALIGNED) {
+        i32x4* img = lds + wave * IMG;
+        const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
+        const __amdgpu_buffer_rsrc_t rg = raw_buffer(g0, (uint32_t)rows_n * (uint32_t)rowb);
+        const __amdgpu_buffer_rsrc_t ru = raw_buffer(u0, (uint32_t)rows_n * (uint32_t)rowb);
+        // load i of x: tokens 4 i .. 4 i + 3, sixteen lanes each; load r of a matrix: lane (lr, lg) reads
+        // 64 codes of row 16 r + lr.  Rows past the end repeat the last one.
+        uint32_t xo[4 * MT], wo[RB];
+#pragma unroll
+        for (int i = 0; i < 4 * MT; ++i)
+            xo[i] = (uint32_t)min(4 * i + lg, rows_m - 1) * (uint32_t)K + 16u * (uint32_t)(lr ^ ((4 * i + lg) & 15));
+#pragma unroll
+        for (int r = 0; r < RB; ++r) wo[r] = (uint32_t)min(16 * r + lr, rows_n - 1) * (uint32_t)rowb + 16u * (uint32_t)lg;
+        auto fetch = [&](int s) {
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                load_lds16(rg, wo[r], (uint32_t)s * 64u, img + 64 * (4 * MT + r));
+                load_lds16(ru, wo[r], (uint32_t)s * 64u, img + 64 * (4 * MT + RB + r));
+            }
+#pragma unroll
+            for (int i = 0; i < 4 * MT; ++i) load_lds16(rx, xo[i], (uint32_t)s * 256u, img + 64 * i);
+        };
+        if (wave < steps) fetch(wave);
+        for (int s = wave; s < steps; s += GD_WAVES) {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0x0F70);                     // vmcnt(0): the image is whole
+            __builtin_amdgcn_sched_barrier(0);
+            i32x4 xv[MT][4];
+            u32x4 w[2 * RB];
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) xv[t][q] = img[(16 * t + lr) * 16 + ((4 * lg + q) ^ lr)];
+#pragma unroll
+            for (int r = 0; r < 2 * RB; ++r) w[r] = (u32x4)img[64 * (4 * MT + r) + lane];
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0xC07F);                     // lgkmcnt(0): every read of it is over
+            __builtin_amdgcn_sched_barrier(0);
+            if (s + GD_WAVES < steps) fetch(s + GD_WAVES);
+            multiply(xv, w);
+        }
+    } else {
+        for (int s = wave; s < steps; s += GD_WAVES) {
+            const int64_t k = (int64_t)s * 256 + 64 * lg;
+            i32x4 xv[MT][4];
+            u32x4 w[2 * RB];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const int64_t row = (int64_t)min(16 * r + lr, rows_n - 1) * rowb;
+                w[r] = row_16(g0 + row, k >> 2, rowb);
+                w[RB + r] = row_16(u0 + row, k >> 2, rowb);
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    xv[t][q] = (i32x4)row_16(reinterpret_cast<const uint8_t*>(x0) + (int64_t)min(16 * t + lr, rows_m - 1) * K,
+                                             k + 16 * q, K);
+            multiply(xv, w);
+        }
+    }
+    __syncthreads();                                                // every wave is done with its image
+#pragma unroll
+    for (int r = 0; r < 2 * RB; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) lds[(wave * 2 * RB * MT + r * MT + t) * 64 + lane] = acc[r][t];
+    __syncthreads();
+    const float ag = a.ag[0], au = a.au[0];
+    // element e = (block, token block, lane, i): i-th accumulator
+    for (int e = tid; e < RB * MT * 256; e += 64 * GD_WAVES) {
+        const int l = e & 63, i = (e >> 6) & 3, tile = e >> 8, r = tile / MT, t = tile % MT;
+        const int n = 16 * r + (l & 15), m = 16 * t + 4 * (l >> 4) + i;
+        if (n >= rows_n || m >= rows_m) continue;
+        int sg = 0, su = 0;
+#pragma unroll
+        for (int w = 0; w < GD_WAVES; ++w) {
+            const int* p = reinterpret_cast<const int*>(lds + (w * 2 * RB * MT + tile) * 64 + l);
+            sg += p[i];
+            su += p[i + RB * MT * 256];
+        }
+        const float beta = a.beta[m0 + m];
+        gated_store(a, (m0 + m) * a.F + n0 + n, n0 + n, sg, su, dequant_scale(ag, beta), dequant_scale(au, beta));
+    }
+}
+
+template <bool ALIGNED, int MT, int RB>
+static hipError_t launch_gated_dec_rb(const GatedArgs& a, hipStream_t s) {
+    const int64_t slices = (a.M + 16 * MT - 1) / (16 * MT), blocks = (a.F + 16 * RB - 1) / (16 * RB);
+    hipLaunchKernelGGL((k_gated_dec<ALIGNED, MT, RB>), dim3((unsigned)(slices * blocks)), dim3(64 * GD_WAVES), 0, s, a, (int)slices);
+    return hipGetLastError();
+}
+
+template <bool ALIGNED, int MT>
+static hipError_t launch_gated_dec_mt(const GatedArgs& a, hipStream_t s) {
+    const int64_t wgs = (a.M + 16 * MT - 1) / (16 * MT) * ((a.F + 15) / 16);
+    return wgs <= 256 ? launch_gated_dec_rb<ALIGNED, MT, 1>(a, s) : launch_gated_dec_rb<ALIGNED, MT, 2>(a, s);
+}
+
+template <bool ALIGNED>
+static hipError_t launch_gated_dec(const GatedArgs& a, hipStream_t s) {
+    const int64_t tiles = (a.M + 15) / 16;
+    return tiles == 1   ? launch_gated_dec_mt<ALIGNED, 1>(a, s)
+           : tiles == 2 ? launch_gated_dec_mt<ALIGNED, 2>(a, s)
+           : tiles == 3 ? launch_gated_dec_mt<ALIGNED, 3>(a, s)
+                        : launch_gated_dec_mt<ALIGNED, 4>(a, s);
+}
+
+// ---- more tokens ----------------------------------------------------------------------------
+// A workgroup of four waves computes 128 tokens x 128 columns of both projections, a wave all 128
+// tokens x 32 columns of each: four 32-token operands against one gate and one up operand, so that
+// the expansion of a weight operand (17 instructions) serves four MFMAs.  Steps of 128 k, three LDS
+// stages (24 KiB each: 128 token rows of 128 bytes, 256 weight rows of 32 bytes) filled two steps
+// ahead by loads that go past the registers (aligned rows: K % 128 == 0), or two filled through
+// registers.  Unit u of token row r lies at slot u ^ ((r / 2) % 8), unit u of weight row r at slot
+// u ^ ((r / 8) % 2), so that an operand read spreads over all banks.
+// In the two MFMAs of k 64 h .. 64 h + 63 (h = 0, 1) a lane group holds 32 codes, eight bytes of a
+// weight row: the lane's unit h, of which group lg uses dwords 2 lg and 2 lg + 1.
+constexpr int GG_BM = 128, GG_BF = 128, GG_BK = 128;
+
+template <bool ALIGNED>
+__global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m, int tiles_f) {
+    constexpr int OB = GG_BM * 8, UNITS = OB + 2 * GG_BF * 2;
+    __shared__ i32x4 st0[UNITS];
+    __shared__ i32x4 st1[UNITS];
+    __shared__ i32x4 st2[ALIGNED ? UNITS : 1];
+    __shared__ __align__(16) float scale[2][GG_BM];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // a contiguous run of tiles for each XCD, four rows of tiles at a time
+    const int T = tiles_m * tiles_f, xcd = blockIdx.x & 7, per = T >> 3, rem = T & 7;
+    int t = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+    const int grp = t / (4 * tiles_f), gm = tiles_m - 4 * grp < 4 ? tiles_m - 4 * grp : 4;
+    t -= grp * 4 * tiles_f;
+    const int64_t m0 = (int64_t)(4 * grp + t % gm) * GG_BM, n0 = (int64_t)(t / gm) * GG_BF;
+    const int64_t K = a.K, rowb = K >> 2;
+    const int rows_m = (int)(a.M - m0 < GG_BM ? a.M - m0 : GG_BM), rows_n = (int)(a.F - n0 < GG_BF ? a.F - n0 : GG_BF);
+    const uint8_t* x0 = reinterpret_cast<const uint8_t*>(a.xq) + m0 * K;
+    const uint8_t *g0 = a.wg + n0 * rowb, *u0 = a.wu + n0 * rowb;
+    if (tid < GG_BM) {
+        const float beta = a.beta[m0 + (tid < rows_m ? tid : 0)];
+        scale[0][tid] = dequant_scale(a.ag[0], beta);
+        scale[1][tid] = dequant_scale(a.au[0], beta);
+    }
+
+    i32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
+    const int lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7, sb = (lr >> 3) & 1;
+    auto multiply = [&](const i32x4* st) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // weight rows of a stage: 128 gate rows, then 128 up rows
+            uint2 w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                w[j] = reinterpret_cast<const uint2*>(st + OB + (128 * j + 32 * wave + lr) * 2 + (h ^ sb))[lg];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                i32x4 fa[4], fb[2];
+                const int u = 4 * h + 2 * lg + kk;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fa[i] = st[(32 * i + lr) * 8 + (u ^ sw)];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) fb[j] = expand_signed_in_order(kk ? w[j].y : w[j].x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+            }
+        }
+    };
+    // load block q of x: token rows 8 q .. 8 q + 7 (wave w takes 4 w .. 4 w + 3); of a matrix: rows
+    // 32 q .. 32 q + 31 (wave w takes q = w of both)
+    const int wrow = 32 * wave + (lane >> 1), wunit = (lane & 1) ^ ((wrow >> 3) & 1);
+    auto xrow = [&](int q) { return 8 * (4 * wave + q) + (lane >> 3); };
+    auto xunit = [&](int q) { return (lane & 7) ^ ((xrow(q) >> 1) & 7); };
+    if constexpr (ALIGNED) {
+        const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
+        const __amdgpu_buffer_rsrc_t rg = raw_buffer(g0, (uint32_t)rows_n * (uint32_t)rowb);
+        const __amdgpu_buffer_rsrc_t ru = raw_buffer(u0, (uint32_t)rows_n * (uint32_t)rowb);
+        uint32_t xo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) xo[q] = (uint32_t)min(xrow(q), rows_m - 1) * (uint32_t)K + 16u * xunit(q);
+        const uint32_t wo = (uint32_t)min(wrow, rows_n - 1) * (uint32_t)rowb + 16u * wunit;
+        const int steps = (int)(K / GG_BK), last = steps - 1;
+        auto fetch = [&](i32x4* st, int s) {
+            s = s < last ? s : last;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) load_lds16(rx, xo[q], (uint32_t)s * GG_BK, st + 64 * (4 * wave + q));
+            load_lds16(rg, wo, (uint32_t)s * (GG_BK / 4), st + OB + 64 * wave);
+            load_lds16(ru, wo, (uint32_t)s * (GG_BK / 4), st + OB + 256 + 64 * wave);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // the stage to be read has landed, for every wave, and every read of the stage to be filled is
+        // over; loads past the last step repeat it and are not read
+        auto turn = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0x0070 | 6);                 // vmcnt(6: the next stage's loads) lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int s = 0;
+        fetch(st0, 0);
+        fetch(st1, 1);
+        for (; s + 3 <= steps; s += 3) {
+            turn();
+            fetch(st2, s + 2);
+            multiply(st0);
+            turn();
+            fetch(st0, s + 3);
+            multiply(st1);
+            turn();
+            fetch(st1, s + 4);
+            multiply(st2);
+        }
+        if (s < steps) {
+            turn();
+            multiply(st0);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070);                         // nothing is in flight into the stages any more
+        __builtin_amdgcn_s_barrier();
+        if (s + 1 < steps) multiply(st1);
+    } else {
+        u32x4 v[6];
+        const int steps = (int)((K + GG_BK - 1) / GG_BK);
+        auto load = [&](int s) {
+            const int64_t k = (int64_t)s * GG_BK, w = (int64_t)min(wrow, rows_n - 1) * rowb;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = row_16(x0 + (int64_t)min(xrow(q), rows_m - 1) * K, k + 16 * xunit(q), K);
+            v[4] = row_16(g0 + w, (k >> 2) + 16 * wunit, rowb);
+            v[5] = row_16(u0 + w, (k >> 2) + 16 * wunit, rowb);
+        };
+        auto put = [&](i32x4* st) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) st[64 * (4 * wave + q) + lane] = (i32x4)v[q];
+            st[OB + 64 * wave + lane] = (i32x4)v[4];
+            st[OB + 256 + 64 * wave + lane] = (i32x4)v[5];
+        };
+        load(0);
+        put(st0);
+        for (int s = 0; s < steps; ++s) {
+            __syncthreads();                                        // step s is in its stage, and the other stage is free
+            if (s + 1 < steps) load(s + 1);
+            multiply(s & 1 ? st1 : st0);
+            if (s + 1 < steps) put(s & 1 ? st0 : st1);
+        }
+    }
+    // accumulator r of lane l: token 8 (r / 4) + 4 (l / 32) + r % 4 of the block, column l % 32
+    const int n = 32 * wave + lr;
+    if (n >= rows_n) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int m = 32 * i + 8 * q + 4 * lg;
+            const float4 g4 = *reinterpret_cast<const float4*>(&scale[0][m]), u4 = *reinterpret_cast<const float4*>(&scale[1][m]);
+            const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (m + e < rows_m)
+                    gated_store(a, (m0 + m + e) * a.F + n0 + n, n0 + n, acc[i][0][4 * q + e], acc[i][1][4 * q + e], gs[e], us[e]);
+        }
+}
+
+template <bool ALIGNED>
+static hipError_t launch_gated_gemm(const GatedArgs& a, hipStream_t s) {
+    const int64_t tm = (a.M + GG_BM - 1) / GG_BM, tf = (a.F + GG_BF - 1) / GG_BF;
+    hipLaunchKernelGGL((k_gated_gemm<ALIGNED>), dim3((unsigned)(tm * tf)), dim3(256), 0, s, a, (int)tm, (int)tf);
     return hipGetLastError();
 }
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
-    switch (a.act) {
-        case BITLINEAR_ACT_GELU: return launch_gated_act<BITLINEAR_ACT_GELU>(a, s);
-        case BITLINEAR_ACT_SILU: return launch_gated_act<BITLINEAR_ACT_SILU>(a, s);
-        default: return launch_gated_act<BITLINEAR_ACT_RELU2>(a, s);
-    }
+    const bool aligned = (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.wg % 16 == 0 && (uintptr_t)a.wu % 16 == 0;
+    if (a.M <= 64) return aligned && a.K % 256 == 0 ? launch_gated_dec<true>(a, s) : launch_gated_dec<false>(a, s);
+    return aligned && a.K % 128 == 0 ? launch_gated_gemm<true>(a, s) : launch_gated_gemm<false>(a, s);
 }
 
 }  // namespace bitlinear
