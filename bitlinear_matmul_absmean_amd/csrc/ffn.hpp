@@ -7,14 +7,29 @@
 
 namespace bitlinear {
 
-// a(g) of the gated block, in fp32.  SiLU: g / (1 + exp(-g)), the exponential within two units
-// in the last place and the sum and quotient rounded once each (exp(-g) = inf gives -0, the
-// limit).  GELU: the BitMLP's.  Squared ReLU: one rounding.
+// exp(-x) for |x| <= 128, within 4 * 2^-24 relative (x >= -88: finite): the exponent x log2(e) as a
+// rounded product and its remainder, the hardware's 2^h (within one unit) and a first-order factor.
+__device__ __forceinline__ float exp_neg(float x) {
+    constexpr float L = 1.44269504088896341f, L_LO = 1.92596299112661746e-8f, LN2 = 0.69314718055994531f;
+    const float h = x * -L;
+    const float r = __builtin_fmaf(x, -L_LO, __builtin_fmaf(x, -L, -h));
+    const float e = __builtin_amdgcn_exp2f(h);
+    return __builtin_fmaf(e, r * LN2, e);
+}
+
+// a(g) of the gated block, in fp32.  SiLU: g / (1 + exp(-g)), the quotient from the hardware's
+// reciprocal and one correction; below -88 it stays at its value there, -5.3e-37 (13 instructions;
+// the library's exp and an IEEE division took 40, a third of the epilogue of a short GEMM).
+// GELU: the BitMLP's.  Squared ReLU: one rounding.
 template <int ACT>
 __device__ __forceinline__ float act_value(float g) {
-    if constexpr (ACT == BITLINEAR_ACT_SILU) return g / (1.0f + expf(-g));
-    else if constexpr (ACT == BITLINEAR_ACT_GELU) return gelu_f32(g);
-    else {
+    if constexpr (ACT == BITLINEAR_ACT_SILU) {
+        const float v = fmaxf(g, -88.0f), d = 1.0f + exp_neg(fminf(v, 128.0f));
+        const float r = __builtin_amdgcn_rcpf(d), q = v * r;
+        return __builtin_fmaf(__builtin_fmaf(-q, d, v), r, q);
+    } else if constexpr (ACT == BITLINEAR_ACT_GELU) {
+        return gelu_f32(g);
+    } else {
         const float r = fmaxf(g, 0.0f);
         return r * r;
     }
@@ -29,7 +44,7 @@ __device__ __forceinline__ float act_value(float g) {
 template <int ACT>
 __device__ __forceinline__ void act_grad(float g, float& a, float& slope) {
     if constexpr (ACT == BITLINEAR_ACT_SILU) {
-        const float e = expf(-fabsf(g)), t = __builtin_amdgcn_rcpf(1.0f + e), p = e * t;
+        const float e = exp_neg(fminf(fabsf(g), 128.0f)), t = __builtin_amdgcn_rcpf(1.0f + e), p = e * t;
         const float s = g >= 0.0f ? t : p, sc = g >= 0.0f ? p : t;
         a = g * s;
         slope = s + a * sc;

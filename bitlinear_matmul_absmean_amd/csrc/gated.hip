@@ -17,19 +17,27 @@
 
 namespace bitlinear {
 
-// Element (m, n): g and u from their sums and scales, the activation and the product.
-__device__ __forceinline__ void gated_store(const GatedArgs& a, int64_t at, int64_t n, int sg, int su, float scale_g,
-                                            float scale_u) {
-    const float g = dequant(sg, scale_g, a.bg, n);
-    const float u = dequant(su, scale_u, a.bu, n);
-    const float v = a.act == BITLINEAR_ACT_SILU   ? act_value<BITLINEAR_ACT_SILU>(g)
-                    : a.act == BITLINEAR_ACT_GELU ? act_value<BITLINEAR_ACT_GELU>(g)
-                                                  : act_value<BITLINEAR_ACT_RELU2>(g);
-    a.h[at] = v * u;
+// Element `at` of column n: g and u from their sums and scales, the activation and the product.
+template <int ACT>
+__device__ __forceinline__ void gated_store(const GatedArgs& a, int64_t at, int sg, int su, float scale_g, float scale_u, float bg,
+                                            float bu) {
+    float g = (float)sg * scale_g, u = (float)su * scale_u;
+    if (a.bg) g = g + bg;
+    if (a.bu) u = u + bu;
+    a.h[at] = act_value<ACT>(g) * u;
     if (a.g) {
         a.g[at] = g;
         a.u[at] = u;
     }
+}
+
+// The same with the activation chosen at run time, for the kernels with few elements a lane.
+__device__ __forceinline__ void gated_store(const GatedArgs& a, int64_t at, int64_t n, int sg, int su, float scale_g,
+                                            float scale_u) {
+    const float bg = a.bg ? a.bg[n] : 0.0f, bu = a.bu ? a.bu[n] : 0.0f;
+    if (a.act == BITLINEAR_ACT_SILU) gated_store<BITLINEAR_ACT_SILU>(a, at, sg, su, scale_g, scale_u, bg, bu);
+    else if (a.act == BITLINEAR_ACT_GELU) gated_store<BITLINEAR_ACT_GELU>(a, at, sg, su, scale_g, scale_u, bg, bu);
+    else gated_store<BITLINEAR_ACT_RELU2>(a, at, sg, su, scale_g, scale_u, bg, bu);
 }
 
 // 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.
@@ -175,7 +183,7 @@ hipError_t launch_gated_gemv(const GatedArgs& a, const float* x, int8_t* xq, flo
 // the steps of 256 k w, w + 8, ..., and the partial tiles are added at the end (integers: exact in
 // any order).  In MFMA q of a step lane group g (lanes 16 g ..) holds weights 64 g + 16 q ..
 // 64 g + 16 q + 15, dword q of the lane's 16 bytes of codes, expanded in weight order to signed bytes.
-// Aligned rows (K % 256 == 0): operands come through a wave's own LDS image, filled by loads that go
+// Aligned rows (16-byte aligned tensors, K % 64 == 0): operands come through a wave's own LDS image, filled by loads that go
 // past the registers; a step's image is read into registers, the next step's loads are started into
 // it, and the MFMAs run while they are in flight.  Token T's 16-byte unit u of a step lies at position
 // u ^ (T % 16) of its sixteen.  Otherwise operands are read straight into registers.
@@ -214,7 +222,26 @@ __global__ __launch_bounds__(64 * GD_WAVES) void k_gated_dec(GatedArgs a, int sl
                 for (int t = 0; t < MT; ++t) acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv[t][q], b, acc[r][t], 0, 0, 0);
             }
     };
+    // step s with its operands read straight into registers
+    auto direct = [&](int s) {
+        const int64_t k = (int64_t)s * 256 + 64 * lg;
+        i32x4 xv[MT][4];
+        u32x4 w[2 * RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const int64_t row = (int64_t)min(16 * r + lr, rows_n - 1) * rowb;
+            w[r] = row_16(g0 + row, k >> 2, rowb);
+            w[RB + r] = row_16(u0 + row, k >> 2, rowb);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                xv[t][q] = (i32x4)row_16(reinterpret_cast<const uint8_t*>(x0) + (int64_t)min(16 * t + lr, rows_m - 1) * K, k + 16 * q, K);
+        multiply(xv, w);
+    };
     if constexpr (ALIGNED) {
+        const int whole = (int)(K / 256);                           // a last part step is read directly
         i32x4* img = lds + wave * IMG;
         const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
         const __amdgpu_buffer_rsrc_t rg = raw_buffer(g0, (uint32_t)rows_n * (uint32_t)rowb);
@@ -236,8 +263,8 @@ __global__ __launch_bounds__(64 * GD_WAVES) void k_gated_dec(GatedArgs a, int sl
 #pragma unroll
             for (int i = 0; i < 4 * MT; ++i) load_lds16(rx, xo[i], (uint32_t)s * 256u, img + 64 * i);
         };
-        if (wave < steps) fetch(wave);
-        for (int s = wave; s < steps; s += GD_WAVES) {
+        if (wave < whole) fetch(wave);
+        for (int s = wave; s < whole; s += GD_WAVES) {
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0x0F70);                     // vmcnt(0): the image is whole
             __builtin_amdgcn_sched_barrier(0);
@@ -252,28 +279,12 @@ __global__ __launch_bounds__(64 * GD_WAVES) void k_gated_dec(GatedArgs a, int sl
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0xC07F);                     // lgkmcnt(0): every read of it is over
             __builtin_amdgcn_sched_barrier(0);
-            if (s + GD_WAVES < steps) fetch(s + GD_WAVES);
+            if (s + GD_WAVES < whole) fetch(s + GD_WAVES);
             multiply(xv, w);
         }
+        if (whole < steps && whole % GD_WAVES == wave) direct(whole);
     } else {
-        for (int s = wave; s < steps; s += GD_WAVES) {
-            const int64_t k = (int64_t)s * 256 + 64 * lg;
-            i32x4 xv[MT][4];
-            u32x4 w[2 * RB];
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const int64_t row = (int64_t)min(16 * r + lr, rows_n - 1) * rowb;
-                w[r] = row_16(g0 + row, k >> 2, rowb);
-                w[RB + r] = row_16(u0 + row, k >> 2, rowb);
-            }
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    xv[t][q] = (i32x4)row_16(reinterpret_cast<const uint8_t*>(x0) + (int64_t)min(16 * t + lr, rows_m - 1) * K,
-                                             k + 16 * q, K);
-            multiply(xv, w);
-        }
+        for (int s = wave; s < steps; s += GD_WAVES) direct(s);
     }
     __syncthreads();                                                // every wave is done with its image
 #pragma unroll
@@ -326,14 +337,14 @@ static hipError_t launch_gated_dec(const GatedArgs& a, hipStream_t s) {
 // tokens x 32 columns of each: four 32-token operands against one gate and one up operand, so that
 // the expansion of a weight operand (17 instructions) serves four MFMAs.  Steps of 128 k, three LDS
 // stages (24 KiB each: 128 token rows of 128 bytes, 256 weight rows of 32 bytes) filled two steps
-// ahead by loads that go past the registers (aligned rows: K % 128 == 0), or two filled through
+// ahead by loads that go past the registers (aligned rows: 16-byte aligned tensors, K % 64 == 0), or two filled through
 // registers.  Unit u of token row r lies at slot u ^ ((r / 2) % 8), unit u of weight row r at slot
 // u ^ ((r / 8) % 2), so that an operand read spreads over all banks.
 // In the two MFMAs of k 64 h .. 64 h + 63 (h = 0, 1) a lane group holds 32 codes, eight bytes of a
 // weight row: the lane's unit h, of which group lg uses dwords 2 lg and 2 lg + 1.
 constexpr int GG_BM = 128, GG_BF = 128, GG_BK = 128;
 
-template <bool ALIGNED>
+template <int ACT, bool ALIGNED>
 __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m, int tiles_f) {
     constexpr int OB = GG_BM * 8, UNITS = OB + 2 * GG_BF * 2;
     __shared__ i32x4 st0[UNITS];
@@ -364,9 +375,10 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
     const int lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7, sb = (lr >> 3) & 1;
-    auto multiply = [&](const i32x4* st) {
+    auto multiply = [&](const i32x4* st, int halves) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            if (h >= halves) break;
             // weight rows of a stage: 128 gate rows, then 128 up rows
             uint2 w[2];
 #pragma unroll
@@ -419,26 +431,41 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
             __builtin_amdgcn_sched_barrier(0);
         };
         int s = 0;
-        fetch(st0, 0);
-        fetch(st1, 1);
+        if (steps > 0) {
+            fetch(st0, 0);
+            fetch(st1, 1);
+        }
         for (; s + 3 <= steps; s += 3) {
             turn();
             fetch(st2, s + 2);
-            multiply(st0);
+            multiply(st0, 2);
             turn();
             fetch(st0, s + 3);
-            multiply(st1);
+            multiply(st1, 2);
             turn();
             fetch(st1, s + 4);
-            multiply(st2);
+            multiply(st2, 2);
         }
         if (s < steps) {
             turn();
-            multiply(st0);
+            multiply(st0, 2);
         }
         __builtin_amdgcn_s_waitcnt(0x0070);                         // nothing is in flight into the stages any more
         __builtin_amdgcn_s_barrier();
-        if (s + 1 < steps) multiply(st1);
+        if (s + 1 < steps) multiply(st1, 2);
+        if (K % GG_BK) {
+            // the last 64 k through st0, which nobody reads any more
+            const int64_t k = (int64_t)steps * GG_BK;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = (tid >> 2) + 64 * j, u = tid & 3;
+                st0[r * 8 + (u ^ ((r >> 1) & 7))] = *reinterpret_cast<const i32x4*>(x0 + (int64_t)min(r, rows_m - 1) * K + k + 16 * u);
+            }
+            const uint8_t* w = tid < 128 ? g0 : u0;
+            st0[OB + tid * 2 + ((tid >> 3) & 1)] = *reinterpret_cast<const i32x4*>(w + (int64_t)min(tid & 127, rows_n - 1) * rowb + (k >> 2));
+            __syncthreads();
+            multiply(st0, 1);
+        }
     } else {
         u32x4 v[6];
         const int steps = (int)((K + GG_BK - 1) / GG_BK);
@@ -460,13 +487,14 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
         for (int s = 0; s < steps; ++s) {
             __syncthreads();                                        // step s is in its stage, and the other stage is free
             if (s + 1 < steps) load(s + 1);
-            multiply(s & 1 ? st1 : st0);
+            multiply(s & 1 ? st1 : st0, 2);
             if (s + 1 < steps) put(s & 1 ? st0 : st1);
         }
     }
     // accumulator r of lane l: token 8 (r / 4) + 4 (l / 32) + r % 4 of the block, column l % 32
     const int n = 32 * wave + lr;
     if (n >= rows_n) return;
+    const float bg = a.bg ? a.bg[n0 + n] : 0.0f, bu = a.bu ? a.bu[n0 + n] : 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -474,24 +502,46 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
             const int m = 32 * i + 8 * q + 4 * lg;
             const float4 g4 = *reinterpret_cast<const float4*>(&scale[0][m]), u4 = *reinterpret_cast<const float4*>(&scale[1][m]);
             const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
+            const int64_t at = (m0 + m) * a.F + n0 + n;
+            float g[4], u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[e] = (float)acc[i][0][4 * q + e] * gs[e];
+                u[e] = (float)acc[i][1][4 * q + e] * us[e];
+                if (a.bg) g[e] = g[e] + bg;
+                if (a.bu) u[e] = u[e] + bu;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (m + e < rows_m)
-                    gated_store(a, (m0 + m + e) * a.F + n0 + n, n0 + n, acc[i][0][4 * q + e], acc[i][1][4 * q + e], gs[e], us[e]);
+                if (m + e < rows_m) a.h[at + e * a.F] = act_value<ACT>(g[e]) * u[e];
+            if (a.g) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (m + e < rows_m) {
+                        a.g[at + e * a.F] = g[e];
+                        a.u[at + e * a.F] = u[e];
+                    }
+            }
         }
 }
 
 template <bool ALIGNED>
 static hipError_t launch_gated_gemm(const GatedArgs& a, hipStream_t s) {
     const int64_t tm = (a.M + GG_BM - 1) / GG_BM, tf = (a.F + GG_BF - 1) / GG_BF;
-    hipLaunchKernelGGL((k_gated_gemm<ALIGNED>), dim3((unsigned)(tm * tf)), dim3(256), 0, s, a, (int)tm, (int)tf);
+    const dim3 grid((unsigned)(tm * tf));
+    if (a.act == BITLINEAR_ACT_SILU)
+        hipLaunchKernelGGL((k_gated_gemm<BITLINEAR_ACT_SILU, ALIGNED>), grid, dim3(256), 0, s, a, (int)tm, (int)tf);
+    else if (a.act == BITLINEAR_ACT_GELU)
+        hipLaunchKernelGGL((k_gated_gemm<BITLINEAR_ACT_GELU, ALIGNED>), grid, dim3(256), 0, s, a, (int)tm, (int)tf);
+    else
+        hipLaunchKernelGGL((k_gated_gemm<BITLINEAR_ACT_RELU2, ALIGNED>), grid, dim3(256), 0, s, a, (int)tm, (int)tf);
     return hipGetLastError();
 }
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
-    const bool aligned = (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.wg % 16 == 0 && (uintptr_t)a.wu % 16 == 0;
-    if (a.M <= 64) return aligned && a.K % 256 == 0 ? launch_gated_dec<true>(a, s) : launch_gated_dec<false>(a, s);
-    return aligned && a.K % 128 == 0 ? launch_gated_gemm<true>(a, s) : launch_gated_gemm<false>(a, s);
+    const bool aligned = a.K % 64 == 0 && (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.wg % 16 == 0 && (uintptr_t)a.wu % 16 == 0;
+    if (a.M <= 64) return aligned ? launch_gated_dec<true>(a, s) : launch_gated_dec<false>(a, s);
+    return aligned ? launch_gated_gemm<true>(a, s) : launch_gated_gemm<false>(a, s);
 }
 
 }  // namespace bitlinear

@@ -349,8 +349,9 @@ typedef enum bitlinear_activation {
  *     g = BitLinear(x; Wg, alpha_g, bias_g),  u = BitLinear(x; Wu, alpha_u, bias_u),
  *     h[m, n] = a(g[m, n]) * u[m, n].
  * x is quantized as by bitlinear_quantize_act; g and u equal bitlinear_forward's y for the two
- * matrices bit for bit; a(g) is evaluated in fp32 (SiLU within 7 * 2^-24 relative; GELU as
- * bitlinear_mlp_forward; squared ReLU one rounding) and the product is one fp32 rounding.  The
+ * matrices bit for bit; a(g) is evaluated in fp32 (SiLU within 7 * 2^-24 relative or 2^-120
+ * absolute; GELU as bitlinear_mlp_forward; squared ReLU one rounding) and the product is one
+ * fp32 rounding.  The
  * block's down projection is a bitlinear_quantize_act of h and any forward call.
  *
  *   x          [M, K] fp32.                                                  (in)
