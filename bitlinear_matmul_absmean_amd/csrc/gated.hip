@@ -320,6 +320,9 @@ static hipError_t launch_gated_dec_rb(const GatedArgs& a, hipStream_t s) {
 template <bool ALIGNED, int MT>
 static hipError_t launch_gated_dec_mt(const GatedArgs& a, hipStream_t s) {
     const int64_t wgs = (a.M + 16 * MT - 1) / (16 * MT) * ((a.F + 15) / 16);
+#ifdef VRB
+    return launch_gated_dec_rb<ALIGNED, MT, VRB>(a, s);
+#endif
     return wgs <= 256 ? launch_gated_dec_rb<ALIGNED, MT, 1>(a, s) : launch_gated_dec_rb<ALIGNED, MT, 2>(a, s);
 }
 
@@ -342,11 +345,11 @@ static hipError_t launch_gated_dec(const GatedArgs& a, hipStream_t s) {
 // u ^ ((r / 8) % 2), so that an operand read spreads over all banks.
 // In the two MFMAs of k 64 h .. 64 h + 63 (h = 0, 1) a lane group holds 32 codes, eight bytes of a
 // weight row: the lane's unit h, of which group lg uses dwords 2 lg and 2 lg + 1.
-constexpr int GG_BM = 128, GG_BF = 128, GG_BK = 128;
+constexpr int GG_BF = 128, GG_BK = 128;
 
-template <int ACT, bool ALIGNED>
+template <int ACT, bool ALIGNED, int FM>
 __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m, int tiles_f) {
-    constexpr int OB = GG_BM * 8, UNITS = OB + 2 * GG_BF * 2;
+    constexpr int GG_BM = 32 * FM, OB = GG_BM * 8, UNITS = OB + 2 * GG_BF * 2;
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
     __shared__ i32x4 st2[ALIGNED ? UNITS : 1];
@@ -369,9 +372,9 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
         scale[1][tid] = dequant_scale(a.au[0], beta);
     }
 
-    i32x16 acc[4][2];
+    i32x16 acc[FM][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
     const int lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7, sb = (lr >> 3) & 1;
@@ -386,38 +389,38 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
                 w[j] = reinterpret_cast<const uint2*>(st + OB + (128 * j + 32 * wave + lr) * 2 + (h ^ sb))[lg];
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                i32x4 fa[4], fb[2];
+                i32x4 fa[FM], fb[2];
                 const int u = 4 * h + 2 * lg + kk;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) fa[i] = st[(32 * i + lr) * 8 + (u ^ sw)];
+                for (int i = 0; i < FM; ++i) fa[i] = st[(32 * i + lr) * 8 + (u ^ sw)];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) fb[j] = expand_signed_in_order(kk ? w[j].y : w[j].x);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < FM; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
             }
         }
     };
-    // load block q of x: token rows 8 q .. 8 q + 7 (wave w takes 4 w .. 4 w + 3); of a matrix: rows
+    // load block q of x: token rows 8 q .. 8 q + 7 (wave w takes FM w .. FM w + FM - 1); of a matrix: rows
     // 32 q .. 32 q + 31 (wave w takes q = w of both)
     const int wrow = 32 * wave + (lane >> 1), wunit = (lane & 1) ^ ((wrow >> 3) & 1);
-    auto xrow = [&](int q) { return 8 * (4 * wave + q) + (lane >> 3); };
+    auto xrow = [&](int q) { return 8 * (FM * wave + q) + (lane >> 3); };
     auto xunit = [&](int q) { return (lane & 7) ^ ((xrow(q) >> 1) & 7); };
     if constexpr (ALIGNED) {
         const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
         const __amdgpu_buffer_rsrc_t rg = raw_buffer(g0, (uint32_t)rows_n * (uint32_t)rowb);
         const __amdgpu_buffer_rsrc_t ru = raw_buffer(u0, (uint32_t)rows_n * (uint32_t)rowb);
-        uint32_t xo[4];
+        uint32_t xo[FM];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) xo[q] = (uint32_t)min(xrow(q), rows_m - 1) * (uint32_t)K + 16u * xunit(q);
+        for (int q = 0; q < FM; ++q) xo[q] = (uint32_t)min(xrow(q), rows_m - 1) * (uint32_t)K + 16u * xunit(q);
         const uint32_t wo = (uint32_t)min(wrow, rows_n - 1) * (uint32_t)rowb + 16u * wunit;
         const int steps = (int)(K / GG_BK), last = steps - 1;
         auto fetch = [&](i32x4* st, int s) {
             s = s < last ? s : last;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) load_lds16(rx, xo[q], (uint32_t)s * GG_BK, st + 64 * (4 * wave + q));
+            for (int q = 0; q < FM; ++q) load_lds16(rx, xo[q], (uint32_t)s * GG_BK, st + 64 * (FM * wave + q));
             load_lds16(rg, wo, (uint32_t)s * (GG_BK / 4), st + OB + 64 * wave);
             load_lds16(ru, wo, (uint32_t)s * (GG_BK / 4), st + OB + 256 + 64 * wave);
             __builtin_amdgcn_sched_barrier(0);
@@ -426,7 +429,7 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
         // over; loads past the last step repeat it and are not read
         auto turn = [&]() {
             __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(0x0070 | 6);                 // vmcnt(6: the next stage's loads) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(0x0070 | (FM + 2));          // vmcnt(the next stage's loads) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -457,7 +460,7 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
             // the last 64 k through st0, which nobody reads any more
             const int64_t k = (int64_t)steps * GG_BK;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < FM / 2; ++j) {
                 const int r = (tid >> 2) + 64 * j, u = tid & 3;
                 st0[r * 8 + (u ^ ((r >> 1) & 7))] = *reinterpret_cast<const i32x4*>(x0 + (int64_t)min(r, rows_m - 1) * K + k + 16 * u);
             }
@@ -467,20 +470,20 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
             multiply(st0, 1);
         }
     } else {
-        u32x4 v[6];
+        u32x4 v[FM + 2];
         const int steps = (int)((K + GG_BK - 1) / GG_BK);
         auto load = [&](int s) {
             const int64_t k = (int64_t)s * GG_BK, w = (int64_t)min(wrow, rows_n - 1) * rowb;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = row_16(x0 + (int64_t)min(xrow(q), rows_m - 1) * K, k + 16 * xunit(q), K);
-            v[4] = row_16(g0 + w, (k >> 2) + 16 * wunit, rowb);
-            v[5] = row_16(u0 + w, (k >> 2) + 16 * wunit, rowb);
+            for (int q = 0; q < FM; ++q) v[q] = row_16(x0 + (int64_t)min(xrow(q), rows_m - 1) * K, k + 16 * xunit(q), K);
+            v[FM] = row_16(g0 + w, (k >> 2) + 16 * wunit, rowb);
+            v[FM + 1] = row_16(u0 + w, (k >> 2) + 16 * wunit, rowb);
         };
         auto put = [&](i32x4* st) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) st[64 * (4 * wave + q) + lane] = (i32x4)v[q];
-            st[OB + 64 * wave + lane] = (i32x4)v[4];
-            st[OB + 256 + 64 * wave + lane] = (i32x4)v[5];
+            for (int q = 0; q < FM; ++q) st[64 * (FM * wave + q) + lane] = (i32x4)v[q];
+            st[OB + 64 * wave + lane] = (i32x4)v[FM];
+            st[OB + 256 + 64 * wave + lane] = (i32x4)v[FM + 1];
         };
         load(0);
         put(st0);
@@ -496,7 +499,7 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
     if (n >= rows_n) return;
     const float bg = a.bg ? a.bg[n0 + n] : 0.0f, bu = a.bu ? a.bu[n0 + n] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int m = 32 * i + 8 * q + 4 * lg;
@@ -511,9 +514,17 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
                 if (a.bg) g[e] = g[e] + bg;
                 if (a.bu) u[e] = u[e] + bu;
             }
+            float v[4];
+            if constexpr (ACT == BITLINEAR_ACT_GELU) {
+                const float4 v4 = gelu4_f32(make_float4(g[0], g[1], g[2], g[3]));
+                v[0] = v4.x, v[1] = v4.y, v[2] = v4.z, v[3] = v4.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = act_value<ACT>(g[e]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (m + e < rows_m) a.h[at + e * a.F] = act_value<ACT>(g[e]) * u[e];
+                if (m + e < rows_m) a.h[at + e * a.F] = v[e] * u[e];
             if (a.g) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -525,22 +536,37 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
         }
 }
 
-template <bool ALIGNED>
-static hipError_t launch_gated_gemm(const GatedArgs& a, hipStream_t s) {
-    const int64_t tm = (a.M + GG_BM - 1) / GG_BM, tf = (a.F + GG_BF - 1) / GG_BF;
-    const dim3 grid((unsigned)(tm * tf));
-    if (a.act == BITLINEAR_ACT_SILU)
-        hipLaunchKernelGGL((k_gated_gemm<BITLINEAR_ACT_SILU, ALIGNED>), grid, dim3(256), 0, s, a, (int)tm, (int)tf);
-    else if (a.act == BITLINEAR_ACT_GELU)
-        hipLaunchKernelGGL((k_gated_gemm<BITLINEAR_ACT_GELU, ALIGNED>), grid, dim3(256), 0, s, a, (int)tm, (int)tf);
-    else
-        hipLaunchKernelGGL((k_gated_gemm<BITLINEAR_ACT_RELU2, ALIGNED>), grid, dim3(256), 0, s, a, (int)tm, (int)tf);
+template <int ACT, bool ALIGNED, int FM>
+static hipError_t launch_gated_gemm_fm(const GatedArgs& a, hipStream_t s) {
+    const int64_t tm = (a.M + 32 * FM - 1) / (32 * FM), tf = (a.F + GG_BF - 1) / GG_BF;
+    hipLaunchKernelGGL((k_gated_gemm<ACT, ALIGNED, FM>), dim3((unsigned)(tm * tf)), dim3(256), 0, s, a, (int)tm, (int)tf);
     return hipGetLastError();
 }
 
+// 64-token tiles while 128-token ones would not fill the 512 workgroup slots well: K = 4096, F = 11008,
+// M = 128 (86 tiles of 128): 27.4 against 39.4 us; M = 512 (344): 58.6 against 61.3; M = 1024 (688):
+// 106.6 against 97.8; K = 8192, F = 28672, M = 256 (448): 131 against 113 us.
+template <bool ALIGNED>
+static hipError_t launch_gated_gemm(const GatedArgs& a, hipStream_t s) {
+    const bool small = (a.M + 127) / 128 * ((a.F + GG_BF - 1) / GG_BF) <= 384;
+    switch (a.act) {
+        case BITLINEAR_ACT_SILU:
+            return small ? launch_gated_gemm_fm<BITLINEAR_ACT_SILU, ALIGNED, 2>(a, s) : launch_gated_gemm_fm<BITLINEAR_ACT_SILU, ALIGNED, 4>(a, s);
+        case BITLINEAR_ACT_GELU:
+            return small ? launch_gated_gemm_fm<BITLINEAR_ACT_GELU, ALIGNED, 2>(a, s) : launch_gated_gemm_fm<BITLINEAR_ACT_GELU, ALIGNED, 4>(a, s);
+        default:
+            return small ? launch_gated_gemm_fm<BITLINEAR_ACT_RELU2, ALIGNED, 2>(a, s) : launch_gated_gemm_fm<BITLINEAR_ACT_RELU2, ALIGNED, 4>(a, s);
+    }
+}
+
+// The streaming kernel up to 32 tokens, and beyond while the GEMM has at most 64 tiles of 64 x 128, too
+// few to fill the chip: K = 4096, F = 11008: M = 32 18.5 against 25.0 us, M = 64 (86 tiles) 26.3 against
+// 26.0, M = 128 38.2 against 27.4; K = 11008, F = 4096: M = 128 (64 tiles) 27.9 against 56.6, M = 512 (256)
+// 86.9 against 61.4; K = 1024, F = 2816: M = 128 (44) 10.0 against 12.0, M = 256 (88) 16.4 against 12.3 us.
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
     const bool aligned = a.K % 64 == 0 && (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.wg % 16 == 0 && (uintptr_t)a.wu % 16 == 0;
-    if (a.M <= 64) return aligned ? launch_gated_dec<true>(a, s) : launch_gated_dec<false>(a, s);
+    if (a.M <= 32 || (a.M + 63) / 64 * ((a.F + GG_BF - 1) / GG_BF) <= 64)
+        return aligned ? launch_gated_dec<true>(a, s) : launch_gated_dec<false>(a, s);
     return aligned ? launch_gated_gemm<true>(a, s) : launch_gated_gemm<false>(a, s);
 }
 

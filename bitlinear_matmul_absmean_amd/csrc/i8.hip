@@ -257,17 +257,17 @@ static hipError_t launch_i8_dec(const I8Args& a, hipStream_t s) {
 }
 
 // ---- many tokens ----------------------------------------------------------------------------
-// A workgroup of eight waves computes 128 tokens x 256 channels, a wave 64 x 64 of them in 32 x 32
+// A workgroup of eight waves computes 64 MI tokens x 256 channels, a wave 32 MI x 64 of them in 32 x 32
 // blocks, in steps of 128 k (rows of whole cache lines); three LDS stages (48 KiB each), filled two
 // steps ahead by loads that go past the registers (aligned rows), or two filled through registers.
 // Unit u (16 bytes) of row r lies at slot u ^ ((r / 2) % 8) of its eight.
 // 32x32x32 lane layout: A/B lane l holds row/column l % 32, k = 16 (l / 32) + j; accumulator r of
 // lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
-constexpr int IG_BM = 128, IG_BN = 256, IG_BK = 128;
+constexpr int IG_BN = 256, IG_BK = 128;
 
-template <bool ALIGNED>
+template <bool ALIGNED, int MI>
 __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int tiles_n) {
-    constexpr int OB = IG_BM * 8, UNITS = OB + IG_BN * 8;
+    constexpr int IG_BM = 64 * MI, OB = IG_BM * 8, UNITS = OB + IG_BN * 8;
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
     __shared__ i32x4 st2[ALIGNED ? UNITS : 1];
@@ -285,9 +285,9 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
     const int8_t* x0 = a.xq + m0 * K;
     const int8_t* w0 = a.wq + n0 * K;
 
-    i32x16 acc[2][2];
+    i32x16 acc[MI][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
     const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
         bias[j] = a.bias ? a.bias[n] : 0.0f;
     }
     struct Frag {
-        i32x4 a[2], b[2];
+        i32x4 a[MI], b[2];
     };
     // operands of k 32 kk .. 32 kk + 31 of the step in stage st
     auto read = [&](const i32x4* st, int kk) {
@@ -310,27 +310,27 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
 #pragma unroll
         for (int j = 0; j < 2; ++j) f.b[j] = st[OB + (64 * wj + 32 * j + lr) * 8 + at];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) f.a[i] = st[(64 * wi + 32 * i + lr) * 8 + at];
+        for (int i = 0; i < MI; ++i) f.a[i] = st[(32 * MI * wi + 32 * i + lr) * 8 + at];
         return f;
     };
     auto multiply = [&](const Frag& f) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // load block q (8 rows): wave w takes 2 w, 2 w + 1 of x_q and 4 w .. 4 w + 3 of W_q
+    // load block q (8 rows): wave w takes MI w .. MI w + MI - 1 of x_q and 4 w .. 4 w + 3 of W_q
     auto block_row = [&](int q) { return 8 * q + (lane >> 3); };
     auto block_unit = [&](int q) { return (lane & 7) ^ ((block_row(q) >> 1) & 7); };
     if constexpr (ALIGNED) {
         const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
         const __amdgpu_buffer_rsrc_t rw = raw_buffer(w0, (uint32_t)rows_n * (uint32_t)K);
-        uint32_t xo[2], wo[4];
+        uint32_t xo[MI], wo[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-            xo[q] = (uint32_t)min(block_row(2 * wave + q), rows_m - 1) * (uint32_t)K + 16u * block_unit(2 * wave + q);
+        for (int q = 0; q < MI; ++q)
+            xo[q] = (uint32_t)min(block_row(MI * wave + q), rows_m - 1) * (uint32_t)K + 16u * block_unit(MI * wave + q);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             wo[q] = (uint32_t)min(block_row(4 * wave + q), rows_n - 1) * (uint32_t)K + 16u * block_unit(4 * wave + q);
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
             const uint32_t so = (uint32_t)s * IG_BK;
             if (third == 0) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) load_lds16(rx, xo[q], so, st + 64 * (2 * wave + q));
+                for (int q = 0; q < MI; ++q) load_lds16(rx, xo[q], so, st + 64 * (MI * wave + q));
             } else {
 #pragma unroll
                 for (int q = 2 * third - 2; q < 2 * third; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (4 * wave + q));
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
             f1 = read(cur, 3);
             multiply(f0);
             // step s + 1 has landed for every wave, and every wave holds the rest of step s in registers
-            __builtin_amdgcn_s_waitcnt(0x0070 | 6);        // vmcnt(6: the loads of step s + 2) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(0x0070 | (MI + 4)); // vmcnt(the loads of step s + 2) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             f0 = read(nxt, 0);
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
 #pragma unroll
             for (int q = 0; q < 3; ++q) fetch(st1, min(1, last), q);
             fetch(st2, min(2, last), 0);
-            __builtin_amdgcn_s_waitcnt(0x0070 | 8);        // vmcnt(8: the loads after step 0's) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(0x0070 | (2 * MI + 4)); // vmcnt(the loads after step 0's) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             Frag f = read(st0, 0);
             int s = 0;
@@ -392,30 +392,30 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
         for (int64_t k = (int64_t)steps * IG_BK; k < K; k += 32) {
             Frag f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) f.a[i] = row_16(x0 + (int64_t)min(64 * wi + 32 * i + lr, rows_m - 1) * K, k + 16 * lg, K);
+            for (int i = 0; i < MI; ++i) f.a[i] = row_16(x0 + (int64_t)min(32 * MI * wi + 32 * i + lr, rows_m - 1) * K, k + 16 * lg, K);
 #pragma unroll
             for (int j = 0; j < 2; ++j) f.b[j] = row_16(w0 + (int64_t)min(64 * wj + 32 * j + lr, rows_n - 1) * K, k + 16 * lg, K);
             multiply(f);
         }
     } else {
-        const int8_t *xp[2], *wp[4];
+        const int8_t *xp[MI], *wp[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) xp[q] = x0 + (int64_t)min(block_row(2 * wave + q), rows_m - 1) * K;
+        for (int q = 0; q < MI; ++q) xp[q] = x0 + (int64_t)min(block_row(MI * wave + q), rows_m - 1) * K;
 #pragma unroll
         for (int q = 0; q < 4; ++q) wp[q] = w0 + (int64_t)min(block_row(4 * wave + q), rows_n - 1) * K;
-        i32x4 v[6];
+        i32x4 v[MI + 4];
         auto load = [&](int s) {
             const int64_t k = (int64_t)s * IG_BK;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) v[q] = row_16(xp[q], k + 16 * block_unit(2 * wave + q), K);
+            for (int q = 0; q < MI; ++q) v[q] = row_16(xp[q], k + 16 * block_unit(MI * wave + q), K);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[2 + q] = row_16(wp[q], k + 16 * block_unit(4 * wave + q), K);
+            for (int q = 0; q < 4; ++q) v[MI + q] = row_16(wp[q], k + 16 * block_unit(4 * wave + q), K);
         };
         auto put = [&](i32x4* st) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) st[64 * (2 * wave + q) + lane] = v[q];
+            for (int q = 0; q < MI; ++q) st[64 * (MI * wave + q) + lane] = v[q];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) st[OB + 64 * (4 * wave + q) + lane] = v[2 + q];
+            for (int q = 0; q < 4; ++q) st[OB + 64 * (4 * wave + q) + lane] = v[MI + q];
         };
         const int steps = (int)((K + IG_BK - 1) / IG_BK);
         load(0);
@@ -431,10 +431,10 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
     }
     // tokens 4 q .. 4 q + 3 of a block are four registers of a lane: their scales are one LDS read
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int m = 64 * wi + 32 * i + 8 * q + 4 * lg;
+            const int m = 32 * MI * wi + 32 * i + 8 * q + 4 * lg;
             const float4 bs4 = *reinterpret_cast<const float4*>(&bscale[m]);
             const float bs[4] = {bs4.x, bs4.y, bs4.z, bs4.w};
             const int64_t at = (m0 + m) * a.N + n0 + 64 * wj + lr;
@@ -449,17 +449,29 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
         }
 }
 
-template <bool ALIGNED>
-static hipError_t launch_i8_gemm(const I8Args& a, hipStream_t s) {
-    const int64_t tm = (a.M + IG_BM - 1) / IG_BM, tn = (a.N + IG_BN - 1) / IG_BN;
-    hipLaunchKernelGGL((k_i8_gemm<ALIGNED>), dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, (int)tm, (int)tn);
+template <bool ALIGNED, int MI>
+static hipError_t launch_i8_gemm_mi(const I8Args& a, hipStream_t s) {
+    const int64_t tm = (a.M + 64 * MI - 1) / (64 * MI), tn = (a.N + IG_BN - 1) / IG_BN;
+    hipLaunchKernelGGL((k_i8_gemm<ALIGNED, MI>), dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
+// 64-token tiles while they all run at once (256 slots): K = N = 4096, M = 128 (32 tiles of 64 x 256) 16.4
+// against 23.1 us, M = 1024 (256) 23.7 against 25.8; K = 4096, N = 11008, M = 512 (344) 51.7 against 33.6.
+template <bool ALIGNED>
+static hipError_t launch_i8_gemm(const I8Args& a, hipStream_t s) {
+    const int64_t tiles = (a.M + 63) / 64 * ((a.N + IG_BN - 1) / IG_BN);
+    return tiles <= 256 ? launch_i8_gemm_mi<ALIGNED, 1>(a, s) : launch_i8_gemm_mi<ALIGNED, 2>(a, s);
+}
+
+// The streaming kernel while the GEMM has at most 48 tiles of 64 x 256, too few to read the weights at
+// speed: K = N = 4096, M = 64 (16 tiles) 8.5 against 16.6 us, M = 128 (32) 11.7 against 16.4, M = 256 (64)
+// 20.2 against 16.7; K = 4096, N = 11008, M = 64 (43) 21.6 against 24.2; K = 4096, N = 32000, M = 16 (125)
+// 28.9 against 25.3 us.
 template <bool ALIGNED>
 static hipError_t launch_i8(const I8Args& a, hipStream_t s) {
     if (a.M == 1) return launch_i8_gemv<ALIGNED>(a, s);
-    if (a.M <= 64) return launch_i8_dec<ALIGNED>(a, s);
+    if ((a.M + 63) / 64 * ((a.N + IG_BN - 1) / IG_BN) <= 48) return launch_i8_dec<ALIGNED>(a, s);
     return launch_i8_gemm<ALIGNED>(a, s);
 }
 
