@@ -247,7 +247,8 @@ __global__ __launch_bounds__(64 * GD_WAVES) void k_gated_dec(GatedArgs a, int sl
         const __amdgpu_buffer_rsrc_t rg = raw_buffer(g0, (uint32_t)rows_n * (uint32_t)rowb);
         const __amdgpu_buffer_rsrc_t ru = raw_buffer(u0, (uint32_t)rows_n * (uint32_t)rowb);
         // load i of x: tokens 4 i .. 4 i + 3, sixteen lanes each; load r of a matrix: lane (lr, lg) reads
-        // 64 codes of row 16 r + lr.  Rows past the end repeat the last one.
+        // 64 codes of row 16 r + lr.  Rows past the end repeat the last one; groups of four tokens past it
+        // are not loaded (what they hold reaches only outputs that are not written).
         uint32_t xo[4 * MT], wo[RB];
 #pragma unroll
         for (int i = 0; i < 4 * MT; ++i)
@@ -261,7 +262,8 @@ __global__ __launch_bounds__(64 * GD_WAVES) void k_gated_dec(GatedArgs a, int sl
                 load_lds16(ru, wo[r], (uint32_t)s * 64u, img + 64 * (4 * MT + RB + r));
             }
 #pragma unroll
-            for (int i = 0; i < 4 * MT; ++i) load_lds16(rx, xo[i], (uint32_t)s * 256u, img + 64 * i);
+            for (int i = 0; i < 4 * MT; ++i)
+                if (4 * i < rows_m) load_lds16(rx, xo[i], (uint32_t)s * 256u, img + 64 * i);
         };
         if (wave < whole) fetch(wave);
         for (int s = wave; s < whole; s += GD_WAVES) {
@@ -317,13 +319,15 @@ static hipError_t launch_gated_dec_rb(const GatedArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// One block of 16 columns a workgroup; two where 48 or 64 tokens leave room for one workgroup per compute
+// unit only and there would be more than 256 (K = 11008, F = 4096: M = 64 (256 workgroups) 20.3 against
+// 25.8 us with two blocks, M = 128 (512) 34.7 against 27.7; K = 4096, F = 11008, M = 16 (688) 12.2 against
+// 13.2; M = 32 15.0 against 18.6 us).
 template <bool ALIGNED, int MT>
 static hipError_t launch_gated_dec_mt(const GatedArgs& a, hipStream_t s) {
-    const int64_t wgs = (a.M + 16 * MT - 1) / (16 * MT) * ((a.F + 15) / 16);
-#ifdef VRB
-    return launch_gated_dec_rb<ALIGNED, MT, VRB>(a, s);
-#endif
-    return wgs <= 256 ? launch_gated_dec_rb<ALIGNED, MT, 1>(a, s) : launch_gated_dec_rb<ALIGNED, MT, 2>(a, s);
+    if constexpr (MT >= 3)
+        if ((a.M + 16 * MT - 1) / (16 * MT) * ((a.F + 15) / 16) > 256) return launch_gated_dec_rb<ALIGNED, MT, 2>(a, s);
+    return launch_gated_dec_rb<ALIGNED, MT, 1>(a, s);
 }
 
 template <bool ALIGNED>

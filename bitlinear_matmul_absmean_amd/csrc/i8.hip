@@ -104,8 +104,8 @@ __device__ __forceinline__ int unit_swizzle(int r) { return ((r >> 2) & 3) ^ (((
 // ---- few tokens -----------------------------------------------------------------------------
 // A workgroup of eight waves computes 16 MT tokens x 16 RB channels; wave w takes the steps of 64 k
 // w, w + 8, ..., and the eight partial tiles are added at the end (integers: exact in any order).
-// Aligned rows: each wave has a ring of three LDS images of a step (16-row blocks of 64 bytes a
-// row), filled by loads that go past the registers, two steps ahead; no wave waits for another.
+// Aligned rows: each wave has a ring of D LDS images of a step (16-row blocks of 64 bytes a row), filled
+// by loads that go past the registers, D - 1 steps ahead; no wave waits for another.
 // Any K and alignment: operands straight into registers in the MFMA's layout.
 // 16x16x64 lane layout: A/B lane l holds row/column l % 16, k = 16 (l / 16) + j; accumulator r of
 // lane l is row 4 (l / 16) + r, column l % 16.
@@ -114,6 +114,7 @@ constexpr int I8_WAVES = 8;
 template <bool ALIGNED, int MT, int RB>
 __global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) {
     constexpr int IMG = (RB + MT) * 64;
+    constexpr int D = 3;                                           // images of a ring
     __shared__ i32x4 st0[I8_WAVES * IMG];
     __shared__ i32x4 st1[ALIGNED ? I8_WAVES * IMG : 1];
     __shared__ i32x4 st2[ALIGNED ? I8_WAVES * IMG : 1];
@@ -157,43 +158,45 @@ __global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) 
             __builtin_amdgcn_sched_barrier(0);
         };
         const int at = lr * 4 + (lg ^ unit_swizzle(lr));
-        // step s from its image, `behind` later steps' loads being in flight
-        auto step = [&](const i32x4* st, int s, int behind) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (behind == 2) __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * (RB + MT));       // vmcnt(two steps' loads)
-            else if (behind == 1) __builtin_amdgcn_s_waitcnt(0x0F70 | (RB + MT));
-            else __builtin_amdgcn_s_waitcnt(0x0F70);                                   // vmcnt(0)
-            __builtin_amdgcn_sched_barrier(0);
+        // step s from its image
+        auto step = [&](const i32x4* st, int s) {
             const i32x4* img = st + wave * IMG + at;
             i32x4 x[MT], w[RB];
 #pragma unroll
             for (int r = 0; r < RB; ++r) w[r] = img[64 * r];
 #pragma unroll
             for (int t = 0; t < MT; ++t) x[t] = img[64 * (RB + t)];
-            if ((int64_t)s * 64 + 64 > K) {
-                const bool live = (int64_t)s * 64 + 16 * lg < K;
+            // past the end of its row (K % 64 != 0) a load has read what follows it
+            const bool live = (int64_t)s * 64 + 16 * lg < K;
 #pragma unroll
-                for (int t = 0; t < MT; ++t) x[t] = live ? x[t] : i32x4{0, 0, 0, 0};
-            }
+            for (int t = 0; t < MT; ++t) x[t] = live ? x[t] : i32x4{0, 0, 0, 0};
             multiply(x, w);
             __builtin_amdgcn_sched_barrier(0);
         };
-        // an image is filled again only after the multiplications that read it
-        constexpr int W = I8_WAVES;
-        int s = wave;
-        if (s < steps) fetch(st0, s);
-        if (s + W < steps) fetch(st1, s + W);
-        for (; s + 2 * W < steps; s += 3 * W) {
-            fetch(st2, s + 2 * W);
-            step(st0, s, 2);
-            const bool more3 = s + 3 * W < steps, more4 = s + 4 * W < steps;
-            if (more3) fetch(st0, s + 3 * W);
-            step(st1, s + W, more3 ? 2 : 1);
-            if (more4) fetch(st1, s + 4 * W);
-            step(st2, s + 2 * W, more4 ? 2 : more3 ? 1 : 0);
+        // The loop has no branches, so that the loads in flight can be counted: loads past the wave's last
+        // step repeat it and are not read.  An image is filled again only after the MFMAs that read it.
+        constexpr int W = I8_WAVES, FLY = (D - 1) * (RB + MT);
+        static_assert(FLY < 16, "the count fits the low four bits of vmcnt");
+        i32x4* const ring[D] = {st0, st1, st2};
+        int left = wave < steps ? (steps - wave + W - 1) / W : 0, s = wave;
+        const int last = wave + (left - 1) * W;
+        if (left > 0) {
+#pragma unroll
+            for (int j = 0; j < D - 1; ++j) fetch(ring[j], min(s + j * W, last));
         }
-        if (s < steps) step(st0, s, s + W < steps ? 1 : 0);
-        if (s + W < steps) step(st1, s + W, 0);
+        for (; left >= D; left -= D, s += D * W) {
+#pragma unroll
+            for (int j = 0; j < D; ++j) {
+                fetch(ring[(j + D - 1) % D], min(s + (j + D - 1) * W, last));
+                __builtin_amdgcn_s_waitcnt(0x0F70 | FLY);                        // vmcnt(the loads of the D - 1 later steps)
+                __builtin_amdgcn_sched_barrier(0);
+                step(ring[j], s + j * W);
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);                                            // vmcnt(0)
+#pragma unroll
+        for (int j = 0; j < D - 1; ++j)
+            if (j < left) step(ring[j], s + j * W);
     } else {
         const int8_t *xp[MT], *wp[RB];
 #pragma unroll
@@ -240,11 +243,14 @@ static hipError_t launch_i8_dec_rb(const I8Args& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// One block of 16 channels a workgroup while that leaves at most 256 workgroups, else two.
+// One block of 16 channels a workgroup; two where 48 or 64 tokens leave room for one workgroup per compute
+// unit only and there would be more than 256 (K = N = 4096, M = 48 (256 workgroups) 7.4 against 9.4 us with
+// two blocks; K = N = 8192, M = 48 (512) 26.7 against 20.9; M = 16 15.5 against 17.9 us).
 template <bool ALIGNED, int MT>
 static hipError_t launch_i8_dec_mt(const I8Args& a, hipStream_t s) {
-    const int64_t wgs = (a.M + 16 * MT - 1) / (16 * MT) * ((a.N + 15) / 16);
-    return wgs <= 256 ? launch_i8_dec_rb<ALIGNED, MT, 1>(a, s) : launch_i8_dec_rb<ALIGNED, MT, 2>(a, s);
+    if constexpr (MT >= 3)
+        if ((a.M + 16 * MT - 1) / (16 * MT) * ((a.N + 15) / 16) > 256) return launch_i8_dec_rb<ALIGNED, MT, 2>(a, s);
+    return launch_i8_dec_rb<ALIGNED, MT, 1>(a, s);
 }
 
 template <bool ALIGNED>
