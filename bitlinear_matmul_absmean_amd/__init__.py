@@ -425,30 +425,43 @@ def bitlinear_forward_fused_rows(x, W_packed, alpha_rows, bias=None, y=None, x_q
     return _forward_fused("bitlinear_forward_fused_rows", x, W_packed, alpha_rows, bias, y, x_q, beta, acc, stream)
 
 
-def _shaped(t, dtype, name, shape, device):
+def _shaped(t, dtype, name, shape, index):
     """Device pointer of t (None for None) after checking that it is a contiguous tensor of exactly
-    this dtype and shape on this device.  Of integer codes and packed bytes as of floats."""
+    this dtype and shape on device `index`.  One test when all is well: a call marshals a dozen
+    tensors, and single-token kernels take less time than their checks would."""
     if t is None:
         return None
-    ptr = _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return ptr
+    raise ValueError(f"{name} must be on device {index}, got {t.device}")
 
 
 def _rows(t, name):
-    """Shape [rows, columns] and device of a matrix argument, which has to lie on the current device
-    (the library launches there)."""
+    """Shape (rows, columns) and device index of a matrix argument, which has to lie on the current
+    device (the library launches there)."""
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
-    if t.device.index != torch.cuda.current_device():
+    index = t.get_device()
+    if index != torch.cuda.current_device():
         raise ValueError(f"{name} must be on the current device")
-    return t.shape[0], t.shape[1], t.device
+    rows, cols = t.shape
+    return rows, cols, index
+
+
+def _first(t, name):
+    """Rows of a matrix argument."""
+    if getattr(t, "ndim", 0) != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape[0]
 
 
 def bitlinear_gated_forward(x, Wg_packed, alpha_g, Wu_packed, alpha_u, act, bias_g=None, bias_u=None, h=None, g=None,
@@ -459,7 +472,7 @@ def bitlinear_gated_forward(x, Wg_packed, alpha_g, Wu_packed, alpha_u, act, bias
     Returns h."""
     torch = _torch()
     M, K, dev = _rows(x, "x")
-    F = Wg_packed.shape[0]
+    F = _first(Wg_packed, "Wg_packed")
     if h is None:
         h = torch.empty((M, F), dtype=torch.float32, device=dev)
     if x_q is None:
@@ -487,13 +500,15 @@ def bitlinear_gated_backward_workspace_size(M, K, F) -> int:
     return lib.bitlinear_gated_backward_workspace_size(M, K, F)
 
 
-def _workspace(workspace, need, dev):
-    torch = _torch()
+def _workspace(workspace, need, index):
+    """Pointer and bytes of the given workspace, or of a new one of the bytes needed."""
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    if workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
-    return _dev(workspace, torch.uint8, "workspace"), workspace.numel()
+        torch = _torch()
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=index)
+    ptr = _dev(workspace, _torch().uint8, "workspace")
+    if workspace.get_device() != index:
+        raise ValueError(f"workspace must be on device {index}, got {workspace.device}")
+    return workspace, ptr, workspace.numel()
 
 
 def bitlinear_backward(dy, x_q, beta, W_packed, alpha, dx=None, dW=None, dbias=None, workspace=None, stream=None):
@@ -507,7 +522,7 @@ def bitlinear_backward(dy, x_q, beta, W_packed, alpha, dx=None, dW=None, dbias=N
     if dx is None and dW is None and dbias is None:
         dx = torch.empty((M, K), dtype=f32, device=dev)
         dW = torch.empty((N, K), dtype=f32, device=dev)
-    ws, ws_bytes = _workspace(workspace, lib.bitlinear_backward_workspace_size(M, K, N), dev)
+    workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_backward_workspace_size(M, K, N), dev)
     _check("bitlinear_backward", lib.bitlinear_backward(
         _shaped(dy, f32, "dy", (M, N), dev), M, N, _shaped(x_q, torch.int8, "x_q", (M, K), dev),
         _shaped(beta, f32, "beta", (M,), dev), K, _shaped(W_packed, torch.uint8, "W_packed", (N, K // 4), dev),
@@ -530,7 +545,7 @@ def bitlinear_gated_backward(dh, g, u, x_q, beta, Wg_packed, alpha_g, Wu_packed,
         dx = torch.empty((M, K), dtype=f32, device=dev)
         dWg = torch.empty((F, K), dtype=f32, device=dev)
         dWu = torch.empty((F, K), dtype=f32, device=dev)
-    ws, ws_bytes = _workspace(workspace, lib.bitlinear_gated_backward_workspace_size(M, K, F), dev)
+    workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_gated_backward_workspace_size(M, K, F), dev)
     _check("bitlinear_gated_backward", lib.bitlinear_gated_backward(
         _shaped(dh, f32, "dh", (M, F), dev), _shaped(g, f32, "g", (M, F), dev), _shaped(u, f32, "u", (M, F), dev), M, F,
         _shaped(x_q, torch.int8, "x_q", (M, K), dev), _shaped(beta, f32, "beta", (M,), dev), K,
@@ -561,7 +576,7 @@ def bitlinear_forward_i8(x_q, beta, W_q, gamma, bias=None, y=None, acc=None, str
     [M, N] tensor) also returns the exact integer sums: (y, acc)."""
     torch = _torch()
     M, K, dev = _rows(x_q, "x_q")
-    N = W_q.shape[0]
+    N = _first(W_q, "W_q")
     f32 = torch.float32
     if y is None:
         y = torch.empty((M, N), dtype=f32, device=dev)

@@ -24,7 +24,7 @@
 // Steps, each one launch over the whole problem:
 //   1. k_grad_prep: the largest |d alpha| of every token and |d beta / 127| of every channel, and the
 //      bias sums, tile by tile; the panels of the integer operands;
-//   2. k_grad_reduce: the tiles' maxima and sums put together;
+//   2. k_grad_reduce (more than 64 tokens): the tiles' maxima and sums put together;
 //   3. k_grad_split: d once more, scaled and split, rows being tokens (dx) and channels (dW);
 //   4. k_split_gemm: both products;
 //   5. k_split_sum, where a sum was cut into parts.
@@ -92,7 +92,7 @@ __device__ __forceinline__ int64_t code_unit(int64_t col, int64_t l, int64_t L) 
 
 struct GradPlan {
     int64_t Np, Mp, Lx;            // N and M rounded up to 64, P Np
-    int tm;                        // tokens of a maximum tile
+    int tm, tn;                    // tokens and columns of a maximum tile
     int64_t mt, ct;                // maximum tiles along the tokens, along the columns
     float *rpart, *cpart;          // largest |d alpha| [M, ct], |d beta / 127| [mt, P N] of a tile
     double* bpart;                 // sums of d [mt, P N] of a tile
@@ -130,8 +130,10 @@ static GradPlan grad_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws)
     p.Np = (N + 63) / 64 * 64;
     p.Mp = (M + 63) / 64 * 64;
     p.Lx = P * p.Np;
-    p.ct = (N + 255) / 256;
-    p.tm = (M + 63) / 64 * p.ct >= 512 ? 64 : 16;
+    // up to 64 tokens one tile holds all of a column's, and nothing is left to put together but rows
+    p.tn = M <= 64 ? 64 : 256;
+    p.ct = (N + p.tn - 1) / p.tn;
+    p.tm = M <= 64 || (M + 63) / 64 * p.ct >= 512 ? 64 : 16;
     p.mt = (M + p.tm - 1) / p.tm;
     p.parts_x = sum_parts(M, K, p.Lx);
     p.parts_w = sum_parts(P * N, K, p.Mp);
@@ -161,59 +163,73 @@ static GradPlan grad_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws)
 size_t backward_workspace(int64_t M, int64_t K, int64_t N, bool gated) { return grad_plan(M, K, N, gated, nullptr).bytes; }
 
 // ---- step 1 -------------------------------------------------------------------------------
-// Maxima and sums.  A workgroup takes p.tm tokens x 256 columns, a wave a quarter of the tokens, a
-// lane four columns 64 apart (whole lines whatever the alignment).
-template <int ACT>
+// Maxima and sums.  A workgroup takes p.tm tokens x 64 C columns, a wave a quarter of the tokens, a
+// lane C columns 64 apart (whole lines whatever the alignment).
+template <int ACT, int C>
 __device__ __forceinline__ void max_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, uint8_t* lds) {
     constexpr int P = ACT == 0 ? 1 : 2;
     double (*cs)[P][256] = reinterpret_cast<double (*)[P][256]>(lds);
     float (*cm)[P][256] = reinterpret_cast<float (*)[P][256]>(lds + 4 * P * 256 * 8);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t tn = b % p.ct, tmi = b / p.ct, n0 = tn * 256, m0 = tmi * p.tm;
+    const int64_t tn = b % p.ct, tmi = b / p.ct, n0 = tn * 64 * C, m0 = tmi * p.tm;
     const float al[2] = {a.al0[0], ACT == 0 ? 0.0f : a.al1[0]};
     const bool bias = a.db0 || a.db1;
-    float cmx[P][4];
-    double sum[P][4];
+    float cmx[P][C];
+    double sum[P][C];
 #pragma unroll
     for (int q = 0; q < P; ++q)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < C; ++c) {
             cmx[q][c] = 0.0f;
             sum[q][c] = 0.0;
         }
+    // TT tokens at a time, their loads under way together: rows and columns past the end read the last
+    // ones and count for nothing
+    constexpr int TT = C == 1 ? 16 : 4;
     const int per = p.tm / 4;
-    for (int t = 0; t < per; ++t) {
-        const int64_t m = m0 + per * wave + t;
-        if (m >= a.M) break;
-        const float bs = a.beta[m] / 127.0f;
-        float rm = 0.0f;
+    for (int t0 = 0; t0 < per; t0 += TT) {
+        const int64_t mb = m0 + per * wave + t0;
+        if (mb >= a.M) break;
+        float d[TT][C][2], bs[TT], rm[TT];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int64_t n = n0 + 64 * c + lane;
-            if (n < a.N) {
-                float d[2];
-                grad_at<ACT>(a, m * a.N + n, d);
+        for (int t = 0; t < TT; ++t) {
+            const int64_t m = mb + t < a.M ? mb + t : a.M - 1;
+            bs[t] = a.beta[m] / 127.0f;
+            rm[t] = 0.0f;
 #pragma unroll
-                for (int q = 0; q < P; ++q) {
-                    rm = fmaxf(rm, fabsf(d[q] * al[q]));
-                    cmx[q][c] = fmaxf(cmx[q][c], fabsf(d[q] * bs));
-                    if (bias) sum[q][c] += (double)d[q];
-                }
+            for (int c = 0; c < C; ++c) {
+                const int64_t n = n0 + 64 * c + lane;
+                grad_at<ACT>(a, m * a.N + (n < a.N ? n : a.N - 1), d[t][c]);
             }
         }
-        rm = wave_max_f32(rm);
-        if (lane == 0) p.rpart[m * p.ct + tn] = rm;
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (mb + t < a.M && n0 + 64 * c + lane < a.N) {
+#pragma unroll
+                    for (int q = 0; q < P; ++q) {
+                        rm[t] = fmaxf(rm[t], fabsf(d[t][c][q] * al[q]));
+                        cmx[q][c] = fmaxf(cmx[q][c], fabsf(d[t][c][q] * bs[t]));
+                        if (bias) sum[q][c] += (double)d[t][c][q];
+                    }
+                }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const float v = wave_max_f32(rm[t]);
+            if (lane == 0 && mb + t < a.M) p.rpart[(mb + t) * p.ct + tn] = v;
+        }
     }
 #pragma unroll
     for (int q = 0; q < P; ++q)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < C; ++c) {
             cm[wave][q][64 * c + lane] = cmx[q][c];
             if (bias) cs[wave][q][64 * c + lane] = sum[q][c];
         }
     __syncthreads();
     const int64_t n = n0 + threadIdx.x;
-    if (n >= a.N) return;
+    if (threadIdx.x >= 64 * C || n >= a.N) return;
 #pragma unroll
     for (int q = 0; q < P; ++q) {
         float v = 0.0f;
@@ -223,8 +239,14 @@ __device__ __forceinline__ void max_tile(const BackwardArgs& a, const GradPlan& 
             v = fmaxf(v, cm[w][q][threadIdx.x]);
             if (bias) s += cs[w][q][threadIdx.x];
         }
-        p.cpart[(tmi * P + q) * a.N + n] = v;
-        if (bias) p.bpart[(tmi * P + q) * a.N + n] = s;
+        if (p.mt == 1) {
+            p.cmax[q * a.N + n] = v;
+            float* out = q ? a.db1 : a.db0;
+            if (out) out[n] = (float)s;
+        } else {
+            p.cpart[(tmi * P + q) * a.N + n] = v;
+            if (bias) p.bpart[(tmi * P + q) * a.N + n] = s;
+        }
     }
 }
 
@@ -283,18 +305,18 @@ __device__ __forceinline__ void codes_tile(const BackwardArgs& a, const GradPlan
     reinterpret_cast<u32x4*>(p.cd)[code_unit(k0 + c, m0 + 16 * u, p.Mp)] = v ^ 0x80808080u;
 }
 
-template <int ACT>
+template <int ACT, int C>
 __global__ __launch_bounds__(256) void k_grad_prep(BackwardArgs a, GradPlan p, int64_t maxima, int64_t weights, int64_t ktw,
                                                    int64_t ktc) {
     constexpr int P = ACT == 0 ? 1 : 2;
     __shared__ __align__(16) uint8_t lds[4 * P * 256 * 12];
     const int64_t b = blockIdx.x;
-    if (b < maxima) max_tile<ACT>(a, p, b, lds);
+    if (b < maxima) max_tile<ACT, C>(a, p, b, lds);
     else if (b < maxima + weights) weights_tile(a, p, b - maxima, ktw, lds);
     else codes_tile(a, p, b - maxima - weights, ktc, lds);
 }
 
-// ---- step 2: columns (a thread each), then rows (a wave each) ------------------------------
+// ---- step 2 (more than one tile of tokens): columns (a thread each), then rows (a wave each) ----
 __global__ __launch_bounds__(256) void k_grad_reduce(BackwardArgs a, GradPlan p, int P, int64_t cblocks) {
     const int64_t NT = P * a.N;
     if (blockIdx.x < cblocks) {
@@ -326,16 +348,15 @@ __device__ __forceinline__ uint32_t split_f16(float v) {
     return (uint32_t)__builtin_bit_cast(uint16_t, hi) | (uint32_t)__builtin_bit_cast(uint16_t, lo) << 16;
 }
 
-// Scaled and split gradients, 64 tokens x 128 columns per workgroup of eight waves; a wave takes
-// eight tokens, a lane two neighbouring columns.  Rows of tokens are written as they come, rows of
-// channels through LDS.  Padded columns
-// and tokens are written as zeros.
+// Scaled and split gradients, 32 tokens x 128 columns per workgroup of eight waves; a wave takes four
+// tokens, their loads under way together, a lane two neighbouring columns.  Rows of tokens are
+// written as they come, rows of channels through LDS.  Padded columns and tokens are written as zeros.
 template <int ACT>
 __global__ __launch_bounds__(512) void k_grad_split(BackwardArgs a, GradPlan p, int ctiles) {
     constexpr int P = ACT == 0 ? 1 : 2;
-    __shared__ uint32_t tile[P][128][65];
+    __shared__ uint32_t tile[P][128][33];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n0 = (int64_t)(blockIdx.x % ctiles) * 128, m0 = (int64_t)(blockIdx.x / ctiles) * 64;
+    const int64_t n0 = (int64_t)(blockIdx.x % ctiles) * 128, m0 = (int64_t)(blockIdx.x / ctiles) * 32;
     const int64_t n = n0 + 2 * lane;
     const float al[2] = {a.al0[0], ACT == 0 ? 0.0f : a.al1[0]};
     float cscale[P][2];
@@ -343,13 +364,33 @@ __global__ __launch_bounds__(512) void k_grad_split(BackwardArgs a, GradPlan p, 
     for (int q = 0; q < P; ++q)
 #pragma unroll
         for (int c = 0; c < 2; ++c) cscale[q][c] = n + c < a.N ? pow2f(scale_exponent(p.cmax[q * a.N + n + c])) : 0.0f;
-#pragma unroll 4
-    for (int t = 0; t < 8; ++t) {
-        const int64_t m = m0 + 8 * wave + t;
+    // with one tile of tokens the rows' maxima are put together here, and kept for the product's scales
+    // (lane l: token l / 16 of the wave, every sixteenth tile)
+    float rmax[4];
+    if (p.mt > 1) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) rmax[t] = m0 + 4 * wave + t < a.M ? p.rmax[m0 + 4 * wave + t] : 0.0f;
+    } else {
+        const int64_t m = m0 + 4 * wave + (lane >> 4);
+        const float* part = p.rpart + (m < a.M ? m : a.M - 1) * p.ct;
+        float v = 0.0f;
+#pragma unroll 8
+        for (int64_t t = lane & 15; t < p.ct; t += 16) v = fmaxf(v, part[t]);
+        v = fmaxf(v, __shfl_xor(v, 1, 64));
+        v = fmaxf(v, __shfl_xor(v, 2, 64));
+        v = fmaxf(v, __shfl_xor(v, 4, 64));
+        v = fmaxf(v, __shfl_xor(v, 8, 64));
+        if (m < a.M && n0 == 0 && (lane & 15) == 0) p.rmax[m] = v;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) rmax[t] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * t));
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int64_t m = m0 + 4 * wave + t;
         float d[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, bs = 0.0f, rscale = 0.0f;   // d[column][projection]
         if (m < a.M) {
             bs = a.beta[m] / 127.0f;
-            rscale = pow2f(scale_exponent(p.rmax[m]));
+            rscale = pow2f(scale_exponent(rmax[t]));
 #pragma unroll
             for (int c = 0; c < 2; ++c)
                 if (n + c < a.N) grad_at<ACT>(a, m * a.N + n + c, d[c]);
@@ -363,29 +404,28 @@ __global__ __launch_bounds__(512) void k_grad_split(BackwardArgs a, GradPlan p, 
                 o[2048] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tile[q][2 * lane + c][8 * wave + t] = split_f16(d[c][q] * bs * cscale[q][c]);
+            for (int c = 0; c < 2; ++c) tile[q][2 * lane + c][4 * wave + t] = split_f16(d[c][q] * bs * cscale[q][c]);
         }
     }
     if (!a.dw0) return;
     __syncthreads();
-    const int u = threadIdx.x & 7;
+    const int u = threadIdx.x & 3, r = threadIdx.x >> 2;
+    if (n0 + r >= a.N) return;
 #pragma unroll
-    for (int q = 0; q < P; ++q)
-        for (int r = threadIdx.x >> 3; r < 128; r += 64) {
-            if (n0 + r >= a.N) break;
-            uint32_t v[8];
+    for (int q = 0; q < P; ++q) {
+        uint32_t v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = tile[q][r][8 * u + j];
-            u32x4 h, l;
+        for (int j = 0; j < 8; ++j) v[j] = tile[q][r][8 * u + j];
+        u32x4 h, l;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[j] = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], 0x05040100u);
-                l[j] = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], 0x07060302u);
-            }
-            u32x4* o = reinterpret_cast<u32x4*>(p.wsp + split_at(q * a.N + n0 + r, m0 + 8 * u, p.Mp));
-            o[0] = h;
-            o[512] = l;
+        for (int j = 0; j < 4; ++j) {
+            h[j] = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], 0x05040100u);
+            l[j] = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], 0x07060302u);
         }
+        u32x4* o = reinterpret_cast<u32x4*>(p.wsp + split_at(q * a.N + n0 + r, m0 + 8 * u, p.Mp));
+        o[0] = h;
+        o[512] = l;
+    }
 }
 
 // ---- step 4 -------------------------------------------------------------------------------
@@ -545,6 +585,7 @@ __global__ __launch_bounds__(256) void k_split_sum(SplitArgs x, SplitArgs w, int
     if (e >= n) return;
     const int64_t row = e / a.J;
     float s = 0.0f;
+#pragma unroll 8
     for (int q = 0; q < a.parts; ++q) s += a.part[q * n + e];
     s *= pow2f(-scale_exponent(a.amax[row]));
     if (row < a.I0) a.c0[e] = s;
@@ -558,12 +599,15 @@ static hipError_t launch_grads(const BackwardArgs& a, hipStream_t s) {
     auto blocks = [](int64_t n) { return dim3((unsigned)n); };
     const int64_t ktw = (a.K + 255) / 256, ktc = (a.K + 63) / 64;
     const int64_t maxima = p.mt * p.ct, weights = a.dx ? p.Lx / 64 * ktw : 0, codes = a.dw0 ? p.Mp / 64 * ktc : 0;
-    hipLaunchKernelGGL(k_grad_prep<ACT>, blocks(maxima + weights + codes), dim3(256), 0, s, a, p, maxima, weights, ktw, ktc);
+    if (p.tn == 64)
+        hipLaunchKernelGGL((k_grad_prep<ACT, 1>), blocks(maxima + weights + codes), dim3(256), 0, s, a, p, maxima, weights, ktw, ktc);
+    else
+        hipLaunchKernelGGL((k_grad_prep<ACT, 4>), blocks(maxima + weights + codes), dim3(256), 0, s, a, p, maxima, weights, ktw, ktc);
     const int64_t cblocks = (P * a.N + 255) / 256;
-    hipLaunchKernelGGL(k_grad_reduce, blocks(cblocks + (a.M + 3) / 4), dim3(256), 0, s, a, p, P, cblocks);
+    if (p.mt > 1) hipLaunchKernelGGL(k_grad_reduce, blocks(cblocks + (a.M + 3) / 4), dim3(256), 0, s, a, p, P, cblocks);
     if (!a.dx && !a.dw0) return hipGetLastError();
     const int64_t ct = (a.N + 127) / 128;
-    hipLaunchKernelGGL(k_grad_split<ACT>, blocks(p.Mp / 64 * ct), dim3(512), 0, s, a, p, (int)ct);
+    hipLaunchKernelGGL(k_grad_split<ACT>, blocks(p.Mp / 32 * ct), dim3(512), 0, s, a, p, (int)ct);
     auto tiles = [](SplitArgs q) {
         q.tiles_i = (int)((q.I + SG_BM - 1) / SG_BM);
         q.tiles_j = (int)((q.J + SG_BN - 1) / SG_BN);
