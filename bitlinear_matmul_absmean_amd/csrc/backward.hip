@@ -104,12 +104,16 @@ struct GradPlan {
     size_t bytes;
 };
 
-// Parts to cut a sum of length L into: the rounds of workgroups over the slots (a last round that
-// leaves one workgroup to a compute unit runs in 0.6 of the time), times a part's share of the sum, plus the exchange of the parts (a part is written and read once for each output, 8
-// bytes, and the output written once more; 4 bytes take the time of 220 terms).  Parts of at least
-// 256 terms, at most 32.
-static int sum_parts(int64_t I, int64_t J, int64_t L) {
-    const int64_t tiles = ((I + SG_BM - 1) / SG_BM) * ((J + SG_BN - 1) / SG_BN);
+static int64_t product_tiles(int64_t I, int64_t J) { return ((I + SG_BM - 1) / SG_BM) * ((J + SG_BN - 1) / SG_BN); }
+
+// Parts to cut a sum of length L into (`tiles` tiles of outputs).  The least cost of: the rounds of
+// workgroups over the slots (a last round that leaves one workgroup to a compute unit runs in 0.6 of the
+// time) times a part's share of the sum, plus the exchange of the parts (a part is written and read once
+// for each output, 8 bytes, and the output written once more; 4 bytes take the time of 220 terms).  But no
+// more parts than bring a workgroup under the time `even` that the workgroups of both products take
+// together, evenly spread: the other product's fill the slots (2048 tokens, K = 4096, F = 11008: dx in one
+// part 1327 us, in two 1369).  Parts of at least 256 terms, at most 32.
+static int sum_parts(int64_t tiles, int64_t L, int64_t even) {
     int best = 1;
     double cost = 1e30;
     for (int s = 1; s <= 32 && (s == 1 || L / s >= 256); ++s) {
@@ -120,6 +124,7 @@ static int sum_parts(int64_t I, int64_t J, int64_t L) {
             cost = c;
             best = s;
         }
+        if (L / s <= even) break;
     }
     return best;
 }
@@ -135,8 +140,9 @@ static GradPlan grad_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws)
     p.ct = (N + p.tn - 1) / p.tn;
     p.tm = M <= 64 || (M + 63) / 64 * p.ct >= 512 ? 64 : 16;
     p.mt = (M + p.tm - 1) / p.tm;
-    p.parts_x = sum_parts(M, K, p.Lx);
-    p.parts_w = sum_parts(P * N, K, p.Mp);
+    const int64_t tx = product_tiles(M, K), tw = product_tiles(P * N, K), even = (tx * p.Lx + tw * p.Mp) / SG_SLOTS;
+    p.parts_x = sum_parts(tx, p.Lx, even);
+    p.parts_w = sum_parts(tw, p.Mp, even);
     uint8_t* base = static_cast<uint8_t*>(ws);
     size_t off = 0;
     auto take = [&](int64_t count, size_t size) {
