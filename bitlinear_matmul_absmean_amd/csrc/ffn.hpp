@@ -68,6 +68,33 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& slope) {
     }
 }
 
+// 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.  What is left
+// of a row at its end comes as the row's last 16 bytes, shifted down.
+__device__ __forceinline__ u32x4 row_16(const uint8_t* __restrict__ p, int64_t i, int64_t row) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (i + 16 <= row) {
+        __builtin_memcpy(&v, p + i, 16);
+    } else if (i < row) {
+        if (row >= 16) {
+            unsigned __int128 t;
+            __builtin_memcpy(&t, p + row - 16, 16);
+            t >>= 8 * (int)(i + 16 - row);
+            v = __builtin_bit_cast(u32x4, t);
+        } else {
+            for (int j = 0; j < 16; ++j)
+                if (i + j < row) v[j >> 2] |= (uint32_t)p[i + j] << (8 * (j & 3));
+        }
+    }
+    return v;
+}
+
+// 16 bytes at p, whatever its alignment.
+__device__ __forceinline__ u32x4 load_16(const uint8_t* __restrict__ p) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
 struct GatedArgs {
     const int8_t* xq;
     const float* beta;

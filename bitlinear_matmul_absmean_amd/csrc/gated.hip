@@ -40,18 +40,6 @@ __device__ __forceinline__ void gated_store(const GatedArgs& a, int64_t at, int6
     else gated_store<BITLINEAR_ACT_RELU2>(a, at, sg, su, scale_g, scale_u, bg, bu);
 }
 
-// 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.
-__device__ __forceinline__ u32x4 row_16(const uint8_t* __restrict__ p, int64_t i, int64_t row) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (i + 16 <= row) {
-        __builtin_memcpy(&v, p + i, 16);
-    } else {
-        for (int j = 0; j < 16; ++j)
-            if (i + j < row) v[j >> 2] |= (uint32_t)p[i + j] << (8 * (j & 3));
-    }
-    return v;
-}
-
 // ---- one token ------------------------------------------------------------------------------
 // A workgroup of eight waves quantizes x for itself (absmax, codes, their sum) while its first weight
 // rows are on their way; a wave then takes `pairs` gate and up rows, R of each at a time.  A lane's
@@ -286,7 +274,37 @@ __global__ __launch_bounds__(64 * GD_WAVES) void k_gated_dec(GatedArgs a, int sl
         }
         if (whole < steps && whole % GD_WAVES == wave) direct(whole);
     } else {
-        for (int s = wave; s < steps; s += GD_WAVES) direct(s);
+        struct Part {
+            i32x4 x[MT][4];
+            u32x4 w[2 * RB];
+        };
+        auto load = [&](int s) {
+            const int64_t k = (int64_t)s * 256 + 64 * lg;
+            Part f;
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const int64_t row = (int64_t)min(16 * r + lr, rows_n - 1) * rowb + (k >> 2);
+                f.w[r] = load_16(g0 + row);
+                f.w[RB + r] = load_16(u0 + row);
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    f.x[t][q] = (i32x4)load_16(reinterpret_cast<const uint8_t*>(x0) + (int64_t)min(16 * t + lr, rows_m - 1) * K + k + 16 * q);
+            return f;
+        };
+        // whole steps, the next one's loads under way; the last part step goes to the next wave in turn
+        const int whole = (int)(K / 256);
+        if (wave < whole) {
+            Part f = load(wave);
+            for (int s = wave; s < whole; s += GD_WAVES) {
+                const Part next = load(min(s + GD_WAVES, whole - 1));
+                multiply(f.x, f.w);
+                f = next;
+            }
+        }
+        if (whole < steps && whole % GD_WAVES == wave) direct(whole);
     }
     __syncthreads();                                                // every wave is done with its image
 #pragma unroll
@@ -474,28 +492,56 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
             multiply(st0, 1);
         }
     } else {
-        u32x4 v[FM + 2];
-        const int steps = (int)((K + GG_BK - 1) / GG_BK);
+        struct Regs {
+            u32x4 v[FM + 2];
+        };
+        const int64_t wr = (int64_t)min(wrow, rows_n - 1) * rowb;
         auto load = [&](int s) {
-            const int64_t k = (int64_t)s * GG_BK, w = (int64_t)min(wrow, rows_n - 1) * rowb;
+            const int64_t k = (int64_t)s * GG_BK;
+            Regs r;
 #pragma unroll
-            for (int q = 0; q < FM; ++q) v[q] = row_16(x0 + (int64_t)min(xrow(q), rows_m - 1) * K, k + 16 * xunit(q), K);
-            v[FM] = row_16(g0 + w, (k >> 2) + 16 * wunit, rowb);
-            v[FM + 1] = row_16(u0 + w, (k >> 2) + 16 * wunit, rowb);
+            for (int q = 0; q < FM; ++q) r.v[q] = load_16(x0 + (int64_t)min(xrow(q), rows_m - 1) * K + k + 16 * xunit(q));
+            r.v[FM] = load_16(g0 + wr + (k >> 2) + 16 * wunit);
+            r.v[FM + 1] = load_16(u0 + wr + (k >> 2) + 16 * wunit);
+            return r;
         };
-        auto put = [&](i32x4* st) {
+        auto put = [&](i32x4* st, const Regs& r) {
 #pragma unroll
-            for (int q = 0; q < FM; ++q) st[64 * (FM * wave + q) + lane] = (i32x4)v[q];
-            st[OB + 64 * wave + lane] = (i32x4)v[FM];
-            st[OB + 256 + 64 * wave + lane] = (i32x4)v[FM + 1];
+            for (int q = 0; q < FM; ++q) st[64 * (FM * wave + q) + lane] = (i32x4)r.v[q];
+            st[OB + 64 * wave + lane] = (i32x4)r.v[FM];
+            st[OB + 256 + 64 * wave + lane] = (i32x4)r.v[FM + 1];
         };
-        load(0);
-        put(st0);
-        for (int s = 0; s < steps; ++s) {
-            __syncthreads();                                        // step s is in its stage, and the other stage is free
-            if (s + 1 < steps) load(s + 1);
-            multiply(s & 1 ? st1 : st0, 2);
-            if (s + 1 < steps) put(s & 1 ? st0 : st1);
+        // The last part step first (sums of integers are exact in any order), through st0, while the first
+        // whole steps' loads are under way; then whole steps in st1 and st0 in turn, loaded three ahead.
+        const int whole = (int)(K / GG_BK), last = whole - 1;
+        Regs r0, r1;
+        if (whole > 0) {
+            r0 = load(0);
+            r1 = load(min(1, last));
+        }
+        if (K % GG_BK) {
+            const int64_t k = (int64_t)whole * GG_BK;
+            Regs r;
+#pragma unroll
+            for (int q = 0; q < FM; ++q) r.v[q] = row_16(x0 + (int64_t)min(xrow(q), rows_m - 1) * K, k + 16 * xunit(q), K);
+            r.v[FM] = row_16(g0 + wr, (k >> 2) + 16 * wunit, rowb);
+            r.v[FM + 1] = row_16(u0 + wr, (k >> 2) + 16 * wunit, rowb);
+            put(st0, r);
+            __syncthreads();
+            multiply(st0, 2);
+        } else {
+            __syncthreads();                                        // the tokens' scales
+        }
+        for (int s = 0; s < whole; s += 2) {
+            put(st1, r0);                                           // its last readers are past the barrier before this one
+            r0 = load(min(s + 2, last));
+            __syncthreads();
+            multiply(st1, 2);
+            if (s + 1 >= whole) break;
+            put(st0, r1);
+            r1 = load(min(s + 3, last));
+            __syncthreads();
+            multiply(st0, 2);
         }
     }
     // accumulator r of lane l: token 8 (r / 4) + 4 (l / 32) + r % 4 of the block, column l % 32

@@ -25,21 +25,15 @@ __device__ __forceinline__ void i8_store(const I8Args& a, int64_t at, int acc, f
     if (a.acc) a.acc[at] = acc;
 }
 
-// 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.
 __device__ __forceinline__ i32x4 row_16(const int8_t* __restrict__ p, int64_t i, int64_t row) {
-    i32x4 v = {0, 0, 0, 0};
-    if (i + 16 <= row) {
-        __builtin_memcpy(&v, p + i, 16);
-    } else {
-        for (int j = 0; j < 16; ++j)
-            if (i + j < row) v[j >> 2] |= (int)((uint32_t)(uint8_t)p[i + j] << (8 * (j & 3)));
-    }
-    return v;
+    return (i32x4)row_16(reinterpret_cast<const uint8_t*>(p), i, row);
 }
+__device__ __forceinline__ i32x4 load_16(const int8_t* __restrict__ p) { return (i32x4)load_16(reinterpret_cast<const uint8_t*>(p)); }
 
 // ---- one token ------------------------------------------------------------------------------
 // A wave takes R weight rows, 1 KiB of each at a time, so that R loads of 16 bytes a lane are in
-// flight while the last ones meet x_q, which lies in LDS as it is (zeros up to the next KiB).
+// flight while the last ones meet x_q, which lies in LDS as it is, in whole units of 16 (zeros up to the
+// next KiB); what is left of K goes to lane 0.
 template <bool ALIGNED, int R>
 __global__ __launch_bounds__(256) void k_i8_gemv(I8Args a) {
     extern __shared__ i32x4 xs[];
@@ -54,14 +48,18 @@ __global__ __launch_bounds__(256) void k_i8_gemv(I8Args a) {
         const int64_t k = (int64_t)c * 1024 + 16 * lane;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            // past the row's end x_q is zero: any bytes will do, the row's first for aligned rows
-            if constexpr (ALIGNED) v[r] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(w[r] + (k < K ? k : 0)));
-            else v[r] = row_16(w[r], k, K);
+            // past the last whole unit x_q is zero: any bytes will do, the row's first (rows of fewer than
+            // 16 have no whole unit, and are not read here)
+            const int8_t* p = w[r] + (k + 16 <= K ? k : 0);
+            if constexpr (ALIGNED) v[r] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p));
+            else if (K >= 16) v[r] = load_16(p);
+            else v[r] = i32x4{0, 0, 0, 0};
         }
     };
     i32x4 v0[R], v1[R];
     load(v0, 0);
-    for (int i = tid; i < chunks * 64; i += 256) xs[i] = row_16(a.xq, (int64_t)i * 16, K);
+    for (int i = tid; i < chunks * 64; i += 256)
+        xs[i] = (int64_t)i * 16 + 16 <= K ? load_16(a.xq + (int64_t)i * 16) : i32x4{0, 0, 0, 0};
     __syncthreads();
     int s[R];
 #pragma unroll
@@ -79,6 +77,16 @@ __global__ __launch_bounds__(256) void k_i8_gemv(I8Args a) {
         if (c + 1 >= chunks) break;
         if (c + 2 < chunks) load(v0, c + 2);
         dot(v1, c + 1);
+    }
+    if (!ALIGNED && K % 16 && lane == 0) {
+        const int64_t k = K / 16 * 16;
+        const i32x4 x = row_16(a.xq, k, K);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const i32x4 v = row_16(w[r], k, K);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[r] = dot4((uint32_t)v[j], (uint32_t)x[j], s[r]);
+        }
     }
     int mine = 0;
 #pragma unroll
@@ -203,14 +211,35 @@ __global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) 
         for (int t = 0; t < MT; ++t) xp[t] = x0 + (int64_t)min(16 * t + lr, rows_m - 1) * K;
 #pragma unroll
         for (int r = 0; r < RB; ++r) wp[r] = w0 + (int64_t)min(16 * r + lr, rows_n - 1) * K;
-        for (int s = wave; s < steps; s += I8_WAVES) {
-            const int64_t k = (int64_t)s * 64 + 16 * lg;
+        struct Part {
             i32x4 x[MT], w[RB];
+        };
+        auto load = [&](int s) {
+            const int64_t k = (int64_t)s * 64 + 16 * lg;
+            Part f;
 #pragma unroll
-            for (int r = 0; r < RB; ++r) w[r] = row_16(wp[r], k, K);
+            for (int r = 0; r < RB; ++r) f.w[r] = load_16(wp[r] + k);
 #pragma unroll
-            for (int t = 0; t < MT; ++t) x[t] = row_16(xp[t], k, K);
-            multiply(x, w);
+            for (int t = 0; t < MT; ++t) f.x[t] = load_16(xp[t] + k);
+            return f;
+        };
+        // whole steps, the next one's loads under way; the last part step goes to the next wave in turn
+        const int whole = (int)(K / 64), last = whole - 1;
+        Part f0, f1;
+        if (wave < whole) f0 = load(wave);
+        for (int s = wave; s < whole; s += 2 * I8_WAVES) {
+            f1 = load(min(s + I8_WAVES, last));
+            multiply(f0.x, f0.w);
+            f0 = load(min(s + 2 * I8_WAVES, last));
+            if (s + I8_WAVES < whole) multiply(f1.x, f1.w);
+        }
+        if (whole < steps && whole % I8_WAVES == wave) {
+            const int64_t k = (int64_t)whole * 64 + 16 * lg;
+#pragma unroll
+            for (int r = 0; r < RB; ++r) f0.w[r] = row_16(wp[r], k, K);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) f0.x[t] = row_16(xp[t], k, K);
+            multiply(f0.x, f0.w);
         }
     }
     // the eight partial tiles through LDS, one block of 16 channels after another
@@ -409,30 +438,59 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
         for (int q = 0; q < MI; ++q) xp[q] = x0 + (int64_t)min(block_row(MI * wave + q), rows_m - 1) * K;
 #pragma unroll
         for (int q = 0; q < 4; ++q) wp[q] = w0 + (int64_t)min(block_row(4 * wave + q), rows_n - 1) * K;
-        i32x4 v[MI + 4];
+        struct Regs {
+            i32x4 v[MI + 4];
+        };
         auto load = [&](int s) {
             const int64_t k = (int64_t)s * IG_BK;
+            Regs r;
 #pragma unroll
-            for (int q = 0; q < MI; ++q) v[q] = row_16(xp[q], k + 16 * block_unit(MI * wave + q), K);
+            for (int q = 0; q < MI; ++q) r.v[q] = load_16(xp[q] + k + 16 * block_unit(MI * wave + q));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[MI + q] = row_16(wp[q], k + 16 * block_unit(4 * wave + q), K);
+            for (int q = 0; q < 4; ++q) r.v[MI + q] = load_16(wp[q] + k + 16 * block_unit(4 * wave + q));
+            return r;
         };
-        auto put = [&](i32x4* st) {
+        auto put = [&](i32x4* st, const Regs& r) {
 #pragma unroll
-            for (int q = 0; q < MI; ++q) st[64 * (MI * wave + q) + lane] = v[q];
+            for (int q = 0; q < MI; ++q) st[64 * (MI * wave + q) + lane] = r.v[q];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) st[OB + 64 * (4 * wave + q) + lane] = v[MI + q];
+            for (int q = 0; q < 4; ++q) st[OB + 64 * (4 * wave + q) + lane] = r.v[MI + q];
         };
-        const int steps = (int)((K + IG_BK - 1) / IG_BK);
-        load(0);
-        put(st0);
-        for (int s = 0; s < steps; ++s) {
-            __syncthreads();                       // step s is in its stage, and the other stage is free
-            if (s + 1 < steps) load(s + 1);
-            const i32x4* cur = s & 1 ? st1 : st0;
+        auto multiply_stage = [&](const i32x4* st) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) multiply(read(cur, kk));
-            if (s + 1 < steps) put(s & 1 ? st0 : st1);
+            for (int kk = 0; kk < 4; ++kk) multiply(read(st, kk));
+        };
+        // The last part step first (sums of integers are exact in any order), through st0, while the first
+        // whole steps' loads are under way; then whole steps in st1 and st0 in turn, loaded three ahead.
+        const int whole = (int)(K / IG_BK), last = whole - 1;
+        Regs r0, r1;
+        if (whole > 0) {
+            r0 = load(0);
+            r1 = load(min(1, last));
+        }
+        if (K % IG_BK) {
+            const int64_t k = (int64_t)whole * IG_BK;
+            Regs r;
+#pragma unroll
+            for (int q = 0; q < MI; ++q) r.v[q] = row_16(xp[q], k + 16 * block_unit(MI * wave + q), K);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) r.v[MI + q] = row_16(wp[q], k + 16 * block_unit(4 * wave + q), K);
+            put(st0, r);
+            __syncthreads();
+            multiply_stage(st0);
+        } else {
+            __syncthreads();                       // the tokens' scales
+        }
+        for (int s = 0; s < whole; s += 2) {
+            put(st1, r0);                          // its last readers are past the barrier before this one
+            r0 = load(min(s + 2, last));
+            __syncthreads();
+            multiply_stage(st1);
+            if (s + 1 >= whole) break;
+            put(st0, r1);
+            r1 = load(min(s + 3, last));
+            __syncthreads();
+            multiply_stage(st0);
         }
     }
     // tokens 4 q .. 4 q + 3 of a block are four registers of a lane: their scales are one LDS read
