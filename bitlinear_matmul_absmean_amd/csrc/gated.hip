@@ -13,6 +13,8 @@
 //   * up to 64: k_gated_dec, the weight streams on the 16x16x64 int8 MFMA;
 //   * more: k_gated_gemm, LDS tiles on the 32x32x32 int8 MFMA;
 // the last two also in a form for any K % 4 == 0 and any alignment.
+#include <type_traits>
+
 #include "ffn.hpp"
 
 namespace bitlinear {
@@ -358,10 +360,10 @@ static hipError_t launch_gated_dec(const GatedArgs& a, hipStream_t s) {
 }
 
 // ---- more tokens ----------------------------------------------------------------------------
-// A workgroup of four waves computes 128 tokens x 128 columns of both projections, a wave all 128
-// tokens x 32 columns of each: four 32-token operands against one gate and one up operand, so that
-// the expansion of a weight operand (17 instructions) serves four MFMAs.  Steps of 128 k, three LDS
-// stages (24 KiB each: 128 token rows of 128 bytes, 256 weight rows of 32 bytes) filled two steps
+// A workgroup of four waves computes 32 FM tokens x 128 columns of both projections, a wave all the
+// tokens x 32 columns of each: FM 32-token operands against one gate and one up operand, so that the
+// expansion of a weight operand (17 instructions) serves FM MFMAs.  Steps of 128 k, three LDS stages
+// (4 FM + 8 KiB each: 32 FM token rows of 128 bytes, 256 weight rows of 32 bytes) filled two steps
 // ahead by loads that go past the registers (aligned rows: 16-byte aligned tensors, K % 64 == 0), or two filled through
 // registers.  Unit u of token row r lies at slot u ^ ((r / 2) % 8), unit u of weight row r at slot
 // u ^ ((r / 8) % 2), so that an operand read spreads over all banks.
@@ -482,8 +484,9 @@ __global__ __launch_bounds__(256, 2) void k_gated_gemm(GatedArgs a, int tiles_m,
             // the last 64 k through st0, which nobody reads any more
             const int64_t k = (int64_t)steps * GG_BK;
 #pragma unroll
-            for (int j = 0; j < FM / 2; ++j) {
+            for (int j = 0; j < (FM + 1) / 2; ++j) {
                 const int r = (tid >> 2) + 64 * j, u = tid & 3;
+                if (r >= GG_BM) break;
                 st0[r * 8 + (u ^ ((r >> 1) & 7))] = *reinterpret_cast<const i32x4*>(x0 + (int64_t)min(r, rows_m - 1) * K + k + 16 * u);
             }
             const uint8_t* w = tid < 128 ? g0 : u0;
@@ -593,26 +596,31 @@ static hipError_t launch_gated_gemm_fm(const GatedArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// 64-token tiles while 128-token ones would not fill the 512 workgroup slots well: K = 4096, F = 11008,
-// M = 128 (86 tiles of 128): 27.4 against 39.4 us; M = 512 (344): 58.6 against 61.3; M = 1024 (688):
-// 106.6 against 97.8; K = 8192, F = 28672, M = 256 (448): 131 against 113 us.
+// Tiles of 32 tokens while they all run at once, of 64 while those of 128 would not fill the 512 workgroup
+// slots well: K = 4096, F = 11008, M = 64 (172 tiles of 32) 21.6 against 26.0 us, M = 128 (344) 30.4 against
+// 27.0 with 64-token tiles and 39.4 with 128, M = 512 (344 of 128) 58.6 against 61.3 with 128, M = 1024 (688)
+// 106.6 against 97.8; K = 8192, F = 28672, M = 256 (448) 131 against 113 us.
 template <bool ALIGNED>
 static hipError_t launch_gated_gemm(const GatedArgs& a, hipStream_t s) {
-    const bool small = (a.M + 127) / 128 * ((a.F + GG_BF - 1) / GG_BF) <= 384;
+    const int64_t tf = (a.F + GG_BF - 1) / GG_BF;
+    const int fm = (a.M + 31) / 32 * tf <= 256 ? 1 : (a.M + 127) / 128 * tf <= 384 ? 2 : 4;
+    auto run = [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        return fm == 1 ? launch_gated_gemm_fm<ACT, ALIGNED, 1>(a, s)
+               : fm == 2 ? launch_gated_gemm_fm<ACT, ALIGNED, 2>(a, s)
+                         : launch_gated_gemm_fm<ACT, ALIGNED, 4>(a, s);
+    };
     switch (a.act) {
-        case BITLINEAR_ACT_SILU:
-            return small ? launch_gated_gemm_fm<BITLINEAR_ACT_SILU, ALIGNED, 2>(a, s) : launch_gated_gemm_fm<BITLINEAR_ACT_SILU, ALIGNED, 4>(a, s);
-        case BITLINEAR_ACT_GELU:
-            return small ? launch_gated_gemm_fm<BITLINEAR_ACT_GELU, ALIGNED, 2>(a, s) : launch_gated_gemm_fm<BITLINEAR_ACT_GELU, ALIGNED, 4>(a, s);
-        default:
-            return small ? launch_gated_gemm_fm<BITLINEAR_ACT_RELU2, ALIGNED, 2>(a, s) : launch_gated_gemm_fm<BITLINEAR_ACT_RELU2, ALIGNED, 4>(a, s);
+        case BITLINEAR_ACT_SILU: return run(std::integral_constant<int, BITLINEAR_ACT_SILU>());
+        case BITLINEAR_ACT_GELU: return run(std::integral_constant<int, BITLINEAR_ACT_GELU>());
+        default: return run(std::integral_constant<int, BITLINEAR_ACT_RELU2>());
     }
 }
 
 // The streaming kernel up to 32 tokens, and beyond while the GEMM has at most 64 tiles of 64 x 128, too
-// few to fill the chip: K = 4096, F = 11008: M = 32 18.5 against 25.0 us, M = 64 (86 tiles) 26.3 against
-// 26.0, M = 128 38.2 against 27.4; K = 11008, F = 4096: M = 128 (64 tiles) 27.9 against 56.6, M = 512 (256)
-// 86.9 against 61.4; K = 1024, F = 2816: M = 128 (44) 10.0 against 12.0, M = 256 (88) 16.4 against 12.3 us.
+// few to fill the chip: K = 4096, F = 11008: M = 32 15.2 against 21.3 us, M = 64 (86 tiles) 26.3 against
+// 21.6, M = 128 38.2 against 27.0; K = 11008, F = 4096: M = 128 (64 tiles) 27.9 against 56.6, M = 512 (256)
+// 86.9 against 61.4; K = 1024, F = 2816: M = 64 (22) 7.2 against 9.4, M = 256 (88) 16.4 against 10.0 us.
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
     const bool aligned = a.K % 64 == 0 && (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.wg % 16 == 0 && (uintptr_t)a.wu % 16 == 0;
     if (a.M <= 32 || (a.M + 63) / 64 * ((a.F + GG_BF - 1) / GG_BF) <= 64)
