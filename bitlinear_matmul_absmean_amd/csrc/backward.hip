@@ -282,11 +282,19 @@ __device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPl
     const int q = l0 >= p.Np;
     const int64_t n0 = l0 - q * p.Np, rowb = a.K >> 2;
     const uint8_t* w = q ? a.w1 : a.w0;
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-        const int r = i >> 4, c = 4 * (i & 15);
-        const int64_t n = n0 + r;
-        put_column_bytes(lds, r, c, n < a.N ? row_dword(w + n * rowb, (k0 >> 2) + c, rowb) : 0x55555555u);
+    // thread t: dword t % 16 of rows t / 16 + 16 i, its four loads under way together
+    const int c4 = 4 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
+    const int64_t at = (k0 >> 2) + c4;
+    uint32_t d[4];
+    if (n0 + 64 <= a.N && (k0 >> 2) + 64 <= rowb) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __builtin_memcpy(&d[i], w + (n0 + r0 + 16 * i) * rowb + at, 4);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = n0 + r0 + 16 * i < a.N ? row_dword(w + (n0 + r0 + 16 * i) * rowb, at, rowb) : 0x55555555u;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put_column_bytes(lds, r0 + 16 * i, c4, d[i]);
     __syncthreads();
     const int u = threadIdx.x & 3, c = threadIdx.x >> 2;
     const u32x4 v = *reinterpret_cast<const u32x4*>(lds + c * 80 + 16 * u);
@@ -300,11 +308,18 @@ __device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPl
 // Panels of x_q^T, 64 tokens x 64 columns per workgroup.
 __device__ __forceinline__ void codes_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint8_t* lds) {
     const int64_t k0 = b % kt * 64, m0 = b / kt * 64;
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-        const int r = i >> 4, c = 4 * (i & 15);
-        const int64_t m = m0 + r;
-        put_column_bytes(lds, r, c, m < a.M ? row_dword(reinterpret_cast<const uint8_t*>(a.xq) + m * a.K, k0 + c, a.K) : 0u);
+    const int c4 = 4 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(a.xq);
+    uint32_t d[4];
+    if (m0 + 64 <= a.M && k0 + 64 <= a.K) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __builtin_memcpy(&d[i], x + (m0 + r0 + 16 * i) * a.K + k0 + c4, 4);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = m0 + r0 + 16 * i < a.M ? row_dword(x + (m0 + r0 + 16 * i) * a.K, k0 + c4, a.K) : 0u;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put_column_bytes(lds, r0 + 16 * i, c4, d[i]);
     __syncthreads();
     const int u = threadIdx.x & 3, c = threadIdx.x >> 2;
     const u32x4 v = *reinterpret_cast<const u32x4*>(lds + c * 80 + 16 * u);
