@@ -222,7 +222,7 @@ __device__ __forceinline__ void max_tile(const BackwardArgs& a, const GradPlan& 
                 }
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const float v = wave_max_f32(rm[t]);
+            const float v = wave_max_pos(rm[t]);
             if (lane == 0 && mb + t < a.M) p.rpart[(mb + t) * p.ct + tn] = v;
         }
     }
@@ -357,7 +357,7 @@ __global__ __launch_bounds__(256) void k_grad_reduce(BackwardArgs a, GradPlan p,
         const int lane = threadIdx.x & 63;
         float v = 0.0f;
         for (int64_t t = lane; t < p.ct; t += 64) v = fmaxf(v, p.rpart[m * p.ct + t]);
-        v = wave_max_f32(v);
+        v = wave_max_pos(v);
         if (lane == 0) p.rmax[m] = v;
     }
 }

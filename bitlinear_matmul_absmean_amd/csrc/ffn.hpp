@@ -2,6 +2,8 @@
 // activation helpers and launch declarations.
 #pragma once
 
+#include <type_traits>
+
 #include "bitlinear.h"
 #include "common.hpp"
 
@@ -66,6 +68,21 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& slope) {
         a = r * r;
         slope = 2.0f * r;
     }
+}
+
+// Largest of the 64 lanes' non-negative values, the same in every lane: exchanges inside rows of 16
+// lanes by DPP (pairs, quads, halves, rows), then the four rows' values.
+__device__ __forceinline__ float wave_max_pos(float v) {
+    auto other = [](float x, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    v = fmaxf(v, other(v, std::integral_constant<int, 0xB1>()));       // quad_perm [1, 0, 3, 2]
+    v = fmaxf(v, other(v, std::integral_constant<int, 0x4E>()));       // quad_perm [2, 3, 0, 1]
+    v = fmaxf(v, other(v, std::integral_constant<int, 0x141>()));      // row_half_mirror
+    v = fmaxf(v, other(v, std::integral_constant<int, 0x140>()));      // row_mirror
+    const int i = __float_as_int(v);
+    return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(i, 0)), __int_as_float(__builtin_amdgcn_readlane(i, 16))),
+                 fmaxf(__int_as_float(__builtin_amdgcn_readlane(i, 32)), __int_as_float(__builtin_amdgcn_readlane(i, 48))));
 }
 
 // 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.  What is left

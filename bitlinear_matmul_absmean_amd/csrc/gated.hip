@@ -13,8 +13,6 @@
 //   * up to 64: k_gated_dec, the weight streams on the 16x16x64 int8 MFMA;
 //   * more: k_gated_gemm, LDS tiles on the 32x32x32 int8 MFMA;
 // the last two also in a form for any K % 4 == 0 and any alignment.
-#include <type_traits>
-
 #include "ffn.hpp"
 
 namespace bitlinear {
@@ -85,7 +83,7 @@ __global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const
     float mx = 0.0f;
 #pragma unroll
     for (int i = 0; i < FPT; ++i) mx = fmaxf(mx, fmaxf(fmaxf(fabsf(xv[i].x), fabsf(xv[i].y)), fmaxf(fabsf(xv[i].z), fabsf(xv[i].w))));
-    mx = wave_max_f32(mx);
+    mx = wave_max_pos(mx);
     if (lane == 0) red_f[wave] = mx;
     __syncthreads();
     mx = red_f[0];
