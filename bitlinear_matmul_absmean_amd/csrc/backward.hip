@@ -344,11 +344,13 @@ __global__ __launch_bounds__(256) void k_grad_reduce(BackwardArgs a, GradPlan p,
         const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
         if (n >= NT) return;
         float v = 0.0f;
+#pragma unroll 8
         for (int64_t t = 0; t < p.mt; ++t) v = fmaxf(v, p.cpart[t * NT + n]);
         p.cmax[n] = v;
         float* out = n < a.N ? a.db0 : a.db1;
         if (!out) return;
         double s = 0.0;
+#pragma unroll 8
         for (int64_t t = 0; t < p.mt; ++t) s += p.bpart[t * NT + n];
         out[n < a.N ? n : n - a.N] = (float)s;
     } else {

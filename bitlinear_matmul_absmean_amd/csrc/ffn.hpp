@@ -2,8 +2,6 @@
 // activation helpers and launch declarations.
 #pragma once
 
-#include <type_traits>
-
 #include "bitlinear.h"
 #include "common.hpp"
 
@@ -70,19 +68,29 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& slope) {
     }
 }
 
-// Largest of the 64 lanes' non-negative values, the same in every lane: exchanges inside rows of 16
-// lanes by DPP (pairs, quads, halves, rows), then the four rows' values.
-__device__ __forceinline__ float wave_max_pos(float v) {
-    auto other = [](float x, auto ctrl) {
-        return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
-    };
-    v = fmaxf(v, other(v, std::integral_constant<int, 0xB1>()));       // quad_perm [1, 0, 3, 2]
-    v = fmaxf(v, other(v, std::integral_constant<int, 0x4E>()));       // quad_perm [2, 3, 0, 1]
-    v = fmaxf(v, other(v, std::integral_constant<int, 0x141>()));      // row_half_mirror
-    v = fmaxf(v, other(v, std::integral_constant<int, 0x140>()));      // row_mirror
-    const int i = __float_as_int(v);
-    return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(i, 0)), __int_as_float(__builtin_amdgcn_readlane(i, 16))),
-                 fmaxf(__int_as_float(__builtin_amdgcn_readlane(i, 32)), __int_as_float(__builtin_amdgcn_readlane(i, 48))));
+// Reductions over the 64 lanes, the same in every lane: exchanges inside rows of 16 lanes by DPP (pairs,
+// quads, halves, rows), then the four rows' values.  The maximum is of non-negative values.
+template <int CTRL>
+__device__ __forceinline__ int row_exchange(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true); }
+
+__device__ __forceinline__ float wave_max_pos(float f) {
+    auto larger = [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); };
+    int v = __float_as_int(f);
+    v = larger(v, row_exchange<0xB1>(v));       // quad_perm [1, 0, 3, 2]
+    v = larger(v, row_exchange<0x4E>(v));       // quad_perm [2, 3, 0, 1]
+    v = larger(v, row_exchange<0x141>(v));      // row_half_mirror
+    v = larger(v, row_exchange<0x140>(v));      // row_mirror
+    return __int_as_float(larger(larger(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+                                 larger(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48))));
+}
+
+__device__ __forceinline__ int wave_sum_rows(int v) {
+    v += row_exchange<0xB1>(v);
+    v += row_exchange<0x4E>(v);
+    v += row_exchange<0x141>(v);
+    v += row_exchange<0x140>(v);
+    return __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) + __builtin_amdgcn_readlane(v, 32) +
+           __builtin_amdgcn_readlane(v, 48);
 }
 
 // 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.  What is left

@@ -13,6 +13,8 @@
 //   * up to 64: k_gated_dec, the weight streams on the 16x16x64 int8 MFMA;
 //   * more: k_gated_gemm, LDS tiles on the 32x32x32 int8 MFMA;
 // the last two also in a form for any K % 4 == 0 and any alignment.
+#include <type_traits>
+
 #include "ffn.hpp"
 
 namespace bitlinear {
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const
         }
     }
     if (blockIdx.x == 0 && tid == 0) beta_out[0] = beta;
-    sum = wave_sum_i32(sum);
+    sum = wave_sum_rows(sum);
     if (lane == 0) red_i[wave] = sum;
     __syncthreads();
     int xsum = 0;
@@ -132,7 +134,7 @@ __global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const
         int mg = 0, mu = 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int tg = wave_sum_i32(sg[r]), tu = wave_sum_i32(su[r]);
+            const int tg = wave_sum_rows(sg[r]), tu = wave_sum_rows(su[r]);
             if (lane == r) {
                 mg = tg;
                 mu = tu;
@@ -142,14 +144,29 @@ __global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const
     }
 }
 
-template <int CPL>
-static hipError_t launch_gated_gemv_cpl(const GatedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s) {
-    constexpr int R = CPL <= 2 ? 4 / CPL : 1;
-    // about 2048 waves: 256 workgroups, since every one of them quantizes x
-    const int64_t pairs = (a.F + 2047) / 2048, waves = (a.F + pairs - 1) / pairs;
+template <int CPL, int R>
+static hipError_t launch_gated_gemv_r(const GatedArgs& a, const float* x, int8_t* xq, float* beta, int64_t pairs, hipStream_t s) {
+    const int64_t waves = (a.F + pairs - 1) / pairs;
     hipLaunchKernelGGL((k_gated_gemv<CPL, R>), dim3((unsigned)((waves + GV_WAVES - 1) / GV_WAVES)), dim3(64 * GV_WAVES), 0, s, a, x,
                        xq, beta, (int)pairs);
     return hipGetLastError();
+}
+
+// About 2048 waves: 256 workgroups, since every one of them quantizes x.  Rows of one chunk a lane: all of
+// a wave's rows at once if they are at most six (K = 4096, F = 11008, six pairs a wave: 8.0 against 8.4 us
+// in steps of four; K = 2048, F = 8192, four: 5.3 against 6.7 us with room for six).  Longer rows: two pairs
+// of two chunks, one of more (K = 8192, F = 28672: 23.6 against 24.1 us with three; K = 16384, F = 4096: 11.2
+// against 12.0 with two).
+template <int CPL>
+static hipError_t launch_gated_gemv_cpl(const GatedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s) {
+    const int64_t pairs = (a.F + 2047) / 2048;
+    if constexpr (CPL > 1) {
+        return launch_gated_gemv_r<CPL, CPL == 2 ? 2 : 1>(a, x, xq, beta, pairs, s);
+    } else {
+        if (pairs <= 2) return launch_gated_gemv_r<1, 2>(a, x, xq, beta, pairs, s);
+        if (pairs <= 4 || pairs > 6) return launch_gated_gemv_r<1, 4>(a, x, xq, beta, pairs, s);
+        return launch_gated_gemv_r<1, 6>(a, x, xq, beta, pairs, s);
+    }
 }
 
 bool gated_gemv_supports(const GatedArgs& a, const float* x) {

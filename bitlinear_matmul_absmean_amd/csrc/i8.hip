@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void k_i8_gemv(I8Args a) {
     int mine = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int t = wave_sum_i32(s[r]);
+        const int t = wave_sum_rows(s[r]);
         if (lane == r) mine = t;
     }
     const int64_t n = r0 + lane;
