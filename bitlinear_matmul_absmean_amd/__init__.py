@@ -448,13 +448,29 @@ def _rows(t, name):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got {len(shape)} dimensions")
     index = t.get_device()
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current device")
-    rows, cols = t.shape
-    return rows, cols, index
+    return shape[0], shape[1], index
+
+
+def _stream_on(stream, index):
+    """_stream for a call whose tensors are known to lie on the current device `index`."""
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else _stream(None)
+
+
+def _held(t, stream):
+    """A buffer that the binding allocated for the call alone: kept from being handed out again before
+    the work on an explicitly given stream is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 def _first(t, name):
@@ -476,9 +492,9 @@ def bitlinear_gated_forward(x, Wg_packed, alpha_g, Wu_packed, alpha_u, act, bias
     if h is None:
         h = torch.empty((M, F), dtype=torch.float32, device=dev)
     if x_q is None:
-        x_q = torch.empty((M, K), dtype=torch.int8, device=dev)
+        x_q = _held(torch.empty((M, K), dtype=torch.int8, device=dev), stream)
     if beta is None:
-        beta = torch.empty(M, dtype=torch.float32, device=dev)
+        beta = _held(torch.empty(M, dtype=torch.float32, device=dev), stream)
     f32, u8 = torch.float32, torch.uint8
     _check("bitlinear_gated_forward", lib.bitlinear_gated_forward(
         _shaped(x, f32, "x", (M, K), dev), M, K, _shaped(Wg_packed, u8, "Wg_packed", (F, K // 4), dev),
@@ -486,7 +502,7 @@ def bitlinear_gated_forward(x, Wg_packed, alpha_g, Wu_packed, alpha_u, act, bias
         _shaped(Wu_packed, u8, "Wu_packed", (F, K // 4), dev), _shaped(alpha_u, f32, "alpha_u", (1,), dev),
         _shaped(bias_u, f32, "bias_u", (F,), dev), F, int(act), _shaped(h, f32, "h", (M, F), dev),
         _shaped(g, f32, "g", (M, F), dev), _shaped(u, f32, "u", (M, F), dev),
-        _shaped(x_q, torch.int8, "x_q", (M, K), dev), _shaped(beta, f32, "beta", (M,), dev), _stream(stream)))
+        _shaped(x_q, torch.int8, "x_q", (M, K), dev), _shaped(beta, f32, "beta", (M,), dev), _stream_on(stream, dev)))
     return h
 
 
@@ -500,11 +516,11 @@ def bitlinear_gated_backward_workspace_size(M, K, F) -> int:
     return lib.bitlinear_gated_backward_workspace_size(M, K, F)
 
 
-def _workspace(workspace, need, index):
-    """Pointer and bytes of the given workspace, or of a new one of the bytes needed."""
+def _workspace(workspace, need, index, stream):
+    """The given workspace, or a new one of the bytes needed, its pointer and its bytes."""
     if workspace is None:
         torch = _torch()
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=index)
+        workspace = _held(torch.empty(max(need, 256), dtype=torch.uint8, device=index), stream)
     ptr = _dev(workspace, _torch().uint8, "workspace")
     if workspace.get_device() != index:
         raise ValueError(f"workspace must be on device {index}, got {workspace.device}")
@@ -522,12 +538,12 @@ def bitlinear_backward(dy, x_q, beta, W_packed, alpha, dx=None, dW=None, dbias=N
     if dx is None and dW is None and dbias is None:
         dx = torch.empty((M, K), dtype=f32, device=dev)
         dW = torch.empty((N, K), dtype=f32, device=dev)
-    workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_backward_workspace_size(M, K, N), dev)
+    workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_backward_workspace_size(M, K, N), dev, stream)
     _check("bitlinear_backward", lib.bitlinear_backward(
         _shaped(dy, f32, "dy", (M, N), dev), M, N, _shaped(x_q, torch.int8, "x_q", (M, K), dev),
         _shaped(beta, f32, "beta", (M,), dev), K, _shaped(W_packed, torch.uint8, "W_packed", (N, K // 4), dev),
         _shaped(alpha, f32, "alpha", (1,), dev), _shaped(dx, f32, "dx", (M, K), dev),
-        _shaped(dW, f32, "dW", (N, K), dev), _shaped(dbias, f32, "dbias", (N,), dev), ws, ws_bytes, _stream(stream)))
+        _shaped(dW, f32, "dW", (N, K), dev), _shaped(dbias, f32, "dbias", (N,), dev), ws, ws_bytes, _stream_on(stream, dev)))
     return dx, dW, dbias
 
 
@@ -545,7 +561,7 @@ def bitlinear_gated_backward(dh, g, u, x_q, beta, Wg_packed, alpha_g, Wu_packed,
         dx = torch.empty((M, K), dtype=f32, device=dev)
         dWg = torch.empty((F, K), dtype=f32, device=dev)
         dWu = torch.empty((F, K), dtype=f32, device=dev)
-    workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_gated_backward_workspace_size(M, K, F), dev)
+    workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_gated_backward_workspace_size(M, K, F), dev, stream)
     _check("bitlinear_gated_backward", lib.bitlinear_gated_backward(
         _shaped(dh, f32, "dh", (M, F), dev), _shaped(g, f32, "g", (M, F), dev), _shaped(u, f32, "u", (M, F), dev), M, F,
         _shaped(x_q, torch.int8, "x_q", (M, K), dev), _shaped(beta, f32, "beta", (M,), dev), K,
@@ -553,7 +569,7 @@ def bitlinear_gated_backward(dh, g, u, x_q, beta, Wg_packed, alpha_g, Wu_packed,
         _shaped(Wu_packed, u8, "Wu_packed", (F, K // 4), dev), _shaped(alpha_u, f32, "alpha_u", (1,), dev), int(act),
         _shaped(dx, f32, "dx", (M, K), dev), _shaped(dWg, f32, "dWg", (F, K), dev), _shaped(dWu, f32, "dWu", (F, K), dev),
         _shaped(dbias_g, f32, "dbias_g", (F,), dev), _shaped(dbias_u, f32, "dbias_u", (F,), dev), ws, ws_bytes,
-        _stream(stream)))
+        _stream_on(stream, dev)))
     return dx, dWg, dWu, dbias_g, dbias_u
 
 
@@ -567,7 +583,7 @@ def bitlinear_quantize_weights_i8(W, W_q=None, gamma=None, stream=None):
         gamma = torch.empty(N, dtype=torch.float32, device=dev)
     _check("bitlinear_quantize_weights_i8", lib.bitlinear_quantize_weights_i8(
         _shaped(W, torch.float32, "W", (N, K), dev), N, K, _shaped(W_q, torch.int8, "W_q", (N, K), dev),
-        _shaped(gamma, torch.float32, "gamma", (N,), dev), _stream(stream)))
+        _shaped(gamma, torch.float32, "gamma", (N,), dev), _stream_on(stream, dev)))
     return W_q, gamma
 
 
@@ -588,7 +604,7 @@ def bitlinear_forward_i8(x_q, beta, W_q, gamma, bias=None, y=None, acc=None, str
         _shaped(x_q, torch.int8, "x_q", (M, K), dev), _shaped(beta, f32, "beta", (M,), dev), M, K,
         _shaped(W_q, torch.int8, "W_q", (N, K), dev), _shaped(gamma, f32, "gamma", (N,), dev), N,
         _shaped(bias, f32, "bias", (N,), dev), _shaped(y, f32, "y", (M, N), dev),
-        _shaped(acc, torch.int32, "acc", (M, N), dev), _stream(stream)))
+        _shaped(acc, torch.int32, "acc", (M, N), dev), _stream_on(stream, dev)))
     return y if acc is None else (y, acc)
 
 

@@ -370,9 +370,17 @@ int bitlinear_gated_forward(const float* x, int64_t M, int64_t K, const uint8_t*
     return hip_status(launch_gated(a, stream));
 }
 
+// Sizes of the gradients: a panel of 128 rows of split gradients (or 256 columns of codes) along M or along
+// both projections' N is addressed with 32 bits.
+static int check_backward(int64_t M, int64_t K, int64_t N) {
+    const int st = check_sizes(M, K, N);
+    if (st) return st;
+    return M > BACKWARD_MAX_ROWS || N > BACKWARD_MAX_ROWS ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
+}
+
 // Workspace of a backward call for valid sizes, else 0.
 static size_t backward_bytes(int64_t M, int64_t K, int64_t N, bool gated) {
-    return check_sizes(M, K, N) == BITLINEAR_OK ? backward_workspace(M, K, N, gated) : 0;
+    return check_backward(M, K, N) == BITLINEAR_OK ? backward_workspace(M, K, N, gated) : 0;
 }
 
 size_t bitlinear_backward_workspace_size(int64_t M, int64_t K, int64_t N) { return backward_bytes(M, K, N, false); }
@@ -382,7 +390,7 @@ size_t bitlinear_gated_backward_workspace_size(int64_t M, int64_t K, int64_t F) 
 }
 
 static int run_backward(const BackwardArgs& a, size_t workspace_bytes, bool gated, hipStream_t stream) {
-    const int st = check_sizes(a.M, a.K, a.N);
+    const int st = check_backward(a.M, a.K, a.N);
     if (st) return st;
     if (!a.ws || workspace_bytes < backward_workspace(a.M, a.K, a.N, gated)) return BITLINEAR_ERR_WORKSPACE;
     if (!aligned(a.ws, 256)) return BITLINEAR_ERR_ALIGNMENT;

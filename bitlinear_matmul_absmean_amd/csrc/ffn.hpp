@@ -167,6 +167,8 @@ struct BackwardArgs {
     float *db0, *db1;              // [N] or null
     void* ws;
 };
+// Largest M and N: 512 bytes of a panel for each row of the sum, two projections, within 2^31 bytes.
+constexpr int64_t BACKWARD_MAX_ROWS = (int64_t)1 << 21;
 size_t backward_workspace(int64_t M, int64_t K, int64_t N, bool gated);
 hipError_t launch_backward(const BackwardArgs& a, hipStream_t s);
 

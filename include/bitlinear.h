@@ -387,8 +387,8 @@ int bitlinear_gated_forward(const float* x, int64_t M, int64_t K, const uint8_t*
  *   dbias     [N] fp32 or NULL.                                              (out)
  *   workspace >= bitlinear_backward_workspace_size(M, K, N) bytes, 256-byte aligned; scratch,
  *             one for each call that may overlap another.
- * K % 4 == 0; any alignment of the tensors.  At least one output is given; outputs must not
- * overlap inputs or each other.  Errors: INVALID_ARG, SHAPE, ALIGNMENT and WORKSPACE (the
+ * K % 4 == 0, M and N <= 2097152; any alignment of the tensors.  At least one output is given;
+ * outputs must not overlap inputs or each other.  Errors: INVALID_ARG, SHAPE, ALIGNMENT and WORKSPACE (the
  * workspace), HIP.
  */
 size_t bitlinear_backward_workspace_size(int64_t M, int64_t K, int64_t N);

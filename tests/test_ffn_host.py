@@ -45,14 +45,14 @@ def test_backward_refusals(bl):  # noqa: F811
     for k in ("M", "K", "N"):
         assert _call(f, BWD, ok, **{k: 0}) == bad and _call(f, BWD, ok, **{k: -4}) == bad
     assert _call(f, BWD, ok, dx=None, dw=None) == bad
-    for kw in (dict(K=62), dict(K=bl.BITLINEAR_MAX_K + 4), dict(M=1 << 31), dict(N=1 << 31), dict(M=1 << 30, N=1 << 30)):
+    for kw in (dict(K=62), dict(K=bl.BITLINEAR_MAX_K + 4), dict(M=(1 << 21) + 1), dict(N=(1 << 21) + 1), dict(M=1 << 21, N=1 << 21)):
         assert _call(f, BWD, ok, **kw) == bl.BITLINEAR_ERR_SHAPE, kw
     need = bl.bitlinear_backward_workspace_size(2, 64, 8)
     assert need > 0
     assert _call(f, BWD, ok, ws=None) == bl.BITLINEAR_ERR_WORKSPACE
     assert _call(f, BWD, ok, bytes=need - 1) == bl.BITLINEAR_ERR_WORKSPACE
     assert _call(f, BWD, ok, ws=A + 16) == bl.BITLINEAR_ERR_ALIGNMENT
-    for size in ((0, 64, 8), (2, 66, 8), (2, 64, -1), (1 << 31, 64, 8)):
+    for size in ((0, 64, 8), (2, 66, 8), (2, 64, -1), ((1 << 21) + 1, 64, 8)):
         assert bl.bitlinear_backward_workspace_size(*size) == 0
         assert bl.bitlinear_gated_backward_workspace_size(*size) == 0
 
@@ -73,6 +73,7 @@ def test_gated_backward_refusals(bl):  # noqa: F811
     assert _call(f, GBWD, ok, dx=None, dwg=None, dwu=None) == bad
     assert _call(f, GBWD, ok, act=0) == bad
     assert _call(f, GBWD, ok, K=66) == bl.BITLINEAR_ERR_SHAPE
+    assert _call(f, GBWD, ok, F=(1 << 21) + 1) == bl.BITLINEAR_ERR_SHAPE
     need = bl.bitlinear_gated_backward_workspace_size(2, 64, 8)
     assert _call(f, GBWD, ok, ws=None) == bl.BITLINEAR_ERR_WORKSPACE
     assert _call(f, GBWD, ok, bytes=need - 1) == bl.BITLINEAR_ERR_WORKSPACE

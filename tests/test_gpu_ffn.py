@@ -481,3 +481,53 @@ def test_served_block_with_an_8bit_down_projection(dev):
     assert np.array_equal(_np(y), ref)
     for i in (0, 7, 19):
         assert torch.equal(serve(st["x"][i:i + 1].contiguous())[0], y[i])
+
+
+def test_explicit_stream_and_the_bindings_own_buffers(dev):
+    """Calls on a given stream that is not the current one, codes, scales and workspace left to the
+    binding, while the current stream allocates and overwrites memory all the time."""
+    torch, bl = dev
+    s = _step_state(torch, bl, 96, 512, 700, 41)
+    want = [t.clone() for t in _step(torch, bl, s)]
+    h_want, dx_want, dwd_want = want[0], want[4], want[3]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for rep in range(5):
+        h = bl.bitlinear_gated_forward(s["x"], s["Wg"], s["ag"], s["Wu"], s["au"], s["act"], stream=side)
+        dx, dwg, dwu, _, _ = bl.bitlinear_gated_backward(s["dh"], s["g"], s["u"], s["x_q"], s["beta"], s["Wg"], s["ag"],
+                                                         s["Wu"], s["au"], s["act"], stream=side)
+        _, dwd, _ = bl.bitlinear_backward(s["dy"], s["h_q"], s["hbeta"], s["Wd"], s["ad"], stream=side)
+        for _ in range(8):
+            torch.full((3 << 20,), 255, dtype=torch.uint8, device="cuda")
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(h, h_want) and torch.equal(dx, dx_want) and torch.equal(dwd, dwd_want)
+        assert torch.equal(dwg, want[5]) and torch.equal(dwu, want[6])
+
+
+def test_arguments_are_checked(dev):
+    """Wrong dtypes, shapes, layouts and buffers are refused in Python, before any launch."""
+    torch, bl = dev
+    s = _step_state(torch, bl, 4, 64, 32, 42)
+    fwd = lambda **kw: bl.bitlinear_gated_forward(**{**dict(x=s["x"], Wg_packed=s["Wg"], alpha_g=s["ag"], Wu_packed=s["Wu"],
+                                                            alpha_u=s["au"], act=s["act"]), **kw})
+    for kw in (dict(x=s["x"].double()), dict(x=s["x"].t()), dict(x=s["x"][0]), dict(Wu_packed=s["Wd"]), dict(h=s["y"]),
+               dict(alpha_g=s["beta"]), dict(bias_g=s["beta"]), dict(x_q=s["h_q"]), dict(x=s["x"].cpu()),
+               dict(Wg_packed=s["Wg"].cpu())):
+        with pytest.raises(ValueError):
+            fwd(**kw)
+    for kw in (dict(act=0), dict(g=s["g"])):
+        with pytest.raises(bl.BitLinearError):
+            fwd(**kw)
+    bwd = lambda **kw: bl.bitlinear_backward(**{**dict(dy=s["dy"], x_q=s["h_q"], beta=s["hbeta"], W_packed=s["Wd"],
+                                                       alpha=s["ad"]), **kw})
+    for kw in (dict(x_q=s["x_q"]), dict(dx=s["dx"]), dict(dW=s["dWg"]), dict(dbias=s["hbeta"]), dict(beta=s["ad"]),
+               dict(workspace=s["y"]), dict(dy=s["dy"].to(torch.bfloat16))):
+        with pytest.raises(ValueError):
+            bwd(**kw)
+    with pytest.raises(bl.BitLinearError):
+        bwd(workspace=s["ws1"][:256])
+    i8 = dict(x_q=s["x_q"], beta=s["beta"], W_q=s["x_q"], gamma=s["beta"])
+    for kw in (dict(W_q=s["h_q"]), dict(gamma=s["ad"]), dict(y=s["dy"]), dict(acc=s["dy"]), dict(bias=s["ad"])):
+        with pytest.raises(ValueError):
+            bl.bitlinear_forward_i8(**{**i8, **kw})
