@@ -78,11 +78,17 @@ def _gradients(d, ws, alphas, x_q, beta):
     return [dx] + dws + dbs, [dx2] + dws2 + dbs2
 
 
-def gradient_tolerance(terms, length):
+def gradient_tolerance(terms, length, total=0.0):
     """Bound on a gradient's error.  A term carries at most 24 half units: a few fp32 roundings of
     a(g), a'(g) and the products that form d (12), the factor alpha or beta / 127 (2), and the 22
     significant bits it is multiplied with (2^-22 = 4).  Each of the `length` additions rounds a
     partial sum by one unit at most (2 half units, whatever the rounding of the matrix cores'
     additions); partial sums stay below about four root sums of squares, and the errors, being
-    independent, add as their squares: 2 * 4 * sqrt(length)."""
-    return U * (24 + 8 * math.sqrt(length)) * terms
+    independent, add as their squares: 2 * 4 * sqrt(length).
+
+    That holds for terms of either sign.  Where they share one (a gradient that follows its input),
+    the sum `total` is many root sums of squares, and the partial sum after l of L terms lies near
+    total l / L besides: the rounding errors' squares then add up to
+    sum_l (2 U total l / L)^2 = 4 U^2 total^2 L / 3, their root 2 U |total| sqrt(L / 3); and the terms'
+    own roundings, independent too, stay inside 24 U times the root sum of squares."""
+    return U * ((24 + 8 * math.sqrt(length)) * terms + 2 * math.sqrt(length / 3) * np.abs(total))

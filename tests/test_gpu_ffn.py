@@ -531,3 +531,39 @@ def test_arguments_are_checked(dev):
     for kw in (dict(W_q=s["h_q"]), dict(gamma=s["ad"]), dict(y=s["dy"]), dict(acc=s["dy"]), dict(bias=s["ad"])):
         with pytest.raises(ValueError):
             bl.bitlinear_forward_i8(**{**i8, **kw})
+
+
+def test_outputs_past_32_bit_offsets(dev):
+    """Outputs and gradients of more than 2^31 elements: the last rows equal those of a small call, the
+    first ones too, and dW over all the tokens agrees with a 64-bit sum."""
+    torch, bl = dev
+    rng = np.random.default_rng(50)
+    m, k, f = 196000, 64, 11008
+    _say(f"gated_forward M={m} K={k} F={f}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(50)
+    x = torch.randn(m, k, device="cuda", generator=gen)
+    wg, wu = (_t(torch, plain.pack(plain.ternary(rng, f, k))) for _ in range(2))
+    al = _t(torch, _f32([0.05]))
+    h = bl.bitlinear_gated_forward(x, wg, al, wu, al, bl.BITLINEAR_ACT_SILU)
+    assert h.numel() > 1 << 31
+    for rows in (slice(0, 5), slice(m - 5, m)):
+        assert torch.equal(h[rows], bl.bitlinear_gated_forward(x[rows].contiguous(), wg, al, wu, al, bl.BITLINEAR_ACT_SILU))
+    _say("forward_i8")
+    x_q, beta = bl.bitlinear_quantize_act(x)
+    w_q, gamma = bl.bitlinear_quantize_weights_i8(torch.randn(f, k, device="cuda", generator=gen))
+    y = bl.bitlinear_forward_i8(x_q, beta, w_q, gamma, y=h)
+    for rows in (slice(0, 5), slice(m - 5, m)):
+        assert torch.equal(y[rows], bl.bitlinear_forward_i8(x_q[rows].contiguous(), beta[rows].contiguous(), w_q, gamma))
+    _say("backward")
+    dx, dw, _ = bl.bitlinear_backward(y, x_q, beta, wg, al)
+    w = (((_np(wg)[:, :, None] >> np.array([0, 2, 4, 6])) & 3).astype(np.int8) - 1).reshape(f, -1)
+    for rows in (slice(0, 3), slice(m - 3, m)):
+        want, terms = plain.linear_gradients(_np(y[rows]), _np(x_q[rows]), _np(beta[rows]), w, float(al[0]))
+        assert np.all(np.abs(_np(dx[rows]) - want[0]) <= plain.gradient_tolerance(terms[0], f))
+    xd = x_q.double() * (beta.double() / 127)[:, None]
+    for n in (0, f - 1):
+        d = y[:, n].double()
+        want, terms = _np(d @ xd), np.sqrt(_np((d * d) @ (xd * xd)))
+        # y follows x: the sums are a hundred root sums of squares
+        assert np.all(np.abs(_np(dw[n]) - want) <= plain.gradient_tolerance(terms, m, want))
