@@ -268,36 +268,42 @@ __device__ __forceinline__ uint32_t row_dword(const uint8_t* __restrict__ p, int
     return v;
 }
 
-// Bytes of a 64-row tile, transposed: column c of row r at lds[c * 80 + r] (80: the 16-byte reads of
-// neighbouring columns spread over the banks).  A thread writes the four columns of a dword.
-__device__ __forceinline__ void put_column_bytes(uint8_t* lds, int r, int c, uint32_t v) {
+// A 64 x 64 byte tile, transposed through LDS.  Thread t holds dword t % 16 (four columns) of rows
+// 4 (t / 16) .. 4 (t / 16) + 3, turns the 4 x 4 bytes round in registers and writes four columns' dwords
+// (a column is 17 dwords, so that the lanes of a write and of a read spread over the banks); it gets back
+// sixteen rows of one column, rows 16 (t % 4) .. of column t / 4.
+__device__ __forceinline__ u32x4 turn_tile(uint32_t* lds, u32x4 rows) {
+    const u32x4 cols = transpose4x4_perm(rows);
+    const int c = 4 * (threadIdx.x & 15), r4 = threadIdx.x >> 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) lds[(c + j) * 80 + r] = (uint8_t)(v >> (8 * j));
+    for (int j = 0; j < 4; ++j) lds[(c + j) * 17 + r4] = cols[j];
+    __syncthreads();
+    const uint32_t* p = lds + (threadIdx.x >> 2) * 17 + 4 * (threadIdx.x & 3);
+    return u32x4{p[0], p[1], p[2], p[3]};
 }
 
 // Panels of W_hat^T, 64 weight rows x 256 columns k per workgroup: a lane expands the codes 0, 1, 2 of
 // sixteen rows at four columns to the bytes 127, 128, 129.
-__device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint8_t* lds) {
+__device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint32_t* lds) {
     const int64_t k0 = b % kt * 256, l0 = b / kt * 64;
     const int q = l0 >= p.Np;
     const int64_t n0 = l0 - q * p.Np, rowb = a.K >> 2;
     const uint8_t* w = q ? a.w1 : a.w0;
-    // thread t: dword t % 16 of rows t / 16 + 16 i, its four loads under way together
-    const int c4 = 4 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
-    const int64_t at = (k0 >> 2) + c4;
-    uint32_t d[4];
+    const int64_t r0 = n0 + 4 * (threadIdx.x >> 4), at = (k0 >> 2) + 4 * (threadIdx.x & 15);
+    u32x4 d;
     if (n0 + 64 <= a.N && (k0 >> 2) + 64 <= rowb) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) __builtin_memcpy(&d[i], w + (n0 + r0 + 16 * i) * rowb + at, 4);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v;
+            __builtin_memcpy(&v, w + (r0 + i) * rowb + at, 4);
+            d[i] = v;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = n0 + r0 + 16 * i < a.N ? row_dword(w + (n0 + r0 + 16 * i) * rowb, at, rowb) : 0x55555555u;
+        for (int i = 0; i < 4; ++i) d[i] = r0 + i < a.N ? row_dword(w + (r0 + i) * rowb, at, rowb) : 0x55555555u;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) put_column_bytes(lds, r0 + 16 * i, c4, d[i]);
-    __syncthreads();
+    const u32x4 v = turn_tile(lds, d);
     const int u = threadIdx.x & 3, c = threadIdx.x >> 2;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + c * 80 + 16 * u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const u32x4 o = ((v >> (uint32_t)(2 * i)) & 0x03030303u) + 0x7F7F7F7Fu;
@@ -306,23 +312,24 @@ __device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPl
 }
 
 // Panels of x_q^T, 64 tokens x 64 columns per workgroup.
-__device__ __forceinline__ void codes_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint8_t* lds) {
+__device__ __forceinline__ void codes_tile(const BackwardArgs& a, const GradPlan& p, int64_t b, int64_t kt, uint32_t* lds) {
     const int64_t k0 = b % kt * 64, m0 = b / kt * 64;
-    const int c4 = 4 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
     const uint8_t* x = reinterpret_cast<const uint8_t*>(a.xq);
-    uint32_t d[4];
+    const int64_t r0 = m0 + 4 * (threadIdx.x >> 4), at = k0 + 4 * (threadIdx.x & 15);
+    u32x4 d;
     if (m0 + 64 <= a.M && k0 + 64 <= a.K) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) __builtin_memcpy(&d[i], x + (m0 + r0 + 16 * i) * a.K + k0 + c4, 4);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v;
+            __builtin_memcpy(&v, x + (r0 + i) * a.K + at, 4);
+            d[i] = v;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = m0 + r0 + 16 * i < a.M ? row_dword(x + (m0 + r0 + 16 * i) * a.K, k0 + c4, a.K) : 0u;
+        for (int i = 0; i < 4; ++i) d[i] = r0 + i < a.M ? row_dword(x + (r0 + i) * a.K, at, a.K) : 0u;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) put_column_bytes(lds, r0 + 16 * i, c4, d[i]);
-    __syncthreads();
+    const u32x4 v = turn_tile(lds, d);
     const int u = threadIdx.x & 3, c = threadIdx.x >> 2;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + c * 80 + 16 * u);
     reinterpret_cast<u32x4*>(p.cd)[code_unit(k0 + c, m0 + 16 * u, p.Mp)] = v ^ 0x80808080u;
 }
 
@@ -333,8 +340,8 @@ __global__ __launch_bounds__(256) void k_grad_prep(BackwardArgs a, GradPlan p, i
     __shared__ __align__(16) uint8_t lds[4 * P * 256 * 12];
     const int64_t b = blockIdx.x;
     if (b < maxima) max_tile<ACT, C>(a, p, b, lds);
-    else if (b < maxima + weights) weights_tile(a, p, b - maxima, ktw, lds);
-    else codes_tile(a, p, b - maxima - weights, ktc, lds);
+    else if (b < maxima + weights) weights_tile(a, p, b - maxima, ktw, reinterpret_cast<uint32_t*>(lds));
+    else codes_tile(a, p, b - maxima - weights, ktc, reinterpret_cast<uint32_t*>(lds));
 }
 
 // ---- step 2 (more than one tile of tokens): columns (a thread each), then rows (a wave each) ----
