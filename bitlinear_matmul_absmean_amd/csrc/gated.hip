@@ -48,6 +48,9 @@ __device__ __forceinline__ void gated_store(const GatedArgs& a, int64_t at, int6
 // load is 64 codes of a row (16 bytes); the matching x_q lies in LDS transposed 4 x 4 in each group
 // of 16, so that a masked dword of codes meets its four fields' x_q in v_dot4 (chunk_sum).
 // CPL: chunks of 64 weights per lane and row.
+// Bound: the weight stream on large layers (K = 8192, F = 28672: 23.0 us, 5.1 TB/s), a launch and one round
+// of loads on small ones (K = 4096, F = 11008: 8.0 us, 2.8 TB/s, six pairs of rows a wave; two BitLinear
+// calls and a product would take 11).
 constexpr int GV_WAVES = 8;
 
 template <int CPL, int R>
@@ -192,6 +195,11 @@ hipError_t launch_gated_gemv(const GatedArgs& a, const float* x, int8_t* xq, flo
 // past the registers; a step's image is read into registers, the next step's loads are started into
 // it, and the MFMAs run while they are in flight.  Token T's 16-byte unit u of a step lies at position
 // u ^ (T % 16) of its sixteen.  Otherwise operands are read straight into registers.
+// Bound: beside the weights every workgroup reads its tokens' x_q, as many bytes at 16 tokens and 16 columns
+// as twice the weights (from L2), and loads reach a compute unit at about 28 bytes a cycle: M = 16, K = 8192,
+// F = 28672: 38 us with quantize_act (117 MB of codes from HBM, 235 MB of x_q from L2), 29 at two tokens.
+// Workgroups that stay and keep x_q in registers measured 35 us there, but 16 against 12.8 us at K = 4096,
+// F = 11008, and are not kept.
 // 16x16x64 lane layout: A/B lane l holds row/column l % 16, k = 16 (l / 16) + j; accumulator r of
 // lane l is row 4 (l / 16) + r, column l % 16.
 constexpr int GD_WAVES = 8;
@@ -382,6 +390,8 @@ static hipError_t launch_gated_dec(const GatedArgs& a, hipStream_t s) {
 // ahead by loads that go past the registers (aligned rows: 16-byte aligned tensors, K % 64 == 0), or two filled through
 // registers.  Unit u of token row r lies at slot u ^ ((r / 2) % 8), unit u of weight row r at slot
 // u ^ ((r / 8) % 2), so that an operand read spreads over all banks.
+// Bound: power.  M = 2048, K = 4096, F = 11008: 181 us, 2.04 POPS (a library's plain int8 product of 8192^3:
+// 2.04); the matrix cores are busy 47% of the cycles and the clock is down at 2.0 GHz.
 // In the two MFMAs of k 64 h .. 64 h + 63 (h = 0, 1) a lane group holds 32 codes, eight bytes of a
 // weight row: the lane's unit h, of which group lg uses dwords 2 lg and 2 lg + 1.
 constexpr int GG_BF = 128, GG_BK = 128;

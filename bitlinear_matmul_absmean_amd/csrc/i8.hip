@@ -34,6 +34,7 @@ __device__ __forceinline__ i32x4 load_16(const int8_t* __restrict__ p) { return 
 // A wave takes R weight rows, 1 KiB of each at a time, so that R loads of 16 bytes a lane are in
 // flight while the last ones meet x_q, which lies in LDS as it is, in whole units of 16 (zeros up to the
 // next KiB); what is left of K goes to lane 0.
+// Bound: the weight stream (K = 4096, N = 32000: 25 us, 5.2 TB/s from HBM).
 template <bool ALIGNED, int R>
 __global__ __launch_bounds__(256) void k_i8_gemv(I8Args a) {
     extern __shared__ i32x4 xs[];
@@ -115,6 +116,9 @@ __device__ __forceinline__ int unit_swizzle(int r) { return ((r >> 2) & 3) ^ (((
 // Aligned rows: each wave has a ring of D LDS images of a step (16-row blocks of 64 bytes a row), filled
 // by loads that go past the registers, D - 1 steps ahead; no wave waits for another.
 // Any K and alignment: operands straight into registers in the MFMA's layout.
+// Bound: the weight stream at 16 tokens (K = N = 8192: 14.9 us, 4.5 TB/s); beyond, every workgroup's own
+// reading of x_q, 100 MB from L2 beside 67 of weights at 48 tokens (19 us).  Steps of 128 k in pairs for
+// whole lines measured 6 to 15% slower.
 // 16x16x64 lane layout: A/B lane l holds row/column l % 16, k = 16 (l / 16) + j; accumulator r of
 // lane l is row 4 (l / 16) + r, column l % 16.
 constexpr int I8_WAVES = 8;
@@ -295,7 +299,11 @@ static hipError_t launch_i8_dec(const I8Args& a, hipStream_t s) {
 // A workgroup of eight waves computes 64 MI tokens x 256 channels, a wave 32 MI x 64 of them in 32 x 32
 // blocks, in steps of 128 k (rows of whole cache lines); three LDS stages (48 KiB each), filled two
 // steps ahead by loads that go past the registers (aligned rows), or two filled through registers.
-// Unit u (16 bytes) of row r lies at slot u ^ ((r / 2) % 8) of its eight.
+// Unit u (16 bytes) of row r lies at slot u ^ ((r / 2) % 8) of its eight: no bank conflicts.
+// Bound: power.  M = 2048, K = 11008, N = 4096: 91 us, 2.03 POPS (a library's plain int8 product of 8192^3:
+// 2.04); the matrix cores are busy 59% of the cycles and the clock is down at 1.8 GHz.  The same tile with a
+// step's loads and operand reads before its MFMAs took 108 us (38% busy, 2.15 GHz), through registers 114,
+// with four waves of 64 x 128 110 us.
 // 32x32x32 lane layout: A/B lane l holds row/column l % 32, k = 16 (l / 32) + j; accumulator r of
 // lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 constexpr int IG_BN = 256, IG_BK = 128;
