@@ -93,30 +93,45 @@ __device__ __forceinline__ int wave_sum_rows(int v) {
            __builtin_amdgcn_readlane(v, 48);
 }
 
-// 16 bytes at p + i of a row of `row` bytes, zeros past its end; no alignment is assumed.  What is left
-// of a row at its end comes as the row's last 16 bytes, shifted down.
+// 16 bytes at p, whatever its alignment.  DWORDS: from the aligned dwords that hold them (five, or four
+// when p is aligned: no dword is read that holds none of the bytes), for operands that lie off a dword's
+// boundary: there a load of 16 bytes takes several times as long.
+template <bool DWORDS = false>
+__device__ __forceinline__ u32x4 load_16(const uint8_t* __restrict__ p) {
+    u32x4 v;
+    if constexpr (!DWORDS) {
+        __builtin_memcpy(&v, p, 16);
+        return v;
+    } else {
+        const uint32_t off = (uint32_t)(uintptr_t)p & 3u;
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p - off);
+        __builtin_memcpy(&v, __builtin_assume_aligned(q, 4), 16);
+        const uint32_t last = q[off ? 4 : 3];
+        return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, off), __builtin_amdgcn_alignbyte(v.z, v.y, off),
+                     __builtin_amdgcn_alignbyte(v.w, v.z, off), __builtin_amdgcn_alignbyte(last, v.w, off)};
+    }
+}
+
+// 16 bytes at p + i (i a multiple of 16) of a row of `row` bytes, zeros past its end; no alignment is
+// assumed.  What is left of a row at its end comes as the row's last 16 bytes, shifted down by `n`.
+template <bool DWORDS = false>
 __device__ __forceinline__ u32x4 row_16(const uint8_t* __restrict__ p, int64_t i, int64_t row) {
     u32x4 v = {0u, 0u, 0u, 0u};
     if (i + 16 <= row) {
-        __builtin_memcpy(&v, p + i, 16);
+        v = load_16<DWORDS>(p + i);
     } else if (i < row) {
         if (row >= 16) {
-            unsigned __int128 t;
-            __builtin_memcpy(&t, p + row - 16, 16);
-            t >>= 8 * (int)(i + 16 - row);
-            v = __builtin_bit_cast(u32x4, t);
+            const u32x4 t = load_16<DWORDS>(p + row - 16);
+            const int n = 16 - (int)(row & 15);
+            const u32x4 a = n & 8 ? u32x4{t.z, t.w, 0u, 0u} : t;
+            const u32x4 b = n & 4 ? u32x4{a.y, a.z, a.w, 0u} : a;
+            v = u32x4{__builtin_amdgcn_alignbyte(b.y, b.x, n & 3), __builtin_amdgcn_alignbyte(b.z, b.y, n & 3),
+                      __builtin_amdgcn_alignbyte(b.w, b.z, n & 3), __builtin_amdgcn_alignbyte(0u, b.w, n & 3)};
         } else {
             for (int j = 0; j < 16; ++j)
                 if (i + j < row) v[j >> 2] |= (uint32_t)p[i + j] << (8 * (j & 3));
         }
     }
-    return v;
-}
-
-// 16 bytes at p, whatever its alignment.
-__device__ __forceinline__ u32x4 load_16(const uint8_t* __restrict__ p) {
-    u32x4 v;
-    __builtin_memcpy(&v, p, 16);
     return v;
 }
 

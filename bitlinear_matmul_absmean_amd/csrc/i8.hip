@@ -5,7 +5,8 @@
 // every step one fp32 rounding.
 //
 // Three kernels by the number of tokens, each in a form for aligned rows (16-byte aligned tensors,
-// K % 16 == 0) and one for any K and alignment:
+// K % 16 == 0) and one for any K and alignment, the last two also in one for rows off dword boundaries
+// (K = 4098, N = 4096, 48 tokens: 13.5 us against 30.3 without):
 //   * one token: k_i8_gemv, the weight stream against x_q in LDS, on v_dot4_i32_i8;
 //   * few tokens: k_i8_dec, the weight stream on the 16x16x64 int8 MFMA, the waves of a workgroup
 //     taking turns along K;
@@ -25,10 +26,17 @@ __device__ __forceinline__ void i8_store(const I8Args& a, int64_t at, int acc, f
     if (a.acc) a.acc[at] = acc;
 }
 
+template <bool DWORDS = false>
 __device__ __forceinline__ i32x4 row_16(const int8_t* __restrict__ p, int64_t i, int64_t row) {
-    return (i32x4)row_16(reinterpret_cast<const uint8_t*>(p), i, row);
+    return (i32x4)row_16<DWORDS>(reinterpret_cast<const uint8_t*>(p), i, row);
 }
-__device__ __forceinline__ i32x4 load_16(const int8_t* __restrict__ p) { return (i32x4)load_16(reinterpret_cast<const uint8_t*>(p)); }
+template <bool DWORDS = false>
+__device__ __forceinline__ i32x4 load_16(const int8_t* __restrict__ p) {
+    return (i32x4)load_16<DWORDS>(reinterpret_cast<const uint8_t*>(p));
+}
+
+// How the rows lie: 16-byte aligned (and K % 16 == 0), on dwords, or anywhere.
+constexpr int ROWS_16 = 16, ROWS_4 = 4, ROWS_1 = 1;
 
 // ---- one token ------------------------------------------------------------------------------
 // A wave takes R weight rows, 1 KiB of each at a time, so that R loads of 16 bytes a lane are in
@@ -123,8 +131,9 @@ __device__ __forceinline__ int unit_swizzle(int r) { return ((r >> 2) & 3) ^ (((
 // lane l is row 4 (l / 16) + r, column l % 16.
 constexpr int I8_WAVES = 8;
 
-template <bool ALIGNED, int MT, int RB>
+template <int ROWS, int MT, int RB>
 __global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) {
+    constexpr bool ALIGNED = ROWS == ROWS_16, DWORDS = ROWS == ROWS_1;
     constexpr int IMG = (RB + MT) * 64;
     constexpr int D = 3;                                           // images of a ring
     __shared__ i32x4 st0[I8_WAVES * IMG];
@@ -222,9 +231,9 @@ __global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) 
             const int64_t k = (int64_t)s * 64 + 16 * lg;
             Part f;
 #pragma unroll
-            for (int r = 0; r < RB; ++r) f.w[r] = load_16(wp[r] + k);
+            for (int r = 0; r < RB; ++r) f.w[r] = load_16<DWORDS>(wp[r] + k);
 #pragma unroll
-            for (int t = 0; t < MT; ++t) f.x[t] = load_16(xp[t] + k);
+            for (int t = 0; t < MT; ++t) f.x[t] = load_16<DWORDS>(xp[t] + k);
             return f;
         };
         // whole steps, the next one's loads under way; the last part step goes to the next wave in turn
@@ -240,9 +249,9 @@ __global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) 
         if (whole < steps && whole % I8_WAVES == wave) {
             const int64_t k = (int64_t)whole * 64 + 16 * lg;
 #pragma unroll
-            for (int r = 0; r < RB; ++r) f0.w[r] = row_16(wp[r], k, K);
+            for (int r = 0; r < RB; ++r) f0.w[r] = row_16<DWORDS>(wp[r], k, K);
 #pragma unroll
-            for (int t = 0; t < MT; ++t) f0.x[t] = row_16(xp[t], k, K);
+            for (int t = 0; t < MT; ++t) f0.x[t] = row_16<DWORDS>(xp[t], k, K);
             multiply(f0.x, f0.w);
         }
     }
@@ -269,30 +278,30 @@ __global__ __launch_bounds__(64 * I8_WAVES) void k_i8_dec(I8Args a, int slices) 
     }
 }
 
-template <bool ALIGNED, int MT, int RB>
+template <int ROWS, int MT, int RB>
 static hipError_t launch_i8_dec_rb(const I8Args& a, hipStream_t s) {
     const int64_t slices = (a.M + 16 * MT - 1) / (16 * MT), blocks = (a.N + 16 * RB - 1) / (16 * RB);
-    hipLaunchKernelGGL((k_i8_dec<ALIGNED, MT, RB>), dim3((unsigned)(slices * blocks)), dim3(64 * I8_WAVES), 0, s, a, (int)slices);
+    hipLaunchKernelGGL((k_i8_dec<ROWS, MT, RB>), dim3((unsigned)(slices * blocks)), dim3(64 * I8_WAVES), 0, s, a, (int)slices);
     return hipGetLastError();
 }
 
 // One block of 16 channels a workgroup; two where 48 or 64 tokens leave room for one workgroup per compute
 // unit only and there would be more than 256 (K = N = 4096, M = 48 (256 workgroups) 7.4 against 9.4 us with
 // two blocks; K = N = 8192, M = 48 (512) 26.7 against 20.9; M = 16 15.5 against 17.9 us).
-template <bool ALIGNED, int MT>
+template <int ROWS, int MT>
 static hipError_t launch_i8_dec_mt(const I8Args& a, hipStream_t s) {
     if constexpr (MT >= 3)
-        if ((a.M + 16 * MT - 1) / (16 * MT) * ((a.N + 15) / 16) > 256) return launch_i8_dec_rb<ALIGNED, MT, 2>(a, s);
-    return launch_i8_dec_rb<ALIGNED, MT, 1>(a, s);
+        if ((a.M + 16 * MT - 1) / (16 * MT) * ((a.N + 15) / 16) > 256) return launch_i8_dec_rb<ROWS, MT, 2>(a, s);
+    return launch_i8_dec_rb<ROWS, MT, 1>(a, s);
 }
 
-template <bool ALIGNED>
+template <int ROWS>
 static hipError_t launch_i8_dec(const I8Args& a, hipStream_t s) {
     const int64_t tiles = (a.M + 15) / 16;
-    return tiles == 1   ? launch_i8_dec_mt<ALIGNED, 1>(a, s)
-           : tiles == 2 ? launch_i8_dec_mt<ALIGNED, 2>(a, s)
-           : tiles == 3 ? launch_i8_dec_mt<ALIGNED, 3>(a, s)
-                        : launch_i8_dec_mt<ALIGNED, 4>(a, s);
+    return tiles == 1   ? launch_i8_dec_mt<ROWS, 1>(a, s)
+           : tiles == 2 ? launch_i8_dec_mt<ROWS, 2>(a, s)
+           : tiles == 3 ? launch_i8_dec_mt<ROWS, 3>(a, s)
+                        : launch_i8_dec_mt<ROWS, 4>(a, s);
 }
 
 // ---- many tokens ----------------------------------------------------------------------------
@@ -308,8 +317,9 @@ static hipError_t launch_i8_dec(const I8Args& a, hipStream_t s) {
 // lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 constexpr int IG_BN = 256, IG_BK = 128;
 
-template <bool ALIGNED, int MI>
+template <int ROWS, int MI>
 __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int tiles_n) {
+    constexpr bool ALIGNED = ROWS == ROWS_16, DWORDS = ROWS == ROWS_1;
     constexpr int IG_BM = 64 * MI, OB = IG_BM * 8, UNITS = OB + IG_BN * 8;
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
@@ -453,9 +463,9 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
             const int64_t k = (int64_t)s * IG_BK;
             Regs r;
 #pragma unroll
-            for (int q = 0; q < MI; ++q) r.v[q] = load_16(xp[q] + k + 16 * block_unit(MI * wave + q));
+            for (int q = 0; q < MI; ++q) r.v[q] = load_16<DWORDS>(xp[q] + k + 16 * block_unit(MI * wave + q));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) r.v[MI + q] = load_16(wp[q] + k + 16 * block_unit(4 * wave + q));
+            for (int q = 0; q < 4; ++q) r.v[MI + q] = load_16<DWORDS>(wp[q] + k + 16 * block_unit(4 * wave + q));
             return r;
         };
         auto put = [&](i32x4* st, const Regs& r) {
@@ -480,9 +490,9 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
             const int64_t k = (int64_t)whole * IG_BK;
             Regs r;
 #pragma unroll
-            for (int q = 0; q < MI; ++q) r.v[q] = row_16(xp[q], k + 16 * block_unit(MI * wave + q), K);
+            for (int q = 0; q < MI; ++q) r.v[q] = row_16<DWORDS>(xp[q], k + 16 * block_unit(MI * wave + q), K);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) r.v[MI + q] = row_16(wp[q], k + 16 * block_unit(4 * wave + q), K);
+            for (int q = 0; q < 4; ++q) r.v[MI + q] = row_16<DWORDS>(wp[q], k + 16 * block_unit(4 * wave + q), K);
             put(st0, r);
             __syncthreads();
             multiply_stage(st0);
@@ -521,35 +531,37 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
         }
 }
 
-template <bool ALIGNED, int MI>
+template <int ROWS, int MI>
 static hipError_t launch_i8_gemm_mi(const I8Args& a, hipStream_t s) {
     const int64_t tm = (a.M + 64 * MI - 1) / (64 * MI), tn = (a.N + IG_BN - 1) / IG_BN;
-    hipLaunchKernelGGL((k_i8_gemm<ALIGNED, MI>), dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, (int)tm, (int)tn);
+    hipLaunchKernelGGL((k_i8_gemm<ROWS, MI>), dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
 // 64-token tiles while they all run at once (256 slots): K = N = 4096, M = 128 (32 tiles of 64 x 256) 16.4
 // against 23.1 us, M = 1024 (256) 23.7 against 25.8; K = 4096, N = 11008, M = 512 (344) 51.7 against 33.6.
-template <bool ALIGNED>
+// Rows off dword boundaries are read dword by dword only there: with many tiles the plain loads' time is
+// hidden (M = 501, K = 1001, N = 1536 15.8 against 20.7 us; M = 2048, K = 4099, N = 4096 60.1 against 55.9).
+template <int ROWS>
 static hipError_t launch_i8_gemm(const I8Args& a, hipStream_t s) {
     const int64_t tiles = (a.M + 63) / 64 * ((a.N + IG_BN - 1) / IG_BN);
-    return tiles <= 256 ? launch_i8_gemm_mi<ALIGNED, 1>(a, s) : launch_i8_gemm_mi<ALIGNED, 2>(a, s);
+    return tiles <= 256 ? launch_i8_gemm_mi<ROWS, 1>(a, s) : launch_i8_gemm_mi<ROWS == ROWS_1 ? ROWS_4 : ROWS, 2>(a, s);
 }
 
 // The streaming kernel while the GEMM has at most 48 tiles of 64 x 256, too few to read the weights at
 // speed: K = N = 4096, M = 64 (16 tiles) 8.5 against 16.6 us, M = 128 (32) 11.7 against 16.4, M = 256 (64)
 // 20.2 against 16.7; K = 4096, N = 11008, M = 64 (43) 21.6 against 24.2; K = 4096, N = 32000, M = 16 (125)
 // 28.9 against 25.3 us.
-template <bool ALIGNED>
+template <int ROWS>
 static hipError_t launch_i8(const I8Args& a, hipStream_t s) {
-    if (a.M == 1) return launch_i8_gemv<ALIGNED>(a, s);
-    if ((a.M + 63) / 64 * ((a.N + IG_BN - 1) / IG_BN) <= 48) return launch_i8_dec<ALIGNED>(a, s);
-    return launch_i8_gemm<ALIGNED>(a, s);
+    if (a.M == 1) return launch_i8_gemv<ROWS == ROWS_16>(a, s);
+    if ((a.M + 63) / 64 * ((a.N + IG_BN - 1) / IG_BN) <= 48) return launch_i8_dec<ROWS>(a, s);
+    return launch_i8_gemm<ROWS>(a, s);
 }
 
 hipError_t launch_forward_i8(const I8Args& a, hipStream_t s) {
-    const bool aligned = a.K % 16 == 0 && (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.wq % 16 == 0;
-    return aligned ? launch_i8<true>(a, s) : launch_i8<false>(a, s);
+    const uintptr_t low = (uintptr_t)a.xq | (uintptr_t)a.wq | (uintptr_t)a.K;
+    return low % 16 == 0 ? launch_i8<ROWS_16>(a, s) : low % 4 == 0 ? launch_i8<ROWS_4>(a, s) : launch_i8<ROWS_1>(a, s);
 }
 
 }  // namespace bitlinear
