@@ -305,8 +305,8 @@ static hipError_t launch_i8_dec(const I8Args& a, hipStream_t s) {
 }
 
 // ---- many tokens ----------------------------------------------------------------------------
-// A workgroup of eight waves computes 64 MI tokens x 256 channels, a wave 32 MI x 64 of them in 32 x 32
-// blocks, in steps of 128 k (rows of whole cache lines); three LDS stages (48 KiB each), filled two
+// A workgroup of eight waves computes 64 MI tokens x 128 FN channels, a wave 32 MI x 32 FN of them in 32 x 32
+// blocks, in steps of 128 k (rows of whole cache lines); three LDS stages (up to 48 KiB each), filled two
 // steps ahead by loads that go past the registers (aligned rows), or two filled through registers.
 // Unit u (16 bytes) of row r lies at slot u ^ ((r / 2) % 8) of its eight: no bank conflicts.
 // Bound: power.  M = 2048, K = 11008, N = 4096: 91 us, 2.03 POPS (a library's plain int8 product of 8192^3:
@@ -315,12 +315,12 @@ static hipError_t launch_i8_dec(const I8Args& a, hipStream_t s) {
 // with four waves of 64 x 128 110 us.
 // 32x32x32 lane layout: A/B lane l holds row/column l % 32, k = 16 (l / 32) + j; accumulator r of
 // lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
-constexpr int IG_BN = 256, IG_BK = 128;
+constexpr int IG_BK = 128;
 
-template <int ROWS, int MI>
+template <int ROWS, int MI, int FN>
 __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int tiles_n) {
     constexpr bool ALIGNED = ROWS == ROWS_16, DWORDS = ROWS == ROWS_1;
-    constexpr int IG_BM = 64 * MI, OB = IG_BM * 8, UNITS = OB + IG_BN * 8;
+    constexpr int IG_BM = 64 * MI, IG_BN = 128 * FN, OB = IG_BM * 8, UNITS = OB + IG_BN * 8;
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
     __shared__ i32x4 st2[ALIGNED ? UNITS : 1];
@@ -338,30 +338,30 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
     const int8_t* x0 = a.xq + m0 * K;
     const int8_t* w0 = a.wq + n0 * K;
 
-    i32x16 acc[MI][2];
+    i32x16 acc[MI][FN];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
+        for (int j = 0; j < FN; ++j) acc[i][j] = i32x16{};
     const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
     // scales before the loop: the tokens' in LDS, the channels' in registers
     if (tid < IG_BM) bscale[tid] = tid < rows_m ? i8_scale(a.beta[m0 + tid]) : 0.0f;
-    float gs[2], bias[2];
+    float gs[FN], bias[FN];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t n = n0 + min(64 * wj + 32 * j + lr, rows_n - 1);
+    for (int j = 0; j < FN; ++j) {
+        const int64_t n = n0 + min(32 * FN * wj + 32 * j + lr, rows_n - 1);
         gs[j] = i8_scale(a.gamma[n]);
         bias[j] = a.bias ? a.bias[n] : 0.0f;
     }
     struct Frag {
-        i32x4 a[MI], b[2];
+        i32x4 a[MI], b[FN];
     };
     // operands of k 32 kk .. 32 kk + 31 of the step in stage st
     auto read = [&](const i32x4* st, int kk) {
         const int u = 2 * kk + lg, at = u ^ sw;
         Frag f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) f.b[j] = st[OB + (64 * wj + 32 * j + lr) * 8 + at];
+        for (int j = 0; j < FN; ++j) f.b[j] = st[OB + (32 * FN * wj + 32 * j + lr) * 8 + at];
 #pragma unroll
         for (int i = 0; i < MI; ++i) f.a[i] = st[(32 * MI * wi + 32 * i + lr) * 8 + at];
         return f;
@@ -370,23 +370,23 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < FN; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // load block q (8 rows): wave w takes MI w .. MI w + MI - 1 of x_q and 4 w .. 4 w + 3 of W_q
+    // load block q (8 rows): wave w takes MI w .. MI w + MI - 1 of x_q and 2 FN w .. 2 FN w + 2 FN - 1 of W_q
     auto block_row = [&](int q) { return 8 * q + (lane >> 3); };
     auto block_unit = [&](int q) { return (lane & 7) ^ ((block_row(q) >> 1) & 7); };
     if constexpr (ALIGNED) {
         const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
         const __amdgpu_buffer_rsrc_t rw = raw_buffer(w0, (uint32_t)rows_n * (uint32_t)K);
-        uint32_t xo[MI], wo[4];
+        uint32_t xo[MI], wo[2 * FN];
 #pragma unroll
         for (int q = 0; q < MI; ++q)
             xo[q] = (uint32_t)min(block_row(MI * wave + q), rows_m - 1) * (uint32_t)K + 16u * block_unit(MI * wave + q);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            wo[q] = (uint32_t)min(block_row(4 * wave + q), rows_n - 1) * (uint32_t)K + 16u * block_unit(4 * wave + q);
+        for (int q = 0; q < 2 * FN; ++q)
+            wo[q] = (uint32_t)min(block_row(2 * FN * wave + q), rows_n - 1) * (uint32_t)K + 16u * block_unit(2 * FN * wave + q);
         // a third of a step's loads
         auto fetch = [&](i32x4* st, int s, int third) {
             const uint32_t so = (uint32_t)s * IG_BK;
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
                 for (int q = 0; q < MI; ++q) load_lds16(rx, xo[q], so, st + 64 * (MI * wave + q));
             } else {
 #pragma unroll
-                for (int q = 2 * third - 2; q < 2 * third; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (4 * wave + q));
+                for (int q = FN * (third - 1); q < FN * third; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (2 * FN * wave + q));
             }
         };
         // Step s in stage `cur`, its first operands in f0.  Operands are read one part ahead of their
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
             f1 = read(cur, 3);
             multiply(f0);
             // step s + 1 has landed for every wave, and every wave holds the rest of step s in registers
-            __builtin_amdgcn_s_waitcnt(0x0070 | (MI + 4)); // vmcnt(the loads of step s + 2) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(0x0070 | (MI + 2 * FN)); // vmcnt(the loads of step s + 2) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             f0 = read(nxt, 0);
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
 #pragma unroll
             for (int q = 0; q < 3; ++q) fetch(st1, min(1, last), q);
             fetch(st2, min(2, last), 0);
-            __builtin_amdgcn_s_waitcnt(0x0070 | (2 * MI + 4)); // vmcnt(the loads after step 0's) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(0x0070 | (2 * MI + 2 * FN)); // vmcnt(the loads after step 0's) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             Frag f = read(st0, 0);
             int s = 0;
@@ -447,17 +447,17 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
 #pragma unroll
             for (int i = 0; i < MI; ++i) f.a[i] = row_16(x0 + (int64_t)min(32 * MI * wi + 32 * i + lr, rows_m - 1) * K, k + 16 * lg, K);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) f.b[j] = row_16(w0 + (int64_t)min(64 * wj + 32 * j + lr, rows_n - 1) * K, k + 16 * lg, K);
+            for (int j = 0; j < FN; ++j) f.b[j] = row_16(w0 + (int64_t)min(32 * FN * wj + 32 * j + lr, rows_n - 1) * K, k + 16 * lg, K);
             multiply(f);
         }
     } else {
-        const int8_t *xp[MI], *wp[4];
+        const int8_t *xp[MI], *wp[2 * FN];
 #pragma unroll
         for (int q = 0; q < MI; ++q) xp[q] = x0 + (int64_t)min(block_row(MI * wave + q), rows_m - 1) * K;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) wp[q] = w0 + (int64_t)min(block_row(4 * wave + q), rows_n - 1) * K;
+        for (int q = 0; q < 2 * FN; ++q) wp[q] = w0 + (int64_t)min(block_row(2 * FN * wave + q), rows_n - 1) * K;
         struct Regs {
-            i32x4 v[MI + 4];
+            i32x4 v[MI + 2 * FN];
         };
         auto load = [&](int s) {
             const int64_t k = (int64_t)s * IG_BK;
@@ -465,14 +465,14 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
 #pragma unroll
             for (int q = 0; q < MI; ++q) r.v[q] = load_16<DWORDS>(xp[q] + k + 16 * block_unit(MI * wave + q));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) r.v[MI + q] = load_16<DWORDS>(wp[q] + k + 16 * block_unit(4 * wave + q));
+            for (int q = 0; q < 2 * FN; ++q) r.v[MI + q] = load_16<DWORDS>(wp[q] + k + 16 * block_unit(2 * FN * wave + q));
             return r;
         };
         auto put = [&](i32x4* st, const Regs& r) {
 #pragma unroll
             for (int q = 0; q < MI; ++q) st[64 * (MI * wave + q) + lane] = r.v[q];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) st[OB + 64 * (4 * wave + q) + lane] = r.v[MI + q];
+            for (int q = 0; q < 2 * FN; ++q) st[OB + 64 * (2 * FN * wave + q) + lane] = r.v[MI + q];
         };
         auto multiply_stage = [&](const i32x4* st) {
 #pragma unroll
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
 #pragma unroll
             for (int q = 0; q < MI; ++q) r.v[q] = row_16<DWORDS>(xp[q], k + 16 * block_unit(MI * wave + q), K);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) r.v[MI + q] = row_16<DWORDS>(wp[q], k + 16 * block_unit(4 * wave + q), K);
+            for (int q = 0; q < 2 * FN; ++q) r.v[MI + q] = row_16<DWORDS>(wp[q], k + 16 * block_unit(2 * FN * wave + q), K);
             put(st0, r);
             __syncthreads();
             multiply_stage(st0);
@@ -519,43 +519,52 @@ __global__ __launch_bounds__(512, 2) void k_i8_gemm(I8Args a, int tiles_m, int t
             const int m = 32 * MI * wi + 32 * i + 8 * q + 4 * lg;
             const float4 bs4 = *reinterpret_cast<const float4*>(&bscale[m]);
             const float bs[4] = {bs4.x, bs4.y, bs4.z, bs4.w};
-            const int64_t at = (m0 + m) * a.N + n0 + 64 * wj + lr;
+            const int64_t at = (m0 + m) * a.N + n0 + 32 * FN * wj + lr;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (m + e >= rows_m) break;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (64 * wj + 32 * j + lr < rows_n)
+                for (int j = 0; j < FN; ++j)
+                    if (32 * FN * wj + 32 * j + lr < rows_n)
                         i8_store(a, at + e * a.N + 32 * j, acc[i][j][4 * q + e], bs[e], gs[j], bias[j]);
             }
         }
 }
 
-template <int ROWS, int MI>
-static hipError_t launch_i8_gemm_mi(const I8Args& a, hipStream_t s) {
-    const int64_t tm = (a.M + 64 * MI - 1) / (64 * MI), tn = (a.N + IG_BN - 1) / IG_BN;
-    hipLaunchKernelGGL((k_i8_gemm<ROWS, MI>), dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, (int)tm, (int)tn);
+template <int ROWS, int MI, int FN>
+static hipError_t launch_i8_gemm_tile(const I8Args& a, hipStream_t s) {
+    const int64_t tm = (a.M + 64 * MI - 1) / (64 * MI), tn = (a.N + 128 * FN - 1) / (128 * FN);
+    hipLaunchKernelGGL((k_i8_gemm<ROWS, MI, FN>), dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
-// 64-token tiles while they all run at once (256 slots): K = N = 4096, M = 128 (32 tiles of 64 x 256) 16.4
-// against 23.1 us, M = 1024 (256) 23.7 against 25.8; K = 4096, N = 11008, M = 512 (344) 51.7 against 33.6.
-// Rows off dword boundaries are read dword by dword only there: with many tiles the plain loads' time is
-// hidden (M = 501, K = 1001, N = 1536 15.8 against 20.7 us; M = 2048, K = 4099, N = 4096 60.1 against 55.9).
+// Tiles of 64 x 256: what the choices below count.
+static int64_t i8_tiles(const I8Args& a) { return (a.M + 63) / 64 * ((a.N + 255) / 256); }
+
+// The largest tile whose workgroups still fill the card.  64 x 128 while 64 x 256 makes at most 128 tiles, so
+// that twice as many still run at once: K = N = 4096, M = 256 (64 tiles) 12.2 against 16.6 us, M = 512 (128)
+// 15.5 against 18.1; K = 4096, N = 11008, M = 256 (172) 30.9 against 26.9.  64 x 256 while those run at once
+// (256 slots): K = N = 4096, M = 1024 (256) 23.7 against 25.8 us with 128 x 256; K = 4096, N = 11008, M = 512
+// (344) 51.7 against 33.6.
+// Rows off dword boundaries are read dword by dword only in 64-token tiles: with many tiles the plain loads'
+// time is hidden (64 x 256, M = 501, K = 1001, N = 1536 15.8 against 20.7 us; 128 x 256, M = 2048, K = 4099,
+// N = 4096 60.1 against 55.9).
 template <int ROWS>
 static hipError_t launch_i8_gemm(const I8Args& a, hipStream_t s) {
-    const int64_t tiles = (a.M + 63) / 64 * ((a.N + IG_BN - 1) / IG_BN);
-    return tiles <= 256 ? launch_i8_gemm_mi<ROWS, 1>(a, s) : launch_i8_gemm_mi<ROWS == ROWS_1 ? ROWS_4 : ROWS, 2>(a, s);
+    const int64_t tiles = i8_tiles(a);
+    if (tiles <= 128) return launch_i8_gemm_tile<ROWS, 1, 1>(a, s);
+    if (tiles <= 256) return launch_i8_gemm_tile<ROWS, 1, 2>(a, s);
+    return launch_i8_gemm_tile<ROWS == ROWS_1 ? ROWS_4 : ROWS, 2, 2>(a, s);
 }
 
-// The streaming kernel while the GEMM has at most 48 tiles of 64 x 256, too few to read the weights at
-// speed: K = N = 4096, M = 64 (16 tiles) 8.5 against 16.6 us, M = 128 (32) 11.7 against 16.4, M = 256 (64)
-// 20.2 against 16.7; K = 4096, N = 11008, M = 64 (43) 21.6 against 24.2; K = 4096, N = 32000, M = 16 (125)
-// 28.9 against 25.3 us.
+// The streaming kernel while 64 x 256 makes at most 32 tiles, too few to read the weights at speed (against
+// 64 x 128): K = N = 4096, M = 64 (16 tiles) 8.5 against 11.9 us, M = 128 (32) 11.7 against 12.1, M = 256 (64)
+// 20.0 against 12.2; K = N = 8192, M = 64 (32) 23.3 against 30.1; K = 4096, N = 11008, M = 64 (43) 22.1 against
+// 17.1; K = 4096, N = 32000, M = 16 (125) 26.4 against 21.5 us.
 template <int ROWS>
 static hipError_t launch_i8(const I8Args& a, hipStream_t s) {
     if (a.M == 1) return launch_i8_gemv<ROWS == ROWS_16>(a, s);
-    if ((a.M + 63) / 64 * ((a.N + IG_BN - 1) / IG_BN) <= 48) return launch_i8_dec<ROWS>(a, s);
+    if (i8_tiles(a) <= 32) return launch_i8_dec<ROWS>(a, s);
     return launch_i8_gemm<ROWS>(a, s);
 }
 

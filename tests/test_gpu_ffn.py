@@ -336,6 +336,29 @@ def test_forward_i8(dev, m, k, n):
     assert torch.equal(y, y2)
 
 
+# (M, N): 36, 144 and 288 tiles of 64 x 256, the last of a row and of a column partial
+@pytest.mark.parametrize("m,n", [(515, 901), (1089, 2017), (1473, 2950)])
+@pytest.mark.parametrize("k", [1, 15, 16, 127, 128, 129, 130, 132, 260, 384, 400, 1001])
+def test_forward_i8_many_tiles(dev, m, n, k):
+    """K below, at and past the steps of 128, in rows on 16-byte and dword boundaries and off them."""
+    torch, bl = dev
+    _say(f"forward_i8 many tiles M={m} K={k} N={n}")
+    rng = np.random.default_rng([12, m, k, n])
+    xq = rng.integers(-127, 128, (m, k)).astype(np.int8)
+    wq = rng.integers(-127, 128, (n, k)).astype(np.int8)
+    beta, gamma = _f32(rng.random(m) + 0.5), _f32(rng.random(n) + 0.5)
+    b = _f32(rng.standard_normal(n)) if k % 2 else None
+    out = torch.full((m + 2, n), 3.0, device="cuda")
+    _, acc = bl.bitlinear_forward_i8(_t(torch, xq), _t(torch, beta), _t(torch, wq), _t(torch, gamma), bias=_t(torch, b),
+                                     y=out[1:m + 1], acc=True)
+    ref = (xq.astype(np.float64) @ wq.astype(np.float64).T).astype(np.int32)     # exact: below 2^53
+    assert np.array_equal(_np(acc), ref)
+    f = np.float32
+    yr = (ref.astype(f) * (beta / f(127))[:, None]) * (gamma / f(127))[None]
+    assert np.array_equal(_np(out[1:m + 1]), yr if b is None else yr + b)
+    assert bool((out[0] == 3).all()) and bool((out[m + 1] == 3).all())
+
+
 def test_forward_i8_largest_sums(dev):
     """Codes of +-127 at the largest K: sums at the end of int32, on every path."""
     torch, bl = dev
