@@ -28,10 +28,11 @@
 //   3. k_grad_split: d once more, scaled and split, rows being tokens (dx) and channels (dW);
 //   4. k_split_gemm: both products;
 //   5. k_split_sum, where a sum was cut into parts.
+// Up to 16 tokens one pass in fp32 takes their place (k_grad_few).
 //
 // 2048 tokens, K = 4096, F = 11008 (gated): 1265 us: step 1 96, 2 5, 3 141 (copies of their bytes would
-// take 83, 1, 132), the products 1.02 ms.  61 tokens, K = 1024, F = 2731: 35 us, 7 tokens, K = 1000, N = 1023:
-// 22 us, launches and their first loads.
+// take 83, 1, 132), the products 1.02 ms.  61 tokens, K = 1024, F = 2731: 35 us,
+// launches and their first loads.
 #include <limits.h>
 
 #include "ffn.hpp"
@@ -170,7 +171,6 @@ static GradPlan grad_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws)
     return p;
 }
 
-size_t backward_workspace(int64_t M, int64_t K, int64_t N, bool gated) { return grad_plan(M, K, N, gated, nullptr).bytes; }
 
 // ---- step 1 -------------------------------------------------------------------------------
 // Maxima and sums.  A workgroup takes p.tm tokens x 64 C columns, a wave a quarter of the tokens, a
@@ -631,9 +631,177 @@ __global__ __launch_bounds__(256) void k_split_sum(SplitArgs x, SplitArgs w, int
     else a.c1[e - a.I0 * a.J] = s;
 }
 
+// ---- few tokens ---------------------------------------------------------------------------
+// One pass in fp32: a workgroup takes 256 columns k and a chunk of the rows n of one projection, wave w the
+// rows w, w + 4, ... of it, a lane four columns.  For a row it holds d of every token (through LDS) and
+//     dW[n, k] = sum_m d[m, n] (x_q[m, k] beta[m] / 127),   written at once,
+//     dx[m, k] += d[m, n] (alpha W[n, k]),                  held for the whole chunk,
+// so that dW is written once and each weight read once, in its two bits.  The waves' dx are added through
+// LDS, the chunks' by k_few_sum, in their order.
+// Against the steps above (us): K = 1000, N = 1023, 1 token 7.8 and 19.8, 7 tokens 10.1 and 20.9, 16 tokens 13.6
+// and 22.2; K = 4096, N = 11008, 4 tokens 36.8 and 76.0, 16 tokens 60.7 and 75.7; gated, F = 11008, 16 tokens
+// 130 and 151.  Bound: writing dW (180 MB in the 36.8 us of 4 tokens) up to 8 tokens, beyond it the
+// multiplications, 2 M + 3 instructions for a weight; more than 16 tokens do not fit the registers.
+// 512 workgroups (two to a compute unit): 256 took 46.3 and 1024 38.1 us where 512 took 36.8.
+constexpr int FEW_TOKENS = 16, FEW_K = 256, FEW_N = 64, FEW_GROUPS = 512;
+struct FewPlan {
+    int64_t kt, chunks, rows;      // column tiles; chunks of a projection, of `rows` rows
+    float* part;                   // [P chunks, M, K]
+    size_t bytes;
+};
+static FewPlan few_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws) {
+    FewPlan p{};
+    const int64_t P = gated ? 2 : 1;
+    p.kt = (K + FEW_K - 1) / FEW_K;
+    const int64_t rows = (P * N * p.kt + FEW_GROUPS - 1) / FEW_GROUPS;
+    p.rows = rows < 16 ? 16 : (rows + 3) / 4 * 4;
+    p.chunks = (N + p.rows - 1) / p.rows;
+    p.part = static_cast<float*>(ws);
+    p.bytes = ((size_t)(P * p.chunks * M * K) * 4 + 255) / 256 * 256;
+    return p;
+}
+
+template <int ACT, int MT>
+__global__ __launch_bounds__(256) void k_grad_few(BackwardArgs a, FewPlan p) {
+    __shared__ __align__(16) float d[FEW_N][MT];
+    __shared__ __align__(16) float red[3][MT][FEW_K];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t tile = blockIdx.x % p.kt, ch = blockIdx.x / p.kt, rowb = a.K >> 2;
+    const int q = ACT != 0 && ch >= p.chunks;
+    const int64_t r0 = (ch - q * p.chunks) * p.rows, r1 = r0 + p.rows < a.N ? r0 + p.rows : a.N;
+    const int64_t k = tile * FEW_K + 4 * lane, kl = k < a.K ? k : 0;       // kl: where the lane loads
+    const uint8_t* w = (q ? a.w1 : a.w0) + (kl >> 2);
+    float* dw = q ? a.dw1 : a.dw0;
+    float* db = q ? a.db1 : a.db0;
+    const float al = q ? a.al1[0] : a.al0[0];
+    float x[MT][4], acc[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        uint32_t v = 0;
+        float bs = 0.0f;
+        if (a.dw0 && m < a.M) {
+            __builtin_memcpy(&v, a.xq + m * a.K + kl, 4);
+            bs = a.beta[m] / 127.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            x[m][c] = (float)(int8_t)(v >> (8 * c)) * bs;
+            acc[m][c] = 0.0f;
+        }
+    }
+    for (int64_t n0 = r0; n0 < r1; n0 += FEW_N) {
+        uint32_t codes[FEW_N / 4];
+        if (a.dx) {
+#pragma unroll
+            for (int i = 0; i < FEW_N / 4; ++i) {
+                const int64_t n = n0 + wave + 4 * i;
+                codes[i] = w[(n < r1 ? n : r1 - 1) * rowb];
+            }
+        }
+        __syncthreads();                               // the rows before have been read
+#pragma unroll
+        for (int e = tid; e < FEW_N * MT; e += 256) {
+            const int j = e % FEW_N, m = e / FEW_N;
+            float v[2] = {0.0f, 0.0f};
+            if (n0 + j < r1 && m < a.M) grad_at<ACT>(a, m * a.N + n0 + j, v);
+            d[j][m] = q ? v[1] : v[0];
+        }
+        __syncthreads();
+        if (db && tile == 0 && tid < FEW_N && n0 + tid < r1) {
+            double sum = 0.0;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) sum += (double)d[tid][m];
+            db[n0 + tid] = (float)sum;
+        }
+#pragma unroll
+        for (int i = 0; i < FEW_N / 4; ++i) {
+            const int j = wave + 4 * i;
+            if (n0 + j >= r1) break;
+            float dm[MT];
+#pragma unroll
+            for (int m = 0; m < MT; m += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(&d[j][m]);
+                dm[m] = v.x, dm[m + 1] = v.y, dm[m + 2] = v.z, dm[m + 3] = v.w;
+            }
+            if (a.dx) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float t = __builtin_fmaf((float)((codes[i] >> (2 * c)) & 3u), al, -al);   // exact
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) acc[m][c] = __builtin_fmaf(dm[m], t, acc[m][c]);
+                }
+            }
+            if (dw) {
+                float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(dm[m], x[m][c], o[c]);
+                if (k < a.K) __builtin_memcpy(dw + (n0 + j) * a.K + k, o, 16);
+            }
+        }
+    }
+    if (!a.dx) return;
+    if (wave > 0) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            *reinterpret_cast<float4*>(&red[wave - 1][m][4 * lane]) = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+    }
+    __syncthreads();
+    if (wave > 0 || k >= a.K) return;
+    float* out = gridDim.x == p.kt ? a.dx : p.part + ch * a.M * a.K;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (m >= a.M) break;
+        float o[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            o[c] = ((acc[m][c] + red[0][m][4 * lane + c]) + red[1][m][4 * lane + c]) + red[2][m][4 * lane + c];
+        __builtin_memcpy(out + m * a.K + k, o, 16);
+    }
+}
+
+// dx from the chunks' parts: 256 elements per workgroup, a wave every fourth chunk.
+__global__ __launch_bounds__(256) void k_few_sum(const float* __restrict__ part, float* __restrict__ dx, int64_t n, int64_t chunks) {
+    __shared__ __align__(16) float4 red[3][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t e = (int64_t)blockIdx.x * 256 + 4 * lane, el = e < n ? e : 0;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int64_t c = wave; c < chunks; c += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(part + c * n + el);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    if (wave > 0) red[wave - 1][lane] = s;
+    __syncthreads();
+    if (wave > 0 || e >= n) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) {
+        const float4 v = red[w][lane];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    __builtin_memcpy(dx + e, &s, 16);
+}
+
+template <int ACT, int MT>
+static hipError_t launch_few(const BackwardArgs& a, hipStream_t s) {
+    FewPlan p = few_plan(a.M, a.K, a.N, ACT != 0, a.ws);
+    if (!a.dx && !a.dw0) p.kt = 1;                     // the bias sums alone
+    const int64_t chunks = (ACT == 0 ? 1 : 2) * p.chunks, n = a.M * a.K;
+    hipLaunchKernelGGL((k_grad_few<ACT, MT>), dim3((unsigned)(chunks * p.kt)), dim3(256), 0, s, a, p);
+    if (a.dx && chunks > 1)
+        hipLaunchKernelGGL(k_few_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p.part, a.dx, n, chunks);
+    return hipGetLastError();
+}
+
+size_t backward_workspace(int64_t M, int64_t K, int64_t N, bool gated) {
+    return M <= FEW_TOKENS ? few_plan(M, K, N, gated, nullptr).bytes : grad_plan(M, K, N, gated, nullptr).bytes;
+}
+
 template <int ACT>
 static hipError_t launch_grads(const BackwardArgs& a, hipStream_t s) {
     constexpr int P = ACT == 0 ? 1 : 2;
+    if (a.M <= FEW_TOKENS) return a.M <= 4 ? launch_few<ACT, 4>(a, s) : a.M <= 8 ? launch_few<ACT, 8>(a, s) : launch_few<ACT, 16>(a, s);
     const GradPlan p = grad_plan(a.M, a.K, a.N, P == 2, a.ws);
     auto blocks = [](int64_t n) { return dim3((unsigned)n); };
     const int64_t ktw = (a.K + 255) / 256, ktc = (a.K + 63) / 64;

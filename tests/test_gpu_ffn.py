@@ -149,6 +149,9 @@ def test_gated_forward_unaligned_views(dev):
 # ---------------------------------------------------------------------------------- gradients
 GRADS = [(1, 4, 1), (1, 256, 33), (2, 64, 130), (7, 100, 31), (16, 512, 64), (33, 132, 70), (61, 1024, 171),
          (64, 64, 64), (100, 260, 300), (129, 516, 129), (257, 320, 65), (300, 128, 520), (700, 68, 40)]
+# few tokens: rows past one, two and three times 64 a workgroup, in one chunk and in many, columns past a tile
+GRADS += [(3, 4, 1), (4, 8, 17), (5, 1028, 70), (8, 4096, 2501), (9, 4100, 4700), (15, 260, 515), (16, 12, 9000),
+          (16, 2052, 1111), (17, 2052, 111)]
 
 
 def _check(got, want, terms, lengths, names):
