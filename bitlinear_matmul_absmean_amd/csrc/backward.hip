@@ -28,11 +28,11 @@
 //   3. k_grad_split: d once more, scaled and split, rows being tokens (dx) and channels (dW);
 //   4. k_split_gemm: both products;
 //   5. k_split_sum, where a sum was cut into parts.
-// Up to 16 tokens one pass in fp32 takes their place (k_grad_few).
+// Up to 16 tokens one pass in fp32 takes their place (k_grad_few), up to 64, where the tiles are few, one that
+// does steps 1 to 4 tile by tile in LDS (k_grad_mid).
 //
 // 2048 tokens, K = 4096, F = 11008 (gated): 1265 us: step 1 96, 2 5, 3 141 (copies of their bytes would
-// take 83, 1, 132), the products 1.02 ms.  61 tokens, K = 1024, F = 2731: 35 us,
-// launches and their first loads.
+// take 83, 1, 132), the products 1.02 ms.
 #include <limits.h>
 
 #include "ffn.hpp"
@@ -65,19 +65,23 @@ __device__ __forceinline__ f16x8 bytes_f16(uint32_t lo, uint32_t hi) {
 }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
-// d of element (m, n): one projection d[0] = dy; gated d[0] = dh u a'(g), d[1] = dh a(g).
-// ACT 0: one projection.
+// d from the incoming gradient and the saved values: one projection d[0] = dy; gated d[0] = dh u a'(g),
+// d[1] = dh a(g).  ACT 0: one projection.
 template <int ACT>
-__device__ __forceinline__ void grad_at(const BackwardArgs& a, int64_t i, float (&d)[2]) {
-    const float dy = a.dy[i];
+__device__ __forceinline__ void grad_of(float dy, float g, float u, float (&d)[2]) {
     if constexpr (ACT == 0) {
         d[0] = dy;
     } else {
         float v, slope;
-        act_grad<ACT>(a.g[i], v, slope);
-        d[0] = dy * a.u[i] * slope;
+        act_grad<ACT>(g, v, slope);
+        d[0] = dy * u * slope;
         d[1] = dy * v;
     }
+}
+// d of element i = (m, n).
+template <int ACT>
+__device__ __forceinline__ void grad_at(const BackwardArgs& a, int64_t i, float (&d)[2]) {
+    grad_of<ACT>(a.dy[i], ACT == 0 ? 0.0f : a.g[i], ACT == 0 ? 0.0f : a.u[i], d);
 }
 
 constexpr int SG_BM = 128, SG_BN = 256, SG_BK = 32, SG_SLOTS = 512;
@@ -276,15 +280,41 @@ __device__ __forceinline__ uint32_t row_dword(const uint8_t* __restrict__ p, int
 // 4 (t / 16) .. 4 (t / 16) + 3, turns the 4 x 4 bytes round in registers and writes four columns' dwords
 // (a column is 17 dwords, so that the lanes of a write and of a read spread over the banks); it gets back
 // sixteen rows of one column, rows 16 (t % 4) .. of column t / 4.
-__device__ __forceinline__ u32x4 turn_tile(uint32_t* lds, u32x4 rows) {
+__device__ __forceinline__ void turn_put(uint32_t* lds, u32x4 rows, int t) {
     const u32x4 cols = transpose4x4_perm(rows);
-    const int c = 4 * (threadIdx.x & 15), r4 = threadIdx.x >> 4;
+    const int c = 4 * (t & 15), r4 = t >> 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) lds[(c + j) * 17 + r4] = cols[j];
-    __syncthreads();
-    const uint32_t* p = lds + (threadIdx.x >> 2) * 17 + 4 * (threadIdx.x & 3);
+}
+__device__ __forceinline__ u32x4 turn_get(const uint32_t* lds, int t) {
+    const uint32_t* p = lds + (t >> 2) * 17 + 4 * (t & 3);
     return u32x4{p[0], p[1], p[2], p[3]};
 }
+__device__ __forceinline__ u32x4 turn_tile(uint32_t* lds, u32x4 rows) {
+    turn_put(lds, rows, threadIdx.x);
+    __syncthreads();
+    return turn_get(lds, threadIdx.x);
+}
+// The thread's dwords of such a tile: bytes at .. at + 3 of rows r0 .. r0 + 3 of a matrix with rows of `row`
+// bytes; zeros past a row's end, `fill` for rows past the last (whole: the tile has neither).
+__device__ __forceinline__ u32x4 tile_rows(const uint8_t* __restrict__ p, int64_t r0, int64_t rows, int64_t at, int64_t row,
+                                           uint32_t fill, bool whole) {
+    u32x4 d;
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v;
+            __builtin_memcpy(&v, p + (r0 + i) * row + at, 4);
+            d[i] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = r0 + i < rows ? row_dword(p + (r0 + i) * row, at, row) : fill;
+    }
+    return d;
+}
+// Sixteen bytes of codes 0, 1, 2 (four to a byte) to the weights of code i as bytes 127, 128, 129.
+__device__ __forceinline__ u32x4 code_bytes(u32x4 v, int i) { return ((v >> (uint32_t)(2 * i)) & 0x03030303u) + 0x7F7F7F7Fu; }
 
 // Panels of W_hat^T, 64 weight rows x 256 columns k per workgroup: a lane expands the codes 0, 1, 2 of
 // sixteen rows at four columns to the bytes 127, 128, 129.
@@ -294,24 +324,11 @@ __device__ __forceinline__ void weights_tile(const BackwardArgs& a, const GradPl
     const int64_t n0 = l0 - q * p.Np, rowb = a.K >> 2;
     const uint8_t* w = q ? a.w1 : a.w0;
     const int64_t r0 = n0 + 4 * (threadIdx.x >> 4), at = (k0 >> 2) + 4 * (threadIdx.x & 15);
-    u32x4 d;
-    if (n0 + 64 <= a.N && (k0 >> 2) + 64 <= rowb) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t v;
-            __builtin_memcpy(&v, w + (r0 + i) * rowb + at, 4);
-            d[i] = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = r0 + i < a.N ? row_dword(w + (r0 + i) * rowb, at, rowb) : 0x55555555u;
-    }
-    const u32x4 v = turn_tile(lds, d);
+    const u32x4 v = turn_tile(lds, tile_rows(w, r0, a.N, at, rowb, 0x55555555u, n0 + 64 <= a.N && (k0 >> 2) + 64 <= rowb));
     const int u = threadIdx.x & 3, c = threadIdx.x >> 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const u32x4 o = ((v >> (uint32_t)(2 * i)) & 0x03030303u) + 0x7F7F7F7Fu;
-        reinterpret_cast<u32x4*>(p.wt)[code_unit(k0 + 4 * c + i, l0 + 16 * u, p.Lx)] = o;
+        reinterpret_cast<u32x4*>(p.wt)[code_unit(k0 + 4 * c + i, l0 + 16 * u, p.Lx)] = code_bytes(v, i);
     }
 }
 
@@ -320,19 +337,7 @@ __device__ __forceinline__ void codes_tile(const BackwardArgs& a, const GradPlan
     const int64_t k0 = b % kt * 64, m0 = b / kt * 64;
     const uint8_t* x = reinterpret_cast<const uint8_t*>(a.xq);
     const int64_t r0 = m0 + 4 * (threadIdx.x >> 4), at = k0 + 4 * (threadIdx.x & 15);
-    u32x4 d;
-    if (m0 + 64 <= a.M && k0 + 64 <= a.K) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t v;
-            __builtin_memcpy(&v, x + (r0 + i) * a.K + at, 4);
-            d[i] = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = r0 + i < a.M ? row_dword(x + (r0 + i) * a.K, at, a.K) : 0u;
-    }
-    const u32x4 v = turn_tile(lds, d);
+    const u32x4 v = turn_tile(lds, tile_rows(x, r0, a.M, at, a.K, 0u, m0 + 64 <= a.M && k0 + 64 <= a.K));
     const int u = threadIdx.x & 3, c = threadIdx.x >> 2;
     reinterpret_cast<u32x4*>(p.cd)[code_unit(k0 + c, m0 + 16 * u, p.Mp)] = v ^ 0x80808080u;
 }
@@ -654,7 +659,7 @@ static FewPlan few_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws) {
     const int64_t P = gated ? 2 : 1;
     p.kt = (K + FEW_K - 1) / FEW_K;
     const int64_t rows = (P * N * p.kt + FEW_GROUPS - 1) / FEW_GROUPS;
-    p.rows = rows < 16 ? 16 : (rows + 3) / 4 * 4;
+    p.rows = M > FEW_TOKENS ? FEW_N : rows < 16 ? 16 : (rows + 3) / 4 * 4;
     p.chunks = (N + p.rows - 1) / p.rows;
     p.part = static_cast<float*>(ws);
     p.bytes = ((size_t)(P * p.chunks * M * K) * 4 + 255) / 256 * 256;
@@ -761,6 +766,243 @@ __global__ __launch_bounds__(256) void k_grad_few(BackwardArgs a, FewPlan p) {
     }
 }
 
+// ---- some tokens, few tiles ---------------------------------------------------------------
+// The products on the matrix cores without panels: a workgroup takes 256 columns k of 64 rows n of one
+// projection and all tokens, up to 64.  It scales and splits its d as above, in both orders, into LDS, where x_q
+// and W are turned and stay bytes v + 128; dW is written at once, dx as a part for each 64 rows (a token's scale
+// is taken over those, and the part scaled back before it leaves), which k_few_sum adds.
+// Against the steps above (us): gated, K = 1024, F = 2731, 61 tokens (344 workgroups) 25.1 and 38.6; K = 512,
+// N = 512, 64 tokens (16) 10.9 and 23.8; K = 2944, N = 5335 (1008), 32 tokens 34.8 and 44.2, 64 tokens 43.3 and
+// 45.5; gated, K = 2048, F = 5504 (1376), 64 tokens 65.3 and 55.5: the parts of dx, as many bytes as dW.
+// Several tiles of rows in a workgroup halve those but hold twice the registers (gated, K = 1024, F = 2731, 61
+// tokens 33 us).  Bound: at a single tile latency, loads, three barriers and some 700 instructions of a wave.
+// LDS images: split gradients, rows of 64 values, the 16-byte unit u at position u ^ (row / 2) % 8; bytes,
+// columns of 64, the 16-byte unit u at position u ^ split_swizzle(column).
+constexpr int MID_TOKENS = 64, MID_GROUPS = 1024;
+constexpr int64_t MID_K = (int64_t)1 << 28;            // 16 K bytes are a 32-bit offset
+
+// acc[i] += sum_l (hi + lo)[row, l] b[column, l]: rows 32 i .. 32 i + 31 (i = 0 alone if !high), columns c0 ..
+// c0 + 31, l 0 .. 63 (0 .. 31 if !deep); operands in lanes as k_split_gemm's.
+__device__ __forceinline__ void mid_multiply(f32x16 (&acc)[2], const u32x4* hi, const u32x4* lo, const u32x4* b, int c0, bool high,
+                                             bool deep) {
+    const int lr = threadIdx.x & 31, lg = (threadIdx.x >> 5) & 1, c = c0 + lr;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (s && !deep) break;
+        const u32x4 cb = b[4 * c + ((2 * s + lg) ^ split_swizzle(c))];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const f16x8 fb = bytes_f16(cb[2 * kk], cb[2 * kk + 1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i && !high) break;
+                const int r = 32 * i + lr, at = 8 * r + ((4 * s + 2 * lg + kk) ^ ((r >> 1) & 7));
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, hi[at]), fb, acc[i], 0, 0, 0);
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, lo[at]), fb, acc[i], 0, 0, 0);
+            }
+        }
+    }
+}
+
+// out[row, column] = acc scale[row], rows below `rows`, columns below `cols` (lane: column lane % 32 of rows
+// 4 (lane / 32) .. of eight).  A running row and one lane offset (below 2^32: MID_K): the addresses of every
+// row would fill the registers.
+__device__ __forceinline__ void mid_store(const f32x16 (&acc)[2], const float* scale, float* out, int64_t stride, int64_t rows,
+                                          int64_t cols) {
+    const int lr = threadIdx.x & 31, lg = (threadIdx.x >> 5) & 1;
+    if (lr >= cols) return;
+    const uint32_t off = 4u * (4u * lg * (uint32_t)stride + lr);
+    const int left = (int)(rows < 64 ? rows : 64) - 4 * lg;
+    auto rows_out = [&](auto inside) {
+        char* row = reinterpret_cast<char*>(out);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float4 v = *reinterpret_cast<const float4*>(&scale[32 * i + 8 * g + 4 * lg]);
+                const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (inside(32 * i + 8 * g + e)) *reinterpret_cast<float*>(row + off) = acc[i][4 * g + e] * f[e];
+                    row += 4 * stride;
+                }
+                row += 16 * stride;
+            }
+    };
+    if (rows >= 64) rows_out([](int) { return true; });
+    else rows_out([&](int r) { return r < left; });
+}
+
+template <int ACT>
+__global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) {
+    // split gradients: hi and lo of d alpha, a row for a token, then of d beta / 127, a row for a channel
+    __shared__ u32x4 sp[4][512];
+    __shared__ u32x4 xb[1024], wb[1024];               // bytes of x_q^T and of W_hat^T
+    __shared__ uint32_t turn[64 * 17];
+    __shared__ float cmx[8][64];
+    __shared__ double csum[8][64];
+    __shared__ __align__(16) float rinv[64];
+    __shared__ __align__(16) float cinv[64];
+    __shared__ float rscale[64], bscale[64];           // of the tokens: d alpha's scale, beta / 127
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = wave >> 2, tt = tid & 255;        // a tile of bytes is turned by 256 threads
+    const int64_t tile = blockIdx.x % p.kt, ch = blockIdx.x / p.kt, rowb = a.K >> 2, k0 = tile * FEW_K;
+    const int q = ACT != 0 && ch >= p.chunks;
+    const int64_t n0 = (ch - q * p.chunks) * FEW_N;
+    const uint8_t* w = q ? a.w1 : a.w0;
+    float* dw = q ? a.dw1 : a.dw0;
+    float* db = tile > 0 ? nullptr : q ? a.db1 : a.db0;
+    const float al = q ? a.al1[0] : a.al0[0];
+    // tokens and rows past the end repeat the last (their d is zero), columns past it are not stored
+    u32x4 x[2], wr{};
+    if (dw) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int64_t k = k0 + 64 * (2 * half + c) + 4 * (tt & 15);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t m = 4 * (tt >> 4) + i;
+                uint32_t v;
+                __builtin_memcpy(&v, a.xq + (m < a.M ? m : a.M - 1) * a.K + (k < a.K ? k : 0), 4);
+                x[c][i] = v;
+            }
+        }
+    }
+    // four bytes of W in four rows, zeros past a row's end
+    if (a.dx && half == 0) {
+        const int64_t at = (k0 >> 2) + 4 * (tt & 15), end = rowb - 4, from = at < end ? at : end;
+        const int past = at - from < 4 ? (int)(at - from) : 0;     // bytes of the dword past the row's end
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t n = n0 + 4 * (tt >> 4) + i;
+            const uint8_t* row = w + (n < a.N ? n : a.N - 1) * rowb;
+            uint32_t v = 0;
+            if (end >= 0) {
+                __builtin_memcpy(&v, row + from, 4);
+                v >>= 8 * past;
+            } else if (at == 0) {
+#pragma nounroll
+                for (int b = 0; b < (int)rowb; ++b) v |= (uint32_t)row[b] << (8 * b);
+            }
+            wr[i] = v;
+        }
+    }
+    // d of tokens 8 wave .. 8 wave + 7 in row n0 + lane, zeros past the ends; offsets below 2^31 bytes
+    float d[8];
+    {
+        const uint32_t n = (uint32_t)(n0 + lane < a.N ? n0 + lane : a.N - 1), M = (uint32_t)a.M, N = (uint32_t)a.N;
+        auto at = [](const float* p, uint32_t i) { return *reinterpret_cast<const float*>(reinterpret_cast<const char*>(p) + 4u * i); };
+        float y[8], g[8], u[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const uint32_t m = 8 * wave + t, i = (m < M ? m : M - 1) * N + n;
+            y[t] = at(a.dy, i);
+            g[t] = ACT == 0 ? 0.0f : at(a.g, i);
+            u[t] = ACT == 0 ? 0.0f : at(a.u, i);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            float e[2];
+            grad_of<ACT>(y[t], g[t], u[t], e);
+            d[t] = n0 + lane < a.N && 8 * wave + t < a.M ? (q ? e[1] : e[0]) : 0.0f;
+        }
+    }
+    // x_q: four tiles of 64 columns, turned in the split gradients' place; W
+    uint32_t* room = reinterpret_cast<uint32_t*>(sp);
+    if (dw) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) turn_put(room + 64 * 17 * (2 * half + c), x[c], tt);
+    }
+    if (a.dx && half == 0) turn_put(turn, wr, tt);
+    // the tokens' and the channels' scales
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        const int m = 8 * wave + t, s = scale_exponent(wave_max_pos(fabsf(d[t] * al)));
+        if (lane == 0) {
+            rscale[m] = pow2f(s);
+            rinv[m] = pow2f(-s);
+            bscale[m] = m < a.M ? a.beta[m] / 127.0f : 0.0f;
+        }
+    }
+    if (dw) {
+        float v = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v = fmaxf(v, fabsf(d[t] * bscale[8 * wave + t]));
+        cmx[wave][lane] = v;
+    }
+    if (db) {
+        double v = 0.0;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v += (double)d[t];
+        csum[wave][lane] = v;
+    }
+    __syncthreads();
+    u32x4 xt[2];
+    if (dw) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) xt[c] = turn_get(room + 64 * 17 * (2 * half + c), tt) ^ 0x80808080u;
+    }
+    __syncthreads();                                   // the room is free
+    if (dw) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int col = 64 * (2 * half + c) + (tt >> 2);
+            xb[4 * col + ((tt & 3) ^ split_swizzle(col))] = xt[c];
+        }
+        float v = cmx[0][lane];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v = fmaxf(v, cmx[i][lane]);
+        const int s = scale_exponent(v), at = 8 * lane + (wave ^ ((lane >> 1) & 7));
+        const float cs = pow2f(s);
+        if (wave == 0) cinv[lane] = pow2f(-s);
+        u32x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t v0 = split_f16(d[2 * e] * bscale[8 * wave + 2 * e] * cs);
+            const uint32_t v1 = split_f16(d[2 * e + 1] * bscale[8 * wave + 2 * e + 1] * cs);
+            hi[e] = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
+            lo[e] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
+        }
+        sp[2][at] = hi;
+        sp[3][at] = lo;
+    }
+    if (a.dx) {
+        uint16_t* hi = reinterpret_cast<uint16_t*>(sp[0]);
+        uint16_t* lo = reinterpret_cast<uint16_t*>(sp[1]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const int m = 8 * wave + t, at = 8 * (8 * m + ((lane >> 3) ^ ((m >> 1) & 7))) + (lane & 7);
+            const uint32_t v = split_f16(d[t] * al * rscale[m]);
+            hi[at] = (uint16_t)v;
+            lo[at] = (uint16_t)(v >> 16);
+        }
+        const u32x4 v = turn_get(turn, tt);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = 4 * (tt >> 2) + 2 * half + i;
+            wb[4 * c + ((tt & 3) ^ split_swizzle(c))] = code_bytes(v, 2 * half + i);
+        }
+    }
+    if (db && tid < 64 && n0 + tid < a.N) {
+        double v = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += csum[i][tid];
+        db[n0 + tid] = (float)v;
+    }
+    __syncthreads();
+    const int64_t left = a.K - (k0 + 32 * wave);       // columns from the wave's first to the end
+    if (a.dx) {
+        f32x16 acc[2] = {};
+        mid_multiply(acc, sp[0], sp[1], wb, 32 * wave, a.M > 32, true);
+        mid_store(acc, rinv, (gridDim.x == p.kt ? a.dx : p.part + ch * a.M * a.K) + k0 + 32 * wave, a.K, a.M, left);
+    }
+    if (dw) {
+        f32x16 acc[2] = {};
+        mid_multiply(acc, sp[2], sp[3], xb, 32 * wave, true, a.M > 32);
+        mid_store(acc, cinv, dw + n0 * a.K + k0 + 32 * wave, a.K, a.N - n0, left);
+    }
+}
+
 // dx from the chunks' parts: 256 elements per workgroup, a wave every fourth chunk.
 __global__ __launch_bounds__(256) void k_few_sum(const float* __restrict__ part, float* __restrict__ dx, int64_t n, int64_t chunks) {
     __shared__ __align__(16) float4 red[3][64];
@@ -783,25 +1025,36 @@ __global__ __launch_bounds__(256) void k_few_sum(const float* __restrict__ part,
     __builtin_memcpy(dx + e, &s, 16);
 }
 
+static bool use_mid(int64_t M, int64_t K, int64_t N, bool gated) {
+    return M > FEW_TOKENS && M <= MID_TOKENS && K < MID_K &&
+           ((K + FEW_K - 1) / FEW_K) * ((N + FEW_N - 1) / FEW_N) * (gated ? 2 : 1) <= MID_GROUPS;
+}
+
+// MT: tokens that k_grad_few holds, 0 for k_grad_mid.
 template <int ACT, int MT>
 static hipError_t launch_few(const BackwardArgs& a, hipStream_t s) {
     FewPlan p = few_plan(a.M, a.K, a.N, ACT != 0, a.ws);
     if (!a.dx && !a.dw0) p.kt = 1;                     // the bias sums alone
     const int64_t chunks = (ACT == 0 ? 1 : 2) * p.chunks, n = a.M * a.K;
-    hipLaunchKernelGGL((k_grad_few<ACT, MT>), dim3((unsigned)(chunks * p.kt)), dim3(256), 0, s, a, p);
+    if constexpr (MT > 0)
+        hipLaunchKernelGGL((k_grad_few<ACT, MT>), dim3((unsigned)(chunks * p.kt)), dim3(256), 0, s, a, p);
+    else
+        hipLaunchKernelGGL(k_grad_mid<ACT>, dim3((unsigned)(chunks * p.kt)), dim3(512), 0, s, a, p);
     if (a.dx && chunks > 1)
         hipLaunchKernelGGL(k_few_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p.part, a.dx, n, chunks);
     return hipGetLastError();
 }
 
 size_t backward_workspace(int64_t M, int64_t K, int64_t N, bool gated) {
-    return M <= FEW_TOKENS ? few_plan(M, K, N, gated, nullptr).bytes : grad_plan(M, K, N, gated, nullptr).bytes;
+    return M <= FEW_TOKENS || use_mid(M, K, N, gated) ? few_plan(M, K, N, gated, nullptr).bytes
+                                                      : grad_plan(M, K, N, gated, nullptr).bytes;
 }
 
 template <int ACT>
 static hipError_t launch_grads(const BackwardArgs& a, hipStream_t s) {
     constexpr int P = ACT == 0 ? 1 : 2;
     if (a.M <= FEW_TOKENS) return a.M <= 4 ? launch_few<ACT, 4>(a, s) : a.M <= 8 ? launch_few<ACT, 8>(a, s) : launch_few<ACT, 16>(a, s);
+    if (use_mid(a.M, a.K, a.N, P == 2)) return launch_few<ACT, 0>(a, s);
     const GradPlan p = grad_plan(a.M, a.K, a.N, P == 2, a.ws);
     auto blocks = [](int64_t n) { return dim3((unsigned)n); };
     const int64_t ktw = (a.K + 255) / 256, ktc = (a.K + 63) / 64;

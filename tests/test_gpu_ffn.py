@@ -152,6 +152,9 @@ GRADS = [(1, 4, 1), (1, 256, 33), (2, 64, 130), (7, 100, 31), (16, 512, 64), (33
 # few tokens: rows past one, two and three times 64 a workgroup, in one chunk and in many, columns past a tile
 GRADS += [(3, 4, 1), (4, 8, 17), (5, 1028, 70), (8, 4096, 2501), (9, 4100, 4700), (15, 260, 515), (16, 12, 9000),
           (16, 2052, 1111), (17, 2052, 111)]
+# up to 64 tokens: short rows of codes, rows and columns past a tile, and more tiles than go in one pass
+GRADS += [(17, 4, 1), (20, 8, 70), (33, 12, 64), (64, 16, 65), (32, 1028, 129), (40, 260, 700), (64, 2052, 190),
+          (24, 4100, 4200), (61, 8200, 2100)]
 
 
 def _check(got, want, terms, lengths, names):
