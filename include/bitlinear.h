@@ -378,7 +378,8 @@ int bitlinear_gated_forward(const float* x, int64_t M, int64_t K, const uint8_t*
  * Each gradient element enters its products with at least 22 significant bits, relative to
  * itself down to 2^-17 of the largest of its row (dx) or column (dW) and as a fixed-point value
  * below that; products are exact, and sums are taken in fp32 (dbias in fp64) in an order fixed
- * by the sizes, so results are reproducible bit for bit.
+ * by the sizes, so results are reproducible bit for bit.  (Up to 16 tokens it enters whole, and
+ * beta x_q / 127 rounded to fp32.)
  *
  *   dy        [M, N] fp32.                                                   (in)
  *   x_q       [M, K] int8, beta [M] fp32: as bitlinear_forward used them.    (in)

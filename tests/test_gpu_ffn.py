@@ -221,12 +221,10 @@ def test_gated_backward(dev, m, k, f):
             assert alone[q] is None if q not in keep else torch.equal(alone[q], out[names.index(q)]), (keep, q)
 
 
-def test_backward_wide_range(dev):
-    """Gradients of very different sizes in one row and one column, zero rows and columns, and rows
-    at the ends of the fp32 range: every row of dx and of dW keeps its own accuracy."""
+def _wide_range(dev, m):
     torch, bl = dev
     rng = np.random.default_rng(3)
-    m, k, n = 70, 132, 90
+    k, n = 132, 90
     dy = _f32(rng.standard_normal((m, n)))
     dy[0] = 0
     dy[:, 1] = 0
@@ -246,6 +244,68 @@ def test_backward_wide_range(dev):
     col = v.max(0)[:, None] * 2.0 ** -40 * m * 127
     assert np.all(np.abs(dw - want[1]) <= plain.gradient_tolerance(terms[1], m) + col)
     assert np.all(dx[0] == 0) and np.all(dw[1] == 0)
+
+
+def test_backward_wide_range(dev):
+    """Gradients of very different sizes in one row and one column, zero rows and columns, and rows
+    at the ends of the fp32 range: every row of dx and of dW keeps its own accuracy."""
+    _wide_range(dev, 70)
+
+
+@pytest.mark.parametrize("m", [6, 12, 40])
+def test_backward_wide_range_few_tokens(dev, m):
+    _wide_range(dev, m)
+
+
+@pytest.mark.parametrize("m", [5, 13, 40, 100])
+def test_backward_unaligned_views(dev, m):
+    """Every tensor off its alignment; what lies around the outputs stays."""
+    torch, bl = dev
+    k, n = 268, 131
+    _say(f"backward unaligned M={m}")
+    rng = np.random.default_rng([13, m])
+    dy = _f32(rng.standard_normal((m, n)))
+    x_q, beta = plain.absmax(rng.standard_normal((m, k)))
+    w, al, _ = _layer(rng, n, k, False)
+
+    def off(a, s):
+        t = _t(torch, np.ascontiguousarray(a))
+        v = torch.empty(t.numel() + s, dtype=t.dtype, device="cuda")[s:].view(t.shape)
+        v.copy_(t)
+        return v
+
+    room = [torch.full((a * b + 64,), 3.0, device="cuda") for a, b in ((m, k), (n, k), (n, 1))]
+    out = [r[1:1 + a * b].view(a, b) for r, (a, b) in zip(room, ((m, k), (n, k), (n, 1)))]
+    bl.bitlinear_backward(off(dy, 1), off(x_q, 1), off(beta, 3), off(plain.pack(w), 3), off(al, 1), dx=out[0], dW=out[1],
+                          dbias=out[2].view(n))
+    want, terms = plain.linear_gradients(dy, x_q, beta, w, al[0])
+    _check([out[0], out[1], out[2].view(n)], want, terms, [n, m, m], ["dx", "dW", "dbias"])
+    for r, o in zip(room, out):
+        assert float(r[0]) == 3.0 and bool((r[1 + o.numel():] == 3.0).all())
+
+
+@pytest.mark.parametrize("m,k,f", [(1, 512, 300), (9, 260, 1100), (16, 1024, 640), (50, 520, 200)])
+def test_backward_in_a_graph(dev, m, k, f):
+    """Captured once and replayed with other inputs and eager work between: the eager call's bits."""
+    torch, bl = dev
+    _say(f"backward in a graph M={m} K={k} F={f}")
+    s = _step_state(torch, bl, m, k, f, [14, m])
+    _step(torch, bl, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _step(torch, bl, s)
+    for seed in range(3):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        s["x"].copy_(torch.randn(m, k, device="cuda", generator=gen))
+        s["dy"].copy_(torch.randn(m, k, device="cuda", generator=gen) / m)
+        eager = [t.clone() for t in _step(torch, bl, s)]
+        for t in ("dh", "dWd", "dx", "dWg", "dWu"):
+            s[t].fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager, [s[q] for q in ("h", "y", "dh", "dWd", "dx", "dWg", "dWu")]):
+            assert torch.equal(a, b)
 
 
 def test_backward_against_differences(dev):
