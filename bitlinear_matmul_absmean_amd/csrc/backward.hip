@@ -28,8 +28,8 @@
 //   3. k_grad_split: d once more, scaled and split, rows being tokens (dx) and channels (dW);
 //   4. k_split_gemm: both products;
 //   5. k_split_sum, where a sum was cut into parts.
-// Up to 16 tokens one pass in fp32 takes their place (k_grad_few), up to 64, where the tiles are few, one that
-// does steps 1 to 4 tile by tile in LDS (k_grad_mid).
+// Up to 16 tokens one pass in fp32 takes their place (k_grad_few), beyond, where the tiles are few, one that does
+// steps 1 to 4 tile by tile in LDS (k_grad_mid).
 //
 // 2048 tokens, K = 4096, F = 11008 (gated): 1265 us: step 1 96, 2 5, 3 141 (copies of their bytes would
 // take 83, 1, 132), the products 1.02 ms.
@@ -648,10 +648,13 @@ __global__ __launch_bounds__(256) void k_split_sum(SplitArgs x, SplitArgs w, int
 // 130 and 151.  Bound: writing dW (180 MB in the 36.8 us of 4 tokens) up to 8 tokens, beyond it the
 // multiplications, 2 M + 3 instructions for a weight; more than 16 tokens do not fit the registers.
 // 512 workgroups (two to a compute unit): 256 took 46.3 and 1024 38.1 us where 512 took 36.8.
-constexpr int FEW_TOKENS = 16, FEW_K = 256, FEW_N = 64, FEW_GROUPS = 512;
+constexpr int FEW_TOKENS = 16, MID_TOKENS = 64, FEW_K = 256, FEW_N = 64, FEW_GROUPS = 512;
 struct FewPlan {
     int64_t kt, chunks, rows;      // column tiles; chunks of a projection, of `rows` rows
-    float* part;                   // [P chunks, M, K]
+    int64_t groups;                // of 64 tokens (k_grad_mid)
+    float* part;                   // dx [P chunks, M, K]
+    float* wpart;                  // several groups: dW [groups, P N, K] and the bias sums [groups, P N]
+    double* bpart;
     size_t bytes;
 };
 static FewPlan few_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws) {
@@ -661,8 +664,18 @@ static FewPlan few_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws) {
     const int64_t rows = (P * N * p.kt + FEW_GROUPS - 1) / FEW_GROUPS;
     p.rows = M > FEW_TOKENS ? FEW_N : rows < 16 ? 16 : (rows + 3) / 4 * 4;
     p.chunks = (N + p.rows - 1) / p.rows;
-    p.part = static_cast<float*>(ws);
-    p.bytes = ((size_t)(P * p.chunks * M * K) * 4 + 255) / 256 * 256;
+    p.groups = (M + MID_TOKENS - 1) / MID_TOKENS;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    size_t off = 0;
+    auto take = [&](int64_t bytes) {
+        uint8_t* q = base ? base + off : nullptr;
+        off += ((size_t)bytes + 255) / 256 * 256;
+        return q;
+    };
+    p.part = reinterpret_cast<float*>(take(P * p.chunks * M * K * 4));
+    p.wpart = reinterpret_cast<float*>(take(p.groups > 1 ? p.groups * P * N * K * 4 : 0));
+    p.bpart = reinterpret_cast<double*>(take(p.groups > 1 ? p.groups * P * N * 8 : 0));
+    p.bytes = off;
     return p;
 }
 
@@ -767,18 +780,21 @@ __global__ __launch_bounds__(256) void k_grad_few(BackwardArgs a, FewPlan p) {
 }
 
 // ---- some tokens, few tiles ---------------------------------------------------------------
-// The products on the matrix cores without panels: a workgroup takes 256 columns k of 64 rows n of one
-// projection and all tokens, up to 64.  It scales and splits its d as above, in both orders, into LDS, where x_q
-// and W are turned and stay bytes v + 128; dW is written at once, dx as a part for each 64 rows (a token's scale
-// is taken over those, and the part scaled back before it leaves), which k_few_sum adds.
+// The products on the matrix cores without panels: a workgroup takes 256 columns k, 64 rows n of one
+// projection and a group of 64 tokens.  It scales and splits its d as above, in both orders, into LDS, where x_q
+// and W are turned and stay bytes v + 128; dx is written as a part for each 64 rows, dW at once or, with
+// several groups, as a part for each (a scale is taken over a part's terms, and the part scaled back before it
+// leaves); k_few_sum adds them.
 // Against the steps above (us): gated, K = 1024, F = 2731, 61 tokens (344 workgroups) 25.1 and 38.6; K = 512,
 // N = 512, 64 tokens (16) 10.9 and 23.8; K = 2944, N = 5335 (1008), 32 tokens 34.8 and 44.2, 64 tokens 43.3 and
-// 45.5; gated, K = 2048, F = 5504 (1376), 64 tokens 65.3 and 55.5: the parts of dx, as many bytes as dW.
+// 45.5; gated, K = 2048, F = 5504 (1376), 64 tokens 65.3 and 55.5: the parts of dx, as many bytes as dW.  With parts
+// of dW: K = 512, N = 512, 250 tokens (64) 15.0 and 25.2; K = 1280, N = 1230, 256 tokens (400) 28.6 and 31.8; K = 1000,
+// N = 1023, 500 tokens (512) 32.0 and 38.6; K = 2048, N = 2048, 250 tokens (1024) 54.4 and 36.3.
 // Several tiles of rows in a workgroup halve those but hold twice the registers (gated, K = 1024, F = 2731, 61
 // tokens 33 us).  Bound: at a single tile latency, loads, three barriers and some 700 instructions of a wave.
 // LDS images: split gradients, rows of 64 values, the 16-byte unit u at position u ^ (row / 2) % 8; bytes,
 // columns of 64, the 16-byte unit u at position u ^ split_swizzle(column).
-constexpr int MID_TOKENS = 64, MID_GROUPS = 1024;
+constexpr int MID_TILES = 1024, MID_TILES_GROUPS = 512;
 constexpr int64_t MID_K = (int64_t)1 << 28;            // 16 K bytes are a 32-bit offset
 
 // acc[i] += sum_l (hi + lo)[row, l] b[column, l]: rows 32 i .. 32 i + 31 (i = 0 alone if !high), columns c0 ..
@@ -846,12 +862,19 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
     __shared__ float rscale[64], bscale[64];           // of the tokens: d alpha's scale, beta / 127
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = wave >> 2, tt = tid & 255;        // a tile of bytes is turned by 256 threads
-    const int64_t tile = blockIdx.x % p.kt, ch = blockIdx.x / p.kt, rowb = a.K >> 2, k0 = tile * FEW_K;
+    const uint32_t kt = (uint32_t)p.kt, chs = (uint32_t)p.chunks * (ACT == 0 ? 1 : 2), idx = blockIdx.x / kt;
+    const int64_t tile = blockIdx.x % kt, ch = idx % chs, grp = idx / chs, m0 = MID_TOKENS * grp;
+    const int64_t rowb = a.K >> 2, k0 = tile * FEW_K;
+    const int M = (int)(a.M - m0 < MID_TOKENS ? a.M - m0 : MID_TOKENS);
     const int q = ACT != 0 && ch >= p.chunks;
     const int64_t n0 = (ch - q * p.chunks) * FEW_N;
     const uint8_t* w = q ? a.w1 : a.w0;
+    const int8_t* xq = a.xq + m0 * a.K;
+    const float *dy = a.dy + m0 * a.N, *sg = ACT == 0 ? nullptr : a.g + m0 * a.N, *su = ACT == 0 ? nullptr : a.u + m0 * a.N;
     float* dw = q ? a.dw1 : a.dw0;
     float* db = tile > 0 ? nullptr : q ? a.db1 : a.db0;
+    if (dw && p.groups > 1) dw = p.wpart + (grp * (ACT == 0 ? 1 : 2) + q) * a.N * a.K;
+    double* bp = p.bpart + (grp * (ACT == 0 ? 1 : 2) + q) * a.N;   // several groups: in db's place
     const float al = q ? a.al1[0] : a.al0[0];
     // tokens and rows past the end repeat the last (their d is zero), columns past it are not stored
     u32x4 x[2], wr{};
@@ -863,7 +886,7 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
             for (int i = 0; i < 4; ++i) {
                 const int64_t m = 4 * (tt >> 4) + i;
                 uint32_t v;
-                __builtin_memcpy(&v, a.xq + (m < a.M ? m : a.M - 1) * a.K + (k < a.K ? k : 0), 4);
+                __builtin_memcpy(&v, xq + (m < M ? m : M - 1) * a.K + (k < a.K ? k : 0), 4);
                 x[c][i] = v;
             }
         }
@@ -890,21 +913,22 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
     // d of tokens 8 wave .. 8 wave + 7 in row n0 + lane, zeros past the ends; offsets below 2^31 bytes
     float d[8];
     {
-        const uint32_t n = (uint32_t)(n0 + lane < a.N ? n0 + lane : a.N - 1), M = (uint32_t)a.M, N = (uint32_t)a.N;
+        const uint32_t n = (uint32_t)(n0 + lane < a.N ? n0 + lane : a.N - 1), N = (uint32_t)a.N;
         auto at = [](const float* p, uint32_t i) { return *reinterpret_cast<const float*>(reinterpret_cast<const char*>(p) + 4u * i); };
         float y[8], g[8], u[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const uint32_t m = 8 * wave + t, i = (m < M ? m : M - 1) * N + n;
-            y[t] = at(a.dy, i);
-            g[t] = ACT == 0 ? 0.0f : at(a.g, i);
-            u[t] = ACT == 0 ? 0.0f : at(a.u, i);
+            const int m = 8 * wave + t;
+            const uint32_t i = (uint32_t)(m < M ? m : M - 1) * N + n;
+            y[t] = at(dy, i);
+            g[t] = ACT == 0 ? 0.0f : at(sg, i);
+            u[t] = ACT == 0 ? 0.0f : at(su, i);
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             float e[2];
             grad_of<ACT>(y[t], g[t], u[t], e);
-            d[t] = n0 + lane < a.N && 8 * wave + t < a.M ? (q ? e[1] : e[0]) : 0.0f;
+            d[t] = n0 + lane < a.N && 8 * wave + t < M ? (q ? e[1] : e[0]) : 0.0f;
         }
     }
     // x_q: four tiles of 64 columns, turned in the split gradients' place; W
@@ -921,7 +945,7 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
         if (lane == 0) {
             rscale[m] = pow2f(s);
             rinv[m] = pow2f(-s);
-            bscale[m] = m < a.M ? a.beta[m] / 127.0f : 0.0f;
+            bscale[m] = m < M ? a.beta[m0 + m] / 127.0f : 0.0f;
         }
     }
     if (dw) {
@@ -987,47 +1011,75 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
         double v = 0.0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v += csum[i][tid];
-        db[n0 + tid] = (float)v;
+        if (p.groups > 1) bp[n0 + tid] = v;
+        else db[n0 + tid] = (float)v;
     }
     __syncthreads();
     const int64_t left = a.K - (k0 + 32 * wave);       // columns from the wave's first to the end
     if (a.dx) {
         f32x16 acc[2] = {};
-        mid_multiply(acc, sp[0], sp[1], wb, 32 * wave, a.M > 32, true);
-        mid_store(acc, rinv, (gridDim.x == p.kt ? a.dx : p.part + ch * a.M * a.K) + k0 + 32 * wave, a.K, a.M, left);
+        mid_multiply(acc, sp[0], sp[1], wb, 32 * wave, M > 32, true);
+        mid_store(acc, rinv, (chs == 1 ? a.dx : p.part + ch * a.M * a.K) + m0 * a.K + k0 + 32 * wave, a.K, M, left);
     }
     if (dw) {
         f32x16 acc[2] = {};
-        mid_multiply(acc, sp[2], sp[3], xb, 32 * wave, true, a.M > 32);
+        mid_multiply(acc, sp[2], sp[3], xb, 32 * wave, true, M > 32);
         mid_store(acc, cinv, dw + n0 * a.K + k0 + 32 * wave, a.K, a.N - n0, left);
     }
 }
 
-// dx from the chunks' parts: 256 elements per workgroup, a wave every fourth chunk.
-__global__ __launch_bounds__(256) void k_few_sum(const float* __restrict__ part, float* __restrict__ dx, int64_t n, int64_t chunks) {
+// Sums of parts, in their order: dx from the chunks', dW from the token groups', 256 elements per workgroup, a wave
+// every fourth part; last the bias sums.
+struct PartSum {
+    const float* part;
+    float* out;
+    int64_t n, parts, stride, blocks;
+};
+__global__ __launch_bounds__(256) void k_few_sum(PartSum x, PartSum w0, PartSum w1, const double* __restrict__ bpart, float* db0,
+                                                 float* db1, int64_t N, int64_t P, int64_t groups) {
     __shared__ __align__(16) float4 red[3][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t e = (int64_t)blockIdx.x * 256 + 4 * lane, el = e < n ? e : 0;
+    int64_t b = blockIdx.x;
+    PartSum a = x;
+    if (b >= a.blocks) {
+        b -= a.blocks;
+        a = w0;
+    }
+    if (b >= a.blocks) {
+        b -= a.blocks;
+        a = w1;
+    }
+    if (b >= a.blocks) {
+        const int64_t i = (b - a.blocks) * 256 + threadIdx.x;
+        float* out = i < N ? db0 : db1;
+        if (i >= P * N || !out) return;
+        double s = 0.0;
+        for (int64_t g = 0; g < groups; ++g) s += bpart[g * P * N + i];
+        out[i < N ? i : i - N] = (float)s;
+        return;
+    }
+    const int64_t e = b * 256 + 4 * lane, el = e < a.n ? e : 0;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-    for (int64_t c = wave; c < chunks; c += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(part + c * n + el);
+    for (int64_t c = wave; c < a.parts; c += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part + c * a.stride + el);
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
     if (wave > 0) red[wave - 1][lane] = s;
     __syncthreads();
-    if (wave > 0 || e >= n) return;
+    if (wave > 0 || e >= a.n) return;
 #pragma unroll
     for (int w = 0; w < 3; ++w) {
         const float4 v = red[w][lane];
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    __builtin_memcpy(dx + e, &s, 16);
+    __builtin_memcpy(a.out + e, &s, 16);
 }
 
 static bool use_mid(int64_t M, int64_t K, int64_t N, bool gated) {
-    return M > FEW_TOKENS && M <= MID_TOKENS && K < MID_K &&
-           ((K + FEW_K - 1) / FEW_K) * ((N + FEW_N - 1) / FEW_N) * (gated ? 2 : 1) <= MID_GROUPS;
+    const int64_t groups = (M + MID_TOKENS - 1) / MID_TOKENS;
+    const int64_t tiles = ((K + FEW_K - 1) / FEW_K) * ((N + FEW_N - 1) / FEW_N) * (gated ? 2 : 1) * groups;
+    return M > FEW_TOKENS && K < MID_K && tiles <= (groups == 1 ? MID_TILES : MID_TILES_GROUPS);
 }
 
 // MT: tokens that k_grad_few holds, 0 for k_grad_mid.
@@ -1035,13 +1087,20 @@ template <int ACT, int MT>
 static hipError_t launch_few(const BackwardArgs& a, hipStream_t s) {
     FewPlan p = few_plan(a.M, a.K, a.N, ACT != 0, a.ws);
     if (!a.dx && !a.dw0) p.kt = 1;                     // the bias sums alone
-    const int64_t chunks = (ACT == 0 ? 1 : 2) * p.chunks, n = a.M * a.K;
+    const int64_t P = ACT == 0 ? 1 : 2, chunks = P * p.chunks, n = a.M * a.K;
     if constexpr (MT > 0)
         hipLaunchKernelGGL((k_grad_few<ACT, MT>), dim3((unsigned)(chunks * p.kt)), dim3(256), 0, s, a, p);
     else
-        hipLaunchKernelGGL(k_grad_mid<ACT>, dim3((unsigned)(chunks * p.kt)), dim3(512), 0, s, a, p);
-    if (a.dx && chunks > 1)
-        hipLaunchKernelGGL(k_few_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p.part, a.dx, n, chunks);
+        hipLaunchKernelGGL(k_grad_mid<ACT>, dim3((unsigned)(chunks * p.kt * p.groups)), dim3(512), 0, s, a, p);
+    auto sum = [](const float* part, float* out, int64_t n, int64_t parts, int64_t stride) {
+        return PartSum{part, out, n, parts, stride, out && parts > 1 ? (n + 255) / 256 : 0};
+    };
+    const PartSum x = sum(p.part, a.dx, n, chunks, n), w0 = sum(p.wpart, a.dw0, a.N * a.K, p.groups, P * a.N * a.K),
+                  w1 = sum(p.wpart + a.N * a.K, a.dw1, a.N * a.K, p.groups, P * a.N * a.K);
+    const int64_t bias = (a.db0 || a.db1) && p.groups > 1 ? (P * a.N + 255) / 256 : 0;
+    if (x.blocks + w0.blocks + w1.blocks + bias)
+        hipLaunchKernelGGL(k_few_sum, dim3((unsigned)(x.blocks + w0.blocks + w1.blocks + bias)), dim3(256), 0, s, x, w0, w1, p.bpart,
+                           a.db0, a.db1, a.N, P, p.groups);
     return hipGetLastError();
 }
 

@@ -155,6 +155,8 @@ GRADS += [(3, 4, 1), (4, 8, 17), (5, 1028, 70), (8, 4096, 2501), (9, 4100, 4700)
 # up to 64 tokens: short rows of codes, rows and columns past a tile, and more tiles than go in one pass
 GRADS += [(17, 4, 1), (20, 8, 70), (33, 12, 64), (64, 16, 65), (32, 1028, 129), (40, 260, 700), (64, 2052, 190),
           (24, 4100, 4200), (61, 8200, 2100)]
+# more tokens, in too many tiles for one pass: every size of tile of the maxima
+GRADS += [(100, 2100, 2100), (129, 4100, 700), (257, 2052, 1030), (300, 260, 4100), (700, 68, 3100)]
 
 
 def _check(got, want, terms, lengths, names):
@@ -221,10 +223,9 @@ def test_gated_backward(dev, m, k, f):
             assert alone[q] is None if q not in keep else torch.equal(alone[q], out[names.index(q)]), (keep, q)
 
 
-def _wide_range(dev, m):
+def _wide_range(dev, m, k=132, n=90):
     torch, bl = dev
     rng = np.random.default_rng(3)
-    k, n = 132, 90
     dy = _f32(rng.standard_normal((m, n)))
     dy[0] = 0
     dy[:, 1] = 0
@@ -257,11 +258,14 @@ def test_backward_wide_range_few_tokens(dev, m):
     _wide_range(dev, m)
 
 
-@pytest.mark.parametrize("m", [5, 13, 40, 100])
-def test_backward_unaligned_views(dev, m):
+def test_backward_wide_range_many_tiles(dev):
+    _wide_range(dev, 70, 2100, 2300)
+
+
+@pytest.mark.parametrize("m,k,n", [(5, 268, 131), (13, 268, 131), (40, 268, 131), (100, 268, 131), (100, 2100, 2107)])
+def test_backward_unaligned_views(dev, m, k, n):
     """Every tensor off its alignment; what lies around the outputs stays."""
     torch, bl = dev
-    k, n = 268, 131
     _say(f"backward unaligned M={m}")
     rng = np.random.default_rng([13, m])
     dy = _f32(rng.standard_normal((m, n)))
