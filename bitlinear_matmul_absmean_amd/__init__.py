@@ -465,11 +465,22 @@ def _stream_on(stream, index):
     return raw(index) if raw is not None else _stream(None)
 
 
-def _held(t, stream):
-    """A buffer that the binding allocated for the call alone: kept from being handed out again before
-    the work on an explicitly given stream is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
+def _empty(shape, dtype, device, stream, scratch=False):
+    """A tensor that the binding allocates for a call on `stream` (None: the current stream).
+
+    The block comes from the pool of the stream that the call runs on: one from the current stream's
+    pool may still be in use by work queued there before the call, which a given stream does not
+    wait for.  What is handed back is recorded on the caller's stream as well, so that the block is
+    not handed out again before the caller's work on it is done; scratch nobody else sees."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -490,11 +501,11 @@ def bitlinear_gated_forward(x, Wg_packed, alpha_g, Wu_packed, alpha_u, act, bias
     M, K, dev = _rows(x, "x")
     F = _first(Wg_packed, "Wg_packed")
     if h is None:
-        h = torch.empty((M, F), dtype=torch.float32, device=dev)
+        h = _empty((M, F), torch.float32, dev, stream)
     if x_q is None:
-        x_q = _held(torch.empty((M, K), dtype=torch.int8, device=dev), stream)
+        x_q = _empty((M, K), torch.int8, dev, stream, scratch=True)
     if beta is None:
-        beta = _held(torch.empty(M, dtype=torch.float32, device=dev), stream)
+        beta = _empty(M, torch.float32, dev, stream, scratch=True)
     f32, u8 = torch.float32, torch.uint8
     _check("bitlinear_gated_forward", lib.bitlinear_gated_forward(
         _shaped(x, f32, "x", (M, K), dev), M, K, _shaped(Wg_packed, u8, "Wg_packed", (F, K // 4), dev),
@@ -519,8 +530,7 @@ def bitlinear_gated_backward_workspace_size(M, K, F) -> int:
 def _workspace(workspace, need, index, stream):
     """The given workspace, or a new one of the bytes needed, its pointer and its bytes."""
     if workspace is None:
-        torch = _torch()
-        workspace = _held(torch.empty(max(need, 256), dtype=torch.uint8, device=index), stream)
+        workspace = _empty(max(need, 256), _torch().uint8, index, stream, scratch=True)
     ptr = _dev(workspace, _torch().uint8, "workspace")
     if workspace.get_device() != index:
         raise ValueError(f"workspace must be on device {index}, got {workspace.device}")
@@ -536,8 +546,8 @@ def bitlinear_backward(dy, x_q, beta, W_packed, alpha, dx=None, dW=None, dbias=N
     _, K, _ = _rows(x_q, "x_q")
     f32 = torch.float32
     if dx is None and dW is None and dbias is None:
-        dx = torch.empty((M, K), dtype=f32, device=dev)
-        dW = torch.empty((N, K), dtype=f32, device=dev)
+        dx = _empty((M, K), f32, dev, stream)
+        dW = _empty((N, K), f32, dev, stream)
     workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_backward_workspace_size(M, K, N), dev, stream)
     _check("bitlinear_backward", lib.bitlinear_backward(
         _shaped(dy, f32, "dy", (M, N), dev), M, N, _shaped(x_q, torch.int8, "x_q", (M, K), dev),
@@ -558,9 +568,9 @@ def bitlinear_gated_backward(dh, g, u, x_q, beta, Wg_packed, alpha_g, Wu_packed,
     _, K, _ = _rows(x_q, "x_q")
     f32, u8 = torch.float32, torch.uint8
     if dx is None and dWg is None and dWu is None and dbias_g is None and dbias_u is None:
-        dx = torch.empty((M, K), dtype=f32, device=dev)
-        dWg = torch.empty((F, K), dtype=f32, device=dev)
-        dWu = torch.empty((F, K), dtype=f32, device=dev)
+        dx = _empty((M, K), f32, dev, stream)
+        dWg = _empty((F, K), f32, dev, stream)
+        dWu = _empty((F, K), f32, dev, stream)
     workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_gated_backward_workspace_size(M, K, F), dev, stream)
     _check("bitlinear_gated_backward", lib.bitlinear_gated_backward(
         _shaped(dh, f32, "dh", (M, F), dev), _shaped(g, f32, "g", (M, F), dev), _shaped(u, f32, "u", (M, F), dev), M, F,
@@ -578,9 +588,9 @@ def bitlinear_quantize_weights_i8(W, W_q=None, gamma=None, stream=None):
     torch = _torch()
     N, K, dev = _rows(W, "W")
     if W_q is None:
-        W_q = torch.empty((N, K), dtype=torch.int8, device=dev)
+        W_q = _empty((N, K), torch.int8, dev, stream)
     if gamma is None:
-        gamma = torch.empty(N, dtype=torch.float32, device=dev)
+        gamma = _empty(N, torch.float32, dev, stream)
     _check("bitlinear_quantize_weights_i8", lib.bitlinear_quantize_weights_i8(
         _shaped(W, torch.float32, "W", (N, K), dev), N, K, _shaped(W_q, torch.int8, "W_q", (N, K), dev),
         _shaped(gamma, torch.float32, "gamma", (N,), dev), _stream_on(stream, dev)))
@@ -595,9 +605,9 @@ def bitlinear_forward_i8(x_q, beta, W_q, gamma, bias=None, y=None, acc=None, str
     N = _first(W_q, "W_q")
     f32 = torch.float32
     if y is None:
-        y = torch.empty((M, N), dtype=f32, device=dev)
+        y = _empty((M, N), f32, dev, stream)
     if acc is True:
-        acc = torch.empty((M, N), dtype=torch.int32, device=dev)
+        acc = _empty((M, N), torch.int32, dev, stream)
     elif acc is False:
         acc = None
     _check("bitlinear_forward_i8", lib.bitlinear_forward_i8(
