@@ -5,6 +5,10 @@ Argument marshalling only: every step of the computation runs in the HIP kernels
 memory (tensors) and the current HIP stream; nothing here computes on the host.  If the
 library has not been built, importing this package raises -- there is no fallback.
 
+A call runs on ``stream`` if one is given, else on the current stream; what it allocates belongs
+to the stream it runs on.  Ordering it with the work that made its arguments and that uses its
+results is up to the caller.
+
 The functions carry the C names.  ``lib`` exposes the raw C entry points (ctypes) for
 callers that manage pointers themselves.
 """
@@ -137,17 +141,36 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _empty(shape, dtype, device, stream, scratch=False):
+    """A tensor that the binding allocates for a call on `stream` (None: the current stream).
+
+    The block comes from the pool of the stream that the call runs on: one from the current stream's
+    pool may still be in use by work queued there before the call, which a given stream does not
+    wait for.  What is handed back is recorded on the caller's stream as well, so that the block is
+    not handed out again before the caller's work on it is done; scratch nobody else sees."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def bitlinear_quantize_weights(W, W_packed=None, alpha=None, workspace=None, stream=None):
     """W [N, K] fp32 -> (W_packed uint8 [N, K/4], alpha fp32 [1]) on the device."""
     torch = _torch()
     N, K = W.shape
     if W_packed is None:
-        W_packed = torch.empty((N, K // 4), dtype=torch.uint8, device=W.device)
+        W_packed = _empty((N, K // 4), torch.uint8, W.device, stream)
     if alpha is None:
-        alpha = torch.empty(1, dtype=torch.float32, device=W.device)
+        alpha = _empty(1, torch.float32, W.device, stream)
     need = lib.bitlinear_quantize_weights_workspace_size(N, K)
     if workspace is None:
-        workspace = torch.empty(max(need, 8), dtype=torch.uint8, device=W.device)
+        workspace = _empty(max(need, 8), torch.uint8, W.device, stream, scratch=True)
     _check("bitlinear_quantize_weights", lib.bitlinear_quantize_weights(
         _dev(W, torch.float32, "W", N * K), N, K, _dev(W_packed, torch.uint8, "W_packed", N * (K // 4)),
         _dev(alpha, torch.float32, "alpha", 1), _dev(workspace, torch.uint8, "workspace"),
@@ -172,9 +195,9 @@ def bitlinear_quantize_weights_rows(W, W_packed=None, alpha_rows=None, stream=No
     torch = _torch()
     N, K = W.shape
     if W_packed is None:
-        W_packed = torch.empty((N, K // 4), dtype=torch.uint8, device=W.device)
+        W_packed = _empty((N, K // 4), torch.uint8, W.device, stream)
     if alpha_rows is None:
-        alpha_rows = torch.empty(N, dtype=torch.float32, device=W.device)
+        alpha_rows = _empty(N, torch.float32, W.device, stream)
     _check("bitlinear_quantize_weights_rows", lib.bitlinear_quantize_weights_rows(
         _dev(W, torch.float32, "W", N * K), N, K, _dev(W_packed, torch.uint8, "W_packed", N * (K // 4)),
         _dev(alpha_rows, torch.float32, "alpha_rows", N), _stream(stream)))
@@ -186,9 +209,9 @@ def bitlinear_quantize_act(x, x_q=None, beta=None, stream=None):
     torch = _torch()
     M, K = x.shape
     if x_q is None:
-        x_q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        x_q = _empty((M, K), torch.int8, x.device, stream)
     if beta is None:
-        beta = torch.empty(M, dtype=torch.float32, device=x.device)
+        beta = _empty(M, torch.float32, x.device, stream)
     _check("bitlinear_quantize_act", lib.bitlinear_quantize_act(
         _dev(x, torch.float32, "x", M * K), M, K, _dev(x_q, torch.int8, "x_q", M * K),
         _dev(beta, torch.float32, "beta", M), _stream(stream)))
@@ -201,12 +224,12 @@ def bitlinear_quantize_weights_t5(W, W_t5=None, alpha=None, workspace=None, stre
     N, K = W.shape
     rb = lib.bitlinear_t5_row_bytes(K)
     if W_t5 is None:
-        W_t5 = torch.empty((N, rb), dtype=torch.uint8, device=W.device)
+        W_t5 = _empty((N, rb), torch.uint8, W.device, stream)
     if alpha is None:
-        alpha = torch.empty(1, dtype=torch.float32, device=W.device)
+        alpha = _empty(1, torch.float32, W.device, stream)
     need = lib.bitlinear_quantize_weights_workspace_size(N, K)
     if workspace is None:
-        workspace = torch.empty(max(need, 8), dtype=torch.uint8, device=W.device)
+        workspace = _empty(max(need, 8), torch.uint8, W.device, stream, scratch=True)
     _check("bitlinear_quantize_weights_t5", lib.bitlinear_quantize_weights_t5(
         _dev(W, torch.float32, "W", N * K), N, K, _dev(W_t5, torch.uint8, "W_t5", N * rb),
         _dev(alpha, torch.float32, "alpha", 1),
@@ -221,7 +244,7 @@ def bitlinear_repack_t5(W_packed, K, W_t5=None, stream=None):
     if W_packed.shape[1] * 4 != K:
         raise ValueError("W_packed must be [N, K/4]")
     if W_t5 is None:
-        W_t5 = torch.empty((N, lib.bitlinear_t5_row_bytes(K)), dtype=torch.uint8, device=W_packed.device)
+        W_t5 = _empty((N, lib.bitlinear_t5_row_bytes(K)), torch.uint8, W_packed.device, stream)
     _check("bitlinear_repack_t5", lib.bitlinear_repack_t5(
         _dev(W_packed, torch.uint8, "W_packed"), N, K,
         _dev(W_t5, torch.uint8, "W_t5", N * lib.bitlinear_t5_row_bytes(K)), _stream(stream)))
@@ -236,7 +259,7 @@ def bitlinear_forward_t5(x_q, beta, W_t5, alpha, bias=None, y=None, stream=None)
     if W_t5.shape[1] != lib.bitlinear_t5_row_bytes(K):
         raise ValueError("W_t5 must be [N, bitlinear_t5_row_bytes(K)]")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x_q.device)
+        y = _empty((M, N), torch.float32, x_q.device, stream)
     _check("bitlinear_forward_t5", lib.bitlinear_forward_t5(
         _dev(x_q, torch.int8, "x_q"), _dev(beta, torch.float32, "beta", M), M, K, _dev(W_t5, torch.uint8, "W_t5"),
         _dev(alpha, torch.float32, "alpha", 1), N,
@@ -250,9 +273,9 @@ def bitlinear_quantize_weights_blocks(W, W_packed=None, alpha_blocks=None, strea
     torch = _torch()
     N, K = W.shape
     if W_packed is None:
-        W_packed = torch.empty((N, K // 4), dtype=torch.uint8, device=W.device)
+        W_packed = _empty((N, K // 4), torch.uint8, W.device, stream)
     if alpha_blocks is None:
-        alpha_blocks = torch.empty((N, K // 128), dtype=torch.float32, device=W.device)
+        alpha_blocks = _empty((N, K // 128), torch.float32, W.device, stream)
     _check("bitlinear_quantize_weights_blocks", lib.bitlinear_quantize_weights_blocks(
         _dev(W, torch.float32, "W", N * K), N, K, _dev(W_packed, torch.uint8, "W_packed", N * (K // 4)),
         _dev(alpha_blocks, torch.float32, "alpha_blocks", N * (K // 128)), _stream(stream)))
@@ -267,7 +290,7 @@ def bitlinear_forward_blocks(x_q, beta, W_packed, alpha_blocks, bias=None, y=Non
     if W_packed.shape[1] * 4 != K:
         raise ValueError("W_packed must be [N, K/4]")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x_q.device)
+        y = _empty((M, N), torch.float32, x_q.device, stream)
     _check("bitlinear_forward_blocks", lib.bitlinear_forward_blocks(
         _dev(x_q, torch.int8, "x_q"), _dev(beta, torch.float32, "beta", M), M, K,
         _dev(W_packed, torch.uint8, "W_packed"), _dev(alpha_blocks, torch.float32, "alpha_blocks", N * (K // 128)),
@@ -287,18 +310,18 @@ def bitlinear_mlp_forward(x, W1_packed, alpha1, W2_packed, alpha2, bias1=None, b
     if W1_packed.shape[1] * 4 != d_model or W2_packed.shape != (d_model, d_ff // 4):
         raise ValueError("W1_packed must be [d_ff, d_model/4] and W2_packed [d_model, d_ff/4]")
     if y is None:
-        y = torch.empty((M, d_model), dtype=torch.float32, device=x.device)
+        y = _empty((M, d_model), torch.float32, x.device, stream)
     if g is None:
-        g = torch.empty((M, d_ff), dtype=torch.float32, device=x.device)
+        g = _empty((M, d_ff), torch.float32, x.device, stream)
     if M > 1:
         if x_q1 is None:
-            x_q1 = torch.empty((M, d_model), dtype=torch.int8, device=x.device)
+            x_q1 = _empty((M, d_model), torch.int8, x.device, stream, scratch=True)
         if beta1 is None:
-            beta1 = torch.empty(M, dtype=torch.float32, device=x.device)
+            beta1 = _empty(M, torch.float32, x.device, stream, scratch=True)
         if x_q2 is None:
-            x_q2 = torch.empty((M, d_ff), dtype=torch.int8, device=x.device)
+            x_q2 = _empty((M, d_ff), torch.int8, x.device, stream, scratch=True)
         if beta2 is None:
-            beta2 = torch.empty(M, dtype=torch.float32, device=x.device)
+            beta2 = _empty(M, torch.float32, x.device, stream, scratch=True)
     opt = lambda t, dt, n, k: _dev(t, dt, n, k) if t is not None else None
     _check("bitlinear_mlp_forward", lib.bitlinear_mlp_forward(
         _dev(x, torch.float32, "x", M * d_model), M, d_model, d_ff, _dev(W1_packed, torch.uint8, "W1_packed"),
@@ -316,7 +339,7 @@ def bitlinear_hadamard_rows(x, block, signs=None, out=None, stream=None):
     torch = _torch()
     M, K = x.shape
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float32, device=x.device)
+        out = _empty((M, K), torch.float32, x.device, stream)
     _check("bitlinear_hadamard_rows", lib.bitlinear_hadamard_rows(
         _dev(x, torch.float32, "x", M * K), M, K, int(block),
         _dev(signs, torch.int8, "signs", K) if signs is not None else None,
@@ -329,9 +352,9 @@ def bitlinear_quantize_act_hadamard(x, block, signs=None, x_q=None, beta=None, s
     torch = _torch()
     M, K = x.shape
     if x_q is None:
-        x_q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        x_q = _empty((M, K), torch.int8, x.device, stream)
     if beta is None:
-        beta = torch.empty(M, dtype=torch.float32, device=x.device)
+        beta = _empty(M, torch.float32, x.device, stream)
     _check("bitlinear_quantize_act_hadamard", lib.bitlinear_quantize_act_hadamard(
         _dev(x, torch.float32, "x", M * K), M, K, int(block),
         _dev(signs, torch.int8, "signs", K) if signs is not None else None,
@@ -348,7 +371,7 @@ def bitlinear_forward_fused_hadamard(x, block, signs, W_packed, alpha, bias=None
     if W_packed.shape[1] * 4 != K:
         raise ValueError("W_packed must be [N, K/4]")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty((M, N), torch.float32, x.device, stream)
     opt = lambda t, dt, n, k: _dev(t, dt, n, k) if t is not None else None
     _check("bitlinear_forward_fused_hadamard", lib.bitlinear_forward_fused_hadamard(
         _dev(x, torch.float32, "x", M * K), M, K, int(block), opt(signs, torch.int8, "signs", K),
@@ -365,9 +388,9 @@ def _forward(fn, what, x_q, beta, W_packed, alpha, bias, y, acc, stream, alpha_n
     if W_packed.shape[1] * 4 != K:
         raise ValueError("W_packed must be [N, K/4]")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x_q.device)
+        y = _empty((M, N), torch.float32, x_q.device, stream)
     if acc is True:
-        acc = torch.empty((M, N), dtype=torch.int32, device=x_q.device)
+        acc = _empty((M, N), torch.int32, x_q.device, stream)
     acc_ptr = _dev(acc, torch.int32, "acc", M * N) if acc is not None and acc is not False else None
     bias_ptr = _dev(bias, torch.float32, "bias", N) if bias is not None else None
     _check(what, fn(
@@ -397,9 +420,9 @@ def _forward_fused(name, x, W_packed, alpha, bias, y, x_q, beta, acc, stream):
     if W_packed.shape[1] * 4 != K:
         raise ValueError("W_packed must be [N, K/4]")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty((M, N), torch.float32, x.device, stream)
     if acc is True:
-        acc = torch.empty((M, N), dtype=torch.int32, device=x.device)
+        acc = _empty((M, N), torch.int32, x.device, stream)
     acc_ptr = _dev(acc, torch.int32, "acc", M * N) if acc is not None and acc is not False else None
     _check(name, getattr(lib, name)(
         _dev(x, torch.float32, "x", M * K), M, K, _dev(W_packed, torch.uint8, "W_packed"),
@@ -463,25 +486,6 @@ def _stream_on(stream, index):
         return stream.cuda_stream
     raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
     return raw(index) if raw is not None else _stream(None)
-
-
-def _empty(shape, dtype, device, stream, scratch=False):
-    """A tensor that the binding allocates for a call on `stream` (None: the current stream).
-
-    The block comes from the pool of the stream that the call runs on: one from the current stream's
-    pool may still be in use by work queued there before the call, which a given stream does not
-    wait for.  What is handed back is recorded on the caller's stream as well, so that the block is
-    not handed out again before the caller's work on it is done; scratch nobody else sees."""
-    torch = _torch()
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if not scratch:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
 
 
 def _first(t, name):

@@ -113,6 +113,32 @@ def _new_calls(bl):  # noqa: F811
     }
 
 
+def _old_calls(bl):  # noqa: F811
+    f, i8, u8 = _operands()
+    one, w = f(1), u8(N, K // 4)
+    return {
+        "quantize_weights": lambda s: bl.bitlinear_quantize_weights(f(N, K), stream=s),
+        "quantize_weights_rows": lambda s: bl.bitlinear_quantize_weights_rows(f(N, K), stream=s),
+        "quantize_act": lambda s: bl.bitlinear_quantize_act(f(M, K), stream=s),
+        "quantize_weights_t5": lambda s: bl.bitlinear_quantize_weights_t5(f(N, K), stream=s),
+        "repack_t5": lambda s: bl.bitlinear_repack_t5(w, K, stream=s),
+        "forward_t5": lambda s: bl.bitlinear_forward_t5(i8(M, K), f(M), u8(N, 64), one, stream=s),
+        "quantize_weights_blocks": lambda s: bl.bitlinear_quantize_weights_blocks(f(N, 2 * K), stream=s),
+        "forward_blocks": lambda s: bl.bitlinear_forward_blocks(i8(M, K), f(M), w, f(N), stream=s),
+        "mlp_forward": lambda s: bl.bitlinear_mlp_forward(f(M, K), w, one, w, one, stream=s),
+        "hadamard_rows": lambda s: bl.bitlinear_hadamard_rows(f(M, K), 64, stream=s),
+        "quantize_act_hadamard": lambda s: bl.bitlinear_quantize_act_hadamard(f(M, K), 64, stream=s),
+        "forward_fused_hadamard": lambda s: bl.bitlinear_forward_fused_hadamard(f(M, K), 64, None, w, one, stream=s),
+        "forward": lambda s: bl.bitlinear_forward(i8(M, K), f(M), w, one, acc=True, stream=s),
+        "forward_rows": lambda s: bl.bitlinear_forward_rows(i8(M, K), f(M), w, f(N), acc=True, stream=s),
+        "forward_fused": lambda s: bl.bitlinear_forward_fused(f(M, K), w, one, acc=True, stream=s),
+        "forward_fused_rows": lambda s: bl.bitlinear_forward_fused_rows(f(M, K), w, f(N), acc=True, stream=s),
+    }
+
+
+OLD = ["quantize_weights", "quantize_weights_rows", "quantize_act", "quantize_weights_t5", "repack_t5", "forward_t5",
+       "quantize_weights_blocks", "forward_blocks", "mlp_forward", "hadamard_rows", "quantize_act_hadamard",
+       "forward_fused_hadamard", "forward", "forward_rows", "forward_fused", "forward_fused_rows"]
 NEW = ["gated_forward", "backward", "gated_backward", "quantize_weights_i8", "forward_i8"]
 
 
@@ -150,3 +176,13 @@ def test_buffers_of_a_call_on_a_given_stream(bl, monkeypatch, name):  # noqa: F8
 @pytest.mark.parametrize("name", NEW)
 def test_buffers_of_a_call_on_the_current_stream(bl, monkeypatch, name):  # noqa: F811
     _current_stream(bl, monkeypatch, _new_calls(bl)[name])
+
+
+@pytest.mark.parametrize("name", OLD)
+def test_buffers_of_a_single_layer_call_on_a_given_stream(bl, monkeypatch, name):  # noqa: F811
+    _given_stream(bl, monkeypatch, _old_calls(bl)[name])
+
+
+@pytest.mark.parametrize("name", OLD)
+def test_buffers_of_a_single_layer_call_on_the_current_stream(bl, monkeypatch, name):  # noqa: F811
+    _current_stream(bl, monkeypatch, _old_calls(bl)[name])
