@@ -481,8 +481,11 @@ def _rows(t, name):
 
 
 def _stream_on(stream, index):
-    """_stream for a call whose tensors are known to lie on the current device `index`."""
+    """_stream for a call whose tensors are known to lie on the current device `index`, which a given
+    stream has to be of too."""
     if stream is not None:
+        if getattr(stream, "device_index", index) != index:
+            raise ValueError(f"stream must be of device {index}")
         return stream.cuda_stream
     raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
     return raw(index) if raw is not None else _stream(None)

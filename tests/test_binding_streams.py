@@ -186,3 +186,13 @@ def test_buffers_of_a_single_layer_call_on_a_given_stream(bl, monkeypatch, name)
 @pytest.mark.parametrize("name", OLD)
 def test_buffers_of_a_single_layer_call_on_the_current_stream(bl, monkeypatch, name):  # noqa: F811
     _current_stream(bl, monkeypatch, _old_calls(bl)[name])
+
+
+@pytest.mark.parametrize("name", NEW)
+def test_a_stream_of_another_device_is_refused(bl, monkeypatch, name):  # noqa: F811
+    library = Library()
+    monkeypatch.setattr(bl, "_torch", Torch)
+    monkeypatch.setattr(bl, "lib", library)
+    with pytest.raises(ValueError, match="stream"):
+        _new_calls(bl)[name](Stream(77, device_index=1))
+    assert library.streams == []
