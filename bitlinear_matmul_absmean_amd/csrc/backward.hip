@@ -859,7 +859,7 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
     __shared__ double csum[8][64];
     __shared__ __align__(16) float rinv[64];
     __shared__ __align__(16) float cinv[64];
-    __shared__ float rscale[64], bscale[64];           // of the tokens: d alpha's scale, beta / 127
+    __shared__ float rscale[64];                       // of the tokens: d alpha's scale
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = wave >> 2, tt = tid & 255;        // a tile of bytes is turned by 256 threads
     const uint32_t kt = (uint32_t)p.kt, chs = (uint32_t)p.chunks * (ACT == 0 ? 1 : 2), idx = blockIdx.x / kt;
@@ -938,20 +938,21 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
         for (int c = 0; c < 2; ++c) turn_put(room + 64 * 17 * (2 * half + c), x[c], tt);
     }
     if (a.dx && half == 0) turn_put(turn, wr, tt);
-    // the tokens' and the channels' scales
+    // the tokens' and the channels' scales; beta / 127 of the wave's tokens (the same in every lane)
+    float bs[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
         const int m = 8 * wave + t, s = scale_exponent(wave_max_pos(fabsf(d[t] * al)));
+        bs[t] = m < M ? a.beta[m0 + m] / 127.0f : 0.0f;
         if (lane == 0) {
             rscale[m] = pow2f(s);
             rinv[m] = pow2f(-s);
-            bscale[m] = m < M ? a.beta[m0 + m] / 127.0f : 0.0f;
         }
     }
     if (dw) {
         float v = 0.0f;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v = fmaxf(v, fabsf(d[t] * bscale[8 * wave + t]));
+        for (int t = 0; t < 8; ++t) v = fmaxf(v, fabsf(d[t] * bs[t]));
         cmx[wave][lane] = v;
     }
     if (db) {
@@ -982,8 +983,8 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
         u32x4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t v0 = split_f16(d[2 * e] * bscale[8 * wave + 2 * e] * cs);
-            const uint32_t v1 = split_f16(d[2 * e + 1] * bscale[8 * wave + 2 * e + 1] * cs);
+            const uint32_t v0 = split_f16(d[2 * e] * bs[2 * e] * cs);
+            const uint32_t v1 = split_f16(d[2 * e + 1] * bs[2 * e + 1] * cs);
             hi[e] = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
             lo[e] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
         }
