@@ -17,37 +17,47 @@ __device__ __forceinline__ float exp_neg(float x) {
     return __builtin_fmaf(e, r * LN2, e);
 }
 
-// a(g) of the gated block, in fp32.  SiLU: g / (1 + exp(-g)), the quotient from the hardware's
-// reciprocal and one correction; below -88 it stays at its value there, -5.3e-37 (13 instructions;
-// the library's exp and an IEEE division took 40, a third of the epilogue of a short GEMM).
+// The larger of g and a bound; NaN for NaN (fmaxf would give the bound).
+__device__ __forceinline__ float at_least(float g, float bound) { return __builtin_elementwise_maximum(g, bound); }
+
+// a(g) of the gated block, in fp32.  SiLU: g / (1 + exp(-g)), by the hardware's reciprocal and one
+// correction of it; below -88 it stays at its value there, -5.3e-37.  Both sides of the quotient are taken
+// 2^-8 times: the hardware's reciprocal of more than 2^126 is zero, and exp(88) is 2^127.  (The reciprocal
+// is corrected, not the quotient, whose remainder is NaN where g is infinite.  14 instructions; the
+// library's exp and an IEEE division took 40, a third of the epilogue of a short GEMM.)
 // GELU: the BitMLP's.  Squared ReLU: one rounding.
 template <int ACT>
 __device__ __forceinline__ float act_value(float g) {
     if constexpr (ACT == BITLINEAR_ACT_SILU) {
-        const float v = fmaxf(g, -88.0f), d = 1.0f + exp_neg(fminf(v, 128.0f));
-        const float r = __builtin_amdgcn_rcpf(d), q = v * r;
-        return __builtin_fmaf(__builtin_fmaf(-q, d, v), r, q);
+        constexpr float S = 0x1p-8f;
+        const float v = at_least(g, -88.0f), d = __builtin_fmaf(exp_neg(fminf(v, 128.0f)), S, S);
+        const float r = __builtin_amdgcn_rcpf(d);
+        return v * S * __builtin_fmaf(__builtin_fmaf(-r, d, 1.0f), r, r);
     } else if constexpr (ACT == BITLINEAR_ACT_GELU) {
         return gelu_f32(g);
     } else {
-        const float r = fmaxf(g, 0.0f);
+        const float r = at_least(g, 0.0f);
         return r * r;
     }
 }
 
 // a(g) and a'(g) for the gradients, to a few fp32 roundings.
 //   SiLU: with e = exp(-|g|), s(|g|) = 1 / (1 + e) and s(-|g|) = e / (1 + e), so neither
-//     logistic value is formed as a difference (the reciprocal is the hardware's, within one unit); a = g s(g), a' = s(g) + a s(-g).
+//     logistic value is formed as a difference (the reciprocal is the hardware's, within one unit); a = g s(g),
+//     a' = s(g) + g s(g) s(-g).
 //   GELU: a = g Phi(g), a' = Phi(g) + g phi(g) in fp64 (Phi from the erfc polynomial of the
 //     forward pass, whose tail below g = -8 is off relative to itself but below 1e-14).
 //   Squared ReLU: a = r^2, a' = 2 r.
+// At an infinite g the limits (GELU: a(-inf) is NaN, as in the forward pass): a factor g beside one that has
+// underflowed is bounded where the product has long been zero.  NaN stays NaN.
 template <int ACT>
 __device__ __forceinline__ void act_grad(float g, float& a, float& slope) {
     if constexpr (ACT == BITLINEAR_ACT_SILU) {
         const float e = exp_neg(fminf(fabsf(g), 128.0f)), t = __builtin_amdgcn_rcpf(1.0f + e), p = e * t;
         const float s = g >= 0.0f ? t : p, sc = g >= 0.0f ? p : t;
-        a = g * s;
-        slope = s + a * sc;
+        const float low = at_least(g, -128.0f), v = __builtin_elementwise_minimum(low, 128.0f);
+        a = low * s;
+        slope = s + v * s * sc;
     } else if constexpr (ACT == BITLINEAR_ACT_GELU) {
         const double v = (double)g, y = fabs(v) * 0.70710678118654752440, d = 2.0 + y;
         double r = __builtin_amdgcn_rcp(d);
@@ -60,9 +70,10 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& slope) {
         const double ex = exp(-0.5 * v * v), q = 0.5 * ex * c;
         const double cdf = v < 0.0 ? q : 1.0 - q;
         a = (float)(v * cdf);
-        slope = (float)(cdf + v * ex * 0.39894228040143267794);
+        const double b = y > 64.0 ? 0.0 : v;                    // exp(-v^2 / 2) is zero long before
+        slope = (float)(cdf + b * ex * 0.39894228040143267794);
     } else {
-        const float r = fmaxf(g, 0.0f);
+        const float r = at_least(g, 0.0f);
         a = r * r;
         slope = 2.0f * r;
     }

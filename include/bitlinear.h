@@ -351,8 +351,9 @@ typedef enum bitlinear_activation {
  * x is quantized as by bitlinear_quantize_act; g and u equal bitlinear_forward's y for the two
  * matrices bit for bit; a(g) is evaluated in fp32 (SiLU within 7 * 2^-24 relative or 2^-120
  * absolute; GELU as bitlinear_mlp_forward; squared ReLU one rounding) and the product is one
- * fp32 rounding.  The
- * block's down projection is a bitlinear_quantize_act of h and any forward call.
+ * fp32 rounding.  Where g overflows or a bias is not finite, a(g) is its limit (NaN for GELU at
+ * -infinity) and NaN for NaN.  The block's down projection is a bitlinear_quantize_act of h and
+ * any forward call.
  *
  *   x          [M, K] fp32.                                                  (in)
  *   Wg_packed, Wu_packed  [F, K/4] uint8; alpha_g, alpha_u [1]; bias_g, bias_u [F] or NULL. (in)
@@ -401,7 +402,8 @@ int bitlinear_backward(const float* dy, int64_t M, int64_t N, const int8_t* x_q,
  * Gradients of bitlinear_gated_forward from dh, the gradient of h, and the g, u, x_q and beta it
  * left.  With dg = dh u a'(g) and du = dh a(g) (fp32), dx is the sum of both projections' dx of
  * bitlinear_backward, and dWg, dWu, dbias_g, dbias_u are those of the two projections; the same
- * accuracy holds.  a' of squared ReLU is 2 max(g, 0).
+ * accuracy holds.  a' of squared ReLU is 2 max(g, 0); a and a' of g that is not finite are their
+ * limits and NaN as in the forward pass.
  *
  *   dh, g, u  [M, F] fp32.                                                   (in)
  *   dx        [M, K] or NULL.   dWg, dWu  [F, K], both or neither.           (out)

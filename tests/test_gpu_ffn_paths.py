@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 import ffn_plain as plain
+from ffn_plain import U
 from test_gpu_ffn import _code, _f32, _layer, _np, _say, _step, _step_state, _t, dev  # noqa: F401  (dev: fixture)
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +49,100 @@ def test_buffers_of_a_given_stream_leave_queued_work_alone(dev):  # noqa: F811
         torch.cuda.synchronize()
         assert [int(v) for v in sums] == [(i + 1) * n for i, n in enumerate(sizes)]
         assert all(torch.equal(a, b) for a, b in zip(got, [want[0], want[4], want[5], want[6], want[3]]))
+
+
+# ------------------------------------------------------------------- values at the ends of the range
+def _gates():
+    """Gates over the whole range, the borders of the exponential's range densely."""
+    ends = [0.0, -0.0, -88.0, 88.0, -87.33, -87.34, 3e38, -3e38, 1e-40, -1e-40, 1e-38, -1e-38]
+    g = np.concatenate([np.linspace(-90, -85, 4001), np.linspace(80, 130, 2001), np.linspace(-140, 140, 8001),
+                        np.linspace(-9, 9, 8001), ends])
+    return _f32(g)
+
+
+NOT_FINITE = _f32([np.inf, -np.inf, np.nan, -np.nan])
+
+
+def _limits(act):
+    """a and a' at NOT_FINITE (SiLU and its slope at -infinity: within the bounds of their zero limits)."""
+    nan = np.nan
+    return {"silu": ([np.inf, 0, nan, nan], [1, 0, nan, nan]), "gelu": ([np.inf, nan, nan, nan], [1, 0, nan, nan]),
+            "relu2": ([np.inf, 0, nan, nan], [np.inf, 0, nan, nan])}[act]
+
+
+def _same(got, want, slack):
+    nan = np.isnan(want)
+    inf = np.isinf(want)
+    rest = ~nan & ~inf
+    return (np.array_equal(np.isnan(got), nan) and np.array_equal(got[inf], np.asarray(want)[inf])
+            and bool(np.all(np.abs(got[rest] - np.asarray(want)[rest]) <= slack)))
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "relu2"])
+@pytest.mark.parametrize("m", [1, 2, 70])
+def test_gated_forward_activation_over_the_range(dev, act, m):  # noqa: F811
+    """The gate driven through its bias (all codes zero), u = 1: h is a(g).  One token, the streaming
+    kernel, the GEMM (2 x 173 tiles).  Bounds: the header's for SiLU; one rounding for squared ReLU, and
+    for GELU one rounding of a value that 64 bits hold to a few 2^-53 times its exponent's size."""
+    torch, bl = dev
+    g = np.concatenate([_gates(), NOT_FINITE])
+    f, end = len(g), len(NOT_FINITE)
+    _say(f"activation over the range {act} M={m} F={f}")
+    x = torch.zeros(m, 64, device="cuda")
+    w = torch.full((f, 16), 0x55, dtype=torch.uint8, device="cuda")
+    al = torch.ones(1, device="cuda")
+    gk, uk = torch.empty(m, f, device="cuda"), torch.empty(m, f, device="cuda")
+    h = bl.bitlinear_gated_forward(x, w, al, w, al, _code(bl, act), bias_g=_t(torch, g), bias_u=torch.ones(f, device="cuda"),
+                                   g=gk, u=uk)
+    h2 = bl.bitlinear_gated_forward(x, w, al, w, al, _code(bl, act), bias_g=_t(torch, g), bias_u=torch.ones(f, device="cuda"))
+    h, h2 = _np(h).astype(np.float64), _np(h2).astype(np.float64)
+    assert np.array_equal(h, h2, equal_nan=True)
+    with np.errstate(over="ignore"):
+        ref = plain.activation(g[:-end], act)[0]
+    for row in h:
+        got = row[:-end]
+        big = np.abs(ref) > np.finfo(np.float32).max
+        assert np.all(np.isinf(got[big])) and np.all(np.isfinite(got[~big]))
+        n, low = {"silu": (7, 2.0 ** -120), "gelu": (1.001, 2.0 ** -149), "relu2": (1, 2.0 ** -150)}[act]
+        err = np.abs(got[~big] - ref[~big]) - n * U * np.abs(ref[~big]) - low
+        assert err.max() <= 0, (float(g[:-end][~big][err.argmax()]), float(err.max()))
+        assert _same(row[-end:], _limits(act)[0], 2.0 ** -120)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "relu2"])
+@pytest.mark.parametrize("m", [1, 20, 70])
+def test_gated_backward_activation_over_the_range(dev, act, m):  # noqa: F811
+    """dh = u = 1 in the first token, zero in the others: the bias sums are a'(g) and a(g).  One pass, one
+    pass on the matrix cores, panels (too many tiles for one pass).  Roundings of SiLU: the exponential 4,
+    1 + e 1, its reciprocal 2, e / (1 + e) 1, so 8 of s and s(-g) and 9 of a; 18 of g s s(-g) and the sum's,
+    so at most 20 of the parts of a'.  An exponential below 2^-126 is zero: 2^-119 with the factor g.  The
+    others have fewer."""
+    torch, bl = dev
+    g = np.concatenate([_gates(), NOT_FINITE])
+    k = {1: 4, 20: 4, 70: 2052}[m]
+    f, end = len(g), len(NOT_FINITE)
+    _say(f"slopes over the range {act} M={m} F={f} K={k}")
+    dh = torch.zeros(m, f, device="cuda")
+    dh[0] = 1
+    gk, u = torch.zeros(m, f, device="cuda"), torch.ones(m, f, device="cuda")
+    gk[0] = _t(torch, g)
+    x_q = torch.zeros(m, k, dtype=torch.int8, device="cuda")
+    w = torch.full((f, k // 4), 0x55, dtype=torch.uint8, device="cuda")
+    al, beta = torch.ones(1, device="cuda"), torch.ones(m, device="cuda")
+    dbg, dbu = torch.empty(f, device="cuda"), torch.empty(f, device="cuda")
+    bl.bitlinear_gated_backward(dh, gk, u, x_q, beta, w, al, w, al, _code(bl, act), dbias_g=dbg, dbias_u=dbu)
+    gd = g[:-end].astype(np.float64)
+    with np.errstate(over="ignore"):
+        a, slope = plain.activation(g[:-end], act)
+    e = np.exp(-np.abs(gd))
+    cdf = np.where(gd != 0, a / np.where(gd != 0, gd, 1), 0.5)                 # or s(g)
+    parts = {"silu": cdf + np.abs(gd) * e, "gelu": cdf + 0.4 * np.abs(gd) * np.exp(-gd * gd / 2), "relu2": np.abs(slope)}[act]
+    got_a, got_s = _np(dbu).astype(np.float64), _np(dbg).astype(np.float64)
+    big = np.abs(a) > np.finfo(np.float32).max
+    big_s = np.abs(slope) > np.finfo(np.float32).max
+    assert np.all(np.isinf(got_a[:-end][big])) and np.all(np.isinf(got_s[:-end][big_s]))
+    # GELU's tail below -8 is good to 1e-14 absolute
+    low = 1e-14 if act == "gelu" else 2.0 ** -119
+    assert np.all(np.abs(got_a[:-end][~big] - a[~big]) <= 12 * U * np.abs(a[~big]) + low)
+    assert np.all(np.abs(got_s[:-end][~big_s] - slope[~big_s]) <= 20 * U * parts[~big_s] + low)
+    assert _same(got_a[-end:], _limits(act)[0], 0) and _same(got_s[-end:], _limits(act)[1], 0)
