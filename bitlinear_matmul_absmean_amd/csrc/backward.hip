@@ -9,10 +9,17 @@
 // Both products pair an fp32 gradient with a small integer (a ternary weight, an int8 code) that
 // fp16 holds exactly.  So each gradient row (a token's for dx, a channel's for dW) is scaled by a
 // power of two that brings its largest element to [2^14, 2^15), and every element is split into
-// hi + lo, two fp16 numbers: hi is the element rounded to 11 bits, lo the exact remainder rounded
-// to 11 bits, together at least 22 bits (2^-40 of the row's largest where lo is subnormal).  Two
-// f16 MFMA products into one fp32 accumulator then give the product to fp32 accuracy at half the
-// f16 matrix rate, several times the rate of fp32 products.
+// hi + 2^-12 lo, two fp16 numbers: hi is the element rounded to 11 bits, lo the exact remainder, 2^12
+// times it, rounded to 11 bits, together within 2^-23 of the element down to 2^-14, 2^-28 of the row's
+// largest (2^-23 is what two fp32 roundings may lose; the products that follow are exact, where fp32's
+// own are rounded once more).  2^-12 goes to the integer operand, which fp16 still holds exactly: without
+// the factor lo was subnormal from 2^-17 of the largest down, and columns where the largest elements
+// meet zeros lost their bits.  Two f16 MFMA products into one fp32 accumulator then give the product to
+// fp32 accuracy at half the f16 matrix rate, several times the rate of fp32 products.
+// Smaller elements have hi = 0 and 11 bits in lo (none below 2^-26), off by 2^-26 at most; fp16's subnormal
+// numbers are left alone, since the matrix cores align sums as if those were 2^-14 (measured: sums of
+// products near 2^-17 came out 2^-31 off).  What small elements lack is below 2^-23 of a sum unless the sum is
+// tiny itself, where all larger elements meet zeros: to such sums it is added in fp32 (step 5).
 //
 // Operands lie in panels, the blocks that a step of the product reads, each contiguous and in the
 // order of its LDS image, so that every load is 1 KiB of whole cache lines:
@@ -27,12 +34,13 @@
 //   2. k_grad_reduce (more than 64 tokens): the tiles' maxima and sums put together;
 //   3. k_grad_split: d once more, scaled and split, rows being tokens (dx) and channels (dW);
 //   4. k_split_gemm: both products;
-//   5. k_split_sum, where a sum was cut into parts.
+//   5. k_grad_finish: the parts of a sum added, where it was cut, and to tiny sums what their small elements
+//      lack.
 // Up to 16 tokens one pass in fp32 takes their place (k_grad_few), beyond, where the tiles are few, one that does
 // steps 1 to 4 tile by tile in LDS (k_grad_mid).
 //
-// 2048 tokens, K = 4096, F = 11008 (gated): 1265 us: step 1 96, 2 5, 3 141 (copies of their bytes would
-// take 83, 1, 132), the products 1.02 ms.
+// 2048 tokens, K = 4096, F = 11008 (gated): 1290 us: step 1 92, 2 5, 3 130 (copies of their bytes would
+// take 83, 1, 132), 5 5, the products 1.05 ms.  (Without the factor 2^-12 and step 5: 1265.)
 #include <limits.h>
 
 #include "ffn.hpp"
@@ -63,6 +71,8 @@ __device__ __forceinline__ f16x8 bytes_f16(uint32_t lo, uint32_t hi) {
     for (int i = 0; i < 8; ++i) o[i] = r[i / 2][i % 2];
     return o;
 }
+// The same 2^-12 times (exact: fp16 is normal down to 2^-14), for the products with lo.
+__device__ __forceinline__ f16x8 lower_operand(f16x8 v) { return v * (_Float16)0x1p-12f; }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
 // d from the incoming gradient and the saved values: one projection d[0] = dy; gated d[0] = dh u a'(g),
@@ -110,6 +120,13 @@ struct GradPlan {
     uint8_t *wt, *cd;              // panels of W_hat^T, K columns of Lx, and of x_q^T, K columns of Mp
     float *part_x, *part_w;        // sums cut into parts
     int parts_x, parts_w;
+    int64_t st;                    // tiles of 128 columns (step 3)
+    uint8_t* small_x;              // where elements below 2^-14 are: for every four tokens, in rows of tx bytes, for
+    int64_t tx;                    // each tile of 128 columns of a projection a bit for each token; and for each
+    uint64_t* small_w;             // projection, parity and tile and every four tokens a bit for each of 64 columns
+    int64_t nb;                    // blocks of 128 columns k, rounded up to eight
+    uint8_t *need_x, *need_w;      // the whole sums that step 5 looks at: for each row of dx and dW a byte for each block
+    int *smalls;                   // [M + P N] small elements of a row: of tokens, of channels
     size_t bytes;
 };
 
@@ -171,6 +188,14 @@ static GradPlan grad_plan(int64_t M, int64_t K, int64_t N, bool gated, void* ws)
     p.cd = take(K256 * p.Mp, 1);
     p.part_x = reinterpret_cast<float*>(take(p.parts_x > 1 ? p.parts_x * M * K : 0, 4));
     p.part_w = reinterpret_cast<float*>(take(p.parts_w > 1 ? p.parts_w * P * N * K : 0, 4));
+    p.st = (N + 127) / 128;
+    p.tx = (P * p.st + 3) / 4 * 4;
+    p.small_x = take(p.Mp / 4 * p.tx, 1);
+    p.small_w = reinterpret_cast<uint64_t*>(take(P * 2 * p.st * (p.Mp / 4), 8));
+    p.nb = (K + 1023) / 1024 * 8;
+    p.need_x = take(M * p.nb, 1);
+    p.need_w = take(P * N * p.nb, 1);
+    p.smalls = reinterpret_cast<int*>(take(M + P * N, 4));
     p.bytes = off;
     return p;
 }
@@ -348,6 +373,7 @@ __global__ __launch_bounds__(256) void k_grad_prep(BackwardArgs a, GradPlan p, i
     constexpr int P = ACT == 0 ? 1 : 2;
     __shared__ __align__(16) uint8_t lds[4 * P * 256 * 12];
     const int64_t b = blockIdx.x;
+    for (int64_t i = b * 256 + threadIdx.x; i < a.M + P * a.N; i += (int64_t)gridDim.x * 256) p.smalls[i] = 0;
     if (b < maxima) max_tile<ACT, C>(a, p, b, lds);
     else if (b < maxima + weights) weights_tile(a, p, b - maxima, ktw, reinterpret_cast<uint32_t*>(lds));
     else codes_tile(a, p, b - maxima - weights, ktc, reinterpret_cast<uint32_t*>(lds));
@@ -381,11 +407,23 @@ __global__ __launch_bounds__(256) void k_grad_reduce(BackwardArgs a, GradPlan p,
 }
 
 // ---- step 3 -------------------------------------------------------------------------------
+__device__ __forceinline__ bool is_small(float v) { return fabsf(v) < 0x1p-14f && v != 0.0f; }
+// Whether there is a small element among several: twice the bits of a number less one order them by size, zeros
+// last (two instructions where a comparison each would take four).
+__device__ __forceinline__ uint32_t size_bits(float v) { return 2 * __float_as_uint(v) - 1; }
+constexpr uint32_t SMALL_BITS = 2u * (127 - 14) << 23;
 __device__ __forceinline__ uint32_t split_f16(float v) {
-    const _Float16 hi = (_Float16)v;
-    const _Float16 lo = (_Float16)(v - (float)hi);
+    const _Float16 hi = fabsf(v) < 0x1p-14f ? (_Float16)0.0f : (_Float16)v;
+    const _Float16 lo = fabsf(v) < 0x1p-26f ? (_Float16)0.0f : (_Float16)((v - (float)hi) * 0x1p12f);
     return (uint32_t)__builtin_bit_cast(uint16_t, hi) | (uint32_t)__builtin_bit_cast(uint16_t, lo) << 16;
 }
+// What a small element lacks when split (exact).
+__device__ __forceinline__ float split_rest(float v) {
+    return fabsf(v) < 0x1p-26f ? v : v - (float)(_Float16)(v * 0x1p12f) * 0x1p-12f;
+}
+// Sums below this many times the number of small elements are looked at in step 5: 2^23 times what one may lack,
+// times the largest of the integer operand.
+constexpr float NEED_X = 0x1p-3f, NEED_W = 0x1p-3f * 128.0f;
 
 // Scaled and split gradients, 32 tokens x 128 columns per workgroup of eight waves; a wave takes four
 // tokens, their loads under way together, a lane two neighbouring columns.  Rows of tokens are
@@ -423,30 +461,72 @@ __global__ __launch_bounds__(512) void k_grad_split(BackwardArgs a, GradPlan p, 
 #pragma unroll
         for (int t = 0; t < 4; ++t) rmax[t] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * t));
     }
+    // tokens and columns past the end read the last ones and count as zeros
+    float d[4][2][2], bs[4], rscale[4];                // d[token][column][projection]
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int64_t m = m0 + 4 * wave + t, ml = m < a.M ? m : a.M - 1;
+        bs[t] = a.beta[ml] / 127.0f;
+        rscale[t] = pow2f(scale_exponent(rmax[t]));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            grad_at<ACT>(a, ml * a.N + (n + c < a.N ? n + c : a.N - 1), d[t][c]);
+            if (m >= a.M || n + c >= a.N) d[t][c][0] = d[t][c][1] = 0.0f;
+        }
+    }
+    uint32_t least = ~0u;                              // the smallest element
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const int64_t m = m0 + 4 * wave + t;
-        float d[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, bs = 0.0f, rscale = 0.0f;   // d[column][projection]
-        if (m < a.M) {
-            bs = a.beta[m] / 127.0f;
-            rscale = pow2f(scale_exponent(rmax[t]));
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (n + c < a.N) grad_at<ACT>(a, m * a.N + n + c, d[c]);
-        }
 #pragma unroll
         for (int q = 0; q < P; ++q) {
             if (a.dx && m < a.M && n < p.Np) {
-                const uint32_t v0 = split_f16(d[0][q] * al[q] * rscale), v1 = split_f16(d[1][q] * al[q] * rscale);
+                const float f0 = d[t][0][q] * al[q] * rscale[t], f1 = d[t][1][q] * al[q] * rscale[t];
+                const uint32_t v0 = split_f16(f0), v1 = split_f16(f1);
                 uint32_t* o = reinterpret_cast<uint32_t*>(p.xs + split_at(m, q * p.Np + n, p.Lx));
                 o[0] = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
                 o[2048] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
+                least = min(least, min(size_bits(f0), size_bits(f1)));
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tile[q][2 * lane + c][4 * wave + t] = split_f16(d[c][q] * bs * cscale[q][c]);
+            for (int c = 0; c < 2; ++c) {
+                const float f = d[t][c][q] * bs[t] * cscale[q][c];
+                tile[q][2 * lane + c][4 * wave + t] = split_f16(f);
+                least = min(least, size_bits(f));
+            }
         }
     }
+    uint32_t small_x[P] = {};                          // a bit for each of the wave's tokens with small elements
+    uint64_t small_w[P][2] = {};                       // and for each of its columns
+    if (__ballot(least < SMALL_BITS - 1)) {
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            int of_column[2] = {0, 0};
+            for (int t = 0; t < 4; ++t) {
+                const int of_token = is_small(d[t][0][q] * al[q] * rscale[t]) + is_small(d[t][1][q] * al[q] * rscale[t]);
+                small_x[q] |= __ballot(of_token) ? 1u << t : 0u;
+                if (a.dx && of_token) atomicAdd(p.smalls + m0 + 4 * wave + t, of_token);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) of_column[c] += is_small(d[t][c][q] * bs[t] * cscale[q][c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                small_w[q][c] = __ballot(of_column[c]);
+                if (a.dw0 && of_column[c]) atomicAdd(p.smalls + a.M + q * a.N + n + c, of_column[c]);
+            }
+        }
+    }
+    if (a.dx) {
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            if (lane == 0) p.small_x[(m0 / 4 + wave) * p.tx + q * p.st + n0 / 128] = (uint8_t)small_x[q];
+    }
     if (!a.dw0) return;
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            if (lane == 0) p.small_w[((2 * q + c) * p.st + n0 / 128) * (p.Mp / 4) + m0 / 4 + wave] = small_w[q][c];
     __syncthreads();
     const int u = threadIdx.x & 3, r = threadIdx.x >> 2;
     if (n0 + r >= a.N) return;
@@ -477,9 +557,13 @@ struct SplitArgs {
     int64_t I0;
     float* part;                   // parts > 1: [parts][I][J] unscaled sums
     int parts, tiles_i, tiles_j;
+    uint8_t* need;                 // [I][nb]
+    int64_t nb;
+    const int* smalls;             // [I]
+    float below;                   // sums below it times a row's small elements are marked
 };
 
-// C[i, j] = 2^-s_i sum_l (hi[i, l] + lo[i, l]) b[j, l].  A workgroup of four waves computes 128 x 256
+// C[i, j] = 2^-s_i sum_l (hi[i, l] + 2^-12 lo[i, l]) b[j, l].  A workgroup of four waves computes 128 x 256
 // outputs, a wave 64 x 128 of them in 32 x 32 blocks (128 accumulator registers), in steps of 32 l.
 // Three LDS stages (24 KiB each: a panel block of each operand) are filled two steps ahead by loads
 // that go past the registers; two workgroups share a compute unit.  Bytes v + 128 become fp16 as
@@ -502,6 +586,7 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w)
     __shared__ i32x4 st1[UNITS];
     __shared__ i32x4 st2[UNITS];
     __shared__ __align__(16) float scale[SG_BM];               // 2^-s of the rows (1 for parts of a sum)
+    __shared__ __align__(16) float limit[SG_BM];               // below it a sum of the row is marked
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // consecutive workgroups go to the eight XCDs in turn: give each XCD a contiguous run of tiles,
@@ -555,11 +640,11 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w)
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const f16x8 fb = bytes_f16((uint32_t)cb[j][2 * kk], (uint32_t)cb[j][2 * kk + 1]);
+                const f16x8 fb = bytes_f16((uint32_t)cb[j][2 * kk], (uint32_t)cb[j][2 * kk + 1]), fd = lower_operand(fb);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fh[kk][i], fb, acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[kk][i], fb, acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[kk][i], fd, acc[i][j], 0, 0, 0);
                 }
             }
     };
@@ -574,6 +659,7 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w)
     int ks = ks0;
     fetch(st0, ks);
     fetch(st1, ks + 1);
+    if (tid < SG_BM) limit[tid] = i0 + tid < a.I ? a.below * (float)a.smalls[i0 + tid] : 0.0f;
     if (tid < SG_BM) scale[tid] = a.parts > 1 ? 1.0f : pow2f(-scale_exponent(a.amax[i0 + tid < a.I ? i0 + tid : a.I - 1]));
     for (; ks + 3 <= ks1; ks += 3) {
         turn();
@@ -599,6 +685,29 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w)
 
     // accumulator r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4 of the block, column l % 32
     const int64_t left = a.J - (j0 + 128 * wj + lr);           // columns from this lane's first to the end
+    if (a.parts == 1) {                                        // rows with tiny sums, a lane each
+        uint64_t tiny = 0;
+        if (__ballot(limit[64 * wi + lane] > 0.0f)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 l4 = *reinterpret_cast<const float4*>(&limit[64 * wi + 32 * i + 8 * q + 4 * lg]);
+                    const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float least = INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) least = fminf(least, 32 * j < left ? fabsf(acc[i][j][4 * q + e]) : INFINITY);
+                        const uint64_t lanes = __ballot(least < l[e]);
+                        const int row = 32 * i + 8 * q + e;
+                        tiny |= (uint64_t)((uint32_t)lanes != 0) << row | (uint64_t)((lanes >> 32) != 0) << (row + 4);
+                    }
+                }
+        }
+        const int64_t row = i0 + 64 * wi + lane;
+        if (row < a.I) a.need[row * a.nb + 2 * tj + wj] = (uint8_t)(tiny >> lane & 1u);
+    }
     const int rows = (int)(a.I - i0 < SG_BM ? a.I - i0 : SG_BM);
     const int split = (int)(a.I0 - i0 < 0 ? 0 : a.I0 - i0 < SG_BM ? a.I0 - i0 : SG_BM);   // rows of c0 in the tile
     float* top = (a.parts > 1 ? a.part + (int64_t)part * a.I * a.J : a.c0) + i0 * a.J + j0 + 128 * wj + lr;
@@ -621,19 +730,158 @@ __global__ __launch_bounds__(256, 2) void k_split_gemm(SplitArgs x, SplitArgs w)
         }
 }
 
-// ---- step 5: the parts of a sum added in their order, scaled back ---------------------------
-__global__ __launch_bounds__(256) void k_split_sum(SplitArgs x, SplitArgs w, int64_t xblocks) {
-    const bool first = blockIdx.x < xblocks;
-    const SplitArgs& a = first ? x : w;
-    const int64_t e = ((int64_t)blockIdx.x - (first ? 0 : xblocks)) * 256 + threadIdx.x, n = a.I * a.J;
-    if (e >= n) return;
-    const int64_t row = e / a.J;
-    float s = 0.0f;
+// ---- step 5: parts of sums, and what small elements lack in tiny sums --------------------------
+// Where a sum was cut, a wave adds the parts of 128 columns of a row in their order, two a lane, and scales them
+// back.  Where it was not, a workgroup looks at the marks of 64 pieces of rows, of 1024 columns each; that no sum
+// is marked is the rule.  To tiny sums, a wave adds what small elements lack: it forms the elements of the
+// tiles of the row that hold small ones again, a lane one or two, and adds to its columns, in fp32 and in the
+// order of l, the rest of each small one times its integer.  Bound: a launch and a round of loads (5 us
+// beside 1.27 ms) or the parts' bytes; where most sums are tiny and most elements small, a vector product's
+// time.
+
+// A lane's C codes of a row from column k on (sixteen, or two at an even k), zeros past its end, and
+// s += e times what they stand for.
+template <int C>
+__device__ __forceinline__ uint32_t codes_at(const uint8_t* __restrict__ w, int64_t k, int64_t K) {
+    if constexpr (C == 16) return row_dword(w, k >> 2, K >> 2);
+    return k < K ? (uint32_t)w[k >> 2] >> (2 * (k & 3)) : 0u;
+}
+template <int C>
+__device__ __forceinline__ u32x4 codes_at(const int8_t* __restrict__ x, int64_t k, int64_t K) {
+    if constexpr (C == 16) return row_16(reinterpret_cast<const uint8_t*>(x), k, K);
+    uint16_t v = 0;
+    if (k < K) __builtin_memcpy(&v, x + k, 2);
+    return u32x4{v, 0u, 0u, 0u};
+}
+template <int C>
+__device__ __forceinline__ void add_codes(float (&s)[C], float e, uint32_t codes) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = __builtin_fmaf(e, (float)(int)(codes >> (2 * c) & 3u) - 1.0f, s[c]);
+}
+template <int C>
+__device__ __forceinline__ void add_codes(float (&s)[C], float e, u32x4 codes) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = __builtin_fmaf(e, (float)(int8_t)(codes[c / 4] >> (8 * (c % 4))), s[c]);
+}
+// s += the products of the elements e of the lanes in `bits` with the rows of codes b0 + lane `step`.
+template <int C, typename Codes>
+__device__ __forceinline__ void add_rests(float (&s)[C], uint64_t bits, float e, const Codes* b0, int64_t step, int64_t k, int64_t K) {
+    for (; bits; bits &= bits - 1) {
+        const int l = __builtin_ctzll(bits);
+        add_codes<C>(s, __int_as_float(__builtin_amdgcn_readlane(__float_as_int(e), l)), codes_at<C>(b0 + l * step, k, K));
+    }
+}
+
+// Token m of dx: C columns a lane from k on.
+template <int ACT, int C>
+__device__ __forceinline__ void tail_token(const BackwardArgs& a, const GradPlan& p, int64_t m, int64_t k, float (&sum)[C]) {
+    constexpr int P = ACT == 0 ? 1 : 2;
+    const int lane = threadIdx.x & 63;
+    const int64_t tiles = P * p.st, rowb = a.K >> 2;
+    const uint32_t* marks = reinterpret_cast<const uint32_t*>(p.small_x + m / 4 * p.tx);
+    const int s = scale_exponent(p.rmax[m]);
+    for (int64_t t0 = 0; t0 < tiles; t0 += 256) {                  // four tiles a lane
+        uint32_t mine = t0 + 4 * lane < tiles ? marks[t0 / 4 + lane] >> (m & 3) & 0x01010101u : 0u;
+        const int64_t behind = t0 + 4 * lane + 4 - tiles;          // bytes past the last tile hold anything
+        if (behind > 0 && behind < 4) mine &= 0xFFFFFFFFu >> (8 * behind);
+        for (uint64_t lanes = __ballot(mine != 0); lanes; lanes &= lanes - 1) {
+            const int from = __builtin_ctzll(lanes);
+            for (uint32_t bytes = __builtin_amdgcn_readlane(mine, from); bytes; bytes &= bytes - 1) {
+                const int64_t t = t0 + 4 * from + __builtin_ctz(bytes) / 8;
+                const int q = t >= p.st;
+                const float al = q ? a.al1[0] : a.al0[0];
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t n0 = (t - q * p.st) * 128 + 64 * h, n = n0 + lane;
+                    float d[2];
+                    grad_at<ACT>(a, m * a.N + (n < a.N ? n : a.N - 1), d);
+                    const float v = n < a.N ? (q ? d[1] : d[0]) * al * pow2f(s) : 0.0f;
+                    add_rests<C>(sum, __ballot(is_small(v)), split_rest(v) * pow2f(-s), (q ? a.w1 : a.w0) + n0 * rowb, rowb, k, a.K);
+                }
+            }
+        }
+    }
+}
+
+// Channel n of projection q of dW.
+template <int ACT, int C>
+__device__ __forceinline__ void tail_channel(const BackwardArgs& a, const GradPlan& p, int q, int64_t n, int64_t k, float (&sum)[C]) {
+    const int lane = threadIdx.x & 63;
+    const int64_t fours = p.Mp / 4;
+    const uint64_t* marks = p.small_w + ((2 * q + (n & 1)) * p.st + n / 128) * fours;
+    const int s = scale_exponent(p.cmax[q * a.N + n]);
+    for (int64_t t0 = 0; t0 < fours; t0 += 64) {                   // four tokens a lane
+        uint64_t lanes = __ballot(t0 + lane < fours && (marks[t0 + lane] >> ((n & 127) / 2) & 1u));
+        while (lanes) {                                            // 64 tokens from the first marked ones on
+            const int from = __builtin_ctzll(lanes);
+            lanes &= from < 48 ? ~0ull << (from + 16) : 0;
+            const int64_t m0 = 4 * (t0 + from), m = m0 + lane, ml = m < a.M ? m : a.M - 1;
+            float d[2];
+            grad_at<ACT>(a, ml * a.N + n, d);
+            const bool next = from > 48 && lane >= 4 * (64 - from);   // tokens of the next round
+            const float v = m < a.M && !next ? (q ? d[1] : d[0]) * (a.beta[ml] / 127.0f) * pow2f(s) : 0.0f;
+            add_rests<C>(sum, __ballot(is_small(v)), split_rest(v) * pow2f(-s), a.xq + m0 * a.K, a.K, k, a.K);
+        }
+    }
+}
+
+// Workgroups: first the sums in parts (xwaves waves for dx, then those for dW), then the pieces of the others
+// (xpieces of dx, then those of dW).
+template <int ACT>
+__global__ __launch_bounds__(256) void k_grad_finish(BackwardArgs a, GradPlan p, SplitArgs x, SplitArgs w, int64_t xwaves, int64_t waves,
+                                                     int64_t xpieces, int64_t pieces) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t sums = (waves + 3) / 4, blocks = (a.K + 127) / 128;
+    if (blockIdx.x < sums) {
+        int64_t id = (int64_t)blockIdx.x * 4 + wave;
+        if (id >= waves) return;
+        const bool first = id < xwaves;
+        const SplitArgs& sa = first ? x : w;
+        id -= first ? 0 : xwaves;
+        const int64_t row = id / blocks, k = id % blocks * 128 + 2 * lane, n = sa.I * sa.J;
+        const bool inside = k < a.K;
+        const float* part = sa.part + row * a.K + (inside ? k : 0);
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll 8
-    for (int q = 0; q < a.parts; ++q) s += a.part[q * n + e];
-    s *= pow2f(-scale_exponent(a.amax[row]));
-    if (row < a.I0) a.c0[e] = s;
-    else a.c1[e - a.I0 * a.J] = s;
+        for (int q = 0; q < sa.parts; ++q) {
+            const float2 v = *reinterpret_cast<const float2*>(part + q * n);
+            s[0] += v.x, s[1] += v.y;
+        }
+        const uint64_t tiny = __ballot(inside && fminf(fabsf(s[0]), fabsf(s[1])) < sa.below * (float)sa.smalls[row]);
+        const float scale = pow2f(-scale_exponent(sa.amax[row]));
+        s[0] *= scale, s[1] *= scale;
+        const int q = !first && row >= a.N;
+        if (tiny) {
+            if (first) tail_token<ACT, 2>(a, p, row, k, s);
+            else tail_channel<ACT, 2>(a, p, q, row - q * a.N, k, s);
+        }
+        if (inside) __builtin_memcpy((first ? a.dx : q ? a.dw1 : a.dw0) + (row - q * a.N) * a.K + k, s, 8);
+        return;
+    }
+    const int64_t group = (int64_t)blockIdx.x - sums, pass = p.nb / 8, mine = group * 64 + lane;
+    uint64_t marks = 0;                                            // the piece's eight blocks, those below K
+    if (mine < pieces) {
+        marks = *reinterpret_cast<const uint64_t*>(mine < xpieces ? p.need_x + 8 * mine : p.need_w + 8 * (mine - xpieces));
+        const int64_t left = blocks - mine % pass * 8;
+        if (left < 8) marks &= ~0ull >> (64 - 8 * left);
+    }
+    uint64_t bits = __ballot(marks != 0);
+    for (int i = 0; bits; bits &= bits - 1, ++i) {                 // a wave every fourth
+        if (i % 4 != wave) continue;
+        const int64_t piece = group * 64 + __builtin_ctzll(bits);
+        const bool first = piece < xpieces;
+        const int64_t id = first ? piece : piece - xpieces, row = id / pass, k = id % pass * 1024 + 16 * lane;
+        const int q = !first && row >= a.N;
+        float* out = (first ? a.dx : q ? a.dw1 : a.dw0) + (row - q * a.N) * a.K;
+        float s[16] = {};
+#pragma unroll
+        for (int c = 0; c < 16; c += 4)
+            if (k + c < a.K) __builtin_memcpy(s + c, out + k + c, 16);
+        if (first) tail_token<ACT, 16>(a, p, row, k, s);
+        else tail_channel<ACT, 16>(a, p, q, row - q * a.N, k, s);
+#pragma unroll
+        for (int c = 0; c < 16; c += 4)
+            if (k + c < a.K) __builtin_memcpy(out + k + c, s + c, 16);
+    }
 }
 
 // ---- few tokens ---------------------------------------------------------------------------
@@ -785,6 +1033,7 @@ __global__ __launch_bounds__(256) void k_grad_few(BackwardArgs a, FewPlan p) {
 // and W are turned and stay bytes v + 128; dx is written as a part for each 64 rows, dW at once or, with
 // several groups, as a part for each (a scale is taken over a part's terms, and the part scaled back before it
 // leaves); k_few_sum adds them.
+// Small elements as above: where there are tiny sums too, the workgroup adds what the elements lack.
 // Against the steps above (us): gated, K = 1024, F = 2731, 61 tokens (344 workgroups) 25.1 and 38.6; K = 512,
 // N = 512, 64 tokens (16) 10.9 and 23.8; K = 2944, N = 5335 (1008), 32 tokens 34.8 and 44.2, 64 tokens 43.3 and
 // 45.5; gated, K = 2048, F = 5504 (1376), 64 tokens 65.3 and 55.5: the parts of dx, as many bytes as dW.  With parts
@@ -797,7 +1046,7 @@ __global__ __launch_bounds__(256) void k_grad_few(BackwardArgs a, FewPlan p) {
 constexpr int MID_TILES = 1024, MID_TILES_GROUPS = 512;
 constexpr int64_t MID_K = (int64_t)1 << 28;            // 16 K bytes are a 32-bit offset
 
-// acc[i] += sum_l (hi + lo)[row, l] b[column, l]: rows 32 i .. 32 i + 31 (i = 0 alone if !high), columns c0 ..
+// acc[i] += sum_l (hi + 2^-12 lo)[row, l] b[column, l]: rows 32 i .. 32 i + 31 (i = 0 alone if !high), columns c0 ..
 // c0 + 31, l 0 .. 63 (0 .. 31 if !deep); operands in lanes as k_split_gemm's.
 __device__ __forceinline__ void mid_multiply(f32x16 (&acc)[2], const u32x4* hi, const u32x4* lo, const u32x4* b, int c0, bool high,
                                              bool deep) {
@@ -808,13 +1057,13 @@ __device__ __forceinline__ void mid_multiply(f32x16 (&acc)[2], const u32x4* hi, 
         const u32x4 cb = b[4 * c + ((2 * s + lg) ^ split_swizzle(c))];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            const f16x8 fb = bytes_f16(cb[2 * kk], cb[2 * kk + 1]);
+            const f16x8 fb = bytes_f16(cb[2 * kk], cb[2 * kk + 1]), fd = lower_operand(fb);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (i && !high) break;
                 const int r = 32 * i + lr, at = 8 * r + ((4 * s + 2 * lg + kk) ^ ((r >> 1) & 7));
                 acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, hi[at]), fb, acc[i], 0, 0, 0);
-                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, lo[at]), fb, acc[i], 0, 0, 0);
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, lo[at]), fd, acc[i], 0, 0, 0);
             }
         }
     }
@@ -849,6 +1098,22 @@ __device__ __forceinline__ void mid_store(const f32x16 (&acc)[2], const float* s
     else rows_out([&](int r) { return r < left; });
 }
 
+// Whether one of the lane's sums is below `need` times its row's small elements, in the first `cols` columns.
+__device__ __forceinline__ bool mid_tiny(const f32x16 (&acc)[2], const float* smalls, float need, int64_t cols) {
+    const int lr = threadIdx.x & 31, lg = (threadIdx.x >> 5) & 1;
+    float over = INFINITY;                             // the least |sum| - limit
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float4 v = *reinterpret_cast<const float4*>(&smalls[32 * i + 8 * g + 4 * lg]);
+            const float n[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) over = fminf(over, __builtin_fmaf(n[e], -need, fabsf(acc[i][4 * g + e])));
+        }
+    return over < 0.0f && lr < cols;
+}
+
 template <int ACT>
 __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) {
     // split gradients: hi and lo of d alpha, a row for a token, then of d beta / 127, a row for a channel
@@ -859,7 +1124,9 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
     __shared__ double csum[8][64];
     __shared__ __align__(16) float rinv[64];
     __shared__ __align__(16) float cinv[64];
-    __shared__ float rscale[64];                       // of the tokens: d alpha's scale
+    __shared__ float rscale[64], cscale[64];           // scales of the tokens' d alpha and the channels' d beta / 127
+    __shared__ __align__(16) float small_x[64], small_w[64];   // small elements of the tokens' d alpha, of the channels' d beta / 127
+    __shared__ int again[2];                           // small elements' rests are to be added to dx, to dW
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = wave >> 2, tt = tid & 255;        // a tile of bytes is turned by 256 threads
     const uint32_t kt = (uint32_t)p.kt, chs = (uint32_t)p.chunks * (ACT == 0 ? 1 : 2), idx = blockIdx.x / kt;
@@ -911,8 +1178,7 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
         }
     }
     // d of tokens 8 wave .. 8 wave + 7 in row n0 + lane, zeros past the ends; offsets below 2^31 bytes
-    float d[8];
-    {
+    auto load_d = [&](float (&d)[8]) {
         const uint32_t n = (uint32_t)(n0 + lane < a.N ? n0 + lane : a.N - 1), N = (uint32_t)a.N;
         auto at = [](const float* p, uint32_t i) { return *reinterpret_cast<const float*>(reinterpret_cast<const char*>(p) + 4u * i); };
         float y[8], g[8], u[8];
@@ -930,7 +1196,11 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
             grad_of<ACT>(y[t], g[t], u[t], e);
             d[t] = n0 + lane < a.N && 8 * wave + t < M ? (q ? e[1] : e[0]) : 0.0f;
         }
-    }
+    };
+    float d[8];
+    load_d(d);
+    if (tid < 2) again[tid] = 0;
+    if (tid < 64) small_x[tid] = small_w[tid] = 0.0f;
     // x_q: four tiles of 64 columns, turned in the split gradients' place; W
     uint32_t* room = reinterpret_cast<uint32_t*>(sp);
     if (dw) {
@@ -979,14 +1249,25 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
         for (int i = 1; i < 8; ++i) v = fmaxf(v, cmx[i][lane]);
         const int s = scale_exponent(v), at = 8 * lane + (wave ^ ((lane >> 1) & 7));
         const float cs = pow2f(s);
-        if (wave == 0) cinv[lane] = pow2f(-s);
+        if (wave == 0) {
+            cscale[lane] = cs;
+            cinv[lane] = pow2f(-s);
+        }
         u32x4 hi, lo;
+        uint32_t least = ~0u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t v0 = split_f16(d[2 * e] * bs[2 * e] * cs);
-            const uint32_t v1 = split_f16(d[2 * e + 1] * bs[2 * e + 1] * cs);
+            const float f0 = d[2 * e] * bs[2 * e] * cs, f1 = d[2 * e + 1] * bs[2 * e + 1] * cs;
+            const uint32_t v0 = split_f16(f0), v1 = split_f16(f1);
             hi[e] = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
             lo[e] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
+            least = min(least, min(size_bits(f0), size_bits(f1)));
+        }
+        if (least < SMALL_BITS - 1) {
+            float n = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) n += is_small(d[t] * bs[t] * cs);
+            atomicAdd(&small_w[lane], n);              // exact in any order
         }
         sp[2][at] = hi;
         sp[3][at] = lo;
@@ -994,12 +1275,21 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
     if (a.dx) {
         uint16_t* hi = reinterpret_cast<uint16_t*>(sp[0]);
         uint16_t* lo = reinterpret_cast<uint16_t*>(sp[1]);
+        uint32_t least = ~0u;
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             const int m = 8 * wave + t, at = 8 * (8 * m + ((lane >> 3) ^ ((m >> 1) & 7))) + (lane & 7);
-            const uint32_t v = split_f16(d[t] * al * rscale[m]);
+            const float f = d[t] * al * rscale[m];
+            const uint32_t v = split_f16(f);
             hi[at] = (uint16_t)v;
             lo[at] = (uint16_t)(v >> 16);
+            least = min(least, size_bits(f));
+        }
+        if (__ballot(least < SMALL_BITS - 1)) {
+            for (int t = 0; t < 8; ++t) {
+                const float n = (float)__popcll(__ballot(is_small(d[t] * al * rscale[8 * wave + t])));
+                if (lane == 0) small_x[8 * wave + t] = n;
+            }
         }
         const u32x4 v = turn_get(turn, tt);
 #pragma unroll
@@ -1017,15 +1307,69 @@ __global__ __launch_bounds__(512, 4) void k_grad_mid(BackwardArgs a, FewPlan p) 
     }
     __syncthreads();
     const int64_t left = a.K - (k0 + 32 * wave);       // columns from the wave's first to the end
+    bool some_x = false, some_w = false;               // there are small elements
+    if (a.dx) some_x = __ballot(small_x[lane] > 0.0f) != 0;
+    if (dw) some_w = __ballot(small_w[lane] > 0.0f) != 0;
     if (a.dx) {
         f32x16 acc[2] = {};
         mid_multiply(acc, sp[0], sp[1], wb, 32 * wave, M > 32, true);
+        if (some_x && mid_tiny(acc, small_x, NEED_X, left)) again[0] = 1;
         mid_store(acc, rinv, (chs == 1 ? a.dx : p.part + ch * a.M * a.K) + m0 * a.K + k0 + 32 * wave, a.K, M, left);
     }
     if (dw) {
         f32x16 acc[2] = {};
         mid_multiply(acc, sp[2], sp[3], xb, 32 * wave, true, M > 32);
+        if (some_w && mid_tiny(acc, small_w, NEED_W, left)) again[1] = 1;
         mid_store(acc, cinv, dw + n0 * a.K + k0 + 32 * wave, a.K, a.N - n0, left);
+    }
+    if (!some_x && !some_w) return;
+    __syncthreads();
+    if (!again[0] && !again[1]) return;
+    // tiny sums and small elements, rare: those are formed again, and what they lack when split is added
+    // to what has been stored in the order of the sums, to dx by each wave in its own tokens, to dW by one wave
+    // after another; a lane takes four columns (every lane stays: a rest is read from any of them)
+    const int64_t k = k0 + 4 * lane, kl = k < a.K ? k : 0;
+    load_d(d);
+    if (again[0]) {
+        float* out = (chs == 1 ? a.dx : p.part + ch * a.M * a.K) + m0 * a.K;
+        for (int t = 0; t < 8; ++t) {
+            const int m = 8 * wave + t;
+            const float v = d[t] * al * rscale[m], rest = split_rest(v) * rinv[m];
+            uint64_t bits = __ballot(is_small(v));
+            if (!bits) continue;
+            float s[4];
+            __builtin_memcpy(s, out + m * a.K + kl, 16);
+            for (; bits; bits &= bits - 1) {
+                const int j = __builtin_ctzll(bits);
+                const float e = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rest), j));
+                const uint32_t codes = w[(n0 + j) * rowb + (kl >> 2)];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[c] = __builtin_fmaf(e, (float)(int)(codes >> (2 * c) & 3u) - 1.0f, s[c]);
+            }
+            if (k < a.K) __builtin_memcpy(out + m * a.K + k, s, 16);
+        }
+    }
+    if (!again[1]) return;
+    for (int i = 0; i < 8; ++i) {
+        if (i == wave) {
+            for (int t = 0; t < 8; ++t) {
+                const int m = 8 * wave + t;
+                const float v = d[t] * bs[t] * cscale[lane], rest = split_rest(v) * cinv[lane];
+                for (uint64_t bits = __ballot(is_small(v)); bits; bits &= bits - 1) {
+                    const int j = __builtin_ctzll(bits);
+                    const float e = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rest), j));
+                    float* out = dw + (n0 + j) * a.K;
+                    uint32_t codes;
+                    float s[4];
+                    __builtin_memcpy(&codes, xq + m * a.K + kl, 4);
+                    __builtin_memcpy(s, out + kl, 16);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[c] = __builtin_fmaf(e, (float)(int8_t)(codes >> (8 * c)), s[c]);
+                    if (k < a.K) __builtin_memcpy(out + k, s, 16);
+                }
+            }
+        }
+        __syncthreads();                               // the next wave's elements may be of the same rows
     }
 }
 
@@ -1134,12 +1478,18 @@ static hipError_t launch_grads(const BackwardArgs& a, hipStream_t s) {
         return q;
     };
     SplitArgs x{}, w{};
-    if (a.dx) x = tiles(SplitArgs{p.xs, p.wt, p.rmax, a.M, a.K, p.Lx, a.dx, nullptr, a.M, p.part_x, p.parts_x, 0, 0});
-    if (a.dw0) w = tiles(SplitArgs{p.wsp, p.cd, p.cmax, P * a.N, a.K, p.Mp, a.dw0, a.dw1, a.N, p.part_w, p.parts_w, 0, 0});
+    if (a.dx)
+        x = tiles(SplitArgs{p.xs, p.wt, p.rmax, a.M, a.K, p.Lx, a.dx, nullptr, a.M, p.part_x, p.parts_x, 0, 0, p.need_x, p.nb,
+                            p.smalls, NEED_X});
+    if (a.dw0)
+        w = tiles(SplitArgs{p.wsp, p.cd, p.cmax, P * a.N, a.K, p.Mp, a.dw0, a.dw1, a.N, p.part_w, p.parts_w, 0, 0, p.need_w, p.nb,
+                            p.smalls + a.M, NEED_W});
     const int64_t grid = (int64_t)x.parts * x.tiles_i * x.tiles_j + (int64_t)w.parts * w.tiles_i * w.tiles_j;
     hipLaunchKernelGGL(k_split_gemm, blocks(grid), dim3(256), 0, s, x, w);
-    const int64_t xb = x.parts > 1 ? (x.I * x.J + 255) / 256 : 0, wb = w.parts > 1 ? (w.I * w.J + 255) / 256 : 0;
-    if (xb + wb) hipLaunchKernelGGL(k_split_sum, blocks(xb + wb), dim3(256), 0, s, x, w, xb);
+    const int64_t cols = (a.K + 127) / 128, xw = x.parts > 1 ? x.I * cols : 0, waves = xw + (w.parts > 1 ? w.I * cols : 0);
+    const int64_t xp = x.parts == 1 ? x.I * (p.nb / 8) : 0, pieces = xp + (w.parts == 1 ? w.I * (p.nb / 8) : 0);
+    hipLaunchKernelGGL(k_grad_finish<ACT>, blocks((waves + 3) / 4 + (pieces + 63) / 64), dim3(256), 0, s, a, p, x, w, xw, waves, xp,
+                       pieces);
     return hipGetLastError();
 }
 

@@ -146,3 +146,76 @@ def test_gated_backward_activation_over_the_range(dev, act, m):  # noqa: F811
     assert np.all(np.abs(got_a[:-end][~big] - a[~big]) <= 12 * U * np.abs(a[~big]) + low)
     assert np.all(np.abs(got_s[:-end][~big_s] - slope[~big_s]) <= 20 * U * parts[~big_s] + low)
     assert _same(got_a[-end:], _limits(act)[0], 0) and _same(got_s[-end:], _limits(act)[1], 0)
+
+
+# ------------------------------------------------------ gradients of very different sizes in a row
+# (M, K, N): one pass in fp32; one pass on the matrix cores, one group of tokens and several; panels, with
+# up to 64 tokens, with sums in parts and whole
+RANGES = [(12, 132, 90), (40, 132, 90), (64, 260, 130), (150, 132, 90), (64, 2052, 2100), (300, 1028, 1100),
+          (700, 132, 4100)]
+
+
+def _within(got, want, terms, length, name, slack=0.0):
+    """Every element within its own bound: gradient_tolerance counts the terms that enter it."""
+    err = np.abs(got.astype(np.float64) - want)
+    tol = plain.gradient_tolerance(terms, length) + slack
+    bad = err > tol
+    assert not bad.any(), (name, int(bad.sum()), float((err[bad] / np.maximum(np.abs(want[bad]), 1e-300)).max()))
+
+
+@pytest.mark.parametrize("m,k,n", RANGES)
+@pytest.mark.parametrize("s", [20, 24, 30, 45])
+def test_backward_dominated_by_one_token_and_one_channel(dev, m, k, n, s):  # noqa: F811
+    """A token and a channel 2^s larger than the others, whose code and whose weights are zero in every
+    third column: there the sums are those of the others, and hold their own accuracy."""
+    torch, bl = dev
+    _say(f"backward dominated M={m} K={k} N={n} 2^{s}")
+    rng = np.random.default_rng([60, m, k, n, s])
+    dy = rng.standard_normal((m, n))
+    dy[m // 2] *= 2.0 ** s
+    dy[:, n // 3] *= 2.0 ** s
+    dy = _f32(dy)
+    x_q, beta = plain.absmax(rng.standard_normal((m, k)))
+    x_q[m // 2, ::3] = 0
+    w, al, _ = _layer(rng, n, k, False)
+    w[n // 3, ::3] = 0
+    dx, dw, _ = bl.bitlinear_backward(_t(torch, dy), _t(torch, x_q), _t(torch, beta), _t(torch, plain.pack(w)), _t(torch, al))
+    want, terms = plain.linear_gradients(dy, x_q, beta, w, al[0])
+    _within(_np(dx), want[0], terms[0], n, "dx")
+    _within(_np(dw), want[1], terms[1], m, "dW")
+
+
+@pytest.mark.parametrize("m,k,n", RANGES)
+@pytest.mark.parametrize("gated", [False, True])
+def test_backward_over_a_hundred_binades(dev, m, k, n, gated):  # noqa: F811
+    """Elements of sizes spread over 2^-100 .. 1, most codes and weights zero, so that in many columns
+    the largest elements are absent; rows and columns of zeros among them."""
+    torch, bl = dev
+    _say(f"backward hundred binades M={m} K={k} N={n} gated={gated}")
+    rng = np.random.default_rng([61, m, k, n])
+    dy = _f32(rng.standard_normal((m, n)) * np.exp2(rng.integers(-100, 1, (m, n))))
+    dy[1] = 0
+    dy[:, 2] = 0
+    sparse = lambda a, keep: (a * (rng.random(a.shape) < keep)).astype(np.int8)
+    x_q, beta = plain.absmax(rng.standard_normal((m, k)))
+    x_q = sparse(x_q, 0.2)
+    tx, tb = _t(torch, x_q), _t(torch, beta)
+    w0, al, _ = _layer(rng, n, k, False)
+    w0 = sparse(w0, 0.2)
+    if not gated:
+        dx, dw, _ = bl.bitlinear_backward(_t(torch, dy), tx, tb, _t(torch, plain.pack(w0)), _t(torch, al))
+        want, terms = plain.linear_gradients(dy, x_q, beta, w0, al[0])
+        _within(_np(dx), want[0], terms[0], n, "dx")
+        _within(_np(dw), want[1], terms[1], m, "dW")
+        assert not dx[1].any() and not dw[2].any()
+        return
+    w1, al1, _ = _layer(rng, n, k, False)
+    w1 = sparse(w1, 0.2)
+    g, u = (_f32(np.abs(rng.standard_normal((m, n))) + 0.1) for _ in range(2))
+    dx, dwg, dwu, _, _ = bl.bitlinear_gated_backward(_t(torch, dy), _t(torch, g), _t(torch, u), tx, tb,
+                                                     _t(torch, plain.pack(w0)), _t(torch, al), _t(torch, plain.pack(w1)),
+                                                     _t(torch, al1), bl.BITLINEAR_ACT_RELU2)
+    want, terms = plain.gated_gradients(dy, g, u, x_q, beta, w0, al[0], w1, al1[0], "relu2")
+    for t, w, s, length, name in zip((dx, dwg, dwu), want, terms, (2 * n, m, m), ("dx", "dWg", "dWu")):
+        _within(_np(t), w, s, length, name)
+    assert not dx[1].any() and not dwg[2].any() and not dwu[2].any()
