@@ -219,3 +219,209 @@ def test_backward_over_a_hundred_binades(dev, m, k, n, gated):  # noqa: F811
     for t, w, s, length, name in zip((dx, dwg, dwu), want, terms, (2 * n, m, m), ("dx", "dWg", "dWu")):
         _within(_np(t), w, s, length, name)
     assert not dx[1].any() and not dwg[2].any() and not dwu[2].any()
+
+
+# ------------------------------------------------------------------ every kernel of the choices by size
+def _int_product(torch, x_q, w):
+    """x_q . w^T, exact: sums of integers below 2^53 in 64-bit floating point on the device."""
+    return _np(_t(torch, x_q).double() @ _t(torch, w).double().t().contiguous())
+
+
+def _off(torch, a, n):
+    """A contiguous view of a's values that starts n elements into its buffer."""
+    if a is None:
+        return None
+    t = _t(torch, a)
+    v = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")[n:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+def _gated_case(dev, m, k, f, act, bias, keep, views=False):  # noqa: F811
+    """One call against the documented 32-bit steps: x_q, beta, g and u bit for bit, h within the
+    activation's roundings; what lies behind the outputs stays."""
+    torch, bl = dev
+    _say(f"gated_forward M={m} K={k} F={f} {act} bias={bias} keep={keep} views={views}")
+    rng = np.random.default_rng([70, m, k, f])
+    x = _f32(rng.standard_normal((m, k)))
+    wg, ag, bg = _layer(rng, f, k, bias)
+    wu, au, bu = _layer(rng, f, k, bias)
+    put = (lambda a, n: _off(torch, a, n)) if views else (lambda a, n: _t(torch, a))
+    room = [torch.full((m * f + 64,), 7.0, device="cuda") for _ in range(3)]
+    s = 1 if views else 0
+    h, g, u = (r[s:s + m * f].view(m, f) for r in room)
+    bytes_ = torch.empty(m * k + 3, dtype=torch.int8, device="cuda")
+    x_q = bytes_[3 * s:3 * s + m * k].view(m, k)
+    beta = torch.empty(m, device="cuda")
+    bl.bitlinear_gated_forward(put(x, 1), put(plain.pack(wg), 1), put(ag, 1), put(plain.pack(wu), 3), put(au, 3),
+                               _code(bl, act), bias_g=put(bg, 1), bias_u=put(bu, 1), h=h, g=g if keep else None,
+                               u=u if keep else None, x_q=x_q, beta=beta)
+    xq_p, beta_p = plain.absmax(x)
+    assert np.array_equal(_np(x_q), xq_p) and np.array_equal(_np(beta), beta_p)
+
+    def project(w, alpha, b):
+        y = _int_product(torch, xq_p, w).astype(np.float32) * (np.float64(alpha) * beta_p.astype(np.float64) / 127).astype(np.float32)[:, None]
+        return y if b is None else y + b
+
+    g_p, u_p = project(wg, ag[0], bg), project(wu, au[0], bu)
+    assert g_p.dtype == np.float32
+    if keep:
+        assert np.array_equal(_np(g), g_p) and np.array_equal(_np(u), u_p)
+    else:
+        assert bool((room[1] == 7).all()) and bool((room[2] == 7).all())
+    if act == "gelu":
+        v = torch.from_numpy(g_p).double()
+        a = (0.5 * v * torch.special.erfc(-v * 0.5 ** 0.5)).numpy()
+    else:
+        a = plain.activation(g_p, act)[0]
+    ref = a * u_p.astype(np.float64)
+    n = {"silu": 8, "gelu": 2, "relu2": 2}[act]
+    assert np.all(np.abs(_np(h) - ref) <= 1.01 * n * U * np.abs(ref) + 2.0 ** -120)
+    assert bool((room[0][:s] == 7).all()) and bool((room[0][s + m * f:] == 7).all())
+
+
+ACTS = ["gelu", "silu", "relu2"]
+# more than 64 tiles of 64 x 128, so the GEMM: tiles of 32 tokens (102 of them), of 64 (170, since 340 of 32) and of
+# 128 (426, more than 384); the last row and column of tiles partial
+GEMM = [(65, 4300), (300, 4300), (700, 9000)]
+
+
+@pytest.mark.parametrize("m,f", GEMM)
+@pytest.mark.parametrize("i,k", list(enumerate([64, 128, 192, 256, 320, 384, 448, 512, 1088])))
+def test_gated_gemm(dev, m, f, i, k):  # noqa: F811
+    """Rows on 16-byte boundaries: no whole step of 128, one to four, with and without a last half step."""
+    _gated_case(dev, m, k, f, ACTS[i % 3], bias=i % 2 == 0, keep=i % 4 < 2)
+
+
+@pytest.mark.parametrize("m,f", GEMM)
+@pytest.mark.parametrize("i,k", list(enumerate([4, 60, 132, 260, 388, 1028])))
+def test_gated_gemm_any_rows(dev, m, f, i, k):  # noqa: F811
+    """Rows off those boundaries: fewer than 16 bytes, part steps alone and after one to eight whole ones."""
+    _gated_case(dev, m, k, f, ACTS[i % 3], bias=i % 2 == 1, keep=i % 4 > 1)
+
+
+@pytest.mark.parametrize("m,f", GEMM)
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_gemm_unaligned_views(dev, m, f, act):  # noqa: F811
+    _gated_case(dev, m, 256, f, act, bias=True, keep=True, views=True)
+
+
+# Pairs of rows a wave, pairs at a time: K <= 4096: 2 of 2, 3 of 4, 6 of 6, 7 of 4 (twice), 10 of 4 (three times);
+# two chunks of 4096: 3 of 2, three chunks: 3 of 1, four: 2 of 1 and (the last chunk partial) 3 of 1
+@pytest.mark.parametrize("k,f", [(320, 3000), (4096, 5000), (1024, 11008), (640, 13000), (64, 20011), (8192, 5000), (9024, 4099),
+                                 (16384, 4090), (12352, 4100)])
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_one_token(dev, k, f, act):  # noqa: F811
+    _gated_case(dev, 1, k, f, act, bias=f % 2 == 0, keep=act == "silu")
+
+
+# Token blocks of a workgroup, column blocks: 1 x 1, 2 x 1, 3 x 1, 4 x 1, 3 x 2, 4 x 2, and 4 x 2 in several slices
+@pytest.mark.parametrize("m,f", [(9, 500), (30, 700), (41, 900), (64, 1000), (48, 4500), (64, 4500), (130, 2100)])
+@pytest.mark.parametrize("i,k", list(enumerate([64, 256, 2368, 4, 260, 1100])))
+def test_gated_few_tokens(dev, m, f, i, k):  # noqa: F811
+    """The streaming kernel: a part step alone, one whole step, more steps than waves and a part; aligned or not."""
+    _gated_case(dev, m, k, f, ACTS[(i + m) % 3], bias=i % 2 == 0, keep=m % 2 == 0)
+
+
+def _i8_case(dev, m, k, n):  # noqa: F811
+    torch, bl = dev
+    _say(f"forward_i8 M={m} K={k} N={n}")
+    rng = np.random.default_rng([71, m, k, n])
+    xq = rng.integers(-127, 128, (m, k)).astype(np.int8)
+    wq = rng.integers(-127, 128, (n, k)).astype(np.int8)
+    beta, gamma = _f32(rng.random(m) + 0.5), _f32(rng.random(n) + 0.5)
+    b = _f32(rng.standard_normal(n)) if (m + k) % 2 else None
+    out = torch.full((m + 2, n), 3.0, device="cuda")
+    _, acc = bl.bitlinear_forward_i8(_t(torch, xq), _t(torch, beta), _t(torch, wq), _t(torch, gamma), bias=_t(torch, b),
+                                     y=out[1:m + 1], acc=True)
+    ref = _int_product(torch, xq, wq).astype(np.int32)
+    assert np.array_equal(_np(acc), ref)
+    f = np.float32
+    y = (ref.astype(f) * (beta / f(127))[:, None]) * (gamma / f(127))[None]
+    assert np.array_equal(_np(out[1:m + 1]), y if b is None else y + b)
+    assert bool((out[0] == 3).all()) and bool((out[m + 1] == 3).all())
+
+
+# Token blocks, channel blocks: 3 x 2, 4 x 2, 4 x 2 in two slices
+@pytest.mark.parametrize("m,n", [(48, 5000), (33, 4111), (64, 4500), (100, 2100)])
+@pytest.mark.parametrize("k", [16, 272, 1552, 260, 1100, 15, 257, 1001])
+def test_forward_i8_few_tokens_two_blocks(dev, m, n, k):  # noqa: F811
+    """The streaming kernel with two blocks of channels, rows on 16-byte and dword boundaries and off them."""
+    _i8_case(dev, m, k, n)
+
+
+@pytest.mark.parametrize("m,n", [(70, 4200), (520, 4200), (1100, 4200)])
+@pytest.mark.parametrize("k", [133136, 133144, 133143])
+def test_forward_i8_largest_sums_in_tiles(dev, m, n, k):  # noqa: F811
+    """Codes of +-127 at the largest K in every tile size of the GEMM (34, 153 and 306 tiles of 64 x 256)."""
+    torch, bl = dev
+    _say(f"forward_i8 largest sums M={m} K={k} N={n}")
+    x_q = torch.full((m, k), 127, dtype=torch.int8, device="cuda")
+    x_q[1::3] = -127
+    w_q = torch.full((n, k), -127, dtype=torch.int8, device="cuda")
+    w_q[1::2] = 127
+    _, acc = bl.bitlinear_forward_i8(x_q, torch.ones(m, device="cuda"), w_q, torch.ones(n, device="cuda"), acc=True)
+    want = (torch.where(torch.arange(m) % 3 == 1, -1, 1)[:, None] * torch.where(torch.arange(n) % 2 == 1, 1, -1)) * (127 * 127 * k)
+    assert torch.equal(acc.cpu().long(), want)
+
+
+# 64 tokens x 256 columns a tile of the maxima (561 tiles, at least 512), the last of both directions partial
+@pytest.mark.parametrize("gated", [False, True])
+def test_backward_large_tiles_of_the_maxima(dev, gated):  # noqa: F811
+    torch, bl = dev
+    m, k, n = 2100, 68, 4100
+    _say(f"backward M={m} K={k} N={n} gated={gated}")
+    rng = np.random.default_rng([72, gated])
+    dy = _f32(rng.standard_normal((m, n)) * np.exp(rng.standard_normal((m, 1))) / m)
+    dy[:, 5] *= 1000
+    dy[7] *= 1000
+    x_q, beta = plain.absmax(rng.standard_normal((m, k)))
+    tx, tb = _t(torch, x_q), _t(torch, beta)
+    w0, al, _ = _layer(rng, n, k, False)
+    nan = lambda *s: torch.full(s, float("nan"), device="cuda")
+    if not gated:
+        out = bl.bitlinear_backward(_t(torch, dy), tx, tb, _t(torch, plain.pack(w0)), _t(torch, al), dx=nan(m, k), dW=nan(n, k),
+                                    dbias=nan(n))
+        want, terms = plain.linear_gradients(dy, x_q, beta, w0, al[0])
+        lengths = [n, m, m]
+    else:
+        w1, al1, _ = _layer(rng, n, k, False)
+        g, u = (_f32(rng.standard_normal((m, n))) for _ in range(2))
+        out = bl.bitlinear_gated_backward(_t(torch, dy), _t(torch, g), _t(torch, u), tx, tb, _t(torch, plain.pack(w0)),
+                                          _t(torch, al), _t(torch, plain.pack(w1)), _t(torch, al1), bl.BITLINEAR_ACT_RELU2,
+                                          dx=nan(m, k), dWg=nan(n, k), dWu=nan(n, k), dbias_g=nan(n), dbias_u=nan(n))
+        want, terms = plain.gated_gradients(dy, g, u, x_q, beta, w0, al[0], w1, al1[0], "relu2")
+        lengths = [2 * n, m, m, m, m]
+    for i, (t, w, s, length) in enumerate(zip(out, want, terms, lengths)):
+        _within(_np(t), w, s, length, i)
+
+
+def test_forward_i8_three_token_blocks_on_dwords(dev):  # noqa: F811
+    _i8_case(dev, 41, 260, 900)
+
+
+# One pass in fp32 with room for 4, 8 and 16 tokens; one pass on the matrix cores; panels, up to 64 tokens and more
+@pytest.mark.parametrize("m,k,f", [(3, 68, 70), (8, 260, 300), (16, 260, 300), (40, 260, 300), (33, 4100, 4200), (300, 1028, 1100)])
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_backward_every_activation(dev, m, k, f, act):  # noqa: F811
+    torch, bl = dev
+    _say(f"gated_backward M={m} K={k} F={f} {act}")
+    rng = np.random.default_rng([73, m, k, f])
+    dh = _f32(rng.standard_normal((m, f)) / m)
+    g, u = (_f32(rng.standard_normal((m, f)) * 2) for _ in range(2))
+    x_q, beta = plain.absmax(rng.standard_normal((m, k)))
+    wg, ag, _ = _layer(rng, f, k, False)
+    wu, au, _ = _layer(rng, f, k, False)
+    nan = lambda *s: torch.full(s, float("nan"), device="cuda")
+    out = bl.bitlinear_gated_backward(_t(torch, dh), _t(torch, g), _t(torch, u), _t(torch, x_q), _t(torch, beta),
+                                      _t(torch, plain.pack(wg)), _t(torch, ag), _t(torch, plain.pack(wu)), _t(torch, au),
+                                      _code(bl, act), dx=nan(m, k), dWg=nan(f, k), dWu=nan(f, k), dbias_g=nan(f),
+                                      dbias_u=nan(f))
+    want, terms = plain.gated_gradients(dh, g, u, x_q, beta, wg, ag[0], wu, au[0], act)
+    # a'(g) of SiLU and GELU passes through zero, where its error is that of its parts, at most 2 in size:
+    # counted as roundings of dh u
+    d0 = 24 * U * np.abs(dh.astype(np.float64) * u) * (act != "relu2")
+    xd = np.abs(x_q.astype(np.float64)) * beta[:, None] / 127
+    slack = [d0 @ np.abs(wg).astype(np.float64) * ag[0], d0.T @ xd, 0, d0.sum(0), 0]
+    for t, w, s, n, sl, name in zip(out, want, terms, [2 * f, m, m, m, m], slack, ("dx", "dWg", "dWu", "dbias_g", "dbias_u")):
+        _within(_np(t), w, s, n, name, sl)
