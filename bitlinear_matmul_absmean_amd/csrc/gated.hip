@@ -8,10 +8,11 @@
 // so that gate and up equal two BitLinear forwards bit for bit.
 //
 // Every kernel gives the same lanes a gate row and the up row of the same column, so that the
-// product is formed where the sums end.  Three kernels by the number of tokens:
-//   * one token: k_gated_gemv, which also quantizes x, on v_dot4_i32_i8;
-//   * up to 64: k_gated_dec, the weight streams on the 16x16x64 int8 MFMA;
-//   * more: k_gated_gemm, LDS tiles on the 32x32x32 int8 MFMA;
+// product is formed where the sums end.  Three kernels:
+//   * one token in aligned rows: k_gated_gemv, which also quantizes x, on v_dot4_i32_i8;
+//   * up to 32 tokens, and more where a GEMM would have few tiles (64 of 64 tokens x 128 columns):
+//     k_gated_dec, the weight streams on the 16x16x64 int8 MFMA;
+//   * else: k_gated_gemm, LDS tiles on the 32x32x32 int8 MFMA;
 // the last two also in a form for any K % 4 == 0 and any alignment.
 #include <type_traits>
 
@@ -186,7 +187,7 @@ hipError_t launch_gated_gemv(const GatedArgs& a, const float* x, int8_t* xq, flo
     }
 }
 
-// ---- up to 64 tokens ------------------------------------------------------------------------
+// ---- few tokens or few tiles ----------------------------------------------------------------
 // A workgroup of eight waves computes 16 MT tokens x 16 RB columns of both projections; wave w takes
 // the steps of 256 k w, w + 8, ..., and the partial tiles are added at the end (integers: exact in
 // any order).  In MFMA q of a step lane group g (lanes 16 g ..) holds weights 64 g + 16 q ..
@@ -382,7 +383,7 @@ static hipError_t launch_gated_dec(const GatedArgs& a, hipStream_t s) {
                         : launch_gated_dec_mt<ALIGNED, 4>(a, s);
 }
 
-// ---- more tokens ----------------------------------------------------------------------------
+// ---- many tiles -----------------------------------------------------------------------------
 // A workgroup of four waves computes 32 FM tokens x 128 columns of both projections, a wave all the
 // tokens x 32 columns of each: FM 32-token operands against one gate and one up operand, so that the
 // expansion of a weight operand (17 instructions) serves FM MFMAs.  Steps of 128 k, three LDS stages
