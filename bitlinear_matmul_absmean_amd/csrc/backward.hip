@@ -1044,7 +1044,7 @@ __global__ __launch_bounds__(256) void k_grad_few(BackwardArgs a, FewPlan p) {
 // LDS images: split gradients, rows of 64 values, the 16-byte unit u at position u ^ (row / 2) % 8; bytes,
 // columns of 64, the 16-byte unit u at position u ^ split_swizzle(column).
 constexpr int MID_TILES = 1024, MID_TILES_GROUPS = 512;
-constexpr int64_t MID_K = (int64_t)1 << 28;            // 16 K bytes are a 32-bit offset
+static_assert(16 * (int64_t)BITLINEAR_MAX_K + 4 * 32 < (int64_t)1 << 32, "a lane's offset in mid_store has 32 bits");
 
 // acc[i] += sum_l (hi + 2^-12 lo)[row, l] b[column, l]: rows 32 i .. 32 i + 31 (i = 0 alone if !high), columns c0 ..
 // c0 + 31, l 0 .. 63 (0 .. 31 if !deep); operands in lanes as k_split_gemm's.
@@ -1070,8 +1070,8 @@ __device__ __forceinline__ void mid_multiply(f32x16 (&acc)[2], const u32x4* hi, 
 }
 
 // out[row, column] = acc scale[row], rows below `rows`, columns below `cols` (lane: column lane % 32 of rows
-// 4 (lane / 32) .. of eight).  A running row and one lane offset (below 2^32: MID_K): the addresses of every
-// row would fill the registers.
+// 4 (lane / 32) .. of eight).  A running row and one lane offset of 32 bits: the addresses of every row would
+// fill the registers.
 __device__ __forceinline__ void mid_store(const f32x16 (&acc)[2], const float* scale, float* out, int64_t stride, int64_t rows,
                                           int64_t cols) {
     const int lr = threadIdx.x & 31, lg = (threadIdx.x >> 5) & 1;
@@ -1424,7 +1424,7 @@ __global__ __launch_bounds__(256) void k_few_sum(PartSum x, PartSum w0, PartSum 
 static bool use_mid(int64_t M, int64_t K, int64_t N, bool gated) {
     const int64_t groups = (M + MID_TOKENS - 1) / MID_TOKENS;
     const int64_t tiles = ((K + FEW_K - 1) / FEW_K) * ((N + FEW_N - 1) / FEW_N) * (gated ? 2 : 1) * groups;
-    return M > FEW_TOKENS && K < MID_K && tiles <= (groups == 1 ? MID_TILES : MID_TILES_GROUPS);
+    return M > FEW_TOKENS && tiles <= (groups == 1 ? MID_TILES : MID_TILES_GROUPS);
 }
 
 // MT: tokens that k_grad_few holds, 0 for k_grad_mid.
