@@ -425,3 +425,59 @@ def test_gated_backward_every_activation(dev, m, k, f, act):  # noqa: F811
     slack = [d0 @ np.abs(wg).astype(np.float64) * ag[0], d0.T @ xd, 0, d0.sum(0), 0]
     for t, w, s, n, sl, name in zip(out, want, terms, [2 * f, m, m, m, m], slack, ("dx", "dWg", "dWu", "dbias_g", "dbias_u")):
         _within(_np(t), w, s, n, name, sl)
+
+
+@pytest.mark.parametrize("m,k,n", RANGES)
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_backward_keeps_what_is_not_finite_in_its_row_and_column(dev, m, k, n, bad):  # noqa: F811
+    """One gradient that is not a number or infinite: its token's dx and its channel's dW and dbias are
+    not finite, everything else is what it is without it."""
+    torch, bl = dev
+    _say(f"backward with {bad} M={m} K={k} N={n}")
+    rng = np.random.default_rng([74, m, k, n])
+    dy = _f32(rng.standard_normal((m, n)))
+    i, j = m // 3, n // 2
+    dy[i, j] = 0
+    x_q, beta = plain.absmax(rng.standard_normal((m, k)))
+    w, al, _ = _layer(rng, n, k, False)
+    rest = (_t(torch, x_q), _t(torch, beta), _t(torch, plain.pack(w)), _t(torch, al))
+    e = lambda *s: torch.empty(s, device="cuda")
+    want = bl.bitlinear_backward(_t(torch, dy), *rest, dx=e(m, k), dW=e(n, k), dbias=e(n))
+    dy[i, j] = bad
+    got = bl.bitlinear_backward(_t(torch, dy), *rest, dx=e(m, k), dW=e(n, k), dbias=e(n))
+    for t, c, row in zip(got, want, (i, j, j)):
+        assert not torch.isfinite(t[row]).any()
+        others = torch.arange(t.shape[0], device="cuda") != row
+        assert torch.equal(t[others], c[others])
+
+
+@pytest.mark.parametrize("m,k,n", [(40, 132, 90), (700, 132, 4100)])
+def test_backward_over_a_hundred_binades_in_a_graph(dev, m, k, n):  # noqa: F811
+    """Captured once; replays with other inputs, ordinary ones among them, and eager work between give the eager bits."""
+    torch, bl = dev
+    _say(f"backward hundred binades in a graph M={m} K={k} N={n}")
+    rng = np.random.default_rng([75, m, k, n])
+    x_q, beta = plain.absmax(rng.standard_normal((m, k)) * (rng.random((m, k)) < 0.2))
+    w, al, _ = _layer(rng, n, k, False)
+    w = (w * (rng.random((n, k)) < 0.2)).astype(np.int8)
+    e = lambda *s: torch.empty(s, device="cuda")
+    dy = _t(torch, _f32(rng.standard_normal((m, n))))
+    ws = torch.empty(bl.bitlinear_backward_workspace_size(m, k, n), dtype=torch.uint8, device="cuda")
+    args = (dy, _t(torch, x_q), _t(torch, beta), _t(torch, plain.pack(w)), _t(torch, al))
+    out = dict(dx=e(m, k), dW=e(n, k), dbias=e(n), workspace=ws)
+    bl.bitlinear_backward(*args, **out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bl.bitlinear_backward(*args, **out)
+    for rep, spread in enumerate((100, 0, 60, 100)):
+        dy.copy_(_t(torch, _f32(rng.standard_normal((m, n)) * np.exp2(rng.integers(-spread, 1, (m, n))))))
+        bl.bitlinear_backward(*args, **out)
+        eager = [out[q].clone() for q in ("dx", "dW", "dbias")]
+        for q in ("dx", "dW", "dbias"):
+            out[q].fill_(float("nan"))
+        ws.fill_(rep)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, out[q]) for a, q in zip(eager, ("dx", "dW", "dbias")))
