@@ -568,9 +568,10 @@ struct SplitArgs {
 // Three LDS stages (24 KiB each: a panel block of each operand) are filled two steps ahead by loads
 // that go past the registers; two workgroups share a compute unit.  Bytes v + 128 become fp16 as
 // 1024 + (v + 128), the byte under the exponent 0x64, minus 1152: two instructions for two values.
-// Bound: power.  The 739 GFLOP of gradients at 2048 tokens, K = 4096, F = 11008 (1.48 TFLOP in fp16) take 1.02
-// ms, 1.45 PFLOP/s of fp16 (a library's plain fp16 product of 8192^3: 1.48); the matrix cores are busy 77% of
-// the cycles and the clock is down between 1.6 and 1.8 GHz.  Before the panels and the byte operand
+// Bound: power.  The 739 GFLOP of gradients at 2048 tokens, K = 4096, F = 11008 (1.48 TFLOP in fp16) take 1.04
+// ms, 1.42 PFLOP/s of fp16 (a library's plain fp16 product of 8192^3: 1.48); the matrix cores are busy 75% of
+// the cycles and the clock is down between 1.6 and 1.8 GHz.  (Of it 1 to 2% for the integers times 2^-12 and the
+// look at rows with small elements.)  Before the panels and the byte operand
 // (64-byte pieces of rows, fp16 on both sides, 32 KiB a step): 1.16 ms; the order of the MFMAs, 256 x 256
 // tiles, a third stage there and operands read ahead across the barrier all measured level.
 // In the first MFMA of a step lane group g (lanes 32 g ..) holds l 16 g .. 16 g + 7, in the second
@@ -1034,13 +1035,13 @@ __global__ __launch_bounds__(256) void k_grad_few(BackwardArgs a, FewPlan p) {
 // several groups, as a part for each (a scale is taken over a part's terms, and the part scaled back before it
 // leaves); k_few_sum adds them.
 // Small elements as above: where there are tiny sums too, the workgroup adds what the elements lack.
-// Against the steps above (us): gated, K = 1024, F = 2731, 61 tokens (344 workgroups) 25.1 and 38.6; K = 512,
-// N = 512, 64 tokens (16) 10.9 and 23.8; K = 2944, N = 5335 (1008), 32 tokens 34.8 and 44.2, 64 tokens 43.3 and
-// 45.5; gated, K = 2048, F = 5504 (1376), 64 tokens 65.3 and 55.5: the parts of dx, as many bytes as dW.  With parts
-// of dW: K = 512, N = 512, 250 tokens (64) 15.0 and 25.2; K = 1280, N = 1230, 256 tokens (400) 28.6 and 31.8; K = 1000,
-// N = 1023, 500 tokens (512) 32.0 and 38.6; K = 2048, N = 2048, 250 tokens (1024) 54.4 and 36.3.
+// Against the steps above (us): gated, K = 1024, F = 2731, 61 tokens (344 workgroups) 26.7 and 41.2; K = 512,
+// N = 512, 64 tokens (16) 12.2 and 26.3; K = 2944, N = 5335 (1008), 32 tokens 36.2 and 45.4, 64 tokens 44.4 and
+// 47.0; gated, K = 2048, F = 5504 (1376), 64 tokens 64.6 and 58.3: the parts of dx, as many bytes as dW.  With parts
+// of dW: K = 512, N = 512, 250 tokens (64) 16.2 and 27.1; K = 1280, N = 1230, 256 tokens (400) 30.0 and 34.5; K = 1000,
+// N = 1023, 500 tokens (512) 33.4 and 41.2; K = 2048, N = 2048, 250 tokens (1024) 56.9 and 38.4.
 // Several tiles of rows in a workgroup halve those but hold twice the registers (gated, K = 1024, F = 2731, 61
-// tokens 33 us).  Bound: at a single tile latency, loads, three barriers and some 700 instructions of a wave.
+// tokens 33 us).  Bound: at a single tile latency, loads, three barriers and some 800 instructions of a wave.
 // LDS images: split gradients, rows of 64 values, the 16-byte unit u at position u ^ (row / 2) % 8; bytes,
 // columns of 64, the 16-byte unit u at position u ^ split_swizzle(column).
 constexpr int MID_TILES = 1024, MID_TILES_GROUPS = 512;

@@ -391,7 +391,9 @@ int bitlinear_gated_forward(const float* x, int64_t M, int64_t K, const uint8_t*
  *   dx        [M, K] fp32 or NULL.     dW  [N, K] fp32 or NULL.              (out)
  *   dbias     [N] fp32 or NULL.                                              (out)
  *   workspace >= bitlinear_backward_workspace_size(M, K, N) bytes, 256-byte aligned; scratch,
- *             one for each call that may overlap another.
+ *             one for each call that may overlap another.  It grows with the tokens: dy in two
+ *             layouts, x_q and W at a byte an element, and parts of sums (2048 tokens, 11008 ->
+ *             4096: 137 MB; gated 4096 -> 11008: 471 MB).
  * K % 4 == 0, M and N <= 2097152; any alignment of the tensors.  At least one output is given;
  * outputs must not overlap inputs or each other.  Errors: INVALID_ARG, SHAPE, ALIGNMENT and WORKSPACE (the
  * workspace), HIP.
