@@ -70,6 +70,18 @@ SIGNATURES = {
                                         _P, _SZ, _P]),
     "bitlinear_quantize_weights_i8": (_INT, [_P, _I64, _I64, _P, _P, _P]),
     "bitlinear_forward_i8": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P]),
+    "bitlinear_quantize_act_fp8": (_INT, [_P, _I64, _I64, _P, _P, _P]),
+    "bitlinear_quantize_weights_fp8": (_INT, [_P, _I64, _I64, _P, _P, _P]),
+    "bitlinear_forward_fp8": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P]),
+    "bitlinear_grouped_forward": (_INT, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P]),
+    "bitlinear_grouped_gated_forward": (_INT, [_P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _INT,
+                                               _P, _P, _P, _P, _P, _P]),
+    "bitlinear_grouped_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I64]),
+    "bitlinear_grouped_backward": (_INT, [_P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _SZ,
+                                          _P]),
+    "bitlinear_grouped_gated_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I64]),
+    "bitlinear_grouped_gated_backward": (_INT, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P,
+                                                _INT, _P, _P, _P, _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -623,6 +635,183 @@ def bitlinear_forward_i8(x_q, beta, W_q, gamma, bias=None, y=None, acc=None, str
         _shaped(bias, f32, "bias", (N,), dev), _shaped(y, f32, "y", (M, N), dev),
         _shaped(acc, torch.int32, "acc", (M, N), dev), _stream_on(stream, dev)))
     return y if acc is None else (y, acc)
+
+
+def _blocks(n):
+    """Blocks of 128 that n elements take."""
+    return -(-n // 128)
+
+
+def bitlinear_quantize_act_fp8(x, x_q=None, x_scale=None, stream=None):
+    """x [M, K] fp32 -> (x_q float8_e4m3fn [M, K], x_scale fp32 [ceil(K/128), M]): one scale for each
+    token and block of 128."""
+    torch = _torch()
+    M, K, dev = _rows(x, "x")
+    e4m3 = torch.float8_e4m3fn
+    if x_q is None:
+        x_q = _empty((M, K), e4m3, dev, stream)
+    if x_scale is None:
+        x_scale = _empty((_blocks(K), M), torch.float32, dev, stream)
+    _check("bitlinear_quantize_act_fp8", lib.bitlinear_quantize_act_fp8(
+        _shaped(x, torch.float32, "x", (M, K), dev), M, K, _shaped(x_q, e4m3, "x_q", (M, K), dev),
+        _shaped(x_scale, torch.float32, "x_scale", (_blocks(K), M), dev), _stream_on(stream, dev)))
+    return x_q, x_scale
+
+
+def bitlinear_quantize_weights_fp8(W, W_q=None, W_scale=None, stream=None):
+    """W [N, K] fp32 -> (W_q float8_e4m3fn [N, K], W_scale fp32 [ceil(N/128), ceil(K/128)]): one scale
+    for each block of 128 x 128."""
+    torch = _torch()
+    N, K, dev = _rows(W, "W")
+    e4m3 = torch.float8_e4m3fn
+    if W_q is None:
+        W_q = _empty((N, K), e4m3, dev, stream)
+    if W_scale is None:
+        W_scale = _empty((_blocks(N), _blocks(K)), torch.float32, dev, stream)
+    _check("bitlinear_quantize_weights_fp8", lib.bitlinear_quantize_weights_fp8(
+        _shaped(W, torch.float32, "W", (N, K), dev), N, K, _shaped(W_q, e4m3, "W_q", (N, K), dev),
+        _shaped(W_scale, torch.float32, "W_scale", (_blocks(N), _blocks(K)), dev), _stream_on(stream, dev)))
+    return W_q, W_scale
+
+
+def bitlinear_forward_fp8(x_q, x_scale, W_q, W_scale, bias=None, y=None, stream=None):
+    """y [M, N] = x_q . W_q^T with the scales of every block of 128 (+ bias)."""
+    torch = _torch()
+    M, K, dev = _rows(x_q, "x_q")
+    N = _first(W_q, "W_q")
+    f32, e4m3 = torch.float32, torch.float8_e4m3fn
+    if y is None:
+        y = _empty((M, N), f32, dev, stream)
+    _check("bitlinear_forward_fp8", lib.bitlinear_forward_fp8(
+        _shaped(x_q, e4m3, "x_q", (M, K), dev), _shaped(x_scale, f32, "x_scale", (_blocks(K), M), dev), M, K,
+        _shaped(W_q, e4m3, "W_q", (N, K), dev), _shaped(W_scale, f32, "W_scale", (_blocks(N), _blocks(K)), dev), N,
+        _shaped(bias, f32, "bias", (N,), dev), _shaped(y, f32, "y", (M, N), dev), _stream_on(stream, dev)))
+    return y
+
+
+def _experts(t, name):
+    """Experts and rows of each of a tensor of packed weights [E, N, K/4]."""
+    if getattr(t, "ndim", 0) != 3:
+        raise ValueError(f"{name} must have three dimensions")
+    return t.shape[0], t.shape[1]
+
+
+def _grouped_rows(rows, tokens):
+    """Rows of a grouped call: those of `rows`, or the tokens themselves."""
+    if rows is None:
+        return tokens
+    if getattr(rows, "ndim", 0) != 1:
+        raise ValueError("rows must be a vector")
+    return rows.shape[0]
+
+
+def bitlinear_grouped_forward(x_q, beta, offsets, W_packed, alpha, rows=None, bias=None, y=None, stream=None):
+    """y [M, N]: row m, in the group offsets[e] <= m < offsets[e + 1] of expert e, is the BitLinear of token
+    rows[m] (m itself without `rows`) under W_packed[e] [N, K/4], alpha[e] and bias[e].  x_q int8 [T, K],
+    beta [T]; offsets int64 [E + 1] and rows int64 [M] on the device.  Rows outside every group keep what
+    y holds."""
+    torch = _torch()
+    T, K, dev = _rows(x_q, "x_q")
+    E, N = _experts(W_packed, "W_packed")
+    M = _grouped_rows(rows, T)
+    f32, i64 = torch.float32, torch.int64
+    if y is None:
+        y = _empty((M, N), f32, dev, stream)
+    _check("bitlinear_grouped_forward", lib.bitlinear_grouped_forward(
+        _shaped(x_q, torch.int8, "x_q", (T, K), dev), _shaped(beta, f32, "beta", (T,), dev), T, K,
+        _shaped(rows, i64, "rows", (M,), dev), M, _shaped(offsets, i64, "offsets", (E + 1,), dev), E,
+        _shaped(W_packed, torch.uint8, "W_packed", (E, N, K // 4), dev), _shaped(alpha, f32, "alpha", (E,), dev), N,
+        _shaped(bias, f32, "bias", (E, N), dev), _shaped(y, f32, "y", (M, N), dev), _stream_on(stream, dev)))
+    return y
+
+
+def bitlinear_grouped_gated_forward(x, offsets, Wg_packed, alpha_g, Wu_packed, alpha_u, act, rows=None, bias_g=None,
+                                    bias_u=None, h=None, g=None, u=None, x_q=None, beta=None, stream=None):
+    """h [M, F]: row m is the gated block of token rows[m] of fp32 x [T, K] under the projections of its
+    group's expert, Wg_packed and Wu_packed [E, F, K/4]; offsets and rows as bitlinear_grouped_forward, the
+    rest as bitlinear_gated_forward.  Returns h."""
+    torch = _torch()
+    T, K, dev = _rows(x, "x")
+    E, F = _experts(Wg_packed, "Wg_packed")
+    M = _grouped_rows(rows, T)
+    f32, i64, u8 = torch.float32, torch.int64, torch.uint8
+    if h is None:
+        h = _empty((M, F), f32, dev, stream)
+    if x_q is None:
+        x_q = _empty((T, K), torch.int8, dev, stream, scratch=True)
+    if beta is None:
+        beta = _empty(T, f32, dev, stream, scratch=True)
+    _check("bitlinear_grouped_gated_forward", lib.bitlinear_grouped_gated_forward(
+        _shaped(x, f32, "x", (T, K), dev), T, K, _shaped(rows, i64, "rows", (M,), dev), M,
+        _shaped(offsets, i64, "offsets", (E + 1,), dev), E, _shaped(Wg_packed, u8, "Wg_packed", (E, F, K // 4), dev),
+        _shaped(alpha_g, f32, "alpha_g", (E,), dev), _shaped(bias_g, f32, "bias_g", (E, F), dev),
+        _shaped(Wu_packed, u8, "Wu_packed", (E, F, K // 4), dev), _shaped(alpha_u, f32, "alpha_u", (E,), dev),
+        _shaped(bias_u, f32, "bias_u", (E, F), dev), F, int(act), _shaped(h, f32, "h", (M, F), dev),
+        _shaped(g, f32, "g", (M, F), dev), _shaped(u, f32, "u", (M, F), dev), _shaped(x_q, torch.int8, "x_q", (T, K), dev),
+        _shaped(beta, f32, "beta", (T,), dev), _stream_on(stream, dev)))
+    return h
+
+
+def bitlinear_grouped_backward_workspace_size(M, K, N, E) -> int:
+    """Bytes of workspace of bitlinear_grouped_backward (0 for invalid sizes)."""
+    return lib.bitlinear_grouped_backward_workspace_size(M, K, N, E)
+
+
+def bitlinear_grouped_gated_backward_workspace_size(M, K, F, E) -> int:
+    """Bytes of workspace of bitlinear_grouped_gated_backward (0 for invalid sizes)."""
+    return lib.bitlinear_grouped_gated_backward_workspace_size(M, K, F, E)
+
+
+def bitlinear_grouped_backward(dy, x_q, beta, offsets, W_packed, alpha, rows=None, dx=None, dW=None, dbias=None,
+                               workspace=None, stream=None):
+    """Gradients of bitlinear_grouped_forward from dy [M, N]: dx [M, K] of every row, dW [E, N, K] and
+    dbias [E, N] of every expert, each written if its tensor is given; with none given, dx and dW are
+    allocated.  Returns (dx, dW, dbias), None for what was not asked for."""
+    torch = _torch()
+    M, N, dev = _rows(dy, "dy")
+    T, K, _ = _rows(x_q, "x_q")
+    E, _ = _experts(W_packed, "W_packed")
+    f32, i64 = torch.float32, torch.int64
+    if dx is None and dW is None and dbias is None:
+        dx = _empty((M, K), f32, dev, stream)
+        dW = _empty((E, N, K), f32, dev, stream)
+    workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_grouped_backward_workspace_size(M, K, N, E), dev, stream)
+    _check("bitlinear_grouped_backward", lib.bitlinear_grouped_backward(
+        _shaped(dy, f32, "dy", (M, N), dev), M, N, _shaped(x_q, torch.int8, "x_q", (T, K), dev),
+        _shaped(beta, f32, "beta", (T,), dev), T, K, _shaped(rows, i64, "rows", (M,), dev),
+        _shaped(offsets, i64, "offsets", (E + 1,), dev), E, _shaped(W_packed, torch.uint8, "W_packed", (E, N, K // 4), dev),
+        _shaped(alpha, f32, "alpha", (E,), dev), _shaped(dx, f32, "dx", (M, K), dev), _shaped(dW, f32, "dW", (E, N, K), dev),
+        _shaped(dbias, f32, "dbias", (E, N), dev), ws, ws_bytes, _stream_on(stream, dev)))
+    return dx, dW, dbias
+
+
+def bitlinear_grouped_gated_backward(dh, g, u, x_q, beta, offsets, Wg_packed, alpha_g, Wu_packed, alpha_u, act, rows=None,
+                                     dx=None, dWg=None, dWu=None, dbias_g=None, dbias_u=None, workspace=None, stream=None):
+    """Gradients of bitlinear_grouped_gated_forward from dh [M, F] and the g, u, x_q, beta it left: dx
+    [M, K] of every row, dWg and dWu [E, F, K] (both or neither), dbias_g and dbias_u [E, F], each written
+    if its tensor is given; with none given, dx, dWg and dWu are allocated.  Returns (dx, dWg, dWu,
+    dbias_g, dbias_u), None for what was not asked for."""
+    torch = _torch()
+    M, F, dev = _rows(dh, "dh")
+    T, K, _ = _rows(x_q, "x_q")
+    E, _ = _experts(Wg_packed, "Wg_packed")
+    f32, i64, u8 = torch.float32, torch.int64, torch.uint8
+    if dx is None and dWg is None and dWu is None and dbias_g is None and dbias_u is None:
+        dx = _empty((M, K), f32, dev, stream)
+        dWg = _empty((E, F, K), f32, dev, stream)
+        dWu = _empty((E, F, K), f32, dev, stream)
+    workspace, ws, ws_bytes = _workspace(workspace, lib.bitlinear_grouped_gated_backward_workspace_size(M, K, F, E), dev,
+                                         stream)
+    _check("bitlinear_grouped_gated_backward", lib.bitlinear_grouped_gated_backward(
+        _shaped(dh, f32, "dh", (M, F), dev), _shaped(g, f32, "g", (M, F), dev), _shaped(u, f32, "u", (M, F), dev), M, F,
+        _shaped(x_q, torch.int8, "x_q", (T, K), dev), _shaped(beta, f32, "beta", (T,), dev), T, K,
+        _shaped(rows, i64, "rows", (M,), dev), _shaped(offsets, i64, "offsets", (E + 1,), dev), E,
+        _shaped(Wg_packed, u8, "Wg_packed", (E, F, K // 4), dev), _shaped(alpha_g, f32, "alpha_g", (E,), dev),
+        _shaped(Wu_packed, u8, "Wu_packed", (E, F, K // 4), dev), _shaped(alpha_u, f32, "alpha_u", (E,), dev), int(act),
+        _shaped(dx, f32, "dx", (M, K), dev), _shaped(dWg, f32, "dWg", (E, F, K), dev), _shaped(dWu, f32, "dWu", (E, F, K), dev),
+        _shaped(dbias_g, f32, "dbias_g", (E, F), dev), _shaped(dbias_u, f32, "dbias_u", (E, F), dev), ws, ws_bytes,
+        _stream_on(stream, dev)))
+    return dx, dWg, dWu, dbias_g, dbias_u
 
 
 def bitlinear_forward_fused_kernel(M, K, N, x=None, W_packed=None, x_q=None) -> str:

@@ -6,6 +6,7 @@
 #include <limits.h>
 
 #include "common.hpp"
+#include "experts.hpp"
 #include "ffn.hpp"
 
 using namespace bitlinear;
@@ -431,6 +432,123 @@ int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_
     if (K > I8_MAX_K || M > INT_MAX || N > INT_MAX || M > most / N) return BITLINEAR_ERR_SHAPE;
     const I8Args a{x_q, beta, M, K, N, W_q, gamma, bias, y, acc};
     return hip_status(launch_forward_i8(a, stream));
+}
+
+// Sizes of the fp8 calls: element counts within 2^40, rows within a grid dimension.
+static int check_fp8(int64_t R, int64_t K) {
+    if (R <= 0 || K <= 0) return BITLINEAR_ERR_INVALID_ARG;
+    constexpr int64_t most = (int64_t)1 << 40;
+    return R > INT_MAX || K > FP8_MAX_K || R > most / K ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
+}
+
+int bitlinear_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* x_q, float* x_scale, hipStream_t stream) {
+    if (!x || !x_q || !x_scale) return BITLINEAR_ERR_INVALID_ARG;
+    const int st = check_fp8(M, K);
+    return st ? st : hip_status(launch_quantize_act_fp8(x, M, K, x_q, x_scale, stream));
+}
+
+int bitlinear_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t* W_q, float* W_scale, hipStream_t stream) {
+    if (!W || !W_q || !W_scale) return BITLINEAR_ERR_INVALID_ARG;
+    const int st = check_fp8(N, K);
+    return st ? st : hip_status(launch_quantize_weights_fp8(W, N, K, W_q, W_scale, stream));
+}
+
+int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, int64_t K, const uint8_t* W_q,
+                          const float* W_scale, int64_t N, const float* bias, float* y, hipStream_t stream) {
+    if (!x_q || !x_scale || !W_q || !W_scale || !y) return BITLINEAR_ERR_INVALID_ARG;
+    int st = check_fp8(M, K);
+    if (!st) st = check_fp8(N, K);
+    if (st) return st;
+    if (M > ((int64_t)1 << 40) / N) return BITLINEAR_ERR_SHAPE;
+    const Fp8Args a{x_q, x_scale, M, K, N, W_q, W_scale, bias, y};
+    return hip_status(launch_forward_fp8(a, stream));
+}
+
+// Sizes of the grouped calls; M == 0 is valid.
+static int check_grouped(int64_t T, int64_t K, const int64_t* rows, int64_t M, int64_t E, int64_t N) {
+    if (T < 0 || M < 0 || K <= 0 || N <= 0 || E <= 0 || (rows && M > 0 && T == 0)) return BITLINEAR_ERR_INVALID_ARG;
+    if (!rows && M > 0 && T != M) return BITLINEAR_ERR_SHAPE;
+    if (E > GROUPED_MAX_E || N > GROUPED_MAX_N || M > GROUPED_MAX_M) return BITLINEAR_ERR_SHAPE;
+    int st = check_sizes(M > 0 ? M : 1, K, N);
+    if (!st) st = check_sizes(T > 0 ? T : 1, K, N);
+    if (st) return st;
+    return E > ((int64_t)1 << 42) / (N * K) ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
+}
+
+int bitlinear_grouped_forward(const int8_t* x_q, const float* beta, int64_t T, int64_t K, const int64_t* rows, int64_t M,
+                              const int64_t* offsets, int64_t E, const uint8_t* W_packed, const float* alpha, int64_t N,
+                              const float* bias, float* y, hipStream_t stream) {
+    if (!offsets || !W_packed || !alpha || (M > 0 && (!x_q || !beta || !y))) return BITLINEAR_ERR_INVALID_ARG;
+    const int st = check_grouped(T, K, rows, M, E, N);
+    if (st || M == 0) return st;
+    const GroupedArgs a{x_q, beta, T, K, rows, M, offsets, E, W_packed, nullptr, alpha, nullptr, bias, nullptr, N, 0,
+                        y, nullptr, nullptr};
+    return hip_status(launch_grouped(a, stream));
+}
+
+int bitlinear_grouped_gated_forward(const float* x, int64_t T, int64_t K, const int64_t* rows, int64_t M,
+                                    const int64_t* offsets, int64_t E, const uint8_t* Wg_packed, const float* alpha_g,
+                                    const float* bias_g, const uint8_t* Wu_packed, const float* alpha_u,
+                                    const float* bias_u, int64_t F, int act, float* h, float* g, float* u, int8_t* x_q,
+                                    float* beta, hipStream_t stream) {
+    if (!offsets || !Wg_packed || !alpha_g || !Wu_packed || !alpha_u) return BITLINEAR_ERR_INVALID_ARG;
+    if ((T > 0 && (!x || !x_q || !beta)) || (M > 0 && !h)) return BITLINEAR_ERR_INVALID_ARG;
+    if (!g != !u || !known_activation(act)) return BITLINEAR_ERR_INVALID_ARG;
+    int st = check_grouped(T, K, rows, M, E, F);
+    if (st) return st;
+    if (T > 0) {
+        st = hip_status(launch_quantize_act(x, T, K, x_q, beta, stream));
+        if (st) return st;
+    }
+    if (M == 0) return BITLINEAR_OK;
+    const GroupedArgs a{x_q, beta, T, K, rows, M, offsets, E, Wg_packed, Wu_packed, alpha_g, alpha_u, bias_g, bias_u, F, act,
+                        h, g, u};
+    return hip_status(launch_grouped(a, stream));
+}
+
+// Workspace of a grouped backward call for valid sizes, else 0.
+static size_t grouped_backward_bytes(int64_t M, int64_t K, int64_t N, int64_t E, bool gated) {
+    return check_grouped(M, K, nullptr, M, E, N) == BITLINEAR_OK ? grouped_backward_workspace(M, K, N, E, gated) : 0;
+}
+
+size_t bitlinear_grouped_backward_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E) {
+    return grouped_backward_bytes(M, K, N, E, false);
+}
+
+size_t bitlinear_grouped_gated_backward_workspace_size(int64_t M, int64_t K, int64_t F, int64_t E) {
+    return grouped_backward_bytes(M, K, F, E, true);
+}
+
+static int run_grouped_backward(const GroupedBackwardArgs& a, size_t workspace_bytes, bool gated, hipStream_t stream) {
+    const int st = check_grouped(a.T, a.K, a.rows, a.M, a.E, a.N);
+    if (st) return st;
+    if (!a.ws || workspace_bytes < grouped_backward_workspace(a.M, a.K, a.N, a.E, gated)) return BITLINEAR_ERR_WORKSPACE;
+    if (!aligned(a.ws, 256)) return BITLINEAR_ERR_ALIGNMENT;
+    return hip_status(launch_grouped_backward(a, stream));
+}
+
+int bitlinear_grouped_backward(const float* dy, int64_t M, int64_t N, const int8_t* x_q, const float* beta, int64_t T, int64_t K,
+                               const int64_t* rows, const int64_t* offsets, int64_t E, const uint8_t* W_packed,
+                               const float* alpha, float* dx, float* dW, float* dbias, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+    if (!offsets || !W_packed || !alpha || (M > 0 && (!dy || !x_q || !beta))) return BITLINEAR_ERR_INVALID_ARG;
+    if (!dx && !dW && !dbias && M > 0) return BITLINEAR_ERR_INVALID_ARG;
+    const GroupedBackwardArgs a{dy, nullptr, nullptr, 0, M, K, N, T, x_q, beta, rows, offsets, E, W_packed, nullptr, alpha,
+                                nullptr, dx, dW, nullptr, dbias, nullptr, workspace};
+    return run_grouped_backward(a, workspace_bytes, false, stream);
+}
+
+int bitlinear_grouped_gated_backward(const float* dh, const float* g, const float* u, int64_t M, int64_t F, const int8_t* x_q,
+                                     const float* beta, int64_t T, int64_t K, const int64_t* rows, const int64_t* offsets,
+                                     int64_t E, const uint8_t* Wg_packed, const float* alpha_g, const uint8_t* Wu_packed,
+                                     const float* alpha_u, int act, float* dx, float* dWg, float* dWu, float* dbias_g,
+                                     float* dbias_u, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!offsets || !Wg_packed || !alpha_g || !Wu_packed || !alpha_u) return BITLINEAR_ERR_INVALID_ARG;
+    if (M > 0 && (!dh || !g || !u || !x_q || !beta)) return BITLINEAR_ERR_INVALID_ARG;
+    if (!dWg != !dWu || (!dx && !dWg && !dbias_g && !dbias_u && M > 0) || !known_activation(act)) return BITLINEAR_ERR_INVALID_ARG;
+    const GroupedBackwardArgs a{dh, g, u, act, M, K, F, T, x_q, beta, rows, offsets, E, Wg_packed, Wu_packed, alpha_g, alpha_u,
+                                dx, dWg, dWu, dbias_g, dbias_u, workspace};
+    return run_grouped_backward(a, workspace_bytes, true, stream);
 }
 
 const char* bitlinear_forward_fused_kernel(int64_t M, int64_t K, int64_t N, const float* x, const uint8_t* W_packed,

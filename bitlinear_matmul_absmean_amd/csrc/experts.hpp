@@ -1,0 +1,82 @@
+// experts.hpp -- products grouped by expert, their gradients, and the fp8 product with block scales: helpers
+// and launch declarations.
+#pragma once
+
+#include "bitlinear.h"
+#include "common.hpp"
+
+namespace bitlinear {
+
+// Largest sizes of the grouped calls: a grid's dimensions and thread count (one workgroup for each 16 rows
+// and 16 columns at most, of 512 threads, below 2^32 threads).
+constexpr int64_t GROUPED_MAX_E = 65535, GROUPED_MAX_N = (int64_t)1 << 21, GROUPED_MAX_M = (int64_t)1 << 24;
+
+// Group e as rows [lo, hi): offsets outside 0 .. M are taken as 0 or M.
+struct Group {
+    int64_t lo, hi;
+};
+__device__ __forceinline__ Group group_rows(const int64_t* __restrict__ offsets, int64_t e, int64_t M) {
+    const int64_t lo = offsets[e], hi = offsets[e + 1];
+    return Group{lo < 0 ? 0 : lo > M ? M : lo, hi < 0 ? 0 : hi > M ? M : hi};
+}
+
+// Token of row m: -1 for an index outside 0 .. T - 1.
+__device__ __forceinline__ int64_t row_token(const int64_t* __restrict__ rows, int64_t m, int64_t T) {
+    if (!rows) return m;
+    const int64_t r = rows[m];
+    return r >= 0 && r < T ? r : -1;
+}
+
+struct GroupedArgs {
+    const int8_t* xq;              // [T, K]
+    const float* beta;             // [T]
+    int64_t T, K;
+    const int64_t* rows;           // [M] or null
+    int64_t M;
+    const int64_t* offsets;        // [E + 1]
+    int64_t E;
+    const uint8_t *w0, *w1;        // packed [E, N, K/4]: one projection (w1 null), or gate and up
+    const float *al0, *al1;        // alpha [E]
+    const float *b0, *b1;          // bias [E, N] or null
+    int64_t N;
+    int act;                       // gated: a bitlinear_activation
+    float* y;                      // [M, N]: y, or h of the gated block
+    float *g, *u;                  // gated: [M, N] or both null
+};
+hipError_t launch_grouped(const GroupedArgs& a, hipStream_t s);
+
+struct GroupedBackwardArgs {
+    const float* dy;               // [M, N]; gated: dh
+    const float *g, *u;            // gated: [M, N]; else null
+    int act;
+    int64_t M, K, N, T;
+    const int8_t* xq;
+    const float* beta;
+    const int64_t *rows, *offsets;
+    int64_t E;
+    const uint8_t *w0, *w1;        // packed [E, N, K/4]; w1 null for one projection
+    const float *al0, *al1;        // alpha [E]
+    float* dx;                     // [M, K] or null
+    float *dw0, *dw1;              // [E, N, K] or null
+    float *db0, *db1;              // [E, N] or null
+    void* ws;
+};
+size_t grouped_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t E, bool gated);
+hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s);
+
+struct Fp8Args {
+    const uint8_t* xq;             // e4m3 [M, K]
+    const float* xs;               // [ceil(K / 128), M]
+    int64_t M, K, N;
+    const uint8_t* wq;             // e4m3 [N, K]
+    const float* ws;               // [ceil(N / 128), ceil(K / 128)]
+    const float* bias;             // [N] or null
+    float* y;                      // [M, N]
+};
+// 128 rows of x_q or W_q within 32-bit offsets.
+constexpr int64_t FP8_MAX_K = (int64_t)1 << 24;
+hipError_t launch_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* xq, float* xs, hipStream_t s);
+hipError_t launch_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t* wq, float* ws, hipStream_t s);
+hipError_t launch_forward_fp8(const Fp8Args& a, hipStream_t s);
+
+}  // namespace bitlinear

@@ -447,6 +447,115 @@ int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_
                          const float* gamma, int64_t N, const float* bias, float* y, int32_t* acc,
                          hipStream_t stream);
 
+/*
+ * Weights and activations in 8-bit floating point (e4m3: sign, 4 exponent and 3 mantissa bits, largest
+ * value 448, no infinities), one fp32 scale for each block of 128 along K:
+ *     scale = fp32(absmax of the block / 448),  code = e4m3(clip(fp32(v / scale), -448, 448)),
+ * rounded to nearest, ties to even.  A block of zeros (or whose scale is below the fp32 range) has
+ * scale 0 and codes 0.  The last block of a row ends with the row.
+ *   quantize_act_fp8:      blocks of one token x 128; x [M, K] fp32 (in); x_q [M, K] e4m3,
+ *                          x_scale [ceil(K / 128), M] fp32 (out): the tokens' scales of a block lie
+ *                          together, as a tile of tokens reads them.
+ *   quantize_weights_fp8:  blocks of 128 x 128; W [N, K] fp32 (in); W_q [N, K] e4m3,
+ *                          W_scale [ceil(N / 128), ceil(K / 128)] fp32 (out).
+ * Any K >= 1 and any alignment of fp32 elements.  Errors: INVALID_ARG, SHAPE, HIP.
+ */
+int bitlinear_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* x_q, float* x_scale,
+                               hipStream_t stream);
+int bitlinear_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t* W_q, float* W_scale,
+                                   hipStream_t stream);
+
+/*
+ * e4m3 x e4m3 matmul with a scale for each block of 128:
+ *     y[m, n] = sum_b (x_scale[b, m] W_scale[n / 128, b]) sum_{k in block b} x_q[m, k] W_q[n, k]  (+ bias[n])
+ * Products are exact; a block's sum, its product with the scales and the sum over blocks are taken in
+ * fp32, in an order fixed by the sizes (and the alignment): results are reproducible bit for bit.
+ *   x_q [M, K], x_scale [ceil(K / 128), M]; W_q [N, K], W_scale [ceil(N / 128), ceil(K / 128)], as the
+ *   quantizers lay them out; bias [N] or NULL.                               (in)
+ *   y [M, N] fp32.                                                           (out)
+ * Any K >= 1 and any alignment.  Errors: INVALID_ARG, SHAPE, HIP.
+ */
+int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, int64_t K, const uint8_t* W_q,
+                          const float* W_scale, int64_t N, const float* bias, float* y, hipStream_t stream);
+
+/*
+ * Products grouped by expert (the experts of a mixture layer): E BitLinears of one shape over M rows that
+ * lie sorted by expert, any number of rows for each, none among them.  Group e is the rows
+ * offsets[e] .. offsets[e + 1] - 1; row m reads token r = rows[m], or r = m where rows is NULL:
+ *     y[m, n] = bitlinear_forward(x_q[r], beta[r], W_packed[e], alpha[e], bias[e])[n],
+ * bit for bit.  Rows outside every group are left as they were in y.
+ *
+ *   x_q       [T, K] int8, beta [T] fp32: the tokens, from bitlinear_quantize_act.   (in)
+ *   rows      [M] int64 token of each row, or NULL (then T == M).  A token may occur any number of
+ *             times; an index outside 0 .. T - 1 reads a token of zeros (x_q = 0, beta = 0).  (in)
+ *   offsets   [E + 1] int64, on the device, not decreasing, within 0 .. M; beyond, they are taken as
+ *             0 or M, and a group that ends before it begins as empty.       (in)
+ *   W_packed  [E, N, K/4] uint8; alpha [E]; bias [E, N] or NULL.              (in)
+ *   y         [M, N] fp32.                                                   (out)
+ * K % 4 == 0, E <= 65535; any alignment of elements of their type.  M == 0 is a call without rows, for
+ * which x_q, beta, rows and y may be NULL.
+ * Outputs must not overlap inputs.  The host reads no device memory: the call can be captured into a graph
+ * and replayed with other offsets and rows.
+ * Errors: INVALID_ARG (null pointer, size < 0, K, N or E == 0, T == 0 with rows), SHAPE (T != M where rows is NULL and M > 0), HIP.
+ */
+int bitlinear_grouped_forward(const int8_t* x_q, const float* beta, int64_t T, int64_t K, const int64_t* rows,
+                              int64_t M, const int64_t* offsets, int64_t E, const uint8_t* W_packed,
+                              const float* alpha, int64_t N, const float* bias, float* y, hipStream_t stream);
+
+/*
+ * bitlinear_gated_forward grouped by expert: the T tokens x are quantized as by bitlinear_quantize_act, and
+ * row m of h (and g, u) is the gated block of token r under expert e's gate and up projections.
+ *   x [T, K] fp32; rows, offsets as bitlinear_grouped_forward.              (in)
+ *   Wg_packed, Wu_packed [E, F, K/4]; alpha_g, alpha_u [E]; bias_g, bias_u [E, F] or NULL.  (in)
+ *   h [M, F]; g, u [M, F], both or neither; x_q [T, K], beta [T]: the quantized tokens.     (out)
+ * Errors: as bitlinear_grouped_forward, and INVALID_ARG for an unknown act or one of g and u.
+ */
+int bitlinear_grouped_gated_forward(const float* x, int64_t T, int64_t K, const int64_t* rows, int64_t M,
+                                    const int64_t* offsets, int64_t E, const uint8_t* Wg_packed,
+                                    const float* alpha_g, const float* bias_g, const uint8_t* Wu_packed,
+                                    const float* alpha_u, const float* bias_u, int64_t F, int act, float* h,
+                                    float* g, float* u, int8_t* x_q, float* beta, hipStream_t stream);
+
+/*
+ * Gradients of bitlinear_grouped_forward, straight through both quantizers: with e the group of m and
+ * r its token,
+ *     dx[m, k]    = alpha[e] sum_n dy[m, n] W_hat[e, n, k]           (of the row; a token's is the sum of its rows')
+ *     dW[e, n, k] = sum_{m in e} dy[m, n] (beta[r] / 127) x_q[r, k]
+ *     dbias[e, n] = sum_{m in e} dy[m, n].
+ * fp32(dy alpha) and fp32(dy fp32(beta / 127)) enter the products whole (but for what lies below 2^-126),
+ * the products are exact, and sums are taken in fp32 (dbias in fp64) in an order fixed by the sizes and the
+ * offsets: results are reproducible bit for bit.  An expert without rows has dW and dbias 0; rows outside
+ * every group are left as they were in dx and add nothing to dW.  A gradient that is not finite makes its
+ * row of dx and its row dW[e, n] not finite, and no others.
+ *
+ *   dy [M, N] fp32; x_q, beta, rows, offsets, W_packed, alpha as the forward call used them.     (in)
+ *   dx [M, K], dW [E, N, K], dbias [E, N], each or NULL, one at least.                           (out)
+ *   workspace >= bitlinear_grouped_backward_workspace_size(M, K, N, E) bytes, 256-byte aligned; scratch,
+ *             one for each call that may overlap another.
+ * Sizes as the forward call's.  Errors: as the forward call, ALIGNMENT and WORKSPACE (the workspace).
+ */
+size_t bitlinear_grouped_backward_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E);
+int bitlinear_grouped_backward(const float* dy, int64_t M, int64_t N, const int8_t* x_q, const float* beta, int64_t T,
+                               int64_t K, const int64_t* rows, const int64_t* offsets, int64_t E,
+                               const uint8_t* W_packed, const float* alpha, float* dx, float* dW, float* dbias,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of bitlinear_grouped_gated_forward from dh and the g, u, x_q and beta it left: with
+ * dg = dh u a'(g) and du = dh a(g) (fp32, as bitlinear_gated_backward), dx is the sum of both projections'
+ * and dWg, dWu, dbias_g, dbias_u are theirs, as bitlinear_grouped_backward.
+ *   dh, g, u [M, F].   dx [M, K] or NULL; dWg, dWu [E, F, K], both or neither; dbias_g, dbias_u [E, F] or NULL.
+ *   workspace >= bitlinear_grouped_gated_backward_workspace_size(M, K, F, E) bytes: dg and du.
+ * Errors: as bitlinear_grouped_backward, and INVALID_ARG for an unknown act or one of dWg and dWu.
+ */
+size_t bitlinear_grouped_gated_backward_workspace_size(int64_t M, int64_t K, int64_t F, int64_t E);
+int bitlinear_grouped_gated_backward(const float* dh, const float* g, const float* u, int64_t M, int64_t F,
+                                     const int8_t* x_q, const float* beta, int64_t T, int64_t K, const int64_t* rows,
+                                     const int64_t* offsets, int64_t E, const uint8_t* Wg_packed,
+                                     const float* alpha_g, const uint8_t* Wu_packed, const float* alpha_u, int act,
+                                     float* dx, float* dWg, float* dWu, float* dbias_g, float* dbias_u,
+                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Kernel(s) bitlinear_forward_fused launches for these arguments ("gemv_fused" or
  * "quantize_act+forward"; a non-NULL x_q stands for x_q and beta given); a static string. */
 const char* bitlinear_forward_fused_kernel(int64_t M, int64_t K, int64_t N, const float* x,
