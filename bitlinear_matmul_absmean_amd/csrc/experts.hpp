@@ -73,8 +73,8 @@ struct Fp8Args {
     const float* bias;             // [N] or null
     float* y;                      // [M, N]
 };
-// 128 rows of x_q or W_q within 32-bit offsets.
-constexpr int64_t FP8_MAX_K = (int64_t)1 << 24;
+// 256 rows of x_q or W_q within 32-bit offsets.
+constexpr int64_t FP8_MAX_K = (int64_t)1 << 23;
 hipError_t launch_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* xq, float* xs, hipStream_t s);
 hipError_t launch_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t* wq, float* ws, hipStream_t s);
 hipError_t launch_forward_fp8(const Fp8Args& a, hipStream_t s);

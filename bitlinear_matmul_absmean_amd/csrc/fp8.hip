@@ -5,6 +5,7 @@
 // 1 x 128 (activations) and 128 x 128 (weights); and
 //     y[m, n] = sum_b (xs[b, m] ws[n / 128, b]) sum_{k in b} x_q[m, k] W_q[n, k]  (+ bias[n]).
 #include "experts.hpp"
+#include "ffn.hpp"
 
 namespace bitlinear {
 
@@ -125,30 +126,458 @@ hipError_t launch_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uin
 }
 
 // ---- product --------------------------------------------------------------------------------
-// One output a thread, block after block.
-__global__ __launch_bounds__(256) void k_fp8_plain(Fp8Args a) {
-    const int64_t n = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63), m = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6);
-    if (n >= a.N || m >= a.M) return;
-    const int64_t nb = (a.K + 127) / 128;
-    const uint8_t *x = a.xq + m * a.K, *w = a.wq + n * a.K;
-    float sum = 0.0f;
-    for (int64_t b = 0; b < nb; ++b) {
-        const int64_t end = (b + 1) * 128 < a.K ? (b + 1) * 128 : a.K;
-        float part = 0.0f;
-        for (int64_t k = b * 128; k < end; ++k)
-            part += __builtin_amdgcn_cvt_f32_fp8((int)x[k], 0) * __builtin_amdgcn_cvt_f32_fp8((int)w[k], 0);
-        sum += part * (a.xs[b * a.M + m] * a.ws[n / 128 * nb + b]);
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// The products run on the f16 matrix cores, into which every e4m3 value fits as it is: those for e4m3 operands
+// (f8f6f4 and the older form alike) align the products of a group of eight to the largest and drop what lies
+// below 2^-13 of it, so that their sums are good to about 2^-16 and not to fp32.
+// Eight e4m3 values as an f16 operand: four conversions of two.
+__device__ __forceinline__ f16x8 f16_of(uint32_t lo, uint32_t hi) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// How the rows lie: 16-byte aligned (and K % 16 == 0), on dwords, or anywhere.
+constexpr int ROWS_16 = 16, ROWS_4 = 4, ROWS_1 = 1;
+
+// Four outputs of one token, channels n .. n + 3 of `left` that are there.
+__device__ __forceinline__ void fp8_store(const Fp8Args& a, int64_t m, int64_t n, int64_t left, float4 v, bool vector) {
+    if (vector && left >= 4) {
+        if (a.bias) {
+            const float4 b = *reinterpret_cast<const float4*>(a.bias + n);
+            v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+        }
+        *reinterpret_cast<float4*>(a.y + m * a.N + n) = v;
+        return;
     }
-    a.y[m * a.N + n] = a.bias ? sum + a.bias[n] : sum;
+    const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < left) a.y[m * a.N + n + i] = a.bias ? e[i] + a.bias[n + i] : e[i];
+}
+
+// ---- few tokens -----------------------------------------------------------------------------
+// A workgroup of eight waves computes 16 MT tokens x 16 RB channels; wave w takes the blocks of 128 k
+// w, w + 8, ..., and the eight partial tiles are added at the end, in the waves' order.  Operands go straight
+// into registers, two blocks ahead.
+// 16x16x32 lane layout: A/B lane l holds row/column l % 16 and eight values of k (the same assignment of k to
+// lanes and bytes serves both, so any will do); accumulator r of lane l is row 4 (l / 16) + r, column l % 16.
+constexpr int FD_WAVES = 8;
+
+template <int ROWS, int MT, int RB>
+__global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices) {
+    constexpr bool DWORDS = ROWS == ROWS_1;
+    __shared__ f32x4 part[FD_WAVES * MT * 64];
+    const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t K = a.K;
+    const int64_t m0 = (int64_t)(blockIdx.x % slices) * (16 * MT), n0 = (int64_t)(blockIdx.x / slices) * (16 * RB);
+    const int rows_m = (int)(a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT), rows_n = (int)(a.N - n0 < 16 * RB ? a.N - n0 : 16 * RB);
+    const int blocks = (int)((K + 127) / 128), whole = (int)(K / 128);
+    const float* ws = a.ws + n0 / 128 * blocks;                 // 16 RB divides 128
+    const uint8_t *xp[MT], *wp[RB];
+    const float* xs[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int64_t m = m0 + min(16 * t + lr, rows_m - 1);
+        xp[t] = a.xq + m * K;
+        xs[t] = a.xs + m;
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) wp[r] = a.wq + (n0 + min(16 * r + lr, rows_n - 1)) * K;
+    struct Part {
+        u32x4 x[MT][2], w[RB][2];
+        float s[MT];
+    };
+    // block b: lane group lg takes bytes 16 lg .. and 64 + 16 lg .. of it
+    auto load = [&](int b) {
+        Part f;
+        const int64_t k = (int64_t)b * 128 + 16 * lg;
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f.w[r][h] = load_16<DWORDS>(wp[r] + k + 64 * h);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f.x[t][h] = load_16<DWORDS>(xp[t] + k + 64 * h);
+        const float w = ws[b];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) f.s[t] = xs[t][(int64_t)b * a.M] * w;
+        return f;
+    };
+    f32x4 acc[RB][MT];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // 16 x 16 products of 32 k (eight bytes a lane): weights are the rows, tokens the columns
+    auto multiply = [&](const Part& f) {
+        f32x4 p[RB][MT];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            f16x8 w[RB], x[MT];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) w[r] = f16_of(f.w[r][q >> 1][2 * (q & 1)], f.w[r][q >> 1][2 * (q & 1) + 1]);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) x[t] = f16_of(f.x[t][q >> 1][2 * (q & 1)], f.x[t][q >> 1][2 * (q & 1) + 1]);
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    p[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[r], x[t], q ? p[r][t] : f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(p[r][t][i], f.s[t], acc[r][t][i]);
+    };
+    if (wave < whole) {
+        const int last = wave + (whole - 1 - wave) / FD_WAVES * FD_WAVES;
+        Part f0 = load(wave), f1 = load(min(wave + FD_WAVES, last));
+        for (int b = wave; b < whole; b += 2 * FD_WAVES) {
+            const Part f2 = load(min(b + 2 * FD_WAVES, last));
+            multiply(f0);
+            f0 = f2;
+            if (b + FD_WAVES >= whole) break;
+            const Part f3 = load(min(b + 3 * FD_WAVES, last));
+            multiply(f1);
+            f1 = f3;
+        }
+    }
+    if (whole < blocks && whole % FD_WAVES == wave) {           // what is left of K
+        Part f;
+        const int64_t k = (int64_t)whole * 128 + 16 * lg;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int r = 0; r < RB; ++r) f.w[r][h] = row_16<DWORDS>(wp[r], k + 64 * h, K);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) f.x[t][h] = row_16<DWORDS>(xp[t], k + 64 * h, K);
+        }
+        const float w = ws[whole];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) f.s[t] = xs[t][(int64_t)whole * a.M] * w;
+        multiply(f);
+    }
+    const bool vector = a.N % 4 == 0 && (uintptr_t)a.y % 16 == 0 && (uintptr_t)a.bias % 16 == 0;
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < MT; ++t) part[(wave * MT + t) * 64 + lane] = acc[r][t];
+        __syncthreads();
+        for (int e = tid; e < MT * 64; e += 64 * FD_WAVES) {
+            const int l = e & 63, t = e >> 6, m = 16 * t + (l & 15), n = 16 * r + 4 * (l >> 4);
+            f32x4 sum = part[t * 64 + l];
+#pragma unroll
+            for (int w = 1; w < FD_WAVES; ++w) sum += part[(w * MT + t) * 64 + l];
+            if (m < rows_m && n < rows_n) fp8_store(a, m0 + m, n0 + n, rows_n - n, make_float4(sum[0], sum[1], sum[2], sum[3]), vector);
+        }
+    }
+}
+
+template <int ROWS, int MT, int RB>
+static hipError_t launch_fp8_dec_rb(const Fp8Args& a, hipStream_t s) {
+    const int64_t slices = (a.M + 16 * MT - 1) / (16 * MT), blocks = (a.N + 16 * RB - 1) / (16 * RB);
+    hipLaunchKernelGGL((k_fp8_dec<ROWS, MT, RB>), dim3((unsigned)(slices * blocks)), dim3(64 * FD_WAVES), 0, s, a, (int)slices);
+    return hipGetLastError();
+}
+
+template <int ROWS>
+static hipError_t launch_fp8_dec(const Fp8Args& a, hipStream_t s) {
+    const int64_t tiles = (a.M + 15) / 16;
+    return tiles == 1   ? launch_fp8_dec_rb<ROWS, 1, 1>(a, s)
+           : tiles == 2 ? launch_fp8_dec_rb<ROWS, 2, 1>(a, s)
+           : tiles == 3 ? launch_fp8_dec_rb<ROWS, 3, 1>(a, s)
+                        : launch_fp8_dec_rb<ROWS, 4, 1>(a, s);
+}
+
+// ---- many tokens ----------------------------------------------------------------------------
+// A workgroup of eight waves computes 64 MI tokens x 128 FN channels, a wave 32 MI x 32 FN of them in 32 x 32
+// blocks, a block of 128 k a step; three LDS stages (up to 48 KiB each), filled two steps ahead by loads that
+// go past the registers (aligned rows), or two filled through registers.
+// Unit u (16 bytes) of row r lies at slot u ^ ((r / 2) % 8) of its eight: no bank conflicts.
+// A step's sums meet their token's scale while the matrix cores are at the next step's first products.
+// 32x32x16 lane layout: A/B lane l holds row/column l % 32 and eight values of k; accumulator r of lane l is
+// row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
+constexpr int FG_BK = 128;
+
+template <int ROWS, int MI, int FN>
+__global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int tiles_n) {
+    constexpr bool ALIGNED = ROWS == ROWS_16, DWORDS = ROWS == ROWS_1;
+    constexpr int BM = 64 * MI, BN = 128 * FN, OB = BM * 8, UNITS = OB + BN * 8;
+    __shared__ i32x4 st0[UNITS];
+    __shared__ i32x4 st1[UNITS];
+    __shared__ i32x4 st2[ALIGNED ? UNITS : 1];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // a contiguous run of tiles for each XCD, four rows of tiles at a time
+    const int T = tiles_m * tiles_n, xcd = blockIdx.x & 7, per = T >> 3, rem = T & 7;
+    int t = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+    const int grp = t / (4 * tiles_n), gm = tiles_m - 4 * grp < 4 ? tiles_m - 4 * grp : 4;
+    t -= grp * 4 * tiles_n;
+    const int64_t m0 = (int64_t)(4 * grp + t % gm) * BM, n0 = (int64_t)(t / gm) * BN;
+    const int64_t K = a.K;
+    const int rows_m = (int)(a.M - m0 < BM ? a.M - m0 : BM), rows_n = (int)(a.N - n0 < BN ? a.N - n0 : BN);
+    const uint8_t* x0 = a.xq + m0 * K;
+    const uint8_t* w0 = a.wq + n0 * K;
+    const int blocks = (int)((K + 127) / 128), steps = (int)(K / FG_BK), last = steps - 1;
+
+    const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
+    // scales: of a lane's tokens, and of the block of 128 channels that holds the wave's (its first row may lie
+    // past the end: then nothing of it is written)
+    const float* xs[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) xs[i] = a.xs + m0 + min(32 * MI * wi + 32 * i + lr, rows_m - 1);
+    const float* ws = a.ws + (n0 + min(32 * FN * wj, rows_n - 1)) / 128 * blocks;
+
+    f32x16 acc[MI][FN], prt[MI][FN];
+    float sc[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        sc[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = prt[i][j] = f32x16{};
+    }
+    struct Frag {
+        u32x4 w[FN], x[MI];
+    };
+    // operands of k 32 kk .. 32 kk + 31 of the step in stage st
+    auto read = [&](const i32x4* st, int kk) {
+        const int at = (2 * kk + lg) ^ sw;
+        Frag f;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) f.w[j] = (u32x4)st[OB + (32 * FN * wj + 32 * j + lr) * 8 + at];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) f.x[i] = (u32x4)st[(32 * MI * wi + 32 * i + lr) * 8 + at];
+        return f;
+    };
+    // the last step's sums, times their scale, into acc
+    auto settle = [&](int i, int j) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(prt[i][j][e], sc[i], acc[i][j][e]);
+    };
+    // two products of 16 k of every block; a step's first ones follow what is left of the step before it
+    auto multiply = [&](const Frag& f, bool first) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f16x8 w[FN], x[MI];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) w[j] = f16_of(f.w[j][2 * h], f.w[j][2 * h + 1]);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) x[i] = f16_of(f.x[i][2 * h], f.x[i][2 * h + 1]);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    if (first && h == 0) {
+                        settle(i, j);
+                        prt[i][j] = f32x16{};
+                    }
+                    prt[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w[j], x[i], prt[i][j], 0, 0, 0);
+                }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    struct Scales {
+        float s[MI];
+    };
+    auto scales = [&](int b) {
+        Scales v;
+        const float w = ws[b];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) v.s[i] = xs[i][(int64_t)b * a.M] * w;
+        return v;
+    };
+    // the scales of the sums that are being formed
+    auto use = [&](const Scales& v) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) sc[i] = v.s[i];
+    };
+    // load block q (8 rows): wave w takes MI w .. MI w + MI - 1 of x_q and 2 FN w .. 2 FN w + 2 FN - 1 of W_q
+    auto block_row = [&](int q) { return 8 * q + (lane >> 3); };
+    auto block_unit = [&](int q) { return (lane & 7) ^ ((block_row(q) >> 1) & 7); };
+    if constexpr (ALIGNED) {
+        const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
+        const __amdgpu_buffer_rsrc_t rw = raw_buffer(w0, (uint32_t)rows_n * (uint32_t)K);
+        uint32_t xo[MI], wo[2 * FN];
+#pragma unroll
+        for (int q = 0; q < MI; ++q)
+            xo[q] = (uint32_t)min(block_row(MI * wave + q), rows_m - 1) * (uint32_t)K + 16u * block_unit(MI * wave + q);
+#pragma unroll
+        for (int q = 0; q < 2 * FN; ++q)
+            wo[q] = (uint32_t)min(block_row(2 * FN * wave + q), rows_n - 1) * (uint32_t)K + 16u * block_unit(2 * FN * wave + q);
+        // a third of a step's loads
+        auto fetch = [&](i32x4* st, int s, int third) {
+            const uint32_t so = (uint32_t)s * FG_BK;
+            if (third == 0) {
+#pragma unroll
+                for (int q = 0; q < MI; ++q) load_lds16(rx, xo[q], so, st + 64 * (MI * wave + q));
+            } else {
+#pragma unroll
+                for (int q = FN * (third - 1); q < FN * third; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (2 * FN * wave + q));
+            }
+        };
+        // Step s in stage `cur`, its first operands in f0, its scales in sv.  Operands are read one part ahead of
+        // their products, across the turn too; the stage that a turn frees is loaded with the step after next but
+        // one, a third at a time.  Loads past the last whole step repeat it and are not read.
+        auto step = [&](i32x4* cur, i32x4* nxt, i32x4* prv, int s, Frag& f0, Scales& sv) {
+            Frag f1 = read(cur, 1);
+            const Scales sn = scales(min(s + 1, last));
+            fetch(prv, min(s + 2, last), 1);
+            multiply(f0, true);
+            use(sv);
+            f0 = read(cur, 2);
+            fetch(prv, min(s + 2, last), 2);
+            multiply(f1, false);
+            f1 = read(cur, 3);
+            multiply(f0, false);
+            sv = sn;
+            // step s + 1 has landed for every wave, and every wave holds the rest of step s in registers
+            __builtin_amdgcn_s_waitcnt(0x0070 | (MI + 2 * FN));                 // vmcnt(the loads of step s + 2) lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            f0 = read(nxt, 0);
+            fetch(cur, min(s + 3, last), 0);
+            multiply(f1, false);
+        };
+        if (steps > 0) {
+            Scales sv = scales(0);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) fetch(st0, 0, q);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) fetch(st1, min(1, last), q);
+            fetch(st2, min(2, last), 0);
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0x0070 | (2 * MI + 2 * FN));             // vmcnt(the loads after step 0's) lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            Frag f = read(st0, 0);
+            int s = 0;
+            for (; s + 3 <= steps; s += 3) {
+                step(st0, st1, st2, s, f, sv);
+                step(st1, st2, st0, s + 1, f, sv);
+                step(st2, st0, st1, s + 2, f, sv);
+            }
+            if (s < steps) step(st0, st1, st2, s, f, sv);
+            if (s + 1 < steps) step(st1, st2, st0, s + 1, f, sv);
+            __builtin_amdgcn_s_waitcnt(0x0070);                                 // nothing is in flight into the stages any more
+        }
+    } else {
+        const uint8_t *xp[MI], *wp[2 * FN];
+#pragma unroll
+        for (int q = 0; q < MI; ++q) xp[q] = x0 + (int64_t)min(block_row(MI * wave + q), rows_m - 1) * K;
+#pragma unroll
+        for (int q = 0; q < 2 * FN; ++q) wp[q] = w0 + (int64_t)min(block_row(2 * FN * wave + q), rows_n - 1) * K;
+        struct Regs {
+            u32x4 v[MI + 2 * FN];
+        };
+        auto load = [&](int s) {
+            const int64_t k = (int64_t)s * FG_BK;
+            Regs r;
+#pragma unroll
+            for (int q = 0; q < MI; ++q) r.v[q] = load_16<DWORDS>(xp[q] + k + 16 * block_unit(MI * wave + q));
+#pragma unroll
+            for (int q = 0; q < 2 * FN; ++q) r.v[MI + q] = load_16<DWORDS>(wp[q] + k + 16 * block_unit(2 * FN * wave + q));
+            return r;
+        };
+        auto put = [&](i32x4* st, const Regs& r) {
+#pragma unroll
+            for (int q = 0; q < MI; ++q) st[64 * (MI * wave + q) + lane] = (i32x4)r.v[q];
+#pragma unroll
+            for (int q = 0; q < 2 * FN; ++q) st[OB + 64 * (2 * FN * wave + q) + lane] = (i32x4)r.v[MI + q];
+        };
+        auto multiply_stage = [&](const i32x4* st, int b) {
+            const Scales sv = scales(b);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                multiply(read(st, kk), kk == 0);
+                if (kk == 0) use(sv);
+            }
+        };
+        // whole steps in st1 and st0 in turn, loaded two ahead
+        Regs r0, r1;
+        if (steps > 0) {
+            r0 = load(0);
+            r1 = load(min(1, last));
+        }
+        for (int s = 0; s < steps; s += 2) {
+            put(st1, r0);                          // its last readers are past the barrier before this one
+            r0 = load(min(s + 2, last));
+            __syncthreads();
+            multiply_stage(st1, s);
+            if (s + 1 >= steps) break;
+            put(st0, r1);
+            r1 = load(min(s + 3, last));
+            __syncthreads();
+            multiply_stage(st0, s + 1);
+        }
+    }
+    if (steps < blocks) {                          // what is left of K straight into the operands
+        const Scales sv = scales(steps);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int64_t k = (int64_t)steps * FG_BK + 32 * kk + 16 * lg;
+            Frag f;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) f.w[j] = row_16<DWORDS>(w0 + (int64_t)min(32 * FN * wj + 32 * j + lr, rows_n - 1) * K, k, K);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) f.x[i] = row_16<DWORDS>(x0 + (int64_t)min(32 * MI * wi + 32 * i + lr, rows_m - 1) * K, k, K);
+            multiply(f, kk == 0);
+            if (kk == 0) use(sv);
+        }
+    }
+    const bool vector = a.N % 4 == 0 && (uintptr_t)a.y % 16 == 0 && (uintptr_t)a.bias % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int m = 32 * MI * wi + 32 * i + lr;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            settle(i, j);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = 32 * FN * wj + 32 * j + 8 * q + 4 * lg;
+                if (m < rows_m && n < rows_n)
+                    fp8_store(a, m0 + m, n0 + n, rows_n - n,
+                              make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]), vector);
+            }
+        }
+    }
+}
+
+template <int ROWS, int MI, int FN>
+static hipError_t launch_fp8_gemm_tile(const Fp8Args& a, hipStream_t s) {
+    const int64_t tm = (a.M + 64 * MI - 1) / (64 * MI), tn = (a.N + 128 * FN - 1) / (128 * FN);
+    hipLaunchKernelGGL((k_fp8_gemm<ROWS, MI, FN>), dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, (int)tm, (int)tn);
+    return hipGetLastError();
+}
+
+// Tiles of 64 x 256: what the choices below count.
+static int64_t fp8_tiles(const Fp8Args& a) { return (a.M + 63) / 64 * ((a.N + 255) / 256); }
+
+template <int ROWS>
+static hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
+    const int64_t tiles = fp8_tiles(a);
+    if (tiles <= 128) return launch_fp8_gemm_tile<ROWS, 1, 1>(a, s);
+    if (tiles <= 256) return launch_fp8_gemm_tile<ROWS, 1, 2>(a, s);
+    return launch_fp8_gemm_tile<ROWS == ROWS_1 ? ROWS_4 : ROWS, 2, 2>(a, s);
+}
+
+template <int ROWS>
+static hipError_t launch_fp8(const Fp8Args& a, hipStream_t s) {
+    return a.M <= 16 || fp8_tiles(a) <= 32 ? launch_fp8_dec<ROWS>(a, s) : launch_fp8_gemm<ROWS>(a, s);
 }
 
 hipError_t launch_forward_fp8(const Fp8Args& a, hipStream_t s) {
-    const int64_t step = (int64_t)65535 * 4;
-    for (int64_t m0 = 0; m0 < a.M; m0 += step) {
-        if (m0) return hipErrorInvalidValue;
-        hipLaunchKernelGGL(k_fp8_plain, dim3((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 3) / 4)), dim3(256), 0, s, a);
-    }
-    return hipGetLastError();
+    const uintptr_t low = (uintptr_t)a.xq | (uintptr_t)a.wq | (uintptr_t)a.K;
+    return low % 16 == 0 ? launch_fp8<ROWS_16>(a, s) : low % 4 == 0 ? launch_fp8<ROWS_4>(a, s) : launch_fp8<ROWS_1>(a, s);
 }
 
 }  // namespace bitlinear

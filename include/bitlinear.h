@@ -458,7 +458,7 @@ int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_
  *                          together, as a tile of tokens reads them.
  *   quantize_weights_fp8:  blocks of 128 x 128; W [N, K] fp32 (in); W_q [N, K] e4m3,
  *                          W_scale [ceil(N / 128), ceil(K / 128)] fp32 (out).
- * Any K >= 1 and any alignment of fp32 elements.  Errors: INVALID_ARG, SHAPE, HIP.
+ * 1 <= K <= 8388608, any alignment of fp32 elements.  Errors: INVALID_ARG, SHAPE, HIP.
  */
 int bitlinear_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* x_q, float* x_scale,
                                hipStream_t stream);
@@ -473,7 +473,7 @@ int bitlinear_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t
  *   x_q [M, K], x_scale [ceil(K / 128), M]; W_q [N, K], W_scale [ceil(N / 128), ceil(K / 128)], as the
  *   quantizers lay them out; bias [N] or NULL.                               (in)
  *   y [M, N] fp32.                                                           (out)
- * Any K >= 1 and any alignment.  Errors: INVALID_ARG, SHAPE, HIP.
+ * 1 <= K <= 8388608, any alignment.  Errors: INVALID_ARG, SHAPE, HIP.
  */
 int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, int64_t K, const uint8_t* W_q,
                           const float* W_scale, int64_t N, const float* bias, float* y, hipStream_t stream);
