@@ -4,6 +4,8 @@
 // What is computed: scale = fp32(absmax / 448), code = e4m3(clip(fp32(v / scale), +-448)) for blocks of
 // 1 x 128 (activations) and 128 x 128 (weights); and
 //     y[m, n] = sum_b (xs[b, m] ws[n / 128, b]) sum_{k in b} x_q[m, k] W_q[n, k]  (+ bias[n]).
+#include <type_traits>
+
 #include "experts.hpp"
 #include "ffn.hpp"
 
@@ -14,8 +16,29 @@ __device__ __forceinline__ uint32_t e4m3_4(float a, float b, float c, float d) {
     int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
-__device__ __forceinline__ float e4m3_quotient(float v, float scale) {
-    return scale > 0.0f ? fminf(fmaxf(v / scale, -448.0f), 448.0f) : 0.0f;
+// v / scale rounded as an IEEE division, clipped to +-448.  With y = fp32(1 / scale), q = fp32(v y) and the exact
+// remainder r = v - q scale, q + r y rounds to the quotient (Markstein).  r is exact where its bits lie above
+// 2^-149: for scales of at least 2^-80 and quotients of at least 2^-11; smaller quotients are a code of zero
+// either way.  Scales beyond take the division (which is three times the instructions).
+struct Divisor {
+    float scale, y;
+    bool fast;
+};
+__device__ __forceinline__ Divisor divisor(float scale) { return Divisor{scale, 1.0f / scale, scale >= 0x1p-80f && scale <= 0x1p100f}; }
+template <bool FAST>
+__device__ __forceinline__ float quotient(float v, const Divisor& d) {
+    float q;
+    if constexpr (FAST) {
+        q = v * d.y;
+        q = __builtin_fmaf(__builtin_fmaf(-q, d.scale, v), d.y, q);
+    } else {
+        q = d.scale > 0.0f ? v / d.scale : 0.0f;
+    }
+    return fminf(fmaxf(q, -448.0f), 448.0f);
+}
+template <bool FAST>
+__device__ __forceinline__ uint32_t codes_4(float4 v, const Divisor& d) {
+    return e4m3_4(quotient<FAST>(v.x, d), quotient<FAST>(v.y, d), quotient<FAST>(v.z, d), quotient<FAST>(v.w, d));
 }
 
 // Four floats at p + i of a row that ends at n, zeros past it.
@@ -58,10 +81,9 @@ __global__ __launch_bounds__(256) void k_quantize_act_fp8(const float* __restric
     float top = abs_max_4(v);
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 32));
-    const float scale = top / 448.0f;
-    put_4<WHOLE>(xq + m * K, b * 128 + 4 * lane, K,
-                 e4m3_4(e4m3_quotient(v.x, scale), e4m3_quotient(v.y, scale), e4m3_quotient(v.z, scale), e4m3_quotient(v.w, scale)));
-    if (lane == 0) xs[b * M + m] = scale;
+    const Divisor d = divisor(top / 448.0f);
+    put_4<WHOLE>(xq + m * K, b * 128 + 4 * lane, K, d.fast ? codes_4<true>(v, d) : codes_4<false>(v, d));
+    if (lane == 0) xs[b * M + m] = d.scale;
 }
 
 hipError_t launch_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* xq, float* xs, hipStream_t s) {
@@ -96,15 +118,17 @@ __global__ __launch_bounds__(256) void k_quantize_weights_fp8(const float* __res
     if ((tid & 63) == 0) red[tid >> 6] = top;
     __syncthreads();
     top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float scale = top / 448.0f;
+    const Divisor d = divisor(top / 448.0f);
+    auto write = [&](auto fast) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t n = n0 + 8 * i + r;
-        if (n < N)
-            put_4<WHOLE>(wq + n * K, k, K, e4m3_4(e4m3_quotient(v[i].x, scale), e4m3_quotient(v[i].y, scale),
-                                                  e4m3_quotient(v[i].z, scale), e4m3_quotient(v[i].w, scale)));
-    }
-    if (tid == 0) ws[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = scale;
+        for (int i = 0; i < 16; ++i) {
+            const int64_t n = n0 + 8 * i + r;
+            if (n < N) put_4<WHOLE>(wq + n * K, k, K, codes_4<decltype(fast)::value>(v[i], d));
+        }
+    };
+    if (d.fast) write(std::true_type());
+    else write(std::false_type());
+    if (tid == 0) ws[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = d.scale;
 }
 
 hipError_t launch_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t* wq, float* ws, hipStream_t s) {
@@ -191,7 +215,7 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
     for (int r = 0; r < RB; ++r) wp[r] = a.wq + (n0 + min(16 * r + lr, rows_n - 1)) * K;
     struct Part {
         u32x4 x[MT][2], w[RB][2];
-        float s[MT];
+        float s[MT], sw;
     };
     // block b: lane group lg takes bytes 16 lg .. and 64 + 16 lg .. of it
     auto load = [&](int b) {
@@ -205,9 +229,9 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) f.x[t][h] = load_16<DWORDS>(xp[t] + k + 64 * h);
-        const float w = ws[b];
+        f.sw = ws[b];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) f.s[t] = xs[t][(int64_t)b * a.M] * w;
+        for (int t = 0; t < MT; ++t) f.s[t] = xs[t][(int64_t)b * a.M];
         return f;
     };
     f32x4 acc[RB][MT];
@@ -236,7 +260,7 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(p[r][t][i], f.s[t], acc[r][t][i]);
+                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(p[r][t][i], f.s[t] * f.sw, acc[r][t][i]);
     };
     if (wave < whole) {
         const int last = wave + (whole - 1 - wave) / FD_WAVES * FD_WAVES;
@@ -261,9 +285,9 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
 #pragma unroll
             for (int t = 0; t < MT; ++t) f.x[t][h] = row_16<DWORDS>(xp[t], k + 64 * h, K);
         }
-        const float w = ws[whole];
+        f.sw = ws[whole];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) f.s[t] = xs[t][(int64_t)whole * a.M] * w;
+        for (int t = 0; t < MT; ++t) f.s[t] = xs[t][(int64_t)whole * a.M];
         multiply(f);
     }
     const bool vector = a.N % 4 == 0 && (uintptr_t)a.y % 16 == 0 && (uintptr_t)a.bias % 16 == 0;
@@ -309,10 +333,14 @@ static hipError_t launch_fp8_dec(const Fp8Args& a, hipStream_t s) {
 // row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 constexpr int FG_BK = 128;
 
+// s_waitcnt for n vector loads under way and no LDS reads.
+constexpr int wait_vm(int n) { return 0x0070 | (n & 15) | (n >> 4) << 14; }
+
 template <int ROWS, int MI, int FN>
 __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int tiles_n) {
     constexpr bool ALIGNED = ROWS == ROWS_16, DWORDS = ROWS == ROWS_1;
     constexpr int BM = 64 * MI, BN = 128 * FN, OB = BM * 8, UNITS = OB + BN * 8;
+    constexpr int XB = MI, WB = 2 * FN;        // load blocks of a wave and step
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
     __shared__ i32x4 st2[ALIGNED ? UNITS : 1];
@@ -386,43 +414,44 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
         }
         __builtin_amdgcn_sched_barrier(0);
     };
+    // a step's scales, loaded a step ahead (their product is formed where it is used)
     struct Scales {
-        float s[MI];
+        float x[MI], w;
     };
     auto scales = [&](int b) {
         Scales v;
-        const float w = ws[b];
+        v.w = ws[b];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) v.s[i] = xs[i][(int64_t)b * a.M] * w;
+        for (int i = 0; i < MI; ++i) v.x[i] = xs[i][(int64_t)b * a.M];
         return v;
     };
     // the scales of the sums that are being formed
     auto use = [&](const Scales& v) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) sc[i] = v.s[i];
+        for (int i = 0; i < MI; ++i) sc[i] = v.x[i] * v.w;
     };
-    // load block q (8 rows): wave w takes MI w .. MI w + MI - 1 of x_q and 2 FN w .. 2 FN w + 2 FN - 1 of W_q
+    // load block q (8 rows): wave w takes XB w .. of x_q and WB w .. of W_q
     auto block_row = [&](int q) { return 8 * q + (lane >> 3); };
     auto block_unit = [&](int q) { return (lane & 7) ^ ((block_row(q) >> 1) & 7); };
     if constexpr (ALIGNED) {
         const __amdgpu_buffer_rsrc_t rx = raw_buffer(x0, (uint32_t)rows_m * (uint32_t)K);
         const __amdgpu_buffer_rsrc_t rw = raw_buffer(w0, (uint32_t)rows_n * (uint32_t)K);
-        uint32_t xo[MI], wo[2 * FN];
+        uint32_t xo[XB], wo[WB];
 #pragma unroll
-        for (int q = 0; q < MI; ++q)
-            xo[q] = (uint32_t)min(block_row(MI * wave + q), rows_m - 1) * (uint32_t)K + 16u * block_unit(MI * wave + q);
+        for (int q = 0; q < XB; ++q)
+            xo[q] = (uint32_t)min(block_row(XB * wave + q), rows_m - 1) * (uint32_t)K + 16u * block_unit(XB * wave + q);
 #pragma unroll
-        for (int q = 0; q < 2 * FN; ++q)
-            wo[q] = (uint32_t)min(block_row(2 * FN * wave + q), rows_n - 1) * (uint32_t)K + 16u * block_unit(2 * FN * wave + q);
+        for (int q = 0; q < WB; ++q)
+            wo[q] = (uint32_t)min(block_row(WB * wave + q), rows_n - 1) * (uint32_t)K + 16u * block_unit(WB * wave + q);
         // a third of a step's loads
         auto fetch = [&](i32x4* st, int s, int third) {
             const uint32_t so = (uint32_t)s * FG_BK;
             if (third == 0) {
 #pragma unroll
-                for (int q = 0; q < MI; ++q) load_lds16(rx, xo[q], so, st + 64 * (MI * wave + q));
+                for (int q = 0; q < XB; ++q) load_lds16(rx, xo[q], so, st + 64 * (XB * wave + q));
             } else {
 #pragma unroll
-                for (int q = FN * (third - 1); q < FN * third; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (2 * FN * wave + q));
+                for (int q = WB / 2 * (third - 1); q < WB / 2 * third; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (WB * wave + q));
             }
         };
         // Step s in stage `cur`, its first operands in f0, its scales in sv.  Operands are read one part ahead of
@@ -441,7 +470,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
             multiply(f0, false);
             sv = sn;
             // step s + 1 has landed for every wave, and every wave holds the rest of step s in registers
-            __builtin_amdgcn_s_waitcnt(0x0070 | (MI + 2 * FN));                 // vmcnt(the loads of step s + 2) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(wait_vm(XB + WB));                 // vmcnt(the loads of step s + 2) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             f0 = read(nxt, 0);
@@ -456,7 +485,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
             for (int q = 0; q < 3; ++q) fetch(st1, min(1, last), q);
             fetch(st2, min(2, last), 0);
             __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(0x0070 | (2 * MI + 2 * FN));             // vmcnt(the loads after step 0's) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(wait_vm(2 * XB + WB));             // vmcnt(the loads after step 0's) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             Frag f = read(st0, 0);
@@ -471,28 +500,28 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
             __builtin_amdgcn_s_waitcnt(0x0070);                                 // nothing is in flight into the stages any more
         }
     } else {
-        const uint8_t *xp[MI], *wp[2 * FN];
+        const uint8_t *xp[XB], *wp[WB];
 #pragma unroll
-        for (int q = 0; q < MI; ++q) xp[q] = x0 + (int64_t)min(block_row(MI * wave + q), rows_m - 1) * K;
+        for (int q = 0; q < XB; ++q) xp[q] = x0 + (int64_t)min(block_row(XB * wave + q), rows_m - 1) * K;
 #pragma unroll
-        for (int q = 0; q < 2 * FN; ++q) wp[q] = w0 + (int64_t)min(block_row(2 * FN * wave + q), rows_n - 1) * K;
+        for (int q = 0; q < WB; ++q) wp[q] = w0 + (int64_t)min(block_row(WB * wave + q), rows_n - 1) * K;
         struct Regs {
-            u32x4 v[MI + 2 * FN];
+            u32x4 v[XB + WB];
         };
         auto load = [&](int s) {
             const int64_t k = (int64_t)s * FG_BK;
             Regs r;
 #pragma unroll
-            for (int q = 0; q < MI; ++q) r.v[q] = load_16<DWORDS>(xp[q] + k + 16 * block_unit(MI * wave + q));
+            for (int q = 0; q < XB; ++q) r.v[q] = load_16<DWORDS>(xp[q] + k + 16 * block_unit(XB * wave + q));
 #pragma unroll
-            for (int q = 0; q < 2 * FN; ++q) r.v[MI + q] = load_16<DWORDS>(wp[q] + k + 16 * block_unit(2 * FN * wave + q));
+            for (int q = 0; q < WB; ++q) r.v[XB + q] = load_16<DWORDS>(wp[q] + k + 16 * block_unit(WB * wave + q));
             return r;
         };
         auto put = [&](i32x4* st, const Regs& r) {
 #pragma unroll
-            for (int q = 0; q < MI; ++q) st[64 * (MI * wave + q) + lane] = (i32x4)r.v[q];
+            for (int q = 0; q < XB; ++q) st[64 * (XB * wave + q) + lane] = (i32x4)r.v[q];
 #pragma unroll
-            for (int q = 0; q < 2 * FN; ++q) st[OB + 64 * (2 * FN * wave + q) + lane] = (i32x4)r.v[MI + q];
+            for (int q = 0; q < WB; ++q) st[OB + 64 * (WB * wave + q) + lane] = (i32x4)r.v[XB + q];
         };
         auto multiply_stage = [&](const i32x4* st, int b) {
             const Scales sv = scales(b);
