@@ -434,11 +434,11 @@ int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_
     return hip_status(launch_forward_i8(a, stream));
 }
 
-// Sizes of the fp8 calls: element counts within 2^40, rows within a grid dimension.
+// Sizes of the fp8 calls.
 static int check_fp8(int64_t R, int64_t K) {
     if (R <= 0 || K <= 0) return BITLINEAR_ERR_INVALID_ARG;
     constexpr int64_t most = (int64_t)1 << 40;
-    return R > INT_MAX || K > FP8_MAX_K || R > most / K ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
+    return R > FP8_MAX_ROWS || K > FP8_MAX_K || R > most / K ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
 }
 
 int bitlinear_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* x_q, float* x_scale, hipStream_t stream) {
@@ -459,7 +459,7 @@ int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, i
     int st = check_fp8(M, K);
     if (!st) st = check_fp8(N, K);
     if (st) return st;
-    if (M > ((int64_t)1 << 40) / N) return BITLINEAR_ERR_SHAPE;
+    if (M > FP8_MAX_Y / N) return BITLINEAR_ERR_SHAPE;
     const Fp8Args a{x_q, x_scale, M, K, N, W_q, W_scale, bias, y};
     return hip_status(launch_forward_fp8(a, stream));
 }
@@ -472,7 +472,13 @@ static int check_grouped(int64_t T, int64_t K, const int64_t* rows, int64_t M, i
     int st = check_sizes(M > 0 ? M : 1, K, N);
     if (!st) st = check_sizes(T > 0 ? T : 1, K, N);
     if (st) return st;
-    return E > ((int64_t)1 << 42) / (N * K) ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
+    return E > ((int64_t)1 << 42) / (N * K) || !grouped_fits(M, N, E) ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
+}
+
+static int check_grouped_backward(int64_t T, int64_t K, const int64_t* rows, int64_t M, int64_t E, int64_t N) {
+    const int st = check_grouped(T, K, rows, M, E, N);
+    if (st) return st;
+    return grouped_backward_fits(M, K, N, E) ? BITLINEAR_OK : BITLINEAR_ERR_SHAPE;
 }
 
 int bitlinear_grouped_forward(const int8_t* x_q, const float* beta, int64_t T, int64_t K, const int64_t* rows, int64_t M,
@@ -508,7 +514,7 @@ int bitlinear_grouped_gated_forward(const float* x, int64_t T, int64_t K, const 
 
 // Workspace of a grouped backward call for valid sizes, else 0.
 static size_t grouped_backward_bytes(int64_t M, int64_t K, int64_t N, int64_t E, bool gated) {
-    return check_grouped(M, K, nullptr, M, E, N) == BITLINEAR_OK ? grouped_backward_workspace(M, K, N, E, gated) : 0;
+    return check_grouped_backward(M, K, nullptr, M, E, N) == BITLINEAR_OK ? grouped_backward_workspace(M, K, N, E, gated) : 0;
 }
 
 size_t bitlinear_grouped_backward_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E) {
@@ -520,7 +526,7 @@ size_t bitlinear_grouped_gated_backward_workspace_size(int64_t M, int64_t K, int
 }
 
 static int run_grouped_backward(const GroupedBackwardArgs& a, size_t workspace_bytes, bool gated, hipStream_t stream) {
-    const int st = check_grouped(a.T, a.K, a.rows, a.M, a.E, a.N);
+    const int st = check_grouped_backward(a.T, a.K, a.rows, a.M, a.E, a.N);
     if (st) return st;
     if (!a.ws || workspace_bytes < grouped_backward_workspace(a.M, a.K, a.N, a.E, gated)) return BITLINEAR_ERR_WORKSPACE;
     if (!aligned(a.ws, 256)) return BITLINEAR_ERR_ALIGNMENT;

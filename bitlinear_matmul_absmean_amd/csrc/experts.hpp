@@ -7,9 +7,11 @@
 
 namespace bitlinear {
 
-// Largest sizes of the grouped calls: a grid's dimensions and thread count (one workgroup for each 16 rows
-// and 16 columns at most, of 512 threads, below 2^32 threads).
-constexpr int64_t GROUPED_MAX_E = 65535, GROUPED_MAX_N = (int64_t)1 << 21, GROUPED_MAX_M = (int64_t)1 << 24;
+// Largest sizes of the grouped calls, and whether their launches hold them (a grid has fewer than 2^32 threads).
+constexpr int64_t GROUPED_MAX_E = 4096, GROUPED_MAX_N = (int64_t)1 << 20, GROUPED_MAX_M = (int64_t)1 << 24;
+inline bool grid_fits(int64_t workgroups, int64_t threads) { return workgroups <= 0xFFFFFFFFll / threads; }
+bool grouped_fits(int64_t M, int64_t N, int64_t E);
+bool grouped_backward_fits(int64_t M, int64_t K, int64_t N, int64_t E);
 
 // Group e as rows [lo, hi): offsets outside 0 .. M are taken as 0 or M.
 struct Group {
@@ -73,8 +75,9 @@ struct Fp8Args {
     const float* bias;             // [N] or null
     float* y;                      // [M, N]
 };
-// 256 rows of x_q or W_q within 32-bit offsets.
-constexpr int64_t FP8_MAX_K = (int64_t)1 << 23;
+// Largest K (256 rows of x_q or W_q within 32-bit offsets, blocks of 128 within a grid's second dimension),
+// and M, N and M N (grids of fewer than 2^32 threads).
+constexpr int64_t FP8_MAX_K = (int64_t)1 << 22, FP8_MAX_ROWS = (int64_t)1 << 26, FP8_MAX_Y = (int64_t)1 << 36;
 hipError_t launch_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* xq, float* xs, hipStream_t s);
 hipError_t launch_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t* wq, float* ws, hipStream_t s);
 hipError_t launch_forward_fp8(const Fp8Args& a, hipStream_t s);

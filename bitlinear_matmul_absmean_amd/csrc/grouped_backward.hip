@@ -13,6 +13,11 @@ size_t grouped_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t E, bo
     return 256 + (gated ? (size_t)M * N * 8 : 0);
 }
 
+bool grouped_backward_fits(int64_t M, int64_t K, int64_t N, int64_t E) {
+    // dW: tiles of 128 x 128 at least, of 512 threads, two projections
+    return grid_fits(E * ((N + 127) / 128) * ((K + 127) / 128) * 2, 512) && grid_fits((M / 64 + E) * ((K + 127) / 128), 512);
+}
+
 // dg and du, one element a thread.
 template <int ACT>
 __global__ __launch_bounds__(256) void k_gate_gradients(const float* __restrict__ dh, const float* __restrict__ g,

@@ -458,7 +458,7 @@ int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_
  *                          together, as a tile of tokens reads them.
  *   quantize_weights_fp8:  blocks of 128 x 128; W [N, K] fp32 (in); W_q [N, K] e4m3,
  *                          W_scale [ceil(N / 128), ceil(K / 128)] fp32 (out).
- * 1 <= K <= 8388608, any alignment of fp32 elements.  Errors: INVALID_ARG, SHAPE, HIP.
+ * 1 <= K <= 4194304, M and N <= 67108864; any alignment of fp32 elements.  Errors: INVALID_ARG, SHAPE, HIP.
  */
 int bitlinear_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* x_q, float* x_scale,
                                hipStream_t stream);
@@ -473,7 +473,7 @@ int bitlinear_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t
  *   x_q [M, K], x_scale [ceil(K / 128), M]; W_q [N, K], W_scale [ceil(N / 128), ceil(K / 128)], as the
  *   quantizers lay them out; bias [N] or NULL.                               (in)
  *   y [M, N] fp32.                                                           (out)
- * 1 <= K <= 8388608, any alignment.  Errors: INVALID_ARG, SHAPE, HIP.
+ * 1 <= K <= 4194304, M and N <= 67108864, M N <= 2^36; any alignment.  Errors: INVALID_ARG, SHAPE, HIP.
  */
 int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, int64_t K, const uint8_t* W_q,
                           const float* W_scale, int64_t N, const float* bias, float* y, hipStream_t stream);
@@ -492,7 +492,8 @@ int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, i
  *             0 or M, and a group that ends before it begins as empty.       (in)
  *   W_packed  [E, N, K/4] uint8; alpha [E]; bias [E, N] or NULL.              (in)
  *   y         [M, N] fp32.                                                   (out)
- * K % 4 == 0, E <= 65535; any alignment of elements of their type.  M == 0 is a call without rows, for
+ * K % 4 == 0, E <= 4096, N <= 2^20, M <= 2^24, and no more work than a launch holds (about 2^36 elements of y);
+ * any alignment of elements of their type.  M == 0 is a call without rows, for
  * which x_q, beta, rows and y may be NULL.
  * Outputs must not overlap inputs.  The host reads no device memory: the call can be captured into a graph
  * and replayed with other offsets and rows.
