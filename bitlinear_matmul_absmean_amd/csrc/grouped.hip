@@ -19,48 +19,6 @@
 
 namespace bitlinear {
 
-// Slot `at` of `tile` rows, the slots of a group following those of the groups before it: its expert, first
-// row and number of rows (0: there is no such slot).  Each lane takes one of 64 experts at a time; `total`
-// receives the number of all slots if asked for.
-struct Slot {
-    int e, rows;
-    int64_t m0;
-};
-template <int TILE, bool TOTAL>
-__device__ __forceinline__ Slot find_slot(const int64_t* __restrict__ offsets, int E, int64_t M, int at, int* total) {
-    const int lane = threadIdx.x & 63;
-    Slot s{0, 0, 0};
-    int before = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        int lo = 0, n = 0;
-        if (e0 + lane < E) {
-            const Group g = group_rows(offsets, e0 + lane, M);
-            lo = (int)g.lo;
-            n = g.hi > g.lo ? (int)(g.hi - g.lo) : 0;
-        }
-        const int mine = (n + TILE - 1) / TILE;
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(upto, d, 64);
-            upto += lane >= d ? v : 0;
-        }
-        const int all = __builtin_amdgcn_readlane(upto, 63);
-        if (at >= before && at < before + all) {
-            const int l = __builtin_ctzll(__ballot(before + upto > at));
-            const int tile = at - before - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l));
-            const int left = __builtin_amdgcn_readlane(n, l) - tile * TILE;
-            s = Slot{e0 + l, left < TILE ? left : TILE, __builtin_amdgcn_readlane(lo, l) + (int64_t)tile * TILE};
-            if (!TOTAL) break;
-        }
-        before += all;
-    }
-    if (TOTAL) *total = before;
-    return s;
-}
-
-// Most slots of `tile` rows that M rows of E experts can make.
-static int64_t most_slots(int64_t M, int64_t E, int64_t tile) { return M / tile + (E < M ? E : M); }
 static int64_t most_slots(const GroupedArgs& a, int64_t tile) { return most_slots(a.M, a.E, tile); }
 
 // The GEMM's smallest tiles, 32 rows x 128 columns of 256 threads (the streaming kernel is taken where its fit).
