@@ -42,19 +42,20 @@ struct Products {
 };
 
 // ---- the two products -----------------------------------------------------------------------
-// A workgroup of eight waves computes 64 MI x 256 of dx (rows x k) or of a dW (n x k), a wave 32 MI x 64, in
-// steps of 64 of the sum.  A stage in LDS is three planes of the split factor, 64 MI rows of 64 bf16 values,
-// and 256 rows (one for each k) of the other; both are loaded from memory into registers while the stage
-// before is multiplied, split or widened there, turned where the sum runs down the rows, and written in 16-byte
-// units: unit u (8 of the sum) of row r at slot u ^ ((r / 2) % 8), which spreads reads and writes over all banks.
-// Row of k: column 2 l + j of the wave's 64 lies in row 32 j + l, so that a lane ends with pairs of columns.
+// A workgroup of eight waves computes BM x 256 of dx (rows x k) or of a dW (n x k), a wave 32 rows x 32 NJ columns,
+// in steps of 64 of the sum.  A stage in LDS is three planes of the split factor, BM rows of 64 bf16 values, and
+// 256 rows (one for each k) of the other; both are loaded from memory into registers two steps ahead, split or
+// widened there, turned where the sum runs down the rows, and written in 16-byte units while the stage before
+// is multiplied: unit u (8 of the sum) of row r at slot u ^ ((r / 2) % 8), which spreads reads and writes over all
+// banks.  Row of k: column NJ l + j of a wave's columns lies in row 32 j + l of theirs, so that a lane ends with
+// NJ neighbouring columns.
 // 32x32x16 lane layout: A/B lane l holds row/column l % 32, 8 (l / 32) + j of the sum; accumulator r of lane l is
 // row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 constexpr int GB_BN = 256;
 
-template <int MI>
+template <int BM>
 struct Grad {
-    static constexpr int BM = 64 * MI, OB = 3 * BM * 8, UNITS = OB + GB_BN * 8;
+    static constexpr int WM = BM / 32, NJ = WM, OB = 3 * BM * 8, UNITS = OB + GB_BN * 8;   // 8 / WM waves along k
 };
 
 // Eight floats as a unit of each of the three planes: truncation leaves exact remainders.
@@ -76,113 +77,146 @@ __device__ __forceinline__ void split_unit(const float (&v)[8], u32x4 (&pl)[3]) 
     }
 }
 
-// The product of stages, two at a time: `load(s)` puts step s into registers, `put(st)` writes them to a stage.
-template <int MI, typename Load, typename Put>
-__device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, f32x16 (&acc)[MI][2], Load load, Put put) {
-    constexpr int BM = Grad<MI>::BM, OB = Grad<MI>::OB;
+// The sum over `steps` steps: load(r, s) starts step s on its way into registers r, put(r, st, part) writes a
+// quarter of them to a stage.  Step s is multiplied while step s + 1 goes from registers to the other stage and
+// step s + 2 is on its way from memory; past the last step the last one is repeated, and not read.
+template <int BM, typename Regs, typename Load, typename Put>
+__device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, f32x16 (&acc)[Grad<BM>::NJ], Load load, Put put) {
+    constexpr int WM = Grad<BM>::WM, NJ = Grad<BM>::NJ, OB = Grad<BM>::OB;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wi = wave & 1, wj = wave >> 1, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
-    auto multiply = [&](const u32x4* st) {
+    const int wi = wave % WM, wj = wave / WM, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
+    struct Frag {
+        bf16x8 a[3], b[NJ];
+    };
+    auto read = [&](const u32x4* st, int ks) {
+        const int at = (2 * ks + lg) ^ sw;
+        Frag f;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const int at = (2 * ks + lg) ^ sw;
-            bf16x8 b[2];
+        for (int q = 2; q >= 0; --q) f.a[q] = __builtin_bit_cast(bf16x8, st[(q * BM + 32 * wi + lr) * 8 + at]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) b[j] = __builtin_bit_cast(bf16x8, st[OB + (64 * wj + 32 * j + lr) * 8 + at]);
+        for (int j = 0; j < NJ; ++j) f.b[j] = __builtin_bit_cast(bf16x8, st[OB + (32 * NJ * wj + 32 * j + lr) * 8 + at]);
+        return f;
+    };
+    auto multiply = [&](const Frag& f) {
 #pragma unroll
-            for (int q = 2; q >= 0; --q)
+        for (int q = 2; q >= 0; --q)
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    const bf16x8 f = __builtin_bit_cast(bf16x8, st[(q * BM + 32 * MI * wi + 32 * i + lr) * 8 + at]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, b[j], acc[i][j], 0, 0, 0);
-                }
-        }
+            for (int j = 0; j < NJ; ++j) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[q], f.b[j], acc[j], 0, 0, 0);
     };
     if (steps == 0) return;
-    load(0);
-    put(st0);
-    if (steps > 1) load(1);
+    const int last = steps - 1;
+    // step s in `cur`, step s + 1 in registers r
+    auto step = [&](const u32x4* cur, u32x4* nxt, const Regs& r) {
+        Frag f = read(cur, 0);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            Frag g;
+            if (ks < 3) g = read(cur, ks + 1);
+            put(r, nxt, ks);
+            multiply(f);
+            // reads first, then a product and what VALU work of the quarter falls to it, in turn
+            __builtin_amdgcn_sched_group_barrier(0x100, 3 + NJ, 0);
+#pragma unroll
+            for (int i = 0; i < 3 * NJ; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x200, 3, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            f = g;
+        }
+        lds_barrier();
+    };
+    Regs r0, r1;
+    load(r0, 0);
+    load(r1, min(1, last));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) put(r0, st0, q);
     lds_barrier();
     for (int s = 0; s < steps; s += 2) {
-        if (s + 1 < steps) put(st1);                   // its last readers are past the barrier before
-        if (s + 2 < steps) load(s + 2);
-        multiply(st0);
-        lds_barrier();
+        load(r0, min(s + 2, last));
+        step(st0, st1, r1);
         if (s + 1 >= steps) break;
-        if (s + 2 < steps) put(st0);
-        if (s + 3 < steps) load(s + 3);
-        multiply(st1);
-        lds_barrier();
+        load(r1, min(s + 3, last));
+        step(st1, st0, r0);
     }
 }
 
-// rows x columns of `out` (row length K) from a wave's accumulators.
-template <int MI>
-__device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, int rows, int64_t k0, const f32x16 (&acc)[MI][2]) {
+// `rows` rows of a tile of `out` (row length K, columns from k0) from a wave's accumulators.
+template <int BM>
+__device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, int rows, int64_t k0, const f32x16 (&acc)[Grad<BM>::NJ]) {
+    constexpr int WM = Grad<BM>::WM, NJ = Grad<BM>::NJ;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t k = k0 + 64 * (wave >> 1) + 2 * (lane & 31);
-    if (k >= K) return;                                // K is even
+    const int64_t k = k0 + 32 * NJ * (wave / WM) + NJ * (lane & 31);
+    if (k >= K) return;                                // K is a multiple of 4
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int r = 0; r < 16; ++r) {
+        const int m = 32 * (wave % WM) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        float v[NJ];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int m = 32 * MI * (wave & 1) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-            const float2 v = make_float2(acc[i][0][r], acc[i][1][r]);
-            if (m < rows) __builtin_memcpy(out + (int64_t)m * K + k, &v, 8);
-        }
+        for (int j = 0; j < NJ; ++j) v[j] = acc[j][r];
+        if (m < rows) __builtin_memcpy(out + (int64_t)m * K + k, v, 4 * NJ);
+    }
 }
 
 // LDS row of k 4 c + j of the tile (c a lane, j < 4).
-__device__ __forceinline__ int grad_row(int c, int j) { return 64 * (c >> 4) + 32 * (j & 1) + 2 * (c & 15) + (j >> 1); }
+template <int BM>
+__device__ __forceinline__ int grad_row(int c, int j) {
+    if constexpr (Grad<BM>::NJ == 4) return 128 * (c >> 5) + 32 * j + (c & 31);
+    else return 64 * (c >> 4) + 32 * (j & 1) + 2 * (c & 15) + (j >> 1);
+}
 
-template <int MI>
+template <int BM>
 __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st1, const Slot& slot, int64_t k0) {
-    constexpr int BM = Grad<MI>::BM, OB = Grad<MI>::OB;
+    constexpr int OB = Grad<BM>::OB, UN = BM / 64;     // units of a plane that a thread forms
     const GroupedBackwardArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t N = a.N, rowb = a.K >> 2, e = slot.e;
     const int per = (int)((N + 63) / 64), steps = per * (a.w1 ? 2 : 1);
-    // of d: row tid / (8 / MI), MI units of 8; of W: rows 8 wave .., the lane's byte of 4 codes
-    const int row = tid / (8 / MI), unit = (tid % (8 / MI)) * MI;
-    const int64_t at = (slot.m0 + min(row, slot.rows - 1)) * N;
-    const int64_t byte = min((k0 >> 2) + lane, rowb - 1);
-    float v[MI][8], alpha;
-    uint32_t w[8];
-    auto load = [&](int s) {
+    // of d: row tid / (8 / UN), UN units of 8; of W: rows 8 wave .., the lane's byte of 4 codes
+    const int row = tid / (8 / UN), unit = (tid % (8 / UN)) * UN;
+    const int64_t at = (slot.m0 + min(row, slot.rows - 1)) * N + 8 * unit;
+    const uint32_t byte = (uint32_t)min((k0 >> 2) + lane, rowb - 1);
+    struct Regs {
+        float v[UN][8], alpha;
+        uint32_t w[8];
+    };
+    auto load = [&](Regs& r, int s) {
         const bool second = s >= per;
-        const int64_t n0 = (int64_t)(second ? s - per : s) * 64, n = n0 + 8 * unit;
-        const float* d = (second ? p.d1 : p.d0) + at;
-        const uint8_t* ww = (second ? a.w1 : a.w0) + e * N * rowb + byte;
-        alpha = (second ? a.al1 : a.al0)[e];
+        const int64_t n0 = (int64_t)(second ? s - per : s) * 64;
+        const float* d = (second ? p.d1 : p.d0) + at + n0;
+        const uint8_t* w = (second ? a.w1 : a.w0) + (e * N + n0 + 8 * wave) * rowb;
+        r.alpha = (second ? a.al1 : a.al0)[e];
         if (n0 + 64 <= N) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i) __builtin_memcpy(v[i], d + n + 8 * i, 32);
+            for (int i = 0; i < UN; ++i) __builtin_memcpy(r.v[i], d + 8 * i, 32);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = ww[(n0 + 8 * wave + i) * rowb];
+            for (int i = 0; i < 8; ++i) r.w[i] = (w + i * rowb)[byte];
         } else {
+            const int left = (int)(N - n0);
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
+            for (int i = 0; i < UN; ++i)
 #pragma unroll
-                for (int x = 0; x < 8; ++x) v[i][x] = n + 8 * i + x < N ? d[n + 8 * i + x] : 0.0f;
+                for (int x = 0; x < 8; ++x) r.v[i][x] = 8 * (unit + i) + x < left ? d[8 * i + x] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = ww[min(n0 + 8 * wave + i, N - 1) * rowb];
+            for (int i = 0; i < 8; ++i) r.w[i] = (w + (min(8 * wave + i, left - 1) - 8 * wave) * rowb)[byte];
         }
     };
-    auto put = [&](u32x4* st) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
+    auto put = [&](const Regs& r, u32x4* st, int part) {
+        if (part < UN) {
+            float t[8];
             u32x4 pl[3];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[i][x] *= alpha;
-            split_unit(v[i], pl);
+            for (int x = 0; x < 8; ++x) t[x] = r.v[part][x] * r.alpha;
+            split_unit(t, pl);
 #pragma unroll
-            for (int q = 0; q < 3; ++q) st[(q * BM + row) * 8 + ((unit + i) ^ ((row >> 1) & 7))] = pl[q];
+            for (int q = 0; q < 3; ++q) st[(q * BM + row) * 8 + ((unit + part) ^ ((row >> 1) & 7))] = pl[q];
         }
+        if (part < 2) return;
         // codes of four n a dword; for each k their bf16 values from tables of the upper and lower bytes
-        const uint32_t c0 = w[0] | w[1] << 8 | w[2] << 16 | w[3] << 24, c1 = w[4] | w[5] << 8 | w[6] << 16 | w[7] << 24;
+        const uint32_t c0 = r.w[0] | r.w[1] << 8 | r.w[2] << 16 | r.w[3] << 24, c1 = r.w[4] | r.w[5] << 8 | r.w[6] << 16 | r.w[7] << 24;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 2 * part - 4; j < 2 * part - 2; ++j) {
             u32x4 o;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -191,120 +225,115 @@ __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st
                 o[2 * h] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
                 o[2 * h + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
             }
-            const int r = grad_row(lane, j);
-            st[OB + r * 8 + (wave ^ ((r >> 1) & 7))] = o;
+            const int k = grad_row<BM>(lane, j);
+            st[OB + k * 8 + (wave ^ ((k >> 1) & 7))] = o;
         }
     };
-    f32x16 acc[MI][2];
+    f32x16 acc[Grad<BM>::NJ];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) acc[i][0] = acc[i][1] = f32x16{};
-    grad_sum<MI>(st0, st1, steps, acc, load, put);
-    grad_store<MI>(a.dx + slot.m0 * a.K, a.K, slot.rows, k0, acc);
+    for (int j = 0; j < Grad<BM>::NJ; ++j) acc[j] = f32x16{};
+    grad_sum<BM, Regs>(st0, st1, steps, acc, load, put);
+    grad_store<BM>(a.dx + slot.m0 * a.K, a.K, slot.rows, k0, acc);
 }
 
-template <int MI>
+template <int BM>
 __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st1, int64_t e, bool second, int64_t n0, int64_t k0) {
-    constexpr int BM = Grad<MI>::BM, OB = Grad<MI>::OB;
+    constexpr int OB = Grad<BM>::OB, UN = BM / 64;     // columns of d of a lane
     const GroupedBackwardArgs& a = p.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t N = a.N, K = a.K;
     const Group g = group_rows(a.offsets, e, a.M);
-    const int steps = g.hi > g.lo ? (int)((g.hi - g.lo + 63) / 64) : 0;
-    const float* d = second ? p.d1 : p.d0;
-    // the wave takes rows 8 wave .. of a step, a lane MI columns of d and four of x_q
-    const int64_t n = n0 + MI * lane, k = min(k0 + 4 * lane, K - 4);
-    const bool whole = n0 + BM <= N;
-    int64_t cols[MI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i) cols[i] = min(n + i, N - 1);
-    // token of row lane % 8 of the wave's rows of a step: of the last row past the end
-    auto row_of = [&](int s, int i) { return min(g.lo + (int64_t)s * 64 + 8 * wave + i, g.hi - 1); };
-    auto tokens = [&](int s) { return (int)row_token(a.rows, row_of(s, lane & 7), a.T); };
-    float v[8][MI], beta;
-    uint32_t x[8];
-    bool there;
-    int token = steps ? tokens(0) : 0;
-    auto load = [&](int s) {
-        beta = token >= 0 ? a.beta[token] : 0.0f;
-        there = g.lo + (int64_t)s * 64 + 8 * wave + (lane & 7) < g.hi;
+    const int rows = g.hi > g.lo ? (int)(g.hi - g.lo) : 0, steps = (rows + 63) / 64;
+    const float* d = (second ? p.d1 : p.d0) + (g.lo + 8 * wave) * N + n0;
+    const uint32_t width = (uint32_t)(N - n0) * 4;
+    // the wave takes rows 8 wave .. of a step, a lane columns lane and lane + 64 of d and four of x_q
+    const uint32_t k = (uint32_t)min(k0 + 4 * lane, K - 4);
+    // tokens of rows lane % 8 of the wave's rows of a step (of the last row past the end)
+    auto tokens = [&](int s) {
+        const int64_t m = g.lo + min(64 * s + 8 * wave + (lane & 7), rows - 1);
+        return a.rows ? a.rows[m] : m;
+    };
+    struct Regs {
+        float v[UN][8], beta;
+        uint32_t x[8];
+        bool live;                                     // the row lies in the group, its token is there
+    };
+    int64_t next = steps ? tokens(0) : 0;              // tokens of the step that is loaded next
+    auto load = [&](Regs& r, int s) {
+        const bool there = next >= 0 && next < a.T;
+        const uint64_t token = there ? (uint64_t)next : 0, off = token * (uint64_t)K;
+        r.beta = a.beta[token];
+        r.live = there && 64 * s + 8 * wave + (lane & 7) < rows;
+        const float* ds = d + (int64_t)s * 64 * N;
+        const int left = rows - 64 * s - 8 * wave;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float* dr = d + row_of(s, i) * N;
-            if (MI == 2 && whole) {
-                __builtin_memcpy(v[i], dr + n, 4 * MI);
-            } else {
+            // a buffer for what is left of each row: columns past it, and rows past the group's end, read zeros
+            const __amdgpu_buffer_rsrc_t rd = raw_buffer(ds + i * N, i < left ? width : 0);
 #pragma unroll
-                for (int c = 0; c < MI; ++c) v[i][c] = dr[cols[c]];
-            }
-            const int t = __builtin_amdgcn_readlane(token, i);
-            __builtin_memcpy(&x[i], a.xq + (int64_t)(t < 0 ? 0 : t) * K + k, 4);
+            for (int c = 0; c < UN; ++c)
+                r.v[c][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, 4u * lane + 256u * c, 0, 0));
+            const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((uint32_t)(off >> 32), i) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((uint32_t)off, i);
+            __builtin_memcpy(&r.x[i], a.xq + o + k, 4);
         }
-        token = tokens(s + 1);
+        next = tokens(min(s + 1, steps - 1));
     };
-    auto put = [&](u32x4* st) {
-        // beta / 127 of the rows; 0 for rows past the end and tokens that are not there
-        const float f = there ? beta / 127.0f : 0.0f;
-        float fi[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fi[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-#pragma unroll
-        for (int c = 0; c < MI; ++c) {
+    auto put = [&](const Regs& r, u32x4* st, int part) {
+        if (part < UN) {
+            const float f = r.live ? r.beta / 127.0f : 0.0f;
             float t[8];
             u32x4 pl[3];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = v[i][c] * fi[i];
+            for (int i = 0; i < 8; ++i) t[i] = r.v[part][i] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
             split_unit(t, pl);
-            const int r = MI * lane + c;
+            const int c = lane + 64 * part;
 #pragma unroll
-            for (int q = 0; q < 3; ++q) st[(q * BM + r) * 8 + (wave ^ ((r >> 1) & 7))] = pl[q];
+            for (int q = 0; q < 3; ++q) st[(q * BM + c) * 8 + (wave ^ ((c >> 1) & 7))] = pl[q];
         }
+        if (part < 2) return;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 2 * part - 4; j < 2 * part - 2; ++j) {
             u32x4 o;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                const float lo = (float)(int8_t)(x[i] >> (8 * j)), hi = (float)(int8_t)(x[i + 1] >> (8 * j));
+                const float lo = (float)(int8_t)(r.x[i] >> (8 * j)), hi = (float)(int8_t)(r.x[i + 1] >> (8 * j));
                 o[i >> 1] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
             }
-            const int r = grad_row(lane, j);
-            st[OB + r * 8 + (wave ^ ((r >> 1) & 7))] = o;
+            const int c = grad_row<BM>(lane, j);
+            st[OB + c * 8 + (wave ^ ((c >> 1) & 7))] = o;
         }
     };
-    f32x16 acc[MI][2];
+    f32x16 acc[Grad<BM>::NJ];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) acc[i][0] = acc[i][1] = f32x16{};
-    grad_sum<MI>(st0, st1, steps, acc, load, put);
-    const int rows = (int)(N - n0 < BM ? N - n0 : BM);
-    grad_store<MI>((second ? a.dw1 : a.dw0) + (e * N + n0) * K, K, rows, k0, acc);
+    for (int j = 0; j < Grad<BM>::NJ; ++j) acc[j] = f32x16{};
+    grad_sum<BM, Regs>(st0, st1, steps, acc, load, put);
+    grad_store<BM>((second ? a.dw1 : a.dw0) + (e * N + n0) * K, K, (int)(N - n0 < BM ? N - n0 : BM), k0, acc);
 }
 
-// dx's tiles first (`slots` x tiles_k of them at most), whose sums are the longer ones, then dW's, so that the
-// short ones fill the card where dx's end.  Of each kind a contiguous run for every XCD.
-template <int MI>
+// dx's tiles first (`dx_wgs` at most), whose sums are the longer ones, then dW's, so that the short ones fill the
+// card where dx's end.  Each XCD gets a contiguous run of dx's tiles and of every expert's tiles of dW (whose work
+// goes with the expert's rows).
+template <int BM>
 __global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx_wgs, int tiles_k, int tiles_n) {
-    __shared__ u32x4 st0[Grad<MI>::UNITS];
-    __shared__ u32x4 st1[Grad<MI>::UNITS];
+    __shared__ u32x4 st0[Grad<BM>::UNITS];
+    __shared__ u32x4 st1[Grad<BM>::UNITS];
     const GroupedBackwardArgs& a = p.a;
     auto run_of = [](int b, int T) { return (b & 7) * (T >> 3) + ((b & 7) < (T & 7) ? b & 7 : T & 7) + (b >> 3); };
     if ((int)blockIdx.x < dx_wgs) {
         int tiles_m;
-        find_slot<Grad<MI>::BM, true>(a.offsets, (int)a.E, a.M, -1, &tiles_m);
+        find_slot<BM, true>(a.offsets, (int)a.E, a.M, -1, &tiles_m);
         const int T = tiles_m * tiles_k;
         if ((int)blockIdx.x >= T) return;
         int t = run_of(blockIdx.x, T);
         const int grp = t / (4 * tiles_k), gm = tiles_m - 4 * grp < 4 ? tiles_m - 4 * grp : 4;
         t -= grp * 4 * tiles_k;
-        dx_tile<MI>(p, st0, st1, find_slot<Grad<MI>::BM, false>(a.offsets, (int)a.E, a.M, 4 * grp + t % gm, nullptr),
-                    (int64_t)(t / gm) * GB_BN);
+        dx_tile<BM>(p, st0, st1, find_slot<BM, false>(a.offsets, (int)a.E, a.M, 4 * grp + t % gm, nullptr), (int64_t)(t / gm) * GB_BN);
     } else {
-        const int two = a.w1 ? 2 : 1, T = (int)a.E * two * tiles_n * tiles_k, b = blockIdx.x - dx_wgs;
-        if (b >= T) return;
-        int t = run_of(b, T);
-        const int tk = t % tiles_k;
-        t /= tiles_k;
-        const int tn = t % tiles_n;
-        t /= tiles_n;
-        dw_tile<MI>(p, st0, st1, t / two, t % two != 0, (int64_t)tn * Grad<MI>::BM, (int64_t)tk * GB_BN);
+        const int T = (a.w1 ? 2 : 1) * tiles_n * tiles_k, T8 = (T + 7) & ~7, b = blockIdx.x - dx_wgs;
+        if (b % T8 >= T) return;
+        const int t = run_of(b % T8, T), tn = t / tiles_k % tiles_n;
+        dw_tile<BM>(p, st0, st1, b / T8, t >= tiles_n * tiles_k, (int64_t)tn * BM, (int64_t)(t % tiles_k) * GB_BN);
     }
 }
 
@@ -335,26 +364,26 @@ __global__ __launch_bounds__(1024) void k_grouped_dbias(Products p) {
 struct GradGrid {
     int64_t dx, dw, tiles_k, tiles_n;
 };
-template <int MI>
+template <int BM>
 static GradGrid grad_grid(int64_t M, int64_t K, int64_t N, int64_t E, bool dx, int projections) {
     GradGrid g;
     g.tiles_k = (K + GB_BN - 1) / GB_BN;
-    g.tiles_n = (N + Grad<MI>::BM - 1) / Grad<MI>::BM;
-    g.dx = dx && M > 0 ? (most_slots(M, E, Grad<MI>::BM) * g.tiles_k + 7) / 8 * 8 : 0;
-    g.dw = E * projections * g.tiles_n * g.tiles_k;
+    g.tiles_n = (N + BM - 1) / BM;
+    g.dx = dx && M > 0 ? (most_slots(M, E, BM) * g.tiles_k + 7) / 8 * 8 : 0;
+    g.dw = E * ((projections * g.tiles_n * g.tiles_k + 7) / 8 * 8);
     return g;
 }
 
-template <int MI>
+template <int BM>
 static hipError_t launch_gradients(const Products& p, hipStream_t s) {
     const GroupedBackwardArgs& a = p.a;
-    const GradGrid g = grad_grid<MI>(a.M, a.K, a.N, a.E, a.dx, a.dw0 ? (a.w1 ? 2 : 1) : 0);
+    const GradGrid g = grad_grid<BM>(a.M, a.K, a.N, a.E, a.dx, a.dw0 ? (a.w1 ? 2 : 1) : 0);
     if (g.dx + g.dw == 0) return hipSuccess;
-    return launch_with_lds(k_grouped_gradients<MI>, dim3((unsigned)(g.dx + g.dw)), dim3(512), 0, s, p, (int)g.dx, (int)g.tiles_k, (int)g.tiles_n);
+    return launch_with_lds(k_grouped_gradients<BM>, dim3((unsigned)(g.dx + g.dw)), dim3(512), 0, s, p, (int)g.dx, (int)g.tiles_k, (int)g.tiles_n);
 }
 
 bool grouped_backward_fits(int64_t M, int64_t K, int64_t N, int64_t E) {
-    const GradGrid g = grad_grid<1>(M, K, N, E, true, 2);
+    const GradGrid g = grad_grid<64>(M, K, N, E, true, 2);
     return grid_fits(g.dx + g.dw, 512);
 }
 
@@ -373,7 +402,7 @@ hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) 
         p.d0 = dg;
         p.d1 = du;
     }
-    const hipError_t e = launch_gradients<2>(p, s);
+    const hipError_t e = launch_gradients<128>(p, s);
     if (e != hipSuccess) return e;
     if (a.db0 || a.db1) {
         hipLaunchKernelGGL(k_grouped_dbias, dim3((unsigned)((a.N + 63) / 64), (unsigned)a.E, a.w1 ? 2u : 1u), dim3(1024), 0, s, p);
