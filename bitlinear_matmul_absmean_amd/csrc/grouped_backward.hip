@@ -42,203 +42,221 @@ struct Products {
 };
 
 // ---- the two products -----------------------------------------------------------------------
-// A workgroup of eight waves computes BM x 256 of dx (rows x k) or of a dW (n x k), a wave 32 rows x 32 NJ columns,
-// in steps of 64 of the sum.  A stage in LDS is three planes of the split factor, BM rows of 64 bf16 values, and
+// A workgroup of eight waves computes 128 x 256 of dx (rows x k) or of a dW (n x k), a wave 32 rows x 128 columns,
+// in steps of 64 of the sum.  A stage in LDS is three planes of the split factor, 128 rows of 64 bf16 values, and
 // 256 rows (one for each k) of the other; both are loaded from memory into registers two steps ahead, split or
 // widened there, turned where the sum runs down the rows, and written in 16-byte units while the stage before
 // is multiplied: unit u (8 of the sum) of row r at slot u ^ ((r / 2) % 8), which spreads reads and writes over all
-// banks.  Row of k: column NJ l + j of a wave's columns lies in row 32 j + l of theirs, so that a lane ends with
-// NJ neighbouring columns.
+// banks.  Row of k: column 4 l + j of a wave's columns lies in row 32 j + l of theirs, so that a lane ends with
+// four neighbouring columns.
 // 32x32x16 lane layout: A/B lane l holds row/column l % 32, 8 (l / 32) + j of the sum; accumulator r of lane l is
 // row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
-constexpr int GB_BN = 256;
+constexpr int GB_BM = 128, GB_BN = 256, GB_NJ = 4, GB_OB = 3 * GB_BM * 8, GB_UNITS = GB_OB + GB_BN * 8;
 
-template <int BM>
-struct Grad {
-    static constexpr int WM = BM / 32, NJ = WM, OB = 3 * BM * 8, UNITS = OB + GB_BN * 8;   // 8 / WM waves along k
-};
+// Loads at base + off: the base (the same for the whole wave) in scalar registers, a lane's 32-bit offset in one
+// vector register.  Any alignment of the type's elements.
+typedef const __attribute__((address_space(1))) char* global_bytes;
+__device__ __forceinline__ global_bytes scalar_base(const void* p) {
+    uint64_t b = (uint64_t)p;
+    asm("" : "+s"(b));                                 // keeps the sum with the lane's offset out of vector registers
+    return (global_bytes)b;
+}
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32u __attribute__((aligned(1)));
 
-// Eight floats as a unit of each of the three planes: truncation leaves exact remainders.
-__device__ __forceinline__ void split_unit(const float (&v)[8], u32x4 (&pl)[3]) {
+// Two floats as a dword of each of the three planes: truncation leaves exact remainders.
+__device__ __forceinline__ void split_2(float v0, float v1, int at, u32x4 (&pl)[3]) {
+    const float v[2] = {v0, v1};
+    uint32_t b[2][3];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        uint32_t b[2][3];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t h = __float_as_uint(v[i + e]) & 0xFFFF0000u;
-            const float r = v[i + e] - __uint_as_float(h);
-            const uint32_t m = __float_as_uint(r) & 0xFFFF0000u;
-            b[e][0] = h;
-            b[e][1] = m;
-            b[e][2] = __float_as_uint(r - __uint_as_float(m));
-        }
-#pragma unroll
-        for (int q = 0; q < 3; ++q) pl[q][i >> 1] = __builtin_amdgcn_perm(b[1][q], b[0][q], 0x07060302u);
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t h = __float_as_uint(v[e]) & 0xFFFF0000u;
+        const float r = v[e] - __uint_as_float(h);
+        const uint32_t m = __float_as_uint(r) & 0xFFFF0000u;
+        b[e][0] = h;
+        b[e][1] = m;
+        b[e][2] = __float_as_uint(r - __uint_as_float(m));
     }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) pl[q][at] = __builtin_amdgcn_perm(b[1][q], b[0][q], 0x07060302u);
 }
 
-// The sum over `steps` steps: load(r, s) starts step s on its way into registers r, put(r, st, part) writes a
-// quarter of them to a stage.  Step s is multiplied while step s + 1 goes from registers to the other stage and
-// step s + 2 is on its way from memory; past the last step the last one is repeated, and not read.
-template <int BM, typename Regs, typename Load, typename Put>
-__device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, f32x16 (&acc)[Grad<BM>::NJ], Load load, Put put) {
-    constexpr int WM = Grad<BM>::WM, NJ = Grad<BM>::NJ, OB = Grad<BM>::OB;
+// The sum over `steps` steps.  load(s, part, j) starts a twelfth of step s on its way into registers (part < 3,
+// j < 4), put(st, part, j) writes a twelfth of them to a stage.  A step's four parts of 16 of the sum each read the
+// next part's operands, across the turn too, write a third of the next step and start a third of the step after
+// it, three parts before it is needed; a quarter of that work goes with the three products of each 32 columns
+// (scheduled apart, so that what it holds in registers stays small).  Past the last step the last one is repeated,
+// and not used.
+template <typename Load, typename Put>
+__device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, f32x16 (&acc)[GB_NJ], Load load, Put put) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wi = wave % WM, wj = wave / WM, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
-    struct Frag {
-        bf16x8 a[3], b[NJ];
+    const int wi = wave & 3, wj = wave >> 2, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
+    // operands of part ks (16 of the sum) of a stage
+    struct Planes {
+        bf16x8 a[3];
     };
-    auto read = [&](const u32x4* st, int ks) {
-        const int at = (2 * ks + lg) ^ sw;
-        Frag f;
+    auto read_a = [&](const u32x4* st, int ks) {
+        Planes f;
 #pragma unroll
-        for (int q = 2; q >= 0; --q) f.a[q] = __builtin_bit_cast(bf16x8, st[(q * BM + 32 * wi + lr) * 8 + at]);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) f.b[j] = __builtin_bit_cast(bf16x8, st[OB + (32 * NJ * wj + 32 * j + lr) * 8 + at]);
+        for (int q = 2; q >= 0; --q) f.a[q] = __builtin_bit_cast(bf16x8, st[(q * GB_BM + 32 * wi + lr) * 8 + ((2 * ks + lg) ^ sw)]);
         return f;
     };
-    auto multiply = [&](const Frag& f) {
-#pragma unroll
-        for (int q = 2; q >= 0; --q)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[q], f.b[j], acc[j], 0, 0, 0);
+    auto read_b = [&](const u32x4* st, int ks, int j) {
+        return __builtin_bit_cast(bf16x8, st[GB_OB + (128 * wj + 32 * j + lr) * 8 + ((2 * ks + lg) ^ sw)]);
     };
+    bf16x8 b[GB_NJ];
     if (steps == 0) return;
     const int last = steps - 1;
-    // step s in `cur`, step s + 1 in registers r
-    auto step = [&](const u32x4* cur, u32x4* nxt, const Regs& r) {
-        Frag f = read(cur, 0);
+    // a part's products with planes f, smallest first; the next part's operands (ks of st) take the place of
+    // those that are done with
+    auto part_of = [&](const Planes& f, const u32x4* st, int ks, auto work) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            Frag g;
-            if (ks < 3) g = read(cur, ks + 1);
-            put(r, nxt, ks);
-            multiply(f);
-            // reads first, then a product and what VALU work of the quarter falls to it, in turn
-            __builtin_amdgcn_sched_group_barrier(0x100, 3 + NJ, 0);
+        for (int j = 0; j < GB_NJ; ++j) {
+            work(j);
 #pragma unroll
-            for (int i = 0; i < 3 * NJ; ++i) {
+            for (int q = 2; q >= 0; --q) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[q], b[j], acc[j], 0, 0, 0);
+            b[j] = read_b(st, ks, j);
+            // a product and what VALU work falls to it, in turn
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x200, 3, 0);
             __builtin_amdgcn_sched_barrier(0);
-            f = g;
         }
-        lds_barrier();
     };
-    Regs r0, r1;
-    load(r0, 0);
-    load(r1, min(1, last));
+    // step s in `cur`, its first operands in f and b, step s + 1 in registers
+    auto step = [&](const u32x4* cur, u32x4* nxt, int s, Planes& f) {
+        const int after = min(s + 2, last);
+        Planes g = read_a(cur, 1);
+        part_of(f, cur, 1, [&](int j) { put(nxt, 0, j); });
+        f = read_a(cur, 2);
+        part_of(g, cur, 2, [&](int j) {
+            put(nxt, 1, j);
+            load(after, 0, j);
+        });
+        g = read_a(cur, 3);
+        part_of(f, cur, 3, [&](int j) {
+            put(nxt, 2, j);
+            load(after, 1, j);
+        });
+        lds_barrier();                 // step s + 1 is whole, and every wave holds the rest of step s in registers
+        f = read_a(nxt, 0);
+        part_of(g, nxt, 0, [&](int j) { load(after, 2, j); });
+    };
 #pragma unroll
-    for (int q = 0; q < 4; ++q) put(r0, st0, q);
+    for (int i = 0; i < 12; ++i) load(0, i >> 2, i & 3);
+#pragma unroll
+    for (int i = 0; i < 12; ++i) put(st0, i >> 2, i & 3);
+#pragma unroll
+    for (int i = 0; i < 12; ++i) load(min(1, last), i >> 2, i & 3);
     lds_barrier();
-    for (int s = 0; s < steps; s += 2) {
-        load(r0, min(s + 2, last));
-        step(st0, st1, r1);
-        if (s + 1 >= steps) break;
-        load(r1, min(s + 3, last));
-        step(st1, st0, r0);
+    Planes f = read_a(st0, 0);
+#pragma unroll
+    for (int j = 0; j < GB_NJ; ++j) b[j] = read_b(st0, 0, j);
+    int s = 0;
+    for (; s + 2 <= steps; s += 2) {
+        step(st0, st1, s, f);
+        step(st1, st0, s + 1, f);
     }
+    if (s < steps) step(st0, st1, s, f);
 }
 
 // `rows` rows of a tile of `out` (row length K, columns from k0) from a wave's accumulators.
-template <int BM>
-__device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, int rows, int64_t k0, const f32x16 (&acc)[Grad<BM>::NJ]) {
-    constexpr int WM = Grad<BM>::WM, NJ = Grad<BM>::NJ;
+__device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, int rows, int64_t k0, const f32x16 (&acc)[GB_NJ]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t k = k0 + 32 * NJ * (wave / WM) + NJ * (lane & 31);
+    const int64_t k = k0 + 128 * (wave >> 2) + 4 * (lane & 31);
     if (k >= K) return;                                // K is a multiple of 4
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        const int m = 32 * (wave % WM) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        float v[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) v[j] = acc[j][r];
-        if (m < rows) __builtin_memcpy(out + (int64_t)m * K + k, v, 4 * NJ);
+        const int m = 32 * (wave & 3) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        const f32x4u v = {acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
+        if (m < rows) *reinterpret_cast<f32x4u*>(out + (int64_t)m * K + k) = v;
     }
 }
 
 // LDS row of k 4 c + j of the tile (c a lane, j < 4).
-template <int BM>
-__device__ __forceinline__ int grad_row(int c, int j) {
-    if constexpr (Grad<BM>::NJ == 4) return 128 * (c >> 5) + 32 * j + (c & 31);
-    else return 64 * (c >> 4) + 32 * (j & 1) + 2 * (c & 15) + (j >> 1);
-}
+__device__ __forceinline__ int grad_row(int c, int j) { return 128 * (c >> 5) + 32 * j + (c & 31); }
 
-template <int BM>
+template <bool SHORT>
 __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st1, const Slot& slot, int64_t k0) {
-    constexpr int OB = Grad<BM>::OB, UN = BM / 64;     // units of a plane that a thread forms
     const GroupedBackwardArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t N = a.N, rowb = a.K >> 2, e = slot.e;
     const int per = (int)((N + 63) / 64), steps = per * (a.w1 ? 2 : 1);
-    // of d: row tid / (8 / UN), UN units of 8; of W: rows 8 wave .., the lane's byte of 4 codes
-    const int row = tid / (8 / UN), unit = (tid % (8 / UN)) * UN;
-    const int64_t at = (slot.m0 + min(row, slot.rows - 1)) * N + 8 * unit;
+    // of d: row tid / 4, two units of 8; of W: rows 8 wave .., the lane's byte of 4 codes
+    const int row = tid >> 2, unit = (tid & 3) * 2;
+    const uint32_t at = ((uint32_t)min(row, slot.rows - 1) * (uint32_t)N + 8u * unit) * 4u;     // bytes
     const uint32_t byte = (uint32_t)min((k0 >> 2) + lane, rowb - 1);
-    struct Regs {
-        float v[UN][8], alpha;
-        uint32_t w[8];
-    };
-    auto load = [&](Regs& r, int s) {
+    // A last part step takes the last 64 n, those that the step before has taken with weights of zero (an
+    // element that is not finite has made its row so already); fewer than 64 n in all are guarded one by one.
+    float v[2][8], alpha;
+    uint32_t w[8];
+    int taken;                                         // of the wave's eight n
+    auto load = [&](int s, int part, int j) {
         const bool second = s >= per;
-        const int64_t n0 = (int64_t)(second ? s - per : s) * 64;
-        const float* d = (second ? p.d1 : p.d0) + at + n0;
-        const uint8_t* w = (second ? a.w1 : a.w0) + (e * N + n0 + 8 * wave) * rowb;
-        r.alpha = (second ? a.al1 : a.al0)[e];
-        if (n0 + 64 <= N) {
+        const int64_t begin = (int64_t)(second ? s - per : s) * 64, n0 = SHORT ? 0 : min(begin, N - 64);
+        if (part < 2) {
+            const float* d = (second ? p.d1 : p.d0) + slot.m0 * N + n0;
+            if constexpr (!SHORT) {
+                if (j == 1 || j == 3) {
+                    const f32x4u x = *(const __attribute__((address_space(1))) f32x4u*)(scalar_base(d) + at + 32 * part + 8 * (j - 1));
 #pragma unroll
-            for (int i = 0; i < UN; ++i) __builtin_memcpy(r.v[i], d + 8 * i, 32);
+                    for (int i = 0; i < 4; ++i) v[part][2 * (j - 1) + i] = x[i];
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r.w[i] = (w + i * rowb)[byte];
+                for (int i = 2 * j; i < 2 * j + 2; ++i) v[part][i] = 8 * (unit + part) + i < N ? d[at / 4 + 8 * part + i] : 0.0f;
+            }
+            // (the second part of the step before is written by then)
+            if (part == 0 && j == 3) alpha = (second ? a.al1 : a.al0)[e];
         } else {
-            const int left = (int)(N - n0);
+            const uint8_t* ws = (second ? a.w1 : a.w0) + (e * N + n0) * rowb;
+            if (j == 0) taken = (int)(begin - n0) - 8 * wave;
 #pragma unroll
-            for (int i = 0; i < UN; ++i)
-#pragma unroll
-                for (int x = 0; x < 8; ++x) r.v[i][x] = 8 * (unit + i) + x < left ? d[8 * i + x] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r.w[i] = (w + (min(8 * wave + i, left - 1) - 8 * wave) * rowb)[byte];
+            for (int i = 2 * j; i < 2 * j + 2; ++i)
+                w[i] = (uint8_t)scalar_base(ws + (SHORT ? min((int64_t)8 * wave + i, N - 1) : 8 * wave + i) * rowb)[byte];
         }
     };
-    auto put = [&](const Regs& r, u32x4* st, int part) {
-        if (part < UN) {
-            float t[8];
-            u32x4 pl[3];
+    u32x4 pl[3];
+    uint32_t codes[2];                                 // of four n each; 01 is a weight of zero
+    auto put = [&](u32x4* st, int part, int j) {
+        if (part < 2) {
+            split_2(v[part][2 * j] * alpha, v[part][2 * j + 1] * alpha, j, pl);
+            if (j == 3) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) t[x] = r.v[part][x] * r.alpha;
-            split_unit(t, pl);
-#pragma unroll
-            for (int q = 0; q < 3; ++q) st[(q * BM + row) * 8 + ((unit + part) ^ ((row >> 1) & 7))] = pl[q];
+                for (int q = 0; q < 3; ++q) st[(q * GB_BM + row) * 8 + ((unit + part) ^ ((row >> 1) & 7))] = pl[q];
+            }
+            return;
         }
-        if (part < 2) return;
-        // codes of four n a dword; for each k their bf16 values from tables of the upper and lower bytes
-        const uint32_t c0 = r.w[0] | r.w[1] << 8 | r.w[2] << 16 | r.w[3] << 24, c1 = r.w[4] | r.w[5] << 8 | r.w[6] << 16 | r.w[7] << 24;
-#pragma unroll
-        for (int j = 2 * part - 4; j < 2 * part - 2; ++j) {
-            u32x4 o;
+        if (j == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t c = ((h ? c1 : c0) >> (2 * j)) & 0x03030303u;
-                const uint32_t hi = __builtin_amdgcn_perm(0u, 0x003F00BFu, c), lo = __builtin_amdgcn_perm(0u, 0x00800080u, c);
-                o[2 * h] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-                o[2 * h + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+                const int gone = taken - 4 * h;
+                const uint32_t keep = gone >= 4 ? 0u : gone > 0 ? ~0u << 8 * gone : ~0u;
+                codes[h] = ((w[4 * h] | w[4 * h + 1] << 8 | w[4 * h + 2] << 16 | w[4 * h + 3] << 24) & keep) | (0x55555555u & ~keep);
             }
-            const int k = grad_row<BM>(lane, j);
-            st[OB + k * 8 + (wave ^ ((k >> 1) & 7))] = o;
         }
-    };
-    f32x16 acc[Grad<BM>::NJ];
+        // the codes' bf16 values from tables of the upper and lower bytes
+        u32x4 o;
 #pragma unroll
-    for (int j = 0; j < Grad<BM>::NJ; ++j) acc[j] = f32x16{};
-    grad_sum<BM, Regs>(st0, st1, steps, acc, load, put);
-    grad_store<BM>(a.dx + slot.m0 * a.K, a.K, slot.rows, k0, acc);
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t c = (codes[h] >> (2 * j)) & 0x03030303u;
+            const uint32_t hi = __builtin_amdgcn_perm(0u, 0x003F00BFu, c), lo = __builtin_amdgcn_perm(0u, 0x00800080u, c);
+            o[2 * h] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+            o[2 * h + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+        }
+        const int k = grad_row(lane, j);
+        st[GB_OB + k * 8 + (wave ^ ((k >> 1) & 7))] = o;
+    };
+    f32x16 acc[GB_NJ];
+#pragma unroll
+    for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
+    grad_sum(st0, st1, steps, acc, load, put);
+    grad_store(a.dx + slot.m0 * a.K, a.K, slot.rows, k0, acc);
 }
 
-template <int BM>
 __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st1, int64_t e, bool second, int64_t n0, int64_t k0) {
-    constexpr int OB = Grad<BM>::OB, UN = BM / 64;     // columns of d of a lane
     const GroupedBackwardArgs& a = p.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t N = a.N, K = a.K;
@@ -251,89 +269,91 @@ __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st
     // tokens of rows lane % 8 of the wave's rows of a step (of the last row past the end)
     auto tokens = [&](int s) {
         const int64_t m = g.lo + min(64 * s + 8 * wave + (lane & 7), rows - 1);
-        return a.rows ? a.rows[m] : m;
+        const int64_t r = *(a.rows ? a.rows + m : a.offsets);      // a load either way: the code has no branches
+        return a.rows ? r : m;
     };
-    struct Regs {
-        float v[UN][8], beta;
-        uint32_t x[8];
-        bool live;                                     // the row lies in the group, its token is there
-    };
+    float v[2][8], scale[8];
+    uint32_t x[8], beta, live;                         // live: all ones where the row lies in the group and its token is there
     int64_t next = steps ? tokens(0) : 0;              // tokens of the step that is loaded next
-    auto load = [&](Regs& r, int s) {
+    auto load = [&](int s, int part, int j) {
         const bool there = next >= 0 && next < a.T;
-        const uint64_t token = there ? (uint64_t)next : 0, off = token * (uint64_t)K;
-        r.beta = a.beta[token];
-        r.live = there && 64 * s + 8 * wave + (lane & 7) < rows;
-        const float* ds = d + (int64_t)s * 64 * N;
-        const int left = rows - 64 * s - 8 * wave;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // a buffer for what is left of each row: columns past it, and rows past the group's end, read zeros
-            const __amdgpu_buffer_rsrc_t rd = raw_buffer(ds + i * N, i < left ? width : 0);
-#pragma unroll
-            for (int c = 0; c < UN; ++c)
-                r.v[c][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, 4u * lane + 256u * c, 0, 0));
-            const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((uint32_t)(off >> 32), i) << 32 |
-                               (uint32_t)__builtin_amdgcn_readlane((uint32_t)off, i);
-            __builtin_memcpy(&r.x[i], a.xq + o + k, 4);
+        const uint64_t token = there ? (uint64_t)next : 0;
+        const int left = rows - 64 * s - 8 * wave;     // of the wave's eight rows
+        if (part == 0 && j == 0) {
+            beta = __float_as_uint(a.beta[token]);
+            live = there && (lane & 7) < left ? ~0u : 0u;
         }
-        next = tokens(min(s + 1, steps - 1));
-    };
-    auto put = [&](const Regs& r, u32x4* st, int part) {
-        if (part < UN) {
-            const float f = r.live ? r.beta / 127.0f : 0.0f;
-            float t[8];
-            u32x4 pl[3];
+        const uint64_t off = token * (uint64_t)K;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = r.v[part][i] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-            split_unit(t, pl);
-            const int c = lane + 64 * part;
-#pragma unroll
-            for (int q = 0; q < 3; ++q) st[(q * BM + c) * 8 + (wave ^ ((c >> 1) & 7))] = pl[q];
-        }
-        if (part < 2) return;
-#pragma unroll
-        for (int j = 2 * part - 4; j < 2 * part - 2; ++j) {
-            u32x4 o;
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float lo = (float)(int8_t)(r.x[i] >> (8 * j)), hi = (float)(int8_t)(r.x[i + 1] >> (8 * j));
-                o[i >> 1] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+        for (int i = 2 * j; i < 2 * j + 2; ++i) {
+            if (part < 2) {
+                // a buffer for what is left of each row: columns past it, and rows past the group's end, read zeros
+                const __amdgpu_buffer_rsrc_t rd = raw_buffer(d + ((int64_t)s * 64 + i) * N, i < left ? width : 0);
+                v[part][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, 4u * lane + 256u * part, 0, 0));
+            } else {
+                const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((uint32_t)(off >> 32), i) << 32 |
+                                   (uint32_t)__builtin_amdgcn_readlane((uint32_t)off, i);
+                x[i] = *(const __attribute__((address_space(1))) u32u*)(scalar_base(a.xq + o) + k);
             }
-            const int c = grad_row<BM>(lane, j);
-            st[OB + c * 8 + (wave ^ ((c >> 1) & 7))] = o;
         }
+        if (part == 2 && j == 3) next = tokens(min(s + 1, steps - 1));
     };
-    f32x16 acc[Grad<BM>::NJ];
+    u32x4 pl[3];
+    auto put = [&](u32x4* st, int part, int j) {
+        if (part < 2) {
+            if (part == 0 && j == 0) {
+                const float f = __uint_as_float(beta & live) / 127.0f;
 #pragma unroll
-    for (int j = 0; j < Grad<BM>::NJ; ++j) acc[j] = f32x16{};
-    grad_sum<BM, Regs>(st0, st1, steps, acc, load, put);
-    grad_store<BM>((second ? a.dw1 : a.dw0) + (e * N + n0) * K, K, (int)(N - n0 < BM ? N - n0 : BM), k0, acc);
+                for (int i = 0; i < 8; ++i) scale[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
+            }
+            split_2(v[part][2 * j] * scale[2 * j], v[part][2 * j + 1] * scale[2 * j + 1], j, pl);
+            if (j == 3) {
+                const int c = lane + 64 * part;
+#pragma unroll
+                for (int q = 0; q < 3; ++q) st[(q * GB_BM + c) * 8 + (wave ^ ((c >> 1) & 7))] = pl[q];
+            }
+            return;
+        }
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float lo = (float)(int8_t)(x[i] >> (8 * j)), hi = (float)(int8_t)(x[i + 1] >> (8 * j));
+            o[i >> 1] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+        }
+        const int c = grad_row(lane, j);
+        st[GB_OB + c * 8 + (wave ^ ((c >> 1) & 7))] = o;
+    };
+    f32x16 acc[GB_NJ];
+#pragma unroll
+    for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
+    grad_sum(st0, st1, steps, acc, load, put);
+    grad_store((second ? a.dw1 : a.dw0) + (e * N + n0) * K, K, (int)(N - n0 < GB_BM ? N - n0 : GB_BM), k0, acc);
 }
 
 // dx's tiles first (`dx_wgs` at most), whose sums are the longer ones, then dW's, so that the short ones fill the
 // card where dx's end.  Each XCD gets a contiguous run of dx's tiles and of every expert's tiles of dW (whose work
 // goes with the expert's rows).
-template <int BM>
 __global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx_wgs, int tiles_k, int tiles_n) {
-    __shared__ u32x4 st0[Grad<BM>::UNITS];
-    __shared__ u32x4 st1[Grad<BM>::UNITS];
+    __shared__ u32x4 st0[GB_UNITS];
+    __shared__ u32x4 st1[GB_UNITS];
     const GroupedBackwardArgs& a = p.a;
     auto run_of = [](int b, int T) { return (b & 7) * (T >> 3) + ((b & 7) < (T & 7) ? b & 7 : T & 7) + (b >> 3); };
     if ((int)blockIdx.x < dx_wgs) {
         int tiles_m;
-        find_slot<BM, true>(a.offsets, (int)a.E, a.M, -1, &tiles_m);
+        find_slot<GB_BM, true>(a.offsets, (int)a.E, a.M, -1, &tiles_m);
         const int T = tiles_m * tiles_k;
         if ((int)blockIdx.x >= T) return;
         int t = run_of(blockIdx.x, T);
         const int grp = t / (4 * tiles_k), gm = tiles_m - 4 * grp < 4 ? tiles_m - 4 * grp : 4;
         t -= grp * 4 * tiles_k;
-        dx_tile<BM>(p, st0, st1, find_slot<BM, false>(a.offsets, (int)a.E, a.M, 4 * grp + t % gm, nullptr), (int64_t)(t / gm) * GB_BN);
+        const Slot slot = find_slot<GB_BM, false>(a.offsets, (int)a.E, a.M, 4 * grp + t % gm, nullptr);
+        if (a.N >= 64) dx_tile<false>(p, st0, st1, slot, (int64_t)(t / gm) * GB_BN);
+        else dx_tile<true>(p, st0, st1, slot, (int64_t)(t / gm) * GB_BN);
     } else {
         const int T = (a.w1 ? 2 : 1) * tiles_n * tiles_k, T8 = (T + 7) & ~7, b = blockIdx.x - dx_wgs;
         if (b % T8 >= T) return;
         const int t = run_of(b % T8, T), tn = t / tiles_k % tiles_n;
-        dw_tile<BM>(p, st0, st1, b / T8, t >= tiles_n * tiles_k, (int64_t)tn * BM, (int64_t)(t % tiles_k) * GB_BN);
+        dw_tile(p, st0, st1, b / T8, t >= tiles_n * tiles_k, (int64_t)tn * GB_BM, (int64_t)(t % tiles_k) * GB_BN);
     }
 }
 
@@ -364,26 +384,24 @@ __global__ __launch_bounds__(1024) void k_grouped_dbias(Products p) {
 struct GradGrid {
     int64_t dx, dw, tiles_k, tiles_n;
 };
-template <int BM>
 static GradGrid grad_grid(int64_t M, int64_t K, int64_t N, int64_t E, bool dx, int projections) {
     GradGrid g;
     g.tiles_k = (K + GB_BN - 1) / GB_BN;
-    g.tiles_n = (N + BM - 1) / BM;
-    g.dx = dx && M > 0 ? (most_slots(M, E, BM) * g.tiles_k + 7) / 8 * 8 : 0;
+    g.tiles_n = (N + GB_BM - 1) / GB_BM;
+    g.dx = dx && M > 0 ? (most_slots(M, E, GB_BM) * g.tiles_k + 7) / 8 * 8 : 0;
     g.dw = E * ((projections * g.tiles_n * g.tiles_k + 7) / 8 * 8);
     return g;
 }
 
-template <int BM>
 static hipError_t launch_gradients(const Products& p, hipStream_t s) {
     const GroupedBackwardArgs& a = p.a;
-    const GradGrid g = grad_grid<BM>(a.M, a.K, a.N, a.E, a.dx, a.dw0 ? (a.w1 ? 2 : 1) : 0);
+    const GradGrid g = grad_grid(a.M, a.K, a.N, a.E, a.dx, a.dw0 ? (a.w1 ? 2 : 1) : 0);
     if (g.dx + g.dw == 0) return hipSuccess;
-    return launch_with_lds(k_grouped_gradients<BM>, dim3((unsigned)(g.dx + g.dw)), dim3(512), 0, s, p, (int)g.dx, (int)g.tiles_k, (int)g.tiles_n);
+    return launch_with_lds(k_grouped_gradients, dim3((unsigned)(g.dx + g.dw)), dim3(512), 0, s, p, (int)g.dx, (int)g.tiles_k, (int)g.tiles_n);
 }
 
 bool grouped_backward_fits(int64_t M, int64_t K, int64_t N, int64_t E) {
-    const GradGrid g = grad_grid<64>(M, K, N, E, true, 2);
+    const GradGrid g = grad_grid(M, K, N, E, true, 2);
     return grid_fits(g.dx + g.dw, 512);
 }
 
@@ -402,7 +420,7 @@ hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) 
         p.d0 = dg;
         p.d1 = du;
     }
-    const hipError_t e = launch_gradients<128>(p, s);
+    const hipError_t e = launch_gradients(p, s);
     if (e != hipSuccess) return e;
     if (a.db0 || a.db1) {
         hipLaunchKernelGGL(k_grouped_dbias, dim3((unsigned)((a.N + 63) / 64), (unsigned)a.E, a.w1 ? 2u : 1u), dim3(1024), 0, s, p);
