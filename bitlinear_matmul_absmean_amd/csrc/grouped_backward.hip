@@ -46,12 +46,15 @@ struct Products {
 // in steps of 64 of the sum.  A stage in LDS is three planes of the split factor, 128 rows of 64 bf16 values, and
 // 256 rows (one for each k) of the other; both are loaded from memory into registers two steps ahead, split or
 // widened there, turned where the sum runs down the rows, and written in 16-byte units while the stage before
-// is multiplied: unit u (8 of the sum) of row r at slot u ^ ((r / 2) % 8), which spreads reads and writes over all
-// banks.  Row of k: column 4 l + j of a wave's columns lies in row 32 j + l of theirs, so that a lane ends with
+// is multiplied: unit u (8 of the sum) of row r at slot u ^ grad_swizzle(r).  Row of k: column 4 l + j of a wave's columns lies in row 32 j + l of theirs, so that a lane ends with
 // four neighbouring columns.
 // 32x32x16 lane layout: A/B lane l holds row/column l % 32, 8 (l / 32) + j of the sum; accumulator r of lane l is
 // row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 constexpr int GB_BM = 128, GB_BN = 256, GB_NJ = 4, GB_OB = 3 * GB_BM * 8, GB_UNITS = GB_OB + GB_BN * 8;
+
+// Eight lanes that write the same unit of neighbouring rows (128 bytes a cycle) meet eight different slots;
+// sixteen that read it (256 bytes, two rows of a stage) as many pairs of a slot and a row's parity.
+__device__ __forceinline__ int grad_swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 // Loads at base + off: the base (the same for the whole wave) in scalar registers, a lane's 32-bit offset in one
 // vector register.  Any alignment of the type's elements.
@@ -90,7 +93,7 @@ __device__ __forceinline__ void split_2(float v0, float v1, int at, u32x4 (&pl)[
 template <typename Load, typename Put>
 __device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, f32x16 (&acc)[GB_NJ], Load load, Put put) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wi = wave & 3, wj = wave >> 2, lr = lane & 31, lg = lane >> 5, sw = (lr >> 1) & 7;
+    const int wi = wave & 3, wj = wave >> 2, lr = lane & 31, lg = lane >> 5, sw = grad_swizzle(lr);
     // operands of part ks (16 of the sum) of a stage
     struct Planes {
         bf16x8 a[3];
@@ -225,7 +228,7 @@ __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st
             split_2(v[part][2 * j] * alpha, v[part][2 * j + 1] * alpha, j, pl);
             if (j == 3) {
 #pragma unroll
-                for (int q = 0; q < 3; ++q) st[(q * GB_BM + row) * 8 + ((unit + part) ^ ((row >> 1) & 7))] = pl[q];
+                for (int q = 0; q < 3; ++q) st[(q * GB_BM + row) * 8 + ((unit + part) ^ grad_swizzle(row))] = pl[q];
             }
             return;
         }
@@ -247,7 +250,7 @@ __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st
             o[2 * h + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
         }
         const int k = grad_row(lane, j);
-        st[GB_OB + k * 8 + (wave ^ ((k >> 1) & 7))] = o;
+        st[GB_OB + k * 8 + (wave ^ grad_swizzle(k))] = o;
     };
     f32x16 acc[GB_NJ];
 #pragma unroll
@@ -310,7 +313,7 @@ __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st
             if (j == 3) {
                 const int c = lane + 64 * part;
 #pragma unroll
-                for (int q = 0; q < 3; ++q) st[(q * GB_BM + c) * 8 + (wave ^ ((c >> 1) & 7))] = pl[q];
+                for (int q = 0; q < 3; ++q) st[(q * GB_BM + c) * 8 + (wave ^ grad_swizzle(c))] = pl[q];
             }
             return;
         }
@@ -321,7 +324,7 @@ __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st
             o[i >> 1] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
         }
         const int c = grad_row(lane, j);
-        st[GB_OB + c * 8 + (wave ^ ((c >> 1) & 7))] = o;
+        st[GB_OB + c * 8 + (wave ^ grad_swizzle(c))] = o;
     };
     f32x16 acc[GB_NJ];
 #pragma unroll
