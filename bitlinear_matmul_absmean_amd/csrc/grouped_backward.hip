@@ -19,10 +19,6 @@ namespace bitlinear {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-size_t grouped_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t E, bool gated) {
-    return 256 + (gated ? (size_t)M * N * 8 : 0);
-}
-
 // dg and du, one element a thread at a time.
 template <int ACT>
 __global__ __launch_bounds__(256) void k_gate_gradients(const float* __restrict__ dh, const float* __restrict__ g,
@@ -39,6 +35,8 @@ __global__ __launch_bounds__(256) void k_gate_gradients(const float* __restrict_
 struct Products {
     GroupedBackwardArgs a;
     const float *d0, *d1;          // [M, N]: dy, or dg and du
+    int parts;                     // of dx's sums
+    float* dx;                     // a.dx, or [parts, M, K] where there are several
 };
 
 // ---- the two products -----------------------------------------------------------------------
@@ -46,7 +44,8 @@ struct Products {
 // in steps of 64 of the sum.  A stage in LDS is three planes of the split factor, 128 rows of 64 bf16 values, and
 // 256 rows (one for each k) of the other; both are loaded from memory into registers two steps ahead, split or
 // widened there, turned where the sum runs down the rows, and written in 16-byte units while the stage before
-// is multiplied: unit u (8 of the sum) of row r at slot u ^ grad_swizzle(r).  Row of k: column 4 l + j of a wave's columns lies in row 32 j + l of theirs, so that a lane ends with
+// is multiplied: unit u (8 of the sum) of row r at slot u ^ grad_swizzle(r).  Row of k: column 4 l + j of a
+// wave's columns lies in row 32 j + l of theirs, so that a lane ends with
 // four neighbouring columns.
 // 32x32x16 lane layout: A/B lane l holds row/column l % 32, 8 (l / 32) + j of the sum; accumulator r of lane l is
 // row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
@@ -84,14 +83,14 @@ __device__ __forceinline__ void split_2(float v0, float v1, int at, u32x4 (&pl)[
     for (int q = 0; q < 3; ++q) pl[q][at] = __builtin_amdgcn_perm(b[1][q], b[0][q], 0x07060302u);
 }
 
-// The sum over `steps` steps.  load(s, part, j) starts a twelfth of step s on its way into registers (part < 3,
+// The sum of `length` terms in `steps` steps.  load(s, part, j) starts a twelfth of step s on its way into registers (part < 3,
 // j < 4), put(st, part, j) writes a twelfth of them to a stage.  A step's four parts of 16 of the sum each read the
 // next part's operands, across the turn too, write a third of the next step and start a third of the step after
 // it, three parts before it is needed; a quarter of that work goes with the three products of each 32 columns
 // (scheduled apart, so that what it holds in registers stays small).  Past the last step the last one is repeated,
 // and not used.
 template <typename Load, typename Put>
-__device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, f32x16 (&acc)[GB_NJ], Load load, Put put) {
+__device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, int length, f32x16 (&acc)[GB_NJ], Load load, Put put) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wi = wave & 3, wj = wave >> 2, lr = lane & 31, lg = lane >> 5, sw = grad_swizzle(lr);
     // operands of part ks (16 of the sum) of a stage
@@ -151,6 +150,19 @@ __device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, f32x
     for (int i = 0; i < 12; ++i) load(0, i >> 2, i & 3);
 #pragma unroll
     for (int i = 0; i < 12; ++i) put(st0, i >> 2, i & 3);
+    if (steps == 1) {                  // a short group: only the parts that hold something of the sum
+        lds_barrier();
+        for (int ks = 0; 16 * ks < length; ++ks) {
+            const Planes f = read_a(st0, ks);
+#pragma unroll
+            for (int j = 0; j < GB_NJ; ++j) {
+                b[j] = read_b(st0, ks, j);
+#pragma unroll
+                for (int q = 2; q >= 0; --q) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[q], b[j], acc[j], 0, 0, 0);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 12; ++i) load(min(1, last), i >> 2, i & 3);
     lds_barrier();
@@ -182,11 +194,13 @@ __device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, i
 __device__ __forceinline__ int grad_row(int c, int j) { return 128 * (c >> 5) + 32 * j + (c & 31); }
 
 template <bool SHORT>
-__device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st1, const Slot& slot, int64_t k0) {
+__device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st1, const Slot& slot, int64_t k0, int part) {
     const GroupedBackwardArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t N = a.N, rowb = a.K >> 2, e = slot.e;
-    const int per = (int)((N + 63) / 64), steps = per * (a.w1 ? 2 : 1);
+    // part `part` of the sum's steps
+    const int per = (int)((N + 63) / 64), all = per * (a.w1 ? 2 : 1);
+    const int first = (int)((int64_t)all * part / p.parts), steps = (int)((int64_t)all * (part + 1) / p.parts) - first;
     // of d: row tid / 4, two units of 8; of W: rows 8 wave .., the lane's byte of 4 codes
     const int row = tid >> 2, unit = (tid & 3) * 2;
     const uint32_t at = ((uint32_t)min(row, slot.rows - 1) * (uint32_t)N + 8u * unit) * 4u;     // bytes
@@ -197,6 +211,7 @@ __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st
     uint32_t w[8];
     int taken;                                         // of the wave's eight n
     auto load = [&](int s, int part, int j) {
+        s += first;
         const bool second = s >= per;
         const int64_t begin = (int64_t)(second ? s - per : s) * 64, n0 = SHORT ? 0 : min(begin, N - 64);
         if (part < 2) {
@@ -255,8 +270,8 @@ __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st
     f32x16 acc[GB_NJ];
 #pragma unroll
     for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
-    grad_sum(st0, st1, steps, acc, load, put);
-    grad_store(a.dx + slot.m0 * a.K, a.K, slot.rows, k0, acc);
+    grad_sum(st0, st1, steps, 64 * steps, acc, load, put);
+    grad_store(p.dx + (part * a.M + slot.m0) * a.K, a.K, slot.rows, k0, acc);
 }
 
 __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st1, int64_t e, bool second, int64_t n0, int64_t k0) {
@@ -329,35 +344,54 @@ __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st
     f32x16 acc[GB_NJ];
 #pragma unroll
     for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
-    grad_sum(st0, st1, steps, acc, load, put);
+    grad_sum(st0, st1, steps, rows, acc, load, put);
     grad_store((second ? a.dw1 : a.dw0) + (e * N + n0) * K, K, (int)(N - n0 < GB_BM ? N - n0 : GB_BM), k0, acc);
 }
 
-// dx's tiles first (`dx_wgs` at most), whose sums are the longer ones, then dW's, so that the short ones fill the
-// card where dx's end.  Each XCD gets a contiguous run of dx's tiles and of every expert's tiles of dW (whose work
-// goes with the expert's rows).
+// dx's tiles first (`dx_wgs` of each part at most), whose sums are the longer ones, then dW's, so that the short
+// ones fill the card where dx's end.  Each XCD gets a contiguous run of dx's tiles and of every expert's tiles of dW
+// (whose work goes with the expert's rows).
 __global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx_wgs, int tiles_k, int tiles_n) {
     __shared__ u32x4 st0[GB_UNITS];
     __shared__ u32x4 st1[GB_UNITS];
     const GroupedBackwardArgs& a = p.a;
     auto run_of = [](int b, int T) { return (b & 7) * (T >> 3) + ((b & 7) < (T & 7) ? b & 7 : T & 7) + (b >> 3); };
-    if ((int)blockIdx.x < dx_wgs) {
+    int b = blockIdx.x;
+    if (b < p.parts * dx_wgs) {
+        const int part = b / dx_wgs;
+        b -= part * dx_wgs;
         int tiles_m;
         find_slot<GB_BM, true>(a.offsets, (int)a.E, a.M, -1, &tiles_m);
         const int T = tiles_m * tiles_k;
-        if ((int)blockIdx.x >= T) return;
-        int t = run_of(blockIdx.x, T);
+        if (b >= T) return;
+        int t = run_of(b, T);
         const int grp = t / (4 * tiles_k), gm = tiles_m - 4 * grp < 4 ? tiles_m - 4 * grp : 4;
         t -= grp * 4 * tiles_k;
         const Slot slot = find_slot<GB_BM, false>(a.offsets, (int)a.E, a.M, 4 * grp + t % gm, nullptr);
-        if (a.N >= 64) dx_tile<false>(p, st0, st1, slot, (int64_t)(t / gm) * GB_BN);
-        else dx_tile<true>(p, st0, st1, slot, (int64_t)(t / gm) * GB_BN);
+        if (a.N >= 64) dx_tile<false>(p, st0, st1, slot, (int64_t)(t / gm) * GB_BN, part);
+        else dx_tile<true>(p, st0, st1, slot, (int64_t)(t / gm) * GB_BN, part);
     } else {
-        const int T = (a.w1 ? 2 : 1) * tiles_n * tiles_k, T8 = (T + 7) & ~7, b = blockIdx.x - dx_wgs;
+        const int T = (a.w1 ? 2 : 1) * tiles_n * tiles_k, T8 = (T + 7) & ~7;
+        b -= p.parts * dx_wgs;
         if (b % T8 >= T) return;
         const int t = run_of(b % T8, T), tn = t / tiles_k % tiles_n;
         dw_tile(p, st0, st1, b / T8, t >= tiles_n * tiles_k, (int64_t)tn * GB_BM, (int64_t)(t % tiles_k) * GB_BN);
     }
+}
+
+// dx from its parts, in their order: a row of a group x 1024 columns a workgroup.
+__global__ __launch_bounds__(256) void k_grouped_dx_sum(Products p) {
+    const GroupedBackwardArgs& a = p.a;
+    const Slot slot = find_slot<1, false>(a.offsets, (int)a.E, a.M, (int)blockIdx.x, nullptr);
+    const int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4, size = a.M * a.K, at = slot.m0 * a.K + k;
+    if (slot.rows == 0 || k >= a.K) return;
+    float4 sum = *reinterpret_cast<const float4*>(p.dx + at);
+#pragma unroll 8
+    for (int q = 1; q < p.parts; ++q) {
+        const float4 v = *reinterpret_cast<const float4*>(p.dx + q * size + at);
+        sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    }
+    *reinterpret_cast<f32x4u*>(a.dx + at) = f32x4u{sum.x, sum.y, sum.z, sum.w};
 }
 
 // ---- bias gradients -------------------------------------------------------------------------
@@ -383,33 +417,40 @@ __global__ __launch_bounds__(1024) void k_grouped_dbias(Products p) {
     }
 }
 
-// Workgroups of both products: dx's, a multiple of the XCDs, and dW's.
+// Workgroups of both products: dx's of a part, a multiple of the XCDs, and dW's; and the parts that dx's sums are
+// cut into where its tiles are too few to fill the card.
 struct GradGrid {
-    int64_t dx, dw, tiles_k, tiles_n;
+    int64_t dx, dw, tiles_k, tiles_n, parts;
 };
-static GradGrid grad_grid(int64_t M, int64_t K, int64_t N, int64_t E, bool dx, int projections) {
+static GradGrid grad_grid(int64_t M, int64_t K, int64_t N, int64_t E, int projections, bool dx = true, bool dw = true) {
     GradGrid g;
     g.tiles_k = (K + GB_BN - 1) / GB_BN;
     g.tiles_n = (N + GB_BM - 1) / GB_BM;
-    g.dx = dx && M > 0 ? (most_slots(M, E, GB_BM) * g.tiles_k + 7) / 8 * 8 : 0;
-    g.dw = E * ((projections * g.tiles_n * g.tiles_k + 7) / 8 * 8);
+    const int64_t tiles = most_slots(M, E, GB_BM) * g.tiles_k, steps = projections * ((N + 63) / 64);
+    g.dx = dx ? (tiles + 7) / 8 * 8 : 0;
+    g.dw = dw ? E * ((projections * g.tiles_n * g.tiles_k + 7) / 8 * 8) : 0;
+    g.parts = 1;
+    if (tiles > 0 && tiles <= 128) {
+        g.parts = 256 / tiles;
+        if (g.parts > (steps + 3) / 4) g.parts = (steps + 3) / 4;
+    }
     return g;
 }
 
-static hipError_t launch_gradients(const Products& p, hipStream_t s) {
-    const GroupedBackwardArgs& a = p.a;
-    const GradGrid g = grad_grid(a.M, a.K, a.N, a.E, a.dx, a.dw0 ? (a.w1 ? 2 : 1) : 0);
-    if (g.dx + g.dw == 0) return hipSuccess;
-    return launch_with_lds(k_grouped_gradients, dim3((unsigned)(g.dx + g.dw)), dim3(512), 0, s, p, (int)g.dx, (int)g.tiles_k, (int)g.tiles_n);
+// dg and du of the gated block, then dx's parts.
+static size_t gate_bytes(int64_t M, int64_t N, bool gated) { return gated ? ((size_t)M * N * 8 + 255) / 256 * 256 : 0; }
+size_t grouped_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t E, bool gated) {
+    const GradGrid g = grad_grid(M, K, N, E, gated ? 2 : 1);
+    return 256 + gate_bytes(M, N, gated) + (g.parts > 1 ? (size_t)g.parts * M * K * 4 : 0);
 }
 
 bool grouped_backward_fits(int64_t M, int64_t K, int64_t N, int64_t E) {
-    const GradGrid g = grad_grid(M, K, N, E, true, 2);
-    return grid_fits(g.dx + g.dw, 512);
+    const GradGrid g = grad_grid(M, K, N, E, 2);
+    return grid_fits(g.parts * g.dx + g.dw, 512);
 }
 
 hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) {
-    Products p{a, a.dy, nullptr};
+    Products p{a, a.dy, nullptr, 1, a.dx};
     if (a.w1 && a.M > 0) {
         float* dg = reinterpret_cast<float*>(a.ws);
         float* du = dg + a.M * a.N;
@@ -423,8 +464,22 @@ hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) 
         p.d0 = dg;
         p.d1 = du;
     }
-    const hipError_t e = launch_gradients(p, s);
-    if (e != hipSuccess) return e;
+    const GradGrid g = grad_grid(a.M, a.K, a.N, a.E, a.w1 ? 2 : 1, a.dx && a.M > 0, a.dw0);
+    if (a.dx && g.parts > 1) {
+        p.parts = (int)g.parts;
+        p.dx = reinterpret_cast<float*>(static_cast<char*>(a.ws) + gate_bytes(a.M, a.N, a.w1));
+    }
+    if (g.dx + g.dw > 0) {
+        hipLaunchKernelGGL(k_grouped_gradients, dim3((unsigned)(p.parts * g.dx + g.dw)), dim3(512), 0, s, p, (int)g.dx, (int)g.tiles_k,
+                           (int)g.tiles_n);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (p.parts > 1) {
+        hipLaunchKernelGGL(k_grouped_dx_sum, dim3((unsigned)most_slots(a.M, a.E, 1), (unsigned)((a.K + 1023) / 1024)), dim3(256), 0, s, p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     if (a.db0 || a.db1) {
         hipLaunchKernelGGL(k_grouped_dbias, dim3((unsigned)((a.N + 63) / 64), (unsigned)a.E, a.w1 ? 2u : 1u), dim3(1024), 0, s, p);
         return hipGetLastError();
