@@ -8,10 +8,11 @@
 // A group is cut into slots of a tile's rows; the host, which does not know the offsets, launches as many
 // workgroups as there can be slots, and each finds its own from the offsets.  A workgroup multiplies its rows
 // with two sets of weight rows: the gate and up rows of the same columns, whose product is then formed where
-// the sums end, or two neighbouring sets of columns of the one projection.  Two kernels, each in a form for
-// aligned rows and one for any K % 4 == 0 and any alignment:
-//   * few rows an expert: k_grouped_dec, the weight streams on the 16x16x64 int8 MFMA;
-//   * else: k_grouped_gemm, LDS tiles on the 32x32x32 int8 MFMA.
+// the sums end, or two neighbouring sets of columns of the one projection.  Two kernels:
+//   * few rows an expert: k_grouped_dec, the weight streams on the 16x16x64 int8 MFMA, for any K % 4 == 0 and any
+//     alignment;
+//   * else: k_grouped_gemm, LDS tiles on the 32x32x32 int8 MFMA, in a form for aligned rows (16-byte aligned
+//     tensors, K % 64 == 0, T K < 2^32) and one for any.
 #include <type_traits>
 
 #include "experts.hpp"
@@ -21,7 +22,7 @@ namespace bitlinear {
 
 static int64_t most_slots(const GroupedArgs& a, int64_t tile) { return most_slots(a.M, a.E, tile); }
 
-// The GEMM's smallest tiles, 32 rows x 128 columns of 256 threads (the streaming kernel is taken where its fit).
+// The GEMM's smallest tiles, 32 rows x 128 columns of 256 threads (the streaming kernel is taken for few).
 bool grouped_fits(int64_t M, int64_t N, int64_t E) { return grid_fits(most_slots(M, E, 32) * ((N + 127) / 128), 256); }
 
 // Element `at` (m N + n) of the gated block from its two sums.
@@ -35,27 +36,21 @@ __device__ __forceinline__ void gate_store(const GroupedArgs& a, int64_t at, flo
 }
 
 // ---- few rows an expert ---------------------------------------------------------------------
-// A workgroup of eight waves computes 16 MT rows x 16 columns of both sets; wave w takes the steps of 256 k
-// w, w + 8, ..., and the partial tiles are added at the end (integers: exact in any order).  In MFMA q of a
-// step lane group g (lanes 16 g ..) holds weights 64 g + 16 q .. 64 g + 16 q + 15, dword q of the lane's 16
-// bytes of codes, expanded in weight order to signed bytes.
-// Aligned rows (16-byte aligned tensors, K % 64 == 0, T K < 2^32): operands come through a wave's own LDS image,
-// filled by loads that go past the registers; a step's image is read into registers, the next step's loads are
-// started into it, and the MFMAs run while they are in flight.  Row R's 16-byte unit u of a step lies at
-// position u ^ (R % 16) of its sixteen.  Otherwise operands are read straight into registers.
+// A workgroup of four waves computes 16 rows x 16 columns of both sets; wave w takes the steps of 256 k w, w + 4,
+// ..., and the partial tiles are added at the end (integers: exact in any order).  In MFMA q of a step lane group g
+// (lanes 16 g ..) holds weights 64 g + 16 q .. 64 g + 16 q + 15, dword q of the lane's 16 bytes of codes, expanded
+// in weight order to signed bytes.  Operands go straight into registers, a step ahead; the first weights are on
+// their way before the rows' tokens are known.
 // 16x16x64 lane layout: A/B lane l holds row/column l % 16, k = 16 (l / 16) + j; accumulator r of
 // lane l is row 4 (l / 16) + r, column l % 16.
-constexpr int ED_WAVES = 8;
+constexpr int ED_WAVES = 4;
 
-template <bool GATED, bool ALIGNED, int MT>
+template <bool GATED>
 __global__ __launch_bounds__(64 * ED_WAVES) void k_grouped_dec(GroupedArgs a, int slots) {
-    constexpr int IMG = (4 * MT + 2) * 64;                          // 16-byte units of a wave's image
-    constexpr int TILES = 2 * MT * 64;                              // of a wave's partial tiles
-    constexpr int PER = ALIGNED && IMG > TILES ? IMG : TILES;
-    __shared__ i32x4 lds[ED_WAVES * PER];
+    __shared__ i32x4 part[ED_WAVES * 2 * 64];
     const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Slot slot = find_slot<16 * MT, false>(a.offsets, (int)a.E, a.M, (int)(blockIdx.x % slots), nullptr);
+    const Slot slot = find_slot<16, false>(a.offsets, (int)a.E, a.M, (int)(blockIdx.x % slots), nullptr);
     const int rows_m = slot.rows;
     if (rows_m == 0) return;
     const int64_t K = a.K, rowb = K >> 2, e = slot.e, m0 = slot.m0;
@@ -66,165 +61,87 @@ __global__ __launch_bounds__(64 * ED_WAVES) void k_grouped_dec(GroupedArgs a, in
     const int rows_n1 = GATED ? rows_n : (int)(a.N - n1 < 0 ? 0 : a.N - n1 < 16 ? a.N - n1 : 16);
     const uint8_t* w0 = a.w0 + (e * a.N + n0) * rowb;
     const uint8_t* w1 = GATED ? a.w1 + (e * a.N + n0) * rowb : rows_n1 ? w0 + 16 * rowb : w0;
-    const int last_n = rows_n - 1, last_n1 = rows_n1 ? rows_n1 - 1 : rows_n - 1;
-    // tokens of the rows, one a lane (of row 0 past the end)
-    int token = 0;
-    float beta = 0.0f;
-    {
-        const int64_t r = row_token(a.rows, m0 + min(lane, rows_m - 1), a.T);
-        if (r >= 0) {
-            token = (int)r;
-            beta = a.beta[r];
-        }
-    }
-    const int steps = (int)((K + 255) / 256);
-    i32x4 acc[2][MT];
+    const uint8_t *wp[2] = {w0 + (int64_t)min(lr, rows_n - 1) * rowb, w1 + (int64_t)min(lr, (rows_n1 ? rows_n1 : rows_n) - 1) * rowb};
+    const int whole = (int)(K / 256);
+    struct Part {
+        i32x4 x[4];
+        u32x4 w[2];
+    };
+    auto load_w = [&](Part& f, int s) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < 2; ++p) f.w[p] = load_16(wp[p] + (int64_t)s * 64 + 16 * lg);
+    };
+    Part f;
+    if (wave < whole) load_w(f, wave);
+    // the lane's row lr (the last one past the end), its token, and beta: 0 for a token that is not there
+    const int64_t r = row_token(a.rows, m0 + min(lr, rows_m - 1), a.T);
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(a.xq) + (r < 0 ? 0 : r) * K;
+    const float beta = r < 0 ? 0.0f : a.beta[r];
+    auto load_x = [&](Part& f, int s) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[p][t] = i32x4{0, 0, 0, 0};
-    auto multiply = [&](const i32x4 (&xv)[MT][4], const u32x4 (&w)[2]) {
+        for (int q = 0; q < 4; ++q) f.x[q] = (i32x4)load_16(x + (int64_t)s * 256 + 64 * lg + 16 * q);
+    };
+    i32x4 acc[2] = {i32x4{0, 0, 0, 0}, i32x4{0, 0, 0, 0}};
+    auto multiply = [&](const Part& f) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const i32x4 b = expand_signed_in_order(w[p][q]);
-#pragma unroll
-                for (int t = 0; t < MT; ++t) acc[p][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv[t][q], b, acc[p][t], 0, 0, 0);
-            }
+            for (int p = 0; p < 2; ++p) acc[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.x[q], expand_signed_in_order(f.w[p][q]), acc[p], 0, 0, 0);
     };
-    const uint8_t *wp[2] = {w0 + (int64_t)min(lr, last_n) * rowb, w1 + (int64_t)min(lr, last_n1) * rowb};
-    const uint8_t* xp[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) xp[t] = reinterpret_cast<const uint8_t*>(a.xq) + (int64_t)__shfl(token, 16 * t + lr, 64) * K;
-    // step s with its operands read straight into registers
-    auto direct = [&](int s) {
-        const int64_t k = (int64_t)s * 256 + 64 * lg;
-        i32x4 xv[MT][4];
-        u32x4 w[2];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) w[p] = row_16(wp[p], k >> 2, rowb);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) xv[t][q] = (i32x4)row_16(xp[t], k + 16 * q, K);
-        multiply(xv, w);
-    };
-    if constexpr (ALIGNED) {
-        const int whole = (int)(K / 256);                           // a last part step is read directly
-        i32x4* img = lds + wave * IMG;
-        const __amdgpu_buffer_rsrc_t rx = raw_buffer(a.xq, (uint32_t)(a.T * K));
-        const __amdgpu_buffer_rsrc_t r0 = raw_buffer(w0, (uint32_t)rows_n * (uint32_t)rowb);
-        const __amdgpu_buffer_rsrc_t r1 = raw_buffer(w1, (uint32_t)(last_n1 + 1) * (uint32_t)rowb);
-        // load i of x: rows 4 i .. 4 i + 3, sixteen lanes each; of a set: lane (lr, lg) reads 64 codes of row
-        // lr.  Rows past the end repeat the last one; groups of four rows past it are not loaded (what they
-        // hold reaches only outputs that are not written).
-        uint32_t xo[4 * MT];
-#pragma unroll
-        for (int i = 0; i < 4 * MT; ++i)
-            xo[i] = (uint32_t)__shfl(token, 4 * i + lg, 64) * (uint32_t)K + 16u * (uint32_t)(lr ^ ((4 * i + lg) & 15));
-        const uint32_t o0 = (uint32_t)min(lr, last_n) * (uint32_t)rowb + 16u * (uint32_t)lg;
-        const uint32_t o1 = (uint32_t)min(lr, last_n1) * (uint32_t)rowb + 16u * (uint32_t)lg;
-        auto fetch = [&](int s) {
-            load_lds16(r0, o0, (uint32_t)s * 64u, img + 64 * (4 * MT));
-            load_lds16(r1, o1, (uint32_t)s * 64u, img + 64 * (4 * MT + 1));
-#pragma unroll
-            for (int i = 0; i < 4 * MT; ++i)
-                if (4 * i < rows_m) load_lds16(rx, xo[i], (uint32_t)s * 256u, img + 64 * i);
-        };
-        if (wave < whole) fetch(wave);
+    if (wave < whole) {
+        load_x(f, wave);
         for (int s = wave; s < whole; s += ED_WAVES) {
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(0x0F70);                     // vmcnt(0): the image is whole
-            __builtin_amdgcn_sched_barrier(0);
-            i32x4 xv[MT][4];
-            u32x4 w[2];
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) xv[t][q] = img[(16 * t + lr) * 16 + ((4 * lg + q) ^ lr)];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) w[p] = (u32x4)img[64 * (4 * MT + p) + lane];
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(0xC07F);                     // lgkmcnt(0): every read of it is over
-            __builtin_amdgcn_sched_barrier(0);
-            if (s + ED_WAVES < whole) fetch(s + ED_WAVES);
-            multiply(xv, w);
+            Part next;
+            load_w(next, min(s + ED_WAVES, whole - 1));
+            load_x(next, min(s + ED_WAVES, whole - 1));
+            multiply(f);
+            f = next;
         }
-        if (whole < steps && whole % ED_WAVES == wave) direct(whole);
-    } else {
-        struct Part {
-            i32x4 x[MT][4];
-            u32x4 w[2];
-        };
-        auto load = [&](int s) {
-            const int64_t k = (int64_t)s * 256 + 64 * lg;
-            Part f;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) f.w[p] = load_16(wp[p] + (k >> 2));
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) f.x[t][q] = (i32x4)load_16(xp[t] + k + 16 * q);
-            return f;
-        };
-        // whole steps, the next one's loads under way; the last part step goes to the next wave in turn
-        const int whole = (int)(K / 256);
-        if (wave < whole) {
-            Part f = load(wave);
-            for (int s = wave; s < whole; s += ED_WAVES) {
-                const Part next = load(min(s + ED_WAVES, whole - 1));
-                multiply(f.x, f.w);
-                f = next;
-            }
-        }
-        if (whole < steps && whole % ED_WAVES == wave) direct(whole);
     }
-    __syncthreads();                                                // every wave is done with its image
+    if (K % 256 && whole % ED_WAVES == wave) {                      // the last part step, to the next wave in turn
+        const int64_t k = (int64_t)whole * 256 + 64 * lg;
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < 2; ++p) f.w[p] = row_16(wp[p], k >> 2, rowb);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) lds[(wave * 2 * MT + p * MT + t) * 64 + lane] = acc[p][t];
+        for (int q = 0; q < 4; ++q) f.x[q] = (i32x4)row_16(x, k + 16 * q, K);
+        multiply(f);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) part[(wave * 2 + p) * 64 + lane] = acc[p];
     __syncthreads();
-    const float al0 = a.al0[e], al1 = GATED ? a.al1[e] : al0;
-    // element i of row block t and column l % 16, of both sets; a wave's elements share t and i
-    for (int x = tid; x < MT * 256; x += 64 * ED_WAVES) {
-        const int l = x & 63, i = (x >> 6) & 3, t = x >> 8, n = l & 15, m = 16 * t + 4 * (l >> 4) + i;
-        const float b = __shfl(beta, m, 64);
-        int s0 = 0, s1 = 0;
+    // wave i takes element i of every lane: row 4 (l / 16) + i, column l % 16, of both sets
+    const int i = wave, n = lr, m = 4 * lg + i;
+    const float b = __shfl(beta, m, 64);
+    int s0 = 0, s1 = 0;
 #pragma unroll
-        for (int w = 0; w < ED_WAVES; ++w) {
-            const int* p = reinterpret_cast<const int*>(lds + (w * 2 * MT + t) * 64 + l);
-            s0 += p[i];
-            s1 += p[i + MT * 256];
-        }
-        if (m >= rows_m) continue;
-        const int64_t at = (m0 + m) * a.N + n0 + n, bn = e * a.N + n0 + n;
-        float v0 = (float)s0 * dequant_scale(al0, b), v1 = (float)s1 * dequant_scale(al1, b);
-        if constexpr (GATED) {
-            if (n >= rows_n) continue;
-            if (a.b0) v0 = v0 + a.b0[bn];
-            if (a.b1) v1 = v1 + a.b1[bn];
-            if (a.act == BITLINEAR_ACT_SILU) gate_store<BITLINEAR_ACT_SILU>(a, at, v0, v1);
-            else if (a.act == BITLINEAR_ACT_GELU) gate_store<BITLINEAR_ACT_GELU>(a, at, v0, v1);
-            else gate_store<BITLINEAR_ACT_RELU2>(a, at, v0, v1);
-        } else {
-            if (n < rows_n) a.y[at] = a.b0 ? v0 + a.b0[bn] : v0;
-            if (n < rows_n1) a.y[at + 16] = a.b0 ? v1 + a.b0[bn + 16] : v1;
-        }
+    for (int w = 0; w < ED_WAVES; ++w) {
+        const int* p = reinterpret_cast<const int*>(part + w * 2 * 64 + lane);
+        s0 += p[i];
+        s1 += p[i + 256];
+    }
+    if (m >= rows_m) return;
+    const int64_t at = (m0 + m) * a.N + n0 + n, bn = e * a.N + n0 + n;
+    float v0 = (float)s0 * dequant_scale(a.al0[e], b);
+    if constexpr (GATED) {
+        if (n >= rows_n) return;
+        float v1 = (float)s1 * dequant_scale(a.al1[e], b);
+        if (a.b0) v0 = v0 + a.b0[bn];
+        if (a.b1) v1 = v1 + a.b1[bn];
+        if (a.act == BITLINEAR_ACT_SILU) gate_store<BITLINEAR_ACT_SILU>(a, at, v0, v1);
+        else if (a.act == BITLINEAR_ACT_GELU) gate_store<BITLINEAR_ACT_GELU>(a, at, v0, v1);
+        else gate_store<BITLINEAR_ACT_RELU2>(a, at, v0, v1);
+    } else {
+        const float v1 = (float)s1 * dequant_scale(a.al0[e], b);
+        if (n < rows_n) a.y[at] = a.b0 ? v0 + a.b0[bn] : v0;
+        if (n < rows_n1) a.y[at + 16] = a.b0 ? v1 + a.b0[bn + 16] : v1;
     }
 }
 
-template <bool GATED, bool ALIGNED, int MT>
-static hipError_t launch_grouped_dec_mt(const GroupedArgs& a, hipStream_t s) {
-    const int64_t slots = most_slots(a, 16 * MT), blocks = (a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32);
-    hipLaunchKernelGGL((k_grouped_dec<GATED, ALIGNED, MT>), dim3((unsigned)(slots * blocks)), dim3(64 * ED_WAVES), 0, s, a, (int)slots);
-    return hipGetLastError();
-}
-
-template <bool GATED, bool ALIGNED>
+template <bool GATED>
 static hipError_t launch_grouped_dec(const GroupedArgs& a, hipStream_t s) {
-    return a.M <= 8 * a.E ? launch_grouped_dec_mt<GATED, ALIGNED, 1>(a, s) : launch_grouped_dec_mt<GATED, ALIGNED, 2>(a, s);
+    const int64_t slots = most_slots(a, 16), blocks = (a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32);
+    hipLaunchKernelGGL(k_grouped_dec<GATED>, dim3((unsigned)(slots * blocks)), dim3(64 * ED_WAVES), 0, s, a, (int)slots);
+    return hipGetLastError();
 }
 
 // ---- many rows an expert --------------------------------------------------------------------
@@ -232,7 +149,7 @@ static hipError_t launch_grouped_dec(const GroupedArgs& a, hipStream_t s) {
 // each: FM 32-row operands against one weight operand of each set, so that the expansion of a weight operand
 // (17 instructions) serves FM MFMAs.  Steps of 128 k, three LDS stages (4 FM + 8 KiB each: 32 FM rows of x_q of
 // 128 bytes, 256 weight rows of 32 bytes) filled two steps ahead by loads that go past the registers (aligned
-// rows, as above), or two filled through registers.  Unit u of x_q's row r lies at slot u ^ ((r / 2) % 8), unit u
+// rows), or two filled through registers.  Unit u of x_q's row r lies at slot u ^ ((r / 2) % 8), unit u
 // of weight row r at slot u ^ ((r / 8) % 2), so that an operand read spreads over all banks.
 // In the two MFMAs of k 64 h .. 64 h + 63 (h = 0, 1) a lane group holds 32 codes, eight bytes of a
 // weight row: the lane's unit h, of which group lg uses dwords 2 lg and 2 lg + 1.
@@ -497,18 +414,25 @@ static hipError_t launch_grouped_gemm_fm(const GroupedArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Tiles of 32 rows where a group has few, or while those tiles are at most about as many as compute units; then 64,
+// and 128 for long sums and many tiles.  Microseconds with 32 / 64 / 128 rows, for experts of so many rows (the
+// number of tiles of 32 as counted below):
+//   8 experts 4096 -> 11008, gated: 16 rows (688) 42.1 / 51.8 / 83.2;  32 (1032) 64.0 / 53.4 / 86.2
+//   8 experts 2048 -> 2816: 64 rows (220) 13.6 / 17.0 / 22.7;  128 (396) 19.2 / 18.8 / 25.3;  gated 32 (264) 13.6 /
+//     16.6 / 23.4;  gated 128 (792) 31.7 / 27.2 / 38.3;  gated 512 (2904) 86.2 / 64.1 / 73.8
+//   16 experts 2816 -> 2048: 48 rows (256) 16.8 / 20.5 / 28.4;  64 (320) 22.9 / 21.5 / 28.9
+//   8 experts 4096 -> 11008: 64 rows (860) 51.1 / 51.0 / 54.9;  128 (1548) 75.9 / 71.3 / 62.0;  512 (5676) 288 / 208 / 200
 template <int ACT, bool ALIGNED>
 static hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
-    const int64_t rows = a.M / (a.E < a.M ? a.E : a.M);
-    return rows <= 32   ? launch_grouped_gemm_fm<ACT, ALIGNED, 1>(a, s)
-           : rows <= 64 ? launch_grouped_gemm_fm<ACT, ALIGNED, 2>(a, s)
-                        : launch_grouped_gemm_fm<ACT, ALIGNED, 4>(a, s);
+    const int64_t used = a.E < a.M ? a.E : a.M, rows = a.M / used;
+    const int64_t tiles = (a.M / 32 + used / 2) * ((a.N + (ACT ? EG_BF : 2 * EG_BF) - 1) / (ACT ? EG_BF : 2 * EG_BF));
+    if (rows <= 24 || tiles <= 288) return launch_grouped_gemm_fm<ACT, ALIGNED, 1>(a, s);
+    if (a.K >= 4096 && rows >= 96 && tiles >= 1280) return launch_grouped_gemm_fm<ACT, ALIGNED, 4>(a, s);
+    return launch_grouped_gemm_fm<ACT, ALIGNED, 2>(a, s);
 }
 
 template <bool ALIGNED>
-static hipError_t launch_grouped_rows(const GroupedArgs& a, hipStream_t s) {
-    if (a.M <= 16 * a.E && grid_fits(most_slots(a, 16) * ((a.N + 15) / 16), 64 * ED_WAVES))
-        return a.w1 ? launch_grouped_dec<true, ALIGNED>(a, s) : launch_grouped_dec<false, ALIGNED>(a, s);
+static hipError_t launch_grouped_tiles(const GroupedArgs& a, hipStream_t s) {
     if (!a.w1) return launch_grouped_gemm<0, ALIGNED>(a, s);
     switch (a.act) {
         case BITLINEAR_ACT_SILU: return launch_grouped_gemm<BITLINEAR_ACT_SILU, ALIGNED>(a, s);
@@ -517,10 +441,21 @@ static hipError_t launch_grouped_rows(const GroupedArgs& a, hipStream_t s) {
     }
 }
 
+// The streaming kernel while its workgroups (slots of 16 rows as counted below, by blocks of columns) are few enough:
+// a GEMM's time is about 5 us and 3.5 ns a unit of K while its tiles run at once, the streaming kernel's 3.5 us and 2
+// ps (up to two rows an expert) to 3.5 ps a workgroup and unit of K.  Microseconds, streaming kernel against GEMM of 32
+// rows (workgroups):  8 experts 2048 -> 2816, gated: 2 rows (1408) 9.4 / 11.3, 4 (1408) 11.6 / 11.6, 16 (2112) 22.9 /
+// 12.0;  16 experts 2816 -> 2048: 8 rows (1024) 11.1 / 15.0, 16 (1536) 17.8 / 15.4;  64 experts 1024 -> 1024: 1 row
+// (2048) 8.2 / 8.7, gated (4096) 12.0 / 9.7;  8 experts 4096 -> 11008: 1 row (2752) 23.9 / 20.7;  4 experts 512 -> 1024:
+// 128 rows (1088) 6.5 / 7.6, 256 (2112) 9.8 / 7.9;  7 experts 1088 -> 1537: 32 rows (857) 7.7 / 9.8, 64 (1519) 11.4 / 10.1.
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t s) {
+    const int64_t used = a.E < a.M ? a.E : a.M, half_full = a.M / 16 + used / 2, slots = used > half_full ? used : half_full;
+    const int64_t blocks = a.w1 ? (a.N + 15) / 16 : (a.N + 31) / 32;
+    const int64_t most = a.M <= 2 * used ? ((int64_t)1 << 20) / a.K + 2048 : ((int64_t)1 << 19) / a.K + 1024;
+    if (slots * blocks <= most) return a.w1 ? launch_grouped_dec<true>(a, s) : launch_grouped_dec<false>(a, s);
     const bool aligned = a.K % 64 == 0 && a.T <= 0xFFFFFFFFll / a.K && (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.w0 % 16 == 0 &&
                          (uintptr_t)a.w1 % 16 == 0;
-    return aligned ? launch_grouped_rows<true>(a, s) : launch_grouped_rows<false>(a, s);
+    return aligned ? launch_grouped_tiles<true>(a, s) : launch_grouped_tiles<false>(a, s);
 }
 
 }  // namespace bitlinear
