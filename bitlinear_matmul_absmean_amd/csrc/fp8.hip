@@ -374,45 +374,61 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = prt[i][j] = f32x16{};
     }
-    struct Frag {
+    // k 32 kk .. 32 kk + 31 of the step in stage st
+    struct Raw {
         u32x4 w[FN], x[MI];
     };
-    // operands of k 32 kk .. 32 kk + 31 of the step in stage st
     auto read = [&](const i32x4* st, int kk) {
         const int at = (2 * kk + lg) ^ sw;
-        Frag f;
+        Raw f;
 #pragma unroll
         for (int j = 0; j < FN; ++j) f.w[j] = (u32x4)st[OB + (32 * FN * wj + 32 * j + lr) * 8 + at];
 #pragma unroll
         for (int i = 0; i < MI; ++i) f.x[i] = (u32x4)st[(32 * MI * wi + 32 * i + lr) * 8 + at];
         return f;
     };
+    // half h of them as operands of 16 k
+    struct Operands {
+        f16x8 w[FN], x[MI];
+    };
+    auto convert = [&](const Raw& f, int h) {
+        Operands o;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) o.w[j] = f16_of(f.w[j][2 * h], f.w[j][2 * h + 1]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) o.x[i] = f16_of(f.x[i][2 * h], f.x[i][2 * h + 1]);
+        return o;
+    };
     // the last step's sums, times their scale, into acc
     auto settle = [&](int i, int j) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(prt[i][j][e], sc[i], acc[i][j][e]);
     };
-    // two products of 16 k of every block; a step's first ones follow what is left of the step before it
-    auto multiply = [&](const Frag& f, bool first) {
+    // a product of 16 k of every block; a step's first one follows what is left of the step before it
+    auto multiply = [&](const Operands& o, bool first) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f16x8 w[FN], x[MI];
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < FN; ++j) w[j] = f16_of(f.w[j][2 * h], f.w[j][2 * h + 1]);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) x[i] = f16_of(f.x[i][2 * h], f.x[i][2 * h + 1]);
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    if (first && h == 0) {
-                        settle(i, j);
-                        prt[i][j] = f32x16{};
-                    }
-                    prt[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w[j], x[i], prt[i][j], 0, 0, 0);
+            for (int j = 0; j < FN; ++j) {
+                if (first) {
+                    settle(i, j);
+                    prt[i][j] = f32x16{};
                 }
+                prt[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.w[j], o.x[i], prt[i][j], 0, 0, 0);
+            }
+    };
+    // the same with half h of f converted meanwhile: a product and what VALU work falls to it, in turn
+    auto part = [&](const Operands& o, const Raw& f, int h, bool first) {
+        const Operands n = convert(f, h);
+        multiply(o, first);
+#pragma unroll
+        for (int i = 0; i < MI * FN; ++i) {
+            if (first) __builtin_amdgcn_sched_group_barrier(0x002, 16, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
+        return n;
     };
     // a step's scales, loaded a step ahead (their product is formed where it is used)
     struct Scales {
@@ -454,28 +470,33 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
                 for (int q = WB / 2 * (third - 1); q < WB / 2 * third; ++q) load_lds16(rw, wo[q], so, st + OB + 64 * (WB * wave + q));
             }
         };
-        // Step s in stage `cur`, its first operands in f0, its scales in sv.  Operands are read one part ahead of
-        // their products, across the turn too; the stage that a turn frees is loaded with the step after next but
-        // one, a third at a time.  Loads past the last whole step repeat it and are not read.
-        auto step = [&](i32x4* cur, i32x4* nxt, i32x4* prv, int s, Frag& f0, Scales& sv) {
-            Frag f1 = read(cur, 1);
+        // Step s in stage `cur`, its first 32 k in r0 and the first 16 of them in o, its scales in sv.  Operands are
+        // read one part and converted half a part ahead of their products, across the turn too; the stage that a
+        // turn frees is loaded with the step after next but one, a third at a time.  Loads past the last whole step
+        // repeat it and are not read.
+        auto step = [&](i32x4* cur, i32x4* nxt, i32x4* prv, int s, Raw& r0, Operands& o, Scales& sv) {
+            Raw r1 = read(cur, 1);
             const Scales sn = scales(min(s + 1, last));
             fetch(prv, min(s + 2, last), 1);
-            multiply(f0, true);
+            o = part(o, r0, 1, true);
             use(sv);
-            f0 = read(cur, 2);
+            o = part(o, r1, 0, false);
+            r0 = read(cur, 2);
             fetch(prv, min(s + 2, last), 2);
-            multiply(f1, false);
-            f1 = read(cur, 3);
-            multiply(f0, false);
+            o = part(o, r1, 1, false);
+            o = part(o, r0, 0, false);
+            r1 = read(cur, 3);
+            o = part(o, r0, 1, false);
+            o = part(o, r1, 0, false);
             sv = sn;
             // step s + 1 has landed for every wave, and every wave holds the rest of step s in registers
-            __builtin_amdgcn_s_waitcnt(wait_vm(XB + WB));                 // vmcnt(the loads of step s + 2) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(wait_vm(XB + WB));                      // vmcnt(the loads of step s + 2) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            f0 = read(nxt, 0);
+            r0 = read(nxt, 0);
             fetch(cur, min(s + 3, last), 0);
-            multiply(f1, false);
+            o = part(o, r1, 1, false);
+            o = part(o, r0, 0, false);
         };
         if (steps > 0) {
             Scales sv = scales(0);
@@ -488,15 +509,16 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
             __builtin_amdgcn_s_waitcnt(wait_vm(2 * XB + WB));             // vmcnt(the loads after step 0's) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            Frag f = read(st0, 0);
+            Raw r = read(st0, 0);
+            Operands o = convert(r, 0);
             int s = 0;
             for (; s + 3 <= steps; s += 3) {
-                step(st0, st1, st2, s, f, sv);
-                step(st1, st2, st0, s + 1, f, sv);
-                step(st2, st0, st1, s + 2, f, sv);
+                step(st0, st1, st2, s, r, o, sv);
+                step(st1, st2, st0, s + 1, r, o, sv);
+                step(st2, st0, st1, s + 2, r, o, sv);
             }
-            if (s < steps) step(st0, st1, st2, s, f, sv);
-            if (s + 1 < steps) step(st1, st2, st0, s + 1, f, sv);
+            if (s < steps) step(st0, st1, st2, s, r, o, sv);
+            if (s + 1 < steps) step(st1, st2, st0, s + 1, r, o, sv);
             __builtin_amdgcn_s_waitcnt(0x0070);                                 // nothing is in flight into the stages any more
         }
     } else {
@@ -527,8 +549,11 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
             const Scales sv = scales(b);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                multiply(read(st, kk), kk == 0);
+                const Raw f = read(st, kk);
+                multiply(convert(f, 0), kk == 0);
                 if (kk == 0) use(sv);
+                multiply(convert(f, 1), false);
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
         // whole steps in st1 and st0 in turn, loaded two ahead
@@ -554,13 +579,14 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(Fp8Args a, int tiles_m, int
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
             const int64_t k = (int64_t)steps * FG_BK + 32 * kk + 16 * lg;
-            Frag f;
+            Raw f;
 #pragma unroll
             for (int j = 0; j < FN; ++j) f.w[j] = row_16<DWORDS>(w0 + (int64_t)min(32 * FN * wj + 32 * j + lr, rows_n - 1) * K, k, K);
 #pragma unroll
             for (int i = 0; i < MI; ++i) f.x[i] = row_16<DWORDS>(x0 + (int64_t)min(32 * MI * wi + 32 * i + lr, rows_m - 1) * K, k, K);
-            multiply(f, kk == 0);
+            multiply(convert(f, 0), kk == 0);
             if (kk == 0) use(sv);
+            multiply(convert(f, 1), false);
         }
     }
     const bool vector = a.N % 4 == 0 && (uintptr_t)a.y % 16 == 0 && (uintptr_t)a.bias % 16 == 0;
