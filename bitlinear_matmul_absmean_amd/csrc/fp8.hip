@@ -614,20 +614,28 @@ static hipError_t launch_fp8_gemm_tile(const Fp8Args& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Tiles of 64 x 256: what the choices below count.
-static int64_t fp8_tiles(const Fp8Args& a) { return (a.M + 63) / 64 * ((a.N + 255) / 256); }
-
+// The largest tile whose workgroups still fill the card, by the number of tiles of 64 x 256.  Microseconds with
+// 64 x 128 / 64 x 256 / 128 x 256:  K = N = 4096, 512 tokens (128 tiles) 27.1 / 33.0 / 50.5, 1024 (256) 43.9 / 41.3 /
+// 54.0, 2048 (512) 88.2 / 83.3 / 69.6;  K = N = 8192, 256 tokens (128) 43.3 / 56.3 / 87.1, 512 (256) 79.0 / 73.0 / 91.3;
+// K = 4096, N = 11008, 192 tokens (129) 37.7 / 33.9 / 53.0, 384 (258) 57.2 / 66.8 / 54.9.
+// Rows off dword boundaries are read dword by dword only in 64-token tiles: with many tiles the plain loads' time
+// is hidden.
 template <int ROWS>
 static hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
-    const int64_t tiles = fp8_tiles(a);
+    const int64_t tiles = (a.M + 63) / 64 * ((a.N + 255) / 256);
     if (tiles <= 128) return launch_fp8_gemm_tile<ROWS, 1, 1>(a, s);
     if (tiles <= 256) return launch_fp8_gemm_tile<ROWS, 1, 2>(a, s);
     return launch_fp8_gemm_tile<ROWS == ROWS_1 ? ROWS_4 : ROWS, 2, 2>(a, s);
 }
 
+// The streaming kernel's time goes with the 16 x 16 blocks of y and K, the GEMM's with K alone while its tiles run
+// at once: they meet near N ceil(M / 16) = 23000.  Microseconds, streaming kernel against 64 x 128 tiles:  K = N = 4096,
+// 64 tokens 13.5 / 20.0, 96 tokens (24576) 23.0 / 20.6;  K = 4096, N = 11008, 32 tokens (22016) 20.3 / 20.8, 48 tokens
+// 26.3 / 21.5;  K = 11008, N = 4096, 64 tokens 29.4 / 46.8, 96 tokens 53.3 / 47.5;  K = 4096, N = 32000, 1 token 26.4 /
+// 23.6;  K = 2048, N = 2816, 128 tokens (22528) 12.9 / 13.0.  (At most 128 tokens: every 64 read the weights again.)
 template <int ROWS>
 static hipError_t launch_fp8(const Fp8Args& a, hipStream_t s) {
-    return a.M <= 16 || fp8_tiles(a) <= 32 ? launch_fp8_dec<ROWS>(a, s) : launch_fp8_gemm<ROWS>(a, s);
+    return a.M <= 128 && a.N * ((a.M + 15) / 16) <= 23000 ? launch_fp8_dec<ROWS>(a, s) : launch_fp8_gemm<ROWS>(a, s);
 }
 
 hipError_t launch_forward_fp8(const Fp8Args& a, hipStream_t s) {
