@@ -47,6 +47,11 @@ __device__ __forceinline__ float4 row_4(const float* __restrict__ p, int64_t i, 
     if constexpr (WHOLE) {
         return i < n ? *reinterpret_cast<const float4*>(p + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     } else {
+        float4 v;
+        if (i + 4 <= n) {
+            __builtin_memcpy(&v, p + i, 16);           // on a float's boundary
+            return v;
+        }
         return make_float4(i < n ? p[i] : 0.0f, i + 1 < n ? p[i + 1] : 0.0f, i + 2 < n ? p[i + 2] : 0.0f,
                            i + 3 < n ? p[i + 3] : 0.0f);
     }
@@ -56,6 +61,8 @@ template <bool WHOLE>
 __device__ __forceinline__ void put_4(uint8_t* __restrict__ p, int64_t i, int64_t n, uint32_t v) {
     if constexpr (WHOLE) {
         if (i < n) *reinterpret_cast<uint32_t*>(p + i) = v;
+    } else if (i + 4 <= n) {
+        __builtin_memcpy(p + i, &v, 4);                // on any boundary
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -97,32 +104,34 @@ hipError_t launch_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t
 }
 
 // ---- weights --------------------------------------------------------------------------------
-// A workgroup takes a block of 128 x 128: 16 times eight rows of 32 lanes, kept in registers between the
+// A workgroup takes a block of 128 x 128: PASSES times 128 / PASSES rows of 32 lanes, kept in registers between the
 // maximum and the codes.
-template <bool WHOLE>
-__global__ __launch_bounds__(256) void k_quantize_weights_fp8(const float* __restrict__ W, int64_t N, int64_t K,
-                                                              uint8_t* __restrict__ wq, float* __restrict__ ws) {
-    __shared__ float red[4];
+template <bool WHOLE, int PASSES>
+__global__ __launch_bounds__(4096 / PASSES) void k_quantize_weights_fp8(const float* __restrict__ W, int64_t N, int64_t K,
+                                                                        uint8_t* __restrict__ wq, float* __restrict__ ws) {
+    constexpr int WAVES = 64 / PASSES, STEP = 128 / PASSES;
+    __shared__ float red[WAVES];
     const int tid = threadIdx.x, r = tid >> 5;
     const int64_t n0 = (int64_t)blockIdx.y * 128, k = (int64_t)blockIdx.x * 128 + 4 * (tid & 31);
-    float4 v[16];
+    float4 v[PASSES];
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t n = n0 + 8 * i + r;
+    for (int i = 0; i < PASSES; ++i) {
+        const int64_t n = n0 + STEP * i + r;
         v[i] = n < N ? row_4<WHOLE>(W + n * K, k, K) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, abs_max_4(v[i]));
+    for (int i = 0; i < PASSES; ++i) top = fmaxf(top, abs_max_4(v[i]));
     top = wave_max_f32(top);
     if ((tid & 63) == 0) red[tid >> 6] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, red[w]);
     const Divisor d = divisor(top / 448.0f);
     auto write = [&](auto fast) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int64_t n = n0 + 8 * i + r;
+        for (int i = 0; i < PASSES; ++i) {
+            const int64_t n = n0 + STEP * i + r;
             if (n < N) put_4<WHOLE>(wq + n * K, k, K, codes_4<decltype(fast)::value>(v[i], d));
         }
     };
@@ -133,6 +142,7 @@ __global__ __launch_bounds__(256) void k_quantize_weights_fp8(const float* __res
 
 hipError_t launch_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t* wq, float* ws, hipStream_t s) {
     const bool whole = K % 4 == 0 && (uintptr_t)W % 16 == 0 && (uintptr_t)wq % 4 == 0;
+    constexpr int FPW = 4;
     // a grid dimension holds 65535 blocks of rows (y): more rows in several launches
     const int64_t nb = (K + 127) / 128, step = (int64_t)65535 * 128;
     for (int64_t n0 = 0; n0 < N; n0 += step) {
@@ -141,8 +151,8 @@ hipError_t launch_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uin
         const float* w = W + n0 * K;
         uint8_t* q = wq + n0 * K;
         float* sc = ws + n0 / 128 * nb;
-        if (whole) hipLaunchKernelGGL((k_quantize_weights_fp8<true>), grid, dim3(256), 0, s, w, n, K, q, sc);
-        else hipLaunchKernelGGL((k_quantize_weights_fp8<false>), grid, dim3(256), 0, s, w, n, K, q, sc);
+        if (whole) hipLaunchKernelGGL((k_quantize_weights_fp8<true, FPW>), grid, dim3(4096 / FPW), 0, s, w, n, K, q, sc);
+        else hipLaunchKernelGGL((k_quantize_weights_fp8<false, FPW>), grid, dim3(4096 / FPW), 0, s, w, n, K, q, sc);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
