@@ -88,11 +88,12 @@ __device__ __forceinline__ void split_2(float v0, float v1, int at, u32x4 (&pl)[
 // next part's operands, across the turn too, write a third of the next step and start a third of the step after
 // it, three parts before it is needed; a quarter of that work goes with the three products of each 32 columns
 // (scheduled apart, so that what it holds in registers stays small).  Past the last step the last one is repeated,
-// and not used.
-template <typename Load, typename Put>
-__device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, int length, f32x16 (&acc)[GB_NJ], Load load, Put put) {
+// and not used.  FEW: waves whose 32 rows lie past the tile's `rows` form no products (neighbouring waves, on other
+// SIMDs, share the rows that there are).
+template <bool FEW, typename Load, typename Put>
+__device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, int length, int rows, f32x16 (&acc)[GB_NJ], Load load, Put put) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wi = wave & 3, wj = wave >> 2, lr = lane & 31, lg = lane >> 5, sw = grad_swizzle(lr);
+    const int wi = wave >> 1, wj = wave & 1, lr = lane & 31, lg = lane >> 5, sw = grad_swizzle(lr);
     // operands of part ks (16 of the sum) of a stage
     struct Planes {
         bf16x8 a[3];
@@ -115,8 +116,10 @@ __device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, int 
 #pragma unroll
         for (int j = 0; j < GB_NJ; ++j) {
             work(j);
+            if (!FEW || 32 * wi < rows) {
 #pragma unroll
-            for (int q = 2; q >= 0; --q) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[q], b[j], acc[j], 0, 0, 0);
+                for (int q = 2; q >= 0; --q) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[q], b[j], acc[j], 0, 0, 0);
+            }
             b[j] = read_b(st, ks, j);
             // a product and what VALU work falls to it, in turn
 #pragma unroll
@@ -180,11 +183,11 @@ __device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, int 
 // `rows` rows of a tile of `out` (row length K, columns from k0) from a wave's accumulators.
 __device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, int rows, int64_t k0, const f32x16 (&acc)[GB_NJ]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t k = k0 + 128 * (wave >> 2) + 4 * (lane & 31);
+    const int64_t k = k0 + 128 * (wave & 1) + 4 * (lane & 31);
     if (k >= K) return;                                // K is a multiple of 4
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        const int m = 32 * (wave & 3) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        const int m = 32 * (wave >> 1) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
         const f32x4u v = {acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
         if (m < rows) *reinterpret_cast<f32x4u*>(out + (int64_t)m * K + k) = v;
     }
@@ -193,7 +196,7 @@ __device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, i
 // LDS row of k 4 c + j of the tile (c a lane, j < 4).
 __device__ __forceinline__ int grad_row(int c, int j) { return 128 * (c >> 5) + 32 * j + (c & 31); }
 
-template <bool SHORT>
+template <bool SHORT, bool FEW>
 __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st1, const Slot& slot, int64_t k0, int part) {
     const GroupedBackwardArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -270,7 +273,7 @@ __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st
     f32x16 acc[GB_NJ];
 #pragma unroll
     for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
-    grad_sum(st0, st1, steps, 64 * steps, acc, load, put);
+    grad_sum<FEW>(st0, st1, steps, 64 * steps, slot.rows, acc, load, put);
     grad_store(p.dx + (part * a.M + slot.m0) * a.K, a.K, slot.rows, k0, acc);
 }
 
@@ -344,14 +347,35 @@ __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st
     f32x16 acc[GB_NJ];
 #pragma unroll
     for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
-    grad_sum(st0, st1, steps, rows, acc, load, put);
+    grad_sum<false>(st0, st1, steps, rows, GB_BM, acc, load, put);
     grad_store((second ? a.dw1 : a.dw0) + (e * N + n0) * K, K, (int)(N - n0 < GB_BM ? N - n0 : GB_BM), k0, acc);
 }
 
+// Bias gradients of 64 columns of an expert: eight rows at a time, sums in fp64 in a fixed order.
+__device__ __forceinline__ void dbias_tile(const Products& p, u32x4* lds, int64_t e, bool second, int64_t n0) {
+    const GroupedBackwardArgs& a = p.a;
+    float* db = second ? a.db1 : a.db0;
+    if (!db) return;
+    double* part = reinterpret_cast<double*>(lds);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n = n0 + lane;
+    const float* d = (second ? p.d1 : p.d0) + min(n, a.N - 1);
+    const Group g = group_rows(a.offsets, e, a.M);
+    double sum = 0.0;
+#pragma unroll 8
+    for (int64_t m = g.lo + wave; m < g.hi; m += 8) sum += (double)d[m * a.N];
+    part[64 * wave + lane] = sum;
+    __syncthreads();
+    if (wave != 0 || n >= a.N) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) sum += part[64 * w + lane];
+    db[e * a.N + n] = (float)sum;
+}
+
 // dx's tiles first (`dx_wgs` of each part at most), whose sums are the longer ones, then dW's, so that the short
-// ones fill the card where dx's end.  Each XCD gets a contiguous run of dx's tiles and of every expert's tiles of dW
+// ones fill the card where dx's end; between them `db_wgs` of the bias gradients.  Each XCD gets a contiguous run of dx's tiles and of every expert's tiles of dW
 // (whose work goes with the expert's rows).
-__global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx_wgs, int tiles_k, int tiles_n) {
+__global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx_wgs, int db_wgs, int tiles_k, int tiles_n) {
     __shared__ u32x4 st0[GB_UNITS];
     __shared__ u32x4 st1[GB_UNITS];
     const GroupedBackwardArgs& a = p.a;
@@ -368,11 +392,16 @@ __global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx
         const int grp = t / (4 * tiles_k), gm = tiles_m - 4 * grp < 4 ? tiles_m - 4 * grp : 4;
         t -= grp * 4 * tiles_k;
         const Slot slot = find_slot<GB_BM, false>(a.offsets, (int)a.E, a.M, 4 * grp + t % gm, nullptr);
-        if (a.N >= 64) dx_tile<false>(p, st0, st1, slot, (int64_t)(t / gm) * GB_BN, part);
-        else dx_tile<true>(p, st0, st1, slot, (int64_t)(t / gm) * GB_BN, part);
+        const int64_t k0 = (int64_t)(t / gm) * GB_BN;
+        if (a.N < 64) dx_tile<true, true>(p, st0, st1, slot, k0, part);
+        else if (slot.rows <= 64) dx_tile<false, true>(p, st0, st1, slot, k0, part);
+        else dx_tile<false, false>(p, st0, st1, slot, k0, part);
+    } else if (b -= p.parts * dx_wgs; b < db_wgs) {
+        const int per = (int)((a.N + 63) / 64), two = a.w1 ? 2 : 1, t = b / per;
+        if (t < (int)a.E * two) dbias_tile(p, st0, t / two, t % two != 0, (int64_t)(b % per) * 64);
     } else {
         const int T = (a.w1 ? 2 : 1) * tiles_n * tiles_k, T8 = (T + 7) & ~7;
-        b -= p.parts * dx_wgs;
+        b -= db_wgs;
         if (b % T8 >= T) return;
         const int t = run_of(b % T8, T), tn = t / tiles_k % tiles_n;
         dw_tile(p, st0, st1, b / T8, t >= tiles_n * tiles_k, (int64_t)tn * GB_BM, (int64_t)(t % tiles_k) * GB_BN);
@@ -394,45 +423,24 @@ __global__ __launch_bounds__(256) void k_grouped_dx_sum(Products p) {
     *reinterpret_cast<f32x4u*>(a.dx + at) = f32x4u{sum.x, sum.y, sum.z, sum.w};
 }
 
-// ---- bias gradients -------------------------------------------------------------------------
-// A workgroup takes 64 columns of an expert's rows, 16 rows at a time; sums in fp64 in a fixed order.
-__global__ __launch_bounds__(1024) void k_grouped_dbias(Products p) {
-    __shared__ double part[16][64];
-    const GroupedBackwardArgs& a = p.a;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t n = (int64_t)blockIdx.x * 64 + lane, e = blockIdx.y;
-    float* db = blockIdx.z ? a.db1 : a.db0;
-    if (!db) return;
-    const float* d = (blockIdx.z ? p.d1 : p.d0) + min(n, a.N - 1);
-    const Group g = group_rows(a.offsets, e, a.M);
-    double sum = 0.0;
-#pragma unroll 8
-    for (int64_t m = g.lo + wave; m < g.hi; m += 16) sum += (double)d[m * a.N];
-    part[wave][lane] = sum;
-    __syncthreads();
-    if (wave == 0 && n < a.N) {
-#pragma unroll
-        for (int w = 1; w < 16; ++w) sum += part[w][lane];
-        db[e * a.N + n] = (float)sum;
-    }
-}
-
-// Workgroups of both products: dx's of a part, a multiple of the XCDs, and dW's; and the parts that dx's sums are
-// cut into where its tiles are too few to fill the card.
+// Workgroups of both products and the bias gradients: dx's of a part, db and dW's, all but dW's multiples of the XCDs;
+// and the parts that dx's sums are cut into where its tiles are too few to fill the card.
 struct GradGrid {
-    int64_t dx, dw, tiles_k, tiles_n, parts;
+    int64_t dx, db, dw, tiles_k, tiles_n, parts;
+    int64_t all(bool split) const { return (split ? parts : 1) * dx + db + dw; }
 };
-static GradGrid grad_grid(int64_t M, int64_t K, int64_t N, int64_t E, int projections, bool dx = true, bool dw = true) {
+static GradGrid grad_grid(int64_t M, int64_t K, int64_t N, int64_t E, int projections, bool dx = true, bool db = true, bool dw = true) {
     GradGrid g;
     g.tiles_k = (K + GB_BN - 1) / GB_BN;
     g.tiles_n = (N + GB_BM - 1) / GB_BM;
     const int64_t tiles = most_slots(M, E, GB_BM) * g.tiles_k, steps = projections * ((N + 63) / 64);
     g.dx = dx ? (tiles + 7) / 8 * 8 : 0;
+    g.db = db ? (E * projections * ((N + 63) / 64) + 7) / 8 * 8 : 0;
     g.dw = dw ? E * ((projections * g.tiles_n * g.tiles_k + 7) / 8 * 8) : 0;
     g.parts = 1;
     if (tiles > 0 && tiles <= 128) {
         g.parts = 256 / tiles;
-        if (g.parts > (steps + 3) / 4) g.parts = (steps + 3) / 4;
+        if (g.parts > (steps + 1) / 2) g.parts = (steps + 1) / 2;
     }
     return g;
 }
@@ -446,7 +454,7 @@ size_t grouped_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t E, bo
 
 bool grouped_backward_fits(int64_t M, int64_t K, int64_t N, int64_t E) {
     const GradGrid g = grad_grid(M, K, N, E, 2);
-    return grid_fits(g.parts * g.dx + g.dw, 512);
+    return grid_fits(g.all(true), 512);
 }
 
 hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) {
@@ -464,14 +472,14 @@ hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) 
         p.d0 = dg;
         p.d1 = du;
     }
-    const GradGrid g = grad_grid(a.M, a.K, a.N, a.E, a.w1 ? 2 : 1, a.dx && a.M > 0, a.dw0);
+    const GradGrid g = grad_grid(a.M, a.K, a.N, a.E, a.w1 ? 2 : 1, a.dx && a.M > 0, a.db0 || a.db1, a.dw0);
     if (a.dx && g.parts > 1) {
         p.parts = (int)g.parts;
         p.dx = reinterpret_cast<float*>(static_cast<char*>(a.ws) + gate_bytes(a.M, a.N, a.w1));
     }
-    if (g.dx + g.dw > 0) {
-        hipLaunchKernelGGL(k_grouped_gradients, dim3((unsigned)(p.parts * g.dx + g.dw)), dim3(512), 0, s, p, (int)g.dx, (int)g.tiles_k,
-                           (int)g.tiles_n);
+    const int64_t wgs = g.all(p.parts > 1);
+    if (wgs > 0) {
+        hipLaunchKernelGGL(k_grouped_gradients, dim3((unsigned)wgs), dim3(512), 0, s, p, (int)g.dx, (int)g.db, (int)g.tiles_k, (int)g.tiles_n);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -479,10 +487,6 @@ hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) 
         hipLaunchKernelGGL(k_grouped_dx_sum, dim3((unsigned)most_slots(a.M, a.E, 1), (unsigned)((a.K + 1023) / 1024)), dim3(256), 0, s, p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-    }
-    if (a.db0 || a.db1) {
-        hipLaunchKernelGGL(k_grouped_dbias, dim3((unsigned)((a.N + 63) / 64), (unsigned)a.E, a.w1 ? 2u : 1u), dim3(1024), 0, s, p);
-        return hipGetLastError();
     }
     return hipSuccess;
 }
