@@ -157,7 +157,7 @@ constexpr int EG_BF = 128, EG_BK = 128;
 
 // ACT 0: one projection, whose columns n0 + 128 .. are the second set.
 template <int ACT, bool ALIGNED, int FM>
-__global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int tiles_f) {
+__global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most_m, int tiles_f) {
     constexpr bool GATED = ACT != 0;
     constexpr int BM = 32 * FM, OB = BM * 8, UNITS = OB + 2 * EG_BF * 2;
     __shared__ i32x4 st0[UNITS];
@@ -169,6 +169,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int tile
     // of the tiles there are, a contiguous run for each XCD, four rows of tiles at a time
     int tiles_m;
     find_slot<BM, true>(a.offsets, (int)a.E, a.M, -1, &tiles_m);
+    tiles_m = min(tiles_m, most_m);                    // offsets that decrease may make more than were launched
     const int T = tiles_m * tiles_f, xcd = blockIdx.x & 7, per = T >> 3, rem = T & 7;
     if ((int)blockIdx.x >= T) return;
     int t = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
@@ -410,7 +411,7 @@ template <int ACT, bool ALIGNED, int FM>
 static hipError_t launch_grouped_gemm_fm(const GroupedArgs& a, hipStream_t s) {
     constexpr int COLUMNS = ACT ? EG_BF : 2 * EG_BF;
     const int64_t tm = most_slots(a, 32 * FM), tf = (a.N + COLUMNS - 1) / COLUMNS;
-    hipLaunchKernelGGL((k_grouped_gemm<ACT, ALIGNED, FM>), dim3((unsigned)(tm * tf)), dim3(256), 0, s, a, (int)tf);
+    hipLaunchKernelGGL((k_grouped_gemm<ACT, ALIGNED, FM>), dim3((unsigned)(tm * tf)), dim3(256), 0, s, a, (int)tm, (int)tf);
     return hipGetLastError();
 }
 

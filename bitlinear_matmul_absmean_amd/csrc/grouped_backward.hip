@@ -36,6 +36,7 @@ struct Products {
     GroupedBackwardArgs a;
     const float *d0, *d1;          // [M, N]: dy, or dg and du
     int parts;                     // of dx's sums
+    int slots;                     // most of its tiles of rows
     float* dx;                     // a.dx, or [parts, M, K] where there are several
 };
 
@@ -386,6 +387,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx
         b -= part * dx_wgs;
         int tiles_m;
         find_slot<GB_BM, true>(a.offsets, (int)a.E, a.M, -1, &tiles_m);
+        tiles_m = min(tiles_m, p.slots);               // offsets that decrease may make more than were launched
         const int T = tiles_m * tiles_k;
         if (b >= T) return;
         int t = run_of(b, T);
@@ -458,7 +460,7 @@ bool grouped_backward_fits(int64_t M, int64_t K, int64_t N, int64_t E) {
 }
 
 hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) {
-    Products p{a, a.dy, nullptr, 1, a.dx};
+    Products p{a, a.dy, nullptr, 1, (int)most_slots(a.M, a.E, GB_BM), a.dx};
     if (a.w1 && a.M > 0) {
         float* dg = reinterpret_cast<float*>(a.ws);
         float* du = dg + a.M * a.N;

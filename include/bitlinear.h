@@ -489,7 +489,8 @@ int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, i
  *   rows      [M] int64 token of each row, or NULL (then T == M).  A token may occur any number of
  *             times; an index outside 0 .. T - 1 reads a token of zeros (x_q = 0, beta = 0).  (in)
  *   offsets   [E + 1] int64, on the device, not decreasing, within 0 .. M; beyond, they are taken as
- *             0 or M, and a group that ends before it begins as empty.       (in)
+ *             0 or M, and a group that ends before it begins as empty.  Offsets that decrease, so that
+ *             groups share rows, leave unspecified values in the outputs and touch nothing else.  (in)
  *   W_packed  [E, N, K/4] uint8; alpha [E]; bias [E, N] or NULL.              (in)
  *   y         [M, N] fp32.                                                   (out)
  * K % 4 == 0, E <= 4096, N <= 2^20, M <= 2^24, and no more work than a launch holds (about 2^36 elements of y);

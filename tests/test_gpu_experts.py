@@ -269,6 +269,36 @@ def test_indices_and_offsets_out_of_range(dev, m):
     _check_gradients([dx, dw, db], values, terms, lengths, "range")
 
 
+@pytest.mark.parametrize("m,e", [(40, 9), (700, 60), (1 << 14, 4096)])
+def test_offsets_that_decrease_touch_nothing_else(dev, m, e):
+    """Groups that share rows make more tiles than were launched: outputs are unspecified, what lies around
+    them is not touched, and the next call is right."""
+    torch, bl = dev
+    rng = np.random.default_rng([19, m])
+    k, n = 64, 40
+    offsets = np.where(np.arange(e + 1) % 2 == 0, 0, m).astype(np.int64)
+    w, alpha, _ = _weights(rng, e, n, k, False)
+    x_q, beta = rng.integers(-127, 128, (m, k)).astype(np.int8), rng.uniform(0.5, 4, m).astype(F32)
+    dy = rng.standard_normal((m, n)).astype(F32)
+    xt, bt, ot, wt, at, dyt = [_t(torch, a) for a in (x_q, beta, offsets, _pack(w), alpha, dy)]
+
+    def between(*shape):
+        size = int(np.prod(shape))
+        buf = torch.full((size + 512,), 7.0, device="cuda")
+        return buf, buf[256:256 + size].view(shape)
+
+    bufs, (y, dx, dw, db) = zip(*[between(*s) for s in ((m, n), (m, k), (e, n, k), (e, n))])
+    bl.bitlinear_grouped_forward(xt, bt, ot, wt, at, y=y)
+    bl.bitlinear_grouped_backward(dyt, xt, bt, ot, wt, at, dx=dx, dW=dw, dbias=db)
+    torch.cuda.synchronize()
+    for b in bufs:
+        assert bool((b[:256] == 7).all()) and bool((b[-256:] == 7).all())
+    one = np.full(e + 1, m, np.int64)
+    one[0] = 0
+    y = bl.bitlinear_grouped_forward(xt[:33], bt[:33], _t(torch, np.minimum(one, 33)), wt, at)
+    assert np.array_equal(_np(y), experts_plain.forward(x_q[:33], beta[:33], np.minimum(one, 33), w, alpha, None, np.zeros((33, n), F32)))
+
+
 def test_no_rows(dev):
     torch, bl = dev
     e, k, n = 3, 64, 40
