@@ -19,7 +19,9 @@ __device__ __forceinline__ uint32_t e4m3_4(float a, float b, float c, float d) {
 // v / scale rounded as an IEEE division, clipped to +-448.  With y = fp32(1 / scale), q = fp32(v y) and the exact
 // remainder r = v - q scale, q + r y rounds to the quotient (Markstein).  r is exact where its bits lie above
 // 2^-149: for scales of at least 2^-80 and quotients of at least 2^-11; smaller quotients are a code of zero
-// either way.  Scales beyond take the division (which is three times the instructions).
+// either way.  Such a scale is absmax / 448 to within 2^-24 of it, so that no quotient is above 448 (1 + 2^-22),
+// which rounds to 448: the clip is left out.  Scales beyond take the division (three times the instructions) and
+// the clip.  NaN stays NaN in both.
 struct Divisor {
     float scale, y;
     bool fast;
@@ -32,9 +34,10 @@ __device__ __forceinline__ float quotient(float v, const Divisor& d) {
         q = v * d.y;
         q = __builtin_fmaf(__builtin_fmaf(-q, d.scale, v), d.y, q);
     } else {
-        q = d.scale > 0.0f ? v / d.scale : 0.0f;
+        q = d.scale > 0.0f ? v / d.scale : v != v ? v : 0.0f;
+        q = q > 448.0f ? 448.0f : q < -448.0f ? -448.0f : q;
     }
-    return fminf(fmaxf(q, -448.0f), 448.0f);
+    return q;
 }
 template <bool FAST>
 __device__ __forceinline__ uint32_t codes_4(float4 v, const Divisor& d) {

@@ -452,7 +452,8 @@ int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_
  * value 448, no infinities), one fp32 scale for each block of 128 along K:
  *     scale = fp32(absmax of the block / 448),  code = e4m3(clip(fp32(v / scale), -448, 448)),
  * rounded to nearest, ties to even.  A block of zeros (or whose scale is below the fp32 range) has
- * scale 0 and codes 0.  The last block of a row ends with the row.
+ * scale 0 and codes 0.  The last block of a row ends with the row.  NaN and infinities have the code
+ * NaN (and an infinity makes its block's scale infinite); the products with them are then not finite.
  *   quantize_act_fp8:      blocks of one token x 128; x [M, K] fp32 (in); x_q [M, K] e4m3,
  *                          x_scale [ceil(K / 128), M] fp32 (out): the tokens' scales of a block lie
  *                          together, as a tile of tokens reads them.

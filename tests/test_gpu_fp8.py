@@ -125,6 +125,41 @@ def test_quantizer_extremes(dev):
         assert np.array_equal(_values(q), want)
 
 
+@pytest.mark.parametrize("k", [128, 300, 1001])
+def test_what_is_not_finite_stays_so(dev, k):
+    """NaN and infinities have the code NaN, whatever else is in their block, and make the products of their
+    token, or of their channel, not finite; other blocks are as without them."""
+    torch, bl = dev
+    rng = np.random.default_rng([23, k])
+    m, n = 9, 140
+    x, w = _data(rng, m, k), _data(rng, n, k)
+    bad = x.copy()
+    bad[1, 5], bad[2, k - 1], bad[4, 0] = np.nan, np.inf, -np.inf
+    bad[6, :128] = 0
+    bad[6, 100] = np.nan                                            # alone in a block of zeros
+    bad[7, :] = np.nan
+    gone = ~np.isfinite(bad)
+    q, s = bl.bitlinear_quantize_act_fp8(_t(torch, bad))
+    assert np.isnan(_values(q)[gone]).all() and not np.isnan(_values(q)[~gone]).any()
+    want, scale = _quantize(x, 1)
+    rows = ~gone.any(axis=1)
+    assert np.array_equal(_values(q)[rows], want[rows]) and np.array_equal(s.cpu().numpy().T[rows], scale[rows])
+    w_q, ws = bl.bitlinear_quantize_weights_fp8(_t(torch, w))
+    for tokens in (m, 200):                                         # the streaming kernel and the tiles
+        qs, ss = q.view(torch.uint8).repeat(tokens // m + 1, 1)[:tokens].view(q.dtype), s.repeat(1, tokens // m + 1)[:, :tokens].contiguous()
+        y = bl.bitlinear_forward_fp8(qs.contiguous(), ss, w_q, ws).cpu().numpy()
+        there = np.resize(rows, (tokens // m + 1) * m)[:tokens]
+        assert np.isfinite(y[there]).all() and not np.isfinite(y[~there]).any()
+    wide = w.copy()
+    wide[3, k // 2] = np.nan
+    q2, _ = bl.bitlinear_quantize_weights_fp8(_t(torch, wide))
+    assert np.isnan(_values(q2)[3, k // 2]) and np.isnan(_values(q2)).sum() == 1
+    wide[3, k // 2] = -np.inf
+    q2, s2 = bl.bitlinear_quantize_weights_fp8(_t(torch, wide))
+    assert np.isnan(_values(q2)[3, k // 2]) and np.isnan(_values(q2)).sum() == 1
+    assert np.isinf(s2.cpu().numpy()).sum() == 1
+
+
 # ------------------------------------------------------------------------------------ the product
 PRODUCT = [(1, 1, 1), (1, 16, 5), (1, 128, 16), (1, 4096, 300), (1, 11008, 64), (1, 1001, 129), (1, 500, 33), (2, 256, 31),
            (7, 1024, 100), (15, 384, 128), (16, 2048, 256), (16, 130, 130), (17, 512, 48), (33, 1000, 65), (48, 1024, 512),
