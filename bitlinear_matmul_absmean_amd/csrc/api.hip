@@ -502,14 +502,14 @@ int bitlinear_grouped_gated_forward(const float* x, int64_t T, int64_t K, const 
     if (!g != !u || !known_activation(act)) return BITLINEAR_ERR_INVALID_ARG;
     int st = check_grouped(T, K, rows, M, E, F);
     if (st) return st;
+    const GroupedArgs a{x_q, beta, T, K, rows, M, offsets, E, Wg_packed, Wu_packed, alpha_g, alpha_u, bias_g, bias_u, F, act,
+                        h, g, u};
+    if (M > 0 && grouped_gemv_supports(a, x)) return hip_status(launch_grouped_gemv(a, x, x_q, beta, stream));
     if (T > 0) {
         st = hip_status(launch_quantize_act(x, T, K, x_q, beta, stream));
         if (st) return st;
     }
-    if (M == 0) return BITLINEAR_OK;
-    const GroupedArgs a{x_q, beta, T, K, rows, M, offsets, E, Wg_packed, Wu_packed, alpha_g, alpha_u, bias_g, bias_u, F, act,
-                        h, g, u};
-    return hip_status(launch_grouped(a, stream));
+    return M > 0 ? hip_status(launch_grouped(a, stream)) : BITLINEAR_OK;
 }
 
 // Workspace of a grouped backward call for valid sizes, else 0.

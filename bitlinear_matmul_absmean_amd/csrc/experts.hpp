@@ -89,6 +89,9 @@ struct GroupedArgs {
     float *g, *u;                  // gated: [M, N] or both null
 };
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t s);
+// The gated block of one token with x quantized in the same launch (xq and beta are written, not read).
+bool grouped_gemv_supports(const GroupedArgs& a, const float* x);
+hipError_t launch_grouped_gemv(const GroupedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s);
 
 struct GroupedBackwardArgs {
     const float* dy;               // [M, N]; gated: dh

@@ -9,13 +9,15 @@
 //
 // Every kernel gives the same lanes a gate row and the up row of the same column, so that the
 // product is formed where the sums end.  Three kernels:
-//   * one token in aligned rows: k_gated_gemv, which also quantizes x, on v_dot4_i32_i8;
+//   * one token in aligned rows: k_gated_gemv, which also quantizes x, on v_dot4_i32_i8 (and the same for one token
+//     under the projections of several experts);
 //   * up to 32 tokens, and more where a GEMM would have few tiles (64 of 64 tokens x 128 columns):
 //     k_gated_dec, the weight streams on the 16x16x64 int8 MFMA;
 //   * else: k_gated_gemm, LDS tiles on the 32x32x32 int8 MFMA;
 // the last two also in a form for any K % 4 == 0 and any alignment.
 #include <type_traits>
 
+#include "experts.hpp"
 #include "ffn.hpp"
 
 namespace bitlinear {
@@ -52,11 +54,21 @@ __device__ __forceinline__ void gated_store(const GatedArgs& a, int64_t at, int6
 // Bound: the weight stream on large layers (K = 8192, F = 28672: 23.0 us, 5.1 TB/s), a launch and one round
 // of loads on small ones (K = 4096, F = 11008: 8.0 us, 2.8 TB/s, six pairs of rows a wave; two BitLinear
 // calls and a product would take 11).
+// EXPERTS: the token under the projections of several experts, which lie one after the other: row m of h is of the
+// group that holds m.  `per` waves take a row, and each looks up the row's expert while x is on its way.  (Two of
+// eight experts, K = 4096, F = 11008: 12.7 us, 3.6 TB/s, against 16.9 for the quantizer and the streaming kernel of
+// grouped.hip; eight of 64, 2048 -> 1408: 8.5 against 8.8; 64 of 64: 31.2 against 33.6.)
 constexpr int GV_WAVES = 8;
 
-template <int CPL, int R>
+struct GatedRows {
+    const int64_t *rows, *offsets; // [M] or null, [E + 1]
+    int64_t M;
+    int E, per;
+};
+
+template <int CPL, int R, bool EXPERTS>
 __global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const float* __restrict__ x, int8_t* __restrict__ xq_out,
-                                                              float* __restrict__ beta_out, int pairs) {
+                                                              float* __restrict__ beta_out, int pairs, GatedRows ex) {
     constexpr int NT = 64 * GV_WAVES, FPT = CPL * 1024 / NT;        // float4s of x per thread, at most
     __shared__ u32x4 xs[CPL * 256];                                 // unit (chunk / 64, group of 16, lane)
     __shared__ float red_f[GV_WAVES];
@@ -65,11 +77,23 @@ __global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t K = a.K, rowb = K >> 2;
     const int C = (int)(K >> 6), k4 = (int)(K >> 2);
-    const int64_t rb = ((int64_t)blockIdx.x * GV_WAVES + wave) * pairs;
-    const int64_t re = rb + pairs < a.F ? rb + pairs : a.F;         // may be <= rb: no rows
     float4 xv[FPT];
 #pragma unroll
     for (int i = 0; i < FPT; ++i) xv[i] = reinterpret_cast<const float4*>(x)[tid + NT * i < k4 ? tid + NT * i : 0];
+    int64_t rb = ((int64_t)blockIdx.x * GV_WAVES + wave) * pairs, end = a.F, e = 0, m = 0;
+    bool there = true;
+    if constexpr (EXPERTS) {
+        const int at = (int)blockIdx.x * GV_WAVES + wave;
+        const Slot slot = find_slot<1, false>(ex.offsets, ex.E, ex.M, at / ex.per, nullptr);
+        rb = (int64_t)(at % ex.per) * pairs;
+        if (slot.rows == 0) end = 0;
+        e = slot.e;
+        m = slot.m0;
+        if (ex.rows && slot.rows) there = ex.rows[m] == 0;
+        a.wg += e * a.F * rowb;
+        a.wu += e * a.F * rowb;
+    }
+    const int64_t re = rb + pairs < end ? rb + pairs : end;         // may be <= rb: no rows
     // rows past the wave's range re-read its last row (not written); chunks past the row re-read
     // chunk 0, whose x_q there is zero
     u32x4 wg[R][CPL], wu[R][CPL];
@@ -122,7 +146,8 @@ __global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const
     int xsum = 0;
 #pragma unroll
     for (int w = 0; w < GV_WAVES; ++w) xsum += red_i[w];
-    const float scale_g = dequant_scale(a.ag[0], beta), scale_u = dequant_scale(a.au[0], beta);
+    const float scale_g = dequant_scale(a.ag[e], there ? beta : 0.0f), scale_u = dequant_scale(a.au[e], there ? beta : 0.0f);
+    const int some = there ? -1 : 0;                                // the sums of a token of zeros
     for (int64_t r0 = rb; r0 < re; r0 += R) {
         int sg[R], su[R];
 #pragma unroll
@@ -144,32 +169,36 @@ __global__ __launch_bounds__(64 * GV_WAVES) void k_gated_gemv(GatedArgs a, const
                 mu = tu;
             }
         }
-        if (lane < R && r0 + lane < re) gated_store(a, r0 + lane, r0 + lane, mg - xsum, mu - xsum, scale_g, scale_u);
+        if (lane < R && r0 + lane < re)
+            gated_store(a, m * a.F + r0 + lane, e * a.F + r0 + lane, (mg - xsum) & some, (mu - xsum) & some, scale_g, scale_u);
     }
 }
 
-template <int CPL, int R>
-static hipError_t launch_gated_gemv_r(const GatedArgs& a, const float* x, int8_t* xq, float* beta, int64_t pairs, hipStream_t s) {
-    const int64_t waves = (a.F + pairs - 1) / pairs;
-    hipLaunchKernelGGL((k_gated_gemv<CPL, R>), dim3((unsigned)((waves + GV_WAVES - 1) / GV_WAVES)), dim3(64 * GV_WAVES), 0, s, a, x,
-                       xq, beta, (int)pairs);
+template <int CPL, int R, bool EXPERTS>
+static hipError_t launch_gated_gemv_r(const GatedArgs& a, const float* x, int8_t* xq, float* beta, int64_t pairs, GatedRows ex,
+                                      hipStream_t s) {
+    ex.per = (int)((a.F + pairs - 1) / pairs);
+    const int64_t waves = (EXPERTS ? ex.M : 1) * ex.per;
+    hipLaunchKernelGGL((k_gated_gemv<CPL, R, EXPERTS>), dim3((unsigned)((waves + GV_WAVES - 1) / GV_WAVES)), dim3(64 * GV_WAVES), 0, s,
+                       a, x, xq, beta, (int)pairs, ex);
     return hipGetLastError();
 }
 
-// About 2048 waves: 256 workgroups, since every one of them quantizes x.  Rows of one chunk a lane: all of
+// About 2048 waves: 256 workgroups, since every one of them quantizes x (two of eight experts, K = 4096, F = 11008:
+// 12.7 us, 15.8 with 4096 waves).  Rows of one chunk a lane: all of
 // a wave's rows at once if they are at most six (K = 4096, F = 11008, six pairs a wave: 8.0 against 8.4 us
 // in steps of four; K = 2048, F = 8192, four: 5.3 against 6.7 us with room for six).  Longer rows: two pairs
 // of two chunks, one of more (K = 8192, F = 28672: 23.6 against 24.1 us with three; K = 16384, F = 4096: 11.2
 // against 12.0 with two).
-template <int CPL>
-static hipError_t launch_gated_gemv_cpl(const GatedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s) {
-    const int64_t pairs = (a.F + 2047) / 2048;
+template <int CPL, bool EXPERTS>
+static hipError_t launch_gated_gemv_cpl(const GatedArgs& a, const float* x, int8_t* xq, float* beta, const GatedRows& ex, hipStream_t s) {
+    const int64_t pairs = ((EXPERTS ? ex.M : 1) * a.F + 2047) / 2048;
     if constexpr (CPL > 1) {
-        return launch_gated_gemv_r<CPL, CPL == 2 ? 2 : 1>(a, x, xq, beta, pairs, s);
+        return launch_gated_gemv_r<CPL, CPL == 2 ? 2 : 1, EXPERTS>(a, x, xq, beta, pairs, ex, s);
     } else {
-        if (pairs <= 2) return launch_gated_gemv_r<1, 2>(a, x, xq, beta, pairs, s);
-        if (pairs <= 4 || pairs > 6) return launch_gated_gemv_r<1, 4>(a, x, xq, beta, pairs, s);
-        return launch_gated_gemv_r<1, 6>(a, x, xq, beta, pairs, s);
+        if (pairs <= 2) return launch_gated_gemv_r<1, 2, EXPERTS>(a, x, xq, beta, pairs, ex, s);
+        if (pairs <= 4 || pairs > 6) return launch_gated_gemv_r<1, 4, EXPERTS>(a, x, xq, beta, pairs, ex, s);
+        return launch_gated_gemv_r<1, 6, EXPERTS>(a, x, xq, beta, pairs, ex, s);
     }
 }
 
@@ -178,13 +207,29 @@ bool gated_gemv_supports(const GatedArgs& a, const float* x) {
            (uintptr_t)a.wu % 16 == 0;
 }
 
-hipError_t launch_gated_gemv(const GatedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s) {
+template <bool EXPERTS>
+static hipError_t launch_gated_gemv(const GatedArgs& a, const float* x, int8_t* xq, float* beta, const GatedRows& ex, hipStream_t s) {
     switch ((a.K / 64 + 63) / 64) {
-        case 1: return launch_gated_gemv_cpl<1>(a, x, xq, beta, s);
-        case 2: return launch_gated_gemv_cpl<2>(a, x, xq, beta, s);
-        case 3: return launch_gated_gemv_cpl<3>(a, x, xq, beta, s);
-        default: return launch_gated_gemv_cpl<4>(a, x, xq, beta, s);
+        case 1: return launch_gated_gemv_cpl<1, EXPERTS>(a, x, xq, beta, ex, s);
+        case 2: return launch_gated_gemv_cpl<2, EXPERTS>(a, x, xq, beta, ex, s);
+        case 3: return launch_gated_gemv_cpl<3, EXPERTS>(a, x, xq, beta, ex, s);
+        default: return launch_gated_gemv_cpl<4, EXPERTS>(a, x, xq, beta, ex, s);
     }
+}
+
+hipError_t launch_gated_gemv(const GatedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s) {
+    return launch_gated_gemv<false>(a, x, xq, beta, GatedRows{nullptr, nullptr, 0, 0, 0}, s);
+}
+
+// A row of its own for each expert at most: more rows than experts are better multiplied together.
+bool grouped_gemv_supports(const GroupedArgs& a, const float* x) {
+    return a.T == 1 && a.M <= a.E && a.K % 64 == 0 && a.K <= 16384 && (uintptr_t)x % 16 == 0 && (uintptr_t)a.w0 % 16 == 0 &&
+           (uintptr_t)a.w1 % 16 == 0;
+}
+
+hipError_t launch_grouped_gemv(const GroupedArgs& a, const float* x, int8_t* xq, float* beta, hipStream_t s) {
+    const GatedArgs b{xq, beta, 1, a.K, a.N, a.w0, a.w1, a.al0, a.al1, a.b0, a.b1, a.act, a.y, a.g, a.u};
+    return launch_gated_gemv<true>(b, x, xq, beta, GatedRows{a.rows, a.offsets, a.M, (int)a.E, 0}, s);
 }
 
 // ---- few tokens or few tiles ----------------------------------------------------------------

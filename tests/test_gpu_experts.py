@@ -158,6 +158,48 @@ def test_gated_forward(dev, case):
     assert np.array_equal(_bits(_np(buf)[1:1 + m * f].reshape(m, f)), _bits(h)) and float(buf[0]) == 7 and np.all(_np(buf)[1 + m * f:] == 7)
 
 
+# experts' rows of the one token, K, F, rows of none before and behind, rows whose token is not there
+ONE = [([1], 64, 1, 0, 0, []), ([0, 1, 0, 1], 4096, 2500, 0, 0, []), ([1, 0, 0, 1, 1, 0, 0, 0], 1024, 100, 1, 1, [2]),
+       ([0, 2, 0, 1], 4160, 333, 0, 1, [0]), ([0] * 70 + [1] + [0] * 29 + [2], 2048, 5000, 1, 0, [3]), ([1, 0, 1], 8256, 40, 0, 0, [0, 1]),
+       ([0, 0, 1], 16384, 77, 0, 2, []), ([1] * 64, 640, 256, 0, 0, [5, 63]), ([0, 3, 0], 192, 3000, 0, 0, [])]
+
+
+@pytest.mark.parametrize("case", ONE, ids=_name)
+@pytest.mark.parametrize("act", ACTS)
+def test_one_token(dev, case, act):
+    """The gated block of one token, quantized in the launch that multiplies it."""
+    torch, bl = dev
+    counts, k, f, before, behind, gone = case
+    rng = np.random.default_rng([29, len(counts), k, f])
+    offsets = (before + np.concatenate([[0], np.cumsum(counts)])).astype(np.int64)
+    e, m = len(counts), int(offsets[-1]) + behind
+    rows = np.zeros(m, np.int64)
+    rows[gone] = [1, -1, 1 << 33][: len(gone)]
+    wg, ag, bg = _weights(rng, e, f, k, act != "gelu")
+    wu, au, bu = _weights(rng, e, f, k, True)
+    x = rng.standard_normal((1, k)).astype(F32)
+    x[0, k // 2] = 20
+    h, g, u = (torch.full((m, f), 7.0, device="cuda") for _ in range(3))
+    x_q, beta = torch.empty((1, k), dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
+    args = [_t(torch, a) for a in (x, offsets, _pack(wg), ag, _pack(wu), au)] + [_code(bl, act)]
+    kw = dict(rows=_t(torch, rows) if gone or m > 1 else None, bias_g=_t(torch, bg), bias_u=_t(torch, bu))
+    bl.bitlinear_grouped_gated_forward(*args, h=h, g=g, u=u, x_q=x_q, beta=beta, **kw)
+    h2 = torch.full((m, f), 7.0, device="cuda")
+    bl.bitlinear_grouped_gated_forward(*args, h=h2, **kw)
+    xq_p, beta_p = plain.absmax(x)
+    assert np.array_equal(_np(x_q), xq_p) and np.array_equal(_bits(_np(beta)), _bits(beta_p))
+    xr, br = experts_plain.tokens(xq_p, beta_p, rows, m)
+    seven = np.full((m, f), 7, F32)
+    g_p = experts_plain.forward(xr, br, offsets, wg, ag, bg, seven)
+    u_p = experts_plain.forward(xr, br, offsets, wu, au, bu, seven)
+    assert np.array_equal(_np(g), g_p) and np.array_equal(_np(u), u_p)
+    lo, hi = before, m - behind
+    ref = plain.activation(g_p, act)[0] * u_p.astype(np.float64)
+    h, n = _np(h), {"silu": 8, "gelu": 2, "relu2": 2}[act]                  # as in test_gated_forward
+    assert np.all(np.abs(h - ref)[lo:hi] <= 1.01 * n * U * np.abs(ref)[lo:hi] + 1e-37)
+    assert np.all(h[:lo] == 7) and np.all(h[hi:] == 7) and np.array_equal(_bits(_np(h2)), _bits(h))
+
+
 def _check_gradients(got, values, terms, lengths, note):
     for i, (a, v, t, l) in enumerate(zip(got, values, terms, lengths)):
         if a is None:
