@@ -38,6 +38,7 @@ struct Products {
     int parts;                     // of dx's sums
     int slots;                     // most of its tiles of rows
     float* dx;                     // a.dx, or [parts, M, K] where there are several
+    bool whole;                    // dW's rows are whole pieces of 64 bytes
 };
 
 // ---- the two products -----------------------------------------------------------------------
@@ -64,6 +65,7 @@ __device__ __forceinline__ global_bytes scalar_base(const void* p) {
     asm("" : "+s"(b));                                 // keeps the sum with the lane's offset out of vector registers
     return (global_bytes)b;
 }
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32u __attribute__((aligned(1)));
 
@@ -181,21 +183,48 @@ __device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, int 
     if (s < steps) step(st0, st1, s, f);
 }
 
-// `rows` rows of a tile of `out` (row length K, columns from k0) from a wave's accumulators.
-__device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, int rows, int64_t k0, const f32x16 (&acc)[GB_NJ]) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t k = k0 + 128 * (wave & 1) + 4 * (lane & 31);
+// Rows m0 .. of the wave's 32 x 128 block, as far as `rows`, and columns from k.  STREAM: past the caches, which
+// keeps d, x_q and the codes there (2048 tokens x 2 of 8 experts, 2816 -> 2048: 291 -> 271 us; 256 rows of 16 experts: 97
+// -> 82), for rows of whole pieces of 64 bytes: others are written in parts (256 rows of 16 experts, N = 2048: K = 1008
+// 39.5 against 40.6 us cached, K = 1004 49.5 against 39.2).
+template <bool STREAM>
+__device__ __forceinline__ void block_store(float* __restrict__ out, int64_t K, int m0, int rows, int64_t k, const f32x16 (&acc)[GB_NJ]) {
+    const int lane = threadIdx.x & 63;
+    k += 4 * (lane & 31);
     if (k >= K) return;                                // K is a multiple of 4
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        const int m = 32 * (wave >> 1) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        const int m = m0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
         const f32x4u v = {acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
-        if (m < rows) *reinterpret_cast<f32x4u*>(out + (int64_t)m * K + k) = v;
+        if (m < rows) {
+            if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<f32x4u*>(out + (int64_t)m * K + k));
+            else *reinterpret_cast<f32x4u*>(out + (int64_t)m * K + k) = v;
+        }
     }
+}
+
+// `rows` rows of a tile of `out` (row length K, columns from k0) from a wave's accumulators.
+template <bool STREAM>
+__device__ __forceinline__ void grad_store(float* __restrict__ out, int64_t K, int rows, int64_t k0, const f32x16 (&acc)[GB_NJ]) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    block_store<STREAM>(out, K, 32 * (wave >> 1), rows, k0 + 128 * (wave & 1), acc);
 }
 
 // LDS row of k 4 c + j of the tile (c a lane, j < 4).
 __device__ __forceinline__ int grad_row(int c, int j) { return 128 * (c >> 5) + 32 * j + (c & 31); }
+
+// bf16 values of code j (of a byte's four) of eight rows: from tables of the upper and lower bytes.
+__device__ __forceinline__ u32x4 code_values(const uint32_t (&codes)[2], int j) {
+    u32x4 o;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t c = (codes[h] >> (2 * j)) & 0x03030303u;
+        const uint32_t hi = __builtin_amdgcn_perm(0u, 0x003F00BFu, c), lo = __builtin_amdgcn_perm(0u, 0x00800080u, c);
+        o[2 * h] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+        o[2 * h + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+    }
+    return o;
+}
 
 template <bool SHORT, bool FEW>
 __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st1, const Slot& slot, int64_t k0, int part) {
@@ -259,15 +288,7 @@ __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st
                 codes[h] = ((w[4 * h] | w[4 * h + 1] << 8 | w[4 * h + 2] << 16 | w[4 * h + 3] << 24) & keep) | (0x55555555u & ~keep);
             }
         }
-        // the codes' bf16 values from tables of the upper and lower bytes
-        u32x4 o;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t c = (codes[h] >> (2 * j)) & 0x03030303u;
-            const uint32_t hi = __builtin_amdgcn_perm(0u, 0x003F00BFu, c), lo = __builtin_amdgcn_perm(0u, 0x00800080u, c);
-            o[2 * h] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-            o[2 * h + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-        }
+        const u32x4 o = code_values(codes, j);
         const int k = grad_row(lane, j);
         st[GB_OB + k * 8 + (wave ^ grad_swizzle(k))] = o;
     };
@@ -275,7 +296,7 @@ __device__ __forceinline__ void dx_tile(const Products& p, u32x4* st0, u32x4* st
 #pragma unroll
     for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
     grad_sum<FEW>(st0, st1, steps, 64 * steps, slot.rows, acc, load, put);
-    grad_store(p.dx + (part * a.M + slot.m0) * a.K, a.K, slot.rows, k0, acc);
+    grad_store<true>(p.dx + (part * a.M + slot.m0) * a.K, a.K, slot.rows, k0, acc);
 }
 
 __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st1, int64_t e, bool second, int64_t n0, int64_t k0) {
@@ -349,11 +370,15 @@ __device__ __forceinline__ void dw_tile(const Products& p, u32x4* st0, u32x4* st
 #pragma unroll
     for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
     grad_sum<false>(st0, st1, steps, rows, GB_BM, acc, load, put);
-    grad_store((second ? a.dw1 : a.dw0) + (e * N + n0) * K, K, (int)(N - n0 < GB_BM ? N - n0 : GB_BM), k0, acc);
+    float* out = (second ? a.dw1 : a.dw0) + (e * N + n0) * K;
+    const int there = (int)(N - n0 < GB_BM ? N - n0 : GB_BM);
+    if (p.whole) grad_store<true>(out, K, there, k0, acc);
+    else grad_store<false>(out, K, there, k0, acc);
 }
 
-// Bias gradients of 64 columns of an expert: eight rows at a time, sums in fp64 in a fixed order.
-__device__ __forceinline__ void dbias_tile(const Products& p, u32x4* lds, int64_t e, bool second, int64_t n0) {
+// Bias gradients of 64 columns of an expert: a row a wave at a time, sums in fp64 in a fixed order.
+template <int WAVES>
+__device__ __forceinline__ void dbias_tile(const Products& p, void* lds, int64_t e, bool second, int64_t n0) {
     const GroupedBackwardArgs& a = p.a;
     float* db = second ? a.db1 : a.db0;
     if (!db) return;
@@ -364,12 +389,12 @@ __device__ __forceinline__ void dbias_tile(const Products& p, u32x4* lds, int64_
     const Group g = group_rows(a.offsets, e, a.M);
     double sum = 0.0;
 #pragma unroll 8
-    for (int64_t m = g.lo + wave; m < g.hi; m += 8) sum += (double)d[m * a.N];
+    for (int64_t m = g.lo + wave; m < g.hi; m += WAVES) sum += (double)d[m * a.N];
     part[64 * wave + lane] = sum;
     __syncthreads();
     if (wave != 0 || n >= a.N) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) sum += part[64 * w + lane];
+    for (int w = 1; w < WAVES; ++w) sum += part[64 * w + lane];
     db[e * a.N + n] = (float)sum;
 }
 
@@ -400,7 +425,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx
         else dx_tile<false, false>(p, st0, st1, slot, k0, part);
     } else if (b -= p.parts * dx_wgs; b < db_wgs) {
         const int per = (int)((a.N + 63) / 64), two = a.w1 ? 2 : 1, t = b / per;
-        if (t < (int)a.E * two) dbias_tile(p, st0, t / two, t % two != 0, (int64_t)(b % per) * 64);
+        if (t < (int)a.E * two) dbias_tile<8>(p, st0, t / two, t % two != 0, (int64_t)(b % per) * 64);
     } else {
         const int T = (a.w1 ? 2 : 1) * tiles_n * tiles_k, T8 = (T + 7) & ~7;
         b -= db_wgs;
@@ -408,6 +433,201 @@ __global__ __launch_bounds__(512, 2) void k_grouped_gradients(Products p, int dx
         const int t = run_of(b % T8, T), tn = t / tiles_k % tiles_n;
         dw_tile(p, st0, st1, b / T8, t >= tiles_n * tiles_k, (int64_t)tn * GB_BM, (int64_t)(t % tiles_k) * GB_BN);
     }
+}
+
+// ---- short groups ----------------------------------------------------------------------------
+// Waves on their own, with operands straight into registers: no stages, no barriers, so that several workgroups share
+// a compute unit and many loads and stores are under way at once.
+//
+// dx: a workgroup of four waves takes 32 rows x 128 k and a part of the sum, each wave a quarter of the part's steps
+// of 16 n; the quarters are added at the end.  A lane reads eight n of its row of d, and the byte of four k of eight
+// rows of codes.  Past the sum's end as in dx_tile.
+template <bool NARROW>
+__device__ __forceinline__ void dx_short(const Products& p, f32x4* lds, const Slot& slot, int64_t k0, int part) {
+    const GroupedBackwardArgs& a = p.a;
+    const int lane = threadIdx.x & 63, lr = lane & 31, lg = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t N = a.N, rowb = a.K >> 2, e = slot.e;
+    const int per = (int)((N + 15) / 16), all = per * (a.w1 ? 2 : 1), at = 4 * part + wave;
+    const int first = (int)((int64_t)all * at / (4 * p.parts)), end = (int)((int64_t)all * (at + 1) / (4 * p.parts));
+    const int64_t row = (slot.m0 + min(lr, slot.rows - 1)) * N, byte = min((k0 >> 2) + lr, rowb - 1);
+    const float al[2] = {a.al0[e], a.w1 ? a.al1[e] : 0.0f};
+    struct Part {
+        float v[8];
+        uint32_t w[8];
+    };
+    auto load = [&](int s) {
+        Part f;
+        const bool second = s >= per;
+        const int64_t begin = (int64_t)(second ? s - per : s) * 16, n0 = (NARROW ? 0 : min(begin, N - 16)) + 8 * lg;
+        const float* d = (second ? p.d1 : p.d0) + row + n0;
+        const uint8_t* w = (second ? a.w1 : a.w0) + (e * N + n0) * rowb + byte;
+        if constexpr (!NARROW) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x4u x = *reinterpret_cast<const f32x4u*>(d + 4 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f.v[4 * i + j] = x[j];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f.w[i] = w[i * rowb];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool there = n0 + i < N;
+                f.v[i] = there ? d[i] : 0.0f;
+                f.w[i] = there ? w[i * rowb] : 0x55u;
+            }
+        }
+        return f;
+    };
+    f32x16 acc[GB_NJ];
+#pragma unroll
+    for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
+    auto multiply = [&](const Part& f, int s) {
+        const bool second = s >= per;
+        const float alpha = second ? al[1] : al[0];
+        u32x4 pl[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_2(f.v[2 * i] * alpha, f.v[2 * i + 1] * alpha, i, pl);
+        uint32_t codes[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) codes[h] = f.w[4 * h] | f.w[4 * h + 1] << 8 | f.w[4 * h + 2] << 16 | f.w[4 * h + 3] << 24;
+        const int64_t begin = (int64_t)(second ? s - per : s) * 16;
+        if (!NARROW && begin > N - 16) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int gone = (int)(begin - (N - 16)) - 8 * lg - 4 * h;
+                const uint32_t keep = gone >= 4 ? 0u : gone > 0 ? ~0u << 8 * gone : ~0u;
+                codes[h] = (codes[h] & keep) | (0x55555555u & ~keep);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < GB_NJ; ++j) {
+            const u32x4 o = code_values(codes, j);
+#pragma unroll
+            for (int q = 2; q >= 0; --q)
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, pl[q]), __builtin_bit_cast(bf16x8, o), acc[j], 0, 0, 0);
+        }
+    };
+    if (first < end) {
+        Part f = load(first);
+        for (int s = first; s < end; ++s) {
+            const Part next = load(min(s + 1, end - 1));
+            multiply(f, s);
+            f = next;
+        }
+    }
+    // waves 2 and 3 to 0 and 1, then 1 to 0
+#pragma unroll
+    for (int half = 2; half >= 1; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                f32x4 v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = acc[c >> 2][4 * (c & 3) + i];
+                lds[((wave - half) * 16 + c) * 64 + lane] = v;
+            }
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const f32x4 v = lds[(wave * 16 + c) * 64 + lane];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[c >> 2][4 * (c & 3) + i] += v[i];
+            }
+        }
+        if (half > 1) __syncthreads();
+    }
+    if (wave == 0) block_store<true>(p.dx + (part * a.M + slot.m0) * a.K, a.K, 0, slot.rows, k0, acc);
+}
+
+// dW: a wave computes 32 n x 128 k, sixteen rows at a time: a lane reads its column n of eight rows of d, and four k of
+// eight rows of x_q.
+__device__ __forceinline__ void dw_short(const Products& p, int64_t e, bool second, int64_t n0, int64_t k0) {
+    const GroupedBackwardArgs& a = p.a;
+    const int lane = threadIdx.x & 63, lr = lane & 31, lg = lane >> 5;
+    const int64_t N = a.N, K = a.K;
+    const Group g = group_rows(a.offsets, e, a.M);
+    const int rows = g.hi > g.lo ? (int)(g.hi - g.lo) : 0;
+    const float* d = (second ? p.d1 : p.d0) + g.lo * N + min(n0 + lr, N - 1);
+    const int8_t* x = a.xq + min(k0 + 4 * lr, K - 4);
+    f32x16 acc[GB_NJ];
+#pragma unroll
+    for (int j = 0; j < GB_NJ; ++j) acc[j] = f32x16{};
+    for (int m0 = 0; m0 < rows; m0 += 16) {
+        float v[8], beta[8];
+        uint32_t c[8];
+        int64_t token[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int m = min(m0 + 8 * lg + i, rows - 1);
+            token[i] = a.rows ? a.rows[g.lo + m] : g.lo + m;
+            v[i] = d[(int64_t)m * N];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool there = token[i] >= 0 && token[i] < a.T;
+            const int64_t r = there ? token[i] : 0;
+            beta[i] = there && m0 + 8 * lg + i < rows ? a.beta[r] : 0.0f;
+            __builtin_memcpy(&c[i], x + r * K, 4);
+        }
+        u32x4 pl[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_2(v[2 * i] * (beta[2 * i] / 127.0f), v[2 * i + 1] * (beta[2 * i + 1] / 127.0f), i, pl);
+#pragma unroll
+        for (int j = 0; j < GB_NJ; ++j) {
+            u32x4 o;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float lo = (float)(int8_t)(c[i] >> (8 * j)), hi = (float)(int8_t)(c[i + 1] >> (8 * j));
+                o[i >> 1] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+            }
+#pragma unroll
+            for (int q = 2; q >= 0; --q)
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, pl[q]), __builtin_bit_cast(bf16x8, o), acc[j], 0, 0, 0);
+        }
+    }
+    float* out = (second ? a.dw1 : a.dw0) + (e * N + n0) * K;
+    const int there = (int)(N - n0 < 32 ? N - n0 : 32);
+    if (p.whole) block_store<true>(out, K, 0, there, k0, acc);
+    else block_store<false>(out, K, 0, there, k0, acc);
+}
+
+// All gradients of short groups: dx's tiles, the bias gradients, dW's tiles, a tile a wave.
+struct ShortGrid {
+    int slots, dx, db, tiles_k, tiles_n;               // slots of 32 rows; workgroups of dx (each part) and db
+};
+__global__ __launch_bounds__(256, 4) void k_grouped_gradients_short(Products p, ShortGrid g) {
+    __shared__ f32x4 lds[2048];
+    const GroupedBackwardArgs& a = p.a;
+    int b = blockIdx.x;
+    if (b < p.parts * g.dx) {
+        const int part = b / g.dx;
+        b -= part * g.dx;
+        const Slot slot = find_slot<32, false>(a.offsets, (int)a.E, a.M, b / g.tiles_k, nullptr);
+        if (slot.rows == 0) return;
+        const int64_t k0 = (int64_t)(b % g.tiles_k) * 128;
+        if (a.N < 16) dx_short<true>(p, lds, slot, k0, part);
+        else dx_short<false>(p, lds, slot, k0, part);
+        return;
+    }
+    b -= p.parts * g.dx;
+    const int two = a.w1 ? 2 : 1;
+    if (b < g.db) {
+        const int per = (int)((a.N + 63) / 64), t = b / per;
+        dbias_tile<4>(p, lds, t / two, t % two != 0, (int64_t)(b % per) * 64);
+        return;
+    }
+    const int64_t per = (int64_t)g.tiles_n * g.tiles_k;
+    int64_t t = (int64_t)(b - g.db) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t e = t / (per * two);
+    if (e >= a.E) return;
+    t -= e * per * two;
+    const bool second = t >= per;
+    if (second) t -= per;
+    dw_short(p, e, second, t / g.tiles_k * 32, t % g.tiles_k * 128);
 }
 
 // dx from its parts, in their order: a row of a group x 1024 columns a workgroup.
@@ -428,18 +648,38 @@ __global__ __launch_bounds__(256) void k_grouped_dx_sum(Products p) {
 // Workgroups of both products and the bias gradients: dx's of a part, db and dW's, all but dW's multiples of the XCDs;
 // and the parts that dx's sums are cut into where its tiles are too few to fill the card.
 struct GradGrid {
-    int64_t dx, db, dw, tiles_k, tiles_n, parts;
+    int64_t dx, db, dw, slots, tiles_k, tiles_n, parts;
+    bool is_short;
     int64_t all(bool split) const { return (split ? parts : 1) * dx + db + dw; }
 };
+// Short groups: at most 32 rows an expert, on average.  Microseconds, the kernel of short groups against tiles of
+// 128 x 256:  8 experts 2816 -> 2048: 32 rows 58 / 66, 64 rows 88 / 81;  16 experts 1024 -> 1024: 40 rows 34 / 37, 75
+// rows 53 / 43;  8 experts gated 1024 -> 1408: 50 rows 55 / 50;  5 experts gated 1024 -> 2731: 24 rows 44 / 55.
+// Parts of dx's sum: about 1024 workgroups, with at least eight steps of 16 n a wave (53 experts 564 -> 230: one part
+// 26 us, two and their sum 31;  16 experts gated 2048 -> 2816 of four rows: three parts 171, one 219).
+constexpr int64_t SHORT_ROWS = 32, SHORT_WGS = 1024;
 static GradGrid grad_grid(int64_t M, int64_t K, int64_t N, int64_t E, int projections, bool dx = true, bool db = true, bool dw = true) {
     GradGrid g;
-    g.tiles_k = (K + GB_BN - 1) / GB_BN;
-    g.tiles_n = (N + GB_BM - 1) / GB_BM;
-    const int64_t tiles = most_slots(M, E, GB_BM) * g.tiles_k, steps = projections * ((N + 63) / 64);
-    g.dx = dx ? (tiles + 7) / 8 * 8 : 0;
-    g.db = db ? (E * projections * ((N + 63) / 64) + 7) / 8 * 8 : 0;
-    g.dw = dw ? E * ((projections * g.tiles_n * g.tiles_k + 7) / 8 * 8) : 0;
+    g.is_short = M <= SHORT_ROWS * E;
+    const int64_t rows = g.is_short ? 32 : GB_BM, columns = g.is_short ? 128 : GB_BN, n = g.is_short ? 32 : GB_BM, of = g.is_short ? 16 : 64;
+    g.tiles_k = (K + columns - 1) / columns;
+    g.tiles_n = (N + n - 1) / n;
+    g.slots = most_slots(M, E, rows);
+    const int64_t tiles = g.slots * g.tiles_k, steps = projections * ((N + of - 1) / of);
+    g.dx = dx ? (g.is_short ? tiles : (tiles + 7) / 8 * 8) : 0;
+    g.db = db ? E * projections * ((N + 63) / 64) : 0;
+    g.dw = dw ? E * projections * g.tiles_n * g.tiles_k : 0;
     g.parts = 1;
+    if (g.is_short) {
+        g.dw = (g.dw + 3) / 4;
+        if (tiles > 0 && tiles <= SHORT_WGS / 2) {
+            g.parts = SHORT_WGS / tiles;
+            if (g.parts > (steps + 31) / 32) g.parts = (steps + 31) / 32;
+        }
+        return g;
+    }
+    g.db = (g.db + 7) / 8 * 8;
+    g.dw = dw ? E * ((projections * g.tiles_n * g.tiles_k + 7) / 8 * 8) : 0;
     if (tiles > 0 && tiles <= 128) {
         g.parts = 256 / tiles;
         if (g.parts > (steps + 1) / 2) g.parts = (steps + 1) / 2;
@@ -456,11 +696,12 @@ size_t grouped_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t E, bo
 
 bool grouped_backward_fits(int64_t M, int64_t K, int64_t N, int64_t E) {
     const GradGrid g = grad_grid(M, K, N, E, 2);
-    return grid_fits(g.all(true), 512);
+    return grid_fits(g.all(true), g.is_short ? 256 : 512);
 }
 
 hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) {
-    Products p{a, a.dy, nullptr, 1, (int)most_slots(a.M, a.E, GB_BM), a.dx};
+    Products p{a, a.dy, nullptr, 1, (int)most_slots(a.M, a.E, GB_BM), a.dx,
+               a.K % 16 == 0 && ((uintptr_t)a.dw0 | (uintptr_t)a.dw1) % 64 == 0};
     if (a.w1 && a.M > 0) {
         float* dg = reinterpret_cast<float*>(a.ws);
         float* du = dg + a.M * a.N;
@@ -481,7 +722,12 @@ hipError_t launch_grouped_backward(const GroupedBackwardArgs& a, hipStream_t s) 
     }
     const int64_t wgs = g.all(p.parts > 1);
     if (wgs > 0) {
-        hipLaunchKernelGGL(k_grouped_gradients, dim3((unsigned)wgs), dim3(512), 0, s, p, (int)g.dx, (int)g.db, (int)g.tiles_k, (int)g.tiles_n);
+        const dim3 grid((unsigned)wgs);
+        if (g.is_short)
+            hipLaunchKernelGGL(k_grouped_gradients_short, grid, dim3(256), 0, s, p,
+                               ShortGrid{(int)g.slots, (int)g.dx, (int)g.db, (int)g.tiles_k, (int)g.tiles_n});
+        else
+            hipLaunchKernelGGL(k_grouped_gradients, grid, dim3(512), 0, s, p, (int)g.dx, (int)g.db, (int)g.tiles_k, (int)g.tiles_n);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -288,6 +288,23 @@ def test_gated_backward(dev, case):
     assert torch.equal(dx2[lo:hi], dx[lo:hi]) and torch.equal(a2, dws[0]) and torch.equal(b2, dws[1])
 
 
+# tiles of 128 rows with sums shorter than a step, of one step, cut into parts; short groups beside a long one, sums
+# in parts, sums shorter than a step
+MORE = [([100, 3], 64, 40, True, 0, 0), ([200], 256, 7, False, 0, 0), ([90, 0, 60], 1000, 63, True, 1, 1), ([129, 70], 516, 64, False, 0, 0),
+        ([65, 64], 1024, 2500, True, 0, 0), ([20] * 3, 512, 2100, True, 0, 0), ([150] + [0] * 7, 132, 200, False, 2, 2),
+        ([33, 31, 1, 0], 2048, 15, True, 0, 0), ([32, 32], 260, 16, False, 0, 0), ([17], 8, 17, True, 0, 0), ([4] * 9, 400, 1031, True, 0, 1)]
+
+
+@pytest.mark.parametrize("case", MORE, ids=_name)
+def test_backward_of_other_tiles(dev, case):
+    test_backward(dev, case)
+
+
+@pytest.mark.parametrize("case", MORE, ids=_name)
+def test_gated_backward_of_other_tiles(dev, case):
+    test_gated_backward(dev, case)
+
+
 @pytest.mark.parametrize("m", [40, 400])
 def test_indices_and_offsets_out_of_range(dev, m):
     """Tokens that are not there are zeros; offsets beyond the rows are taken as their ends."""
