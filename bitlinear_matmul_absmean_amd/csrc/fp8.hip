@@ -198,25 +198,26 @@ __device__ __forceinline__ void fp8_store(const Fp8Args& a, int64_t m, int64_t n
 }
 
 // ---- few tokens -----------------------------------------------------------------------------
-// A workgroup of eight waves computes 16 MT tokens x 16 RB channels; wave w takes the blocks of 128 k
+// A workgroup of eight waves computes 16 MT tokens x 16 channels; wave w takes the blocks of 128 k
 // w, w + 8, ..., and the eight partial tiles are added at the end, in the waves' order.  Operands go straight
 // into registers, two blocks ahead.
 // 16x16x32 lane layout: A/B lane l holds row/column l % 16 and eight values of k (the same assignment of k to
 // lanes and bytes serves both, so any will do); accumulator r of lane l is row 4 (l / 16) + r, column l % 16.
 constexpr int FD_WAVES = 8;
 
-template <int ROWS, int MT, int RB>
+template <int ROWS, int MT>
 __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices) {
     constexpr bool DWORDS = ROWS == ROWS_1;
     __shared__ f32x4 part[FD_WAVES * MT * 64];
     const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t K = a.K;
-    const int64_t m0 = (int64_t)(blockIdx.x % slices) * (16 * MT), n0 = (int64_t)(blockIdx.x / slices) * (16 * RB);
-    const int rows_m = (int)(a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT), rows_n = (int)(a.N - n0 < 16 * RB ? a.N - n0 : 16 * RB);
+    const int64_t m0 = (int64_t)(blockIdx.x % slices) * (16 * MT), n0 = (int64_t)(blockIdx.x / slices) * 16;
+    const int rows_m = (int)(a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT), rows_n = (int)(a.N - n0 < 16 ? a.N - n0 : 16);
     const int blocks = (int)((K + 127) / 128), whole = (int)(K / 128);
-    const float* ws = a.ws + n0 / 128 * blocks;                 // 16 RB divides 128
-    const uint8_t *xp[MT], *wp[RB];
+    const float* ws = a.ws + n0 / 128 * blocks;
+    const uint8_t* xp[MT];
+    const uint8_t* wp = a.wq + (n0 + min(lr, rows_n - 1)) * K;
     const float* xs[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -224,10 +225,8 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
         xp[t] = a.xq + m * K;
         xs[t] = a.xs + m;
     }
-#pragma unroll
-    for (int r = 0; r < RB; ++r) wp[r] = a.wq + (n0 + min(16 * r + lr, rows_n - 1)) * K;
     struct Part {
-        u32x4 x[MT][2], w[RB][2];
+        u32x4 x[MT][2], w[2];
         float s[MT], sw;
     };
     // block b: lane group lg takes bytes 16 lg .. and 64 + 16 lg .. of it
@@ -235,9 +234,7 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
         Part f;
         const int64_t k = (int64_t)b * 128 + 16 * lg;
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) f.w[r][h] = load_16<DWORDS>(wp[r] + k + 64 * h);
+        for (int h = 0; h < 2; ++h) f.w[h] = load_16<DWORDS>(wp + k + 64 * h);
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -247,33 +244,26 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
         for (int t = 0; t < MT; ++t) f.s[t] = xs[t][(int64_t)b * a.M];
         return f;
     };
-    f32x4 acc[RB][MT];
+    f32x4 acc[MT];
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // 16 x 16 products of 32 k (eight bytes a lane): weights are the rows, tokens the columns
     auto multiply = [&](const Part& f) {
-        f32x4 p[RB][MT];
+        f32x4 p[MT];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            f16x8 w[RB], x[MT];
-#pragma unroll
-            for (int r = 0; r < RB; ++r) w[r] = f16_of(f.w[r][q >> 1][2 * (q & 1)], f.w[r][q >> 1][2 * (q & 1) + 1]);
+            const f16x8 w = f16_of(f.w[q >> 1][2 * (q & 1)], f.w[q >> 1][2 * (q & 1) + 1]);
+            f16x8 x[MT];
 #pragma unroll
             for (int t = 0; t < MT; ++t) x[t] = f16_of(f.x[t][q >> 1][2 * (q & 1)], f.x[t][q >> 1][2 * (q & 1) + 1]);
 #pragma unroll
-            for (int r = 0; r < RB; ++r)
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    p[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[r], x[t], q ? p[r][t] : f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+            for (int t = 0; t < MT; ++t)
+                p[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x[t], q ? p[t] : f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
         }
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(p[r][t][i], f.s[t] * f.sw, acc[r][t][i]);
+            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[t][i], f.s[t] * f.sw, acc[t][i]);
     };
     if (wave < whole) {
         const int last = wave + (whole - 1 - wave) / FD_WAVES * FD_WAVES;
@@ -293,8 +283,7 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
         const int64_t k = (int64_t)whole * 128 + 16 * lg;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int r = 0; r < RB; ++r) f.w[r][h] = row_16<DWORDS>(wp[r], k + 64 * h, K);
+            f.w[h] = row_16<DWORDS>(wp, k + 64 * h, K);
 #pragma unroll
             for (int t = 0; t < MT; ++t) f.x[t][h] = row_16<DWORDS>(xp[t], k + 64 * h, K);
         }
@@ -305,35 +294,31 @@ __global__ __launch_bounds__(64 * FD_WAVES) void k_fp8_dec(Fp8Args a, int slices
     }
     const bool vector = a.N % 4 == 0 && (uintptr_t)a.y % 16 == 0 && (uintptr_t)a.bias % 16 == 0;
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-        __syncthreads();
+    for (int t = 0; t < MT; ++t) part[(wave * MT + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    for (int e = tid; e < MT * 64; e += 64 * FD_WAVES) {
+        const int l = e & 63, t = e >> 6, m = 16 * t + (l & 15), n = 4 * (l >> 4);
+        f32x4 sum = part[t * 64 + l];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) part[(wave * MT + t) * 64 + lane] = acc[r][t];
-        __syncthreads();
-        for (int e = tid; e < MT * 64; e += 64 * FD_WAVES) {
-            const int l = e & 63, t = e >> 6, m = 16 * t + (l & 15), n = 16 * r + 4 * (l >> 4);
-            f32x4 sum = part[t * 64 + l];
-#pragma unroll
-            for (int w = 1; w < FD_WAVES; ++w) sum += part[(w * MT + t) * 64 + l];
-            if (m < rows_m && n < rows_n) fp8_store(a, m0 + m, n0 + n, rows_n - n, make_float4(sum[0], sum[1], sum[2], sum[3]), vector);
-        }
+        for (int w = 1; w < FD_WAVES; ++w) sum += part[(w * MT + t) * 64 + l];
+        if (m < rows_m && n < rows_n) fp8_store(a, m0 + m, n0 + n, rows_n - n, make_float4(sum[0], sum[1], sum[2], sum[3]), vector);
     }
 }
 
-template <int ROWS, int MT, int RB>
-static hipError_t launch_fp8_dec_rb(const Fp8Args& a, hipStream_t s) {
-    const int64_t slices = (a.M + 16 * MT - 1) / (16 * MT), blocks = (a.N + 16 * RB - 1) / (16 * RB);
-    hipLaunchKernelGGL((k_fp8_dec<ROWS, MT, RB>), dim3((unsigned)(slices * blocks)), dim3(64 * FD_WAVES), 0, s, a, (int)slices);
+template <int ROWS, int MT>
+static hipError_t launch_fp8_dec_mt(const Fp8Args& a, hipStream_t s) {
+    const int64_t slices = (a.M + 16 * MT - 1) / (16 * MT), blocks = (a.N + 15) / 16;
+    hipLaunchKernelGGL((k_fp8_dec<ROWS, MT>), dim3((unsigned)(slices * blocks)), dim3(64 * FD_WAVES), 0, s, a, (int)slices);
     return hipGetLastError();
 }
 
 template <int ROWS>
 static hipError_t launch_fp8_dec(const Fp8Args& a, hipStream_t s) {
     const int64_t tiles = (a.M + 15) / 16;
-    return tiles == 1   ? launch_fp8_dec_rb<ROWS, 1, 1>(a, s)
-           : tiles == 2 ? launch_fp8_dec_rb<ROWS, 2, 1>(a, s)
-           : tiles == 3 ? launch_fp8_dec_rb<ROWS, 3, 1>(a, s)
-                        : launch_fp8_dec_rb<ROWS, 4, 1>(a, s);
+    return tiles == 1   ? launch_fp8_dec_mt<ROWS, 1>(a, s)
+           : tiles == 2 ? launch_fp8_dec_mt<ROWS, 2>(a, s)
+           : tiles == 3 ? launch_fp8_dec_mt<ROWS, 3>(a, s)
+                        : launch_fp8_dec_mt<ROWS, 4>(a, s);
 }
 
 // ---- many tokens ----------------------------------------------------------------------------
@@ -642,13 +627,16 @@ static hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
 }
 
 // The streaming kernel's time goes with the 16 x 16 blocks of y and K, the GEMM's with K alone while its tiles run
-// at once: they meet near N ceil(M / 16) = 23000.  Microseconds, streaming kernel against 64 x 128 tiles:  K = N = 4096,
-// 64 tokens 13.5 / 20.0, 96 tokens (24576) 23.0 / 20.6;  K = 4096, N = 11008, 32 tokens (22016) 20.3 / 20.8, 48 tokens
-// 26.3 / 21.5;  K = 11008, N = 4096, 64 tokens 29.4 / 46.8, 96 tokens 53.3 / 47.5;  K = 4096, N = 32000, 1 token 26.4 /
-// 23.6;  K = 2048, N = 2816, 128 tokens (22528) 12.9 / 13.0.  (At most 128 tokens: every 64 read the weights again.)
+// at once: they meet near N ceil(M / 16) = 30000 (weights from memory; 23000 from the last cache).  Microseconds, streaming kernel against 64 x 128 tiles:  K = N = 4096,
+// 64 tokens 13.5 / 20.0, 96 tokens (24576) 23.0 / 20.6 (from memory 22.3 / 26.8);  K = 4096, N = 11008, 32 tokens (22016) 20.3 / 20.8, 48 tokens
+// (33024) 26.3 / 21.5 (27.9 / 28.3);  K = 11008, N = 4096, 64 tokens 29.4 / 46.8, 96 tokens 53.3 / 47.5;  K = 2048, N = 2816, 128 tokens
+// (22528) 12.9 / 13.0.  (At most 128 tokens: every 64 read the weights again.)  Up to eight tokens it also streams large
+// weights better (from memory, not the last cache):  K = 4096, N = 32000, one token 28.5 / 36.8, eight 30.6 / 32.8, 16
+// 35.9 / 33.0;  K = 8192, N = 28672, one 48.4 / 59.5, eight 50.0 / 58.7, 16 61.8 / 60.2.
 template <int ROWS>
 static hipError_t launch_fp8(const Fp8Args& a, hipStream_t s) {
-    return a.M <= 128 && a.N * ((a.M + 15) / 16) <= 23000 ? launch_fp8_dec<ROWS>(a, s) : launch_fp8_gemm<ROWS>(a, s);
+    const bool few = a.M <= 8 || (a.M <= 128 && a.N * ((a.M + 15) / 16) <= 30000);
+    return few ? launch_fp8_dec<ROWS>(a, s) : launch_fp8_gemm<ROWS>(a, s);
 }
 
 hipError_t launch_forward_fp8(const Fp8Args& a, hipStream_t s) {
