@@ -80,6 +80,7 @@ __device__ __forceinline__ float abs_max_4(float4 v) {
 // Half a wave takes a block of one token, four values a lane; the eight halves of a workgroup take `tm`
 // tokens (a power of two) of 8 / tm neighbouring blocks, so that their scales are written together.
 // WHOLE: rows of x and x_q are read and written four at a time (K % 4 == 0 and aligned).
+// Bound: the bytes (2048 x 11008: 20.5 us, 5.5 TB/s), a launch for one token (4096: 2.2 us).
 template <bool WHOLE>
 __global__ __launch_bounds__(256) void k_quantize_act_fp8(const float* __restrict__ x, int64_t M, int64_t K,
                                                           uint8_t* __restrict__ xq, float* __restrict__ xs, int tm_log) {
@@ -108,7 +109,8 @@ hipError_t launch_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t
 
 // ---- weights --------------------------------------------------------------------------------
 // A workgroup takes a block of 128 x 128: PASSES times 128 / PASSES rows of 32 lanes, kept in registers between the
-// maximum and the codes.
+// maximum and the codes, so that W is read once.  Bound: the bytes (4096 x 11008: 34.7 us, 6.5 TB/s; 32000 x 4096: 112
+// us, 5.8 TB/s; with 512 threads, eight passes, 120 us).
 template <bool WHOLE, int PASSES>
 __global__ __launch_bounds__(4096 / PASSES) void k_quantize_weights_fp8(const float* __restrict__ W, int64_t N, int64_t K,
                                                                         uint8_t* __restrict__ wq, float* __restrict__ ws) {
@@ -201,6 +203,10 @@ __device__ __forceinline__ void fp8_store(const Fp8Args& a, int64_t m, int64_t n
 // A workgroup of eight waves computes 16 MT tokens x 16 channels; wave w takes the blocks of 128 k
 // w, w + 8, ..., and the eight partial tiles are added at the end, in the waves' order.  Operands go straight
 // into registers, two blocks ahead.
+// Bound: the weight stream (one token 4096 -> 32000: 28.5 us from memory, 4.6 TB/s, 22.7 us from the last cache; 8192
+// -> 28672: 48.4 us, 4.9 TB/s), a launch and one round of loads where it is short (4096 -> 4096: 6.5 us); at 16 tokens
+// also x_q, as many bytes for each workgroup as its weights.  Two sets of channels a workgroup (32) took 27.3 us at N =
+// 32000, but 14.5 against 12.8 at 11008, and 50.9 against 48.4.
 // 16x16x32 lane layout: A/B lane l holds row/column l % 16 and eight values of k (the same assignment of k to
 // lanes and bytes serves both, so any will do); accumulator r of lane l is row 4 (l / 16) + r, column l % 16.
 constexpr int FD_WAVES = 8;
@@ -327,6 +333,9 @@ static hipError_t launch_fp8_dec(const Fp8Args& a, hipStream_t s) {
 // go past the registers (aligned rows), or two filled through registers.
 // Unit u (16 bytes) of row r lies at slot u ^ ((r / 2) % 8) of its eight: no bank conflicts.
 // A step's sums meet their token's scale while the matrix cores are at the next step's first products.
+// Bound: the matrix cores and the clock: 2048 tokens 11008 -> 4096: 163 us, 1.13 PFLOP/s, 53% of cycles with an MFMA at
+// 2.0 GHz (f16 products of a library: 1.34 PFLOP/s).  Conversions ahead of the products, in between them, are hidden
+// (176 us without); four waves of 64 x 128 took 199: sums in accumulator registers are copied to meet their scale.
 // 32x32x16 lane layout: A/B lane l holds row/column l % 32 and eight values of k; accumulator r of lane l is
 // row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 constexpr int FG_BK = 128;
