@@ -573,3 +573,112 @@ def test_outputs_past_32_bit_offsets(dev):
     # dy is k in the last column of group 1
     assert bool((dx[7:] == k).all()) and bool((dx[:7] == 0).all())
     assert bool((dw[1, -1] == float((m - 7) * k)).all()) and bool((dw[0] == 0).all()) and bool((dw[1, :-1] == 0).all())
+
+
+@pytest.mark.parametrize("m", [6, 900])
+def test_tokens_past_32_bit_offsets(dev, m):
+    """Tokens' codes past 2^32 bytes, gathered: forward, gated forward's rows and dW of short and long groups."""
+    torch, bl = dev
+    t, k, n, e = 140000, 32768, 1088, 2
+    x_q, beta = torch.zeros(t, k, dtype=torch.int8, device="cuda"), torch.full((t,), 127.0, device="cuda")
+    x_q[-1] = 3
+    x_q[1, 5] = 7
+    rows = torch.full((m,), t - 1, dtype=torch.int64, device="cuda")
+    rows[0] = 1
+    w = torch.full((e, n, k // 4), 0x55, dtype=torch.uint8, device="cuda")
+    w[1, :, 0] = 0xAA                                                                 # four ones
+    alpha = torch.full((e,), 2.0, device="cuda")
+    offsets = torch.tensor([0, 2, m], dtype=torch.int64, device="cuda")
+    _say(f"grouped calls with tokens past 2^32 bytes, M={m}")
+    y = bl.bitlinear_grouped_forward(x_q, beta, offsets, w, alpha, rows=rows)
+    assert bool((y[:2] == 0).all()) and bool((y[2:] == 24).all())
+    dy = torch.ones(m, n, device="cuda")
+    dx, dw, _ = bl.bitlinear_grouped_backward(dy, x_q, beta, offsets, w, alpha, rows=rows)
+    assert bool((dx[2:, :4] == 2 * n).all()) and bool((dx[:, 4:] == 0).all()) and bool((dx[:2] == 0).all())
+    want = torch.full((k,), 3.0, device="cuda")
+    want[5] += 7
+    assert bool((dw[0] == want).all()) and bool((dw[1] == 3.0 * (m - 2)).all())
+
+
+def test_gradients_past_32_bit_offsets(dev):
+    """dW of short groups past 2^32 elements."""
+    torch, bl = dev
+    m, n, k, e = 40, 16384, 16384, 18
+    w = torch.full((e, n, k // 4), 0x55, dtype=torch.uint8, device="cuda")
+    w[-1, :, -1] = 0xAA
+    offsets = torch.full((e + 1,), m, dtype=torch.int64, device="cuda")
+    offsets[:-1] = 0
+    offsets[1:-1] = 1
+    x_q, beta = torch.ones((m, k), dtype=torch.int8, device="cuda"), torch.full((m,), 127.0, device="cuda")
+    _say("grouped_backward with dW past 2^32 elements")
+    dy = torch.zeros(m, n, device="cuda")
+    dy[:, -1] = 2
+    dx, dw, _ = bl.bitlinear_grouped_backward(dy, x_q, beta, offsets, w, torch.ones(e, device="cuda"))
+    assert bool((dw[-1, -1] == 2.0 * (m - 1)).all()) and bool((dw[-1, :-1] == 0).all()) and bool((dw[1:-1] == 0).all())
+    assert bool((dw[0, -1] == 2).all()) and bool((dw[0, :-1] == 0).all())
+    assert bool((dx[1:, -4:] == 2).all()) and bool((dx[:, :-4] == 0).all()) and bool((dx[0] == 0).all())
+
+
+@pytest.mark.parametrize("each", [1, 36])
+def test_most_experts(dev, each):
+    """4096 experts, every third without rows, of few rows and of many."""
+    torch, bl = dev
+    rng = np.random.default_rng([31, each])
+    e, k, n = 4096, 64, 24
+    counts = rng.integers(0, 2 * each + 1, e)
+    counts[::3] = 0
+    if each > 1:
+        counts[1::3] += 33
+    offsets, rows, m, t = _layout(rng, counts, True, 0, 2)
+    w, alpha, _ = _weights(rng, e, n, k, False)
+    x_q, beta = rng.integers(-127, 128, (t, k)).astype(np.int8), rng.uniform(0.5, 4, t).astype(F32)
+    dy = _gradient_inputs(rng, m, n)
+    args = [_t(torch, a) for a in (x_q, beta, offsets, _pack(w), alpha)]
+    kw = dict(rows=_t(torch, rows))
+    _say(f"4096 experts, M={m}")
+    y = torch.full((m, n), 7.0, device="cuda")
+    bl.bitlinear_grouped_forward(*args, y=y, **kw)
+    xr, br = experts_plain.tokens(x_q, beta, rows, m)
+    assert np.array_equal(_np(y), experts_plain.forward(xr, br, offsets, w, alpha, None, np.full((m, n), 7, F32)))
+    dx, dw, db = (torch.zeros(s, device="cuda") for s in ((m, k), (e, n, k), (e, n)))
+    bl.bitlinear_grouped_backward(_t(torch, dy), *args, dx=dx, dW=dw, dbias=db, **kw)
+    values, terms, lengths = experts_plain.gradients([dy.astype(np.float64)], [w], [alpha], xr, br, offsets, np.zeros((m, k)))
+    _check_gradients([dx, dw, db], values, terms, lengths, "4096")
+
+
+@pytest.mark.parametrize("counts,k,n", [([20, 3, 40], 1024, 600), ([300, 90], 512, 1024)])
+def test_two_calls_at_once(dev, counts, k, n):
+    """Calls on two streams, each with its workspace and outputs, over and over: as the calls one after the other."""
+    torch, bl = dev
+    rng = np.random.default_rng([37, k])
+    e = len(counts)
+    offsets, rows, m, t = _layout(rng, counts, True)
+    sides = []
+    for _ in range(2):
+        wg, ag, _ = _weights(rng, e, n, k, False)
+        wu, au, _ = _weights(rng, e, n, k, False)
+        x = rng.standard_normal((t, k)).astype(F32)
+        dh = _gradient_inputs(rng, m, n)
+        sides.append([_t(torch, a) for a in (x, offsets, _pack(wg), ag, _pack(wu), au, rows, dh)])
+
+    def call(x, offsets, wg, ag, wu, au, rows, dh, stream):
+        act = bl.BITLINEAR_ACT_SILU
+        new = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device="cuda")
+        o = dict(h=new(m, n), g=new(m, n), u=new(m, n), x_q=new(t, k, dtype=torch.int8), beta=new(t), dx=new(m, k), dg=new(e, n, k), du=new(e, n, k))
+        ws = new(bl.bitlinear_grouped_gated_backward_workspace_size(m, k, n, e), dtype=torch.uint8)
+        stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(5):
+            bl.bitlinear_grouped_gated_forward(x, offsets, wg, ag, wu, au, act, rows=rows, h=o["h"], g=o["g"], u=o["u"], x_q=o["x_q"],
+                                               beta=o["beta"], stream=stream)
+            bl.bitlinear_grouped_gated_backward(dh, o["g"], o["u"], o["x_q"], o["beta"], offsets, wg, ag, wu, au, act, rows=rows, dx=o["dx"],
+                                                dWg=o["dg"], dWu=o["du"], workspace=ws, stream=stream)
+        return o, ws
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    at_once = [call(*s, stream) for s, stream in zip(sides, streams)]
+    torch.cuda.synchronize()
+    for s, (o, _) in zip(sides, at_once):
+        alone, _ = call(*s, streams[0])
+        torch.cuda.synchronize()
+        for name in ("h", "g", "u", "dx", "dg", "du"):
+            assert torch.equal(o[name], alone[name]), name
