@@ -76,41 +76,67 @@ __device__ __forceinline__ float abs_max_4(float4 v) {
     return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 }
 
+// The largest of a half wave, in each of its lanes: four steps within rows of sixteen lanes (neighbours, pairs, the
+// mirrored eight and sixteen), then the other row's.
+__device__ __forceinline__ float half_max(float v) {
+    auto turned = [&](auto ctrl) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true)); };
+    v = fmaxf(v, turned(std::integral_constant<int, 0xB1>()));       // quad_perm 1 0 3 2
+    v = fmaxf(v, turned(std::integral_constant<int, 0x4E>()));       // quad_perm 2 3 0 1
+    v = fmaxf(v, turned(std::integral_constant<int, 0x141>()));      // row_half_mirror
+    v = fmaxf(v, turned(std::integral_constant<int, 0x140>()));      // row_mirror
+    return fmaxf(v, __shfl_xor(v, 16, 32));
+}
+
 // ---- activations ----------------------------------------------------------------------------
-// Half a wave takes a block of one token, four values a lane; the eight halves of a workgroup take `tm`
-// tokens (a power of two) of 8 / tm neighbouring blocks, so that their scales are written together.
+// Half a wave takes RUN neighbouring blocks of one token, four values a lane and block; the eight halves of a workgroup
+// take `tm` tokens (a power of two) of 8 / tm such runs, so that their scales are written together.
 // WHOLE: rows of x and x_q are read and written four at a time (K % 4 == 0 and aligned).
-// Bound: the bytes (2048 x 11008: 20.5 us, 5.5 TB/s), a launch for one token (4096: 2.2 us).
-template <bool WHOLE>
+// Bound: the bytes (2048 x 11008: 28.6 us from memory, 18.7 from the last cache, 6.0 TB/s), a launch for one token (4096:
+// 1.8 us).
+template <bool WHOLE, int RUN>
 __global__ __launch_bounds__(256) void k_quantize_act_fp8(const float* __restrict__ x, int64_t M, int64_t K,
                                                           uint8_t* __restrict__ xq, float* __restrict__ xs, int tm_log) {
     const int half = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t m = ((int64_t)blockIdx.x << tm_log) + (half & ((1 << tm_log) - 1));
-    const int64_t b = ((int64_t)blockIdx.y << (3 - tm_log)) + (half >> tm_log);
-    if (m >= M || b * 128 >= K) return;
-    const float4 v = row_4<WHOLE>(x + m * K, b * 128 + 4 * lane, K);
-    float top = abs_max_4(v);
+    const int64_t b0 = (((int64_t)blockIdx.y << (3 - tm_log)) + (half >> tm_log)) * RUN;
+    if (m >= M || b0 * 128 >= K) return;
+    float4 v[RUN];
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 32));
-    const Divisor d = divisor(top / 448.0f);
-    put_4<WHOLE>(xq + m * K, b * 128 + 4 * lane, K, d.fast ? codes_4<true>(v, d) : codes_4<false>(v, d));
-    if (lane == 0) xs[b * M + m] = d.scale;
+    for (int i = 0; i < RUN; ++i) v[i] = row_4<WHOLE>(x + m * K, (b0 + i) * 128 + 4 * lane, K);
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+        const int64_t b = b0 + i;
+        if (RUN > 1 && b * 128 >= K) return;
+        const float top = half_max(abs_max_4(v[i]));
+        const Divisor d = divisor(top / 448.0f);
+        put_4<WHOLE>(xq + m * K, b * 128 + 4 * lane, K, d.fast ? codes_4<true>(v[i], d) : codes_4<false>(v[i], d));
+        if (lane == 0) xs[b * M + m] = d.scale;
+    }
 }
 
-hipError_t launch_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* xq, float* xs, hipStream_t s) {
-    const int tm_log = M >= 8 ? 3 : M >= 4 ? 2 : M >= 2 ? 1 : 0;
+template <int RUN>
+static hipError_t launch_quantize_act_fp8_run(const float* x, int64_t M, int64_t K, uint8_t* xq, float* xs, hipStream_t s) {
+    const int tm_log = M >= 8 ? 3 : M >= 4 ? 2 : M >= 2 ? 1 : 0, per = RUN << (3 - tm_log);
     const int64_t nb = (K + 127) / 128;
-    const dim3 grid((unsigned)((M + (1 << tm_log) - 1) >> tm_log), (unsigned)((nb + (8 >> tm_log) - 1) >> (3 - tm_log)));
+    const dim3 grid((unsigned)((M + (1 << tm_log) - 1) >> tm_log), (unsigned)((nb + per - 1) / per));
     const bool whole = K % 4 == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)xq % 4 == 0;
-    if (whole) hipLaunchKernelGGL((k_quantize_act_fp8<true>), grid, dim3(256), 0, s, x, M, K, xq, xs, tm_log);
-    else hipLaunchKernelGGL((k_quantize_act_fp8<false>), grid, dim3(256), 0, s, x, M, K, xq, xs, tm_log);
+    if (whole) hipLaunchKernelGGL((k_quantize_act_fp8<true, RUN>), grid, dim3(256), 0, s, x, M, K, xq, xs, tm_log);
+    else hipLaunchKernelGGL((k_quantize_act_fp8<false, RUN>), grid, dim3(256), 0, s, x, M, K, xq, xs, tm_log);
     return hipGetLastError();
+}
+
+// Runs of two where there are many blocks: more loads are under way (32768 blocks 6.0 us, 6.6 one by one; 2048 x 11008
+// 28.6 / 31.1), but fewer workgroups (8192 blocks 3.0 / 2.9).  Runs of four: 7.0 and 28.1.
+hipError_t launch_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* xq, float* xs, hipStream_t s) {
+    return M * ((K + 127) / 128) >= 24576 ? launch_quantize_act_fp8_run<2>(x, M, K, xq, xs, s)
+                                          : launch_quantize_act_fp8_run<1>(x, M, K, xq, xs, s);
 }
 
 // ---- weights --------------------------------------------------------------------------------
 // A workgroup takes a block of 128 x 128: PASSES times 128 / PASSES rows of 32 lanes, kept in registers between the
-// maximum and the codes, so that W is read once.  Bound: the bytes (4096 x 11008: 34.7 us, 6.5 TB/s; 32000 x 4096: 112
-// us, 5.8 TB/s; with 512 threads, eight passes, 120 us).
+// maximum and the codes, so that W is read once.  Bound: the bytes (4096 x 11008: 42.6 us, 5.3 TB/s; 32000 x 4096: 113
+// us, 5.8 TB/s; with 512 threads, eight passes, 7% more.  Loads past the caches
+// 40.4 and 105, but the call that reads the codes next lost as much).
 template <bool WHOLE, int PASSES>
 __global__ __launch_bounds__(4096 / PASSES) void k_quantize_weights_fp8(const float* __restrict__ W, int64_t N, int64_t K,
                                                                         uint8_t* __restrict__ wq, float* __restrict__ ws) {

@@ -102,6 +102,11 @@ def test_quantizers(dev, r, k):
         assert np.array_equal(_values(w_q), want) and np.array_equal(ws.cpu().numpy(), s)
 
 
+@pytest.mark.parametrize("r,k", [(2500, 1281), (3100, 1028), (1, 3200001), (6, 640128), (24600, 128)])
+def test_quantizers_of_many_blocks(dev, r, k):
+    test_quantizers(dev, r, k)
+
+
 def test_quantizer_extremes(dev):
     """Ties, subnormal codes, subnormal scales, the largest floats, blocks of zeros."""
     torch, bl = dev
