@@ -188,8 +188,8 @@ __device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, int 
 
 // Rows m0 .. of the wave's 32 x 128 block, as far as `rows`, and columns from k.  STREAM: past the caches, which
 // keeps d, x_q and the codes there (2048 tokens x 2 of 8 experts, 2816 -> 2048: 291 -> 271 us; 256 rows of 16 experts: 97
-// -> 82), for rows of whole pieces of 64 bytes: others are written in parts (256 rows of 16 experts, N = 2048: K = 1008
-// 39.5 against 40.6 us cached, K = 1004 49.5 against 39.2).
+// -> 82).  dx always; dW, which is most of what is written, where its rows are whole pieces of 64 bytes: others are
+// written in parts (256 rows of 16 experts, N = 2048: K = 1008 39.5 against 40.6 us cached, K = 1004 49.5 against 39.2).
 template <bool STREAM>
 __device__ __forceinline__ void block_store(float* __restrict__ out, int64_t K, int m0, int rows, int64_t k, const f32x16 (&acc)[GB_NJ]) {
     const int lane = threadIdx.x & 63;
