@@ -36,7 +36,7 @@ __device__ __forceinline__ void gate_store(const GroupedArgs& a, int64_t at, flo
 }
 
 // ---- few rows an expert ---------------------------------------------------------------------
-// A workgroup of four waves computes 16 rows x 16 columns of both sets; wave w takes the steps of 256 k w, w + 4,
+// A workgroup of WAVES waves computes 16 rows x 16 columns of both sets; wave w takes the steps of 256 k w, w + WAVES,
 // ..., and the partial tiles are added at the end (integers: exact in any order).  In MFMA q of a step lane group g
 // (lanes 16 g ..) holds weights 64 g + 16 q .. 64 g + 16 q + 15, dword q of the lane's 16 bytes of codes, expanded
 // in weight order to signed bytes.  Operands go straight into registers, a step ahead; the first weights are on
@@ -44,14 +44,11 @@ __device__ __forceinline__ void gate_store(const GroupedArgs& a, int64_t at, flo
 // 16x16x64 lane layout: A/B lane l holds row/column l % 16, k = 16 (l / 16) + j; accumulator r of
 // lane l is row 4 (l / 16) + r, column l % 16.
 // Bound: a chain of loads (offsets, tokens, x_q and beta) and one or two rounds of workgroups beside the weight stream:
-// 64 rows of 16 experts 2816 -> 2048 7.8 us, 3.0 TB/s.  Workgroups of eight waves took 10.5 against 8.2 us (64 rows of 64
-// experts, 1024 -> 1024); one load of x_q a step for slots of up to four rows won half a microsecond there and lost as
+// 64 rows of 16 experts 2816 -> 2048 7.8 us, 3.0 TB/s; one load of x_q a step for slots of up to four rows won half a microsecond there and lost as
 // much at sixteen rows.
-constexpr int ED_WAVES = 4;
-
-template <bool GATED>
-__global__ __launch_bounds__(64 * ED_WAVES) void k_grouped_dec(GroupedArgs a, int slots) {
-    __shared__ i32x4 part[ED_WAVES * 2 * 64];
+template <bool GATED, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_grouped_dec(GroupedArgs a, int slots) {
+    __shared__ i32x4 part[WAVES * 2 * 64];
     const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Slot slot = find_slot<16, false>(a.offsets, (int)a.E, a.M, (int)(blockIdx.x % slots), nullptr);
@@ -94,15 +91,15 @@ __global__ __launch_bounds__(64 * ED_WAVES) void k_grouped_dec(GroupedArgs a, in
     };
     if (wave < whole) {
         load_x(f, wave);
-        for (int s = wave; s < whole; s += ED_WAVES) {
+        for (int s = wave; s < whole; s += WAVES) {
             Part next;
-            load_w(next, min(s + ED_WAVES, whole - 1));
-            load_x(next, min(s + ED_WAVES, whole - 1));
+            load_w(next, min(s + WAVES, whole - 1));
+            load_x(next, min(s + WAVES, whole - 1));
             multiply(f);
             f = next;
         }
     }
-    if (K % 256 && whole % ED_WAVES == wave) {                      // the last part step, to the next wave in turn
+    if (K % 256 && whole % WAVES == wave) {                      // the last part step, to the next wave in turn
         const int64_t k = (int64_t)whole * 256 + 64 * lg;
 #pragma unroll
         for (int p = 0; p < 2; ++p) f.w[p] = row_16(wp[p], k >> 2, rowb);
@@ -113,12 +110,13 @@ __global__ __launch_bounds__(64 * ED_WAVES) void k_grouped_dec(GroupedArgs a, in
 #pragma unroll
     for (int p = 0; p < 2; ++p) part[(wave * 2 + p) * 64 + lane] = acc[p];
     __syncthreads();
+    if (wave >= 4) return;
     // wave i takes element i of every lane: row 4 (l / 16) + i, column l % 16, of both sets
     const int i = wave, n = lr, m = 4 * lg + i;
     const float b = __shfl(beta, m, 64);
     int s0 = 0, s1 = 0;
 #pragma unroll
-    for (int w = 0; w < ED_WAVES; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         const int* p = reinterpret_cast<const int*>(part + w * 2 * 64 + lane);
         s0 += p[i];
         s1 += p[i + 256];
@@ -141,10 +139,10 @@ __global__ __launch_bounds__(64 * ED_WAVES) void k_grouped_dec(GroupedArgs a, in
     }
 }
 
-template <bool GATED>
+template <bool GATED, int WAVES>
 static hipError_t launch_grouped_dec(const GroupedArgs& a, hipStream_t s) {
     const int64_t slots = most_slots(a, 16), blocks = (a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32);
-    hipLaunchKernelGGL(k_grouped_dec<GATED>, dim3((unsigned)(slots * blocks)), dim3(64 * ED_WAVES), 0, s, a, (int)slots);
+    hipLaunchKernelGGL((k_grouped_dec<GATED, WAVES>), dim3((unsigned)(slots * blocks)), dim3(64 * WAVES), 0, s, a, (int)slots);
     return hipGetLastError();
 }
 
@@ -456,11 +454,15 @@ static hipError_t launch_grouped_tiles(const GroupedArgs& a, hipStream_t s) {
 // 12.0;  16 experts 2816 -> 2048: 8 rows (1024) 11.1 / 15.0, 16 (1536) 17.8 / 15.4;  64 experts 1024 -> 1024: 1 row
 // (2048) 8.2 / 8.7, gated (4096) 12.0 / 9.7;  8 experts 4096 -> 11008: 1 row (2752) 23.9 / 20.7;  4 experts 512 -> 1024:
 // 128 rows (1088) 6.5 / 7.6, 256 (2112) 9.8 / 7.9;  7 experts 1088 -> 1537: 32 rows (857) 7.7 / 9.8, 64 (1519) 11.4 / 10.1.
+// Eight waves for up to two workgroups a compute unit, four beyond (microseconds, eight / four):  8 experts 11008 ->
+// 4096: 2 rows in all (256 workgroups) 8.2 / 11.1, 4 rows (512) 12.9 / 13.4, 32 rows (1024) 27.2 / 24.8;  16 experts
+// 2816 -> 2048: 4 rows (256) 4.4 / 4.9, 16 rows (1024) 11.7 / 9.3.
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t s) {
     const int64_t used = a.E < a.M ? a.E : a.M, half_full = a.M / 16 + used / 2, slots = used > half_full ? used : half_full;
     const int64_t blocks = a.w1 ? (a.N + 15) / 16 : (a.N + 31) / 32;
     const int64_t most = a.M <= 2 * used ? ((int64_t)1 << 20) / a.K + 2048 : ((int64_t)1 << 19) / a.K + 1024;
-    if (slots * blocks <= most) return a.w1 ? launch_grouped_dec<true>(a, s) : launch_grouped_dec<false>(a, s);
+    if (slots * blocks <= 512) return a.w1 ? launch_grouped_dec<true, 8>(a, s) : launch_grouped_dec<false, 8>(a, s);
+    if (slots * blocks <= most) return a.w1 ? launch_grouped_dec<true, 4>(a, s) : launch_grouped_dec<false, 4>(a, s);
     const bool aligned = a.K % 64 == 0 && a.T <= 0xFFFFFFFFll / a.K && (uintptr_t)a.xq % 16 == 0 && (uintptr_t)a.w0 % 16 == 0 &&
                          (uintptr_t)a.w1 % 16 == 0;
     return aligned ? launch_grouped_tiles<true>(a, s) : launch_grouped_tiles<false>(a, s);
