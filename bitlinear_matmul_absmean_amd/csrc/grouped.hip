@@ -114,6 +114,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_grouped_dec(GroupedArgs a, int s
     // wave i takes element i of every lane: row 4 (l / 16) + i, column l % 16, of both sets
     const int i = wave, n = lr, m = 4 * lg + i;
     const float b = __shfl(beta, m, 64);
+    // the sums of a token that is not there are those of zeros (a scale of zero alone would leave them their sign)
+    const int some = (int)((uint32_t)__ballot(r < 0) >> m & 1) - 1;
     int s0 = 0, s1 = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
@@ -121,6 +123,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_grouped_dec(GroupedArgs a, int s
         s0 += p[i];
         s1 += p[i + 256];
     }
+    s0 &= some;
+    s1 &= some;
     if (m >= rows_m) return;
     const int64_t at = (m0 + m) * a.N + n0 + n, bn = e * a.N + n0 + n;
     float v0 = (float)s0 * dequant_scale(a.al0[e], b);
@@ -196,6 +200,15 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
         const int64_t v = row_token(a.rows, m0 + min(r, rows_m - 1), a.T);
         return v < 0 ? (int64_t)0 : v;
     };
+    // tokens of the tile's rows, for every wave to see whether they are all there (once its first loads are under way)
+    int64_t all[(BM + 63) / 64];
+#pragma unroll
+    for (int i = 0; i < (BM + 63) / 64; ++i) all[i] = row_token(a.rows, m0 + min(64 * i + lane, rows_m - 1), a.T);
+    bool gone = false;
+    auto look = [&]() {
+#pragma unroll
+        for (int i = 0; i < (BM + 63) / 64; ++i) gone |= __any(all[i] < 0);
+    };
     if (tid < BM) {
         const int64_t r = row_token(a.rows, m0 + min(tid, rows_m - 1), a.T);
         const float beta = r < 0 ? 0.0f : a.beta[r];
@@ -270,6 +283,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
             fetch(st0, 0);
             fetch(st1, 1);
         }
+        look();
         for (; s + 3 <= steps; s += 3) {
             turn();
             fetch(st2, s + 2);
@@ -333,6 +347,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
             r0 = load(0);
             r1 = load(min(1, last));
         }
+        look();
         if (K % EG_BK) {
             const int64_t k = (int64_t)whole * EG_BK;
             Regs r;
@@ -410,6 +425,23 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
                 }
             }
         }
+    // A token that is not there is one of zeros, but token 0 was read for it, and a scale of zero leaves its sums their
+    // sign: those rows once more, by the lanes that wrote them, from sums of zero.  (8 experts 4096 -> 11008, 128 rows
+    // each: 90.4 us; 97.9 with the sums cleared ahead of the epilogue, whose loads the compiler then no longer hoisted.)
+    if (!gone) return;
+    for (int m = 4 * lg; m < rows_m; m += (m & 3) == 3 ? 5 : 1) {
+        if (row_token(a.rows, m0 + m, a.T) >= 0) continue;
+        float v0 = 0.0f * scale[0][m], v1 = 0.0f * scale[GATED ? 1 : 0][m];
+        if (a.b0) v0 = v0 + b0;
+        if (bias1) v1 = v1 + b1;
+        const int64_t at = (m0 + m) * a.N + n0 + n;
+        if constexpr (GATED) {
+            gate_store<ACT>(a, at, v0, v1);
+        } else {
+            a.y[at] = v0;
+            if (second) a.y[at + EG_BF] = v1;
+        }
+    }
 }
 
 template <int ACT, bool ALIGNED, int FM>
