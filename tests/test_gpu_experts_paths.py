@@ -96,6 +96,10 @@ def _check_gated(torch, bl, m, e, k, f, act, bias, gone, names):
         assert np.array_equal(_bits(_np(h)), _bits(first)), name
 
 
+def _id(v):
+    return f"M{v[0]}_E{v[1]}_K{v[2]}_N{v[3]}" if isinstance(v, tuple) else v[0] if isinstance(v, list) else str(v)
+
+
 def _gemm(act, aligned, fm):
     return f"k_grouped_gemm<{act}, {int(aligned)}, {fm}>"
 
@@ -105,7 +109,7 @@ GONE = [(42, 3, 256, 160, ["k_grouped_dec<0, 8>"] * 2), (300, 9, 320, 1000, ["k_
         (403, 3, 320, 3300, [_gemm(0, 1, 1), _gemm(0, 0, 1)]), (700, 5, 192, 3100, [_gemm(0, 1, 2), _gemm(0, 0, 2)])]
 
 
-@pytest.mark.parametrize("m,e,k,n,names", GONE, ids=lambda v: v[0] if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("m,e,k,n,names", GONE, ids=_id)
 def test_rows_without_a_token_are_of_zeros(dev, m, e, k, n, names):  # noqa: F811
     """A row whose index is no token reads x_q = 0 and beta = 0: +0 in every column, not the sign of another
     token's sum."""
@@ -118,8 +122,109 @@ GONE_GATED = [(42, 3, 256, 160, ["k_grouped_dec<1, 8>"] * 2), (300, 9, 320, 500,
               (403, 3, 320, 1700, [_gemm(2, 1, 1), _gemm(2, 0, 1)]), (700, 5, 192, 1550, [_gemm(2, 1, 2), _gemm(2, 0, 2)])]
 
 
-@pytest.mark.parametrize("m,e,k,f,names", GONE_GATED, ids=lambda v: v[0] if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("m,e,k,f,names", GONE_GATED, ids=_id)
 def test_gated_rows_without_a_token_are_of_zeros(dev, m, e, k, f, names):  # noqa: F811
     torch, bl = dev
     for bias in (False, True):
         _check_gated(torch, bl, m, e, k, f, "silu", bias, 0.4, names)
+
+
+# M, experts, K, columns of every height of the GEMM's tiles: no whole step of 128, one to seven, with and without a rest,
+# rows of codes that are not whole pieces of 16 bytes
+TILES_32 = [(1990, 100, 60, 1801), (1990, 100, 64, 1700), (1990, 100, 100, 1160), (1990, 100, 128, 930), (403, 3, 192, 4700),
+            (403, 3, 256, 3801), (403, 3, 260, 3750), (403, 3, 384, 2950), (403, 3, 512, 2513), (403, 3, 576, 2400), (403, 3, 640, 2250),
+            (403, 3, 768, 2111), (403, 3, 896, 1985), (403, 3, 960, 1953), (403, 3, 1028, 1900)]
+TILES_64 = [(700, 5, 60, 7001), (700, 5, 64, 6600), (700, 5, 100, 4500), (700, 5, 128, 3700), (700, 5, 192, 3073), (700, 5, 256, 3100),
+            (700, 5, 260, 3201), (700, 5, 384, 3100), (700, 5, 512, 3329), (700, 5, 576, 3100), (700, 5, 640, 3077), (700, 5, 768, 3100),
+            (700, 5, 896, 3263), (700, 5, 960, 3100)]
+TILES_128 = [(1500, 4, 4096, 6700), (1500, 4, 4160, 6657), (1500, 4, 4100, 6721), (1500, 4, 4224, 6801), (1500, 4, 4352, 6657)]
+
+
+@pytest.mark.parametrize("fm,size", [(1, s) for s in TILES_32] + [(2, s) for s in TILES_64] + [(4, s) for s in TILES_128], ids=_id)
+def test_tiles(dev, fm, size):  # noqa: F811
+    torch, bl = dev
+    m, e, k, n = size
+    _check_forward(torch, bl, m, e, k, n, k % 128 != 0, 0.05, [_gemm(0, k % 64 == 0, fm), _gemm(0, 0, fm)])
+
+
+GATED_32 = [(1990, 100, 64, 850), (1990, 100, 100, 577), (1990, 100, 128, 470), (403, 3, 192, 2350), (403, 3, 256, 1900),
+            (403, 3, 260, 1901), (403, 3, 384, 1500), (403, 3, 576, 1200), (403, 3, 896, 1001)]
+GATED_64 = [(700, 5, 64, 3300), (700, 5, 128, 1900), (700, 5, 192, 1537), (700, 5, 256, 1600), (700, 5, 260, 1577), (700, 5, 384, 1555),
+            (700, 5, 512, 1600), (700, 5, 576, 1537), (700, 5, 960, 1600)]
+GATED_128 = [(1500, 4, 4096, 3400), (1500, 4, 4160, 3329), (1500, 4, 4100, 3401)]
+
+
+@pytest.mark.parametrize("fm,size,act", [(fm, s, act) for fm, sizes in ((1, GATED_32), (2, GATED_64), (4, GATED_128))
+                                         for i, s in enumerate(sizes) for act in (["silu", "gelu", "relu2"][(i + fm) % 3:][:1] if fm != 4
+                                                                                  else ["silu", "gelu", "relu2"])], ids=_id)
+def test_gated_tiles(dev, fm, size, act):  # noqa: F811
+    """Every height with every activation; of 128 rows every activation at every size."""
+    torch, bl = dev
+    m, e, k, f = size
+    number = ACT_NUMBER[act]
+    _check_gated(torch, bl, m, e, k, f, act, f % 2 == 1, 0.05, [_gemm(number, k % 64 == 0, fm), _gemm(number, 0, fm)])
+
+
+def test_tiles_of_tokens_past_2_gib(dev):  # noqa: F811
+    """Tokens' codes between 2^31 and 2^32 bytes: the offsets of the aligned tiles are unsigned."""
+    torch, bl = dev
+    t, k, m, e, n = 125000, 32768, 900, 2, 1088
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(47)
+    x_q = torch.zeros(t, k, dtype=torch.int8, device="cuda")
+    rows = torch.randint(0, t, (m,), device="cuda", generator=gen)
+    rows[:4] = torch.tensor([t - 1, 65535, 65536, 0], device="cuda")
+    x_q[rows] = torch.randint(-127, 128, (m, k), device="cuda", generator=gen).to(torch.int8)
+    beta = torch.rand(t, device="cuda", generator=gen) + 0.5
+    w = torch.randint(0, 256, (e, n, k // 4), device="cuda", generator=gen).to(torch.uint8)
+    w &= ~(w >> 1) | 0xAA                                           # no code of three
+    alpha, offsets = torch.tensor([0.5, 0.25], device="cuda"), torch.tensor([0, 333, m], dtype=torch.int64, device="cuda")
+    _say(f"grouped_forward of {t * k} bytes of tokens")
+    call = lambda: bl.bitlinear_grouped_forward(x_q, beta, offsets, w, alpha, rows=rows, y=y)
+    y = torch.empty(m, n, device="cuda")
+    assert kernels(torch, call) == [_gemm(0, 1, 1)]
+    call()
+    shifts = torch.tensor([0, 2, 4, 6], device="cuda", dtype=torch.uint8)
+    for i, j, g in ((0, 333, 0), (333, m, 1)):
+        codes = ((w[g][:, :, None] >> shifts) & 3).reshape(n, k).double() - 1
+        acc = (x_q[rows[i:j]].double() @ codes.t().contiguous()).float()           # exact: below 2^53
+        s = (alpha[g].double() * beta[rows[i:j]].double() / 127.0).float()
+        assert torch.equal(y[i:j], acc * s[:, None])
+
+
+@pytest.mark.parametrize("m,e,k,n,name", [(1990, 100, 256, 600, _gemm(0, 1, 1)), (700, 5, 192, 3100, _gemm(0, 1, 2)),
+                                          (1500, 4, 4096, 6657, _gemm(0, 1, 4))], ids=str)
+def test_offsets_that_decrease_make_no_more_tiles(dev, m, e, k, n, name):  # noqa: F811
+    """Groups that share rows make more tiles than were launched.  The tiles and the gradients of long groups stop at
+    those that were: outputs are unspecified, what lies around them is not touched, and the next call is right."""
+    torch, bl = dev
+    rng = np.random.default_rng([53, m])
+    bad = np.where(np.arange(e + 1) % 2 == 0, 0, m).astype(np.int64)
+    offsets, rows, x_q, beta, t = _case(rng, m, e, k, 0.0)
+    w, alpha, _ = _weights(rng, e, n, k, False)
+    dy = rng.standard_normal((m, n)).astype(F32)
+    xt, bt, wt, at, rt, dyt = (_t(torch, a) for a in (x_q, beta, _pack(w), alpha, rows, dy))
+
+    def between(*shape):
+        size = int(np.prod(shape))
+        buf = torch.full((size + 512,), 7.0, device="cuda")
+        return buf, buf[256:256 + size].view(shape)
+
+    bufs, (y, dx, dw, db) = zip(*[between(*s) for s in ((m, n), (m, k), (e, n, k), (e, n))])
+    ws = torch.empty(bl.bitlinear_grouped_backward_workspace_size(m, k, n, e), dtype=torch.uint8, device="cuda")
+    for off in (bad, offsets):
+        ot = _t(torch, off)
+        forward = lambda: bl.bitlinear_grouped_forward(xt, bt, ot, wt, at, rows=rt, y=y)  # noqa: B023
+        assert kernels(torch, forward) == [name]
+        forward()
+        if m > 32 * e:
+            backward = lambda: bl.bitlinear_grouped_backward(dyt, xt, bt, ot, wt, at, rows=rt, dx=dx, dW=dw, dbias=db,  # noqa: B023
+                                                             workspace=ws)
+            assert kernels(torch, backward)[0] == "k_grouped_gradients"
+            backward()
+        torch.cuda.synchronize()
+        for b in bufs:
+            assert bool((b[:256] == 7).all()) and bool((b[-256:] == 7).all())
+    want = experts_plain.forward(*experts_plain.tokens(x_q, beta, rows, m), offsets, w, alpha, None, np.zeros((m, n), F32))
+    live = int(offsets[-1])
+    assert np.array_equal(_bits(_np(y))[:live], _bits(want)[:live])
