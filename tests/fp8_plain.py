@@ -10,6 +10,16 @@ def _scaled(x, xs, w, ws):
     return (x * xs.T[:, b]).astype(np.float64) @ (w * ws[np.arange(w.shape[0]) // 128][:, b]).astype(np.float64).T
 
 
+def integers(rng, m, k, n):
+    """Integers up to 4 and scales 2^-1 .. 2^1: a term is at most 4 * 4 * 2 * 2 = 2^6 and a multiple of 2^-2, so a sum of
+    K of them is at most 2^8 K steps of 2^-2: an fp32 number for K up to 2^16."""
+    assert k <= 1 << 16
+    x, w = rng.integers(-4, 5, (m, k)).astype(F32), rng.integers(-4, 5, (n, k)).astype(F32)
+    xs = np.exp2(rng.integers(-1, 2, (-(-k // 128), m))).astype(F32)
+    ws = np.exp2(rng.integers(-1, 2, (-(-n // 128), -(-k // 128)))).astype(F32)
+    return x, xs, w, ws, _scaled(x, xs, w, ws)
+
+
 def wide(rng, m, k, n):
     """Every eight neighbouring k hold two large products, +-2^16 and its negative, and six of 2^-2 .. 2^2 with either sign:
     2^14 to 2^18 times smaller.  A block's partial sums are at most 16 * 2^16 + 96 * 2^2 < 2^21 and multiples of 2^-2,

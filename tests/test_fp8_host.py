@@ -28,3 +28,19 @@ def test_wide_products_need_every_bit(k):
         for i in order:
             acc = acc + np.outer(x[:, i], w[:, i]).astype(np.float32)
         assert np.array_equal(acc, want)
+
+
+def test_integers_are_exact():
+    rng = np.random.default_rng(2)
+    x, xs, w, ws, want = fp8_plain.integers(rng, 5, 4000, 130)
+    assert _e4m3(x) and _e4m3(w) and np.array_equal(want.astype(np.float32), want)
+    b = np.arange(4000) // 128
+    acc = np.zeros(want.shape, np.float32)
+    for i in range(4000):
+        term = np.outer(x[:, i] * xs[b[i]], w[:, i] * ws[np.arange(130) // 128, b[i]]).astype(np.float32)
+        acc = acc + term
+    assert np.array_equal(acc, want)
+    # a scale one block off, and two blocks exchanged, are seen
+    assert not np.array_equal(fp8_plain._scaled(x, np.roll(xs, 1, 0), w, ws), want)
+    swapped = np.concatenate([x[:, 128:256], x[:, :128], x[:, 256:]], axis=1)
+    assert not np.array_equal(fp8_plain._scaled(swapped, xs, w, ws), want)

@@ -36,6 +36,26 @@ def _check(torch, bl, m, k, n, data, names):
         assert bool((out[:b] == 7).all()) and bool((out[b + m * n:] == 7).all())
 
 
+# M, K, N and the kernel with its sizes
+DEC = [(1, 1024, 300, 1), (3, 4097, 200, 1), (16, 2064, 130, 1), (17, 1300, 77, 2), (40, 1040, 150, 3), (64, 900, 140, 4), (100, 1153, 90, 4)]
+# one to eight whole blocks of 128 in every tile, with and without a rest
+TILES = [(140, 256 + 128 * i + r, 300 + i, 1, 1) for i, r in enumerate((0, 16, 4, 0, 1, 64, 0))] + \
+        [(200, 128 + 128 * i + r, 8400 + i, 1, 2) for i, r in enumerate((16, 0, 4, 0, 64, 1, 0, 0))] + \
+        [(640, 128 + 128 * i + r, 8200 + i, 2, 2) for i, r in enumerate((0, 0, 16, 0, 4, 0, 105, 0))] + [(1030, 1001, 4100, 2, 2)]
+
+
+@pytest.mark.parametrize("m,k,n,mt", DEC)
+def test_streaming_kernel(dev, m, k, n, mt):  # noqa: F811
+    torch, bl = dev
+    _check(torch, bl, m, k, n, fp8_plain.integers(np.random.default_rng([1, m, k, n]), m, k, n), _names("k_fp8_dec", k, mt))
+
+
+@pytest.mark.parametrize("m,k,n,mi,fn", TILES)
+def test_tiles(dev, m, k, n, mi, fn):  # noqa: F811
+    torch, bl = dev
+    _check(torch, bl, m, k, n, fp8_plain.integers(np.random.default_rng([2, m, k, n]), m, k, n), _names("k_fp8_gemm", k, mi, fn))
+
+
 WIDE = [(1, 1032, 200, "k_fp8_dec", 1), (20, 520, 100, "k_fp8_dec", 2), (64, 256, 64, "k_fp8_dec", 4), (140, 384, 300, "k_fp8_gemm", 1, 1),
         (200, 520, 8400, "k_fp8_gemm", 1, 2), (640, 648, 8200, "k_fp8_gemm", 2, 2)]
 
