@@ -459,7 +459,8 @@ int bitlinear_forward_i8(const int8_t* x_q, const float* beta, int64_t M, int64_
  *                          together, as a tile of tokens reads them.
  *   quantize_weights_fp8:  blocks of 128 x 128; W [N, K] fp32 (in); W_q [N, K] e4m3,
  *                          W_scale [ceil(N / 128), ceil(K / 128)] fp32 (out).
- * 1 <= K <= 4194304, M and N <= 67108864; any alignment of fp32 elements.  Errors: INVALID_ARG, SHAPE, HIP.
+ * 1 <= K <= 4194304, M and N <= 67108864, M K and N K <= 2^40; any alignment of fp32 elements.
+ * Errors: INVALID_ARG, SHAPE, HIP.
  */
 int bitlinear_quantize_act_fp8(const float* x, int64_t M, int64_t K, uint8_t* x_q, float* x_scale,
                                hipStream_t stream);
@@ -474,7 +475,8 @@ int bitlinear_quantize_weights_fp8(const float* W, int64_t N, int64_t K, uint8_t
  *   x_q [M, K], x_scale [ceil(K / 128), M]; W_q [N, K], W_scale [ceil(N / 128), ceil(K / 128)], as the
  *   quantizers lay them out; bias [N] or NULL.                               (in)
  *   y [M, N] fp32.                                                           (out)
- * 1 <= K <= 4194304, M and N <= 67108864, M N <= 2^36; any alignment.  Errors: INVALID_ARG, SHAPE, HIP.
+ * 1 <= K <= 4194304, M and N <= 67108864, M K and N K <= 2^40, M N <= 2^36; any alignment.
+ * Errors: INVALID_ARG, SHAPE, HIP.
  */
 int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, int64_t K, const uint8_t* W_q,
                           const float* W_scale, int64_t N, const float* bias, float* y, hipStream_t stream);
@@ -494,9 +496,9 @@ int bitlinear_forward_fp8(const uint8_t* x_q, const float* x_scale, int64_t M, i
  *             groups share rows, leave unspecified values in the outputs and touch nothing else.  (in)
  *   W_packed  [E, N, K/4] uint8; alpha [E]; bias [E, N] or NULL.              (in)
  *   y         [M, N] fp32.                                                   (out)
- * K % 4 == 0, E <= 4096, N <= 2^20, M <= 2^24, and no more work than a launch holds (about 2^36 elements of y);
- * any alignment of elements of their type.  M == 0 is a call without rows, for
- * which x_q, beta, rows and y may be NULL.
+ * K % 4 == 0, E <= 4096, N <= 2^20, M <= 2^24, T < 2^31, T K and T N <= 2^40, E N K <= 2^42, and no more work than a
+ * launch holds: M N <= 2^35 and min(E, M) N <= 2^29, with N counted in multiples of 128, always do.  Any alignment of
+ * elements of their type.  M == 0 is a call without rows, for which x_q, beta, rows and y may be NULL.
  * Outputs must not overlap inputs.  The host reads no device memory: the call can be captured into a graph
  * and replayed with other offsets and rows.
  * Errors: INVALID_ARG (null pointer, size < 0, K, N or E == 0, T == 0 with rows), SHAPE (T != M where rows is NULL and M > 0), HIP.
@@ -535,7 +537,10 @@ int bitlinear_grouped_gated_forward(const float* x, int64_t T, int64_t K, const 
  *   dx [M, K], dW [E, N, K], dbias [E, N], each or NULL, one at least.                           (out)
  *   workspace >= bitlinear_grouped_backward_workspace_size(M, K, N, E) bytes, 256-byte aligned; scratch,
  *             one for each call that may overlap another.
- * Sizes as the forward call's.  Errors: as the forward call, ALIGNMENT and WORKSPACE (the workspace).
+ * Sizes as the forward call's, and no more work than a launch holds: E N K <= 2^36, E N <= 2^26, E K <= 2^27 and
+ * M K <= 2^35, with N counted in multiples of 128 and K of 256, always do.  (Whichever gradients are asked for; the
+ * workspace size of what does not fit is 0.)  Errors: as the forward call, SHAPE (does not fit), ALIGNMENT and WORKSPACE
+ * (the workspace).
  */
 size_t bitlinear_grouped_backward_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E);
 int bitlinear_grouped_backward(const float* dy, int64_t M, int64_t N, const int8_t* x_q, const float* beta, int64_t T,
