@@ -359,8 +359,8 @@ static hipError_t launch_fp8_dec(const Fp8Args& a, hipStream_t s) {
 // go past the registers (aligned rows), or two filled through registers.
 // Unit u (16 bytes) of row r lies at slot u ^ ((r / 2) % 8) of its eight: no bank conflicts.
 // A step's sums meet their token's scale while the matrix cores are at the next step's first products.
-// Bound: the matrix cores and the clock: 2048 tokens 11008 -> 4096: 163 us, 1.13 PFLOP/s, 53% of cycles with an MFMA at
-// 2.0 GHz (f16 products of a library: 1.34 PFLOP/s).  Conversions ahead of the products, in between them, are hidden
+// Bound: the matrix cores and the clock: 2048 tokens 11008 -> 4096: 160 us, 1.15 PFLOP/s, 57% of cycles with an MFMA at
+// 1.9 GHz (f16 products of a library: 1.34 PFLOP/s).  Conversions ahead of the products, in between them, are hidden
 // (176 us without); four waves of 64 x 128 took 199: sums in accumulator registers are copied to meet their scale.
 // 32x32x16 lane layout: A/B lane l holds row/column l % 32 and eight values of k; accumulator r of lane l is
 // row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.

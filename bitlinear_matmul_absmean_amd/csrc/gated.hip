@@ -56,8 +56,8 @@ __device__ __forceinline__ void gated_store(const GatedArgs& a, int64_t at, int6
 // calls and a product would take 11).
 // EXPERTS: the token under the projections of several experts, which lie one after the other: row m of h is of the
 // group that holds m.  `per` waves take a row, and each looks up the row's expert while x is on its way.  (Two of
-// eight experts, K = 4096, F = 11008: 12.7 us, 3.6 TB/s, against 16.9 for the quantizer and the streaming kernel of
-// grouped.hip; eight of 64, 2048 -> 1408: 8.5 against 8.8; 64 of 64: 31.2 against 33.6.)
+// eight experts, K = 4096, F = 11008: 12.4 us, 3.6 TB/s, against 16.7 for the quantizer and the streaming kernel of
+// grouped.hip; eight of 64, 2048 -> 1408: 7.9 against 8.0; 64 of 64, which would be the GEMM's: 29.7 against 28.6.)
 constexpr int GV_WAVES = 8;
 
 struct GatedRows {
@@ -185,7 +185,7 @@ static hipError_t launch_gated_gemv_r(const GatedArgs& a, const float* x, int8_t
 }
 
 // About 2048 waves: 256 workgroups, since every one of them quantizes x (two of eight experts, K = 4096, F = 11008:
-// 12.7 us, 15.8 with 4096 waves).  Rows of one chunk a lane: all of
+// a quarter slower with 4096 waves).  Rows of one chunk a lane: all of
 // a wave's rows at once if they are at most six (K = 4096, F = 11008, six pairs a wave: 8.0 against 8.4 us
 // in steps of four; K = 2048, F = 8192, four: 5.3 against 6.7 us with room for six).  Longer rows: two pairs
 // of two chunks, one of more (K = 8192, F = 28672: 23.6 against 24.1 us with three; K = 16384, F = 4096: 11.2

@@ -161,7 +161,8 @@ static hipError_t launch_grouped_dec(const GroupedArgs& a, hipStream_t s) {
 // weight row: the lane's unit h, of which group lg uses dwords 2 lg and 2 lg + 1.
 // Bound: VALU instructions, 15 for each MFMA with FM = 2 (8.5 of the expansion, 5 of the gated epilogue at K = 2048):
 // 8192 rows of 16 experts 2048 -> 2816 gated 126 us, 1.5 PFLOP/s in int8, 68% of cycles in VALU and 38% in MFMA.  FM = 4
-// halves the expansion, but leaves two workgroups a compute unit and more of a tile's rows empty.
+// halves the expansion, but its 180 registers leave two workgroups a compute unit in place of three, and more of a tile's
+// rows are empty: with the quantizer 137 us against 130.
 constexpr int EG_BF = 128, EG_BK = 128;
 
 // ACT 0: one projection, whose columns n0 + 128 .. are the second set.

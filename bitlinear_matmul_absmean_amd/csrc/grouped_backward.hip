@@ -190,6 +190,9 @@ __device__ __forceinline__ void grad_sum(u32x4* st0, u32x4* st1, int steps, int 
 // keeps d, x_q and the codes there (2048 tokens x 2 of 8 experts, 2816 -> 2048: 291 -> 271 us; 256 rows of 16 experts: 97
 // -> 82).  dx always; dW, which is most of what is written, where its rows are whole pieces of 64 bytes: others are
 // written in parts (256 rows of 16 experts, N = 2048: K = 1008 39.5 against 40.6 us cached, K = 1004 49.5 against 39.2).
+// For dx alone the rows' ends hardly matter (N = 2048, past the caches / cached, us): K = 1004, 256 rows of 16 experts 19.9 /
+// 19.3, 1024 of 8 29.6 / 29.9, 4096 of 8 67.9 / 69.0; K = 2816 and 2820, 4096 of 8: 141.7 / 142.1 and 143.4 / 143.3.  Parts of
+// dx, which the next kernel reads, would gain most from the caches: 122 rows of 5 experts 1024 -> 2731 16.8 / 15.8.
 template <bool STREAM>
 __device__ __forceinline__ void block_store(float* __restrict__ out, int64_t K, int m0, int rows, int64_t k, const f32x16 (&acc)[GB_NJ]) {
     const int lane = threadIdx.x & 63;
@@ -656,7 +659,9 @@ struct GradGrid {
     bool is_short;
     int64_t all(bool split) const { return (split ? parts : 1) * dx + db + dw; }
 };
-// Short groups: at most 32 rows an expert, on average.  Microseconds, the kernel of short groups against tiles of
+// Short groups: at most 32 rows an expert, on average (the host does not read the offsets).  Where one expert has all the
+// rows, its short sums read x_q again for every 32 n: 2048 rows of 64 experts 2048 -> 1408 519 us, 199 with even groups;
+// 4096 of 160 1090 and 561.  Microseconds, the kernel of short groups against tiles of
 // 128 x 256:  8 experts 2816 -> 2048: 32 rows 58 / 66, 64 rows 88 / 81;  16 experts 1024 -> 1024: 40 rows 34 / 37, 75
 // rows 53 / 43;  8 experts gated 1024 -> 1408: 50 rows 55 / 50;  5 experts gated 1024 -> 2731: 24 rows 44 / 55.
 // Parts of dx's sum: about 1024 workgroups, with at least eight steps of 16 n a wave (53 experts 564 -> 230: one part
