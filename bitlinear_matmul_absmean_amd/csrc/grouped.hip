@@ -173,7 +173,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
     __shared__ i32x4 st0[UNITS];
     __shared__ i32x4 st1[UNITS];
     __shared__ i32x4 st2[ALIGNED ? UNITS : 1];
-    __shared__ __align__(16) float scale[2][BM];
+    __shared__ __align__(16) float scale[3][BM];       // of the two sets; and what is added to a row's sums
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // of the tiles there are, a contiguous run for each XCD, four rows of tiles at a time
@@ -201,18 +201,12 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
         const int64_t v = row_token(a.rows, m0 + min(r, rows_m - 1), a.T);
         return v < 0 ? (int64_t)0 : v;
     };
-    // tokens of the tile's rows, for every wave to see whether they are all there (once its first loads are under way)
-    int64_t all[(BM + 63) / 64];
-#pragma unroll
-    for (int i = 0; i < (BM + 63) / 64; ++i) all[i] = row_token(a.rows, m0 + min(64 * i + lane, rows_m - 1), a.T);
-    bool gone = false;
-    auto look = [&]() {
-#pragma unroll
-        for (int i = 0; i < (BM + 63) / 64; ++i) gone |= __any(all[i] < 0);
-    };
     if (tid < BM) {
         const int64_t r = row_token(a.rows, m0 + min(tid, rows_m - 1), a.T);
         const float beta = r < 0 ? 0.0f : a.beta[r];
+        // A token that is not there is one of zeros, but token 0 is read for it: times a scale of zero its sums keep their
+        // sign, which adding 0 takes away.  Adding -0 changes nothing.
+        scale[2][tid] = r < 0 ? 0.0f : -0.0f;
         scale[0][tid] = dequant_scale(a.al0[e], beta);
         if (GATED) scale[1][tid] = dequant_scale(a.al1[e], beta);
     }
@@ -284,7 +278,6 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
             fetch(st0, 0);
             fetch(st1, 1);
         }
-        look();
         for (; s + 3 <= steps; s += 3) {
             turn();
             fetch(st2, s + 2);
@@ -348,7 +341,6 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
             r0 = load(0);
             r1 = load(min(1, last));
         }
-        look();
         if (K % EG_BK) {
             const int64_t k = (int64_t)whole * EG_BK;
             Regs r;
@@ -379,7 +371,10 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
     if (n >= rows_n) return;
     const bool second = n < rows_n1;
     const float* bias1 = GATED ? a.b1 : a.b0;
-    const float b0 = a.b0 ? a.b0[e * a.N + n0 + n] : 0.0f, b1 = bias1 && second ? bias1[e * a.N + n1 + n] : 0.0f;
+    float b0 = a.b0 ? a.b0[e * a.N + n0 + n] : -0.0f, b1 = bias1 && second ? bias1[e * a.N + n1 + n] : -0.0f;
+    // both are there before the first store: waited for behind the stores' conditions they would be waited for at each,
+    // and the stores before it with them
+    asm volatile("" : "+v"(b0), "+v"(b1));
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -387,15 +382,14 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
             const int m = 32 * i + 8 * q + 4 * lg;
             const float4 s4 = *reinterpret_cast<const float4*>(&scale[0][m]);
             const float4 t4 = *reinterpret_cast<const float4*>(&scale[GATED ? 1 : 0][m]);
-            const float s0[4] = {s4.x, s4.y, s4.z, s4.w}, s1[4] = {t4.x, t4.y, t4.z, t4.w};
+            const float4 z4 = *reinterpret_cast<const float4*>(&scale[2][m]);
+            const float s0[4] = {s4.x, s4.y, s4.z, s4.w}, s1[4] = {t4.x, t4.y, t4.z, t4.w}, z[4] = {z4.x, z4.y, z4.z, z4.w};
             const int64_t at = (m0 + m) * a.N + n0 + n;
             float v0[4], v1[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                v0[c] = (float)acc[i][0][4 * q + c] * s0[c];
-                v1[c] = (float)acc[i][1][4 * q + c] * s1[c];
-                if (a.b0) v0[c] = v0[c] + b0;
-                if (bias1) v1[c] = v1[c] + b1;
+                v0[c] = (float)acc[i][0][4 * q + c] * s0[c] + z[c] + b0;
+                v1[c] = (float)acc[i][1][4 * q + c] * s1[c] + z[c] + b1;
             }
             if constexpr (!GATED) {
 #pragma unroll
@@ -426,23 +420,6 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm(GroupedArgs a, int most
                 }
             }
         }
-    // A token that is not there is one of zeros, but token 0 was read for it, and a scale of zero leaves its sums their
-    // sign: those rows once more, by the lanes that wrote them, from sums of zero.  (8 experts 4096 -> 11008, 128 rows
-    // each: 90.4 us; 97.9 with the sums cleared ahead of the epilogue, whose loads the compiler then no longer hoisted.)
-    if (!gone) return;
-    for (int m = 4 * lg; m < rows_m; m += (m & 3) == 3 ? 5 : 1) {
-        if (row_token(a.rows, m0 + m, a.T) >= 0) continue;
-        float v0 = 0.0f * scale[0][m], v1 = 0.0f * scale[GATED ? 1 : 0][m];
-        if (a.b0) v0 = v0 + b0;
-        if (bias1) v1 = v1 + b1;
-        const int64_t at = (m0 + m) * a.N + n0 + n;
-        if constexpr (GATED) {
-            gate_store<ACT>(a, at, v0, v1);
-        } else {
-            a.y[at] = v0;
-            if (second) a.y[at + EG_BF] = v1;
-        }
-    }
 }
 
 template <int ACT, bool ALIGNED, int FM>

@@ -38,6 +38,8 @@ def _check_forward(torch, bl, m, e, k, n, bias, gone, names):
     rng = np.random.default_rng([41, m, e, k, n])
     offsets, rows, x_q, beta, t = _case(rng, m, e, k, gone)
     w, alpha, b = _weights(rng, e, n, k, bias)
+    if bias:
+        b[:, ::7] = -0.0
     want = experts_plain.forward(*experts_plain.tokens(x_q, beta, rows, m), offsets, w, alpha, b, np.full((m, n), 7, F32))
     args = [x_q, beta, offsets, _pack(w), alpha]
     for name, off in zip(names, (0, 1)):
